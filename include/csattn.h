@@ -56,7 +56,8 @@ typedef enum {
   CSATTN_ERR_DEVICE_ARG = -6    /* a device-side check failed (status word)    */
 } csattn_status;
 
-typedef enum { CSATTN_F32 = 0, CSATTN_BF16 = 1 } csattn_dtype;
+/* CSATTN_E4M3: a KV cache in 8 bits, for the calls that say so (see "8-bit KV cache"). */
+typedef enum { CSATTN_F32 = 0, CSATTN_BF16 = 1, CSATTN_E4M3 = 2 } csattn_dtype;
 
 typedef enum { CSATTN_ROPE_SPLIT_HALF = 0, CSATTN_ROPE_ADJACENT = 1 } csattn_rope_layout;
 
@@ -511,6 +512,173 @@ int csattn_cache_append_paged(const void* k_new, const void* v_new, void* k_page
                               const int32_t* block_table, const int32_t* cache_lens, int B,
                               int Hkv, int Tn, int page_size, int num_pages, int max_pages, int d,
                               int dtype, float rope_base, int rope_layout, void* stream);
+
+/*
+ * 8-bit KV cache.  A cache row of one KV head is d e4m3 values and one scale byte: channel i
+ * stands for x8_i * 2^(code - 127).  k_cache, v_cache hold the values in the layouts of the
+ * bf16 caches ([B, Hkv, Lmax, d], or pages [num_pages, Hkv, page_size, d]), one byte each;
+ * k_scale, v_scale the codes, [B, Hkv, Lmax] or [num_pages, Hkv, page_size] (E8M0 bytes).
+ * A write takes the least code with a <= 448 * 2^(code - 127) (code within [3, 247]), a the
+ * largest finite magnitude of the row; for keys that are rotated, sqrt(2) * a of the row
+ * before its rotation, so that the code does not depend on the position.  Each value is
+ * rounded once (to nearest even) from fp32; infinities and NaN are stored as NaN, and what
+ * would round to 2^128 as 1.875 * 2^127.  The value x8 * 2^(code - 127) is a bf16 number, so reading a row back is exact.  The calls
+ * below read codes in [3, 247] (another code reads as some power of two, infinity or 0).
+ */
+
+/*
+ * Appends Tn tokens per sequence to an 8-bit cache: csattn_cache_append with the rows
+ * quantised as they are written ("The Transformer architecture", "Hands-on").  Token t of
+ * sequence b goes to row r = cache_lens[b] + t, its key rotated at r.
+ *   k_new, v_new  [B, Hkv, Tn, d] bf16 (keys not rotated)
+ *   rope_base, rope_layout  as csattn_attn_fwd (rope_base <= 0: no rotation)
+ * Requirements: dtype CSATTN_BF16 (of k_new and v_new), d in {64, 128}, 1 <= Tn <= Lmax <
+ * 2^30, B * Hkv * Tn * d < 2^33, Lmax <= 49152 with RoPE; k_new, v_new and the caches 16-byte
+ * aligned, cache_lens 4-byte.  A sequence with cache_lens[b] < 0 or cache_lens[b] + Tn > Lmax
+ * is left untouched and raises CSATTN_ERR_DEVICE_ARG in the status word.
+ */
+int csattn_cache_append_fp8(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                            void* k_scale, void* v_scale, const int32_t* cache_lens, int B,
+                            int Hkv, int Tn, int Lmax, int d, int dtype, float rope_base,
+                            int rope_layout, void* stream);
+
+/* csattn_cache_append_fp8 into pages (block_table, page sizes and the handling of a page
+ * index outside the pool as csattn_cache_append_paged). */
+int csattn_cache_append_fp8_paged(const void* k_new, const void* v_new, void* k_pages,
+                                  void* v_pages, void* k_scale, void* v_scale,
+                                  const int32_t* block_table, const int32_t* cache_lens, int B,
+                                  int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                                  int d, int dtype, float rope_base, int rope_layout,
+                                  void* stream);
+
+/*
+ * Reads rows 0..seq_lens[b]-1 of an 8-bit cache back to bf16 (exactly): k_out, v_out
+ * [B, Hkv, Lout, d], in the form csattn_attn_fwd_ext (k given rotated) and
+ * csattn_attn_prefill_paged (each sequence one page) read.  Rows at or past seq_lens[b] are
+ * left as they were.  Requirements: dtype CSATTN_BF16 (of the outputs), 1 <= Lout < 2^24,
+ * B * Hkv * Lout < 2^33; outputs 16-byte aligned.  A seq_lens[b] outside [0, min(Lmax, Lout)]
+ * leaves the sequence's outputs as they were and raises CSATTN_ERR_DEVICE_ARG in the status
+ * word; a page index outside the pool raises it and its rows read as zeros.
+ */
+int csattn_cache_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
+                          const void* v_scale, const int32_t* seq_lens, void* k_out, void* v_out,
+                          int B, int Hkv, int Lmax, int Lout, int d, int dtype, void* stream);
+int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const void* k_scale,
+                                const void* v_scale, const int32_t* block_table,
+                                const int32_t* seq_lens, void* k_out, void* v_out, int B, int Hkv,
+                                int page_size, int num_pages, int max_pages, int Lout, int d,
+                                int dtype, void* stream);
+
+/*
+ * Bytes of device workspace csattn_attn_decode_fp8 and its paged form (Lmax = max_pages *
+ * page_size) need, for any max_seq_len <= Lmax.  0 for sizes they reject.
+ */
+size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits);
+
+/*
+ * csattn_attn_decode over an 8-bit cache: one new query per sequence, whose own key and value
+ * are in the cache already.
+ *   q         [B, Hq, 1, d] bf16; rotated here at position seq_lens[b] - 1 (and rounded to
+ *             bf16) when rope_base > 0, used as given otherwise
+ *   seq_lens  device int32 [B], 1 <= seq_lens[b] <= max_seq_len <= Lmax
+ *   out       [B, Hq, 1, d] bf16
+ *   num_splits  0: automatic; > 0: splits of every sequence's rows
+ *   workspace   >= csattn_decode_fp8_workspace_size() bytes, 16-byte aligned, in use until the
+ *             work on `stream` completes (calls that may run at once need one each)
+ * Requirements: dtype CSATTN_BF16 (of q and out), d in {64, 128}, any Hq / Hkv,
+ * max_seq_len <= 49152 with RoPE.  Rows at or beyond seq_lens[b] are never used.  A
+ * seq_lens[b] outside [1, max_seq_len] raises CSATTN_ERR_DEVICE_ARG in the status word and
+ * that sequence's output is zero; a page index outside the pool raises it and its rows read
+ * as zeros.
+ */
+int csattn_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
+                           const void* k_scale, const void* v_scale, const int32_t* seq_lens,
+                           void* out, int B, int Hq, int Hkv, int Lmax, int d, int dtype,
+                           float rope_base, int rope_layout, float scale, int max_seq_len,
+                           int num_splits, void* workspace, size_t workspace_bytes,
+                           void* stream);
+int csattn_attn_decode_fp8_paged(const void* q, const void* k_pages, const void* v_pages,
+                                 const void* k_scale, const void* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                 int B, int Hq, int Hkv, int page_size, int num_pages,
+                                 int max_pages, int d, int dtype, float rope_base, int rope_layout,
+                                 float scale, int max_seq_len, int num_splits, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of device workspace csattn_attn_tree_step and its paged form (Lmax = max_pages *
+ * page_size) need: split partials, rotated queries, the drafts' masks, lengths and flags.
+ */
+size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int d,
+                                  int num_splits);
+
+/*
+ * One verification step of drafted tokens: a tree of Tn drafts per sequence is appended to the
+ * cache and every draft attends to the sequence's rows, the drafts above it and itself (with
+ * Tn = 1 and parent -1 this is csattn_attn_decode_step, over either cache).
+ *   parents    device int32 [B, Tn]: the draft that draft t continues, parents[b][t] < t;
+ *              -1: it continues the sequence itself; -2: no token (padding of a batch of
+ *              trees of different sizes)
+ *   Draft t has as depth the number of drafts above it, sits at position cache_lens[b] +
+ *   depth and is stored in cache row cache_lens[b] + t:
+ *     k_cache row = RoPE_position(k_new[b, :, t]) rounded to the cache's type, v_cache row =
+ *     v_new[b, :, t] likewise;
+ *     out[b, h, t] = softmax over rows j < cache_lens[b] and the rows of t and of the drafts
+ *     above it of scale * RoPE_position(q_new[b, h, t]) . k_j, times v_j.
+ *   Padding: its output is 0 (lse -inf), no draft sees it; its cache row is written, too.
+ *   q_new [B, Hq, Tn, d], k_new, v_new [B, Hkv, Tn, d] bf16, not rotated
+ *   k_scale, v_scale  the codes of an 8-bit cache (cache_dtype CSATTN_E4M3); NULL for a bf16
+ *              cache (CSATTN_BF16)
+ *   cache_lens device int32 [B], 0 <= cache_lens[b] <= max_seq_len - Tn; not modified
+ *   out        [B, Hq, Tn, d] bf16;  lse  NULL or fp32 [B, Hq, Tn] (natural log)
+ *   rope_base, rope_layout  as csattn_attn_fwd;  scale, num_splits as csattn_attn_decode
+ *   max_seq_len  bounds cache_lens[b] + Tn (<= Lmax; <= 49152 with RoPE)
+ *   workspace  >= csattn_tree_workspace_size() bytes, 16-byte aligned, in use until the work on
+ *              `stream` completes (calls that may run at once need one each)
+ * Requirements: 1 <= Tn <= 256, d in {64, 128}, any Hq / Hkv.  Values of drafts that a query
+ * does not see have no part in its output whatever they hold (NaN and infinities included).
+ * Rows at or past cache_lens[b] + Tn are neither used nor written.  A length out of range or
+ * an invalid parent (parents[b][t] >= t, < -2, or a parent that is padding) raises
+ * CSATTN_ERR_DEVICE_ARG in the status word, leaves that sequence's cache as it was and makes
+ * its output 0; a page index outside the pool raises it, its rows read as zeros and are not
+ * written.
+ */
+int csattn_attn_tree_step(const void* q_new, const void* k_new, const void* v_new, void* k_cache,
+                          void* v_cache, void* k_scale, void* v_scale, const int32_t* cache_lens,
+                          const int32_t* parents, void* out, float* lse, int B, int Hq, int Hkv,
+                          int Tn, int Lmax, int d, int cache_dtype, float rope_base,
+                          int rope_layout, float scale, int max_seq_len, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int csattn_attn_tree_step_paged(const void* q_new, const void* k_new, const void* v_new,
+                                void* k_pages, void* v_pages, void* k_scale, void* v_scale,
+                                const int32_t* block_table, const int32_t* cache_lens,
+                                const int32_t* parents, void* out, float* lse, int B, int Hq,
+                                int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                                int d, int cache_dtype, float rope_base, int rope_layout,
+                                float scale, int max_seq_len, int num_splits, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * Keeps the accepted path of a verified tree: accepted[b] is its last draft (-1: none is
+ * accepted), the path a_0 < a_1 < ... < a_n-1 = accepted[b] that draft and those above it.
+ * Row cache_lens[b] + a_i of every KV head moves to row cache_lens[b] + i (keys and values,
+ * and the scale codes of an 8-bit cache; keys carry their position already), and
+ * new_lens[b] = cache_lens[b] + n.  The rows behind, up to cache_lens[b] + Tn, are free.
+ *   parents    as csattn_attn_tree_step;  accepted device int32 [B]
+ *   new_lens   device int32 [B], written; must not overlap the other arguments
+ * An accepted[b] outside [-1, Tn), an invalid parent on the path, padding, a length outside
+ * [0, Lmax - Tn] or a page index outside the pool on the path raises CSATTN_ERR_DEVICE_ARG in
+ * the status word; that sequence's rows are left as they were and new_lens[b] = cache_lens[b].
+ */
+int csattn_tree_commit(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                       const int32_t* cache_lens, const int32_t* parents, const int32_t* accepted,
+                       int32_t* new_lens, int B, int Hkv, int Tn, int Lmax, int d, int cache_dtype,
+                       void* stream);
+int csattn_tree_commit_paged(void* k_pages, void* v_pages, void* k_scale, void* v_scale,
+                             const int32_t* block_table, const int32_t* cache_lens,
+                             const int32_t* parents, const int32_t* accepted, int32_t* new_lens,
+                             int B, int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                             int d, int cache_dtype, void* stream);
 
 /*
  * Synchronize `stream`, then read and clear this device's status word.

@@ -50,7 +50,8 @@ __all__ = [
     "round_to_bf16", "expand_kv_heads", "causal_additive_mask", "attention_scores",
     "attention", "attention_rows", "attention_lse", "attention_backward", "decode",
     "decode_paged", "decode_step", "merge_partials", "split_partials", "rope_rotate_transpose",
-    "cache_append", "cache_append_paged", "prefill_paged"]
+    "cache_append", "cache_append_paged", "prefill_paged", "round_to_e4m3", "e4m3_exponents",
+    "quantise_rows", "tree_ancestors", "tree_attention", "tree_path"]
 
 _BF16_MAX = float.fromhex("0x1.fep127")
 
@@ -507,6 +508,87 @@ def merge_partials(ms, ls, os):
     w = np.exp(ms - m)
     l_tot = np.sum(np.asarray(ls) * w)
     return (w[:, None] * np.asarray(os, dtype=np.float64)).sum(axis=0) / l_tot
+
+
+def round_to_e4m3(x):
+    """Nearest e4m3 value (ties to even; 4 significant bits, exponents -6..8, subnormal step
+    2^-9, largest 448), in float64.  Values that are not finite become NaN."""
+    x = np.asarray(x, dtype=np.float64)
+    fin = np.isfinite(x)
+    a = np.where(fin, x, 0.0)
+    e = np.clip(np.floor(np.log2(np.maximum(np.abs(a), 2.0 ** -60))), -6, None)
+    step = np.exp2(e - 3)
+    y = np.clip(np.round(a / step) * step, -448.0, 448.0)  # (np.round is ties to even)
+    return np.where(fin, y, np.nan)
+
+
+def e4m3_exponents(x, rotated: bool):
+    """Scale exponents of rows x [..., d]: the least e in [-124, 120] with a <= 448 * 2^e, a the
+    largest finite magnitude of the row (times sqrt(2) for keys about to be rotated)."""
+    x = np.asarray(_as_np(x), dtype=np.float64)
+    top = np.max(np.where(np.isfinite(x), np.abs(x), 0.0), axis=-1)
+    if rotated:
+        top = top * math.sqrt(2.0)
+    out = np.full(top.shape, 120, dtype=np.int64)
+    for e in range(120, -125, -1):
+        out = np.where(top <= 448.0 * 2.0 ** e, e, out)
+    return out
+
+
+def quantise_rows(x, exponents):
+    """(e4m3 values, the values they stand for) of rows x [..., d] with scales 2^exponents; at
+    the largest exponent finite values stop at 240, the last that bf16 holds times 2^120."""
+    s = np.exp2(np.asarray(exponents, dtype=np.float64))[..., None]
+    y = round_to_e4m3(np.asarray(x, dtype=np.float64) / s)
+    y = np.where(s == 2.0 ** 120, np.clip(y, -240.0, 240.0), y)
+    return y, y * s
+
+
+def tree_ancestors(parents):
+    """Boolean [T, T] of one tree: draft j is draft t or above it (padding, parent -2: nothing).
+    Raises ValueError for an invalid parent."""
+    parents = [int(p) for p in parents]
+    anc = np.zeros((len(parents), len(parents)), dtype=bool)
+    for t, p in enumerate(parents):
+        if p < -2 or p >= t or (p >= 0 and parents[p] == -2):
+            raise ValueError(f"parent {p} of draft {t}")
+        if p >= 0:
+            anc[t] = anc[p]
+        anc[t, t] = p != -2
+    return anc
+
+
+def tree_path(parents, last: int):
+    """Drafts from the root to `last` (empty for -1)."""
+    path = []
+    while last >= 0:
+        path.append(last)
+        last = int(parents[last])
+    return path[::-1]
+
+
+def tree_attention(q_rot, k_rows, v_rows, L: int, anc, scale=None):
+    """One sequence's drafts over its cache rows: q_rot [Hq, T, d] (rotated), k_rows, v_rows
+    [Hkv, L + T, d] (rotated keys; the drafts' rows last).  Draft t sees rows 0..L-1 and row
+    L + j where anc[t, j]; a draft that does not see itself (padding) gives 0.  Rows a query
+    does not see have no part in its sums.  Returns (out [Hq, T, d], lse [Hq, T])."""
+    Hq, T, d = q_rot.shape
+    sc = _default_scale(d, scale)
+    out = np.zeros((Hq, T, v_rows.shape[-1]))
+    lse = np.full((Hq, T), -np.inf)
+    rep = Hq // k_rows.shape[0]
+    for t in range(T):
+        if not anc[t, t]:
+            continue
+        seen = np.concatenate([np.arange(L), L + np.nonzero(anc[t])[0]])
+        for h in range(Hq):
+            k, v = k_rows[h // rep][seen], v_rows[h // rep][seen]
+            z = (k @ q_rot[h, t]) * sc
+            m = np.max(z)
+            p = np.exp(z - m)
+            out[h, t] = (p @ v) / p.sum()
+            lse[h, t] = m + math.log(p.sum())
+    return out, lse
 
 
 def _as_np(t):

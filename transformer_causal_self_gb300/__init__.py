@@ -22,12 +22,15 @@ __all__ = [
     "bwd_workspace_size", "bwd_ext_workspace_size", "decode_workspace_size",
     "decode_host_workspace_size", "decode_step_workspace_size", "check_status",
     "selftest_bounded_wait", "EXPORTED_SYMBOLS",
+    "cache_append_fp8", "cache_append_fp8_paged", "cache_read_fp8", "cache_read_fp8_paged",
+    "attn_decode_fp8", "attn_decode_fp8_paged", "attn_tree_step", "attn_tree_step_paged",
+    "tree_commit", "tree_commit_paged", "decode_fp8_workspace_size", "tree_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB: Optional[ctypes.CDLL] = None
 
-CSATTN_F32, CSATTN_BF16 = 0, 1
+CSATTN_F32, CSATTN_BF16, CSATTN_E4M3 = 0, 1, 2
 K_PREROTATED = 0x100
 _ROPE_LAYOUT = {"split_half": 0, "adjacent": 1}
 _STATUS = {0: "CSATTN_OK", -1: "CSATTN_ERR_INVALID_ARG", -2: "CSATTN_ERR_UNSUPPORTED",
@@ -76,6 +79,26 @@ _SIGNATURES = {
     "csattn_prefill_paged_workspace_size": (_c_size, [_c_int] * 5),
     "csattn_cache_append": (_c_int, [_vp] * 5 + [_c_int] * 6 + [_c_float, _c_int, _vp]),
     "csattn_cache_append_paged": (_c_int, [_vp] * 6 + [_c_int] * 8 + [_c_float, _c_int, _vp]),
+    "csattn_cache_append_fp8": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_c_float, _c_int, _vp]),
+    "csattn_cache_append_fp8_paged": (_c_int, [_vp] * 8 + [_c_int] * 8 + [_c_float, _c_int, _vp]),
+    "csattn_cache_read_fp8": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_vp]),
+    "csattn_cache_read_fp8_paged": (_c_int, [_vp] * 8 + [_c_int] * 8 + [_vp]),
+    "csattn_decode_fp8_workspace_size": (_c_size, [_c_int] * 6),
+    "csattn_attn_decode_fp8": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_c_float, _c_int, _c_float,
+                                                                  _c_int, _c_int, _vp, _c_size,
+                                                                  _vp]),
+    "csattn_attn_decode_fp8_paged": (_c_int, [_vp] * 8 + [_c_int] * 8 +
+                                     [_c_float, _c_int, _c_float, _c_int, _c_int, _vp, _c_size,
+                                      _vp]),
+    "csattn_tree_workspace_size": (_c_size, [_c_int] * 7),
+    "csattn_attn_tree_step": (_c_int, [_vp] * 11 + [_c_int] * 7 + [_c_float, _c_int, _c_float,
+                                                                  _c_int, _c_int, _vp, _c_size,
+                                                                  _vp]),
+    "csattn_attn_tree_step_paged": (_c_int, [_vp] * 12 + [_c_int] * 9 +
+                                    [_c_float, _c_int, _c_float, _c_int, _c_int, _vp, _c_size,
+                                     _vp]),
+    "csattn_tree_commit": (_c_int, [_vp] * 8 + [_c_int] * 6 + [_vp]),
+    "csattn_tree_commit_paged": (_c_int, [_vp] * 9 + [_c_int] * 8 + [_vp]),
     "csattn_check_status": (_c_int, [_vp]),
     "csattn_selftest_bounded_wait": (_c_int, [_c_int, _vp]),
     "csattn_last_error": (ctypes.c_char_p, []),
@@ -601,6 +624,370 @@ def cache_append_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.
                                          block_table.shape[1], d, _dtype_code(k_new),
                                          float(rope_base), _ROPE_LAYOUT[rope_layout],
                                          _stream_handle(stream)))
+
+
+# ------------------------------------------------- 8-bit cache and token trees
+# These calls check shapes, types and devices of every tensor, run on the tensors' device
+# (whichever is current) and, when they allocate an output or a workspace for a `stream` other
+# than the current one, tie it to that stream.
+
+def _tensor(name: str, t: torch.Tensor, shape, dtypes, device) -> int:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+_BF16, _I32, _F32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
+_E4M3 = (torch.float8_e4m3fn,)
+_SCALE = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _cuda_device(name: str, t: torch.Tensor, ndim: int) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be on a CUDA device")
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {ndim}")
+    return t.device
+
+
+class _Launch:
+    """The stream of a call and the tensors it allocates, on `device`."""
+
+    __slots__ = ("device", "stream", "handle", "foreign")
+
+    def __init__(self, device: torch.device, stream):
+        self.device = device
+        current = torch.cuda.current_stream(device)
+        self.stream = current if stream is None else stream
+        self.handle = _stream_handle(self.stream)
+        self.foreign = self.handle != current.cuda_stream
+
+    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.foreign:  # not handed out again before that stream's work is done
+            st = self.stream
+            t.record_stream(st if isinstance(st, torch.cuda.Stream)
+                            else torch.cuda.ExternalStream(self.handle, device=self.device))
+        return t
+
+    def workspace(self, given: Optional[torch.Tensor], need: int):
+        if given is None:
+            given = self.empty((max(need, 16),), torch.uint8)
+        elif given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"workspace: must be contiguous on {self.device}")
+        return given, given.data_ptr(), given.numel() * given.element_size()
+
+    def run(self, fn, *args) -> None:
+        if self.device.index == torch.cuda.current_device():
+            _check(fn(*args, self.handle))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(*args, self.handle))
+
+
+def _cache_ptrs(k, v, k_scale, v_scale, dev, dtypes):
+    """Pointers of a cache (4-D, [.., Hkv, rows, d]) and its scales; all of one shape."""
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"caches have 4 dimensions, got {len(shape)}")
+    dtypes = dtypes if dtypes is not None else (_E4M3 if k_scale is not None else _BF16)
+    ptrs = [_tensor("keys' cache", k, shape, dtypes, dev),
+            _tensor("values' cache", v, shape, dtypes, dev)]
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    if k_scale is None:
+        if k.dtype in _E4M3:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        return ptrs + [None, None]
+    return ptrs + [_tensor("k_scale", k_scale, shape[:3], _SCALE, dev),
+                   _tensor("v_scale", v_scale, shape[:3], _SCALE, dev)]
+
+
+def _table(block_table, B, dev) -> int:
+    if block_table.dim() != 2:
+        raise ValueError("block_table: 2 dimensions expected")
+    return _tensor("block_table", block_table, (B, block_table.shape[1]), _I32, dev)
+
+
+def _cache_sizes(k, block_table, B):
+    """Size arguments of a cache ([Lmax] or [page_size, num_pages, max_pages]), its rows a
+    sequence and its KV heads."""
+    if block_table is None:
+        if k.shape[0] != B:
+            raise ValueError(f"cache of {k.shape[0]} sequences for a batch of {B}")
+        return [k.shape[2]], k.shape[2]
+    return [k.shape[2], k.shape[0], block_table.shape[1]], k.shape[2] * block_table.shape[1]
+
+
+def _append_fp8(fn, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                rope_base, rope_layout, stream):
+    dev = _cuda_device("k_new", k_new, 4)
+    B, Hkv, Tn, d = k_new.shape
+    new = [_tensor("k_new", k_new, k_new.shape, _BF16, dev),
+           _tensor("v_new", v_new, k_new.shape, _BF16, dev)]
+    cache = _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev, _E4M3)
+    table = [] if block_table is None else [_table(block_table, B, dev)]
+    size, _ = _cache_sizes(k_cache, block_table, B)
+    if k_cache.shape[1] != Hkv or k_cache.shape[3] != d:
+        raise ValueError("k_new and the cache differ in heads or head size")
+    lens = _tensor("cache_lens", cache_lens, (B,), _I32, dev)
+    _Launch(dev, stream).run(fn, *new, *cache, *table, lens, B, Hkv, Tn, *size, d, CSATTN_BF16,
+                             float(rope_base), _ROPE_LAYOUT[rope_layout])
+
+
+def cache_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                     cache_lens: torch.Tensor, *, rope_base: float = 0.0,
+                     rope_layout: str = "split_half", stream=None) -> None:
+    """Append Tn tokens per sequence to an 8-bit cache (C: csattn_cache_append_fp8).
+
+    k_new, v_new [B,Hkv,Tn,d] bf16 (keys not rotated); caches [B,Hkv,Lmax,d] float8_e4m3fn;
+    k_scale, v_scale [B,Hkv,Lmax] (uint8 or float8_e8m0fnu: a row stands for its values times
+    2^(code - 127)); cache_lens int32 [B] on the device, not advanced.
+    """
+    _append_fp8(load_library().csattn_cache_append_fp8, k_new, v_new, k_cache, v_cache, k_scale,
+                v_scale, None, cache_lens, rope_base, rope_layout, stream)
+
+
+def cache_append_fp8_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                           v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           block_table: torch.Tensor, cache_lens: torch.Tensor, *,
+                           rope_base: float = 0.0, rope_layout: str = "split_half",
+                           stream=None) -> None:
+    """cache_append_fp8 into pages [num_pages,Hkv,page_size,d], scales [num_pages,Hkv,page_size]
+    (C: csattn_cache_append_fp8_paged)."""
+    _append_fp8(load_library().csattn_cache_append_fp8_paged, k_new, v_new, k_pages, v_pages,
+                k_scale, v_scale, block_table, cache_lens, rope_base, rope_layout, stream)
+
+
+def _read_fp8(fn, k, v, k_scale, v_scale, block_table, seq_lens, k_out, v_out, stream):
+    dev = _cuda_device("seq_lens", seq_lens, 1)
+    B = seq_lens.shape[0]
+    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, _E4M3)
+    table = [] if block_table is None else [_table(block_table, B, dev)]
+    size, rows = _cache_sizes(k, block_table, B)
+    Hkv, d = k.shape[1], k.shape[3]
+    lens = _tensor("seq_lens", seq_lens, (B,), _I32, dev)
+    call = _Launch(dev, stream)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        k_out, v_out = (call.empty((B, Hkv, rows, d), torch.bfloat16) for _ in range(2))
+    if k_out.dim() != 4:
+        raise ValueError("k_out: 4 dimensions expected")
+    shape = (B, Hkv, k_out.shape[2], d)
+    outs = [_tensor("k_out", k_out, shape, _BF16, dev), _tensor("v_out", v_out, shape, _BF16, dev)]
+    call.run(fn, *cache, *table, lens, *outs, B, Hkv, *size, shape[2], d, CSATTN_BF16)
+    return k_out, v_out
+
+
+def cache_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                   v_scale: torch.Tensor, seq_lens: torch.Tensor,
+                   k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None, *,
+                   stream=None):
+    """Rows 0..seq_lens[b]-1 of an 8-bit cache as bf16, exactly (C: csattn_cache_read_fp8).
+
+    k_out, v_out [B,Hkv,Lout,d] (allocated with Lout = Lmax when not given; rows at or past
+    seq_lens[b] are not written).  Returns (k_out, v_out).
+    """
+    return _read_fp8(load_library().csattn_cache_read_fp8, k_cache, v_cache, k_scale, v_scale,
+                     None, seq_lens, k_out, v_out, stream)
+
+
+def cache_read_fp8_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                         k_out: Optional[torch.Tensor] = None,
+                         v_out: Optional[torch.Tensor] = None, *, stream=None):
+    """cache_read_fp8 from pages (C: csattn_cache_read_fp8_paged); the outputs are contiguous,
+    [B,Hkv,Lout,d]."""
+    return _read_fp8(load_library().csattn_cache_read_fp8_paged, k_pages, v_pages, k_scale,
+                     v_scale, block_table, seq_lens, k_out, v_out, stream)
+
+
+def decode_fp8_workspace_size(B, Hq, Hkv, Lmax, d, num_splits: int = 0) -> int:
+    return int(load_library().csattn_decode_fp8_workspace_size(B, Hq, Hkv, Lmax, d, num_splits))
+
+
+def tree_workspace_size(B, Hq, Hkv, Tn, Lmax, d, num_splits: int = 0) -> int:
+    return int(load_library().csattn_tree_workspace_size(B, Hq, Hkv, Tn, Lmax, d, num_splits))
+
+
+def _decode_fp8(fn, q, k, v, k_scale, v_scale, block_table, seq_lens, out, rope_base, rope_layout,
+                scale, max_seq_len, num_splits, workspace, stream):
+    dev = _cuda_device("q", q, 4)
+    B, Hq, _, d = q.shape
+    qp = _tensor("q", q, (B, Hq, 1, d), _BF16, dev)
+    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, _E4M3)
+    table = [] if block_table is None else [_table(block_table, B, dev)]
+    size, rows = _cache_sizes(k, block_table, B)
+    Hkv = k.shape[1]
+    if k.shape[3] != d:
+        raise ValueError("q and the cache differ in head size")
+    lens = _tensor("seq_lens", seq_lens, (B,), _I32, dev)
+    call = _Launch(dev, stream)
+    if out is None:
+        out = call.empty((B, Hq, 1, d), torch.bfloat16)
+    op = _tensor("out", out, (B, Hq, 1, d), _BF16, dev)
+    if max_seq_len is None:
+        max_seq_len = rows
+    workspace, wp, wn = call.workspace(
+        workspace, 0 if workspace is not None
+        else decode_fp8_workspace_size(B, Hq, Hkv, max_seq_len, d, num_splits))
+    call.run(fn, qp, *cache, *table, lens, op, B, Hq, Hkv, *size, d, CSATTN_BF16,
+             float(rope_base), _ROPE_LAYOUT[rope_layout], float(scale), int(max_seq_len),
+             int(num_splits), wp, wn)
+    return out
+
+
+def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scale: torch.Tensor, v_scale: torch.Tensor, seq_lens: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, *, rope_base: float = 0.0,
+                    rope_layout: str = "split_half", scale: float = 0.0,
+                    max_seq_len: Optional[int] = None, num_splits: int = 0,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Decode over an 8-bit cache (C: csattn_attn_decode_fp8).
+
+    q [B,Hq,1,d] bf16, rotated here at seq_lens[b] - 1 when rope_base > 0; caches
+    [B,Hkv,Lmax,d] float8_e4m3fn with k_scale, v_scale [B,Hkv,Lmax] as cache_append_fp8 writes
+    them (the new token included); seq_lens int32 [B] on the device.  max_seq_len defaults to
+    Lmax (always a valid bound).
+    """
+    return _decode_fp8(load_library().csattn_attn_decode_fp8, q, k_cache, v_cache, k_scale,
+                       v_scale, None, seq_lens, out, rope_base, rope_layout, scale, max_seq_len,
+                       num_splits, workspace, stream)
+
+
+def attn_decode_fp8_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                          k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                          seq_lens: torch.Tensor, out: Optional[torch.Tensor] = None, *,
+                          rope_base: float = 0.0, rope_layout: str = "split_half",
+                          scale: float = 0.0, max_seq_len: Optional[int] = None,
+                          num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """attn_decode_fp8 over pages [num_pages,Hkv,page_size,d], scales [num_pages,Hkv,page_size]
+    (C: csattn_attn_decode_fp8_paged)."""
+    return _decode_fp8(load_library().csattn_attn_decode_fp8_paged, q, k_pages, v_pages, k_scale,
+                       v_scale, block_table, seq_lens, out, rope_base, rope_layout, scale,
+                       max_seq_len, num_splits, workspace, stream)
+
+
+def _tree_step(fn, q_new, k_new, v_new, k, v, k_scale, v_scale, block_table, cache_lens, parents,
+               out, lse, rope_base, rope_layout, scale, max_seq_len, num_splits, workspace, stream):
+    dev = _cuda_device("q_new", q_new, 4)
+    B, Hq, Tn, d = q_new.shape
+    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, None)
+    Hkv = k.shape[1]
+    if k.shape[3] != d:
+        raise ValueError("q_new and the cache differ in head size")
+    new = [_tensor("q_new", q_new, (B, Hq, Tn, d), _BF16, dev),
+           _tensor("k_new", k_new, (B, Hkv, Tn, d), _BF16, dev),
+           _tensor("v_new", v_new, (B, Hkv, Tn, d), _BF16, dev)]
+    table = [] if block_table is None else [_table(block_table, B, dev)]
+    size, rows = _cache_sizes(k, block_table, B)
+    lens = _tensor("cache_lens", cache_lens, (B,), _I32, dev)
+    tree = _tensor("parents", parents, (B, Tn), _I32, dev)
+    call = _Launch(dev, stream)
+    if out is None:
+        out = call.empty((B, Hq, Tn, d), torch.bfloat16)
+    op = _tensor("out", out, (B, Hq, Tn, d), _BF16, dev)
+    lp = None if lse is None else _tensor("lse", lse, (B, Hq, Tn), _F32, dev)
+    if max_seq_len is None:
+        max_seq_len = rows
+    workspace, wp, wn = call.workspace(
+        workspace, 0 if workspace is not None
+        else tree_workspace_size(B, Hq, Hkv, Tn, max_seq_len, d, num_splits))
+    call.run(fn, *new, *cache, *table, lens, tree, op, lp, B, Hq, Hkv, Tn, *size, d,
+             CSATTN_BF16 if k_scale is None else CSATTN_E4M3, float(rope_base),
+             _ROPE_LAYOUT[rope_layout], float(scale), int(max_seq_len), int(num_splits), wp, wn)
+    return out
+
+
+def attn_tree_step(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                   k_cache: torch.Tensor, v_cache: torch.Tensor, cache_lens: torch.Tensor,
+                   parents: torch.Tensor, out: Optional[torch.Tensor] = None, *,
+                   k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, rope_base: float = 0.0,
+                   rope_layout: str = "split_half", scale: float = 0.0,
+                   max_seq_len: Optional[int] = None, num_splits: int = 0,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A tree of drafted tokens appended to the cache and attended (C: csattn_attn_tree_step).
+
+    q_new [B,Hq,Tn,d], k_new/v_new [B,Hkv,Tn,d] bf16, not rotated; parents int32 [B,Tn]: the
+    draft that draft t continues (< t), -1 where it continues the sequence, -2 for padding.
+    Draft t sits at position cache_lens[b] + the number of drafts above it, is written to cache
+    row cache_lens[b] + t, and sees rows below cache_lens[b], the drafts above it and itself.
+    Caches [B,Hkv,Lmax,d]: bf16, or float8_e4m3fn with k_scale, v_scale [B,Hkv,Lmax].
+    max_seq_len bounds cache_lens + Tn (default Lmax).  lse: optional fp32 [B,Hq,Tn].
+    """
+    return _tree_step(load_library().csattn_attn_tree_step, q_new, k_new, v_new, k_cache, v_cache,
+                      k_scale, v_scale, None, cache_lens, parents, out, lse, rope_base,
+                      rope_layout, scale, max_seq_len, num_splits, workspace, stream)
+
+
+def attn_tree_step_paged(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                         k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                         cache_lens: torch.Tensor, parents: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, *,
+                         k_scale: Optional[torch.Tensor] = None,
+                         v_scale: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None, rope_base: float = 0.0,
+                         rope_layout: str = "split_half", scale: float = 0.0,
+                         max_seq_len: Optional[int] = None, num_splits: int = 0,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """attn_tree_step over pages [num_pages,Hkv,page_size,d] (C: csattn_attn_tree_step_paged)."""
+    return _tree_step(load_library().csattn_attn_tree_step_paged, q_new, k_new, v_new, k_pages,
+                      v_pages, k_scale, v_scale, block_table, cache_lens, parents, out, lse,
+                      rope_base, rope_layout, scale, max_seq_len, num_splits, workspace, stream)
+
+
+def _tree_commit(fn, k, v, k_scale, v_scale, block_table, cache_lens, parents, accepted, new_lens,
+                 stream):
+    dev = _cuda_device("parents", parents, 2)
+    B, Tn = parents.shape
+    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, None)
+    table = [] if block_table is None else [_table(block_table, B, dev)]
+    size, _ = _cache_sizes(k, block_table, B)
+    lens = _tensor("cache_lens", cache_lens, (B,), _I32, dev)
+    tree = _tensor("parents", parents, (B, Tn), _I32, dev)
+    acc = _tensor("accepted", accepted, (B,), _I32, dev)
+    call = _Launch(dev, stream)
+    if new_lens is None:
+        new_lens = call.empty((B,), torch.int32)
+    np_ = _tensor("new_lens", new_lens, (B,), _I32, dev)
+    call.run(fn, *cache, *table, lens, tree, acc, np_, B, k.shape[1], Tn, *size, k.shape[3],
+             CSATTN_BF16 if k_scale is None else CSATTN_E4M3)
+    return new_lens
+
+
+def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, cache_lens: torch.Tensor,
+                parents: torch.Tensor, accepted: torch.Tensor,
+                new_lens: Optional[torch.Tensor] = None, *,
+                k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """Keep the accepted path of a verified tree (C: csattn_tree_commit).
+
+    accepted int32 [B]: the last accepted draft of attn_tree_step, -1 for none.  The rows of
+    that draft and those above it move to rows cache_lens[b].. of the cache.  Returns new_lens
+    int32 [B], cache_lens plus their number (a tensor of its own, not cache_lens).
+    """
+    return _tree_commit(load_library().csattn_tree_commit, k_cache, v_cache, k_scale, v_scale,
+                        None, cache_lens, parents, accepted, new_lens, stream)
+
+
+def tree_commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                      cache_lens: torch.Tensor, parents: torch.Tensor, accepted: torch.Tensor,
+                      new_lens: Optional[torch.Tensor] = None, *,
+                      k_scale: Optional[torch.Tensor] = None,
+                      v_scale: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tree_commit over pages (C: csattn_tree_commit_paged)."""
+    return _tree_commit(load_library().csattn_tree_commit_paged, k_pages, v_pages, k_scale,
+                        v_scale, block_table, cache_lens, parents, accepted, new_lens, stream)
 
 
 def check_status(stream=None) -> None:

@@ -89,11 +89,24 @@ void rope_table(RopeTable* t, int d, double base) {
   }
 }
 
-// Largest position whose angle the kernels' Cody-Waite reduction keeps exact
-// (|k| < 2^13 multiples of 2 pi for theta_0 = 1).
-constexpr int kMaxRopePositions = 49152;
+// kMaxRopePositions (internal.h): the largest position whose angle the kernels' Cody-Waite
+// reduction keeps exact (|k| < 2^13 multiples of 2 pi for theta_0 = 1).
 
 }  // namespace
+
+int api_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return code;
+}
+int api_fail_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what); }
+int api_device_info(uint32_t** status, int* num_sms) { return device_info(status, num_sms); }
+bool api_valid_page_size(int page_size) { return valid_page_size(page_size); }
+void api_rope_table(RopeTable* t, int d, double base) { rope_table(t, d, base); }
 
 void set_last_error(const char* msg) { g_last_error = msg; }
 
@@ -123,6 +136,24 @@ bool make_tmap_bf16_3d(void* tmap_out, const void* base, int d, int rows, int pl
   CUresult r = encode(static_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                       const_cast<void*>(base), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_u8_3d(void* tmap_out, const void* base, int d, int rows, int planes,
+                     int box_rows) {
+  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (encode == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(planes)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d),
+                           static_cast<cuuint64_t>(d) * static_cast<cuuint64_t>(rows)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = encode(static_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                      const_cast<void*>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

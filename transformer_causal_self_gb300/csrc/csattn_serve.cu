@@ -1,0 +1,531 @@
+// C ABI of the 8-bit KV cache and of the token-tree calls: argument checks, split sizes,
+// workspace layout and dispatch.  See include/csattn.h for the contract of every entry point.
+#include <algorithm>
+#include <cmath>
+
+#include "csattn.h"
+#include "internal.h"
+
+namespace csattn {
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+constexpr int kMaxTree = 256;  // drafts of a tree
+
+// The paged arguments; *lmax receives the rows a sequence has room for.
+int check_pages(const char* fn, const int32_t* block_table, int Hkv, int page_size, int num_pages,
+                int max_pages, int* lmax) {
+  if (block_table == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: block_table must be non-null", fn);
+  if (!aligned(block_table, 4))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: block_table must be 4-byte aligned", fn);
+  if (!api_valid_page_size(page_size))
+    return api_fail(CSATTN_ERR_INVALID_ARG,
+                    "%s: page_size=%d must be 16, 32 or a multiple of 64 in [64, 65536]", fn,
+                    page_size);
+  if (num_pages < 1 || max_pages < 1)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: num_pages=%d and max_pages=%d must be >= 1", fn,
+                    num_pages, max_pages);
+  if (Hkv >= 1 && static_cast<long long>(num_pages) * Hkv > (1LL << 31) - 1)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: num_pages * Hkv too large", fn);
+  const long long rows = static_cast<long long>(max_pages) * page_size;
+  if (rows >= (1 << 30))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: max_pages * page_size too large", fn);
+  *lmax = static_cast<int>(rows);
+  return CSATTN_OK;
+}
+
+// The cache itself (its pointers, sizes and head width); `scales`: 1 wanted, 0 must be null.
+int check_cache(const char* fn, const KvCache& c, bool scales, const int32_t* lens, int B, int Hkv,
+                int d) {
+  if (c.k == nullptr || c.v == nullptr || lens == nullptr ||
+      (scales && (c.k_scale == nullptr || c.v_scale == nullptr)))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!scales && (c.k_scale != nullptr || c.v_scale != nullptr))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: a bf16 cache has no scales", fn);
+  if (B < 1 || Hkv < 1 || c.Lmax < 1)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: B=%d Hkv=%d Lmax=%d must be >= 1", fn, B, Hkv,
+                    c.Lmax);
+  if (d != 64 && d != 128)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: d=%d not in {64,128}", fn, d);
+  if (c.Lmax >= (1 << 30))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: %d cache rows too many", fn, c.Lmax);
+  if (B > 65535 || Hkv > 65535 || static_cast<long long>(B) * Hkv > (1LL << 31) - 1)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: B=%d or Hkv=%d too large", fn, B, Hkv);
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(lens, 4))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  return CSATTN_OK;
+}
+
+int check_dtype(const char* fn, int dtype) {
+  if (dtype == CSATTN_BF16) return CSATTN_OK;
+  return api_fail(dtype == CSATTN_F32 ? CSATTN_ERR_UNSUPPORTED : CSATTN_ERR_INVALID_ARG,
+                  "%s: only bf16 is implemented (dtype %d)", fn, dtype);
+}
+
+// positions: how many the call may rotate at
+int check_rope(const char* fn, float rope_base, int rope_layout, int positions) {
+  if (rope_layout != CSATTN_ROPE_SPLIT_HALF && rope_layout != CSATTN_ROPE_ADJACENT)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: unknown rope_layout %d", fn, rope_layout);
+  if (!std::isfinite(rope_base))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: rope_base must be finite", fn);
+  if (rope_base > 0.f && positions > kMaxRopePositions)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: RoPE supports positions < %d, got %d", fn,
+                    kMaxRopePositions, positions);
+  return CSATTN_OK;
+}
+
+int rope_of(float rope_base, int rope_layout, int d, RopeTable* th) {
+  if (!(rope_base > 0.f)) return 0;
+  api_rope_table(th, d, static_cast<double>(rope_base));
+  return rope_layout == CSATTN_ROPE_SPLIT_HALF ? 1 : 2;
+}
+
+int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int max_seq_len,
+                int lmax, int num_splits) {
+  if (Hq < 1 || Hq % Hkv != 0)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Hq=%d is not a multiple of Hkv=%d", fn, Hq, Hkv);
+  if (max_seq_len < T || max_seq_len > lmax)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: max_seq_len=%d not in [%d, Lmax=%d]", fn,
+                    max_seq_len, T, lmax);
+  if (num_splits < 0) return api_fail(CSATTN_ERR_INVALID_ARG, "%s: num_splits < 0", fn);
+  if (!std::isfinite(scale))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: scale not finite", fn);
+  if (static_cast<long long>(B) * Hq * T > (1LL << 31) - 1)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: B * Hq * queries too large", fn);
+  return CSATTN_OK;
+}
+
+// Rows of a query-row block of the attention kernel (launch_group_attn).
+int row_blocks(int rows) { return rows <= 16 ? 1 : (rows <= 32 ? 1 : (rows + 63) / 64); }
+
+// Cache rows per split.  Splits as long as 256 rows (a split costs a partial result per query
+// row and a CTA's start) as many as give every SM 32 CTAs, so that ragged lengths even out;
+// where even that leaves SMs idle (few heads and sequences), down to 64 rows, until there
+// are 4 CTAs per SM.
+constexpr long long kSms = 152;
+long long splits_for(long long per_sm, int B, int Hkv, int mblocks) {
+  const long long ctas = static_cast<long long>(B) * Hkv * mblocks;
+  return std::max<long long>(1, (kSms * per_sm + ctas - 1) / ctas);
+}
+int round64(long long x) { return static_cast<int>((x + 63) / 64 * 64); }
+int chunk_for(int B, int Hkv, int mblocks, int max_seq_len, int num_splits) {
+  if (num_splits > 0) return round64((max_seq_len + num_splits - 1LL) / num_splits);
+  const long long few = splits_for(4, B, Hkv, mblocks), many = splits_for(32, B, Hkv, mblocks);
+  const int fine = round64((max_seq_len + few - 1) / few);
+  if (fine < 256) return fine;
+  return std::max(256, round64((max_seq_len + many - 1) / many));
+}
+
+// Bytes of the splits' partial results for any max_seq_len <= Lmax.
+size_t partial_bytes(int B, int Hq, int Hkv, int T, int Lmax, int d, int num_splits) {
+  const int mb = row_blocks(T * (Hq / Hkv));
+  const long long most = num_splits > 0 ? num_splits : splits_for(32, B, Hkv, mb);
+  const long long splits = std::min<long long>(most, (static_cast<long long>(Lmax) + 63) / 64);
+  return static_cast<size_t>(B) * Hq * T * splits * (static_cast<size_t>(d) + 2) * 4;
+}
+
+bool sizes_ok(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
+  return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Lmax >= 1 && d >= 1 && num_splits >= 0;
+}
+
+int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+  if (workspace == nullptr || bytes < need || !aligned(workspace, 16))
+    return api_fail(CSATTN_ERR_WORKSPACE,
+                    "%s: needs a 16-byte aligned workspace of %zu bytes (got %zu)", fn, need,
+                    bytes);
+  return CSATTN_OK;
+}
+
+int encoder_ready(const char* fn) {
+  if (tensor_map_encoder() == nullptr)
+    return api_fail(CSATTN_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", fn);
+  return CSATTN_OK;
+}
+
+int append_fp8(const char* fn, const void* k_new, const void* v_new, const KvCache& c,
+               const int32_t* cache_lens, int B, int Hkv, int Tn, int d, int dtype,
+               float rope_base, int rope_layout, void* stream) {
+  int rc = check_cache(fn, c, true, cache_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (k_new == nullptr || v_new == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(k_new, 16) || !aligned(v_new, 16))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
+  if (Tn < 1 || Tn > c.Lmax)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Tn=%d not in [1, cache rows %d]", fn, Tn, c.Lmax);
+  if (static_cast<long long>(B) * Hkv * Tn * d >= (1LL << 33))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Tn=%d too large", fn, Tn);
+  if ((rc = check_rope(fn, rope_base, rope_layout, c.Lmax)) != CSATTN_OK) return rc;
+  RopeTable th{};
+  const int rope = rope_of(rope_base, rope_layout, d, &th);
+  uint32_t* status = nullptr;
+  int sms = 0;
+  if ((rc = api_device_info(&status, &sms)) != CSATTN_OK) return rc;
+  const cudaError_t e = launch_cache_append_fp8(k_new, v_new, c, cache_lens, B, Hkv, Tn, d, rope,
+                                                th, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "cache_append_fp8: kernel launch");
+}
+
+int read_fp8(const char* fn, const KvCache& c, const int32_t* seq_lens, void* k_out, void* v_out,
+             int B, int Hkv, int Lout, int d, int dtype, void* stream) {
+  int rc = check_cache(fn, c, true, seq_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (k_out == nullptr || v_out == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(k_out, 16) || !aligned(v_out, 16))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
+  if (Lout < 1) return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Lout=%d must be >= 1", fn, Lout);
+  if (Lout >= (1 << 24) || static_cast<long long>(B) * Hkv * Lout >= (1LL << 33))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Lout=%d too large", fn, Lout);
+  uint32_t* status = nullptr;
+  int sms = 0;
+  if ((rc = api_device_info(&status, &sms)) != CSATTN_OK) return rc;
+  const cudaError_t e = launch_cache_read_fp8(c, seq_lens, k_out, v_out, B, Hkv, Lout, d, status,
+                                              static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "cache_read_fp8: kernel launch");
+}
+
+int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* seq_lens, void* out,
+               int B, int Hq, int Hkv, int d, int dtype, float rope_base, int rope_layout,
+               float scale, int max_seq_len, int num_splits, void* workspace,
+               size_t workspace_bytes, void* stream) {
+  int rc = check_cache(fn, c, true, seq_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (q == nullptr || out == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
+  if ((rc = check_heads(fn, B, Hq, Hkv, 1, scale, max_seq_len, c.Lmax, num_splits)) != CSATTN_OK)
+    return rc;
+  if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
+  GroupArgs a{};
+  a.chunk = chunk_for(B, Hkv, row_blocks(Hq / Hkv), max_seq_len, num_splits);
+  a.n_splits = (max_seq_len + a.chunk - 1) / a.chunk;
+  const size_t rows = static_cast<size_t>(B) * Hq * a.n_splits;
+  if ((rc = check_workspace(fn, workspace, workspace_bytes, rows * (d + 2) * 4)) != CSATTN_OK)
+    return rc;
+  a.cache = c;
+  a.q = q;
+  a.lens = seq_lens;
+  a.rope = rope_of(rope_base, rope_layout, d, &a.theta);
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.T = 1;
+  a.d = d;
+  a.scale = scale > 0.f ? scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+  a.max_seq_len = max_seq_len;
+  a.min_len = 1;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + rows * d;
+  int sms = 0;
+  if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
+  if ((rc = encoder_ready(fn)) != CSATTN_OK) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_group_attn(a, st);
+  if (e != cudaSuccess) return api_fail_cuda(e, "attn_decode_fp8: kernel launch");
+  e = launch_group_merge(a, nullptr, nullptr, out, nullptr, st);
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "attn_decode_fp8: merge launch");
+}
+
+// Workspace of a tree step: partials, then rotated queries, masks, lengths and value flags.
+struct TreeSpace {
+  size_t q_rot, anc, lens, vflag, total;
+  TreeSpace(size_t partials, int B, int Hq, int Hkv, int Tn, int d) {
+    const size_t words = (Tn + 31) / 32;
+    q_rot = align256(partials);
+    anc = q_rot + align256(static_cast<size_t>(B) * Hq * Tn * d * 2);
+    lens = anc + align256(static_cast<size_t>(B) * Tn * words * 4);
+    vflag = lens + align256(static_cast<size_t>(B) * 4);
+    total = vflag + align256(static_cast<size_t>(B) * Hkv * Tn);
+  }
+};
+
+int tree_step(const char* fn, const void* q_new, const void* k_new, const void* v_new,
+              const KvCache& c, const int32_t* cache_lens, const int32_t* parents, void* out,
+              float* lse, int B, int Hq, int Hkv, int Tn, int d, int cache_dtype, float rope_base,
+              int rope_layout, float scale, int max_seq_len, int num_splits, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  if (cache_dtype != CSATTN_BF16 && cache_dtype != CSATTN_E4M3)
+    return api_fail(cache_dtype == CSATTN_F32 ? CSATTN_ERR_UNSUPPORTED : CSATTN_ERR_INVALID_ARG,
+                    "%s: the cache is bf16 or e4m3 (cache_dtype %d)", fn, cache_dtype);
+  int rc = check_cache(fn, c, cache_dtype == CSATTN_E4M3, cache_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (q_new == nullptr || k_new == nullptr || v_new == nullptr || parents == nullptr ||
+      out == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(q_new, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(out, 16) ||
+      !aligned(parents, 4) || !aligned(lse, 4))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if (Tn < 1) return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Tn=%d must be >= 1", fn, Tn);
+  if (Tn > kMaxTree)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Tn=%d exceeds %d drafts", fn, Tn, kMaxTree);
+  if ((rc = check_heads(fn, B, Hq, Hkv, Tn, scale, max_seq_len, c.Lmax, num_splits)) != CSATTN_OK)
+    return rc;
+  if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
+  GroupArgs a{};
+  a.chunk = chunk_for(B, Hkv, row_blocks(Tn * (Hq / Hkv)), max_seq_len, num_splits);
+  a.n_splits = (max_seq_len + a.chunk - 1) / a.chunk;
+  const size_t rows = static_cast<size_t>(B) * Hq * Tn * a.n_splits;
+  const TreeSpace at(rows * (d + 2) * 4, B, Hq, Hkv, Tn, d);
+  if ((rc = check_workspace(fn, workspace, workspace_bytes, at.total)) != CSATTN_OK) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+
+  TreePrepArgs p{};
+  p.q_new = q_new;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.cache = c;
+  p.cache_lens = cache_lens;
+  p.parents = parents;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Tn = Tn;
+  p.d = d;
+  p.max_seq_len = max_seq_len;
+  p.rope = rope_of(rope_base, rope_layout, d, &p.theta);
+  p.q_rot = ws + at.q_rot;
+  p.anc = reinterpret_cast<uint32_t*>(ws + at.anc);
+  p.lens = reinterpret_cast<int32_t*>(ws + at.lens);
+  p.vflag = ws + at.vflag;
+  p.words = (Tn + 31) / 32;
+  int sms = 0;
+  if ((rc = api_device_info(&p.status, &sms)) != CSATTN_OK) return rc;
+  if ((rc = encoder_ready(fn)) != CSATTN_OK) return rc;
+
+  a.cache = c;
+  a.q = p.q_rot;
+  a.lens = p.lens;
+  a.anc = p.anc;
+  a.drafts = Tn;
+  a.words = p.words;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.T = Tn;
+  a.d = d;
+  a.scale = scale > 0.f ? scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+  a.max_seq_len = max_seq_len;
+  a.min_len = 0;
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = a.part_o + rows * d;
+  a.after_prep = true;
+  a.status = p.status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_tree_prep(p, st);
+  if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: append launch");
+  e = launch_group_attn(a, st);
+  if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: kernel launch");
+  e = launch_group_merge(a, p.vflag, v_new, out, lse, st);
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "attn_tree_step: merge launch");
+}
+
+int tree_commit(const char* fn, const KvCache& c, const int32_t* cache_lens,
+                const int32_t* parents, const int32_t* accepted, int32_t* new_lens, int B, int Hkv,
+                int Tn, int d, int cache_dtype, void* stream) {
+  if (cache_dtype != CSATTN_BF16 && cache_dtype != CSATTN_E4M3)
+    return api_fail(cache_dtype == CSATTN_F32 ? CSATTN_ERR_UNSUPPORTED : CSATTN_ERR_INVALID_ARG,
+                    "%s: the cache is bf16 or e4m3 (cache_dtype %d)", fn, cache_dtype);
+  int rc = check_cache(fn, c, cache_dtype == CSATTN_E4M3, cache_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (parents == nullptr || accepted == nullptr || new_lens == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(parents, 4) || !aligned(accepted, 4) || !aligned(new_lens, 4))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if (Tn < 1 || Tn > c.Lmax)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Tn=%d not in [1, cache rows %d]", fn, Tn, c.Lmax);
+  if (Tn > kMaxTree)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Tn=%d exceeds %d drafts", fn, Tn, kMaxTree);
+  // every KV head's CTA reads the lengths while one writes the new ones
+  const uintptr_t n0 = reinterpret_cast<uintptr_t>(new_lens), n1 = n0 + 4ull * B;
+  for (const void* in : {static_cast<const void*>(cache_lens), static_cast<const void*>(accepted),
+                         static_cast<const void*>(parents)}) {
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(in);
+    const uintptr_t i1 = i0 + 4ull * B * (in == parents ? Tn : 1);
+    if (n0 < i1 && i0 < n1)
+      return api_fail(CSATTN_ERR_INVALID_ARG, "%s: new_lens overlaps an input", fn);
+  }
+  uint32_t* status = nullptr;
+  int sms = 0;
+  if ((rc = api_device_info(&status, &sms)) != CSATTN_OK) return rc;
+  const cudaError_t e = launch_tree_commit(c, cache_lens, parents, accepted, new_lens, B, Hkv, Tn,
+                                           d, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "tree_commit: kernel launch");
+}
+
+KvCache contiguous(const void* k, const void* v, const void* ks, const void* vs, int Lmax) {
+  KvCache c{};
+  c.k = const_cast<void*>(k);
+  c.v = const_cast<void*>(v);
+  c.k_scale = const_cast<void*>(ks);
+  c.v_scale = const_cast<void*>(vs);
+  c.Lmax = Lmax;
+  return c;
+}
+KvCache paged(const void* k, const void* v, const void* ks, const void* vs,
+              const int32_t* block_table, int lmax, int page_size, int num_pages, int max_pages) {
+  KvCache c = contiguous(k, v, ks, vs, lmax);
+  c.block_table = block_table;
+  c.page_size = page_size;
+  c.num_pages = num_pages;
+  c.max_pages = max_pages;
+  return c;
+}
+
+}  // namespace
+}  // namespace csattn
+
+using namespace csattn;
+
+extern "C" {
+
+int csattn_cache_append_fp8(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                            void* k_scale, void* v_scale, const int32_t* cache_lens, int B,
+                            int Hkv, int Tn, int Lmax, int d, int dtype, float rope_base,
+                            int rope_layout, void* stream) {
+  return append_fp8("cache_append_fp8", k_new, v_new,
+                    contiguous(k_cache, v_cache, k_scale, v_scale, Lmax), cache_lens, B, Hkv, Tn,
+                    d, dtype, rope_base, rope_layout, stream);
+}
+
+int csattn_cache_append_fp8_paged(const void* k_new, const void* v_new, void* k_pages,
+                                  void* v_pages, void* k_scale, void* v_scale,
+                                  const int32_t* block_table, const int32_t* cache_lens, int B,
+                                  int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                                  int d, int dtype, float rope_base, int rope_layout,
+                                  void* stream) {
+  const char* fn = "cache_append_fp8_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return append_fp8(fn, k_new, v_new,
+                    paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                          num_pages, max_pages),
+                    cache_lens, B, Hkv, Tn, d, dtype, rope_base, rope_layout, stream);
+}
+
+int csattn_cache_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
+                          const void* v_scale, const int32_t* seq_lens, void* k_out, void* v_out,
+                          int B, int Hkv, int Lmax, int Lout, int d, int dtype, void* stream) {
+  return read_fp8("cache_read_fp8", contiguous(k_cache, v_cache, k_scale, v_scale, Lmax), seq_lens,
+                  k_out, v_out, B, Hkv, Lout, d, dtype, stream);
+}
+
+int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const void* k_scale,
+                                const void* v_scale, const int32_t* block_table,
+                                const int32_t* seq_lens, void* k_out, void* v_out, int B, int Hkv,
+                                int page_size, int num_pages, int max_pages, int Lout, int d,
+                                int dtype, void* stream) {
+  const char* fn = "cache_read_fp8_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return read_fp8(fn,
+                  paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                        num_pages, max_pages),
+                  seq_lens, k_out, v_out, B, Hkv, Lout, d, dtype, stream);
+}
+
+size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
+  if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits)) return 0;
+  return partial_bytes(B, Hq, Hkv, 1, Lmax, d, num_splits);
+}
+
+int csattn_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
+                           const void* k_scale, const void* v_scale, const int32_t* seq_lens,
+                           void* out, int B, int Hq, int Hkv, int Lmax, int d, int dtype,
+                           float rope_base, int rope_layout, float scale, int max_seq_len,
+                           int num_splits, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return decode_fp8("attn_decode_fp8", q, contiguous(k_cache, v_cache, k_scale, v_scale, Lmax),
+                    seq_lens, out, B, Hq, Hkv, d, dtype, rope_base, rope_layout, scale,
+                    max_seq_len, num_splits, workspace, workspace_bytes, stream);
+}
+
+int csattn_attn_decode_fp8_paged(const void* q, const void* k_pages, const void* v_pages,
+                                 const void* k_scale, const void* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                 int B, int Hq, int Hkv, int page_size, int num_pages,
+                                 int max_pages, int d, int dtype, float rope_base, int rope_layout,
+                                 float scale, int max_seq_len, int num_splits, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const char* fn = "attn_decode_fp8_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return decode_fp8(fn, q,
+                    paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                          num_pages, max_pages),
+                    seq_lens, out, B, Hq, Hkv, d, dtype, rope_base, rope_layout, scale,
+                    max_seq_len, num_splits, workspace, workspace_bytes, stream);
+}
+
+size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int d,
+                                  int num_splits) {
+  if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits) || Tn < 1 || Tn > kMaxTree) return 0;
+  return TreeSpace(partial_bytes(B, Hq, Hkv, Tn, Lmax, d, num_splits), B, Hq, Hkv, Tn, d).total;
+}
+
+int csattn_attn_tree_step(const void* q_new, const void* k_new, const void* v_new, void* k_cache,
+                          void* v_cache, void* k_scale, void* v_scale, const int32_t* cache_lens,
+                          const int32_t* parents, void* out, float* lse, int B, int Hq, int Hkv,
+                          int Tn, int Lmax, int d, int cache_dtype, float rope_base,
+                          int rope_layout, float scale, int max_seq_len, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return tree_step("attn_tree_step", q_new, k_new, v_new,
+                   contiguous(k_cache, v_cache, k_scale, v_scale, Lmax), cache_lens, parents, out,
+                   lse, B, Hq, Hkv, Tn, d, cache_dtype, rope_base, rope_layout, scale, max_seq_len,
+                   num_splits, workspace, workspace_bytes, stream);
+}
+
+int csattn_attn_tree_step_paged(const void* q_new, const void* k_new, const void* v_new,
+                                void* k_pages, void* v_pages, void* k_scale, void* v_scale,
+                                const int32_t* block_table, const int32_t* cache_lens,
+                                const int32_t* parents, void* out, float* lse, int B, int Hq,
+                                int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                                int d, int cache_dtype, float rope_base, int rope_layout,
+                                float scale, int max_seq_len, int num_splits, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  const char* fn = "attn_tree_step_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return tree_step(fn, q_new, k_new, v_new,
+                   paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                         num_pages, max_pages),
+                   cache_lens, parents, out, lse, B, Hq, Hkv, Tn, d, cache_dtype, rope_base,
+                   rope_layout, scale, max_seq_len, num_splits, workspace, workspace_bytes,
+                   stream);
+}
+
+int csattn_tree_commit(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                       const int32_t* cache_lens, const int32_t* parents, const int32_t* accepted,
+                       int32_t* new_lens, int B, int Hkv, int Tn, int Lmax, int d, int cache_dtype,
+                       void* stream) {
+  return tree_commit("tree_commit", contiguous(k_cache, v_cache, k_scale, v_scale, Lmax),
+                     cache_lens, parents, accepted, new_lens, B, Hkv, Tn, d, cache_dtype, stream);
+}
+
+int csattn_tree_commit_paged(void* k_pages, void* v_pages, void* k_scale, void* v_scale,
+                             const int32_t* block_table, const int32_t* cache_lens,
+                             const int32_t* parents, const int32_t* accepted, int32_t* new_lens,
+                             int B, int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                             int d, int cache_dtype, void* stream) {
+  const char* fn = "tree_commit_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return tree_commit(fn,
+                     paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                           num_pages, max_pages),
+                     cache_lens, parents, accepted, new_lens, B, Hkv, Tn, d, cache_dtype, stream);
+}
+
+}  // extern "C"

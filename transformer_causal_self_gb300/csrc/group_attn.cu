@@ -1,0 +1,766 @@
+// Attention of a few query rows per KV head over a cache, bf16 or e4m3: the decode of an
+// 8-bit cache (one query per head) and the drafts of a token tree (T queries per head).
+//
+// All T * Hq/Hkv query rows of a KV head read the same cache rows, so they are the rows of
+// one matrix product and every cache row is read from HBM once per 16 * WM of them.  Grid
+// (split * row block, KV head, sequence); a CTA takes `chunk` cache rows of its sequence:
+//   warp NW       TMA producer: 64-row K and V tiles into a ring
+//   warps 0..NW-1 WM row tiles of 16 query rows x WK slices of the tile's keys: S = Q K^T and
+//                 O += P V by mma.sync m16n8k16, softmax statistics in fp32 between the two.
+// The splits are merged by group_merge_kernel.
+//
+// e4m3 rows k8 * 2^ek, v8 * 2^ev enter the products as f16 (exact), never scaled:
+//   S column j:  x_j = (q16 . k8_j) * 2^ek_j * row factor  (q is taken to f16 with its largest
+//                channel in [2^14, 2^15): f16 has more bits than the bf16 it came from, and
+//                channels below 2^-38 of the largest vanish)
+//   denominator: sum_j 2^(x_j - m)      with m the running maximum of x
+//   numerator:   sum_j w_j v8_j, w_j = 2^((x_j - m) + ev_j - n), n that of (x - m) + ev
+// Two maxima keep w_j in f16's range whatever the values' scales: a row with small values and
+// a large weight (a first token that takes up attention) counts in full.  n is relative to m, so
+// that no exponent is lost beside a large score.  w is rounded to f16
+// (11 bits) scaled by 2^7, so what is below 2^-32 of the largest vanishes; the bf16 cache's
+// P is rounded to bf16 (8 bits), as in the other bf16 kernels; sums are fp32 throughout.
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace csattn {
+namespace {
+
+constexpr int KT = 64;  // cache rows per tile
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 100000000ull;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kWeightLog2 = 7.0f;  // e4m3: w is held times 2^7 (w <= 2^(8 + 7) < 65504)
+
+template <int D, bool F8, int WM>
+struct Cfg {
+  static constexpr int WK = WM == 4 ? 2 : 4;  // key slices side by side
+  static constexpr int NW = WM * WK;
+  static constexpr int kThreads = 32 * (NW + 1);
+  static constexpr int ROW = F8 ? D : 2 * D;
+  static constexpr int TILE = KT * ROW;
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? 4 : 6);
+  static constexpr int RING = NS * STAGE;
+  static constexpr int Q_BYTES = 16 * WM * D * 2;
+  static constexpr int ML_BYTES = NW * 16 * 3 * 4;
+  static constexpr int SMEM = 1024 + RING + Q_BYTES + 256 + ML_BYTES + 16 * WM * 4;
+  static_assert(NW * 16 * D * 4 <= RING, "per-warp results fit in the ring");
+};
+
+struct GParams {
+  const __nv_bfloat16* q;
+  const int32_t* lens;
+  const uint32_t* anc;
+  CacheRows rows;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  int drafts, words, rope;
+  int box_rows;
+  float* part_o;
+  float* part_ml;
+  uint32_t* status;
+  int Hq, Hkv, T, rep, max_seq_len, min_len, chunk, n_splits, mblocks;
+  float scale_log2;
+  RopeTable theta;
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool F8>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (F8) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// byte offset of the 16-byte chunk cc of row r of a TMA tile: bf16 tiles are 64-channel
+// blocks of 128-byte rows, e4m3 tiles rows of D bytes; the swizzle is as wide as the row
+template <int D, bool F8>
+__device__ __forceinline__ uint32_t tile_off(int r, int cc) {
+  if constexpr (!F8) return (cc >> 3) * (KT * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
+  if constexpr (D == 128) return r * 128 + ((cc ^ (r & 7)) << 4);
+  return r * 64 + ((cc ^ ((r >> 1) & 3)) << 4);
+}
+
+// the 16 mask bits of drafts j0.. (j0 > -16) of a query with mask words `anc`; the rows
+// before the drafts (j < 0) are seen by every query
+__device__ __forceinline__ uint32_t draft_bits(const uint32_t* anc, int words, int j0) {
+  if (words == 0) return j0 >= 0 ? 0u : (1u << -j0) - 1u;
+  if (j0 < 0) return ((anc[0] << -j0) | ((1u << -j0) - 1u)) & 0xffffu;
+  const int w = j0 >> 5;
+  if (w >= words) return 0u;
+  return __funnelshift_r(anc[w], w + 1 < words ? anc[w + 1] : 0u, j0 & 31) & 0xffffu;
+}
+
+// zero the halves (bf16) or bytes (e4m3) of a word that hold an infinity or NaN
+template <bool F8>
+__device__ __forceinline__ uint32_t finite_word(uint32_t w) {
+  if constexpr (F8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (((w >> (8 * i)) & 0x7fu) == 0x7fu) w &= ~(0xffu << (8 * i));
+  } else {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  }
+  return w;
+}
+
+template <int D, bool F8, int WM>
+__global__ void __launch_bounds__(Cfg<D, F8, WM>::kThreads)
+    group_attn_kernel(const __grid_constant__ GParams p, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v) {
+  using C = Cfg<D, F8, WM>;
+  constexpr int NS = C::NS, NW = C::NW, WK = C::WK;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + C::RING);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING + C::Q_BYTES);
+  uint64_t* empty = full + NS;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
+  float* s_ml = reinterpret_cast<float*>(smem + C::RING + C::Q_BYTES + 256);  // [NW][16][3]
+  float* s_qf = s_ml + NW * 16 * 3;                                           // [16 * WM]
+
+  const int split = blockIdx.x / p.mblocks, mb = blockIdx.x - split * p.mblocks;
+  const int kvh = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // what launch_tree_prep wrote is visible from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // let the merge be scheduled once every CTA has started; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int L = p.lens[b];  // rows that every query sees
+  if (L < p.min_len || L > p.max_seq_len - p.drafts) {
+    // (launch_tree_prep has reported what it marks with -1)
+    if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && (p.drafts == 0 || L != -1))
+      atomicOr(p.status, kStatusDeviceArg);
+    return;
+  }
+  const int total = L + p.drafts;
+  const int k_begin = split * p.chunk;
+  const int k_end = min(total, k_begin + p.chunk);
+  if (k_begin >= k_end) return;  // the merge reads only splits that hold rows
+  const int ntiles = (k_end - k_begin + KT - 1) / KT;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NW);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == NW) {
+    // ------------------------------------------------------------ producer
+    // lane i copies box i of a tile (paged: boxes of box_rows rows never cross a page; a
+    // box past the sequence, or a page index outside the pool, which is reported, reads
+    // zeros: its plane is past the tensor map).  Lane 0 waits and arms the stage first.
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    const CacheRows& R = p.rows;
+    const int nbox = KT / p.box_rows;
+    int issued = 0;
+    for (int t = 0; t < ntiles; ++t) {
+      const int s = t % NS, use = t / NS;
+      int plane = b * p.Hkv + kvh, prow = k_begin + t * KT;
+      const int r0 = lane * p.box_rows;
+      if (lane < nbox && R.block_table != nullptr) {
+        const int tr = prow + r0;
+        plane = R.num_pages * p.Hkv;
+        prow = 0;
+        if (tr < total) {
+          const int page = R.block_table[static_cast<size_t>(b) * R.max_pages + tr / R.page_size];
+          if (page >= 0 && page < R.num_pages)
+            plane = page * p.Hkv + kvh;
+          else
+            atomicOr(p.status, kStatusDeviceArg);
+          prow = tr % R.page_size;
+        }
+      }
+      int okw = 1;
+      if (lane == 0) {
+        if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
+          okw = 0;
+        else
+          mbar_arrive_expect_tx(&full[s], C::STAGE);
+      }
+      okw = __shfl_sync(0xffffffffu, okw, 0);
+      if (!okw) break;
+      if (lane < nbox) {
+        uint8_t* kd = smem + s * C::STAGE + r0 * (F8 ? D : 128);
+        uint8_t* vd = kd + C::TILE;
+        constexpr int kBlocks = F8 ? 1 : D / 64;
+        for (int kb = 0; kb < kBlocks; ++kb)
+          tma_load_3d(kd + kb * (KT * 128), &tm_k, &full[s], kb * 64, prow, plane);
+        for (int kb = 0; kb < kBlocks; ++kb)
+          tma_load_3d(vd + kb * (KT * 128), &tm_v, &full[s], kb * 64, prow, plane);
+      }
+      __syncwarp();
+      ++issued;
+    }
+    if (lane == 0 && *abort_flag) {
+      const int first = issued > NS ? issued - NS : 0;
+      for (int t = first; t < issued; ++t)
+        mbar_wait(&full[t % NS], (t / NS) & 1, nullptr, p.status, kDrainNs);
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- compute warps
+  const int mw = warp / WK, kw = warp % WK;
+  const int M = p.T * p.rep;            // query rows of the KV head: row = t * rep + head
+  const int row_base = mb * (16 * WM);  // first of this CTA
+
+  // scale bytes of the warp's slice of a tile: lanes 0..15 the keys', 16..31 the values';
+  // rows past the sequence and pages outside the pool read 0 (their data is zero or masked)
+  auto load_codes = [&](int t, int sl) -> uint32_t {
+    if constexpr (!F8) return 0u;
+    if (t >= ntiles) return 0u;
+    const int r = k_begin + t * KT + 16 * (kw + WK * sl) + (lane & 15);
+    if (r >= total) return 0u;
+    const long long at = p.rows.at(b, kvh, r);
+    if (at < 0) return 0u;
+    return (lane < 16 ? p.k_scale : p.v_scale)[at];
+  };
+  constexpr int NSL = 4 / WK;
+  uint32_t codes[NSL];
+#pragma unroll
+  for (int sl = 0; sl < NSL; ++sl) codes[sl] = load_codes(0, sl);
+
+  // queries into shared memory: D/16 lanes per row, 16 channels each
+  {
+    constexpr int G = D / 16;
+    for (int r = threadIdx.x / G; r < 16 * WM; r += 32 * NW / G) {
+      const int c = threadIdx.x % G, row = row_base + r;
+      int e0, e1;
+      rope_piece(p.rope, D / 2, c, &e0, &e1);
+      uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+      if (row < M) {
+        const int t = row / p.rep, h = kvh * p.rep + row - t * p.rep;
+        const __nv_bfloat16* x =
+            p.q + ((static_cast<size_t>(b) * p.Hq + h) * p.T + t) * static_cast<size_t>(D);
+        lo = *reinterpret_cast<const uint4*>(x + e0);
+        hi = *reinterpret_cast<const uint4*>(x + e1);
+      }
+      if (p.rope != 0) {
+        float cs[8], sn[8], y[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          rope_cos_sin<false>(L - 1, p.theta.hi[8 * c + j], p.theta.lo[8 * c + j], cs[j], sn[j]);
+        rope16(lo, hi, p.rope, cs, sn, y);
+        lo = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                        pack_bf16x2(y[6], y[7]));
+        hi = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]),
+                        pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
+      }
+      if constexpr (F8) {
+        bool bad;
+        const uint32_t top = row_absmax<G>(lo, hi, &bad);
+        // 2^(14 - exponent of the largest channel), kept to normal numbers
+        const int E = min(max(static_cast<int>(top >> 7), 15), 254);
+        const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+        uint32_t ol[4], oh[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ol[j] = pack_f16x2(bf16lo_to_f32(wl[j]) * f, bf16hi_to_f32(wl[j]) * f);
+          oh[j] = pack_f16x2(bf16lo_to_f32(wh[j]) * f, bf16hi_to_f32(wh[j]) * f);
+        }
+        lo = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+        hi = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        if (c == 0)
+          s_qf[r] = __uint_as_float(static_cast<uint32_t>(E - 14) << 23) * p.scale_log2;
+      }
+      *reinterpret_cast<uint4*>(s_q + r * D + e0) = lo;
+      *reinterpret_cast<uint4*>(s_q + r * D + e1) = hi;
+    }
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
+
+  const int r0 = lane >> 2;      // fragment rows r0 and r0 + 8
+  const int cq = 2 * (lane & 3);  // fragment column pair
+  uint32_t qa[D / 16][4];
+  float qf[2] = {p.scale_log2, p.scale_log2};
+  {
+    const uint16_t* q0 = s_q + (16 * mw + r0) * D;
+    const uint16_t* q8 = q0 + 8 * D;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      // e4m3: a thread's four bytes of a K row are channels 4(lane%4).. of the 16, so the
+      // product's index runs over the channels in that order in both operands
+      const int c0 = 16 * kk + (F8 ? 2 * cq : cq), c1 = c0 + (F8 ? 2 : 8);
+      qa[kk][0] = *reinterpret_cast<const uint32_t*>(q0 + c0);
+      qa[kk][1] = *reinterpret_cast<const uint32_t*>(q8 + c0);
+      qa[kk][2] = *reinterpret_cast<const uint32_t*>(q0 + c1);
+      qa[kk][3] = *reinterpret_cast<const uint32_t*>(q8 + c1);
+    }
+    if constexpr (F8) {
+      qf[0] = s_qf[16 * mw + r0];
+      qf[1] = s_qf[16 * mw + r0 + 8];
+    }
+  }
+  const uint32_t* anc[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = min((row_base + 16 * mw + r0 + 8 * h) / p.rep, p.T - 1);
+    anc[h] = p.anc + (static_cast<size_t>(b) * p.T + t) * p.words;
+  }
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  float m_used[2] = {-INFINITY, -INFINITY};  // of x, rows r0 and r0 + 8
+  float n_used[2] = {-INFINITY, -INFINITY};  // of (x - m_used) + ev (e4m3)
+  float l_part[2] = {0.f, 0.f};
+  const uint32_t smem_base = smem_u32(smem);
+
+  bool ok = true;
+  for (int t = 0; t < ntiles; ++t) {
+    const int s = t % NS;
+    uint32_t next[NSL];
+#pragma unroll
+    for (int sl = 0; sl < NSL; ++sl) next[sl] = load_codes(t + 1, sl);
+    if (!mbar_wait(&full[s], (t / NS) & 1, abort_flag, p.status, kWaitNs)) {
+      ok = false;
+      break;
+    }
+    const uint32_t kbase = smem_base + s * C::STAGE;
+    const uint32_t vbase = kbase + C::TILE;
+    bool wrote = false;
+#pragma unroll
+    for (int sl = 0; sl < NSL; ++sl) {
+      const int slice = kw + WK * sl;
+      const int key0 = k_begin + t * KT + 16 * slice;  // first cache row of the slice
+      const int mi = lane >> 3;                        // which 8x8 matrix this lane addresses
+      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      {
+        const int kr = 16 * slice + (lane & 7) + 8 * (mi >> 1);
+        if constexpr (F8) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; kk += 2) {
+            uint32_t w[4];
+            ldsm_x4(kbase + tile_off<D, F8>(kr, kk + (mi & 1)), w);
+            mma<F8>(sc[0], qa[kk], e4m3x2_to_f16x2(w[0]), e4m3x2_hi_to_f16x2(w[0]));
+            mma<F8>(sc[1], qa[kk], e4m3x2_to_f16x2(w[2]), e4m3x2_hi_to_f16x2(w[2]));
+            mma<F8>(sc[0], qa[kk + 1], e4m3x2_to_f16x2(w[1]), e4m3x2_hi_to_f16x2(w[1]));
+            mma<F8>(sc[1], qa[kk + 1], e4m3x2_to_f16x2(w[3]), e4m3x2_hi_to_f16x2(w[3]));
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t w[4];
+            ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + (mi & 1)), w);
+            mma<F8>(sc[0], qa[kk], w[0], w[1]);
+            mma<F8>(sc[1], qa[kk], w[2], w[3]);
+          }
+        }
+      }
+      // which of the slice's 16 rows each of the two query rows sees
+      const bool edge = key0 + 16 > min(L, k_end);
+      uint32_t see[2] = {0xffffu, 0xffffu};
+      if (edge) {
+        const uint32_t in = key0 + 16 <= k_end ? 0xffffu
+                            : key0 >= k_end    ? 0u
+                                               : (1u << (k_end - key0)) - 1u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          see[h] = in & (key0 + 16 <= L ? 0xffffu : draft_bits(anc[h], p.words, key0 - L));
+      }
+      float x[2][4], ev[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float kf[2] = {1.f, 1.f};
+        if constexpr (F8) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            kf[e] = __uint_as_float(__shfl_sync(0xffffffffu, codes[sl], 8 * nt + cq + e) << 23);
+            ev[nt][e] = static_cast<float>(static_cast<int>(
+                            __shfl_sync(0xffffffffu, codes[sl], 16 + 8 * nt + cq + e)) - 127);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = e >> 1;
+          float v = sc[nt][e] * qf[h];
+          if constexpr (F8) v = sc[nt][e] * kf[e & 1] * qf[h];
+          v = (see[h] >> (8 * nt + cq + (e & 1))) & 1u ? v : -INFINITY;
+          x[nt][e] = v;
+          mx[h] = fmaxf(mx[h], v);
+        }
+      }
+      float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
+      bool need = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        if (mx[h] > m_used[h] + kRescaleThreshold) {
+          const float r = m_used[h] - mx[h];
+          l_part[h] *= ex2_approx(r);  // 0 when m_used was -inf
+          if constexpr (F8) {
+            n_used[h] += r;  // the numerator's reference m + n stays where it was
+          } else {
+            f[h] = ex2_approx(r);
+            need = true;
+          }
+          m_used[h] = mx[h];
+        }
+        // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
+        const float m_ref = m_used[h] == -INFINITY ? 0.f : m_used[h];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          x[nt][2 * h] -= m_ref;
+          x[nt][2 * h + 1] -= m_ref;
+        }
+        if constexpr (F8) {
+          float my = fmaxf(fmaxf(x[0][2 * h] + ev[0][0], x[0][2 * h + 1] + ev[0][1]),
+                           fmaxf(x[1][2 * h] + ev[1][0], x[1][2 * h + 1] + ev[1][1]));
+          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 1));
+          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 2));
+          if (my > n_used[h] + kRescaleThreshold) {
+            f[h] = ex2_approx(n_used[h] - my);
+            n_used[h] = my;
+            need = true;
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][0] *= f[0];
+          o[n][1] *= f[0];
+          o[n][2] *= f[1];
+          o[n][3] *= f[1];
+        }
+      }
+      float w[2][4], n_ref[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        n_ref[h] = n_used[h] == -INFINITY ? 0.f : n_used[h] - kWeightLog2;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = ex2_approx(x[nt][e]);
+          l_part[e >> 1] += v;
+          w[nt][e] = F8 ? ex2_approx(x[nt][e] + (ev[nt][e & 1] - n_ref[e >> 1])) : v;
+        }
+      uint32_t pa[4];
+      if constexpr (F8) {
+        pa[0] = pack_f16x2(w[0][0], w[0][1]);
+        pa[1] = pack_f16x2(w[0][2], w[0][3]);
+        pa[2] = pack_f16x2(w[1][0], w[1][1]);
+        pa[3] = pack_f16x2(w[1][2], w[1][3]);
+      } else {
+        pa[0] = pack_bf16x2(w[0][0], w[0][1]);
+        pa[1] = pack_bf16x2(w[0][2], w[0][3]);
+        pa[2] = pack_bf16x2(w[1][0], w[1][1]);
+        pa[3] = pack_bf16x2(w[1][2], w[1][3]);
+      }
+      // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
+      // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
+      // merge puts it where it belongs).  Warps that share the slice write the same words.
+      if (key0 + 16 > min(L, k_end)) {
+        uint8_t* vt = smem + s * C::STAGE + C::TILE;
+        for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
+          const int rr = e / (C::ROW / 16), cc = e % (C::ROW / 16);
+          uint4* at = reinterpret_cast<uint4*>(vt + tile_off<D, F8>(16 * slice + rr, cc));
+          if (key0 + rr >= k_end) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+          } else if (key0 + rr >= L) {
+            const uint4 v = *at;
+            *at = make_uint4(finite_word<F8>(v.x), finite_word<F8>(v.y), finite_word<F8>(v.z),
+                             finite_word<F8>(v.w));
+          }
+        }
+        wrote = true;
+        __syncwarp();
+      }
+      {
+        const int vr = 16 * slice + (lane & 7) + 8 * (mi & 1);
+        if constexpr (F8) {
+#pragma unroll
+          for (int cc = 0; cc < D / 16; cc += 2) {
+            // rows 0-7 and 8-15 of chunk cc, then of chunk cc + 1; a transposed load hands a
+            // thread channels (2n, 2n+1) of two keys: regrouped by channel, they are the
+            // operands of the even and of the odd channels' products
+            uint32_t r[4];
+            ldsm_x4_t(vbase + tile_off<D, F8>(vr, cc + (mi >> 1)), r);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a = __byte_perm(r[2 * j], 0u, 0x3120);
+              const uint32_t c = __byte_perm(r[2 * j + 1], 0u, 0x3120);
+              mma<F8>(o[2 * (cc + j)], pa, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(c));
+              mma<F8>(o[2 * (cc + j) + 1], pa, e4m3x2_hi_to_f16x2(a), e4m3x2_hi_to_f16x2(c));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int np = 0; np < D / 16; ++np) {
+            uint32_t r[4];
+            ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * np + (mi >> 1)), r);
+            mma<F8>(o[2 * np], pa, r[0], r[1]);
+            mma<F8>(o[2 * np + 1], pa, r[2], r[3]);
+          }
+        }
+      }
+    }
+    if (wrote) fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+#pragma unroll
+    for (int sl = 0; sl < NSL; ++sl) codes[sl] = next[sl];
+  }
+
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], 1);
+    l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], 2);
+  }
+  // all tiles consumed: the ring is free to hold the per-warp results
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
+  if (!ok || *abort_flag) return;
+  float* s_o = reinterpret_cast<float*>(smem);  // [NW][16][D]
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int rr = warp * 16 + r0 + 8 * h;
+    if ((lane & 3) == 0) {
+      s_ml[rr * 3 + 0] = m_used[h];
+      s_ml[rr * 3 + 1] = l_part[h];
+      s_ml[rr * 3 + 2] = n_used[h];
+    }
+    if constexpr (F8) {
+#pragma unroll
+      for (int cc = 0; cc < D / 16; ++cc)
+        *reinterpret_cast<float4*>(s_o + rr * D + 16 * cc + 2 * cq) =
+            make_float4(o[2 * cc][2 * h], o[2 * cc + 1][2 * h], o[2 * cc][2 * h + 1],
+                        o[2 * cc + 1][2 * h + 1]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(s_o + rr * D + 8 * n + cq) =
+            make_float2(o[n][2 * h], o[n][2 * h + 1]);
+    }
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
+  // merge the warps' key slices; one partial per query row, relative to the maximum of x
+  for (int e = threadIdx.x; e < 16 * WM * (D / 4); e += 32 * NW) {
+    const int r = e / (D / 4), c = e % (D / 4), row = row_base + r;
+    if (row >= M) continue;
+    const int w0 = (r / 16) * WK, rr = r % 16;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) m = fmaxf(m, s_ml[((w0 + w) * 16 + rr) * 3]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) {
+      const float* ml = s_ml + ((w0 + w) * 16 + rr) * 3;
+      // (a warp that saw nothing holds zeros, or NaN if its scores were NaN)
+      const bool none = ml[0] == -INFINITY;
+      l += (none ? 1.f : ex2_approx(ml[0] - m)) * ml[1];
+      const float fw = none ? 1.f : ex2_approx(F8 ? ml[0] - m + (ml[2] - kWeightLog2) : ml[0] - m);
+      const float4 v = *reinterpret_cast<const float4*>(s_o + ((w0 + w) * 16 + rr) * D + 4 * c);
+      acc.x += fw * v.x;
+      acc.y += fw * v.y;
+      acc.z += fw * v.z;
+      acc.w += fw * v.w;
+    }
+    const int t = row / p.rep, h = kvh * p.rep + row - t * p.rep;
+    const size_t at =
+        ((static_cast<size_t>(b) * p.Hq + h) * p.T + t) * static_cast<size_t>(p.n_splits) + split;
+    *reinterpret_cast<float4*>(p.part_o + at * D + 4 * c) = acc;
+    if (c == 0) {
+      p.part_ml[2 * at] = m;
+      p.part_ml[2 * at + 1] = l;
+    }
+  }
+}
+
+// out[b, h, t, :] = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the splits that hold
+// rows of sequence b.  A warp per query row, four (d = 128) or two channels per lane.
+template <int D>
+__global__ void __launch_bounds__(128) group_merge_kernel(
+    const float* __restrict__ part_o, const float* __restrict__ part_ml,
+    const int32_t* __restrict__ lens, const uint32_t* __restrict__ anc,
+    const uint8_t* __restrict__ vflag, const __nv_bfloat16* __restrict__ v_new, bool f8,
+    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int rows, int Hq, int Hkv, int T,
+    int drafts, int words, int n_splits, int chunk, int min_len, int max_seq_len) {
+  constexpr int V = D / 32;
+  const int row = static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= rows) return;
+  const int t = row % T, bh = row / T, b = bh / Hq, g = (bh - b * Hq) / (Hq / Hkv);
+  const int L = lens[b];
+  const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
+  int ns = 0;
+  if (L >= min_len && L <= max_seq_len - drafts) ns = (L + drafts + chunk - 1) / chunk;
+  if (drafts > 0 && ((mine[t >> 5] >> (t & 31)) & 1u) == 0u) ns = 0;  // not a token
+  const float* ml = part_ml + static_cast<size_t>(row) * n_splits * 2;
+  const float* po = part_o + static_cast<size_t>(row) * n_splits * D + V * lane;
+  float m = -INFINITY;
+  for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[2 * s]);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+  float acc[V], l = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < ns; ++s) {
+    const float ms = ml[2 * s];
+    const float f = ms == -INFINITY ? 1.f : ex2_approx(ms - m);  // (a split that saw nothing: 0)
+    l += f * ml[2 * s + 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += f * po[static_cast<size_t>(s) * D + i];
+  }
+  const bool any = !(l <= 0.f);  // NaN stays
+  const float inv = any ? 1.f / l : 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = any ? acc[i] * inv : 0.f;
+  if (vflag != nullptr && ns > 0) {
+    for (int w = 0; w < words; ++w) {
+      const int j = 32 * w + lane;
+      const bool hit = j < T && ((mine[w] >> lane) & 1u) &&
+                       vflag[(static_cast<size_t>(b) * Hkv + g) * T + j] != 0;
+      for (uint32_t left = __ballot_sync(0xffffffffu, hit); left != 0u; left &= left - 1u) {
+        const __nv_bfloat16* v =
+            v_new + ((static_cast<size_t>(b) * Hkv + g) * T + 32 * w + __ffs(left) - 1) * D;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float x = __bfloat162float(v[V * lane + i]);
+          // (an e4m3 cache holds NaN for an infinity)
+          if (!isfinite(x)) acc[i] += f8 ? __int_as_float(0x7fffffff) : x;
+        }
+      }
+    }
+  }
+  __nv_bfloat16* o = out + static_cast<size_t>(row) * D + V * lane;
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<uint32_t*>(o + i) = pack_bf16x2(acc[i], acc[i + 1]);
+  if (lse != nullptr && lane == 0)
+    lse[row] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, bool F8, int WM>
+cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, F8, WM>;
+  GParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.lens = a.lens;
+  p.anc = a.anc;
+  p.rows = CacheRows{a.cache.block_table, a.Hkv, a.cache.Lmax, a.cache.page_size,
+                     a.cache.num_pages, a.cache.max_pages};
+  p.k_scale = static_cast<const uint8_t*>(a.cache.k_scale);
+  p.v_scale = static_cast<const uint8_t*>(a.cache.v_scale);
+  p.drafts = a.drafts;
+  p.words = a.words;
+  p.rope = a.rope;
+  const bool paged = a.cache.block_table != nullptr;
+  p.box_rows = paged && a.cache.page_size < KT ? a.cache.page_size : KT;
+  p.part_o = a.part_o;
+  p.part_ml = a.part_ml;
+  p.status = a.status;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.T = a.T;
+  p.rep = a.Hq / a.Hkv;
+  p.max_seq_len = a.max_seq_len;
+  p.min_len = a.min_len;
+  p.chunk = a.chunk;
+  p.n_splits = a.n_splits;
+  p.mblocks = (a.T * p.rep + 16 * WM - 1) / (16 * WM);
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.theta = a.theta;
+
+  alignas(64) CUtensorMap tk, tv;
+  const int rows = paged ? a.cache.page_size : a.cache.Lmax;
+  const int planes = paged ? a.cache.num_pages * a.Hkv : a.B * a.Hkv;
+  auto* make = F8 ? make_tmap_u8_3d : make_tmap_bf16_3d;
+  if (!make(&tk, a.cache.k, D, rows, planes, p.box_rows) ||
+      !make(&tv, a.cache.v, D, rows, planes, p.box_rows))
+    return cudaErrorInvalidValue;
+  static SmemLimitOnce smem_limit;
+  cudaError_t e = smem_limit.set(group_attn_kernel<D, F8, WM>, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_splits) * p.mblocks, a.Hkv, a.B);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.after_prep ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, group_attn_kernel<D, F8, WM>, p, tk, tv);
+}
+
+template <int D, bool F8>
+cudaError_t launch_rows(const GroupArgs& a, cudaStream_t stream) {
+  const int rows = a.T * (a.Hq / a.Hkv);
+  if (rows <= 16) return launch_t<D, F8, 1>(a, stream);
+  if (rows <= 32) return launch_t<D, F8, 2>(a, stream);
+  return launch_t<D, F8, 4>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream) {
+  const bool f8 = a.cache.k_scale != nullptr;
+  if (a.d == 64) return f8 ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream);
+  return f8 ? launch_rows<128, true>(a, stream) : launch_rows<128, false>(a, stream);
+}
+
+cudaError_t launch_group_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
+                               void* out, float* lse, cudaStream_t stream) {
+  const int rows = a.B * a.Hq * a.T;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((static_cast<unsigned>(rows) + 3) / 4, 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(
+      &cfg, a.d == 128 ? group_merge_kernel<128> : group_merge_kernel<64>,
+      static_cast<const float*>(a.part_o), static_cast<const float*>(a.part_ml), a.lens, a.anc,
+      vflag, static_cast<const __nv_bfloat16*>(v_new), a.cache.k_scale != nullptr,
+      static_cast<__nv_bfloat16*>(out), lse, rows, a.Hq, a.Hkv, a.T, a.drafts, a.words,
+      a.n_splits, a.chunk, a.min_len, a.max_seq_len);
+}
+
+}  // namespace csattn

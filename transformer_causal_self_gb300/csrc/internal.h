@@ -173,6 +173,99 @@ cudaError_t launch_gather_pages_bf16(const void* k_pages, const void* v_pages,
                                      int Tq, int d, int page_size, int num_pages, int max_pages,
                                      int Lpad, uint32_t* status, cudaStream_t stream);
 
+// A KV cache: contiguous [B, Hkv, Lmax, d] (block_table == nullptr) or paged [num_pages,
+// Hkv, page_size, d] with Lmax = max_pages * page_size; bf16 (no scales) or e4m3 with one
+// scale byte per row and KV head ([B, Hkv, Lmax] or [num_pages, Hkv, page_size]; fp8.cuh).
+struct KvCache {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  const int32_t* block_table;
+  int Lmax, page_size, num_pages, max_pages;
+};
+
+// Quantising append: token t of sequence b to row cache_lens[b] + t, keys rotated there.
+cudaError_t launch_cache_append_fp8(const void* k_new, const void* v_new, const KvCache& cache,
+                                    const int32_t* cache_lens, int B, int Hkv, int Tn, int d,
+                                    int rope, const RopeTable& theta, uint32_t* status,
+                                    cudaStream_t stream);
+
+// Rows 0..seq_lens[b]-1 of an e4m3 cache as bf16 [B, Hkv, Lout, d]; other rows are left.
+cudaError_t launch_cache_read_fp8(const KvCache& cache, const int32_t* seq_lens, void* k_out,
+                                  void* v_out, int B, int Hkv, int Lout, int d, uint32_t* status,
+                                  cudaStream_t stream);
+
+// Grouped attention over a cache: T queries per sequence and query head, all T * Hq / Hkv
+// query rows of a KV head against its rows at once.  Sequence b has lens[b] rows that every
+// query sees (a negative length: none, its output is zero), then `drafts` rows of which
+// query t sees those in its bit mask anc[b, t] (words of 32 bits; drafts = 0: no such rows).
+struct GroupArgs {
+  KvCache cache;
+  const void* q;         // [B, Hq, T, d] bf16
+  const int32_t* lens;   // device [B]
+  const uint32_t* anc;   // device [B, T, words]
+  int drafts, words;
+  int rope;              // 0, or the layout in which q is rotated at position lens[b] - 1
+  RopeTable theta;
+  int B, Hq, Hkv, T, d;
+  float scale;
+  int max_seq_len;       // bound of lens[b] + drafts
+  int min_len;           // lens[b] below it or above max_seq_len - drafts is an error (decode: 1)
+  int chunk, n_splits;   // cache rows per split (a multiple of 64), splits
+  float* part_o;         // [B, Hq, T, n_splits, d]
+  float* part_ml;        // [B, Hq, T, n_splits, 2]
+  bool after_prep;       // launched behind launch_tree_prep (programmatic dependent launch)
+  uint32_t* status;
+};
+cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
+
+// Merge of the splits of launch_group_attn into out [B, Hq, T, d] bf16 and, if non-null, lse
+// [B, Hq, T].  vflag (with v_new; may be null): bytes [B, Hkv, T], set where v_new[b, g, t]
+// holds an infinity or NaN; such values left the products (launch_group_attn reads them as
+// zeros) and are put into the outputs of the queries that see them here.
+cudaError_t launch_group_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
+                               void* out, float* lse, cudaStream_t stream);
+
+// The work of a tree step ahead of its attention: checks lengths and parents, appends the
+// drafts' keys and values at rows L + t (keys rotated at L + depth), rotates the queries.
+struct TreePrepArgs {
+  const void* q_new;
+  const void* k_new;
+  const void* v_new;
+  KvCache cache;
+  const int32_t* cache_lens;
+  const int32_t* parents;  // [B, Tn]
+  int B, Hq, Hkv, Tn, d, max_seq_len;
+  int rope;
+  RopeTable theta;
+  void* q_rot;      // [B, Hq, Tn, d] bf16
+  uint32_t* anc;    // [B, Tn, words]
+  int32_t* lens;    // [B]: cache_lens, or -1 where a check failed
+  uint8_t* vflag;   // [B, Hkv, Tn]
+  int words;
+  uint32_t* status;
+};
+cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream);
+
+// Moves the rows of the accepted token's path (root first) to rows L, L + 1, ... and writes
+// new_lens[b] = L + their number.
+cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
+                               const int32_t* parents, const int32_t* accepted, int32_t* new_lens,
+                               int B, int Hkv, int Tn, int d, uint32_t* status,
+                               cudaStream_t stream);
+
+// 3-D map over rows of `d` bytes (64 or 128): box {d, box_rows, 1}, swizzle as wide as a row.
+bool make_tmap_u8_3d(void* tmap_out, const void* base, int d, int rows, int planes, int box_rows);
+
+// Shared by the C ABI's translation units (csattn_api.cu).
+int api_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int api_fail_cuda(cudaError_t e, const char* what);
+int api_device_info(uint32_t** status, int* num_sms);
+bool api_valid_page_size(int page_size);
+void api_rope_table(RopeTable* t, int d, double base);
+constexpr int kMaxRopePositions = 49152;  // largest position whose angle reduction is exact
+
 // Raises a kernel's dynamic shared-memory limit once per device (the attribute
 // lasts for the process), so repeated launches skip the driver call.
 struct SmemLimitOnce {

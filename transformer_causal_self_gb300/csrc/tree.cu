@@ -1,0 +1,265 @@
+// A tree of drafted tokens over a KV cache: what a step does ahead of its attention, and the
+// move of the accepted path afterwards.
+//
+// Draft t of sequence b (length L) has a parent p[t] < t among the drafts, -1 (its parent is
+// the sequence's last token) or -2 (no token: padding).  Its depth is the number of drafts
+// above it, its position L + depth, its cache row L + t.  With the position in the key, the
+// rows of an accepted path need only be moved to L, L + 1, ... once the tree is verified.
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace csattn {
+namespace {
+
+constexpr int kThreads = 256;  // >= the largest Tn
+constexpr int kWords = kThreads / 32;
+
+// Ancestor masks (self included; zero for padding) of a sequence's drafts into s_anc and
+// whether every parent is valid, by pointer doubling: after round r a token's mask holds
+// its 2^r nearest, and its pointer the next one above.  All kThreads threads call it.
+__device__ __forceinline__ bool tree_masks(const int32_t* parents, int Tn, int words,
+                                           uint32_t (*s_anc)[kWords], int* s_up) {
+  const int t = static_cast<int>(threadIdx.x);
+  int up = t < Tn ? parents[t] : -2;
+  bool bad = t < Tn && (up < -2 || up >= t);
+  s_up[t] = up;
+  __syncthreads();
+  if (!bad && up >= 0) bad = s_up[up] == -2;  // below padding
+  if (__syncthreads_or(bad)) return false;
+  for (int w = 0; w < words; ++w)
+    s_anc[t][w] = (up != -2 && (t >> 5) == w) ? 1u << (t & 31) : 0u;
+  while (__syncthreads_or(up >= 0)) {
+    uint32_t more[kWords];
+    int next = -1;
+    if (up >= 0) {
+      for (int w = 0; w < words; ++w) more[w] = s_anc[up][w];
+      next = s_up[up];
+    }
+    __syncthreads();
+    if (up >= 0) {
+      for (int w = 0; w < words; ++w) s_anc[t][w] |= more[w];
+      s_up[t] = next;
+      up = next;
+    }
+  }
+  return true;
+}
+
+// One CTA per (draft, sequence): the masks are worked out by every CTA (a few rounds in
+// shared memory), then the draft's rows, 16 channels per thread: keys rotated at its
+// position and values to the cache (bf16 or e4m3), queries rotated into q_rot.  A few
+// hundred KB at most: bound by launch and memory latency.
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads) tree_prep_kernel(
+    const __nv_bfloat16* __restrict__ q_new, const __nv_bfloat16* __restrict__ k_new,
+    const __nv_bfloat16* __restrict__ v_new, void* __restrict__ k_cache,
+    void* __restrict__ v_cache, uint8_t* __restrict__ k_scale, uint8_t* __restrict__ v_scale,
+    const int32_t* __restrict__ cache_lens, const int32_t* __restrict__ parents, CacheRows rows,
+    int Hq, int Tn, int max_seq_len, int rope, RopeTable theta, __nv_bfloat16* __restrict__ q_rot,
+    uint32_t* __restrict__ anc, int32_t* __restrict__ lens, uint8_t* __restrict__ vflag, int words,
+    uint32_t* status) {
+  constexpr int G = D / 16;
+  __shared__ uint32_t s_anc[kThreads][kWords];
+  __shared__ int s_up[kThreads];
+  __shared__ float s_cos[64], s_sin[64];
+  const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, Hkv = rows.Hkv;
+  // the attention kernel may be scheduled; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int L = cache_lens[b];
+  const bool fine = tree_masks(parents + static_cast<size_t>(b) * Tn, Tn, words, s_anc, s_up) &&
+                    L >= 0 && L <= max_seq_len - Tn;
+  if (tid == 0 && t == 0) {
+    lens[b] = fine ? L : -1;
+    if (!fine) atomicOr(status, kStatusDeviceArg);
+  }
+  if (!fine) return;  // the sequence's cache is left as it was
+  __syncthreads();
+  if (tid < words) anc[(static_cast<size_t>(b) * Tn + t) * words + tid] = s_anc[t][tid];
+  int depth = -1;
+  for (int w = 0; w < words; ++w) depth += __popc(s_anc[t][w]);
+  const int pos = L + max(depth, 0);  // (padding is written like a first token, never seen)
+  if (rope != 0 && tid < D / 2)
+    rope_cos_sin<false>(pos, theta.hi[tid], theta.lo[tid], s_cos[tid], s_sin[tid]);
+  __syncthreads();
+  const int items = (Hq + 2 * Hkv) * G;
+  for (int i0 = 0; i0 < items; i0 += kThreads) {  // (whole warps take part in the shuffles)
+    const int i = i0 + tid;
+    const bool live = i < items;
+    const int head = live ? i / G : 0, c = i % G;
+    const bool is_q = head < Hq, is_v = head >= Hq + Hkv;
+    const int g = is_q ? head : head - Hq - (is_v ? Hkv : 0);
+    const int layout = is_v ? 0 : rope;
+    int e0, e1;
+    rope_piece(layout, D / 2, c, &e0, &e1);
+    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+    if (live) {
+      const __nv_bfloat16* x =
+          (is_q ? q_new : (is_v ? v_new : k_new)) +
+          ((static_cast<size_t>(b) * (is_q ? Hq : Hkv) + g) * Tn + t) * static_cast<size_t>(D);
+      lo = *reinterpret_cast<const uint4*>(x + e0);
+      hi = *reinterpret_cast<const uint4*>(x + e1);
+    }
+    bool bad;
+    const uint32_t top = row_absmax<G>(lo, hi, &bad);
+    if (!live) continue;  // (no shuffle below)
+    float cs[8], sn[8], y[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      cs[j] = layout != 0 ? s_cos[8 * c + j] : 1.f;
+      sn[j] = layout != 0 ? s_sin[8 * c + j] : 0.f;
+    }
+    rope16(lo, hi, layout, cs, sn, y);
+    if (layout != 0) {
+      lo = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                      pack_bf16x2(y[6], y[7]));
+      hi = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]),
+                      pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
+    }
+    if (is_q) {
+      __nv_bfloat16* dst =
+          q_rot + ((static_cast<size_t>(b) * Hq + g) * Tn + t) * static_cast<size_t>(D);
+      *reinterpret_cast<uint4*>(dst + e0) = lo;
+      *reinterpret_cast<uint4*>(dst + e1) = hi;
+      continue;
+    }
+    if (is_v && c == 0) vflag[(static_cast<size_t>(b) * Hkv + g) * Tn + t] = bad ? 1 : 0;
+    const long long row = rows.at(b, g, L + t);
+    if (row < 0) {
+      if (c == 0) atomicOr(status, kStatusDeviceArg);
+      continue;
+    }
+    if constexpr (F8) {
+      const int code = scale_code(top, layout != 0);
+      uint8_t* dst = static_cast<uint8_t*>(is_v ? v_cache : k_cache) + row * D;
+      *reinterpret_cast<uint2*>(dst + e0) =
+          make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
+                     pack_e4m3x4(y[4], y[5], y[6], y[7], code, bad));
+      *reinterpret_cast<uint2*>(dst + e1) =
+          make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11], code, bad),
+                     pack_e4m3x4(y[12], y[13], y[14], y[15], code, bad));
+      if (c == 0) (is_v ? v_scale : k_scale)[row] = static_cast<uint8_t>(code);
+    } else {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? v_cache : k_cache) + row * D;
+      *reinterpret_cast<uint4*>(dst + e0) = lo;
+      *reinterpret_cast<uint4*>(dst + e1) = hi;
+    }
+  }
+}
+
+// The path of accepted[b] (its ancestors and itself, a_0 < a_1 < ...): row L + i receives row
+// L + a_i.  a_i >= i, so a row is read before it is overwritten when i goes up; a thread
+// owns one 16-byte piece (or a scale byte) of the rows of one KV head and moves it in order,
+// kBatch loads in flight.  CTA (KV head, sequence): latency-bound, a few KB each.
+constexpr int kBatch = 8;
+template <typename T>
+__device__ __forceinline__ void move_rows(T* base, const CacheRows& rows, int b, int g, int L,
+                                          const uint8_t* path, int n, int per, int at) {
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    T x[kBatch];
+    long long to[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      to[j] = -1;
+      if (i0 + j >= n || path[i0 + j] == i0 + j) continue;
+      const long long from = rows.at(b, g, L + path[i0 + j]);
+      to[j] = rows.at(b, g, L + i0 + j);
+      if (from < 0) to[j] = -1;
+      if (to[j] >= 0) x[j] = base[from * per + at];
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (to[j] >= 0) base[to[j] * per + at] = x[j];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) tree_commit_kernel(
+    uint4* k_cache, uint4* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+    const int32_t* __restrict__ cache_lens, const int32_t* __restrict__ parents,
+    const int32_t* __restrict__ accepted, int32_t* __restrict__ new_lens, CacheRows rows, int Tn,
+    int pieces, uint32_t* status) {
+  __shared__ int s_up[kThreads];
+  __shared__ uint8_t s_path[kThreads];
+  __shared__ int s_n;
+  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int L = cache_lens[b], last = accepted[b];
+  if (tid < Tn) s_up[tid] = parents[static_cast<size_t>(b) * Tn + tid];
+  __syncthreads();
+  if (tid < 32) {
+    // every lane walks up from the accepted token; a walk leaves the tree after at most Tn
+    // steps because each must go down in number
+    int n = 0, t = last;
+    bool bad = L < 0 || L > rows.Lmax - Tn || last < -1 || last >= Tn;
+    if (!bad)
+      while (t >= 0) {
+        const int up = s_up[t];
+        ++n;
+        if (up >= t || up < -1) {
+          bad = true;
+          break;
+        }
+        t = up;
+      }
+    if (!bad) {
+      t = last;
+      for (int i = n - 1; i >= 0; --i) {
+        if (tid == 0) s_path[i] = static_cast<uint8_t>(t);
+        t = s_up[t];
+      }
+      // a page outside the pool leaves the sequence as it was
+      __syncwarp();
+      if (rows.block_table != nullptr)
+        for (int i = tid; i < n; i += 32)
+          bad |= rows.at(b, g, L + i) < 0 || rows.at(b, g, L + s_path[i]) < 0;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (tid == 0) {
+      s_n = bad ? 0 : n;
+      if (g == 0) {
+        new_lens[b] = bad ? L : L + n;
+        if (bad) atomicOr(status, kStatusDeviceArg);
+      }
+    }
+  }
+  __syncthreads();
+  const int n = s_n;
+  if (tid < 2 * pieces) {
+    const bool is_v = tid >= pieces;
+    move_rows(is_v ? v_cache : k_cache, rows, b, g, L, s_path, n, pieces,
+              is_v ? tid - pieces : tid);
+  } else if (k_scale != nullptr && tid < 2 * pieces + 2) {
+    move_rows(tid == 2 * pieces ? k_scale : v_scale, rows, b, g, L, s_path, n, 1, 0);
+  }
+}
+
+CacheRows rows_of(const KvCache& c, int Hkv) {
+  return CacheRows{c.block_table, Hkv, c.Lmax, c.page_size, c.num_pages, c.max_pages};
+}
+
+}  // namespace
+
+cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
+  const bool f8 = a.cache.k_scale != nullptr;
+  auto* kernel = a.d == 128 ? (f8 ? tree_prep_kernel<128, true> : tree_prep_kernel<128, false>)
+                            : (f8 ? tree_prep_kernel<64, true> : tree_prep_kernel<64, false>);
+  kernel<<<dim3(a.Tn, a.B), kThreads, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(a.q_new), static_cast<const __nv_bfloat16*>(a.k_new),
+      static_cast<const __nv_bfloat16*>(a.v_new), a.cache.k, a.cache.v,
+      static_cast<uint8_t*>(a.cache.k_scale), static_cast<uint8_t*>(a.cache.v_scale),
+      a.cache_lens, a.parents, rows_of(a.cache, a.Hkv), a.Hq, a.Tn, a.max_seq_len, a.rope, a.theta,
+      static_cast<__nv_bfloat16*>(a.q_rot), a.anc, a.lens, a.vflag, a.words, a.status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
+                               const int32_t* parents, const int32_t* accepted, int32_t* new_lens,
+                               int B, int Hkv, int Tn, int d, uint32_t* status,
+                               cudaStream_t stream) {
+  const int pieces = d * (cache.k_scale != nullptr ? 1 : 2) / 16;
+  tree_commit_kernel<<<dim3(Hkv, B), kThreads, 0, stream>>>(
+      static_cast<uint4*>(cache.k), static_cast<uint4*>(cache.v),
+      static_cast<uint8_t*>(cache.k_scale), static_cast<uint8_t*>(cache.v_scale), cache_lens,
+      parents, accepted, new_lens, rows_of(cache, Hkv), Tn, pieces, status);
+  return cudaGetLastError();
+}
+
+}  // namespace csattn
