@@ -579,7 +579,7 @@ size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d,
  * csattn_attn_decode over an 8-bit cache: one new query per sequence, whose own key and value
  * are in the cache already.
  *   q         [B, Hq, 1, d] bf16; rotated here at position seq_lens[b] - 1 (and rounded to
- *             bf16) when rope_base > 0, used as given otherwise
+ *             11 bits) when rope_base > 0, used as given otherwise
  *   seq_lens  device int32 [B], 1 <= seq_lens[b] <= max_seq_len <= Lmax
  *   out       [B, Hq, 1, d] bf16
  *   num_splits  0: automatic; > 0: splits of every sequence's rows

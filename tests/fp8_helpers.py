@@ -16,6 +16,15 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device=dev())
 
 
+def round_query(x, e4m3):
+    """The rotated query as the products take it: bf16, or 11 significant bits with an 8-bit
+    cache (float64 in and out)."""
+    if not e4m3:
+        return OA.round_to_bf16(x)
+    m, e = np.frexp(x)
+    return np.ldexp(np.round(np.ldexp(m, 11)), e - 11)
+
+
 def values(k8, code):
     """What e4m3 rows and scale codes stand for, in float64."""
     return k8.float().cpu().double().numpy() * np.exp2(

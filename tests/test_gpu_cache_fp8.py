@@ -6,8 +6,8 @@ a key is rounded from an fp32 rotation whose error is below 2^-20 of the pair's 
 border: such a key is one e4m3 step away, 2^-3 of its value at most, and fewer than
 1 in 1000 do (the border's width over a step's, 2^-20 / 2^-4, times the two sides).
 A decode's output is bf16: it is held to the bounds of the bf16 decode (max-abs 2e-2, relative
-L2 5e-3), which allow for the bf16 rounding of output and rotated query (2^-9 rms each at
-most); the weights' f16 rounding, 2^-11, is below either.  Those bounds are for outputs below
+L2 5e-3), which allow for the bf16 rounding of the output (2^-9); the weights' f16 rounding,
+2^-11, is below it, and the query's 11 bits are the reference's, too.  Those bounds are for outputs below
 4; test_decode_parity's values reach 8 |N(0,1)|, so outputs of 8 and more occur, whose storing in
 bf16 alone costs half a step, 2^(e-8) for [2^e, 2^(e+1)): 2^-5 = 3.1e-2 at 8.  Its max-abs
 bound is 2e-2 plus that half step of the largest expected output.
@@ -165,7 +165,7 @@ def _expect(c, q, lens, base=0.0, layout="split_half", scale=None):
         k, v = H.rows(c, b, L)
         x = q[b, :, 0].double().numpy()
         if base > 0:
-            x = OA.round_to_bf16(OA.rope_rotate(x[:, None], np.array([L - 1]), base, layout))[:, 0]
+            x = H.round_query(OA.rope_rotate(x[:, None], np.array([L - 1]), base, layout), True)[:, 0]
         out[b] = OA.decode(torch.from_numpy(x)[None, :, None], torch.from_numpy(k)[None],
                            torch.from_numpy(v)[None], [L], scale=scale)[0]
     return out

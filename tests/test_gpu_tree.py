@@ -1,8 +1,8 @@
 """Token trees over a cache (csattn_attn_tree_step, csattn_tree_commit) against float64.
 
 Tolerances: outputs as in the other bf16 attention tests (max-abs 2e-2, relative L2 5e-3);
-lse: a sum of fp32 exponentials (each off by 2^-22) of scores that are off by the bf16 rounding
-of the rotated query alone, which the reference makes too, so 1e-3 covers fp32 sums of the
+lse: a sum of fp32 exponentials (each off by 2^-22) of scores that are off by the rounding of
+the rotated query alone (bf16, or 11 bits with an 8-bit cache), which the reference makes too, so 1e-3 covers fp32 sums of the
 d products (d * 2^-24 * |score| below 2^-10 here).  Appended rows: values bit-exact, rotated keys
 as in the append tests.
 """
@@ -87,7 +87,7 @@ def _check(c0, c1, q, k, v, parents, lens, out, lse, base, layout):
         assert np.all(np.abs(kk[:, L:] - kw) <= np.maximum(np.abs(kw) * step, top * 2.0 ** -15))
         qr = q[b].double().numpy()
         if base > 0:
-            qr = OA.round_to_bf16(OA.rope_rotate(qr, pos, base, layout))
+            qr = H.round_query(OA.rope_rotate(qr, pos, base, layout), "ks" in c1)
         ref[b], ref_lse[b] = OA.tree_attention(qr, kk, vv, L, anc)
     assert wrong <= max(2, 2e-3 * total), (wrong, total)
     assert_bf16_close(to_np(out), ref, "tree attention")

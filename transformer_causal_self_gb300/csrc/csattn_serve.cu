@@ -99,7 +99,7 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
 }
 
 // Rows of a query-row block of the attention kernel (launch_group_attn).
-int row_blocks(int rows) { return rows <= 16 ? 1 : (rows <= 32 ? 1 : (rows + 63) / 64); }
+int row_blocks(int rows) { return (rows + 31) / 32; }
 
 // Cache rows per split.  Splits as long as 256 rows (a split costs a partial result per query
 // row and a CTA's start) as many as give every SM 32 CTAs, so that ragged lengths even out;
@@ -236,11 +236,12 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
 
 // Workspace of a tree step: partials, then rotated queries, masks, lengths and value flags.
 struct TreeSpace {
-  size_t q_rot, anc, lens, vflag, total;
+  size_t q_rot, q_factor, anc, lens, vflag, total;
   TreeSpace(size_t partials, int B, int Hq, int Hkv, int Tn, int d) {
     const size_t words = (Tn + 31) / 32;
     q_rot = align256(partials);
-    anc = q_rot + align256(static_cast<size_t>(B) * Hq * Tn * d * 2);
+    q_factor = q_rot + align256(static_cast<size_t>(B) * Hq * Tn * d * 2);
+    anc = q_factor + align256(static_cast<size_t>(B) * Hq * Tn * 4);
     lens = anc + align256(static_cast<size_t>(B) * Tn * words * 4);
     vflag = lens + align256(static_cast<size_t>(B) * 4);
     total = vflag + align256(static_cast<size_t>(B) * Hkv * Tn);
@@ -292,6 +293,7 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   p.max_seq_len = max_seq_len;
   p.rope = rope_of(rope_base, rope_layout, d, &p.theta);
   p.q_rot = ws + at.q_rot;
+  p.q_factor = reinterpret_cast<float*>(ws + at.q_factor);
   p.anc = reinterpret_cast<uint32_t*>(ws + at.anc);
   p.lens = reinterpret_cast<int32_t*>(ws + at.lens);
   p.vflag = ws + at.vflag;
@@ -302,6 +304,7 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
 
   a.cache = c;
   a.q = p.q_rot;
+  a.q_factor = cache_dtype == CSATTN_E4M3 ? p.q_factor : nullptr;
   a.lens = p.lens;
   a.anc = p.anc;
   a.drafts = Tn;

@@ -123,6 +123,11 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t four) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Where the rows of a cache are: contiguous [B, Hkv, Lmax, ...] (block_table == nullptr)
 // or pages [num_pages, Hkv, page_size, ...].
 struct CacheRows {
@@ -174,6 +179,32 @@ __device__ __forceinline__ void rope16(const uint4& a, const uint4& b, int layou
 __device__ __forceinline__ void rope_piece(int layout, int half, int c, int* e0, int* e1) {
   *e0 = layout == 2 ? 16 * c : 8 * c;
   *e1 = layout == 2 ? 16 * c + 8 : half + 8 * c;
+}
+
+// A query row for the products with an e4m3 cache: 16 channels of it (bf16) in each of G lanes
+// are rotated at `pos` (rope != 0) in fp32 and rounded once, to f16, scaled by a power of two
+// that puts the largest channel before the rotation in [2^14, 2^15).  Returns what the scores
+// are multiplied by.  All lanes of the warp call it.
+template <int G>
+__device__ __forceinline__ float query_to_f16(uint4& lo, uint4& hi, int rope, int pos,
+                                              const RopeTable& theta, int c) {
+  bool bad;
+  const uint32_t top = row_absmax<G>(lo, hi, &bad);
+  const int E = min(max(static_cast<int>(top >> 7), 15), 254);  // (scales stay normal numbers)
+  const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
+  float cs[8], sn[8], y[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cs[j] = 1.f;
+    sn[j] = 0.f;
+    if (rope != 0) rope_cos_sin<false>(pos, theta.hi[8 * c + j], theta.lo[8 * c + j], cs[j], sn[j]);
+  }
+  rope16(lo, hi, rope, cs, sn, y);
+  lo = make_uint4(pack_f16x2(y[0] * f, y[1] * f), pack_f16x2(y[2] * f, y[3] * f),
+                  pack_f16x2(y[4] * f, y[5] * f), pack_f16x2(y[6] * f, y[7] * f));
+  hi = make_uint4(pack_f16x2(y[8] * f, y[9] * f), pack_f16x2(y[10] * f, y[11] * f),
+                  pack_f16x2(y[12] * f, y[13] * f), pack_f16x2(y[14] * f, y[15] * f));
+  return __uint_as_float(static_cast<uint32_t>(E - 14) << 23);
 }
 
 }  // namespace csattn

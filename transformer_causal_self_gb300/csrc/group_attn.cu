@@ -1,25 +1,31 @@
 // Attention of a few query rows per KV head over a cache, bf16 or e4m3: the decode of an
 // 8-bit cache (one query per head) and the drafts of a token tree (T queries per head).
 //
-// All T * Hq/Hkv query rows of a KV head read the same cache rows, so they are the rows of
-// one matrix product and every cache row is read from HBM once per 16 * WM of them.  Grid
-// (split * row block, KV head, sequence); a CTA takes `chunk` cache rows of its sequence:
-//   warp NW       TMA producer: 64-row K and V tiles into a ring
-//   warps 0..NW-1 WM row tiles of 16 query rows x WK slices of the tile's keys: S = Q K^T and
-//                 O += P V by mma.sync m16n8k16, softmax statistics in fp32 between the two.
-// The splits are merged by group_merge_kernel.
+// All T * Hq/Hkv query rows of a KV head read the same cache rows, so they are one side of a
+// matrix product and every cache row is read from HBM once per 8 * NT of them.  Grid (split *
+// row block, KV head, sequence); a CTA takes `chunk` cache rows of its sequence:
+//   warp 4      TMA producer: 64-row K and V tiles into a ring
+//   warps 0..3  16 cache rows each per tile, by mma.sync m16n8k16 with the cache rows (then the
+//               channels) on the side of 16 and the query rows on the side of 8:
+//               S^T = K Q^T, then O^T += V^T P^T; softmax statistics in fp32 between the two.
+// With one query per head a KV head has 4 or 8 query rows: on the side of 8 nothing or little
+// is padding, which halves products, exponentials and accumulators against the other way
+// round, and an e4m3 row is taken to f16 once for all query rows.  The splits are merged by
+// group_merge_kernel.
 //
 // e4m3 rows k8 * 2^ek, v8 * 2^ev enter the products as f16 (exact), never scaled:
 //   S column j:  x_j = (q16 . k8_j) * 2^ek_j * row factor  (q is taken to f16 with its largest
-//                channel in [2^14, 2^15): f16 has more bits than the bf16 it came from, and
-//                channels below 2^-38 of the largest vanish)
+//                channel in [2^14, 2^15.5): 11 bits, and channels below 2^-38 of the largest
+//                vanish)
 //   denominator: sum_j 2^(x_j - m)      with m the running maximum of x
 //   numerator:   sum_j w_j v8_j, w_j = 2^((x_j - m) + ev_j - n), n that of (x - m) + ev
 // Two maxima keep w_j in f16's range whatever the values' scales: a row with small values and
 // a large weight (a first token that takes up attention) counts in full.  n is relative to m, so
-// that no exponent is lost beside a large score.  w is rounded to f16
-// (11 bits) scaled by 2^7, so what is below 2^-32 of the largest vanishes; the bf16 cache's
-// P is rounded to bf16 (8 bits), as in the other bf16 kernels; sums are fp32 throughout.
+// that no exponent is lost beside a large score.  w is rounded to f16 (11 bits) scaled by 2^7,
+// so what is below 2^-32 of the largest vanishes; the bf16 cache's P is rounded to bf16 (8
+// bits), as in the other bf16 kernels; sums are fp32 throughout.
+// A maximum is raised only when a score exceeds it by 2^8, and only then do the lanes exchange
+// theirs: the usual tile costs one vote.
 #include "fp8.cuh"
 #include "internal.h"
 
@@ -27,29 +33,34 @@ namespace csattn {
 namespace {
 
 constexpr int KT = 64;  // cache rows per tile
+constexpr int NW = 4;   // compute warps, 16 rows of a tile each
+constexpr int kThreads = 32 * (NW + 1);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kWeightLog2 = 7.0f;  // e4m3: w is held times 2^7 (w <= 2^(8 + 7) < 65504)
 
-template <int D, bool F8, int WM>
+template <int D, bool F8, int NT>
 struct Cfg {
-  static constexpr int WK = WM == 4 ? 2 : 4;  // key slices side by side
-  static constexpr int NW = WM * WK;
-  static constexpr int kThreads = 32 * (NW + 1);
   static constexpr int ROW = F8 ? D : 2 * D;
   static constexpr int TILE = KT * ROW;
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? 4 : 6);
-  static constexpr int RING = NS * STAGE;
-  static constexpr int Q_BYTES = 16 * WM * D * 2;
-  static constexpr int ML_BYTES = NW * 16 * 3 * 4;
-  static constexpr int SMEM = 1024 + RING + Q_BYTES + 256 + ML_BYTES + 16 * WM * 4;
-  static_assert(NW * 16 * D * 4 <= RING, "per-warp results fit in the ring");
+  static constexpr int ROWS = 8 * NT;               // query rows of a CTA
+  static constexpr int QS = 2 * D + 16;             // bytes between query rows (no bank twice)
+  static constexpr int OS = D + 8;                  // floats between rows of a warp's result
+  static constexpr int O_BYTES = NW * ROWS * OS * 4;
+  // resident CTAs and ring: about 190 KB in flight per SM
+  static constexpr int CTAS = NT == 4 ? 2 : (F8 ? (NT == 1 ? 4 : 3) : 2);
+  static constexpr int NS = (STAGE == 32768 ? 3 : (STAGE == 16384 ? (NT == 4 ? 5 : (NT == 2 ? 4 : 3))
+                                                                  : 6));
+  static constexpr int RING = NS * STAGE > O_BYTES ? NS * STAGE : (O_BYTES + 1023) / 1024 * 1024;
+  static constexpr int Q_BYTES = ROWS * QS;
+  static constexpr int SMEM = 1024 + RING + Q_BYTES + 256 + NW * ROWS * 3 * 4 + ROWS * 4;
 };
 
 struct GParams {
   const __nv_bfloat16* q;
+  const float* q_factor;
   const int32_t* lens;
   const uint32_t* anc;
   CacheRows rows;
@@ -75,6 +86,11 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 template <bool F8>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
@@ -91,10 +107,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // byte offset of the 16-byte chunk cc of row r of a TMA tile: bf16 tiles are 64-channel
@@ -130,21 +142,29 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
   return w;
 }
 
-template <int D, bool F8, int WM>
-__global__ void __launch_bounds__(Cfg<D, F8, WM>::kThreads)
+// max over the eight lanes that hold one query row's column
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+
+template <int D, bool F8, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
     group_attn_kernel(const __grid_constant__ GParams p, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v) {
-  using C = Cfg<D, F8, WM>;
-  constexpr int NS = C::NS, NW = C::NW, WK = C::WK;
+  using C = Cfg<D, F8, NT>;
+  constexpr int NS = C::NS;
+  constexpr bool kQInRegs = NT <= 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + C::RING);
+  uint8_t* s_q = smem + C::RING;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING + C::Q_BYTES);
   uint64_t* empty = full + NS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
-  float* s_ml = reinterpret_cast<float*>(smem + C::RING + C::Q_BYTES + 256);  // [NW][16][3]
-  float* s_qf = s_ml + NW * 16 * 3;                                           // [16 * WM]
+  float* s_ml = reinterpret_cast<float*>(smem + C::RING + C::Q_BYTES + 256);  // [NW][ROWS][3]
+  float* s_qf = s_ml + NW * C::ROWS * 3;                                      // [ROWS]
 
   const int split = blockIdx.x / p.mblocks, mb = blockIdx.x - split * p.mblocks;
   const int kvh = blockIdx.y, b = blockIdx.z;
@@ -236,361 +256,360 @@ __global__ void __launch_bounds__(Cfg<D, F8, WM>::kThreads)
   }
 
   // ---------------------------------------------------------------- compute warps
-  const int mw = warp / WK, kw = warp % WK;
-  const int M = p.T * p.rep;            // query rows of the KV head: row = t * rep + head
-  const int row_base = mb * (16 * WM);  // first of this CTA
+  const int M = p.T * p.rep;          // query rows of the KV head: row = t * rep + head
+  const int row_base = mb * C::ROWS;  // first of this CTA
+  const int r0 = lane >> 2;           // fragment rows r0 and r0 + 8 (cache rows)
+  const int cq = 2 * (lane & 3);      // fragment columns cq and cq + 1 (query rows)
 
-  // scale bytes of the warp's slice of a tile: lanes 0..15 the keys', 16..31 the values';
+  // scale bytes of the warp's 16 rows of a tile: lanes 0..15 the keys', 16..31 the values';
   // rows past the sequence and pages outside the pool read 0 (their data is zero or masked)
-  auto load_codes = [&](int t, int sl) -> uint32_t {
+  auto load_codes = [&](int t) -> uint32_t {
     if constexpr (!F8) return 0u;
-    if (t >= ntiles) return 0u;
-    const int r = k_begin + t * KT + 16 * (kw + WK * sl) + (lane & 15);
-    if (r >= total) return 0u;
+    const int r = k_begin + t * KT + 16 * warp + (lane & 15);
+    if (t >= ntiles || r >= total) return 0u;
     const long long at = p.rows.at(b, kvh, r);
     if (at < 0) return 0u;
     return (lane < 16 ? p.k_scale : p.v_scale)[at];
   };
-  constexpr int NSL = 4 / WK;
-  uint32_t codes[NSL];
-#pragma unroll
-  for (int sl = 0; sl < NSL; ++sl) codes[sl] = load_codes(0, sl);
+  uint32_t codes = load_codes(0), codes1 = load_codes(1);
 
   // queries into shared memory: D/16 lanes per row, 16 channels each
   {
     constexpr int G = D / 16;
-    for (int r = threadIdx.x / G; r < 16 * WM; r += 32 * NW / G) {
+    for (int r1 = 0; r1 < C::ROWS; r1 += 32 * NW / G) {  // (whole warps shuffle below)
+      const int r = r1 + static_cast<int>(threadIdx.x) / G;
       const int c = threadIdx.x % G, row = row_base + r;
       int e0, e1;
       rope_piece(p.rope, D / 2, c, &e0, &e1);
       uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-      if (row < M) {
+      float factor = 1.f;
+      if (r < C::ROWS && row < M) {
         const int t = row / p.rep, h = kvh * p.rep + row - t * p.rep;
-        const __nv_bfloat16* x =
-            p.q + ((static_cast<size_t>(b) * p.Hq + h) * p.T + t) * static_cast<size_t>(D);
-        lo = *reinterpret_cast<const uint4*>(x + e0);
-        hi = *reinterpret_cast<const uint4*>(x + e1);
+        const size_t at = (static_cast<size_t>(b) * p.Hq + h) * p.T + t;
+        lo = *reinterpret_cast<const uint4*>(p.q + at * D + e0);
+        hi = *reinterpret_cast<const uint4*>(p.q + at * D + e1);
+        if (F8 && p.q_factor != nullptr) factor = p.q_factor[at];
       }
-      if (p.rope != 0) {
-        float cs[8], sn[8], y[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          rope_cos_sin<false>(L - 1, p.theta.hi[8 * c + j], p.theta.lo[8 * c + j], cs[j], sn[j]);
-        rope16(lo, hi, p.rope, cs, sn, y);
-        lo = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                        pack_bf16x2(y[6], y[7]));
-        hi = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]),
-                        pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
-      }
+      if (F8 && p.q_factor == nullptr)
+        factor = query_to_f16<G>(lo, hi, p.rope, L - 1, p.theta, c);
+      if (r >= C::ROWS) continue;  // (no shuffle below)
+      if (F8 && c == 0) s_qf[r] = factor * p.scale_log2;
+      uint8_t* dst = s_q + r * C::QS;
       if constexpr (F8) {
-        bool bad;
-        const uint32_t top = row_absmax<G>(lo, hi, &bad);
-        // 2^(14 - exponent of the largest channel), kept to normal numbers
-        const int E = min(max(static_cast<int>(top >> 7), 15), 254);
-        const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
+        // a lane's four bytes of a K row are channels 4(lane%4).. of 16, so the product's
+        // index runs over the 16 channels as 0 1, 4 5, 8 9, 12 13, then 2 3, 6 7, ...
         const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-        uint32_t ol[4], oh[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          ol[j] = pack_f16x2(bf16lo_to_f32(wl[j]) * f, bf16hi_to_f32(wl[j]) * f);
-          oh[j] = pack_f16x2(bf16lo_to_f32(wh[j]) * f, bf16hi_to_f32(wh[j]) * f);
+          const int off = 2 * ((j >> 1) * 2 + (j & 1) * 8);  // bytes within a half chunk
+          const int b0 = (e0 & 15) ? 8 : 0, b1 = (e1 & 15) ? 8 : 0;
+          *reinterpret_cast<uint32_t*>(dst + 2 * (e0 & ~15) + off + b0) = wl[j];
+          *reinterpret_cast<uint32_t*>(dst + 2 * (e1 & ~15) + off + b1) = wh[j];
         }
-        lo = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-        hi = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-        if (c == 0)
-          s_qf[r] = __uint_as_float(static_cast<uint32_t>(E - 14) << 23) * p.scale_log2;
+      } else {
+        *reinterpret_cast<uint4*>(dst + 2 * e0) = lo;
+        *reinterpret_cast<uint4*>(dst + 2 * e1) = hi;
       }
-      *reinterpret_cast<uint4*>(s_q + r * D + e0) = lo;
-      *reinterpret_cast<uint4*>(s_q + r * D + e1) = hi;
     }
   }
   asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
 
-  const int r0 = lane >> 2;      // fragment rows r0 and r0 + 8
-  const int cq = 2 * (lane & 3);  // fragment column pair
-  uint32_t qa[D / 16][4];
-  float qf[2] = {p.scale_log2, p.scale_log2};
-  {
-    const uint16_t* q0 = s_q + (16 * mw + r0) * D;
-    const uint16_t* q8 = q0 + 8 * D;
+  const int mi = lane >> 3;  // which 8x8 matrix this lane addresses
+  const uint32_t q_addr = smem_u32(s_q) + (lane & 7) * C::QS + mi * 16;
+  uint32_t qb[kQInRegs ? NT : 1][D / 16][2];
+  if constexpr (kQInRegs) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      // e4m3: a thread's four bytes of a K row are channels 4(lane%4).. of the 16, so the
-      // product's index runs over the channels in that order in both operands
-      const int c0 = 16 * kk + (F8 ? 2 * cq : cq), c1 = c0 + (F8 ? 2 : 8);
-      qa[kk][0] = *reinterpret_cast<const uint32_t*>(q0 + c0);
-      qa[kk][1] = *reinterpret_cast<const uint32_t*>(q8 + c0);
-      qa[kk][2] = *reinterpret_cast<const uint32_t*>(q0 + c1);
-      qa[kk][3] = *reinterpret_cast<const uint32_t*>(q8 + c1);
-    }
-    if constexpr (F8) {
-      qf[0] = s_qf[16 * mw + r0];
-      qf[1] = s_qf[16 * mw + r0 + 8];
-    }
-  }
-  const uint32_t* anc[2];
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int t = min((row_base + 16 * mw + r0 + 8 * h) / p.rep, p.T - 1);
-    anc[h] = p.anc + (static_cast<size_t>(b) * p.T + t) * p.words;
+      for (int kk = 0; kk < D / 16; kk += 2) {
+        uint32_t w[4];
+        ldsm_x4(q_addr + j * 8 * C::QS + kk * 32, w);
+        qb[j][kk][0] = w[0];
+        qb[j][kk][1] = w[1];
+        qb[j][kk + 1][0] = w[2];
+        qb[j][kk + 1][1] = w[3];
+      }
   }
+  float qf[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) qf[j][h] = F8 ? s_qf[8 * j + cq + h] : p.scale_log2;
 
-  float o[D / 8][4];
+  float o[D / 16][NT][4];
+  float m_used[NT][2], n_used[NT][2], l_part[NT][2];
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m_used[2] = {-INFINITY, -INFINITY};  // of x, rows r0 and r0 + 8
-  float n_used[2] = {-INFINITY, -INFINITY};  // of (x - m_used) + ev (e4m3)
-  float l_part[2] = {0.f, 0.f};
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) o[c][j][0] = o[c][j][1] = o[c][j][2] = o[c][j][3] = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) m_used[j][h] = n_used[j][h] = -INFINITY, l_part[j][h] = 0.f;
+  }
   const uint32_t smem_base = smem_u32(smem);
+  // addresses of the lane's matrix rows within a tile
+  const int kr = 16 * warp + (lane & 7) + 8 * (mi & 1);
+  const int vr = 16 * warp + (lane & 7) + 8 * (F8 ? (mi & 1) : (mi >> 1));
 
-  bool ok = true;
+  bool ok = true, unset = true;  // unset: some query row has no maximum yet
   for (int t = 0; t < ntiles; ++t) {
     const int s = t % NS;
-    uint32_t next[NSL];
-#pragma unroll
-    for (int sl = 0; sl < NSL; ++sl) next[sl] = load_codes(t + 1, sl);
+    const uint32_t codes2 = load_codes(t + 2);
     if (!mbar_wait(&full[s], (t / NS) & 1, abort_flag, p.status, kWaitNs)) {
       ok = false;
       break;
     }
     const uint32_t kbase = smem_base + s * C::STAGE;
     const uint32_t vbase = kbase + C::TILE;
-    bool wrote = false;
+    const int key0 = k_begin + t * KT + 16 * warp;  // first cache row of the warp
+    float sc[NT][4];
 #pragma unroll
-    for (int sl = 0; sl < NSL; ++sl) {
-      const int slice = kw + WK * sl;
-      const int key0 = k_begin + t * KT + 16 * slice;  // first cache row of the slice
-      const int mi = lane >> 3;                        // which 8x8 matrix this lane addresses
-      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        const int kr = 16 * slice + (lane & 7) + 8 * (mi >> 1);
-        if constexpr (F8) {
+    for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; kk += 2) {
-            uint32_t w[4];
-            ldsm_x4(kbase + tile_off<D, F8>(kr, kk + (mi & 1)), w);
-            mma<F8>(sc[0], qa[kk], e4m3x2_to_f16x2(w[0]), e4m3x2_hi_to_f16x2(w[0]));
-            mma<F8>(sc[1], qa[kk], e4m3x2_to_f16x2(w[2]), e4m3x2_hi_to_f16x2(w[2]));
-            mma<F8>(sc[0], qa[kk + 1], e4m3x2_to_f16x2(w[1]), e4m3x2_hi_to_f16x2(w[1]));
-            mma<F8>(sc[1], qa[kk + 1], e4m3x2_to_f16x2(w[3]), e4m3x2_hi_to_f16x2(w[3]));
-          }
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t w[4];
-            ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + (mi & 1)), w);
-            mma<F8>(sc[0], qa[kk], w[0], w[1]);
-            mma<F8>(sc[1], qa[kk], w[2], w[3]);
-          }
-        }
-      }
-      // which of the slice's 16 rows each of the two query rows sees
-      const bool edge = key0 + 16 > min(L, k_end);
-      uint32_t see[2] = {0xffffu, 0xffffu};
-      if (edge) {
-        const uint32_t in = key0 + 16 <= k_end ? 0xffffu
-                            : key0 >= k_end    ? 0u
-                                               : (1u << (k_end - key0)) - 1u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          see[h] = in & (key0 + 16 <= L ? 0xffffu : draft_bits(anc[h], p.words, key0 - L));
-      }
-      float x[2][4], ev[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float kf[2] = {1.f, 1.f};
-        if constexpr (F8) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            kf[e] = __uint_as_float(__shfl_sync(0xffffffffu, codes[sl], 8 * nt + cq + e) << 23);
-            ev[nt][e] = static_cast<float>(static_cast<int>(
-                            __shfl_sync(0xffffffffu, codes[sl], 16 + 8 * nt + cq + e)) - 127);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = e >> 1;
-          float v = sc[nt][e] * qf[h];
-          if constexpr (F8) v = sc[nt][e] * kf[e & 1] * qf[h];
-          v = (see[h] >> (8 * nt + cq + (e & 1))) & 1u ? v : -INFINITY;
-          x[nt][e] = v;
-          mx[h] = fmaxf(mx[h], v);
-        }
-      }
-      float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
-      bool need = false;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        if (mx[h] > m_used[h] + kRescaleThreshold) {
-          const float r = m_used[h] - mx[h];
-          l_part[h] *= ex2_approx(r);  // 0 when m_used was -inf
-          if constexpr (F8) {
-            n_used[h] += r;  // the numerator's reference m + n stays where it was
-          } else {
-            f[h] = ex2_approx(r);
-            need = true;
-          }
-          m_used[h] = mx[h];
-        }
-        // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
-        const float m_ref = m_used[h] == -INFINITY ? 0.f : m_used[h];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          x[nt][2 * h] -= m_ref;
-          x[nt][2 * h + 1] -= m_ref;
-        }
-        if constexpr (F8) {
-          float my = fmaxf(fmaxf(x[0][2 * h] + ev[0][0], x[0][2 * h + 1] + ev[0][1]),
-                           fmaxf(x[1][2 * h] + ev[1][0], x[1][2 * h + 1] + ev[1][1]));
-          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 1));
-          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 2));
-          if (my > n_used[h] + kRescaleThreshold) {
-            f[h] = ex2_approx(n_used[h] - my);
-            n_used[h] = my;
-            need = true;
-          }
-        }
-      }
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[n][0] *= f[0];
-          o[n][1] *= f[0];
-          o[n][2] *= f[1];
-          o[n][3] *= f[1];
-        }
-      }
-      float w[2][4], n_ref[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        n_ref[h] = n_used[h] == -INFINITY ? 0.f : n_used[h] - kWeightLog2;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = ex2_approx(x[nt][e]);
-          l_part[e >> 1] += v;
-          w[nt][e] = F8 ? ex2_approx(x[nt][e] + (ev[nt][e & 1] - n_ref[e >> 1])) : v;
-        }
-      uint32_t pa[4];
+    for (int kk = 0; kk < D / 16; kk += 2) {
+      uint32_t a[2][4];
       if constexpr (F8) {
-        pa[0] = pack_f16x2(w[0][0], w[0][1]);
-        pa[1] = pack_f16x2(w[0][2], w[0][3]);
-        pa[2] = pack_f16x2(w[1][0], w[1][1]);
-        pa[3] = pack_f16x2(w[1][2], w[1][3]);
-      } else {
-        pa[0] = pack_bf16x2(w[0][0], w[0][1]);
-        pa[1] = pack_bf16x2(w[0][2], w[0][3]);
-        pa[2] = pack_bf16x2(w[1][0], w[1][1]);
-        pa[3] = pack_bf16x2(w[1][2], w[1][3]);
-      }
-      // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
-      // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
-      // merge puts it where it belongs).  Warps that share the slice write the same words.
-      if (key0 + 16 > min(L, k_end)) {
-        uint8_t* vt = smem + s * C::STAGE + C::TILE;
-        for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
-          const int rr = e / (C::ROW / 16), cc = e % (C::ROW / 16);
-          uint4* at = reinterpret_cast<uint4*>(vt + tile_off<D, F8>(16 * slice + rr, cc));
-          if (key0 + rr >= k_end) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-          } else if (key0 + rr >= L) {
-            const uint4 v = *at;
-            *at = make_uint4(finite_word<F8>(v.x), finite_word<F8>(v.y), finite_word<F8>(v.z),
-                             finite_word<F8>(v.w));
-          }
+        uint32_t w[4];
+        ldsm_x4(kbase + tile_off<D, F8>(kr, kk + (mi >> 1)), w);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a[i][0] = e4m3x2_to_f16x2(w[2 * i]);
+          a[i][1] = e4m3x2_to_f16x2(w[2 * i + 1]);
+          a[i][2] = e4m3x2_hi_to_f16x2(w[2 * i]);
+          a[i][3] = e4m3x2_hi_to_f16x2(w[2 * i + 1]);
         }
-        wrote = true;
-        __syncwarp();
+      } else {
+        ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + (mi >> 1)), a[0]);
+        ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + 2 + (mi >> 1)), a[1]);
       }
-      {
-        const int vr = 16 * slice + (lane & 7) + 8 * (mi & 1);
-        if constexpr (F8) {
 #pragma unroll
-          for (int cc = 0; cc < D / 16; cc += 2) {
-            // rows 0-7 and 8-15 of chunk cc, then of chunk cc + 1; a transposed load hands a
-            // thread channels (2n, 2n+1) of two keys: regrouped by channel, they are the
-            // operands of the even and of the odd channels' products
-            uint32_t r[4];
-            ldsm_x4_t(vbase + tile_off<D, F8>(vr, cc + (mi >> 1)), r);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t a = __byte_perm(r[2 * j], 0u, 0x3120);
-              const uint32_t c = __byte_perm(r[2 * j + 1], 0u, 0x3120);
-              mma<F8>(o[2 * (cc + j)], pa, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(c));
-              mma<F8>(o[2 * (cc + j) + 1], pa, e4m3x2_hi_to_f16x2(a), e4m3x2_hi_to_f16x2(c));
-            }
-          }
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (kQInRegs) {
+          mma<F8>(sc[j], a[0], qb[j][kk][0], qb[j][kk][1]);
+          mma<F8>(sc[j], a[1], qb[j][kk + 1][0], qb[j][kk + 1][1]);
         } else {
-#pragma unroll
-          for (int np = 0; np < D / 16; ++np) {
-            uint32_t r[4];
-            ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * np + (mi >> 1)), r);
-            mma<F8>(o[2 * np], pa, r[0], r[1]);
-            mma<F8>(o[2 * np + 1], pa, r[2], r[3]);
-          }
+          uint32_t w[4];
+          ldsm_x4(q_addr + j * 8 * C::QS + kk * 32, w);
+          mma<F8>(sc[j], a[0], w[0], w[1]);
+          mma<F8>(sc[j], a[1], w[2], w[3]);
         }
       }
     }
-    if (wrote) fence_proxy_async_smem();
+    // factors of the thread's two cache rows
+    float kf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        kf[i] = __uint_as_float(__shfl_sync(0xffffffffu, codes, r0 + 8 * i) << 23);
+        ev[i] = static_cast<float>(
+            static_cast<int>(__shfl_sync(0xffffffffu, codes, 16 + r0 + 8 * i)) - 127);
+      }
+    }
+    // cache rows that a query row does not see: their scores become -inf
+    const bool edge = key0 + 16 > min(L, k_end);
+    uint32_t hide = 0u;  // bit 4j + 2i + h
+    if (edge) {
+      const uint32_t in = key0 + 16 <= k_end ? 0xffffu
+                          : key0 >= k_end    ? 0u
+                                             : (1u << (k_end - key0)) - 1u;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tq = min((row_base + 8 * j + cq + h) / p.rep, p.T - 1);
+          const uint32_t* anc = p.anc + (static_cast<size_t>(b) * p.T + tq) * p.words;
+          const uint32_t see =
+              in & (key0 + 16 <= L ? 0xffffu : draft_bits(anc, p.words, key0 - L));
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            hide |= (1u ^ ((see >> (r0 + 8 * i)) & 1u)) << (4 * j + 2 * i + h);
+        }
+    }
+    // x - m for every score (x rounded by itself, as in m: the largest gives 0); where one exceeds its maximum by the threshold (or there is none
+    // yet) the maxima are raised first
+    float d[NT][4];
+    bool over = false;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = e >> 1, h = e & 1;
+        d[j][e] = __fmul_rn(sc[j][e], F8 ? kf[i] * qf[j][h] : qf[j][h]) - m_used[j][h];
+        if (edge && ((hide >> (4 * j + e)) & 1u)) d[j][e] = -INFINITY;
+        over |= d[j][e] > kRescaleThreshold;
+        if constexpr (F8) over |= d[j][e] + ev[i] > n_used[j][h] + kRescaleThreshold;
+      }
+    if (__any_sync(0xffffffffu, over || unset)) {
+      unset = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            x[i] = __fmul_rn(sc[j][2 * i + h], F8 ? kf[i] * qf[j][h] : qf[j][h]);
+            if (edge && ((hide >> (4 * j + 2 * i + h)) & 1u)) x[i] = -INFINITY;
+          }
+          const float mx = column_max(fmaxf(x[0], x[1]));
+          if (mx > m_used[j][h] + kRescaleThreshold) {
+            const float r = m_used[j][h] - mx;
+            l_part[j][h] *= ex2_approx(r);  // 0 when m_used was -inf
+            if constexpr (F8)
+              n_used[j][h] += r;  // the numerator's reference m + n stays where it was
+            else
+              f[h] = ex2_approx(r);
+            m_used[j][h] = mx;
+          }
+          // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
+          const float m_ref = m_used[j][h] == -INFINITY ? 0.f : m_used[j][h];
+          unset |= m_used[j][h] == -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) d[j][2 * i + h] = x[i] - m_ref;
+          if constexpr (F8) {
+            const float my = column_max(fmaxf(d[j][h] + ev[0], d[j][2 + h] + ev[1]));
+            if (my > n_used[j][h] + kRescaleThreshold) {
+              f[h] = ex2_approx(n_used[j][h] - my);
+              n_used[j][h] = my;
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            o[c][j][0] *= f[0];
+            o[c][j][1] *= f[1];
+            o[c][j][2] *= f[0];
+            o[c][j][3] *= f[1];
+          }
+        }
+      }
+      unset = __any_sync(0xffffffffu, unset);
+    }
+    // weights, turned to the layout of the second product
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = ex2_approx(d[j][e]);
+        l_part[j][e & 1] += v;
+        w[e] = v;
+        if constexpr (F8) {
+          const float n_ref = n_used[j][e & 1] == -INFINITY ? 0.f : n_used[j][e & 1];
+          w[e] = ex2_approx(d[j][e] + (ev[e >> 1] + (kWeightLog2 - n_ref)));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        pb[j][i] = transpose8x8(F8 ? pack_f16x2(w[2 * i], w[2 * i + 1])
+                                   : pack_bf16x2(w[2 * i], w[2 * i + 1]));
+    }
+    // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
+    // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
+    // merge puts it where it belongs).
+    if (edge) {
+      uint8_t* vt = smem + s * C::STAGE + C::TILE;
+      for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
+        const int rr = e / (C::ROW / 16), cc = e % (C::ROW / 16);
+        uint4* at = reinterpret_cast<uint4*>(vt + tile_off<D, F8>(16 * warp + rr, cc));
+        if (key0 + rr >= k_end) {
+          *at = make_uint4(0u, 0u, 0u, 0u);
+        } else if (key0 + rr >= L) {
+          const uint4 v = *at;
+          *at = make_uint4(finite_word<F8>(v.x), finite_word<F8>(v.y), finite_word<F8>(v.z),
+                           finite_word<F8>(v.w));
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2) {
+      uint32_t a[2][4];
+      if constexpr (F8) {
+        // a transposed load hands a lane channels (2n, 2n + 1) of two cache rows: regrouped by
+        // channel they are rows n (even channels) and n + 8 (odd) of the operand
+        uint32_t r[4];
+        ldsm_x4_t(vbase + tile_off<D, F8>(vr, c + (mi >> 1)), r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t u = __byte_perm(r[2 * i], 0u, 0x3120);
+          const uint32_t v = __byte_perm(r[2 * i + 1], 0u, 0x3120);
+          a[i][0] = e4m3x2_to_f16x2(u);
+          a[i][1] = e4m3x2_hi_to_f16x2(u);
+          a[i][2] = e4m3x2_to_f16x2(v);
+          a[i][3] = e4m3x2_hi_to_f16x2(v);
+        }
+      } else {
+        ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * c + (mi & 1)), a[0]);
+        ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * c + 2 + (mi & 1)), a[1]);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        mma<F8>(o[c][j], a[0], pb[j][0], pb[j][1]);
+        mma<F8>(o[c + 1][j], a[1], pb[j][0], pb[j][1]);
+      }
+    }
+    if (edge) fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
-#pragma unroll
-    for (int sl = 0; sl < NSL; ++sl) codes[sl] = next[sl];
+    codes = codes1;
+    codes1 = codes2;
   }
 
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], 1);
-    l_part[h] += __shfl_xor_sync(0xffffffffu, l_part[h], 2);
-  }
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 4);
+      l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 8);
+      l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 16);
+    }
   // all tiles consumed: the ring is free to hold the per-warp results
   asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
   if (!ok || *abort_flag) return;
-  float* s_o = reinterpret_cast<float*>(smem);  // [NW][16][D]
+  float* s_o = reinterpret_cast<float*>(smem);  // [NW][ROWS][OS]
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int rr = warp * 16 + r0 + 8 * h;
-    if ((lane & 3) == 0) {
-      s_ml[rr * 3 + 0] = m_used[h];
-      s_ml[rr * 3 + 1] = l_part[h];
-      s_ml[rr * 3 + 2] = n_used[h];
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int rr = warp * C::ROWS + 8 * j + cq + h;
+      if (r0 == 0) {
+        s_ml[rr * 3 + 0] = m_used[j][h];
+        s_ml[rr * 3 + 1] = l_part[j][h];
+        s_ml[rr * 3 + 2] = n_used[j][h];
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        float* at = s_o + rr * C::OS + 16 * c;
+        if constexpr (F8) {
+          *reinterpret_cast<float2*>(at + 2 * r0) = make_float2(o[c][j][h], o[c][j][2 + h]);
+        } else {
+          at[r0] = o[c][j][h];
+          at[r0 + 8] = o[c][j][2 + h];
+        }
+      }
     }
-    if constexpr (F8) {
-#pragma unroll
-      for (int cc = 0; cc < D / 16; ++cc)
-        *reinterpret_cast<float4*>(s_o + rr * D + 16 * cc + 2 * cq) =
-            make_float4(o[2 * cc][2 * h], o[2 * cc + 1][2 * h], o[2 * cc][2 * h + 1],
-                        o[2 * cc + 1][2 * h + 1]);
-    } else {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-        *reinterpret_cast<float2*>(s_o + rr * D + 8 * n + cq) =
-            make_float2(o[n][2 * h], o[n][2 * h + 1]);
-    }
-  }
   asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
-  // merge the warps' key slices; one partial per query row, relative to the maximum of x
-  for (int e = threadIdx.x; e < 16 * WM * (D / 4); e += 32 * NW) {
+  // merge the warps' slices; one partial per query row, relative to the maximum of x
+  for (int e = threadIdx.x; e < C::ROWS * (D / 4); e += 32 * NW) {
     const int r = e / (D / 4), c = e % (D / 4), row = row_base + r;
-    if (row >= M) continue;
-    const int w0 = (r / 16) * WK, rr = r % 16;
+    if (row >= M) break;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < WK; ++w) m = fmaxf(m, s_ml[((w0 + w) * 16 + rr) * 3]);
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, s_ml[(w * C::ROWS + r) * 3]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      const float* ml = s_ml + ((w0 + w) * 16 + rr) * 3;
+    for (int w = 0; w < NW; ++w) {
+      const float* ml = s_ml + (w * C::ROWS + r) * 3;
       // (a warp that saw nothing holds zeros, or NaN if its scores were NaN)
       const bool none = ml[0] == -INFINITY;
       l += (none ? 1.f : ex2_approx(ml[0] - m)) * ml[1];
-      const float fw = none ? 1.f : ex2_approx(F8 ? ml[0] - m + (ml[2] - kWeightLog2) : ml[0] - m);
-      const float4 v = *reinterpret_cast<const float4*>(s_o + ((w0 + w) * 16 + rr) * D + 4 * c);
+      const float fw =
+          none ? 1.f : ex2_approx(F8 ? ml[0] - m + (ml[2] - kWeightLog2) : ml[0] - m);
+      const float4 v = *reinterpret_cast<const float4*>(s_o + (w * C::ROWS + r) * C::OS + 4 * c);
       acc.x += fw * v.x;
       acc.y += fw * v.y;
       acc.z += fw * v.z;
@@ -673,11 +692,12 @@ __global__ void __launch_bounds__(128) group_merge_kernel(
     lse[row] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D, bool F8, int WM>
+template <int D, bool F8, int NT>
 cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, F8, WM>;
+  using C = Cfg<D, F8, NT>;
   GParams p{};
   p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.q_factor = a.q_factor;
   p.lens = a.lens;
   p.anc = a.anc;
   p.rows = CacheRows{a.cache.block_table, a.Hkv, a.cache.Lmax, a.cache.page_size,
@@ -700,7 +720,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.min_len = a.min_len;
   p.chunk = a.chunk;
   p.n_splits = a.n_splits;
-  p.mblocks = (a.T * p.rep + 16 * WM - 1) / (16 * WM);
+  p.mblocks = (a.T * p.rep + C::ROWS - 1) / C::ROWS;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.theta = a.theta;
 
@@ -712,11 +732,11 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
       !make(&tv, a.cache.v, D, rows, planes, p.box_rows))
     return cudaErrorInvalidValue;
   static SmemLimitOnce smem_limit;
-  cudaError_t e = smem_limit.set(group_attn_kernel<D, F8, WM>, C::SMEM);
+  cudaError_t e = smem_limit.set(group_attn_kernel<D, F8, NT>, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.n_splits) * p.mblocks, a.Hkv, a.B);
-  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -724,14 +744,14 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.after_prep ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, group_attn_kernel<D, F8, WM>, p, tk, tv);
+  return cudaLaunchKernelEx(&cfg, group_attn_kernel<D, F8, NT>, p, tk, tv);
 }
 
 template <int D, bool F8>
 cudaError_t launch_rows(const GroupArgs& a, cudaStream_t stream) {
   const int rows = a.T * (a.Hq / a.Hkv);
-  if (rows <= 16) return launch_t<D, F8, 1>(a, stream);
-  if (rows <= 32) return launch_t<D, F8, 2>(a, stream);
+  if (rows <= 8) return launch_t<D, F8, 1>(a, stream);
+  if (rows <= 16) return launch_t<D, F8, 2>(a, stream);
   return launch_t<D, F8, 4>(a, stream);
 }
 

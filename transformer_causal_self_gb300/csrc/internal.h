@@ -202,7 +202,9 @@ cudaError_t launch_cache_read_fp8(const KvCache& cache, const int32_t* seq_lens,
 // query t sees those in its bit mask anc[b, t] (words of 32 bits; drafts = 0: no such rows).
 struct GroupArgs {
   KvCache cache;
-  const void* q;         // [B, Hq, T, d] bf16
+  const void* q;         // [B, Hq, T, d] bf16; with q_factor f16 (query_to_f16, fp8.cuh)
+  const float* q_factor; // null, or [B, Hq, T]: an 8-bit cache's queries as launch_tree_prep
+                         // leaves them
   const int32_t* lens;   // device [B]
   const uint32_t* anc;   // device [B, T, words]
   int drafts, words;
@@ -239,7 +241,8 @@ struct TreePrepArgs {
   int B, Hq, Hkv, Tn, d, max_seq_len;
   int rope;
   RopeTable theta;
-  void* q_rot;      // [B, Hq, Tn, d] bf16
+  void* q_rot;      // [B, Hq, Tn, d] bf16, or f16 for an 8-bit cache, then with
+  float* q_factor;  // [B, Hq, Tn]
   uint32_t* anc;    // [B, Tn, words]
   int32_t* lens;    // [B]: cache_lens, or -1 where a check failed
   uint8_t* vflag;   // [B, Hkv, Tn]

@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     void* __restrict__ v_cache, uint8_t* __restrict__ k_scale, uint8_t* __restrict__ v_scale,
     const int32_t* __restrict__ cache_lens, const int32_t* __restrict__ parents, CacheRows rows,
     int Hq, int Tn, int max_seq_len, int rope, RopeTable theta, __nv_bfloat16* __restrict__ q_rot,
-    uint32_t* __restrict__ anc, int32_t* __restrict__ lens, uint8_t* __restrict__ vflag, int words,
+    float* __restrict__ q_factor, uint32_t* __restrict__ anc, int32_t* __restrict__ lens, uint8_t* __restrict__ vflag, int words,
     uint32_t* status) {
   constexpr int G = D / 16;
   __shared__ uint32_t s_anc[kThreads][kWords];
@@ -116,6 +116,17 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
                       pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
     }
     if (is_q) {
+      if constexpr (F8) {  // (query_to_f16 with the angles at hand)
+        const int E = min(max(static_cast<int>(top >> 7), 15), 254);
+        const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
+        lo = make_uint4(pack_f16x2(y[0] * f, y[1] * f), pack_f16x2(y[2] * f, y[3] * f),
+                        pack_f16x2(y[4] * f, y[5] * f), pack_f16x2(y[6] * f, y[7] * f));
+        hi = make_uint4(pack_f16x2(y[8] * f, y[9] * f), pack_f16x2(y[10] * f, y[11] * f),
+                        pack_f16x2(y[12] * f, y[13] * f), pack_f16x2(y[14] * f, y[15] * f));
+        if (c == 0)
+          q_factor[(static_cast<size_t>(b) * Hq + g) * Tn + t] =
+              __uint_as_float(static_cast<uint32_t>(E - 14) << 23);
+      }
       __nv_bfloat16* dst =
           q_rot + ((static_cast<size_t>(b) * Hq + g) * Tn + t) * static_cast<size_t>(D);
       *reinterpret_cast<uint4*>(dst + e0) = lo;
@@ -246,7 +257,7 @@ cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
       static_cast<const __nv_bfloat16*>(a.v_new), a.cache.k, a.cache.v,
       static_cast<uint8_t*>(a.cache.k_scale), static_cast<uint8_t*>(a.cache.v_scale),
       a.cache_lens, a.parents, rows_of(a.cache, a.Hkv), a.Hq, a.Tn, a.max_seq_len, a.rope, a.theta,
-      static_cast<__nv_bfloat16*>(a.q_rot), a.anc, a.lens, a.vflag, a.words, a.status);
+      static_cast<__nv_bfloat16*>(a.q_rot), a.q_factor, a.anc, a.lens, a.vflag, a.words, a.status);
   return cudaGetLastError();
 }
 
