@@ -141,7 +141,7 @@ bool make_tmap_bf16_3d(void* tmap_out, const void* base, int d, int rows, int pl
 }
 
 bool make_tmap_u8_3d(void* tmap_out, const void* base, int d, int rows, int planes,
-                     int box_rows) {
+                     int box_rows, bool swizzle) {
   auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
   if (encode == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
@@ -153,7 +153,9 @@ bool make_tmap_u8_3d(void* tmap_out, const void* base, int d, int rows, int plan
   CUresult r = encode(static_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                       const_cast<void*>(base), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      !swizzle   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                 : CU_TENSOR_MAP_SWIZZLE_64B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

@@ -98,33 +98,61 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
   return CSATTN_OK;
 }
 
-// Rows of a query-row block of the attention kernel (launch_group_attn).
-int row_blocks(int rows) { return (rows + 31) / 32; }
-
-// Cache rows per split.  Splits as long as 256 rows (a split costs a partial result per query
-// row and a CTA's start) as many as give every SM 32 CTAs, so that ragged lengths even out;
-// where even that leaves SMs idle (few heads and sequences), down to 64 rows, until there
-// are 4 CTAs per SM.
+// How the attention of `rows` query rows per KV head over at most max_seq_len cache rows is cut:
+// the kernel, the cache rows per split and the splits.
+struct Plan {
+  bool tc;
+  int chunk, n_splits;
+};
 constexpr long long kSms = 152;
-long long splits_for(long long per_sm, int B, int Hkv, int mblocks) {
-  const long long ctas = static_cast<long long>(B) * Hkv * mblocks;
+constexpr int kTcRows = 16;  // more query rows than this per KV head go to launch_group_tc
+
+// Splits that give every SM `per_sm` CTAs.
+long long splits_for(long long per_sm, long long ctas) {
   return std::max<long long>(1, (kSms * per_sm + ctas - 1) / ctas);
 }
-int round64(long long x) { return static_cast<int>((x + 63) / 64 * 64); }
-int chunk_for(int B, int Hkv, int mblocks, int max_seq_len, int num_splits) {
-  if (num_splits > 0) return round64((max_seq_len + num_splits - 1LL) / num_splits);
-  const long long few = splits_for(4, B, Hkv, mblocks), many = splits_for(32, B, Hkv, mblocks);
-  const int fine = round64((max_seq_len + few - 1) / few);
-  if (fine < 256) return fine;
-  return std::max(256, round64((max_seq_len + many - 1) / many));
+int round_to(long long x, int m) { return static_cast<int>((x + m - 1) / m * m); }
+
+// The automatic splits of any length are at most this.
+long long most_splits(bool tc, long long ctas) { return splits_for(tc ? 4 : 32, ctas); }
+
+Plan plan_for(int B, int Hkv, int rows, int max_seq_len, int num_splits) {
+  Plan p{};
+  p.tc = rows > kTcRows;
+  const int unit = p.tc ? 128 : 64;
+  const long long ctas = static_cast<long long>(B) * Hkv * (p.tc ? (rows + 255) / 256 : 1);
+  if (num_splits > 0) {
+    p.chunk = round_to((max_seq_len + num_splits - 1LL) / num_splits, unit);
+  } else if (p.tc) {
+    p.chunk = std::max(256, round_to((max_seq_len + most_splits(true, ctas) - 1) /
+                                         most_splits(true, ctas), unit));
+  } else {
+    // Few sequences and heads: one wave of 4 CTAs per SM, down to 64 rows each.  Many: up to
+    // 32 CTAs per SM, so that ragged lengths even out, but no less than 256 rows (a split
+    // costs a CTA's start and a partial result per query row).
+    const long long few = splits_for(4, ctas), many = most_splits(false, ctas);
+    p.chunk = few >= 4 ? round_to((max_seq_len + few - 1) / few, unit)
+                       : std::max(256, round_to((max_seq_len + many - 1) / many, unit));
+  }
+  p.n_splits = (max_seq_len + p.chunk - 1) / p.chunk;
+  return p;
 }
 
 // Bytes of the splits' partial results for any max_seq_len <= Lmax.
 size_t partial_bytes(int B, int Hq, int Hkv, int T, int Lmax, int d, int num_splits) {
-  const int mb = row_blocks(T * (Hq / Hkv));
-  const long long most = num_splits > 0 ? num_splits : splits_for(32, B, Hkv, mb);
+  const int rows = T * (Hq / Hkv);
+  const bool tc = rows > kTcRows;
+  const long long ctas = static_cast<long long>(B) * Hkv * (tc ? (rows + 255) / 256 : 1);
+  const long long most = num_splits > 0 ? num_splits : most_splits(tc, ctas);
   const long long splits = std::min<long long>(most, (static_cast<long long>(Lmax) + 63) / 64);
   return static_cast<size_t>(B) * Hq * T * splits * (static_cast<size_t>(d) + 2) * 4;
+}
+
+size_t decode_partial_bytes(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
+  const long long most =
+      num_splits > 0 ? num_splits : most_splits(false, static_cast<long long>(B) * Hkv);
+  const long long splits = std::min<long long>(most, (static_cast<long long>(Lmax) + 63) / 64);
+  return static_cast<size_t>(B) * Hq * splits * (static_cast<size_t>(d) + 2) * 4;
 }
 
 bool sizes_ok(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
@@ -205,8 +233,10 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
     return rc;
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
-  a.chunk = chunk_for(B, Hkv, row_blocks(Hq / Hkv), max_seq_len, num_splits);
-  a.n_splits = (max_seq_len + a.chunk - 1) / a.chunk;
+  // (one query per head: always the small kernel, 32 query rows a CTA)
+  const Plan plan = plan_for(B, Hkv, std::min(Hq / Hkv, kTcRows), max_seq_len, num_splits);
+  a.chunk = plan.chunk;
+  a.n_splits = plan.n_splits;
   const size_t rows = static_cast<size_t>(B) * Hq * a.n_splits;
   if ((rc = check_workspace(fn, workspace, workspace_bytes, rows * (d + 2) * 4)) != CSATTN_OK)
     return rc;
@@ -271,8 +301,9 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
     return rc;
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
-  a.chunk = chunk_for(B, Hkv, row_blocks(Tn * (Hq / Hkv)), max_seq_len, num_splits);
-  a.n_splits = (max_seq_len + a.chunk - 1) / a.chunk;
+  const Plan plan = plan_for(B, Hkv, Tn * (Hq / Hkv), max_seq_len, num_splits);
+  a.chunk = plan.chunk;
+  a.n_splits = plan.n_splits;
   const size_t rows = static_cast<size_t>(B) * Hq * Tn * a.n_splits;
   const TreeSpace at(rows * (d + 2) * 4, B, Hq, Hkv, Tn, d);
   if ((rc = check_workspace(fn, workspace, workspace_bytes, at.total)) != CSATTN_OK) return rc;
@@ -324,7 +355,7 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_tree_prep(p, st);
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: append launch");
-  e = launch_group_attn(a, st);
+  e = plan.tc ? launch_group_tc(a, st) : launch_group_attn(a, st);
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: kernel launch");
   e = launch_group_merge(a, p.vflag, v_new, out, lse, st);
   return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "attn_tree_step: merge launch");
@@ -438,7 +469,7 @@ int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const 
 
 size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
   if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits)) return 0;
-  return partial_bytes(B, Hq, Hkv, 1, Lmax, d, num_splits);
+  return decode_partial_bytes(B, Hq, Hkv, Lmax, d, num_splits);
 }
 
 int csattn_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,

@@ -128,6 +128,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// zero the bytes of four e4m3 that are NaN
+__device__ __forceinline__ uint32_t finite_e4m3x4(uint32_t w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (((w >> (8 * i)) & 0x7fu) == 0x7fu) w &= ~(0xffu << (8 * i));
+  return w;
+}
+
 // Where the rows of a cache are: contiguous [B, Hkv, Lmax, ...] (block_table == nullptr)
 // or pages [num_pages, Hkv, page_size, ...].
 struct CacheRows {

@@ -131,14 +131,9 @@ __device__ __forceinline__ uint32_t draft_bits(const uint32_t* anc, int words, i
 // zero the halves (bf16) or bytes (e4m3) of a word that hold an infinity or NaN
 template <bool F8>
 __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
-  if constexpr (F8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (((w >> (8 * i)) & 0x7fu) == 0x7fu) w &= ~(0xffu << (8 * i));
-  } else {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-  }
+  if constexpr (F8) return finite_e4m3x4(w);
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
   return w;
 }
 
@@ -727,10 +722,11 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   alignas(64) CUtensorMap tk, tv;
   const int rows = paged ? a.cache.page_size : a.cache.Lmax;
   const int planes = paged ? a.cache.num_pages * a.Hkv : a.B * a.Hkv;
-  auto* make = F8 ? make_tmap_u8_3d : make_tmap_bf16_3d;
-  if (!make(&tk, a.cache.k, D, rows, planes, p.box_rows) ||
-      !make(&tv, a.cache.v, D, rows, planes, p.box_rows))
-    return cudaErrorInvalidValue;
+  const bool made = F8 ? make_tmap_u8_3d(&tk, a.cache.k, D, rows, planes, p.box_rows, true) &&
+                             make_tmap_u8_3d(&tv, a.cache.v, D, rows, planes, p.box_rows, true)
+                       : make_tmap_bf16_3d(&tk, a.cache.k, D, rows, planes, p.box_rows) &&
+                             make_tmap_bf16_3d(&tv, a.cache.v, D, rows, planes, p.box_rows);
+  if (!made) return cudaErrorInvalidValue;
   static SmemLimitOnce smem_limit;
   cudaError_t e = smem_limit.set(group_attn_kernel<D, F8, NT>, C::SMEM);
   if (e != cudaSuccess) return e;

@@ -221,6 +221,8 @@ struct GroupArgs {
   uint32_t* status;
 };
 cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
+// The same on tcgen05, for many query rows; a.chunk is a multiple of 128, rope is 0.
+cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream);
 
 // Merge of the splits of launch_group_attn into out [B, Hq, T, d] bf16 and, if non-null, lse
 // [B, Hq, T].  vflag (with v_new; may be null): bytes [B, Hkv, T], set where v_new[b, g, t]
@@ -258,8 +260,10 @@ cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
                                int B, int Hkv, int Tn, int d, uint32_t* status,
                                cudaStream_t stream);
 
-// 3-D map over rows of `d` bytes (64 or 128): box {d, box_rows, 1}, swizzle as wide as a row.
-bool make_tmap_u8_3d(void* tmap_out, const void* base, int d, int rows, int planes, int box_rows);
+// 3-D map over rows of `d` bytes (64 or 128): box {d, box_rows, 1}, with a swizzle as wide as
+// a row or none.
+bool make_tmap_u8_3d(void* tmap_out, const void* base, int d, int rows, int planes, int box_rows,
+                     bool swizzle);
 
 // Shared by the C ABI's translation units (csattn_api.cu).
 int api_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
