@@ -98,62 +98,46 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
   return CSATTN_OK;
 }
 
-// How the attention of `rows` query rows per KV head over at most max_seq_len cache rows is cut:
-// the kernel, the cache rows per split and the splits.
-struct Plan {
-  bool tc;
-  int chunk, n_splits;
-};
-constexpr long long kSms = 152;
-constexpr int kTcRows = 16;  // more query rows than this per KV head go to launch_group_tc
+// The kernel for `rows` query rows per KV head, and how its work is shared out: a wave of CTAs,
+// or, with an explicit number of splits, as many CTAs as parts of that many equal ones of the
+// longest sequence can fill.
+constexpr int kSms = 152;
+constexpr int kTcRows = 16;  // trees with more query rows than this go to launch_group_tc
 
-// Splits that give every SM `per_sm` CTAs.
-long long splits_for(long long per_sm, long long ctas) {
-  return std::max<long long>(1, (kSms * per_sm + ctas - 1) / ctas);
-}
-int round_to(long long x, int m) { return static_cast<int>((x + m - 1) / m * m); }
-
-// The automatic splits of any length are at most this.
-long long most_splits(bool tc, long long ctas) { return splits_for(tc ? 4 : 32, ctas); }
-
-Plan plan_for(int B, int Hkv, int rows, int max_seq_len, int num_splits) {
-  Plan p{};
-  p.tc = rows > kTcRows;
-  const int unit = p.tc ? 128 : 64;
-  const long long ctas = static_cast<long long>(B) * Hkv * (p.tc ? (rows + 255) / 256 : 1);
+GroupPlan plan_for(int B, int Hkv, int rows, bool tc, bool f8, int max_seq_len, int num_splits) {
+  GroupPlan p{};
+  p.tc = tc;
+  p.unit = tc ? 128 : 64;
+  p.block_rows = tc ? (rows > 128 ? 256 : 128) : (rows > 8 ? 16 : 8);
+  p.rblocks = (rows + p.block_rows - 1) / p.block_rows;
+  p.part_rows = std::min(rows, p.block_rows);
+  p.subs = tc ? 1 : 4;  // launch_group_attn: one for each of its four warps
   if (num_splits > 0) {
-    p.chunk = round_to((max_seq_len + num_splits - 1LL) / num_splits, unit);
-  } else if (p.tc) {
-    p.chunk = std::max(256, round_to((max_seq_len + most_splits(true, ctas) - 1) /
-                                         most_splits(true, ctas), unit));
+    const long long tiles = (max_seq_len + p.unit - 1) / p.unit;
+    p.tiles_per_cta = static_cast<int>((tiles + num_splits - 1) / num_splits);
+    const long long parts = (tiles + p.tiles_per_cta - 1) / p.tiles_per_cta;
+    // (a shorter bound may cut finer: as many parts as asked for, or a tile each)
+    p.most_grid = static_cast<int>(std::min<long long>(
+        0x7fffffff, std::min<long long>(num_splits, tiles) * B * Hkv * p.rblocks));
+    p.grid = static_cast<int>(std::min<long long>(0x7fffffff, parts * B * Hkv * p.rblocks));
   } else {
-    // Few sequences and heads: one wave of 4 CTAs per SM, down to 64 rows each.  Many: up to
-    // 32 CTAs per SM, so that ragged lengths even out, but no less than 256 rows (a split
-    // costs a CTA's start and a partial result per query row).
-    const long long few = splits_for(4, ctas), many = most_splits(false, ctas);
-    p.chunk = few >= 4 ? round_to((max_seq_len + few - 1) / few, unit)
-                       : std::max(256, round_to((max_seq_len + many - 1) / many, unit));
+    // resident CTAs (launch bounds and shared memory of the kernels)
+    p.most_grid = p.grid = kSms * (tc ? 1 : (f8 ? (p.block_rows == 8 ? 4 : 3) : 2));
   }
-  p.n_splits = (max_seq_len + p.chunk - 1) / p.chunk;
   return p;
 }
 
-// Bytes of the splits' partial results for any max_seq_len <= Lmax.
-size_t partial_bytes(int B, int Hq, int Hkv, int T, int Lmax, int d, int num_splits) {
-  const int rows = T * (Hq / Hkv);
-  const bool tc = rows > kTcRows;
-  const long long ctas = static_cast<long long>(B) * Hkv * (tc ? (rows + 255) / 256 : 1);
-  const long long most = num_splits > 0 ? num_splits : most_splits(tc, ctas);
-  const long long splits = std::min<long long>(most, (static_cast<long long>(Lmax) + 63) / 64);
-  return static_cast<size_t>(B) * Hq * T * splits * (static_cast<size_t>(d) + 2) * 4;
+// Bytes of the partial results: [grid + segments, subs, part_rows] rows of d + 2 floats, with
+// room for any smaller max_seq_len.
+size_t partial_floats(const GroupPlan& p, int B, int Hkv) {
+  return (static_cast<size_t>(p.most_grid) + static_cast<size_t>(B) * Hkv * p.rblocks) * p.subs *
+         p.part_rows;
 }
-
-size_t decode_partial_bytes(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
-  const long long most =
-      num_splits > 0 ? num_splits : most_splits(false, static_cast<long long>(B) * Hkv);
-  const long long splits = std::min<long long>(most, (static_cast<long long>(Lmax) + 63) / 64);
-  return static_cast<size_t>(B) * Hq * splits * (static_cast<size_t>(d) + 2) * 4;
+size_t partial_bytes(const GroupPlan& p, int B, int Hkv, int d) {
+  return partial_floats(p, B, Hkv) * (static_cast<size_t>(d) + 2) * 4;
 }
+// The tiles' sums per sequence (GroupLine::prefix) follow the partials.
+size_t prefix_bytes(int B) { return align256((static_cast<size_t>(B) + 1) * 8); }
 
 bool sizes_ok(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
   return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Lmax >= 1 && d >= 1 && num_splits >= 0;
@@ -233,12 +217,10 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
     return rc;
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
-  // (one query per head: always the small kernel, 32 query rows a CTA)
-  const Plan plan = plan_for(B, Hkv, std::min(Hq / Hkv, kTcRows), max_seq_len, num_splits);
-  a.chunk = plan.chunk;
-  a.n_splits = plan.n_splits;
-  const size_t rows = static_cast<size_t>(B) * Hq * a.n_splits;
-  if ((rc = check_workspace(fn, workspace, workspace_bytes, rows * (d + 2) * 4)) != CSATTN_OK)
+  a.plan = plan_for(B, Hkv, Hq / Hkv, false, true, max_seq_len, num_splits);
+  const size_t partials = partial_bytes(a.plan, B, Hkv, d);
+  if ((rc = check_workspace(fn, workspace, workspace_bytes,
+                            align256(partials) + prefix_bytes(B))) != CSATTN_OK)
     return rc;
   a.cache = c;
   a.q = q;
@@ -253,7 +235,8 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
   a.max_seq_len = max_seq_len;
   a.min_len = 1;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = a.part_o + rows * d;
+  a.part_ml = a.part_o + partial_floats(a.plan, B, Hkv) * d;
+  a.prefix = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + align256(partials));
   int sms = 0;
   if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
   if ((rc = encoder_ready(fn)) != CSATTN_OK) return rc;
@@ -266,10 +249,11 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
 
 // Workspace of a tree step: partials, then rotated queries, masks, lengths and value flags.
 struct TreeSpace {
-  size_t q_rot, q_factor, anc, lens, vflag, total;
+  size_t prefix, q_rot, q_factor, anc, lens, vflag, total;
   TreeSpace(size_t partials, int B, int Hq, int Hkv, int Tn, int d) {
     const size_t words = (Tn + 31) / 32;
-    q_rot = align256(partials);
+    prefix = align256(partials);
+    q_rot = prefix + prefix_bytes(B);
     q_factor = q_rot + align256(static_cast<size_t>(B) * Hq * Tn * d * 2);
     anc = q_factor + align256(static_cast<size_t>(B) * Hq * Tn * 4);
     lens = anc + align256(static_cast<size_t>(B) * Tn * words * 4);
@@ -277,6 +261,11 @@ struct TreeSpace {
     total = vflag + align256(static_cast<size_t>(B) * Hkv * Tn);
   }
 };
+
+GroupPlan tree_plan(int B, int Hq, int Hkv, int Tn, bool f8, int max_seq_len, int num_splits) {
+  const int rows = Tn * (Hq / Hkv);
+  return plan_for(B, Hkv, rows, rows > kTcRows, f8, max_seq_len, num_splits);
+}
 
 int tree_step(const char* fn, const void* q_new, const void* k_new, const void* v_new,
               const KvCache& c, const int32_t* cache_lens, const int32_t* parents, void* out,
@@ -301,11 +290,8 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
     return rc;
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
-  const Plan plan = plan_for(B, Hkv, Tn * (Hq / Hkv), max_seq_len, num_splits);
-  a.chunk = plan.chunk;
-  a.n_splits = plan.n_splits;
-  const size_t rows = static_cast<size_t>(B) * Hq * Tn * a.n_splits;
-  const TreeSpace at(rows * (d + 2) * 4, B, Hq, Hkv, Tn, d);
+  a.plan = tree_plan(B, Hq, Hkv, Tn, cache_dtype == CSATTN_E4M3, max_seq_len, num_splits);
+  const TreeSpace at(partial_bytes(a.plan, B, Hkv, d), B, Hq, Hkv, Tn, d);
   if ((rc = check_workspace(fn, workspace, workspace_bytes, at.total)) != CSATTN_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
@@ -349,13 +335,14 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   a.max_seq_len = max_seq_len;
   a.min_len = 0;
   a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = a.part_o + rows * d;
+  a.part_ml = a.part_o + partial_floats(a.plan, B, Hkv) * d;
+  a.prefix = reinterpret_cast<long long*>(ws + at.prefix);
   a.after_prep = true;
   a.status = p.status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_tree_prep(p, st);
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: append launch");
-  e = plan.tc ? launch_group_tc(a, st) : launch_group_attn(a, st);
+  e = a.plan.tc ? launch_group_tc(a, st) : launch_group_attn(a, st);
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: kernel launch");
   e = launch_group_merge(a, p.vflag, v_new, out, lse, st);
   return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "attn_tree_step: merge launch");
@@ -469,7 +456,9 @@ int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const 
 
 size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
   if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits)) return 0;
-  return decode_partial_bytes(B, Hq, Hkv, Lmax, d, num_splits);
+  return align256(partial_bytes(plan_for(B, Hkv, Hq / Hkv, false, true, Lmax, num_splits), B, Hkv,
+                                d)) +
+         prefix_bytes(B);
 }
 
 int csattn_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
@@ -504,7 +493,9 @@ int csattn_attn_decode_fp8_paged(const void* q, const void* k_pages, const void*
 size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int d,
                                   int num_splits) {
   if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits) || Tn < 1 || Tn > kMaxTree) return 0;
-  return TreeSpace(partial_bytes(B, Hq, Hkv, Tn, Lmax, d, num_splits), B, Hq, Hkv, Tn, d).total;
+  // (an 8-bit cache's plan takes no less room)
+  const GroupPlan p = tree_plan(B, Hq, Hkv, Tn, true, Lmax, num_splits);
+  return TreeSpace(partial_bytes(p, B, Hkv, d), B, Hq, Hkv, Tn, d).total;
 }
 
 int csattn_attn_tree_step(const void* q_new, const void* k_new, const void* v_new, void* k_cache,

@@ -2,16 +2,17 @@
 // 8-bit cache (one query per head) and the drafts of a token tree (T queries per head).
 //
 // All T * Hq/Hkv query rows of a KV head read the same cache rows, so they are one side of a
-// matrix product and every cache row is read from HBM once per 8 * NT of them.  Grid (split *
-// row block, KV head, sequence); a CTA takes `chunk` cache rows of its sequence:
+// matrix product and every cache row is read from HBM once per 8 * NT of them.  A CTA:
 //   warp 4      TMA producer: 64-row K and V tiles into a ring
 //   warps 0..3  16 cache rows each per tile, by mma.sync m16n8k16 with the cache rows (then the
 //               channels) on the side of 16 and the query rows on the side of 8:
-//               S^T = K Q^T, then O^T += V^T P^T; softmax statistics in fp32 between the two.
+//               S^T = K Q^T, then O^T += V^T P^T; softmax statistics in fp32 between the two;
+//               each leaves a partial result of its own per piece.
+// CTAs, a wave of them, take equal ranges of all the tiles (group_work.cuh).
 // With one query per head a KV head has 4 or 8 query rows: on the side of 8 nothing or little
 // is padding, which halves products, exponentials and accumulators against the other way
-// round, and an e4m3 row is taken to f16 once for all query rows.  The splits are merged by
-// group_merge_kernel.
+// round, and an e4m3 row is taken to f16 once for all query rows.  The partial results are
+// merged by group_merge_kernel.
 //
 // e4m3 rows k8 * 2^ek, v8 * 2^ev enter the products as f16 (exact), never scaled:
 //   S column j:  x_j = (q16 . k8_j) * 2^ek_j * row factor  (q is taken to f16 with its largest
@@ -26,7 +27,10 @@
 // bits), as in the other bf16 kernels; sums are fp32 throughout.
 // A maximum is raised only when a score exceeds it by 2^8, and only then do the lanes exchange
 // theirs: the usual tile costs one vote.
+#include <climits>
+
 #include "fp8.cuh"
+#include "group_work.cuh"
 #include "internal.h"
 
 namespace csattn {
@@ -47,31 +51,28 @@ struct Cfg {
   static constexpr int STAGE = 2 * TILE;
   static constexpr int ROWS = 8 * NT;               // query rows of a CTA
   static constexpr int QS = 2 * D + 16;             // bytes between query rows (no bank twice)
-  static constexpr int OS = D + 8;                  // floats between rows of a warp's result
-  static constexpr int O_BYTES = NW * ROWS * OS * 4;
   // resident CTAs and ring: about 190 KB in flight per SM
-  static constexpr int CTAS = NT == 4 ? 2 : (F8 ? (NT == 1 ? 4 : 3) : 2);
-  static constexpr int NS = (STAGE == 32768 ? 3 : (STAGE == 16384 ? (NT == 4 ? 5 : (NT == 2 ? 4 : 3))
-                                                                  : 6));
-  static constexpr int RING = NS * STAGE > O_BYTES ? NS * STAGE : (O_BYTES + 1023) / 1024 * 1024;
-  static constexpr int Q_BYTES = ROWS * QS;
-  static constexpr int SMEM = 1024 + RING + Q_BYTES + 256 + NW * ROWS * 3 * 4 + ROWS * 4;
+  static constexpr int CTAS = F8 ? (NT == 1 ? 4 : 3) : 2;
+  static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? (NT == 1 ? 3 : 4) : 6);
+  static constexpr int RING = NS * STAGE;
+  static constexpr int Q_BYTES = ROWS * QS;         // twice: the next piece's go to the other
+  static constexpr int SMEM = 1024 + RING + 2 * Q_BYTES + 128 + 2 * ROWS * 4 + kLineSmem;
 };
 
 struct GParams {
   const __nv_bfloat16* q;
   const float* q_factor;
-  const int32_t* lens;
   const uint32_t* anc;
+  GroupLine line;
   CacheRows rows;
   const uint8_t* k_scale;
   const uint8_t* v_scale;
-  int drafts, words, rope;
+  int words, rope;
   int box_rows;
   float* part_o;
   float* part_ml;
   uint32_t* status;
-  int Hq, Hkv, T, rep, max_seq_len, min_len, chunk, n_splits, mblocks;
+  int Hq, Hkv, T, rep, rblocks, part_rows;
   float scale_log2;
   RopeTable theta;
 };
@@ -150,38 +151,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
                       const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, F8, NT>;
   constexpr int NS = C::NS;
-  constexpr bool kQInRegs = NT <= 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* s_q = smem + C::RING;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING + C::Q_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING + 2 * C::Q_BYTES);
   uint64_t* empty = full + NS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
-  float* s_ml = reinterpret_cast<float*>(smem + C::RING + C::Q_BYTES + 256);  // [NW][ROWS][3]
-  float* s_qf = s_ml + NW * C::ROWS * 3;                                      // [ROWS]
-
-  const int split = blockIdx.x / p.mblocks, mb = blockIdx.x - split * p.mblocks;
-  const int kvh = blockIdx.y, b = blockIdx.z;
+  float* s_qf = reinterpret_cast<float*>(smem + C::RING + 2 * C::Q_BYTES + 128);  // [2][ROWS]
+  uint8_t* s_line = reinterpret_cast<uint8_t*>(s_qf + 2 * C::ROWS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // what launch_tree_prep wrote is visible from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // let the merge be scheduled once every CTA has started; it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int L = p.lens[b];  // rows that every query sees
-  if (L < p.min_len || L > p.max_seq_len - p.drafts) {
-    // (launch_tree_prep has reported what it marks with -1)
-    if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && (p.drafts == 0 || L != -1))
-      atomicOr(p.status, kStatusDeviceArg);
-    return;
-  }
-  const int total = L + p.drafts;
-  const int k_begin = split * p.chunk;
-  const int k_end = min(total, k_begin + p.chunk);
-  if (k_begin >= k_end) return;  // the merge reads only splits that hold rows
-  const int ntiles = (k_end - k_begin + KT - 1) / KT;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
@@ -190,7 +174,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  __syncthreads();
+  // (launch_tree_prep has reported what it marks with -1)
+  GroupPiece pc = group_start(p.line, s_line, p.status, p.line.drafts > 0 ? -1 : INT_MIN);
+  if (pc.n == 0) return;
 
   if (warp == NW) {
     // ------------------------------------------------------------ producer
@@ -202,45 +188,51 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       tma_prefetch_desc(&tm_v);
     }
     const CacheRows& R = p.rows;
-    const int nbox = KT / p.box_rows;
+    const int nbox = KT / p.box_rows, r0 = lane * p.box_rows;
     int issued = 0;
-    for (int t = 0; t < ntiles; ++t) {
-      const int s = t % NS, use = t / NS;
-      int plane = b * p.Hkv + kvh, prow = k_begin + t * KT;
-      const int r0 = lane * p.box_rows;
-      if (lane < nbox && R.block_table != nullptr) {
-        const int tr = prow + r0;
-        plane = R.num_pages * p.Hkv;
-        prow = 0;
-        if (tr < total) {
-          const int page = R.block_table[static_cast<size_t>(b) * R.max_pages + tr / R.page_size];
-          if (page >= 0 && page < R.num_pages)
-            plane = page * p.Hkv + kvh;
-          else
-            atomicOr(p.status, kStatusDeviceArg);
-          prow = tr % R.page_size;
+    bool ok = true;
+    for (; pc.n > 0 && ok; pc.next(p.line)) {
+      const int b = pc.b, kvh = pc.head / p.rblocks, total = pc.L + p.line.drafts;
+      for (int t = 0; t < pc.n; ++t) {
+        const int s = issued % NS, use = issued / NS;
+        int plane = b * p.Hkv + kvh, prow = (pc.t0 + t) * KT;
+        if (lane < nbox && R.block_table != nullptr) {
+          const int tr = prow + r0;
+          plane = R.num_pages * p.Hkv;
+          prow = 0;
+          if (tr < total) {
+            const int page =
+                R.block_table[static_cast<size_t>(b) * R.max_pages + tr / R.page_size];
+            if (page >= 0 && page < R.num_pages)
+              plane = page * p.Hkv + kvh;
+            else
+              atomicOr(p.status, kStatusDeviceArg);
+            prow = tr % R.page_size;
+          }
         }
+        int okw = 1;
+        if (lane == 0) {
+          if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
+            okw = 0;
+          else
+            mbar_arrive_expect_tx(&full[s], C::STAGE);
+        }
+        if (!__shfl_sync(0xffffffffu, okw, 0)) {
+          ok = false;
+          break;
+        }
+        if (lane < nbox) {
+          uint8_t* kd = smem + s * C::STAGE + r0 * (F8 ? D : 128);
+          uint8_t* vd = kd + C::TILE;
+          constexpr int kBlocks = F8 ? 1 : D / 64;
+          for (int kb = 0; kb < kBlocks; ++kb)
+            tma_load_3d(kd + kb * (KT * 128), &tm_k, &full[s], kb * 64, prow, plane);
+          for (int kb = 0; kb < kBlocks; ++kb)
+            tma_load_3d(vd + kb * (KT * 128), &tm_v, &full[s], kb * 64, prow, plane);
+        }
+        __syncwarp();
+        ++issued;
       }
-      int okw = 1;
-      if (lane == 0) {
-        if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
-          okw = 0;
-        else
-          mbar_arrive_expect_tx(&full[s], C::STAGE);
-      }
-      okw = __shfl_sync(0xffffffffu, okw, 0);
-      if (!okw) break;
-      if (lane < nbox) {
-        uint8_t* kd = smem + s * C::STAGE + r0 * (F8 ? D : 128);
-        uint8_t* vd = kd + C::TILE;
-        constexpr int kBlocks = F8 ? 1 : D / 64;
-        for (int kb = 0; kb < kBlocks; ++kb)
-          tma_load_3d(kd + kb * (KT * 128), &tm_k, &full[s], kb * 64, prow, plane);
-        for (int kb = 0; kb < kBlocks; ++kb)
-          tma_load_3d(vd + kb * (KT * 128), &tm_v, &full[s], kb * 64, prow, plane);
-      }
-      __syncwarp();
-      ++issued;
     }
     if (lane == 0 && *abort_flag) {
       const int first = issued > NS ? issued - NS : 0;
@@ -251,10 +243,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   }
 
   // ---------------------------------------------------------------- compute warps
-  const int M = p.T * p.rep;          // query rows of the KV head: row = t * rep + head
-  const int row_base = mb * C::ROWS;  // first of this CTA
-  const int r0 = lane >> 2;           // fragment rows r0 and r0 + 8 (cache rows)
-  const int cq = 2 * (lane & 3);      // fragment columns cq and cq + 1 (query rows)
+  const int M = p.T * p.rep;      // query rows of the KV head: row = t * rep + head
+  const int r0 = lane >> 2;       // fragment rows r0 and r0 + 8 (cache rows)
+  const int cq = 2 * (lane & 3);  // fragment columns cq and cq + 1 (query rows)
+  const int mi = lane >> 3;       // which 8x8 matrix this lane addresses
+  const uint32_t smem_base = smem_u32(smem);
+  // addresses of the lane's matrix rows within a tile
+  const int kr = 16 * warp + (lane & 7) + 8 * (mi & 1);
+  const int vr = 16 * warp + (lane & 7) + 8 * (F8 ? (mi & 1) : (mi >> 1));
+  bool ok = true;
+  int used = 0;  // tiles of the CTA so far
+  for (int piece = 0; pc.n > 0; pc.next(p.line), ++piece) {
+  const int b = pc.b, kvh = pc.head / p.rblocks, L = pc.L, total = L + p.line.drafts;
+  const int row_base = (pc.head - kvh * p.rblocks) * C::ROWS;  // first query row
+  const int k_begin = pc.t0 * KT, ntiles = pc.n;
+  const int k_end = min(total, k_begin + ntiles * KT);
 
   // scale bytes of the warp's 16 rows of a tile: lanes 0..15 the keys', 16..31 the values';
   // rows past the sequence and pages outside the pool read 0 (their data is zero or masked)
@@ -288,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       if (F8 && p.q_factor == nullptr)
         factor = query_to_f16<G>(lo, hi, p.rope, L - 1, p.theta, c);
       if (r >= C::ROWS) continue;  // (no shuffle below)
-      if (F8 && c == 0) s_qf[r] = factor * p.scale_log2;
-      uint8_t* dst = s_q + r * C::QS;
+      if (F8 && c == 0) s_qf[(piece & 1) * C::ROWS + r] = factor * p.scale_log2;
+      uint8_t* dst = s_q + (piece & 1) * C::Q_BYTES + r * C::QS;
       if constexpr (F8) {
         // a lane's four bytes of a K row are channels 4(lane%4).. of 16, so the product's
         // index runs over the 16 channels as 0 1, 4 5, 8 9, 12 13, then 2 3, 6 7, ...
@@ -309,27 +312,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   }
   asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
 
-  const int mi = lane >> 3;  // which 8x8 matrix this lane addresses
-  const uint32_t q_addr = smem_u32(s_q) + (lane & 7) * C::QS + mi * 16;
-  uint32_t qb[kQInRegs ? NT : 1][D / 16][2];
-  if constexpr (kQInRegs) {
+  const uint32_t q_addr = smem_u32(s_q + (piece & 1) * C::Q_BYTES) + (lane & 7) * C::QS + mi * 16;
+  uint32_t qb[NT][D / 16][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int kk = 0; kk < D / 16; kk += 2) {
-        uint32_t w[4];
-        ldsm_x4(q_addr + j * 8 * C::QS + kk * 32, w);
-        qb[j][kk][0] = w[0];
-        qb[j][kk][1] = w[1];
-        qb[j][kk + 1][0] = w[2];
-        qb[j][kk + 1][1] = w[3];
-      }
-  }
+    for (int kk = 0; kk < D / 16; kk += 2) {
+      uint32_t w[4];
+      ldsm_x4(q_addr + j * 8 * C::QS + kk * 32, w);
+      qb[j][kk][0] = w[0];
+      qb[j][kk][1] = w[1];
+      qb[j][kk + 1][0] = w[2];
+      qb[j][kk + 1][1] = w[3];
+    }
   float qf[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) qf[j][h] = F8 ? s_qf[8 * j + cq + h] : p.scale_log2;
+    for (int h = 0; h < 2; ++h) qf[j][h] = F8 ? s_qf[(piece & 1) * C::ROWS + 8 * j + cq + h] : p.scale_log2;
 
   float o[D / 16][NT][4];
   float m_used[NT][2], n_used[NT][2], l_part[NT][2];
@@ -340,16 +340,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
 #pragma unroll
     for (int h = 0; h < 2; ++h) m_used[j][h] = n_used[j][h] = -INFINITY, l_part[j][h] = 0.f;
   }
-  const uint32_t smem_base = smem_u32(smem);
-  // addresses of the lane's matrix rows within a tile
-  const int kr = 16 * warp + (lane & 7) + 8 * (mi & 1);
-  const int vr = 16 * warp + (lane & 7) + 8 * (F8 ? (mi & 1) : (mi >> 1));
 
-  bool ok = true, unset = true;  // unset: some query row has no maximum yet
-  for (int t = 0; t < ntiles; ++t) {
-    const int s = t % NS;
+  bool unset = true;  // some query row has no maximum yet
+  for (int t = 0; t < ntiles && ok; ++t, ++used) {
+    const int s = used % NS;
     const uint32_t codes2 = load_codes(t + 2);
-    if (!mbar_wait(&full[s], (t / NS) & 1, abort_flag, p.status, kWaitNs)) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (used / NS) & 1, abort_flag, p.status,
+                                           kWaitNs))) {
       ok = false;
       break;
     }
@@ -378,15 +375,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        if constexpr (kQInRegs) {
-          mma<F8>(sc[j], a[0], qb[j][kk][0], qb[j][kk][1]);
-          mma<F8>(sc[j], a[1], qb[j][kk + 1][0], qb[j][kk + 1][1]);
-        } else {
-          uint32_t w[4];
-          ldsm_x4(q_addr + j * 8 * C::QS + kk * 32, w);
-          mma<F8>(sc[j], a[0], w[0], w[1]);
-          mma<F8>(sc[j], a[1], w[2], w[3]);
-        }
+        mma<F8>(sc[j], a[0], qb[j][kk][0], qb[j][kk][1]);
+        mma<F8>(sc[j], a[1], qb[j][kk + 1][0], qb[j][kk + 1][1]);
       }
     }
     // factors of the thread's two cache rows
@@ -561,102 +551,110 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 8);
       l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 16);
     }
-  // all tiles consumed: the ring is free to hold the per-warp results
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
-  if (!ok || *abort_flag) return;
-  float* s_o = reinterpret_cast<float*>(smem);  // [NW][ROWS][OS]
+  if (!ok) continue;  // (to the end: the warps' barriers go together)
+  // the warp's partial result, relative to the maximum of x
+  const size_t slot =
+      (static_cast<size_t>(blockIdx.x) + pc.segment(p.line)) * NW + warp;
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int rr = warp * C::ROWS + 8 * j + cq + h;
-      if (r0 == 0) {
-        s_ml[rr * 3 + 0] = m_used[j][h];
-        s_ml[rr * 3 + 1] = l_part[j][h];
-        s_ml[rr * 3 + 2] = n_used[j][h];
-      }
+      const int r = 8 * j + cq + h;
+      if (row_base + r >= M) continue;
+      // (a row that saw nothing holds zeros, or NaN if its scores were NaN)
+      const float f =
+          F8 && n_used[j][h] != -INFINITY ? ex2_approx(n_used[j][h] - kWeightLog2) : 1.f;
+      const size_t at = slot * p.part_rows + r;
+      float* dst = p.part_o + at * D;
+      if (r0 == 0)
+        *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_used[j][h], l_part[j][h]);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        float* at = s_o + rr * C::OS + 16 * c;
         if constexpr (F8) {
-          *reinterpret_cast<float2*>(at + 2 * r0) = make_float2(o[c][j][h], o[c][j][2 + h]);
+          *reinterpret_cast<float2*>(dst + 16 * c + 2 * r0) =
+              make_float2(o[c][j][h] * f, o[c][j][2 + h] * f);
         } else {
-          at[r0] = o[c][j][h];
-          at[r0 + 8] = o[c][j][2 + h];
+          dst[16 * c + r0] = o[c][j][h];
+          dst[16 * c + r0 + 8] = o[c][j][2 + h];
         }
       }
-    }
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
-  // merge the warps' slices; one partial per query row, relative to the maximum of x
-  for (int e = threadIdx.x; e < C::ROWS * (D / 4); e += 32 * NW) {
-    const int r = e / (D / 4), c = e % (D / 4), row = row_base + r;
-    if (row >= M) break;
-    float m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) m = fmaxf(m, s_ml[(w * C::ROWS + r) * 3]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float* ml = s_ml + (w * C::ROWS + r) * 3;
-      // (a warp that saw nothing holds zeros, or NaN if its scores were NaN)
-      const bool none = ml[0] == -INFINITY;
-      l += (none ? 1.f : ex2_approx(ml[0] - m)) * ml[1];
-      const float fw =
-          none ? 1.f : ex2_approx(F8 ? ml[0] - m + (ml[2] - kWeightLog2) : ml[0] - m);
-      const float4 v = *reinterpret_cast<const float4*>(s_o + (w * C::ROWS + r) * C::OS + 4 * c);
-      acc.x += fw * v.x;
-      acc.y += fw * v.y;
-      acc.z += fw * v.z;
-      acc.w += fw * v.w;
-    }
-    const int t = row / p.rep, h = kvh * p.rep + row - t * p.rep;
-    const size_t at =
-        ((static_cast<size_t>(b) * p.Hq + h) * p.T + t) * static_cast<size_t>(p.n_splits) + split;
-    *reinterpret_cast<float4*>(p.part_o + at * D + 4 * c) = acc;
-    if (c == 0) {
-      p.part_ml[2 * at] = m;
-      p.part_ml[2 * at + 1] = l;
     }
   }
 }
 
-// out[b, h, t, :] = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the splits that hold
-// rows of sequence b.  A warp per query row, four (d = 128) or two channels per lane.
-template <int D>
+// out[b, h, t, :] = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the partial results of a
+// query row: `subs` for each piece of its segment.  W warps per row (W > 1 for few rows with
+// many partials), four (d = 128) or two channels per lane.
+template <int D, int W>
 __global__ void __launch_bounds__(128) group_merge_kernel(
-    const float* __restrict__ part_o, const float* __restrict__ part_ml,
-    const int32_t* __restrict__ lens, const uint32_t* __restrict__ anc,
-    const uint8_t* __restrict__ vflag, const __nv_bfloat16* __restrict__ v_new, bool f8,
-    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int rows, int Hq, int Hkv, int T,
-    int drafts, int words, int n_splits, int chunk, int min_len, int max_seq_len) {
+    const float* __restrict__ part_o, const float* __restrict__ part_ml, const GroupLine line,
+    int grid, int subs, int part_rows, int block_rows, int rblocks,
+    const uint32_t* __restrict__ anc, const uint8_t* __restrict__ vflag,
+    const __nv_bfloat16* __restrict__ v_new, bool f8, __nv_bfloat16* __restrict__ out,
+    float* __restrict__ lse, int rows, int Hq, int Hkv, int T, int words) {
   constexpr int V = D / 32;
-  const int row = static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  __shared__ float s_part[W > 1 ? 4 : 1][V * 32 + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = static_cast<int>(blockIdx.x) * (4 / W) + warp / W;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= rows) return;
-  const int t = row % T, bh = row / T, b = bh / Hq, g = (bh - b * Hq) / (Hq / Hkv);
-  const int L = lens[b];
+  if (row >= rows) return;  // (W > 1: the whole CTA)
+  const int rep = Hq / Hkv;
+  const int t = row % T, bh = row / T, b = bh / Hq, h = bh - b * Hq, g = h / rep;
   const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
+  const int tiles = line.tiles(line.lens[b]);
+  // the segment's place on the line, and from it its pieces
+  const int qrow = t * rep + h - g * rep, rb = qrow / block_rows;
+  const int head = g * rblocks + rb, seg = b * line.heads + head;
+  const long long all = line.prefix[line.B] * line.heads;
+  const long long per = line.tiles_per_cta > 0 ? line.tiles_per_cta : (all + grid - 1) / grid;
+  const long long s0 = line.prefix[b] * line.heads + static_cast<long long>(head) * tiles;
   int ns = 0;
-  if (L >= min_len && L <= max_seq_len - drafts) ns = (L + drafts + chunk - 1) / chunk;
-  if (drafts > 0 && ((mine[t >> 5] >> (t & 31)) & 1u) == 0u) ns = 0;  // not a token
-  const float* ml = part_ml + static_cast<size_t>(row) * n_splits * 2;
-  const float* po = part_o + static_cast<size_t>(row) * n_splits * D + V * lane;
+  long long first = 0;
+  if (tiles > 0 && (line.drafts == 0 || ((mine[t >> 5] >> (t & 31)) & 1u) != 0u)) {
+    first = s0 / per;
+    ns = static_cast<int>((s0 + tiles - 1) / per - first + 1) * subs;
+  }
+  // partial i of the row is row qrow - rb * block_rows of slot (first + seg) * subs + i
+  const size_t at0 = static_cast<size_t>(first + seg) * subs * part_rows + qrow - rb * block_rows;
   float m = -INFINITY;
-  for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[2 * s]);
+  for (int s = lane; s < ns; s += 32)
+    m = fmaxf(m, part_ml[2 * (at0 + static_cast<size_t>(s) * part_rows)]);
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
   float acc[V], l = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < ns; ++s) {
-    const float ms = ml[2 * s];
-    const float f = ms == -INFINITY ? 1.f : ex2_approx(ms - m);  // (a split that saw nothing: 0)
-    l += f * ml[2 * s + 1];
+  for (int s = warp % W; s < ns; s += W) {
+    const size_t at = at0 + static_cast<size_t>(s) * part_rows;
+    const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * at);
+    const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);  // (one that saw nothing: 0)
+    l += f * ml.y;
+    const float* po = part_o + at * D + V * lane;
+    if constexpr (V == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(po);
+      acc[0] += f * x.x;
+      acc[1] += f * x.y;
+      acc[2] += f * x.z;
+      acc[3] += f * x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(po);
+      acc[0] += f * x.x;
+      acc[1] += f * x.y;
+    }
+  }
+  if constexpr (W > 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += f * po[static_cast<size_t>(s) * D + i];
+    for (int i = 0; i < V; ++i) s_part[warp][V * lane + i] = acc[i];
+    if (lane == 0) s_part[warp][V * 32] = l;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      l += s_part[w][V * 32];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += s_part[w][V * lane + i];
+    }
   }
   const bool any = !(l <= 0.f);  // NaN stays
   const float inv = any ? 1.f / l : 0.f;
@@ -693,13 +691,12 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   GParams p{};
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.q_factor = a.q_factor;
-  p.lens = a.lens;
   p.anc = a.anc;
+  p.line = group_line(a);
   p.rows = CacheRows{a.cache.block_table, a.Hkv, a.cache.Lmax, a.cache.page_size,
                      a.cache.num_pages, a.cache.max_pages};
   p.k_scale = static_cast<const uint8_t*>(a.cache.k_scale);
   p.v_scale = static_cast<const uint8_t*>(a.cache.v_scale);
-  p.drafts = a.drafts;
   p.words = a.words;
   p.rope = a.rope;
   const bool paged = a.cache.block_table != nullptr;
@@ -711,11 +708,8 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.Hkv = a.Hkv;
   p.T = a.T;
   p.rep = a.Hq / a.Hkv;
-  p.max_seq_len = a.max_seq_len;
-  p.min_len = a.min_len;
-  p.chunk = a.chunk;
-  p.n_splits = a.n_splits;
-  p.mblocks = (a.T * p.rep + C::ROWS - 1) / C::ROWS;
+  p.rblocks = a.plan.rblocks;
+  p.part_rows = a.plan.part_rows;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.theta = a.theta;
 
@@ -731,7 +725,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   cudaError_t e = smem_limit.set(group_attn_kernel<D, F8, NT>, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_splits) * p.mblocks, a.Hkv, a.B);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.plan.grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
@@ -745,10 +739,28 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
 
 template <int D, bool F8>
 cudaError_t launch_rows(const GroupArgs& a, cudaStream_t stream) {
-  const int rows = a.T * (a.Hq / a.Hkv);
-  if (rows <= 8) return launch_t<D, F8, 1>(a, stream);
-  if (rows <= 16) return launch_t<D, F8, 2>(a, stream);
-  return launch_t<D, F8, 4>(a, stream);
+  return a.plan.block_rows <= 8 ? launch_t<D, F8, 1>(a, stream) : launch_t<D, F8, 2>(a, stream);
+}
+
+template <int D, int W>
+cudaError_t launch_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new, void* out,
+                         float* lse, cudaStream_t stream) {
+  const int rows = a.B * a.Hq * a.T;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((static_cast<unsigned>(rows) + 4 / W - 1) / (4 / W), 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(
+      &cfg, group_merge_kernel<D, W>, static_cast<const float*>(a.part_o),
+      static_cast<const float*>(a.part_ml), group_line(a), a.plan.grid, a.plan.subs,
+      a.plan.part_rows, a.plan.block_rows, a.plan.rblocks, a.anc, vflag,
+      static_cast<const __nv_bfloat16*>(v_new), a.cache.k_scale != nullptr,
+      static_cast<__nv_bfloat16*>(out), lse, rows, a.Hq, a.Hkv, a.T, a.words);
 }
 
 }  // namespace
@@ -761,22 +773,12 @@ cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_group_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
                                void* out, float* lse, cudaStream_t stream) {
-  const int rows = a.B * a.Hq * a.T;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((static_cast<unsigned>(rows) + 3) / 4, 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(
-      &cfg, a.d == 128 ? group_merge_kernel<128> : group_merge_kernel<64>,
-      static_cast<const float*>(a.part_o), static_cast<const float*>(a.part_ml), a.lens, a.anc,
-      vflag, static_cast<const __nv_bfloat16*>(v_new), a.cache.k_scale != nullptr,
-      static_cast<__nv_bfloat16*>(out), lse, rows, a.Hq, a.Hkv, a.T, a.drafts, a.words,
-      a.n_splits, a.chunk, a.min_len, a.max_seq_len);
+  // few rows: four warps each, so that the partials are read side by side
+  if (a.B * a.Hq * a.T <= 4096)
+    return a.d == 128 ? launch_merge<128, 4>(a, vflag, v_new, out, lse, stream)
+                      : launch_merge<64, 4>(a, vflag, v_new, out, lse, stream);
+  return a.d == 128 ? launch_merge<128, 1>(a, vflag, v_new, out, lse, stream)
+                    : launch_merge<64, 1>(a, vflag, v_new, out, lse, stream);
 }
 
 }  // namespace csattn

@@ -8,12 +8,13 @@
 //   more than 128 query rows: stream x is query tile x, both see every cache tile;
 //   up to 128: stream x takes every second cache tile, with sums of its own that meet at
 //              the end.
-// Grid (split * row block, KV head, sequence), one CTA per SM:
-//   warps 0-3, 4-7  softmax of stream 0 and 1, a query row per thread; before that they
-//                   write the queries to shared memory, at the end the partial results
+// One CTA per SM; the CTAs take equal ranges of all the tiles (group_work.cuh), and the rings
+// and barriers run on from one piece to the next:
+//   warps 0-3, 4-7  softmax of stream 0 and 1, a query row per thread; they also write a
+//                   piece's queries to shared memory and its partial results at its end
 //   warp 8          TMA producer          warp 9   TMEM owner and MMA issuer (one thread)
 //   warps 10-11     bf16: clean the values of tiles that not every query sees
-//   warps 12-15     e4m3: take the tiles to f16
+//   warps 12-15     e4m3: take the keys' tiles to f16;  warps 16-19  the values'
 // TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D) O_1 [256+D,256+2D); P overwrites the
 // first half of its S and is read by the second product from there.
 //
@@ -40,7 +41,8 @@ constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 1
 
 template <int D, bool F8>
 struct Cfg {
-  static constexpr int kThreads = F8 ? 512 : 384;
+  // e4m3: registers move from the other warpgroups to the softmax (2*144 + 64 + 2*64 = 5*96)
+  static constexpr int kThreads = F8 ? 640 : 384;
   static constexpr int TILE = BN * D * 2;  // a Q, K or V tile of 16-bit values
   static constexpr int RAW = BN * D;       // an e4m3 tile
   static constexpr int NRAW = F8 ? 4 : 0;
@@ -49,30 +51,53 @@ struct Cfg {
   static constexpr int NS1 = F8 ? 4 : (D == 128 ? 6 : 8);
   static constexpr int NS2 = F8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
   static constexpr int TILES = (NS1 + 1 > NS2 + 2 ? NS1 + 1 : NS2 + 2) * TILE + NRAW * RAW;
-  static constexpr int SMEM = 1024 + TILES + 320 + 128 * 8 + (F8 ? 8 * 8 + 2 * 256 + 32 : 0);
+  static constexpr int BARS = 336;
+  static constexpr int SMEM = 1024 + TILES + BARS + 128 * 8 + (F8 ? 8 * 8 + 2 * 256 + 64 : 0);
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 struct TParams {
   const uint16_t* q;
   const float* q_factor;
-  const int32_t* lens;
   const uint32_t* anc;
+  GroupLine line;
   CacheRows rows;
   const uint8_t* k_scale;
   const uint8_t* v_scale;
-  int drafts, words;
+  int words;
   int box_rows;
   float* part_o;
   float* part_ml;
   uint32_t* status;
-  int Hq, Hkv, T, rep, max_seq_len, min_len, chunk, n_splits, rblocks, pair;
+  int Hq, Hkv, T, rep, rblocks, part_rows, pair;
   float scale_log2;
+};
+
+// What a piece is to every role.
+struct View {
+  int b, kvh, rb;            // sequence, KV head, block of query rows
+  int L, total;              // rows every query sees, and with the drafts
+  int k_begin, k_end, n;     // cache rows and tiles of the piece
+  int first_edge;            // first tile with rows that not every query sees
+  __device__ __forceinline__ View(const GroupPiece& pc, const TParams& p)
+      : b(pc.b), kvh(pc.head / p.rblocks), rb(pc.head - kvh * p.rblocks), L(pc.L),
+        total(pc.L + p.line.drafts), k_begin(pc.t0 * BN),
+        k_end(min(total, k_begin + pc.n * BN)), n(pc.n),
+        first_edge(max(0, min(n, (min(L, k_end) - k_begin) / BN))) {}
 };
 
 // f16 or bf16 operands, fp32 accumulators, M = 128
 constexpr uint32_t idesc(bool f16, int N, int b_mn) {
   return idesc_bf16_f32(128, N, 0, b_mn) & (f16 ? ~((7u << 7) | (7u << 10)) : ~0u);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
@@ -136,47 +161,30 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   uint64_t* s_full = bars + 2;     // [2]
   uint64_t* p_full = bars + 4;     // [2]
   uint64_t* o_full = bars + 6;     // [2]
-  uint64_t* teardown = bars + 8;
-  uint64_t* kv_full = bars + 9;    // [8]
-  uint64_t* kv_empty = bars + 17;  // [8]
-  uint64_t* raw_full = bars + 25;  // [4]
-  uint64_t* raw_empty = bars + 29; // [4]
-  uint64_t* edge_full = bars + 33; // [4] bf16: values to be cleaned, one per edge tile (256
-                                   // drafts that begin inside a tile touch three)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 37);
+  uint64_t* o_empty = bars + 8;    // [2]
+  uint64_t* teardown = bars + 10;
+  uint64_t* kv_full = bars + 11;   // [8]
+  uint64_t* kv_empty = bars + 19;  // [8]
+  uint64_t* raw_full = bars + 27;  // [4]
+  uint64_t* raw_empty = bars + 31; // [4]
+  uint64_t* edge_full = bars + 35; // [4] bf16: values to be cleaned, edge tile by edge tile
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 39);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float2* s_ml = reinterpret_cast<float2*>(smem + C::TILES + 320);  // [128]
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::TILES + C::BARS);  // [128]
   float2* s_tile = s_ml + 128;                           // e4m3 [8]: 2^(E_k - 7), E_v of a tile
   uint16_t* s_mul = reinterpret_cast<uint16_t*>(s_tile + 8);  // e4m3 [2][128] row factors
-  int* s_max = reinterpret_cast<int*>(s_mul + 256);           // e4m3 [2][4]
-
-  const int split = blockIdx.x / p.rblocks, rb = blockIdx.x - split * p.rblocks;
-  const int kvh = blockIdx.y, b = blockIdx.z;
+  int* s_max = reinterpret_cast<int*>(s_mul + 256);           // e4m3 [4][4]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int L = p.lens[b];
-  if (L < p.min_len || L > p.max_seq_len - p.drafts) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && (p.drafts == 0 || L != -1))
-      atomicOr(p.status, kStatusDeviceArg);
-    return;
-  }
-  const int total = L + p.drafts;
-  const int k_begin = split * p.chunk;
-  const int k_end = min(total, k_begin + p.chunk);
-  if (k_begin >= k_end) return;
-  const int n = (k_end - k_begin + BN - 1) / BN;  // tiles
-  const int step = pair ? 1 : 2;                  // between a stream's tiles
-  // first tile with rows that not every query sees
-  const int first_edge = max(0, min(n, (min(L, k_end) - k_begin) / BN));
-
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_ready[x], 4);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
+      mbar_init(&o_empty[x], 4);
     }
     mbar_init(teardown, 1);
     for (int s = 0; s < 8; ++s) {
@@ -191,13 +199,19 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  static_assert(kLineSmem <= 128 * 8, "the line's sums share s_ml");
+  GroupPiece pc = group_start(p.line, reinterpret_cast<uint8_t*>(s_ml), p.status, -1);
+  if (pc.n == 0) return;
+  const int step = pair ? 1 : 2;  // between a stream's tiles
   if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kWarpProducer) {
+  if (warp >= 8 && warp < 12) {
+   if constexpr (F8) regs_dec<64>();
+   if (warp == kWarpProducer) {
     // ------------------------------------------------------------ TMA producer
     // fills K_0, V_0, K_1, V_1, ...; lane i copies box i of a tile (see group_attn.cu)
     if (lane == 0) {
@@ -209,63 +223,68 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const uint32_t depth = F8 ? C::NRAW : NS;
     uint64_t* full = F8 ? raw_full : kv_full;
     uint64_t* empty = F8 ? raw_empty : kv_empty;
-    // the barrier of fill f: bf16 values of edge tiles go by way of the cleaning warps
-    auto landed = [&](uint32_t f) {
-      const int i = static_cast<int>(f >> 1) - first_edge;
-      return !F8 && (f & 1u) && i >= 0 ? &edge_full[i] : &full[f % depth];
-    };
-    uint32_t f = 0;
+    uint32_t f = 0, edges = 0;
+    uint64_t recent = 0;  // a byte per fill, the latest lowest: 8 + (edge % 8), or 0
     bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
-      int plane = b * p.Hkv + kvh, prow = k_begin + j * BN;
-      if (lane < nbox && R.block_table != nullptr) {
-        const int tr = prow + r0;
-        plane = R.num_pages * p.Hkv;
-        prow = 0;
-        if (tr < total) {
-          const int page = R.block_table[static_cast<size_t>(b) * R.max_pages + tr / R.page_size];
-          if (page >= 0 && page < R.num_pages)
-            plane = page * p.Hkv + kvh;
-          else
-            atomicOr(p.status, kStatusDeviceArg);
-          prow = tr % R.page_size;
-        }
-      }
-      for (int v = 0; v < 2; ++v, ++f) {
-        const uint32_t s = f % depth, use = f / depth;
-        int okw = 1;
-        if (lane == 0) {
-          if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
-            okw = 0;
-          else
-            mbar_arrive_expect_tx(landed(f), F8 ? C::RAW : C::TILE);
-        }
-        okw = __shfl_sync(0xffffffffu, okw, 0);
-        if (!okw) {
-          ok = false;
-          break;
-        }
-        const CUtensorMap* tm = v == 0 ? &tm_k : &tm_v;
-        if (lane < nbox) {
-          if constexpr (F8) {
-            tma_load_3d(sRaw + s * C::RAW + r0 * D, tm, landed(f), 0, prow, plane);
-          } else {
-            for (int kb = 0; kb < D / 64; ++kb)
-              tma_load_3d(sKV + s * C::TILE + kb * (BN * 128) + r0 * 128, tm, landed(f), kb * 64,
-                          prow, plane);
+    for (; pc.n > 0 && ok; pc.next(p.line)) {
+      const View w(pc, p);
+      for (int j = 0; j < w.n && ok; ++j) {
+        int plane = w.b * p.Hkv + w.kvh, prow = w.k_begin + j * BN;
+        if (lane < nbox && R.block_table != nullptr) {
+          const int tr = prow + r0;
+          plane = R.num_pages * p.Hkv;
+          prow = 0;
+          if (tr < w.total) {
+            const int page =
+                R.block_table[static_cast<size_t>(w.b) * R.max_pages + tr / R.page_size];
+            if (page >= 0 && page < R.num_pages)
+              plane = page * p.Hkv + w.kvh;
+            else
+              atomicOr(p.status, kStatusDeviceArg);
+            prow = tr % R.page_size;
           }
         }
-        __syncwarp();
+        for (int v = 0; v < 2; ++v, ++f) {
+          const uint32_t s = f % depth, use = f / depth;
+          // bf16 values of edge tiles go by way of the cleaning warps
+          const bool edge = !F8 && v == 1 && j >= w.first_edge;
+          uint64_t* landed = edge ? &edge_full[edges & 3] : &full[s];
+          int okw = 1;
+          if (lane == 0) {
+            if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
+              okw = 0;
+            else
+              mbar_arrive_expect_tx(landed, F8 ? C::RAW : C::TILE);
+          }
+          if (!__shfl_sync(0xffffffffu, okw, 0)) {
+            ok = false;
+            break;
+          }
+          const CUtensorMap* tm = v == 0 ? &tm_k : &tm_v;
+          if (lane < nbox) {
+            if constexpr (F8) {
+              tma_load_3d(sRaw + s * C::RAW + r0 * D, tm, landed, 0, prow, plane);
+            } else {
+              for (int kb = 0; kb < D / 64; ++kb)
+                tma_load_3d(sKV + s * C::TILE + kb * (BN * 128) + r0 * 128, tm, landed, kb * 64,
+                            prow, plane);
+            }
+          }
+          recent = (recent << 8) | (edge ? 8u + (edges & 7u) : 0u);
+          edges += edge;
+          __syncwarp();
+        }
       }
     }
     if (lane == 0 && *abort_flag) {
       // every copy still in flight lands before the CTA's shared memory is released
-      const uint32_t first = f > depth ? f - depth : 0u;
-      for (uint32_t i = first; i < f; ++i)
-        mbar_wait(landed(i), landed(i) == &full[i % depth] ? (i / depth) & 1 : 0, nullptr,
-                  p.status, kDrainNs);
+      for (uint32_t i = 1; i <= depth && i <= f; ++i, recent >>= 8) {
+        const uint32_t e = recent & 15u;
+        mbar_wait(e ? &edge_full[e & 3u] : &full[(f - i) % depth],
+                  e ? (e >> 2) & 1u : ((f - i) / depth) & 1u, nullptr, p.status, kDrainNs);
+      }
     }
-  } else if (warp == kWarpMma) {
+   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t kv0 = smem_u32(sKV);
@@ -278,9 +297,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         return ok;
       };
       auto full = [&](uint32_t f) { return wait(&kv_full[f % NS], (f / NS) & 1); };
-      auto qk = [&](int x, int j) {
+      // S_x = Q K^T with the keys of fill f
+      auto qk = [&](int x, uint32_t f) {
         const uint32_t q = smem_u32(sQ) + (pair ? x : 0) * C::TILE;
-        const uint32_t k = kv0 + (2u * j % NS) * C::TILE;
+        const uint32_t k = kv0 + (f % NS) * C::TILE;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = static_cast<uint32_t>((kk >> 2) * (BN * 128) + (kk & 3) * 32);
@@ -289,123 +309,150 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         tc_commit(&s_full[x]);
       };
-      auto pv = [&](int x, int j) {
-        const uint32_t v = kv0 + ((2u * j + 1u) % NS) * C::TILE;
+      auto pv = [&](int x, uint32_t f, bool accumulate) {
+        const uint32_t v = kv0 + (f % NS) * C::TILE;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
           umma_ts(tmem + 256u + D * x, tmem + 128u * x + 8u * kk,
                   smem_desc_sw128(v + 2048u * kk, BN * 128, 1024), kIdO,
-                  (j >= step || kk > 0) ? 1u : 0u);
+                  (accumulate || kk > 0) ? 1u : 0u);
       };
-      wait(&q_ready[0], 0);
-      if (pair) wait(&q_ready[1], 0);
-      // first tiles of both streams
-      for (int j = 0; j < step && j < n; ++j) {
-        if (!full(2 * j)) break;
-        for (int x = pair ? 0 : j; x <= (pair ? 1 : j); ++x) qk(x, j);
-        tc_commit(&kv_empty[2u * j % NS]);
-      }
-      uint32_t np[2] = {0, 0};
-      for (int j = 0; j < n && ok; ++j) {
-        const int x0 = pair ? 0 : (j & 1), x1 = pair ? 1 : x0, jn = j + step;
-        for (int x = x0; x <= x1 && ok; ++x) {
-          if (!wait(&p_full[x], np[x] & 1)) break;
-          ++np[x];
-          if (x == x0 && !full(2 * j + 1)) break;
-          pv(x, j);
-          if (x == x1) tc_commit(&kv_empty[(2u * j + 1u) % NS]);
-          if (jn >= n) {
-            tc_commit(&o_full[x]);
-          } else {
-            if (x == x0 && !full(2 * jn)) break;
-            qk(x, jn);
-            if (x == x1) tc_commit(&kv_empty[2u * jn % NS]);
+      uint32_t F = 0, np[2] = {0, 0}, used[2] = {0, 0}, piece = 0;
+      for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
+        const int n = pc.n;
+        wait(&q_ready[0], piece & 1);
+        if (pair) wait(&q_ready[1], piece & 1);
+        // first tiles of both streams
+        for (int j = 0; j < step && j < n; ++j) {
+          if (!full(F + 2 * j)) break;
+          for (int x = pair ? 0 : j; x <= (pair ? 1 : j); ++x) qk(x, F + 2 * j);
+          tc_commit(&kv_empty[(F + 2 * j) % NS]);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int x0 = pair ? 0 : (j & 1), x1 = pair ? 1 : x0, jn = j + step;
+          for (int x = x0; x <= x1 && ok; ++x) {
+            if (!wait(&p_full[x], np[x] & 1)) break;
+            ++np[x];
+            if (x == x0 && !full(F + 2 * j + 1)) break;
+            // the stream's first tile of a piece: its O has been read
+            if (j < step) {
+              if (used[x] > 0 && !wait(&o_empty[x], (used[x] - 1) & 1)) break;
+              ++used[x];
+            }
+            pv(x, F + 2 * j + 1, j >= step);
+            if (x == x1) tc_commit(&kv_empty[(F + 2 * j + 1) % NS]);
+            if (jn >= n) {
+              tc_commit(&o_full[x]);
+            } else {
+              if (x == x0 && !full(F + 2 * jn)) break;
+              qk(x, F + 2 * jn);
+              if (x == x1) tc_commit(&kv_empty[(F + 2 * jn) % NS]);
+            }
           }
         }
+        F += 2 * n;
       }
       // every MMA issued above has completed once this barrier flips
       tc_commit(teardown);
       mbar_wait(teardown, 0, nullptr, p.status, kDrainNs);
     }
     __syncwarp();
-  } else if (!F8 && warp >= kWarpClean) {
+   } else if (!F8) {
     // ------------------------------------------------------------ clean values (bf16)
     // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
     // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
     // merge puts it where it belongs).
     bool ok = true;
-    for (int j = first_edge; j < n; ++j) {  // (to the end: the two warps' barriers go together)
-      const uint32_t s = (2 * j + 1) % NS;
-      ok = ok && warp_wait(&edge_full[j - first_edge], 0, abort_flag, p.status);
-      const int key0 = k_begin + j * BN;
-      uint8_t* tile = sKV + s * C::TILE;
-      for (int e = threadIdx.x - 32 * kWarpClean; ok && e < BN * (D / 8); e += 64) {
-        // (chunks of a row in any order: all are treated alike)
-        const int kb = e / (BN * 8), r = e / 8 % BN, c = e % 8;
-        if (key0 + r < L) continue;
-        uint4* at = reinterpret_cast<uint4*>(tile + kb * (BN * 128) + r * 128 + c * 16);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (key0 + r < k_end) {
-          v = *at;
-          v = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z),
-                         finite_bf16x2(v.w));
+    uint32_t F = 0, edges = 0;
+    for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the two warps' barriers go together)
+      const View w(pc, p);
+      for (int j = w.first_edge; j < w.n; ++j, ++edges) {
+        const uint32_t s = (F + 2 * j + 1) % NS;
+        ok = ok && warp_wait(&edge_full[edges & 3], (edges >> 2) & 1, abort_flag, p.status);
+        const int key0 = w.k_begin + j * BN;
+        uint8_t* tile = sKV + s * C::TILE;
+        for (int e = threadIdx.x - 32 * kWarpClean; ok && e < BN * (D / 8); e += 64) {
+          // (chunks of a row in any order: all are treated alike)
+          const int kb = e / (BN * 8), r = e / 8 % BN, c = e % 8;
+          if (key0 + r < w.L) continue;
+          uint4* at = reinterpret_cast<uint4*>(tile + kb * (BN * 128) + r * 128 + c * 16);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (key0 + r < w.k_end) {
+            v = *at;
+            v = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z),
+                           finite_bf16x2(v.w));
+          }
+          *at = v;
         }
-        *at = v;
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 3, 64;" ::: "memory");
+        if (ok && threadIdx.x == 32 * kWarpClean) mbar_arrive(&kv_full[s]);
       }
-      fence_proxy_async_smem();
-      asm volatile("bar.sync 3, 64;" ::: "memory");
-      if (ok && threadIdx.x == 32 * kWarpClean) mbar_arrive(&kv_full[s]);
+      F += 2 * w.n;
     }
-  } else if (F8 && warp >= kWarpConvert) {
+   }
+  } else if (warp >= kWarpConvert) {
     // ------------------------------------------------------------ e4m3 tiles to f16
-    const int tid = threadIdx.x - 32 * kWarpConvert;  // the row whose scale bytes it loads
-    constexpr int G = D / 16;                         // 16-channel pieces of a row
-    auto load_code = [&](int j) -> uint32_t {         // both bytes; 0 where there is no row
-      const int r = k_begin + j * BN + tid;
-      if (j >= n || r >= k_end) return 0u;
-      const long long at = p.rows.at(b, kvh, r);
-      if (at < 0) return 0u;
-      return p.k_scale[at] | (static_cast<uint32_t>(p.v_scale[at]) << 8);
-    };
-    uint32_t code = load_code(0);
+    if constexpr (F8) {
+    regs_dec<64>();
+    const int v = (warp - kWarpConvert) >> 2;               // 0: keys, 1: values
+    const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;  // the row whose scale it loads
+    constexpr int G = D / 16;                               // 16-channel pieces of a row
     bool ok = true;
-    for (int j = 0; j < n; ++j) {  // (to the end: the four warps' barriers go together)
-      const int key0 = k_begin + j * BN;
-      const uint32_t next = load_code(j + 1);
-      // the tile's largest codes, then every row's factor
-      const int ck = code & 0xff, cv = max(static_cast<int>(code >> 8), kMinValueCode);
-      const int mk = __reduce_max_sync(0xffffffffu, ck), mv = __reduce_max_sync(0xffffffffu, cv);
-      if (lane == 0) {
-        s_max[warp - kWarpConvert] = mk;
-        s_max[4 + warp - kWarpConvert] = mv;
-      }
-      asm volatile("bar.sync 3, 128;" ::: "memory");
-      const int Ek = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
-      const int Ev = max(max(s_max[4], s_max[5]), max(s_max[6], s_max[7]));
-      s_mul[tid] = row_scale(Ek - ck);
-      s_mul[128 + tid] = row_scale(Ev - static_cast<int>(code >> 8));
-      if (tid == 0)
-        s_tile[j & 7] = make_float2(__uint_as_float(static_cast<uint32_t>(max(Ek - 7, 1)) << 23),
-                                    static_cast<float>(Ev - 127));
-      asm volatile("bar.sync 3, 128;" ::: "memory");
-      code = next;
-      for (int v = 0; v < 2 && ok; ++v) {
-        const uint32_t f = 2 * j + v, rs = f % C::RAW_DEPTH, s = f % NS;
-        if (!warp_wait(&raw_full[rs], (f / C::RAW_DEPTH) & 1, abort_flag, p.status) ||
-            (f >= static_cast<uint32_t>(NS) &&
-             !warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status))) {
-          ok = false;
-          break;
+    uint32_t f = v, tile = 0;  // its next fill, and tile of the CTA
+    for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the four warps' barriers go together)
+      const View w(pc, p);
+      auto load_code = [&](int j) -> uint32_t {  // both bytes; 0 where there is no row
+        const int r = w.k_begin + j * BN + tid;
+        if (j >= w.n || r >= w.k_end) return 0u;
+        const long long at = p.rows.at(w.b, w.kvh, r);
+        if (at < 0) return 0u;
+        return (v == 0 ? p.k_scale[at] : 0u) | (static_cast<uint32_t>(p.v_scale[at]) << 8);
+      };
+      uint32_t code = load_code(0);
+      for (int j = 0; j < w.n; ++j, f += 2, ++tile) {
+        const int key0 = w.k_begin + j * BN;
+        const uint32_t next = load_code(j + 1);
+        // the tile's largest codes, then every row's factor
+        const int ck = code & 0xff, cv = static_cast<int>(code >> 8);
+        const int mk = __reduce_max_sync(0xffffffffu, ck);
+        const int mv = __reduce_max_sync(0xffffffffu, max(cv, kMinValueCode));
+        int* mx = s_max + 8 * v;
+        if (lane == 0) {
+          mx[warp & 3] = mk;
+          mx[4 + (warp & 3)] = mv;
         }
+        if (v == 0)
+          asm volatile("bar.sync 3, 128;" ::: "memory");
+        else
+          asm volatile("bar.sync 4, 128;" ::: "memory");
+        const int Ek = max(max(mx[0], mx[1]), max(mx[2], mx[3]));
+        const int Ev = max(max(mx[4], mx[5]), max(mx[6], mx[7]));
+        s_mul[128 * v + tid] = row_scale(v == 0 ? Ek - ck : Ev - cv);
+        if (v == 0 && tid == 0)
+          s_tile[tile & 7] =
+              make_float2(__uint_as_float(static_cast<uint32_t>(max(Ek - 7, 1)) << 23),
+                          static_cast<float>(Ev - 127));
+        if (v == 0)
+          asm volatile("bar.sync 3, 128;" ::: "memory");
+        else
+          asm volatile("bar.sync 4, 128;" ::: "memory");
+        code = next;
+        const uint32_t rs = f % C::RAW_DEPTH, s = f % NS;
+        ok = ok && warp_wait(&raw_full[rs], (f / C::RAW_DEPTH) & 1, abort_flag, p.status) &&
+             (f < static_cast<uint32_t>(NS) ||
+              warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
+        if (!ok) continue;
         const uint8_t* src = sRaw + rs * C::RAW;
         uint8_t* dst = sKV + s * C::TILE;
+        const bool edge = key0 + BN > min(w.L, w.k_end);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
           const int e = i * 128 + tid, r = e / G, c = e % G;
           uint4 x = *reinterpret_cast<const uint4*>(src + 16 * e);
           const uint32_t m1 = s_mul[128 * v + r], m = m1 | (m1 << 16);
-          if (key0 + r >= L) {  // rows past the end: zeros; drafts' values: the finite ones
-            if (key0 + r >= k_end) x = make_uint4(0u, 0u, 0u, 0u);
+          if (edge && key0 + r >= w.L) {  // rows past the end: zeros; drafts' values: if finite
+            if (key0 + r >= w.k_end) x = make_uint4(0u, 0u, 0u, 0u);
             if (v == 1) {
               x.x = finite_e4m3x4(x.x);
               x.y = finite_e4m3x4(x.y);
@@ -436,185 +483,224 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
       }
     }
-  } else if (warp < 8) {
+    }
+  } else {
     // ------------------------------------------------------------ softmax
+    if constexpr (F8) regs_inc<144>();
     const int x = warp >> 2;
     const int row = threadIdx.x & 127;  // of the query tile
     const int M = p.T * p.rep;
-    const int qrow = rb * (pair ? 256 : 128) + (pair ? x * 128 : 0) + row;
-    const bool live = qrow < M;
-    const bool warp_live = __any_sync(0xffffffffu, live);
-    const int t = live ? qrow / p.rep : 0;
-    const int h = kvh * p.rep + (live ? qrow - t * p.rep : 0);
-    const size_t qi = (static_cast<size_t>(b) * p.Hq + h) * p.T + t;
-    if (pair || x == 0) {
-      // the row's query, 16-byte chunks in the swizzled layout of a K-major operand
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + 128u * x;
+    const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(D) * x;
+    // the thread's query row of a piece: its index in [B, Hq, T], -1 for padding
+    auto query = [&](const GroupPiece& q, int* t) -> long long {
+      const int kvh = q.head / p.rblocks, rb = q.head - kvh * p.rblocks;
+      const int r = rb * (pair ? 256 : 128) + (pair ? x * 128 : 0) + row;
+      *t = r < M ? r / p.rep : 0;
+      if (r >= M) return -1;
+      return (static_cast<long long>(q.b) * p.Hq + kvh * p.rep + r - *t * p.rep) * p.T + *t;
+    };
+    // the piece's queries, 16-byte chunks in the swizzled layout of a K-major operand; the
+    // products that read the last piece's have completed
+    auto put_queries = [&](const GroupPiece& q) {
+      if (!pair && x == 1) return;
+      int t;
+      const long long qi = query(q, &t);
       uint8_t* dst = sQ + (pair ? x : 0) * C::TILE + row * 128;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + qi * D);
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (qi < 0 ? 0 : qi) * D);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (BN * 128) + (((c & 7) ^ (row & 7)) << 4)) = v;
+      for (int c0 = 0; c0 < D / 8; c0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = qi >= 0 ? src[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c0 >> 3) * (BN * 128) + ((c ^ (row & 7)) << 4)) = v[c];
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_ready[pair ? x : 0]);
-    }
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + 128u * x;
-    const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(D) * x;
-    float row_factor = p.scale_log2;
-    if (F8) row_factor *= p.q_factor[qi];
-    const uint32_t* anc = p.anc + (static_cast<size_t>(b) * p.T + t) * p.words;
+    };
 
-    float R = -INFINITY, l = 0.f;
-    uint32_t ns = 0;
+    uint32_t ns = 0, tile0 = 0, done[2] = {0, 0};  // done: pieces in which stream 0, 1 had tiles
     bool ok = true;
-    for (int j = pair ? 0 : x; j < n; j += step) {
-      if (!warp_wait(&s_full[x], ns & 1, abort_flag, p.status)) {
-        ok = false;
-        break;
-      }
-      ++ns;
-      tc_fence_after();
-      if (warp_live) {
-        float c = row_factor, ev = 0.f;
-        if constexpr (F8) {
-          const float2 ts = s_tile[j & 7];
-          c *= ts.x;
-          ev = ts.y;
+    put_queries(pc);
+    while (pc.n > 0) {  // (to the end: the warps' barriers go together)
+      const View w(pc, p);
+      int t;
+      const long long qi = query(pc, &t);
+      const bool live = qi >= 0;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      float row_factor = p.scale_log2;
+      if (F8 && live) row_factor *= p.q_factor[qi];
+      const uint32_t* anc = p.anc + (static_cast<size_t>(w.b) * p.T + t) * p.words;
+      const size_t slot = static_cast<size_t>(blockIdx.x) + pc.segment(p.line);
+
+      float R = -INFINITY, l = 0.f;
+      for (int j = pair ? 0 : x; j < w.n && ok; j += step) {
+        if (!warp_wait(&s_full[x], ns & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
         }
-        c = fmaxf(c, 1.17549435e-38f);  // (a hidden score's -inf times 0 would be NaN)
-        const int key0 = k_begin + j * BN;
-        const bool edge = j >= first_edge;
-        // the rows that this query does not see
-        uint32_t hide[4] = {0u, 0u, 0u, 0u};
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k0 = key0 + 32 * i;
-            uint32_t see = k0 + 32 <= k_end ? 0xffffffffu
-                           : k0 >= k_end    ? 0u
-                                            : (1u << (k_end - k0)) - 1u;
-            hide[i] = ~(see & draft_bits32(anc, p.words, k0 - L));
+        ++ns;
+        tc_fence_after();
+        if (warp_live) {
+          float c = row_factor, ev = 0.f;
+          if constexpr (F8) {
+            const float2 ts = s_tile[(tile0 + j) & 7];
+            c *= ts.x;
+            ev = ts.y;
           }
-        }
-        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t r[64];
-          tmem_ld64_sync(tS + 64u * i, r);
+          c = fmaxf(c, 1.17549435e-38f);  // (a hidden score's -inf times 0 would be NaN)
+          const int key0 = w.k_begin + j * BN;
+          const bool edge = j >= w.first_edge;
+          // the rows that this query does not see
+          uint32_t hide[4] = {0u, 0u, 0u, 0u};
           if (edge) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if ((hide[2 * i + (e >> 5)] >> (e & 31)) & 1u) r[e] = 0xff800000u;
+            for (int i = 0; i < 4; ++i) {
+              const int k0 = key0 + 32 * i;
+              uint32_t see = k0 + 32 <= w.k_end ? 0xffffffffu
+                             : k0 >= w.k_end    ? 0u
+                                                : (1u << (w.k_end - k0)) - 1u;
+              hide[i] = ~(see & draft_bits32(anc, p.words, k0 - w.L));
+            }
           }
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 64; e += 8)
+          for (int i = 0; i < 2; ++i) {
+            uint32_t r[64];
+            tmem_ld64_sync(tS + 64u * i, r);
+            if (edge) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mq[k] = fmax3(mq[k], __uint_as_float(r[e + k]), __uint_as_float(r[e + 4 + k]));
+              for (int e = 0; e < 64; ++e)
+                if ((hide[2 * i + (e >> 5)] >> (e & 31)) & 1u) r[e] = 0xff800000u;
+            }
+#pragma unroll
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mq[k] = fmax3(mq[k], __uint_as_float(r[e + k]), __uint_as_float(r[e + 4 + k]));
+          }
+          const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
+          const bool mine = top > R + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, mine)) {
+            const float f = mine ? ex2_approx(R - top) : 1.f;
+            l *= f;
+            if (j >= step) {
+#pragma unroll 1
+              for (int i = 0; i < D / 32; ++i) {
+                uint32_t r[32];
+                tmem_ld32_sync(tO + 32u * i, r);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                tmem_st32(tO + 32u * i, r);
+              }
+              tmem_st_wait();
+            }
+            if (mine) R = top;
+          }
+          // (nothing seen yet: 2^-inf = 0, and a NaN score stays NaN)
+          const float off = (F8 ? ev + 7.f : 0.f) - (R == -INFINITY ? 0.f : R);
+          float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t r[32], pk[16];
+            tmem_ld32_sync(tS + 32u * i, r);
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((hide[i] >> e) & 1u) r[e] = 0xff800000u;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float y0, y1;
+              // (two roundings, as in `top`: the largest gives 2^0)
+              fmul2(y0, y1, __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), c);
+              fadd2(y0, y1, y0, y1, off, off);
+              const float w0 = ex2_approx(y0), w1 = ex2_approx(y1);
+              if (e & 1)
+                fadd2(sb0, sb1, sb0, sb1, w0, w1);
+              else
+                fadd2(sa0, sa1, sa0, sa1, w0, w1);
+              pk[e] = F8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
+            }
+            tmem_st16(tS + 16u * i, pk);
+          }
+          const float sum = (sa0 + sa1) + (sb0 + sb1);
+          l += F8 ? sum * ex2_approx(-ev - 7.f) : sum;
+          tmem_st_wait();
         }
-        const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
-        const bool mine = top > R + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, mine)) {
-          const float f = mine ? ex2_approx(R - top) : 1.f;
-          l *= f;
-          if (ns > 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      tile0 += w.n;
+      // The products with this piece's queries have completed (their scores were seen); with
+      // one query tile, those of both streams.
+      if (!pair) {
+        if (x == 1) s_ml[row] = make_float2(R, l);
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+      }
+      pc.next(p.line);
+      if (ok && pc.n > 0) put_queries(pc);
+      // partial result: R, l and O, relative to 2^R
+      const bool two = !pair && w.n > 1;  // both streams had tiles of this row
+      if (pair || x == 0) {
+        ok = ok && warp_wait(&o_full[x], done[0] & 1, abort_flag, p.status) &&
+             (!two || warp_wait(&o_full[1], done[1] & 1, abort_flag, p.status));
+        if (ok) {
+          tc_fence_after();
+          if (warp_live) {
+            const float o_scale = F8 ? 1.f / 16384.f : 1.f;  // 2^-7 of w, 2^-7 of V16
+            float f0 = o_scale, f1 = 0.f;
+            if (two) {
+              const float2 other = s_ml[row];
+              const float m = fmaxf(R, other.x);
+              // (a stream that saw nothing holds zeros, or NaN)
+              const float e0 = R == -INFINITY ? 1.f : ex2_approx(R - m);
+              const float e1 = other.x == -INFINITY ? 1.f : ex2_approx(other.x - m);
+              l = l * e0 + other.y * e1;
+              R = m;
+              f0 = o_scale * e0;
+              f1 = o_scale * e1;
+            }
+            const size_t at = slot * p.part_rows + (pair ? x * 128 : 0) + row;
+            float* dst = p.part_o + at * D;
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
               uint32_t r[32];
               tmem_ld32_sync(tO + 32u * i, r);
+              float o[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tmem_st32(tO + 32u * i, r);
+              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * f0;
+              if (two) {
+                tmem_ld32_sync(tO + D + 32u * i, r);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), f1, o[e]);
+              }
+              if (live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<float4*>(dst + 32 * i + e) =
+                      make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
             }
-            tmem_st_wait();
+            if (live) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(R, l);
           }
-          if (mine) R = top;
-        }
-        // (nothing seen yet: 2^-inf = 0, and a NaN score stays NaN)
-        const float off = (F8 ? ev + 7.f : 0.f) - (R == -INFINITY ? 0.f : R);
-        float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t r[32], pk[16];
-          tmem_ld32_sync(tS + 32u * i, r);
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if ((hide[i] >> e) & 1u) r[e] = 0xff800000u;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&o_empty[x]);
+            if (two) mbar_arrive(&o_empty[1]);
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float y0, y1;
-            // (two roundings, as in `top`: the largest gives 2^0)
-            fmul2(y0, y1, __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]), c);
-            fadd2(y0, y1, y0, y1, off, off);
-            const float w0 = ex2_approx(y0), w1 = ex2_approx(y1);
-            if (e & 1)
-              fadd2(sb0, sb1, sb0, sb1, w0, w1);
-            else
-              fadd2(sa0, sa1, sa0, sa1, w0, w1);
-            pk[e] = F8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
-          }
-          tmem_st16(tS + 16u * i, pk);
-        }
-        const float sum = (sa0 + sa1) + (sb0 + sb1);
-        l += F8 ? sum * ex2_approx(-ev - 7.f) : sum;
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[x]);
-    }
-    // partial result: R, l and O, relative to 2^R
-    const float o_scale = F8 ? 1.f / 16384.f : 1.f;  // 2^-7 of w, 2^-7 of V16
-    if (!pair) {
-      if (x == 1) s_ml[row] = make_float2(R, l);
-      asm volatile("bar.sync 2, 256;" ::: "memory");  // (every softmax warp gets here)
-    }
-    if (ok && (pair || x == 0) && warp_live &&
-        warp_wait(&o_full[x], 0, abort_flag, p.status) &&
-        (pair || n < 2 || warp_wait(&o_full[1], 0, abort_flag, p.status))) {
-      tc_fence_after();
-      float f0 = o_scale, f1 = 0.f;
-      if (!pair && n > 1) {
-        const float2 other = s_ml[row];
-        const float m = fmaxf(R, other.x);
-        // (a stream that saw nothing holds zeros, or NaN)
-        const float e0 = R == -INFINITY ? 1.f : ex2_approx(R - m);
-        const float e1 = other.x == -INFINITY ? 1.f : ex2_approx(other.x - m);
-        l = l * e0 + other.y * e1;
-        R = m;
-        f0 = o_scale * e0;
-        f1 = o_scale * e1;
-      }
-      const size_t at = qi * static_cast<size_t>(p.n_splits) + split;
-      float* dst = p.part_o + at * D;
-#pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t r[32];
-        tmem_ld32_sync(tO + 32u * i, r);
-        float o[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * f0;
-        if (!pair && n > 1) {
-          tmem_ld32_sync(tO + D + 32u * i, r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), f1, o[e]);
-        }
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + 32 * i + e) =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-      if (live) {
-        p.part_ml[2 * at] = R;
-        p.part_ml[2 * at + 1] = l;
-      }
+      ++done[0];
+      done[1] += two || pair;
+      // (stream 1's next sums go to s_ml only after stream 0 has read these)
+      if (!pair) asm volatile("bar.sync 5, 256;" ::: "memory");
     }
   }
 
@@ -632,13 +718,12 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   TParams p{};
   p.q = static_cast<const uint16_t*>(a.q);
   p.q_factor = a.q_factor;
-  p.lens = a.lens;
   p.anc = a.anc;
+  p.line = group_line(a);
   p.rows = CacheRows{a.cache.block_table, a.Hkv, a.cache.Lmax, a.cache.page_size,
                      a.cache.num_pages, a.cache.max_pages};
   p.k_scale = static_cast<const uint8_t*>(a.cache.k_scale);
   p.v_scale = static_cast<const uint8_t*>(a.cache.v_scale);
-  p.drafts = a.drafts;
   p.words = a.words;
   const bool paged = a.cache.block_table != nullptr;
   const int ps = a.cache.page_size;
@@ -650,13 +735,9 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.Hkv = a.Hkv;
   p.T = a.T;
   p.rep = a.Hq / a.Hkv;
-  p.max_seq_len = a.max_seq_len;
-  p.min_len = a.min_len;
-  p.chunk = a.chunk;
-  p.n_splits = a.n_splits;
-  const int rows = a.T * p.rep;
-  p.pair = rows > 128 ? 1 : 0;
-  p.rblocks = (rows + 255) / 256;
+  p.rblocks = a.plan.rblocks;
+  p.part_rows = a.plan.part_rows;
+  p.pair = a.plan.block_rows == 256 ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
 
   alignas(64) CUtensorMap tk, tv;
@@ -671,7 +752,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   cudaError_t e = smem_limit.set(group_tc_kernel<D, F8>, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_splits) * p.rblocks, a.Hkv, a.B);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.plan.grid), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;

@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "group_work.cuh"
 
 namespace csattn {
 
@@ -196,6 +197,19 @@ cudaError_t launch_cache_read_fp8(const KvCache& cache, const int32_t* seq_lens,
                                   void* v_out, int B, int Hkv, int Lout, int d, uint32_t* status,
                                   cudaStream_t stream);
 
+// How launch_group_attn or launch_group_tc shares out its work (group_work.cuh).
+struct GroupPlan {
+  bool tc;             // launch_group_tc
+  int grid;            // CTAs
+  int most_grid;       // CTAs that the partial results have room for
+  int tiles_per_cta;   // 0: the tiles of all segments over the grid, as the device finds them
+  int unit;            // cache rows per tile
+  int block_rows;      // query rows of a block
+  int rblocks;         // blocks of a KV head's query rows
+  int subs;            // partial results per piece and query row
+  int part_rows;       // query rows of a partial result: of a block, or the KV head's if fewer
+};
+
 // Grouped attention over a cache: T queries per sequence and query head, all T * Hq / Hkv
 // query rows of a KV head against its rows at once.  Sequence b has lens[b] rows that every
 // query sees (a negative length: none, its output is zero), then `drafts` rows of which
@@ -214,17 +228,22 @@ struct GroupArgs {
   float scale;
   int max_seq_len;       // bound of lens[b] + drafts
   int min_len;           // lens[b] below it or above max_seq_len - drafts is an error (decode: 1)
-  int chunk, n_splits;   // cache rows per split (a multiple of 64), splits
-  float* part_o;         // [B, Hq, T, n_splits, d]
-  float* part_ml;        // [B, Hq, T, n_splits, 2]
+  GroupPlan plan;
+  long long* prefix;     // [B + 1] scratch
+  float* part_o;         // [pieces, subs, part_rows, d], pieces = grid + segments
+  float* part_ml;        // [pieces, subs, part_rows, 2]
   bool after_prep;       // launched behind launch_tree_prep (programmatic dependent launch)
   uint32_t* status;
 };
+inline GroupLine group_line(const GroupArgs& a) {
+  return GroupLine{a.lens,     a.prefix, a.B,         a.drafts, a.min_len, a.max_seq_len - a.drafts,
+                   a.plan.unit, a.Hkv * a.plan.rblocks, a.plan.tiles_per_cta};
+}
 cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
-// The same on tcgen05, for many query rows; a.chunk is a multiple of 128, rope is 0.
+// The same on tcgen05, for many query rows; rope is 0.
 cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream);
 
-// Merge of the splits of launch_group_attn into out [B, Hq, T, d] bf16 and, if non-null, lse
+// Merge of the partial results into out [B, Hq, T, d] bf16 and, if non-null, lse
 // [B, Hq, T].  vflag (with v_new; may be null): bytes [B, Hkv, T], set where v_new[b, g, t]
 // holds an infinity or NaN; such values left the products (launch_group_attn reads them as
 // zeros) and are put into the outputs of the queries that see them here.
