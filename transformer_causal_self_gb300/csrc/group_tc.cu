@@ -41,12 +41,11 @@ constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 1
 
 template <int D, bool F8>
 struct Cfg {
-  // e4m3: registers move from the other warpgroups to the softmax (2*144 + 64 + 2*64 = 5*96)
+  // e4m3: registers move from the other warpgroups to the softmax (2*136 + 64 + 2*72 = 5*96)
   static constexpr int kThreads = F8 ? 640 : 384;
   static constexpr int TILE = BN * D * 2;  // a Q, K or V tile of 16-bit values
   static constexpr int RAW = BN * D;       // an e4m3 tile
   static constexpr int NRAW = F8 ? 4 : 0;
-  static constexpr int RAW_DEPTH = F8 ? 4 : 1;
   // ring tiles that fit beside one or two query tiles
   static constexpr int NS1 = F8 ? 4 : (D == 128 ? 6 : 8);
   static constexpr int NS2 = F8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
@@ -122,6 +121,44 @@ __device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, 
       "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b));
+}
+
+// A TMEM load of 32 columns in two halves: issue, and the wait after which the registers hold
+// the columns (named in the wait, so that no use can be scheduled before it).
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// -inf into the scores of 32 columns whose bit in `hide` is set
+__device__ __forceinline__ void mask_scores(uint32_t taddr, uint32_t hide) {
+  uint32_t r[32];
+  tmem_ld32_sync(taddr, r);
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if ((hide >> e) & 1u) r[e] = 0xff800000u;
+  tmem_st32(taddr, r);
 }
 
 // zero the halves of a word of bf16 that hold an infinity or NaN
@@ -394,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   } else if (warp >= kWarpConvert) {
     // ------------------------------------------------------------ e4m3 tiles to f16
     if constexpr (F8) {
-    regs_dec<64>();
+    regs_dec<72>();
     const int v = (warp - kWarpConvert) >> 2;               // 0: keys, 1: values
     const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;  // the row whose scale it loads
     constexpr int G = D / 16;                               // 16-channel pieces of a row
@@ -438,15 +475,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         else
           asm volatile("bar.sync 4, 128;" ::: "memory");
         code = next;
-        const uint32_t rs = f % C::RAW_DEPTH, s = f % NS;
-        ok = ok && warp_wait(&raw_full[rs], (f / C::RAW_DEPTH) & 1, abort_flag, p.status) &&
+        const uint32_t rs = f % C::NRAW, s = f % NS;
+        ok = ok && warp_wait(&raw_full[rs], (f / C::NRAW) & 1, abort_flag, p.status) &&
              (f < static_cast<uint32_t>(NS) ||
               warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
         if (!ok) continue;
         const uint8_t* src = sRaw + rs * C::RAW;
         uint8_t* dst = sKV + s * C::TILE;
         const bool edge = key0 + BN > min(w.L, w.k_end);
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < G; ++i) {
           const int e = i * 128 + tid, r = e / G, c = e % G;
           uint4 x = *reinterpret_cast<const uint4*>(src + 16 * e);
@@ -486,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    if constexpr (F8) regs_inc<144>();
+    if constexpr (F8) regs_inc<136>();
     const int x = warp >> 2;
     const int row = threadIdx.x & 127;  // of the query tile
     const int M = p.T * p.rep;
@@ -553,42 +590,48 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             ev = ts.y;
           }
           c = fmaxf(c, 1.17549435e-38f);  // (a hidden score's -inf times 0 would be NaN)
-          const int key0 = w.k_begin + j * BN;
-          const bool edge = j >= w.first_edge;
-          // the rows that this query does not see
-          uint32_t hide[4] = {0u, 0u, 0u, 0u};
-          if (edge) {
-#pragma unroll
+          if (j >= w.first_edge) {  // rows that this query does not see
+            const int key0 = w.k_begin + j * BN;
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               const int k0 = key0 + 32 * i;
-              uint32_t see = k0 + 32 <= w.k_end ? 0xffffffffu
-                             : k0 >= w.k_end    ? 0u
-                                                : (1u << (w.k_end - k0)) - 1u;
-              hide[i] = ~(see & draft_bits32(anc, p.words, k0 - w.L));
+              const uint32_t in = k0 + 32 <= w.k_end ? 0xffffffffu
+                                  : k0 >= w.k_end    ? 0u
+                                                     : (1u << (w.k_end - k0)) - 1u;
+              mask_scores(tS + 32u * i, ~(in & draft_bits32(anc, p.words, k0 - w.L)));
             }
+            tmem_st_wait();
           }
+          // (the next columns' load runs beside the arithmetic on these)
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t ra[32], rb[32];
+          auto max32 = [&](const uint32_t (&r)[32]) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t r[64];
-            tmem_ld64_sync(tS + 64u * i, r);
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if ((hide[2 * i + (e >> 5)] >> (e & 31)) & 1u) r[e] = 0xff800000u;
-            }
-#pragma unroll
-            for (int e = 0; e < 64; e += 8)
+            for (int e = 0; e < 32; e += 8)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mq[k] = fmax3(mq[k], __uint_as_float(r[e + k]), __uint_as_float(r[e + 4 + k]));
-          }
+          };
+          tmem_ld32_issue(tS, ra);
+          tmem_ld32_wait(ra);
+          tmem_ld32_issue(tS + 32u, rb);
+          max32(ra);
+          tmem_ld32_wait(rb);
+          tmem_ld32_issue(tS + 64u, ra);
+          max32(rb);
+          tmem_ld32_wait(ra);
+          tmem_ld32_issue(tS + 96u, rb);
+          max32(ra);
+          tmem_ld32_wait(rb);
+          tmem_ld32_issue(tS, ra);
+          max32(rb);
           const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
           const bool mine = top > R + kRescaleThreshold;
           if (__any_sync(0xffffffffu, mine)) {
             const float f = mine ? ex2_approx(R - top) : 1.f;
             l *= f;
             if (j >= step) {
+              tmem_ld32_wait(ra);  // (ra is read after the wait that follows, too)
 #pragma unroll 1
               for (int i = 0; i < D / 32; ++i) {
                 uint32_t r[32];
@@ -604,15 +647,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           // (nothing seen yet: 2^-inf = 0, and a NaN score stays NaN)
           const float off = (F8 ? ev + 7.f : 0.f) - (R == -INFINITY ? 0.f : R);
           float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t r[32], pk[16];
-            tmem_ld32_sync(tS + 32u * i, r);
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if ((hide[i] >> e) & 1u) r[e] = 0xff800000u;
-            }
+          auto weights32 = [&](const uint32_t (&r)[32], uint32_t at) {
+            uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float y0, y1;
@@ -626,8 +662,19 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 fadd2(sa0, sa1, sa0, sa1, w0, w1);
               pk[e] = F8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
             }
-            tmem_st16(tS + 16u * i, pk);
-          }
+            tmem_st16(at, pk);
+          };
+          tmem_ld32_wait(ra);
+          tmem_ld32_issue(tS + 32u, rb);
+          weights32(ra, tS);
+          tmem_ld32_wait(rb);
+          tmem_ld32_issue(tS + 64u, ra);
+          weights32(rb, tS + 16u);
+          tmem_ld32_wait(ra);
+          tmem_ld32_issue(tS + 96u, rb);
+          weights32(ra, tS + 32u);
+          tmem_ld32_wait(rb);
+          weights32(rb, tS + 48u);
           const float sum = (sa0 + sa1) + (sb0 + sb1);
           l += F8 ? sum * ex2_approx(-ev - 7.f) : sum;
           tmem_st_wait();
