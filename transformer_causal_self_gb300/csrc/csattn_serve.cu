@@ -136,8 +136,17 @@ size_t partial_floats(const GroupPlan& p, int B, int Hkv) {
 size_t partial_bytes(const GroupPlan& p, int B, int Hkv, int d) {
   return partial_floats(p, B, Hkv) * (static_cast<size_t>(d) + 2) * 4;
 }
-// The tiles' sums per sequence (GroupLine::prefix) follow the partials.
-size_t prefix_bytes(int B) { return align256((static_cast<size_t>(B) + 1) * 8); }
+// What the kernel leaves the merge of each segment (GroupLine::seg) follows the partials.
+size_t seg_bytes(const GroupPlan& p, int B, int Hkv) {
+  return align256(static_cast<size_t>(B) * Hkv * p.rblocks * 8);
+}
+
+// (GroupLine counts tiles in 31 bits)
+int check_line(const char* fn, const GroupPlan& p, int B, int Hkv, int max_seq_len) {
+  if (static_cast<long long>(B) * Hkv * p.rblocks > ((1LL << 31) - 1) / (max_seq_len / p.unit + 1))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: B * Hkv * max_seq_len too large", fn);
+  return CSATTN_OK;
+}
 
 bool sizes_ok(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
   return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Lmax >= 1 && d >= 1 && num_splits >= 0;
@@ -218,9 +227,10 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
   a.plan = plan_for(B, Hkv, Hq / Hkv, false, true, max_seq_len, num_splits);
+  if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
   const size_t partials = partial_bytes(a.plan, B, Hkv, d);
   if ((rc = check_workspace(fn, workspace, workspace_bytes,
-                            align256(partials) + prefix_bytes(B))) != CSATTN_OK)
+                            align256(partials) + seg_bytes(a.plan, B, Hkv))) != CSATTN_OK)
     return rc;
   a.cache = c;
   a.q = q;
@@ -236,7 +246,7 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
   a.min_len = 1;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + partial_floats(a.plan, B, Hkv) * d;
-  a.prefix = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + align256(partials));
+  a.seg = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + align256(partials));
   int sms = 0;
   if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
   if ((rc = encoder_ready(fn)) != CSATTN_OK) return rc;
@@ -249,11 +259,11 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
 
 // Workspace of a tree step: partials, then rotated queries, masks, lengths and value flags.
 struct TreeSpace {
-  size_t prefix, q_rot, q_factor, anc, lens, vflag, total;
-  TreeSpace(size_t partials, int B, int Hq, int Hkv, int Tn, int d) {
+  size_t seg, q_rot, q_factor, anc, lens, vflag, total;
+  TreeSpace(const GroupPlan& p, int B, int Hq, int Hkv, int Tn, int d) {
     const size_t words = (Tn + 31) / 32;
-    prefix = align256(partials);
-    q_rot = prefix + prefix_bytes(B);
+    seg = align256(partial_bytes(p, B, Hkv, d));
+    q_rot = seg + seg_bytes(p, B, Hkv);
     q_factor = q_rot + align256(static_cast<size_t>(B) * Hq * Tn * d * 2);
     anc = q_factor + align256(static_cast<size_t>(B) * Hq * Tn * 4);
     lens = anc + align256(static_cast<size_t>(B) * Tn * words * 4);
@@ -291,7 +301,8 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
   a.plan = tree_plan(B, Hq, Hkv, Tn, cache_dtype == CSATTN_E4M3, max_seq_len, num_splits);
-  const TreeSpace at(partial_bytes(a.plan, B, Hkv, d), B, Hq, Hkv, Tn, d);
+  if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
+  const TreeSpace at(a.plan, B, Hq, Hkv, Tn, d);
   if ((rc = check_workspace(fn, workspace, workspace_bytes, at.total)) != CSATTN_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
@@ -336,7 +347,7 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   a.min_len = 0;
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = a.part_o + partial_floats(a.plan, B, Hkv) * d;
-  a.prefix = reinterpret_cast<long long*>(ws + at.prefix);
+  a.seg = reinterpret_cast<int2*>(ws + at.seg);
   a.after_prep = true;
   a.status = p.status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -456,9 +467,8 @@ int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const 
 
 size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
   if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits)) return 0;
-  return align256(partial_bytes(plan_for(B, Hkv, Hq / Hkv, false, true, Lmax, num_splits), B, Hkv,
-                                d)) +
-         prefix_bytes(B);
+  const GroupPlan p = plan_for(B, Hkv, Hq / Hkv, false, true, Lmax, num_splits);
+  return align256(partial_bytes(p, B, Hkv, d)) + seg_bytes(p, B, Hkv);
 }
 
 int csattn_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
@@ -495,7 +505,7 @@ size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int 
   if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits) || Tn < 1 || Tn > kMaxTree) return 0;
   // (an 8-bit cache's plan takes no less room)
   const GroupPlan p = tree_plan(B, Hq, Hkv, Tn, true, Lmax, num_splits);
-  return TreeSpace(partial_bytes(p, B, Hkv, d), B, Hq, Hkv, Tn, d).total;
+  return TreeSpace(p, B, Hq, Hkv, Tn, d).total;
 }
 
 int csattn_attn_tree_step(const void* q_new, const void* k_new, const void* v_new, void* k_cache,

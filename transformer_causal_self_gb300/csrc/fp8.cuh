@@ -145,7 +145,14 @@ struct CacheRows {
   // index (in rows) of row r of KV head g of sequence b, or -1 for a page outside the pool
   __device__ __forceinline__ long long at(int b, int g, int r) const {
     if (block_table == nullptr) return (static_cast<long long>(b) * Hkv + g) * Lmax + r;
-    const int page = block_table[static_cast<size_t>(b) * max_pages + r / page_size];
+    return in_page(b, g, r, page(b, r));
+  }
+  // the same in two steps: the page (of a paged cache), and the row in it
+  __device__ __forceinline__ int page(int b, int r) const {
+    return block_table[static_cast<size_t>(b) * max_pages + r / page_size];
+  }
+  __device__ __forceinline__ long long in_page(int b, int g, int r, int page) const {
+    if (block_table == nullptr) return (static_cast<long long>(b) * Hkv + g) * Lmax + r;
     if (page < 0 || page >= num_pages) return -1;
     return (static_cast<long long>(page) * Hkv + g) * page_size + r % page_size;
   }

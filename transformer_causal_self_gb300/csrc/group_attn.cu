@@ -56,7 +56,7 @@ struct Cfg {
   static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? (NT == 1 ? 3 : 4) : 6);
   static constexpr int RING = NS * STAGE;
   static constexpr int Q_BYTES = ROWS * QS;         // twice: the next piece's go to the other
-  static constexpr int SMEM = 1024 + RING + 2 * Q_BYTES + 128 + 2 * ROWS * 4 + kLineSmem;
+  static constexpr int SMEM = 1024 + RING + 2 * Q_BYTES + 128 + 2 * ROWS * 4;
 };
 
 struct GParams {
@@ -159,7 +159,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   uint64_t* empty = full + NS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
   float* s_qf = reinterpret_cast<float*>(smem + C::RING + 2 * C::Q_BYTES + 128);  // [2][ROWS]
-  uint8_t* s_line = reinterpret_cast<uint8_t*>(s_qf + 2 * C::ROWS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // what launch_tree_prep wrote is visible from here on
@@ -175,8 +174,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
     fence_mbar_init();
   }
   // (launch_tree_prep has reported what it marks with -1)
-  GroupPiece pc = group_start(p.line, s_line, p.status, p.line.drafts > 0 ? -1 : INT_MIN);
+  GroupPiece pc = group_start(p.line, p.status, p.line.drafts > 0 ? -1 : INT_MIN);
   if (pc.n == 0) return;
+  __syncthreads();
 
   if (warp == NW) {
     // ------------------------------------------------------------ producer
@@ -260,16 +260,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   const int k_end = min(total, k_begin + ntiles * KT);
 
   // scale bytes of the warp's 16 rows of a tile: lanes 0..15 the keys', 16..31 the values';
-  // rows past the sequence and pages outside the pool read 0 (their data is zero or masked)
-  auto load_codes = [&](int t) -> uint32_t {
-    if constexpr (!F8) return 0u;
-    const int r = k_begin + t * KT + 16 * warp + (lane & 15);
-    if (t >= ntiles || r >= total) return 0u;
-    const long long at = p.rows.at(b, kvh, r);
+  // rows past the sequence and pages outside the pool read 0 (their data is zero or masked).
+  // Two loads that depend on one another, so each is issued a tile or two ahead of its use.
+  const int code_row = k_begin + 16 * warp + (lane & 15);
+  auto load_page = [&](int t) -> int {
+    const int r = code_row + t * KT;
+    if (!F8 || p.rows.block_table == nullptr || t >= ntiles || r >= total) return 0;
+    return p.rows.page(b, r);
+  };
+  auto load_code = [&](int t, int page) -> uint32_t {
+    const int r = code_row + t * KT;
+    if (!F8 || t >= ntiles || r >= total) return 0u;
+    const long long at = p.rows.in_page(b, kvh, r, page);
     if (at < 0) return 0u;
     return (lane < 16 ? p.k_scale : p.v_scale)[at];
   };
-  uint32_t codes = load_codes(0), codes1 = load_codes(1);
+  const int page0 = load_page(0), page1 = load_page(1);
+  int page2 = load_page(2);
+  uint32_t codes = load_code(0, page0), codes1 = load_code(1, page1);
 
   // queries into shared memory: D/16 lanes per row, 16 channels each
   {
@@ -344,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   bool unset = true;  // some query row has no maximum yet
   for (int t = 0; t < ntiles && ok; ++t, ++used) {
     const int s = used % NS;
-    const uint32_t codes2 = load_codes(t + 2);
+    const uint32_t codes2 = load_code(t + 2, page2);
+    page2 = load_page(t + 3);
     if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (used / NS) & 1, abort_flag, p.status,
                                            kWaitNs))) {
       ok = false;
@@ -552,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 16);
     }
   if (!ok) continue;  // (to the end: the warps' barriers go together)
+  if (threadIdx.x == 0) pc.leave_for_merge(p.line);
   // the warp's partial result, relative to the maximum of x
   const size_t slot =
       (static_cast<size_t>(blockIdx.x) + pc.segment(p.line)) * NW + warp;
@@ -587,12 +597,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
 // many partials), four (d = 128) or two channels per lane.
 template <int D, int W>
 __global__ void __launch_bounds__(128) group_merge_kernel(
-    const float* __restrict__ part_o, const float* __restrict__ part_ml, const GroupLine line,
-    int grid, int subs, int part_rows, int block_rows, int rblocks,
-    const uint32_t* __restrict__ anc, const uint8_t* __restrict__ vflag,
-    const __nv_bfloat16* __restrict__ v_new, bool f8, __nv_bfloat16* __restrict__ out,
-    float* __restrict__ lse, int rows, int Hq, int Hkv, int T, int words) {
+    const float* __restrict__ part_o, const float* __restrict__ part_ml, const int2* seg, int heads,
+    int subs, int part_rows, int block_rows, int rblocks, const uint32_t* __restrict__ anc,
+    const uint8_t* __restrict__ vflag, const __nv_bfloat16* __restrict__ v_new, bool f8,
+    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int rows, int Hq, int Hkv, int T,
+    int words) {
   constexpr int V = D / 32;
+  constexpr int U = 4;  // partial results whose loads are in flight together
   __shared__ float s_part[W > 1 ? 4 : 1][V * 32 + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = static_cast<int>(blockIdx.x) * (4 / W) + warp / W;
@@ -601,60 +612,75 @@ __global__ void __launch_bounds__(128) group_merge_kernel(
   const int rep = Hq / Hkv;
   const int t = row % T, bh = row / T, b = bh / Hq, h = bh - b * Hq, g = h / rep;
   const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
-  const int tiles = line.tiles(line.lens[b]);
-  // the segment's place on the line, and from it its pieces
   const int qrow = t * rep + h - g * rep, rb = qrow / block_rows;
-  const int head = g * rblocks + rb, seg = b * line.heads + head;
-  const long long all = line.prefix[line.B] * line.heads;
-  const long long per = line.tiles_per_cta > 0 ? line.tiles_per_cta : (all + grid - 1) / grid;
-  const long long s0 = line.prefix[b] * line.heads + static_cast<long long>(head) * tiles;
-  int ns = 0;
-  long long first = 0;
-  if (tiles > 0 && (line.drafts == 0 || ((mine[t >> 5] >> (t & 31)) & 1u) != 0u)) {
-    first = s0 / per;
-    ns = static_cast<int>((s0 + tiles - 1) / per - first + 1) * subs;
-  }
-  // partial i of the row is row qrow - rb * block_rows of slot (first + seg) * subs + i
-  const size_t at0 = static_cast<size_t>(first + seg) * subs * part_rows + qrow - rb * block_rows;
-  float m = -INFINITY;
-  for (int s = lane; s < ns; s += 32)
-    m = fmaxf(m, part_ml[2 * (at0 + static_cast<size_t>(s) * part_rows)]);
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-  float acc[V], l = 0.f;
+  const int2 at_seg = seg[b * heads + g * rblocks + rb];
+  int ns = at_seg.y * subs;
+  if (words > 0 && ((mine[t >> 5] >> (t & 31)) & 1u) == 0u) ns = 0;  // padding
+  // partial i of the row is row qrow - rb * block_rows of slot at_seg.x * subs + i
+  const size_t at0 =
+      static_cast<size_t>(at_seg.x) * subs * part_rows + qrow - rb * block_rows;
+  float m = -INFINITY, acc[V], l = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int s = warp % W; s < ns; s += W) {
-    const size_t at = at0 + static_cast<size_t>(s) * part_rows;
-    const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * at);
-    const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);  // (one that saw nothing: 0)
-    l += f * ml.y;
-    const float* po = part_o + at * D + V * lane;
-    if constexpr (V == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(po);
-      acc[0] += f * x.x;
-      acc[1] += f * x.y;
-      acc[2] += f * x.z;
-      acc[3] += f * x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(po);
-      acc[0] += f * x.x;
-      acc[1] += f * x.y;
+  for (int s0 = warp % W; s0 < ns; s0 += U * W) {
+    float2 ml[U];
+    float o[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u * W;
+      ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[u][i] = 0.f;
+      if (s >= ns) continue;
+      const size_t at = at0 + static_cast<size_t>(s) * part_rows;
+      ml[u] = *reinterpret_cast<const float2*>(part_ml + 2 * at);
+      const float* po = part_o + at * D + V * lane;
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(o[u]) = *reinterpret_cast<const float4*>(po);
+      else
+        *reinterpret_cast<float2*>(o[u]) = *reinterpret_cast<const float2*>(po);
+    }
+    float mx = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
+    // (one that saw nothing holds zeros, or NaN)
+    const float f = m == -INFINITY ? 1.f : ex2_approx(m - mx);
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= f;
+    m = mx;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float e = ml[u].x == -INFINITY ? 1.f : ex2_approx(ml[u].x - m);
+      l += e * ml[u].y;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += e * o[u][i];
     }
   }
   if constexpr (W > 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i) s_part[warp][V * lane + i] = acc[i];
-    if (lane == 0) s_part[warp][V * 32] = l;
+    if (lane == 0) {
+      s_part[warp][V * 32] = l;
+      s_part[warp][V * 32 + 1] = m;
+    }
     __syncthreads();
     if (warp != 0) return;
+    float mx = m;
 #pragma unroll
-    for (int w = 1; w < W; ++w) {
-      l += s_part[w][V * 32];
+    for (int w = 1; w < W; ++w) mx = fmaxf(mx, s_part[w][V * 32 + 1]);
+    l = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += s_part[w][V * lane + i];
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float mw = s_part[w][V * 32 + 1];
+      const float e = mw == -INFINITY ? 1.f : ex2_approx(mw - mx);
+      l += e * s_part[w][V * 32];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += e * s_part[w][V * lane + i];
     }
+    m = mx;
   }
   const bool any = !(l <= 0.f);  // NaN stays
   const float inv = any ? 1.f / l : 0.f;
@@ -757,7 +783,7 @@ cudaError_t launch_merge(const GroupArgs& a, const uint8_t* vflag, const void* v
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(
       &cfg, group_merge_kernel<D, W>, static_cast<const float*>(a.part_o),
-      static_cast<const float*>(a.part_ml), group_line(a), a.plan.grid, a.plan.subs,
+      static_cast<const float*>(a.part_ml), a.seg, a.Hkv * a.plan.rblocks, a.plan.subs,
       a.plan.part_rows, a.plan.block_rows, a.plan.rblocks, a.anc, vflag,
       static_cast<const __nv_bfloat16*>(v_new), a.cache.k_scale != nullptr,
       static_cast<__nv_bfloat16*>(out), lse, rows, a.Hq, a.Hkv, a.T, a.words);

@@ -236,8 +236,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  static_assert(kLineSmem <= 128 * 8, "the line's sums share s_ml");
-  GroupPiece pc = group_start(p.line, reinterpret_cast<uint8_t*>(s_ml), p.status, -1);
+  GroupPiece pc = group_start(p.line, p.status, -1);
   if (pc.n == 0) return;
   const int step = pair ? 1 : 2;  // between a stream's tiles
   if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
@@ -439,17 +438,26 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     uint32_t f = v, tile = 0;  // its next fill, and tile of the CTA
     for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the four warps' barriers go together)
       const View w(pc, p);
-      auto load_code = [&](int j) -> uint32_t {  // both bytes; 0 where there is no row
-        const int r = w.k_begin + j * BN + tid;
+      // the row's scale bytes, both; 0 where there is no row.  The page comes first, so each of
+      // the two loads is issued a tile ahead of its use.
+      const int code_row = w.k_begin + tid;
+      auto load_page = [&](int j) -> int {
+        const int r = code_row + j * BN;
+        return p.rows.block_table == nullptr || j >= w.n || r >= w.k_end ? 0 : p.rows.page(w.b, r);
+      };
+      auto load_code = [&](int j, int page) -> uint32_t {
+        const int r = code_row + j * BN;
         if (j >= w.n || r >= w.k_end) return 0u;
-        const long long at = p.rows.at(w.b, w.kvh, r);
+        const long long at = p.rows.in_page(w.b, w.kvh, r, page);
         if (at < 0) return 0u;
         return (v == 0 ? p.k_scale[at] : 0u) | (static_cast<uint32_t>(p.v_scale[at]) << 8);
       };
-      uint32_t code = load_code(0);
+      uint32_t code = load_code(0, load_page(0));
+      int page = load_page(1);
       for (int j = 0; j < w.n; ++j, f += 2, ++tile) {
         const int key0 = w.k_begin + j * BN;
-        const uint32_t next = load_code(j + 1);
+        const uint32_t next = load_code(j + 1, page);
+        page = load_page(j + 2);
         // the tile's largest codes, then every row's factor
         const int ck = code & 0xff, cv = static_cast<int>(code >> 8);
         const int mk = __reduce_max_sync(0xffffffffu, ck);
@@ -483,34 +491,47 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         const uint8_t* src = sRaw + rs * C::RAW;
         uint8_t* dst = sKV + s * C::TILE;
         const bool edge = key0 + BN > min(w.L, w.k_end);
-#pragma unroll 4
-        for (int i = 0; i < G; ++i) {
-          const int e = i * 128 + tid, r = e / G, c = e % G;
-          uint4 x = *reinterpret_cast<const uint4*>(src + 16 * e);
-          const uint32_t m1 = s_mul[128 * v + r], m = m1 | (m1 << 16);
-          if (edge && key0 + r >= w.L) {  // rows past the end: zeros; drafts' values: if finite
-            if (key0 + r >= w.k_end) x = make_uint4(0u, 0u, 0u, 0u);
-            if (v == 1) {
-              x.x = finite_e4m3x4(x.x);
-              x.y = finite_e4m3x4(x.y);
-              x.z = finite_e4m3x4(x.z);
-              x.w = finite_e4m3x4(x.w);
+        // piece i of the thread is row i * (128 / G) + tid / G, chunks 2c and 2c + 1 of it
+        // after; rows' second halves store those the other way round, so that eight lanes write
+        // eight different banks
+        const int r0 = tid / G, c = tid % G, c0 = 2 * (c & 3), flip = (c >> 2) & 1;
+        uint8_t* const at0 = dst + (c >> 2) * (BN * 128) + r0 * 128;
+        const uint32_t off0 = ((c0 + flip) ^ (r0 & 7)) << 4, off1 = ((c0 + 1 - flip) ^ (r0 & 7)) << 4;
+        constexpr int kRowStep = 128 / G;  // (a multiple of 8: the swizzle stays)
+#pragma unroll 1
+        for (int i0 = 0; i0 < G; i0 += 4) {
+          uint4 x[4];
+          uint32_t m[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const uint4*>(src + 16 * ((i0 + i) * 128 + tid));
+            m[i] = s_mul[128 * v + (i0 + i) * kRowStep + r0];
+          }
+          if (edge) {  // rows past the end: zeros; the drafts' values: if finite
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = key0 + (i0 + i) * kRowStep + r0;
+              if (r >= w.k_end) x[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (v == 1 && r >= w.L)
+                x[i] = make_uint4(finite_e4m3x4(x[i].x), finite_e4m3x4(x[i].y),
+                                  finite_e4m3x4(x[i].z), finite_e4m3x4(x[i].w));
             }
           }
-          const uint4 lo = make_uint4(hmul2(e4m3x2_to_f16x2(x.x), m),
-                                      hmul2(e4m3x2_hi_to_f16x2(x.x), m),
-                                      hmul2(e4m3x2_to_f16x2(x.y), m),
-                                      hmul2(e4m3x2_hi_to_f16x2(x.y), m));
-          const uint4 hi = make_uint4(hmul2(e4m3x2_to_f16x2(x.z), m),
-                                      hmul2(e4m3x2_hi_to_f16x2(x.z), m),
-                                      hmul2(e4m3x2_to_f16x2(x.w), m),
-                                      hmul2(e4m3x2_hi_to_f16x2(x.w), m));
-          // chunks 2c and 2c + 1 of the row; rows' second halves store them the other way
-          // round, so that eight lanes write eight different banks
-          uint8_t* at = dst + (c >> 2) * (BN * 128) + r * 128;
-          const int c0 = 2 * (c & 3), flip = (c >> 2) & 1;
-          *reinterpret_cast<uint4*>(at + (((c0 + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
-          *reinterpret_cast<uint4*>(at + (((c0 + 1 - flip) ^ (r & 7)) << 4)) = flip ? lo : hi;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t mm = m[i] | (m[i] << 16);
+            const uint4 lo = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].x), mm),
+                                        hmul2(e4m3x2_hi_to_f16x2(x[i].x), mm),
+                                        hmul2(e4m3x2_to_f16x2(x[i].y), mm),
+                                        hmul2(e4m3x2_hi_to_f16x2(x[i].y), mm));
+            const uint4 hi = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].z), mm),
+                                        hmul2(e4m3x2_hi_to_f16x2(x[i].z), mm),
+                                        hmul2(e4m3x2_to_f16x2(x[i].w), mm),
+                                        hmul2(e4m3x2_hi_to_f16x2(x[i].w), mm));
+            uint8_t* at = at0 + (i0 + i) * (kRowStep * 128);
+            *reinterpret_cast<uint4*>(at + off0) = flip ? hi : lo;
+            *reinterpret_cast<uint4*>(at + off1) = flip ? lo : hi;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -573,6 +594,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       if (F8 && live) row_factor *= p.q_factor[qi];
       const uint32_t* anc = p.anc + (static_cast<size_t>(w.b) * p.T + t) * p.words;
       const size_t slot = static_cast<size_t>(blockIdx.x) + pc.segment(p.line);
+      if (threadIdx.x == 0) pc.leave_for_merge(p.line);
 
       float R = -INFINITY, l = 0.f;
       for (int j = pair ? 0 : x; j < w.n && ok; j += step) {

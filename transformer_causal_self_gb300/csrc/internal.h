@@ -229,14 +229,14 @@ struct GroupArgs {
   int max_seq_len;       // bound of lens[b] + drafts
   int min_len;           // lens[b] below it or above max_seq_len - drafts is an error (decode: 1)
   GroupPlan plan;
-  long long* prefix;     // [B + 1] scratch
+  int2* seg;             // [B * Hkv * rblocks] scratch
   float* part_o;         // [pieces, subs, part_rows, d], pieces = grid + segments
   float* part_ml;        // [pieces, subs, part_rows, 2]
   bool after_prep;       // launched behind launch_tree_prep (programmatic dependent launch)
   uint32_t* status;
 };
 inline GroupLine group_line(const GroupArgs& a) {
-  return GroupLine{a.lens,     a.prefix, a.B,         a.drafts, a.min_len, a.max_seq_len - a.drafts,
+  return GroupLine{a.lens,     a.seg, a.B,         a.drafts, a.min_len, a.max_seq_len - a.drafts,
                    a.plan.unit, a.Hkv * a.plan.rblocks, a.plan.tiles_per_cta};
 }
 cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
