@@ -628,117 +628,119 @@ def cache_append_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.
 
 # ------------------------------------------------- 8-bit cache and token trees
 # These calls check shapes, types and devices of every tensor, run on the tensors' device
-# (whichever is current) and, when they allocate an output or a workspace for a `stream` other
-# than the current one, tie it to that stream.
-
-def _tensor(name: str, t: torch.Tensor, shape, dtypes, device) -> int:
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
-
+# (whichever is current) and, when they allocate an output or a workspace for a `stream` of the
+# caller's, tie it to that stream.  (Written with few Python calls: a step over a short cache
+# takes the GPU less time than this file.)
 
 _BF16, _I32, _F32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
 _E4M3 = (torch.float8_e4m3fn,)
 _SCALE = (torch.uint8, torch.float8_e8m0fnu)
 
 
-def _cuda_device(name: str, t: torch.Tensor, ndim: int) -> torch.device:
+def _ptr(name: str, t: torch.Tensor, shape, dtypes, dev: int) -> int:
+    """Address of a tensor that has to be contiguous, on device `dev`, of that shape and type."""
+    if (t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
+        raise ValueError(f"{name}: must be on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _device_of(name: str, t: torch.Tensor, ndim: int) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name}: must be on a CUDA device")
     if t.dim() != ndim:
         raise ValueError(f"{name}: {t.dim()} dimensions, expected {ndim}")
-    return t.device
+    return dev
 
 
-class _Launch:
-    """The stream of a call and the tensors it allocates, on `device`."""
-
-    __slots__ = ("device", "stream", "handle", "foreign")
-
-    def __init__(self, device: torch.device, stream):
-        self.device = device
-        current = torch.cuda.current_stream(device)
-        self.stream = current if stream is None else stream
-        self.handle = _stream_handle(self.stream)
-        self.foreign = self.handle != current.cuda_stream
-
-    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.foreign:  # not handed out again before that stream's work is done
-            st = self.stream
-            t.record_stream(st if isinstance(st, torch.cuda.Stream)
-                            else torch.cuda.ExternalStream(self.handle, device=self.device))
-        return t
-
-    def workspace(self, given: Optional[torch.Tensor], need: int):
-        if given is None:
-            given = self.empty((max(need, 16),), torch.uint8)
-        elif given.device != self.device or not given.is_contiguous():
-            raise ValueError(f"workspace: must be contiguous on {self.device}")
-        return given, given.data_ptr(), given.numel() * given.element_size()
-
-    def run(self, fn, *args) -> None:
-        if self.device.index == torch.cuda.current_device():
-            _check(fn(*args, self.handle))
-        else:
-            with torch.cuda.device(self.device):
-                _check(fn(*args, self.handle))
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _cache_ptrs(k, v, k_scale, v_scale, dev, dtypes):
-    """Pointers of a cache (4-D, [.., Hkv, rows, d]) and its scales; all of one shape."""
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """An output or workspace of a call on `stream` (None: the current one)."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:  # not handed out again before that stream's work is done
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                        torch.cuda.ExternalStream(_stream_handle(stream), device=dev))
+    return t
+
+
+def _workspace(given: torch.Tensor, dev: int):
+    if given.get_device() != dev or not given.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous on cuda:{dev}")
+    return given.data_ptr(), given.numel() * given.element_size()
+
+
+def _run(dev: int, fn, *args) -> None:
+    if torch.cuda.current_device() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != 0:
+        _check(status)
+
+
+def _handle(dev: int, stream) -> int:
+    return _raw_stream(dev) if stream is None else _stream_handle(stream)
+
+
+def _cache_ptrs(k, v, k_scale, v_scale, dev: int, e4m3: Optional[bool]):
+    """Pointers of a cache (4-D, [.., Hkv, rows, d]) and its scales, all of one shape; e4m3: which
+    type it has to have, None: an 8-bit cache if there are scales."""
     shape = k.shape
     if len(shape) != 4:
         raise ValueError(f"caches have 4 dimensions, got {len(shape)}")
-    dtypes = dtypes if dtypes is not None else (_E4M3 if k_scale is not None else _BF16)
-    ptrs = [_tensor("keys' cache", k, shape, dtypes, dev),
-            _tensor("values' cache", v, shape, dtypes, dev)]
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale go together")
-    if k_scale is None:
-        if k.dtype in _E4M3:
+    if k_scale is None or v_scale is None:
+        if k_scale is not v_scale:
+            raise ValueError("k_scale and v_scale go together")
+        if e4m3 or k.dtype in _E4M3:
             raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        return ptrs + [None, None]
-    return ptrs + [_tensor("k_scale", k_scale, shape[:3], _SCALE, dev),
-                   _tensor("v_scale", v_scale, shape[:3], _SCALE, dev)]
+        return (_ptr("keys' cache", k, shape, _BF16, dev),
+                _ptr("values' cache", v, shape, _BF16, dev), None, None)
+    rows = shape[:3]
+    return (_ptr("keys' cache", k, shape, _E4M3, dev), _ptr("values' cache", v, shape, _E4M3, dev),
+            _ptr("k_scale", k_scale, rows, _SCALE, dev),
+            _ptr("v_scale", v_scale, rows, _SCALE, dev))
 
 
-def _table(block_table, B, dev) -> int:
+def _cache_sizes(shape, block_table, B: int, dev: int):
+    """For a cache of `shape`: the block table's address (none if contiguous), the size arguments
+    ([Lmax] or [page_size, num_pages, max_pages]) and the rows a sequence has room for."""
+    if block_table is None:
+        if shape[0] != B:
+            raise ValueError(f"cache of {shape[0]} sequences for a batch of {B}")
+        return (), (shape[2],), shape[2]
     if block_table.dim() != 2:
         raise ValueError("block_table: 2 dimensions expected")
-    return _tensor("block_table", block_table, (B, block_table.shape[1]), _I32, dev)
-
-
-def _cache_sizes(k, block_table, B):
-    """Size arguments of a cache ([Lmax] or [page_size, num_pages, max_pages]), its rows a
-    sequence and its KV heads."""
-    if block_table is None:
-        if k.shape[0] != B:
-            raise ValueError(f"cache of {k.shape[0]} sequences for a batch of {B}")
-        return [k.shape[2]], k.shape[2]
-    return [k.shape[2], k.shape[0], block_table.shape[1]], k.shape[2] * block_table.shape[1]
+    per = block_table.shape[1]
+    return ((_ptr("block_table", block_table, (B, per), _I32, dev),), (shape[2], shape[0], per),
+            shape[2] * per)
 
 
 def _append_fp8(fn, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
                 rope_base, rope_layout, stream):
-    dev = _cuda_device("k_new", k_new, 4)
-    B, Hkv, Tn, d = k_new.shape
-    new = [_tensor("k_new", k_new, k_new.shape, _BF16, dev),
-           _tensor("v_new", v_new, k_new.shape, _BF16, dev)]
-    cache = _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev, _E4M3)
-    table = [] if block_table is None else [_table(block_table, B, dev)]
-    size, _ = _cache_sizes(k_cache, block_table, B)
-    if k_cache.shape[1] != Hkv or k_cache.shape[3] != d:
+    dev = _device_of("k_new", k_new, 4)
+    shape = k_new.shape
+    B, Hkv, Tn, d = shape
+    cache = _cache_ptrs(k_cache, v_cache, k_scale, v_scale, dev, True)
+    cshape = k_cache.shape
+    table, size, _ = _cache_sizes(cshape, block_table, B, dev)
+    if cshape[1] != Hkv or cshape[3] != d:
         raise ValueError("k_new and the cache differ in heads or head size")
-    lens = _tensor("cache_lens", cache_lens, (B,), _I32, dev)
-    _Launch(dev, stream).run(fn, *new, *cache, *table, lens, B, Hkv, Tn, *size, d, CSATTN_BF16,
-                             float(rope_base), _ROPE_LAYOUT[rope_layout])
+    _run(dev, fn, _ptr("k_new", k_new, shape, _BF16, dev), _ptr("v_new", v_new, shape, _BF16, dev),
+         *cache, *table, _ptr("cache_lens", cache_lens, (B,), _I32, dev), B, Hkv, Tn, *size, d,
+         CSATTN_BF16, rope_base, _ROPE_LAYOUT[rope_layout], _handle(dev, stream))
 
 
 def cache_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
@@ -767,23 +769,22 @@ def cache_append_fp8_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: to
 
 
 def _read_fp8(fn, k, v, k_scale, v_scale, block_table, seq_lens, k_out, v_out, stream):
-    dev = _cuda_device("seq_lens", seq_lens, 1)
+    dev = _device_of("seq_lens", seq_lens, 1)
     B = seq_lens.shape[0]
-    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, _E4M3)
-    table = [] if block_table is None else [_table(block_table, B, dev)]
-    size, rows = _cache_sizes(k, block_table, B)
-    Hkv, d = k.shape[1], k.shape[3]
-    lens = _tensor("seq_lens", seq_lens, (B,), _I32, dev)
-    call = _Launch(dev, stream)
+    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, True)
+    _, Hkv, _, d = k.shape
+    table, size, rows = _cache_sizes(k.shape, block_table, B, dev)
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
     if k_out is None:
-        k_out, v_out = (call.empty((B, Hkv, rows, d), torch.bfloat16) for _ in range(2))
+        k_out, v_out = (_empty((B, Hkv, rows, d), torch.bfloat16, dev, stream) for _ in range(2))
     if k_out.dim() != 4:
         raise ValueError("k_out: 4 dimensions expected")
-    shape = (B, Hkv, k_out.shape[2], d)
-    outs = [_tensor("k_out", k_out, shape, _BF16, dev), _tensor("v_out", v_out, shape, _BF16, dev)]
-    call.run(fn, *cache, *table, lens, *outs, B, Hkv, *size, shape[2], d, CSATTN_BF16)
+    Lout = k_out.shape[2]
+    shape = (B, Hkv, Lout, d)
+    _run(dev, fn, *cache, *table, _ptr("seq_lens", seq_lens, (B,), _I32, dev),
+         _ptr("k_out", k_out, shape, _BF16, dev), _ptr("v_out", v_out, shape, _BF16, dev), B, Hkv,
+         *size, Lout, d, CSATTN_BF16, _handle(dev, stream))
     return k_out, v_out
 
 
@@ -820,28 +821,27 @@ def tree_workspace_size(B, Hq, Hkv, Tn, Lmax, d, num_splits: int = 0) -> int:
 
 def _decode_fp8(fn, q, k, v, k_scale, v_scale, block_table, seq_lens, out, rope_base, rope_layout,
                 scale, max_seq_len, num_splits, workspace, stream):
-    dev = _cuda_device("q", q, 4)
+    dev = _device_of("q", q, 4)
     B, Hq, _, d = q.shape
-    qp = _tensor("q", q, (B, Hq, 1, d), _BF16, dev)
-    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, _E4M3)
-    table = [] if block_table is None else [_table(block_table, B, dev)]
-    size, rows = _cache_sizes(k, block_table, B)
-    Hkv = k.shape[1]
-    if k.shape[3] != d:
+    shape = (B, Hq, 1, d)
+    cache = _cache_ptrs(k, v, k_scale, v_scale, dev, True)
+    cshape = k.shape
+    Hkv = cshape[1]
+    table, size, rows = _cache_sizes(cshape, block_table, B, dev)
+    if cshape[3] != d:
         raise ValueError("q and the cache differ in head size")
-    lens = _tensor("seq_lens", seq_lens, (B,), _I32, dev)
-    call = _Launch(dev, stream)
     if out is None:
-        out = call.empty((B, Hq, 1, d), torch.bfloat16)
-    op = _tensor("out", out, (B, Hq, 1, d), _BF16, dev)
+        out = _empty(shape, torch.bfloat16, dev, stream)
     if max_seq_len is None:
         max_seq_len = rows
-    workspace, wp, wn = call.workspace(
-        workspace, 0 if workspace is not None
-        else decode_fp8_workspace_size(B, Hq, Hkv, max_seq_len, d, num_splits))
-    call.run(fn, qp, *cache, *table, lens, op, B, Hq, Hkv, *size, d, CSATTN_BF16,
-             float(rope_base), _ROPE_LAYOUT[rope_layout], float(scale), int(max_seq_len),
-             int(num_splits), wp, wn)
+    if workspace is None:
+        workspace = _empty(decode_fp8_workspace_size(B, Hq, Hkv, max_seq_len, d, num_splits),
+                           torch.uint8, dev, stream)
+    wp, wn = _workspace(workspace, dev)
+    _run(dev, fn, _ptr("q", q, shape, _BF16, dev), *cache, *table,
+         _ptr("seq_lens", seq_lens, (B,), _I32, dev), _ptr("out", out, shape, _BF16, dev), B, Hq,
+         Hkv, *size, d, CSATTN_BF16, rope_base, _ROPE_LAYOUT[rope_layout], scale, max_seq_len,
+         num_splits, wp, wn, _handle(dev, stream))
     return out
 
 
@@ -879,32 +879,31 @@ def attn_decode_fp8_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
 
 def _tree_step(fn, q_new, k_new, v_new, k, v, k_scale, v_scale, block_table, cache_lens, parents,
                out, lse, rope_base, rope_layout, scale, max_seq_len, num_splits, workspace, stream):
-    dev = _cuda_device("q_new", q_new, 4)
-    B, Hq, Tn, d = q_new.shape
+    dev = _device_of("q_new", q_new, 4)
+    qshape = q_new.shape
+    B, Hq, Tn, d = qshape
     cache = _cache_ptrs(k, v, k_scale, v_scale, dev, None)
-    Hkv = k.shape[1]
-    if k.shape[3] != d:
+    cshape = k.shape
+    Hkv = cshape[1]
+    table, size, rows = _cache_sizes(cshape, block_table, B, dev)
+    if cshape[3] != d:
         raise ValueError("q_new and the cache differ in head size")
-    new = [_tensor("q_new", q_new, (B, Hq, Tn, d), _BF16, dev),
-           _tensor("k_new", k_new, (B, Hkv, Tn, d), _BF16, dev),
-           _tensor("v_new", v_new, (B, Hkv, Tn, d), _BF16, dev)]
-    table = [] if block_table is None else [_table(block_table, B, dev)]
-    size, rows = _cache_sizes(k, block_table, B)
-    lens = _tensor("cache_lens", cache_lens, (B,), _I32, dev)
-    tree = _tensor("parents", parents, (B, Tn), _I32, dev)
-    call = _Launch(dev, stream)
+    kshape = (B, Hkv, Tn, d)
     if out is None:
-        out = call.empty((B, Hq, Tn, d), torch.bfloat16)
-    op = _tensor("out", out, (B, Hq, Tn, d), _BF16, dev)
-    lp = None if lse is None else _tensor("lse", lse, (B, Hq, Tn), _F32, dev)
+        out = _empty(qshape, torch.bfloat16, dev, stream)
     if max_seq_len is None:
         max_seq_len = rows
-    workspace, wp, wn = call.workspace(
-        workspace, 0 if workspace is not None
-        else tree_workspace_size(B, Hq, Hkv, Tn, max_seq_len, d, num_splits))
-    call.run(fn, *new, *cache, *table, lens, tree, op, lp, B, Hq, Hkv, Tn, *size, d,
-             CSATTN_BF16 if k_scale is None else CSATTN_E4M3, float(rope_base),
-             _ROPE_LAYOUT[rope_layout], float(scale), int(max_seq_len), int(num_splits), wp, wn)
+    if workspace is None:
+        workspace = _empty(tree_workspace_size(B, Hq, Hkv, Tn, max_seq_len, d, num_splits),
+                           torch.uint8, dev, stream)
+    wp, wn = _workspace(workspace, dev)
+    _run(dev, fn, _ptr("q_new", q_new, qshape, _BF16, dev),
+         _ptr("k_new", k_new, kshape, _BF16, dev), _ptr("v_new", v_new, kshape, _BF16, dev),
+         *cache, *table, _ptr("cache_lens", cache_lens, (B,), _I32, dev),
+         _ptr("parents", parents, (B, Tn), _I32, dev), _ptr("out", out, qshape, _BF16, dev),
+         None if lse is None else _ptr("lse", lse, (B, Hq, Tn), _F32, dev), B, Hq, Hkv, Tn, *size,
+         d, CSATTN_BF16 if k_scale is None else CSATTN_E4M3, rope_base, _ROPE_LAYOUT[rope_layout],
+         scale, max_seq_len, num_splits, wp, wn, _handle(dev, stream))
     return out
 
 
@@ -948,20 +947,18 @@ def attn_tree_step_paged(q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.
 
 def _tree_commit(fn, k, v, k_scale, v_scale, block_table, cache_lens, parents, accepted, new_lens,
                  stream):
-    dev = _cuda_device("parents", parents, 2)
+    dev = _device_of("parents", parents, 2)
     B, Tn = parents.shape
     cache = _cache_ptrs(k, v, k_scale, v_scale, dev, None)
-    table = [] if block_table is None else [_table(block_table, B, dev)]
-    size, _ = _cache_sizes(k, block_table, B)
-    lens = _tensor("cache_lens", cache_lens, (B,), _I32, dev)
-    tree = _tensor("parents", parents, (B, Tn), _I32, dev)
-    acc = _tensor("accepted", accepted, (B,), _I32, dev)
-    call = _Launch(dev, stream)
+    cshape = k.shape
+    table, size, _ = _cache_sizes(cshape, block_table, B, dev)
     if new_lens is None:
-        new_lens = call.empty((B,), torch.int32)
-    np_ = _tensor("new_lens", new_lens, (B,), _I32, dev)
-    call.run(fn, *cache, *table, lens, tree, acc, np_, B, k.shape[1], Tn, *size, k.shape[3],
-             CSATTN_BF16 if k_scale is None else CSATTN_E4M3)
+        new_lens = _empty((B,), torch.int32, dev, stream)
+    _run(dev, fn, *cache, *table, _ptr("cache_lens", cache_lens, (B,), _I32, dev),
+         _ptr("parents", parents, (B, Tn), _I32, dev),
+         _ptr("accepted", accepted, (B,), _I32, dev), _ptr("new_lens", new_lens, (B,), _I32, dev),
+         B, cshape[1], Tn, *size, cshape[3], CSATTN_BF16 if k_scale is None else CSATTN_E4M3,
+         _handle(dev, stream))
     return new_lens
 
 

@@ -77,9 +77,21 @@ int check_rope(const char* fn, float rope_base, int rope_layout, int positions) 
   return CSATTN_OK;
 }
 
+// The frequencies depend on nothing but (d, base) and take d/2 powers to compute, as long as a
+// launch; a thread keeps its last ones.
 int rope_of(float rope_base, int rope_layout, int d, RopeTable* th) {
   if (!(rope_base > 0.f)) return 0;
-  api_rope_table(th, d, static_cast<double>(rope_base));
+  static thread_local struct {
+    int d = 0;
+    float base = 0.f;
+    RopeTable table;
+  } last;
+  if (last.d != d || last.base != rope_base) {
+    api_rope_table(&last.table, d, static_cast<double>(rope_base));
+    last.d = d;
+    last.base = rope_base;
+  }
+  *th = last.table;
   return rope_layout == CSATTN_ROPE_SPLIT_HALF ? 1 : 2;
 }
 
@@ -122,7 +134,7 @@ GroupPlan plan_for(int B, int Hkv, int rows, bool tc, bool f8, int max_seq_len, 
     p.grid = static_cast<int>(std::min<long long>(0x7fffffff, parts * B * Hkv * p.rblocks));
   } else {
     // resident CTAs (launch bounds and shared memory of the kernels)
-    p.most_grid = p.grid = kSms * (tc ? 1 : (f8 ? (p.block_rows == 8 ? 4 : 3) : 2));
+    p.most_grid = p.grid = kSms * (tc ? 1 : (f8 ? 3 : 2));
   }
   return p;
 }

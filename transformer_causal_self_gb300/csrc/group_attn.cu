@@ -52,8 +52,8 @@ struct Cfg {
   static constexpr int ROWS = 8 * NT;               // query rows of a CTA
   static constexpr int QS = 2 * D + 16;             // bytes between query rows (no bank twice)
   // resident CTAs and ring: about 190 KB in flight per SM
-  static constexpr int CTAS = F8 ? (NT == 1 ? 4 : 3) : 2;
-  static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? (NT == 1 ? 3 : 4) : 6);
+  static constexpr int CTAS = F8 ? 3 : 2;
+  static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? 4 : 6);
   static constexpr int RING = NS * STAGE;
   static constexpr int Q_BYTES = ROWS * QS;         // twice: the next piece's go to the other
   static constexpr int SMEM = 1024 + RING + 2 * Q_BYTES + 128 + 2 * ROWS * 4;
@@ -262,21 +262,38 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   // scale bytes of the warp's 16 rows of a tile: lanes 0..15 the keys', 16..31 the values';
   // rows past the sequence and pages outside the pool read 0 (their data is zero or masked).
   // Two loads that depend on one another, so each is issued a tile or two ahead of its use.
+  // (The page's number and the row in it move on by additions: a tile is 64 rows.)
+  const bool paged = F8 && p.rows.block_table != nullptr;
   const int code_row = k_begin + 16 * warp + (lane & 15);
-  auto load_page = [&](int t) -> int {
-    const int r = code_row + t * KT;
-    if (!F8 || p.rows.block_table == nullptr || t >= ntiles || r >= total) return 0;
-    return p.rows.page(b, r);
+  const int ps = paged ? p.rows.page_size : 1;
+  const int32_t* const table = p.rows.block_table + static_cast<size_t>(b) * p.rows.max_pages;
+  const uint8_t* const scale_of = lane < 16 ? p.k_scale : p.v_scale;
+  int pg = code_row / ps, ofs = code_row - pg * ps;  // of the next page lookup
+  auto load_page = [&](int t) -> int2 {              // page of the row in tile t, offset in it
+    const int at = ofs;
+    int page = 0;
+    if (paged) {
+      if (t < ntiles && code_row + t * KT < total) page = table[pg];
+      ofs += KT;
+      if (ps < KT) {
+        pg += KT / ps;
+        ofs = at;
+      } else if (ofs >= ps) {
+        ++pg;
+        ofs -= ps;
+      }
+    }
+    return make_int2(page, at);
   };
-  auto load_code = [&](int t, int page) -> uint32_t {
+  auto load_code = [&](int t, int2 page) -> uint32_t {
     const int r = code_row + t * KT;
     if (!F8 || t >= ntiles || r >= total) return 0u;
-    const long long at = p.rows.in_page(b, kvh, r, page);
-    if (at < 0) return 0u;
-    return (lane < 16 ? p.k_scale : p.v_scale)[at];
+    if (!paged) return scale_of[(static_cast<size_t>(b) * p.Hkv + kvh) * p.rows.Lmax + r];
+    if (page.x < 0 || page.x >= p.rows.num_pages) return 0u;
+    return scale_of[(static_cast<size_t>(page.x) * p.Hkv + kvh) * ps + page.y];
   };
-  const int page0 = load_page(0), page1 = load_page(1);
-  int page2 = load_page(2);
+  const int2 page0 = load_page(0), page1 = load_page(1);
+  int2 page2 = load_page(2);
   uint32_t codes = load_code(0, page0), codes1 = load_code(1, page1);
 
   // queries into shared memory: D/16 lanes per row, 16 channels each
@@ -603,7 +620,7 @@ __global__ void __launch_bounds__(128) group_merge_kernel(
     __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int rows, int Hq, int Hkv, int T,
     int words) {
   constexpr int V = D / 32;
-  constexpr int U = 4;  // partial results whose loads are in flight together
+  constexpr int U = W > 1 ? 8 : 4;  // partial results whose loads are in flight together
   __shared__ float s_part[W > 1 ? 4 : 1][V * 32 + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = static_cast<int>(blockIdx.x) * (4 / W) + warp / W;
