@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -675,10 +676,28 @@ def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
     return t
 
 
-def _workspace(given: torch.Tensor, dev: int):
-    if given.get_device() != dev or not given.is_contiguous():
-        raise ValueError(f"workspace: must be contiguous on cuda:{dev}")
-    return given.data_ptr(), given.numel() * given.element_size()
+# Workspaces of calls that bring none are kept, one per thread and stream: calls of one thread on
+# one stream follow one another on the GPU, and two threads, two streams or two captured graphs
+# never share one.  Larger ones, and those of a capture or a `stream` argument, are allocated.
+_KEPT_BYTES = 64 << 20
+_kept = threading.local()
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, dev: int, stream):
+    """(tensor, address, bytes) of the workspace given, or of one of `need` bytes."""
+    if given is not None:
+        if given.get_device() != dev or not given.is_contiguous():
+            raise ValueError(f"workspace: must be contiguous on cuda:{dev}")
+    elif (stream is None and 0 < need <= _KEPT_BYTES and torch.cuda.current_device() == dev
+          and not torch.cuda.is_current_stream_capturing()):
+        kept = _kept.__dict__
+        key = (dev, _raw_stream(dev))
+        given = kept.get(key)
+        if given is None or given.numel() < need:
+            given = kept[key] = torch.empty((need,), dtype=torch.uint8, device=dev)
+    else:
+        given = _empty((max(need, 16),), torch.uint8, dev, stream)
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 def _run(dev: int, fn, *args) -> None:
@@ -834,10 +853,9 @@ def _decode_fp8(fn, q, k, v, k_scale, v_scale, block_table, seq_lens, out, rope_
         out = _empty(shape, torch.bfloat16, dev, stream)
     if max_seq_len is None:
         max_seq_len = rows
-    if workspace is None:
-        workspace = _empty(decode_fp8_workspace_size(B, Hq, Hkv, max_seq_len, d, num_splits),
-                           torch.uint8, dev, stream)
-    wp, wn = _workspace(workspace, dev)
+    need = 0 if workspace is not None else load_library().csattn_decode_fp8_workspace_size(
+        B, Hq, Hkv, max_seq_len, d, num_splits)
+    workspace, wp, wn = _workspace(workspace, need, dev, stream)
     _run(dev, fn, _ptr("q", q, shape, _BF16, dev), *cache, *table,
          _ptr("seq_lens", seq_lens, (B,), _I32, dev), _ptr("out", out, shape, _BF16, dev), B, Hq,
          Hkv, *size, d, CSATTN_BF16, rope_base, _ROPE_LAYOUT[rope_layout], scale, max_seq_len,
@@ -893,10 +911,9 @@ def _tree_step(fn, q_new, k_new, v_new, k, v, k_scale, v_scale, block_table, cac
         out = _empty(qshape, torch.bfloat16, dev, stream)
     if max_seq_len is None:
         max_seq_len = rows
-    if workspace is None:
-        workspace = _empty(tree_workspace_size(B, Hq, Hkv, Tn, max_seq_len, d, num_splits),
-                           torch.uint8, dev, stream)
-    wp, wn = _workspace(workspace, dev)
+    need = 0 if workspace is not None else load_library().csattn_tree_workspace_size(
+        B, Hq, Hkv, Tn, max_seq_len, d, num_splits)
+    workspace, wp, wn = _workspace(workspace, need, dev, stream)
     _run(dev, fn, _ptr("q_new", q_new, qshape, _BF16, dev),
          _ptr("k_new", k_new, kshape, _BF16, dev), _ptr("v_new", v_new, kshape, _BF16, dev),
          *cache, *table, _ptr("cache_lens", cache_lens, (B,), _I32, dev),

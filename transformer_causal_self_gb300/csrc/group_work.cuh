@@ -19,7 +19,8 @@ struct GroupLine {
   int2* seg;            // [B * heads] of a segment: its first piece and their number
   int B, drafts, min_len, max_len;  // a length outside [min_len, max_len] has no work
   int unit, heads;                  // heads: segments per sequence (KV heads * row blocks)
-  int tiles_per_cta;                // 0: such that the grid takes all
+  int tiles_per_cta;                // 0: such that the grid takes all, but
+  int least_tiles;                  // no fewer than this
   __host__ __device__ __forceinline__ int tiles(int L) const {
     return L < min_len || L > max_len ? 0 : (L + drafts + unit - 1) / unit;
   }
@@ -76,7 +77,8 @@ __device__ __forceinline__ GroupPiece group_start(const GroupLine& g, uint32_t* 
   sum = __reduce_add_sync(0xffffffffu, sum);
   const unsigned line = sum * g.heads;
   GroupPiece p{};
-  p.per = g.tiles_per_cta > 0 ? g.tiles_per_cta : (line + gridDim.x - 1) / gridDim.x;
+  p.per = g.tiles_per_cta > 0 ? g.tiles_per_cta
+                              : max(g.least_tiles, (line + gridDim.x - 1) / gridDim.x);
   const unsigned w0 = static_cast<unsigned>(p.per) * blockIdx.x;
   if (line == 0 || w0 / p.per != blockIdx.x || w0 >= line) return p;  // (w0 may have wrapped)
   unsigned before = 0;

@@ -203,6 +203,7 @@ struct GroupPlan {
   int grid;            // CTAs
   int most_grid;       // CTAs that the partial results have room for
   int tiles_per_cta;   // 0: the tiles of all segments over the grid, as the device finds them
+  int least_tiles;     // then no fewer than this per CTA
   int unit;            // cache rows per tile
   int block_rows;      // query rows of a block
   int rblocks;         // blocks of a KV head's query rows
@@ -237,7 +238,7 @@ struct GroupArgs {
 };
 inline GroupLine group_line(const GroupArgs& a) {
   return GroupLine{a.lens,     a.seg, a.B,         a.drafts, a.min_len, a.max_seq_len - a.drafts,
-                   a.plan.unit, a.Hkv * a.plan.rblocks, a.plan.tiles_per_cta};
+                   a.plan.unit, a.Hkv * a.plan.rblocks, a.plan.tiles_per_cta, a.plan.least_tiles};
 }
 cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
 // The same on tcgen05, for many query rows; rope is 0.
