@@ -5,6 +5,8 @@
 // the sequence's last token) or -2 (no token: padding).  Its depth is the number of drafts
 // above it, its position L + depth, its cache row L + t.  With the position in the key, the
 // rows of an accepted path need only be moved to L, L + 1, ... once the tree is verified.
+#include <algorithm>
+
 #include "fp8.cuh"
 #include "internal.h"
 
@@ -158,87 +160,91 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
 }
 
 // The path of accepted[b] (its ancestors and itself, a_0 < a_1 < ...): row L + i receives row
-// L + a_i.  a_i >= i, so a row is read before it is overwritten when i goes up; a thread
-// owns one 16-byte piece (or a scale byte) of the rows of one KV head and moves it in order,
-// kBatch loads in flight.  CTA (KV head, sequence): latency-bound, a few KB each.
-constexpr int kBatch = 8;
-template <typename T>
-__device__ __forceinline__ void move_rows(T* base, const CacheRows& rows, int b, int g, int L,
-                                          const uint8_t* path, int n, int per, int at) {
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    T x[kBatch];
-    long long to[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      to[j] = -1;
-      if (i0 + j >= n || path[i0 + j] == i0 + j) continue;
-      const long long from = rows.at(b, g, L + path[i0 + j]);
-      to[j] = rows.at(b, g, L + i0 + j);
-      if (from < 0) to[j] = -1;
-      if (to[j] >= 0) x[j] = base[from * per + at];
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      if (to[j] >= 0) base[to[j] * per + at] = x[j];
-  }
-}
+// L + a_i.  A CTA moves some KV heads of one sequence, kMoveRows rows at a time: all of their
+// 16-byte pieces are read, then, behind a barrier, written.  a_i >= i, so what a group of rows
+// overwrites has been read by it or by an earlier one.  Bound by latency (a walk up the tree,
+// the block table, the rows): a few KB per sequence.
+constexpr int kMoveRows = 8;
+constexpr int kMoveBatch = 4;  // pieces per thread in flight
 
 __global__ void __launch_bounds__(kThreads) tree_commit_kernel(
     uint4* k_cache, uint4* v_cache, uint8_t* k_scale, uint8_t* v_scale,
     const int32_t* __restrict__ cache_lens, const int32_t* __restrict__ parents,
     const int32_t* __restrict__ accepted, int32_t* __restrict__ new_lens, CacheRows rows, int Tn,
-    int pieces, uint32_t* status) {
+    int pieces, int heads, uint32_t* status) {
   __shared__ int s_up[kThreads];
-  __shared__ uint8_t s_path[kThreads];
+  __shared__ uint8_t s_path[kThreads];                   // the path, at its end
+  __shared__ long long s_from[kThreads], s_to[kThreads];  // of row i, in rows, KV head 0
   __shared__ int s_n;
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int g0 = blockIdx.x * heads, b = blockIdx.y, tid = threadIdx.x;
+  const int nh = min(heads, rows.Hkv - g0);
   const int L = cache_lens[b], last = accepted[b];
   if (tid < Tn) s_up[tid] = parents[static_cast<size_t>(b) * Tn + tid];
   __syncthreads();
-  if (tid < 32) {
-    // every lane walks up from the accepted token; a walk leaves the tree after at most Tn
-    // steps because each must go down in number
+  if (tid == 0) {
+    // a walk leaves the tree after at most Tn steps because each must go down in number
     int n = 0, t = last;
     bool bad = L < 0 || L > rows.Lmax - Tn || last < -1 || last >= Tn;
-    if (!bad)
-      while (t >= 0) {
-        const int up = s_up[t];
-        ++n;
-        if (up >= t || up < -1) {
-          bad = true;
-          break;
-        }
-        t = up;
-      }
-    if (!bad) {
-      t = last;
-      for (int i = n - 1; i >= 0; --i) {
-        if (tid == 0) s_path[i] = static_cast<uint8_t>(t);
-        t = s_up[t];
-      }
-      // a page outside the pool leaves the sequence as it was
-      __syncwarp();
-      if (rows.block_table != nullptr)
-        for (int i = tid; i < n; i += 32)
-          bad |= rows.at(b, g, L + i) < 0 || rows.at(b, g, L + s_path[i]) < 0;
+    while (!bad && t >= 0) {
+      const int up = s_up[t];
+      s_path[kThreads - ++n] = static_cast<uint8_t>(t);
+      bad = up >= t || up < -1;
+      t = up;
     }
-    bad = __any_sync(0xffffffffu, bad);
-    if (tid == 0) {
-      s_n = bad ? 0 : n;
-      if (g == 0) {
-        new_lens[b] = bad ? L : L + n;
-        if (bad) atomicOr(status, kStatusDeviceArg);
-      }
-    }
+    s_n = bad ? -1 : n;
   }
   __syncthreads();
   const int n = s_n;
-  if (tid < 2 * pieces) {
-    const bool is_v = tid >= pieces;
-    move_rows(is_v ? v_cache : k_cache, rows, b, g, L, s_path, n, pieces,
-              is_v ? tid - pieces : tid);
-  } else if (k_scale != nullptr && tid < 2 * pieces + 2) {
-    move_rows(tid == 2 * pieces ? k_scale : v_scale, rows, b, g, L, s_path, n, 1, 0);
+  bool bad = n < 0;
+  if (tid < n) {
+    s_from[tid] = rows.at(b, 0, L + s_path[kThreads - n + tid]);
+    s_to[tid] = rows.at(b, 0, L + tid);
+    bad = s_from[tid] < 0 || s_to[tid] < 0;  // a page outside the pool: nothing is moved
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0 && g0 == 0) {
+    new_lens[b] = bad ? L : L + n;
+    if (bad) atomicOr(status, kStatusDeviceArg);
+  }
+  if (bad) return;
+  const long long stride = rows.block_table == nullptr ? rows.Lmax : rows.page_size;  // of heads
+  // tasks of a group of rows: (row, head, keys or values, piece), and the scale bytes
+  const int per_head = 2 * pieces, per_row = nh * per_head;
+  for (int i0 = 0; i0 < n; i0 += kMoveRows) {
+    const int group = min(kMoveRows, n - i0);
+    if (k_scale != nullptr) {
+      const int e = tid, i = i0 + e / (2 * nh), gv = e % (2 * nh);
+      // (2 * nh * kMoveRows scale bytes of a group: the launcher keeps them within the CTA)
+      uint8_t x = 0;
+      uint8_t* base = gv & 1 ? v_scale : k_scale;
+      const bool mine = e < group * 2 * nh && s_from[i] != s_to[i];
+      if (mine) x = base[s_from[i] + (g0 + gv / 2) * stride];
+      __syncthreads();
+      if (mine) base[s_to[i] + (g0 + gv / 2) * stride] = x;
+    }
+    for (int c0 = 0; c0 < per_row; c0 += kThreads * kMoveBatch / kMoveRows) {
+      // columns c0.. of the group's rows; a barrier between their loads and their stores
+      const int width = min(per_row - c0, kThreads * kMoveBatch / kMoveRows);
+      uint4 x[kMoveBatch];
+#pragma unroll
+      for (int u = 0; u < kMoveBatch; ++u) {
+        const int e = u * kThreads + tid, i = i0 + e / width, c = c0 + e % width;
+        if (e >= group * width || s_from[i] == s_to[i]) continue;
+        const int h = c / per_head, q = c - h * per_head;
+        x[u] = (q < pieces ? k_cache : v_cache)[(s_from[i] + (g0 + h) * stride) * pieces +
+                                                (q < pieces ? q : q - pieces)];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoveBatch; ++u) {
+        const int e = u * kThreads + tid, i = i0 + e / width, c = c0 + e % width;
+        if (e >= group * width || s_from[i] == s_to[i]) continue;
+        const int h = c / per_head, q = c - h * per_head;
+        (q < pieces ? k_cache : v_cache)[(s_to[i] + (g0 + h) * stride) * pieces +
+                                         (q < pieces ? q : q - pieces)] = x[u];
+      }
+    }
+    __syncthreads();  // (the next group may read what this one has written only in order)
   }
 }
 
@@ -266,10 +272,13 @@ cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
                                int B, int Hkv, int Tn, int d, uint32_t* status,
                                cudaStream_t stream) {
   const int pieces = d * (cache.k_scale != nullptr ? 1 : 2) / 16;
-  tree_commit_kernel<<<dim3(Hkv, B), kThreads, 0, stream>>>(
+  // heads per CTA: few while that leaves SMs idle, at most 16 (their scale bytes fill a CTA)
+  const int heads = std::max(1, std::min({16, Hkv, static_cast<int>(
+                                                       static_cast<long long>(Hkv) * B / 152)}));
+  tree_commit_kernel<<<dim3((Hkv + heads - 1) / heads, B), kThreads, 0, stream>>>(
       static_cast<uint4*>(cache.k), static_cast<uint4*>(cache.v),
       static_cast<uint8_t*>(cache.k_scale), static_cast<uint8_t*>(cache.v_scale), cache_lens,
-      parents, accepted, new_lens, rows_of(cache, Hkv), Tn, pieces, status);
+      parents, accepted, new_lens, rows_of(cache, Hkv), Tn, pieces, heads, status);
   return cudaGetLastError();
 }
 
