@@ -13,17 +13,17 @@ namespace csattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // KV heads per thread: one set of angles, eight loads in flight
+constexpr int kHeads = 4;  // KV heads whose loads (two each) a thread has in flight
 
-// Thread item (b, head group, t, c): 16 channels of a token in up to kHeads KV heads; the
-// G = d/16 threads of a row are neighbouring lanes.  The first k_blocks blocks take the
-// keys, the others the values.
+// Thread item (b, head group, t, c): 16 channels of a token in `span` KV heads, kHeads at a time;
+// the G = d/16 threads of a row are neighbouring lanes.  The first k_blocks blocks take the
+// keys (whose angles serve all of the thread's heads), the others the values.
 template <int D>
-__global__ void __launch_bounds__(kThreads) append_fp8_kernel(
+__global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(
     const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
     uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, uint8_t* __restrict__ k_scale,
     uint8_t* __restrict__ v_scale, const int32_t* __restrict__ cache_lens, CacheRows rows, int B,
-    int Tn, int rope, RopeTable theta, uint32_t* status, int k_blocks) {
+    int Tn, int span, int rope, RopeTable theta, uint32_t* status, int k_blocks) {
   constexpr int G = D / 16;
   __shared__ float th_hi[64], th_lo[64];
   const int tid = static_cast<int>(threadIdx.x);
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(
   }
   __syncthreads();
   const int Hkv = rows.Hkv;
-  const int groups = (Hkv + kHeads - 1) / kHeads;
+  const int groups = (Hkv + span - 1) / span;
   // (32-bit indices: the launcher checks that the items are < 2^31)
   int i = (static_cast<int>(blockIdx.x) - (is_k ? 0 : k_blocks)) * kThreads + tid;
   bool live = i < B * groups * Tn * G;
@@ -44,58 +44,70 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(
   i /= G;
   const int t = i % Tn;
   i /= Tn;
-  const int g0 = (i % groups) * kHeads;
+  const int g0 = (i % groups) * span;
   const int b = i / groups;
+  const int g1 = min(Hkv, g0 + span);
+  int e0, e1;
+  rope_piece(layout, D / 2, c, &e0, &e1);
+  const __nv_bfloat16* src =
+      (is_k ? k_new : v_new) + (static_cast<size_t>(b) * Hkv * Tn + t) * D;
+  const size_t head_step = static_cast<size_t>(Tn) * D;
+  uint4 lo[kHeads], hi[kHeads];
+  auto load = [&](int g) {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (g + k < g1) {
+        lo[k] = *reinterpret_cast<const uint4*>(src + (g + k) * head_step + e0);
+        hi[k] = *reinterpret_cast<const uint4*>(src + (g + k) * head_step + e1);
+      }
+    }
+  };
+  load(g0);
   const int L = cache_lens[b];
   if (L < 0 || L > rows.Lmax - Tn) {  // (no overflow: Lmax, Tn < 2^30)
     if (live && is_k && t == 0 && c == 0 && g0 == 0) atomicOr(status, kStatusDeviceArg);
     live = false;
   }
-  int e0, e1;
-  rope_piece(layout, D / 2, c, &e0, &e1);
-  const __nv_bfloat16* src = is_k ? k_new : v_new;
-  uint4 lo[kHeads], hi[kHeads];
-#pragma unroll
-  for (int k = 0; k < kHeads; ++k) {
-    lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && g0 + k < Hkv) {
-      const __nv_bfloat16* x = src + ((static_cast<size_t>(b) * Hkv + g0 + k) * Tn + t) * D;
-      lo[k] = *reinterpret_cast<const uint4*>(x + e0);
-      hi[k] = *reinterpret_cast<const uint4*>(x + e1);
-    }
+  // the row of KV head 0, and rows from a head to the next
+  const long long row0 = live ? rows.at(b, 0, L + t) : 0;
+  const long long row_step = rows.block_table == nullptr ? rows.Lmax : rows.page_size;
+  if (row0 < 0) {
+    if (c == 0) atomicOr(status, kStatusDeviceArg);
+    live = false;
   }
   float cs[8], sn[8];
-  if (layout != 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 8; ++j) {
+    cs[j] = 1.f;
+    sn[j] = 0.f;
+    if (layout != 0)
       rope_cos_sin<false>(L + t, th_hi[8 * c + j], th_lo[8 * c + j], cs[j], sn[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cs[j] = 1.f, sn[j] = 0.f;
   }
-  uint8_t* out = is_k ? k_cache : v_cache;
-  uint8_t* scale = is_k ? k_scale : v_scale;
+  uint8_t* const out = is_k ? k_cache : v_cache;
+  uint8_t* const scale = is_k ? k_scale : v_scale;
+  // (a block's threads have the same number of rounds but for the last head group's: `span` is
+  // a multiple of kHeads or all heads, and the bound below does not depend on the group)
+  for (int s0 = 0; s0 < span; s0 += kHeads) {
+    if (s0 > 0) load(g0 + s0);
 #pragma unroll
-  for (int k = 0; k < kHeads; ++k) {
-    bool bad;
-    const uint32_t top = row_absmax<G>(lo[k], hi[k], &bad);
-    if (!live || g0 + k >= Hkv) continue;  // (no shuffle below)
-    const long long row = rows.at(b, g0 + k, L + t);
-    if (row < 0) {
-      if (c == 0) atomicOr(status, kStatusDeviceArg);
-      continue;
+    for (int k = 0; k < kHeads; ++k) {
+      bool bad;
+      const uint32_t top = row_absmax<G>(lo[k], hi[k], &bad);
+      if (!live || g0 + s0 + k >= g1) continue;  // (no shuffle below)
+      const long long row = row0 + (g0 + s0 + k) * row_step;
+      const int code = scale_code(top, layout != 0);
+      float y[16];
+      rope16(scale_row(lo[k], code), scale_row(hi[k], code), layout, cs, sn, y);
+      uint8_t* dst = out + row * D;
+      *reinterpret_cast<uint2*>(dst + e0) =
+          make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
+                     pack_e4m3x4(y[4], y[5], y[6], y[7], code, bad));
+      *reinterpret_cast<uint2*>(dst + e1) =
+          make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11], code, bad),
+                     pack_e4m3x4(y[12], y[13], y[14], y[15], code, bad));
+      if (c == 0) scale[row] = static_cast<uint8_t>(code);
     }
-    const int code = scale_code(top, layout != 0);
-    float y[16];
-    rope16(lo[k], hi[k], layout, cs, sn, y);
-    uint8_t* dst = out + row * D;
-    *reinterpret_cast<uint2*>(dst + e0) =
-        make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
-                   pack_e4m3x4(y[4], y[5], y[6], y[7], code, bad));
-    *reinterpret_cast<uint2*>(dst + e1) =
-        make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11], code, bad),
-                   pack_e4m3x4(y[12], y[13], y[14], y[15], code, bad));
-    if (c == 0) scale[row] = static_cast<uint8_t>(code);
   }
 }
 
@@ -170,8 +182,11 @@ cudaError_t launch_cache_append_fp8(const void* k_new, const void* v_new, const 
                                     const int32_t* cache_lens, int B, int Hkv, int Tn, int d,
                                     int rope, const RopeTable& theta, uint32_t* status,
                                     cudaStream_t stream) {
-  const long long items =
-      static_cast<long long>(B) * ((Hkv + kHeads - 1) / kHeads) * Tn * (d / 16);
+  // All heads of a token in one thread while that still fills the GPU (one set of angles serves
+  // them all): 152 SMs * 3 blocks; otherwise kHeads of them.
+  const long long tokens = static_cast<long long>(B) * Tn * (d / 16);
+  const int span = 2 * tokens >= 152LL * 3 * kThreads ? Hkv : std::min(Hkv, kHeads);
+  const long long items = tokens * ((Hkv + span - 1) / span);
   if (items + 2 * kThreads >= 0x3fffffffLL) return cudaErrorInvalidValue;
   const int blocks = static_cast<int>((items + kThreads - 1) / kThreads);
   auto* kernel = d == 128 ? append_fp8_kernel<128> : append_fp8_kernel<64>;
@@ -179,7 +194,7 @@ cudaError_t launch_cache_append_fp8(const void* k_new, const void* v_new, const 
       static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new),
       static_cast<uint8_t*>(cache.k), static_cast<uint8_t*>(cache.v),
       static_cast<uint8_t*>(cache.k_scale), static_cast<uint8_t*>(cache.v_scale), cache_lens,
-      rows_of(cache, Hkv), B, Tn, rope, theta, status, blocks);
+      rows_of(cache, Hkv), B, Tn, span, rope, theta, status, blocks);
   return cudaGetLastError();
 }
 

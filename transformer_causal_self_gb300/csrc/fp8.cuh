@@ -31,17 +31,18 @@ __device__ __forceinline__ int scale_code(uint32_t top, bool rotated) {
   return min(max(c, kScaleMin), kScaleMax);
 }
 
-// 2^-(code - 127) and 2^(code - 127) for codes in [kScaleMin, kScaleMax]
-__device__ __forceinline__ float scale_inv(int code) {
-  return __uint_as_float(static_cast<uint32_t>(254 - code) << 23);
+// the larger magnitude, half by half (signs are left over; a NaN makes the half NaN)
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-
-// largest magnitude bits of the eight bf16 of w, lanes folded: max of both halves
-__device__ __forceinline__ uint32_t absmax8(const uint4& w, uint32_t acc) {
-  acc = __vmaxu2(acc, w.x & 0x7fff7fffu);
-  acc = __vmaxu2(acc, w.y & 0x7fff7fffu);
-  acc = __vmaxu2(acc, w.z & 0x7fff7fffu);
-  return __vmaxu2(acc, w.w & 0x7fff7fffu);
+// largest magnitude bits of 16 bf16; 0x7f80 and above: an infinity or NaN is among them
+__device__ __forceinline__ uint32_t absmax16(const uint4& a, const uint4& b) {
+  const uint32_t x = absmax_bf16x2(absmax_bf16x2(a.x, a.y), absmax_bf16x2(a.z, a.w));
+  const uint32_t y = absmax_bf16x2(absmax_bf16x2(b.x, b.y), absmax_bf16x2(b.z, b.w));
+  const uint32_t m = absmax_bf16x2(x, y) & 0x7fff7fffu;
+  return max(m & 0xffffu, m >> 16);
 }
 __device__ __forceinline__ uint32_t fold2(uint32_t acc) {
   return max(acc & 0xffffu, acc >> 16);
@@ -71,7 +72,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 // whether the row holds an infinity or NaN (then the finite values alone count).
 template <int G>
 __device__ __forceinline__ uint32_t row_absmax(const uint4& a, const uint4& b, bool* bad) {
-  uint32_t top = row_max<G>(fold2(absmax8(b, absmax8(a, 0u))));
+  uint32_t top = row_max<G>(absmax16(a, b));
   *bad = top >= 0x7f80u;
   // every lane takes part in the shuffles of the second pass
   if (__any_sync(0xffffffffu, *bad)) {
@@ -88,14 +89,21 @@ __device__ __forceinline__ float odd_value(float x, bool bad, int code) {
   return code == kScaleMax ? fminf(fmaxf(x, -240.f), 240.f) : x;
 }
 
-// four e4m3 (round to nearest even) of y * 2^-(code - 127), at most 448 by the choice of code
+// The bf16 of a row times 2^-(code - 127): a power of two, so exact (what falls below bf16's
+// normal numbers is far below e4m3's least).
+__device__ __forceinline__ uint4 scale_row(const uint4& w, int code) {
+  const uint32_t s = static_cast<uint32_t>(254 - code) << 7, ss = s | (s << 16);
+  uint4 r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(w.x), "r"(ss));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(w.y), "r"(ss));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.z) : "r"(w.z), "r"(ss));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.w) : "r"(w.w), "r"(ss));
+  return r;
+}
+
+// four e4m3 (round to nearest even) of a scaled row's values, at most 448 by the choice of code
 __device__ __forceinline__ uint32_t pack_e4m3x4(float y0, float y1, float y2, float y3, int code,
                                                 bool bad) {
-  const float inv = scale_inv(code);
-  y0 *= inv;
-  y1 *= inv;
-  y2 *= inv;
-  y3 *= inv;
   if (bad || code == kScaleMax) {
     y0 = odd_value(y0, bad, code);
     y1 = odd_value(y1, bad, code);

@@ -110,6 +110,11 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
       cs[j] = layout != 0 ? s_cos[8 * c + j] : 1.f;
       sn[j] = layout != 0 ? s_sin[8 * c + j] : 0.f;
     }
+    const int code = scale_code(top, layout != 0);
+    if (F8 && !is_q) {
+      lo = scale_row(lo, code);
+      hi = scale_row(hi, code);
+    }
     rope16(lo, hi, layout, cs, sn, y);
     if (layout != 0) {
       lo = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
@@ -142,7 +147,6 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
       continue;
     }
     if constexpr (F8) {
-      const int code = scale_code(top, layout != 0);
       uint8_t* dst = static_cast<uint8_t*>(is_v ? v_cache : k_cache) + row * D;
       *reinterpret_cast<uint2*>(dst + e0) =
           make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
