@@ -13,13 +13,13 @@ namespace csattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // KV heads whose loads (two each) a thread has in flight
+constexpr int kHeads = 2;  // KV heads whose loads (two each) a thread has in flight
 
 // Thread item (b, head group, t, c): 16 channels of a token in `span` KV heads, kHeads at a time;
 // the G = d/16 threads of a row are neighbouring lanes.  The first k_blocks blocks take the
 // keys (whose angles serve all of the thread's heads), the others the values.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(
+__global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(
     const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
     uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, uint8_t* __restrict__ k_scale,
     uint8_t* __restrict__ v_scale, const int32_t* __restrict__ cache_lens, CacheRows rows, int B,
@@ -48,7 +48,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(
   const int b = i / groups;
   const int g1 = min(Hkv, g0 + span);
   int e0, e1;
-  rope_piece(layout, D / 2, c, &e0, &e1);
+  // (16 channels in a row where the rotation does not pair channel p with p + d/2: one store)
+  const bool whole = layout != 1;
+  rope_piece(whole ? 2 : 1, D / 2, c, &e0, &e1);
   const __nv_bfloat16* src =
       (is_k ? k_new : v_new) + (static_cast<size_t>(b) * Hkv * Tn + t) * D;
   const size_t head_step = static_cast<size_t>(Tn) * D;
@@ -100,12 +102,16 @@ __global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(
       float y[16];
       rope16(scale_row(lo[k], code), scale_row(hi[k], code), layout, cs, sn, y);
       uint8_t* dst = out + row * D;
-      *reinterpret_cast<uint2*>(dst + e0) =
-          make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
-                     pack_e4m3x4(y[4], y[5], y[6], y[7], code, bad));
-      *reinterpret_cast<uint2*>(dst + e1) =
-          make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11], code, bad),
-                     pack_e4m3x4(y[12], y[13], y[14], y[15], code, bad));
+      const uint4 x = make_uint4(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
+                                 pack_e4m3x4(y[4], y[5], y[6], y[7], code, bad),
+                                 pack_e4m3x4(y[8], y[9], y[10], y[11], code, bad),
+                                 pack_e4m3x4(y[12], y[13], y[14], y[15], code, bad));
+      if (whole) {
+        *reinterpret_cast<uint4*>(dst + e0) = x;
+      } else {
+        *reinterpret_cast<uint2*>(dst + e0) = make_uint2(x.x, x.y);
+        *reinterpret_cast<uint2*>(dst + e1) = make_uint2(x.z, x.w);
+      }
       if (c == 0) scale[row] = static_cast<uint8_t>(code);
     }
   }
@@ -120,7 +126,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two, float s) {
 
 // 16 channels per thread item (b, g, r, c); consecutive items are consecutive rows of a
 // sequence's KV head.  Blocks of a (b, g): k_blocks for the keys, then as many for the values.
-constexpr int kRows = 4;  // row pieces per thread, kThreads apart: as many loads in flight
+constexpr int kRows = 2;  // row pieces per thread, kThreads apart: as many loads in flight
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_fp8_kernel(
     const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
