@@ -51,7 +51,7 @@ struct Cfg {
   static constexpr int NS2 = F8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
   static constexpr int TILES = (NS1 + 1 > NS2 + 2 ? NS1 + 1 : NS2 + 2) * TILE + NRAW * RAW;
   static constexpr int BARS = 336;
-  static constexpr int SMEM = 1024 + TILES + BARS + 128 * 8 + (F8 ? 8 * 8 + 2 * 256 + 64 : 0);
+  static constexpr int SMEM = 1024 + TILES + BARS + 128 * 8 + (F8 ? 8 * 8 : 0);
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -208,9 +208,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 39);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::TILES + C::BARS);  // [128]
-  float2* s_tile = s_ml + 128;                           // e4m3 [8]: 2^(E_k - 7), E_v of a tile
-  uint16_t* s_mul = reinterpret_cast<uint16_t*>(s_tile + 8);  // e4m3 [2][128] row factors
-  int* s_max = reinterpret_cast<int*>(s_mul + 256);           // e4m3 [4][4]
+  float2* s_tile = s_ml + 128;  // e4m3 [8]: 2^(E_k - 7), E_v of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -431,63 +429,90 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     // ------------------------------------------------------------ e4m3 tiles to f16
     if constexpr (F8) {
     regs_dec<72>();
-    const int v = (warp - kWarpConvert) >> 2;               // 0: keys, 1: values
-    const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;  // the row whose scale it loads
-    constexpr int G = D / 16;                               // 16-channel pieces of a row
+    const int v = (warp - kWarpConvert) >> 2;  // 0: keys, 1: values
+    const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;
+    constexpr int G = D / 16;                  // 16-channel pieces of a row
+    const int ps = p.rows.block_table != nullptr ? p.rows.page_size : 0;
     bool ok = true;
-    uint32_t f = v, tile = 0;  // its next fill, and tile of the CTA
-    for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the four warps' barriers go together)
+    uint32_t f = v, tile = 0;                  // its next fill, and tile of the CTA
+    for (; pc.n > 0 && ok; pc.next(p.line)) {
       const View w(pc, p);
-      // the row's scale bytes, both; 0 where there is no row.  The page comes first, so each of
-      // the two loads is issued a tile ahead of its use.
-      const int code_row = w.k_begin + tid;
+      // Scale bytes: every warp has those of all 128 rows, four per lane (no page ends inside
+      // them), packed.  The page number comes first, so each of the two loads is issued a tile
+      // ahead of its use, and taken over at the tile's end (a register move waits for a load).
+      const int row0 = w.k_begin + 4 * lane;
+      int pg = ps > 0 ? row0 / ps : 0, ofs = row0 - pg * ps;  // of the next page lookup
+      const int32_t* const table =
+          p.rows.block_table + static_cast<size_t>(w.b) * p.rows.max_pages;
       auto load_page = [&](int j) -> int {
-        const int r = code_row + j * BN;
-        return p.rows.block_table == nullptr || j >= w.n || r >= w.k_end ? 0 : p.rows.page(w.b, r);
+        const int page = ps > 0 && j < w.n && row0 + j * BN < w.k_end ? table[pg] : 0;
+        if (ps >= BN) {
+          ofs += BN;
+          if (ofs >= ps) ++pg, ofs -= ps;
+        } else if (ps > 0) {
+          pg += BN / ps;
+        }
+        return page;
       };
-      auto load_code = [&](int j, int page) -> uint32_t {
-        const int r = code_row + j * BN;
-        if (j >= w.n || r >= w.k_end) return 0u;
-        const long long at = p.rows.in_page(w.b, w.kvh, r, page);
-        if (at < 0) return 0u;
-        return (v == 0 ? p.k_scale[at] : 0u) | (static_cast<uint32_t>(p.v_scale[at]) << 8);
+      // four rows' bytes; 0 where there is no row
+      auto load_codes = [&](int j, int page, int at_ofs, uint32_t (&k)[4], uint32_t (&vv)[4]) {
+        const int r = row0 + j * BN;
+        bool have = j < w.n && r < w.k_end;
+        size_t at = 0;
+        if (ps == 0) {
+          at = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.rows.Lmax + r;
+        } else {
+          have = have && page >= 0 && page < p.rows.num_pages;
+          at = (static_cast<size_t>(page) * p.Hkv + w.kvh) * ps + at_ofs;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool mine = have && r + i < w.k_end;
+          k[i] = mine && v == 0 ? p.k_scale[at + i] : 0u;
+          vv[i] = mine ? p.v_scale[at + i] : 0u;
+        }
       };
-      uint32_t code = load_code(0, load_page(0));
-      int page = load_page(1);
+      auto pack = [](const uint32_t (&c)[4]) {
+        return c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
+      };
+      uint32_t nk[4], nv[4];
+      int ofs1 = ofs;
+      int page = load_page(0);
+      load_codes(0, page, ofs1, nk, nv);
+      ofs1 = ofs;
+      page = load_page(1);
+      uint32_t ck = pack(nk), cv = pack(nv);
       for (int j = 0; j < w.n; ++j, f += 2, ++tile) {
         const int key0 = w.k_begin + j * BN;
-        const uint32_t next = load_code(j + 1, page);
-        page = load_page(j + 2);
-        // the tile's largest codes, then every row's factor
-        const int ck = code & 0xff, cv = static_cast<int>(code >> 8);
-        const int mk = __reduce_max_sync(0xffffffffu, ck);
-        const int mv = __reduce_max_sync(0xffffffffu, max(cv, kMinValueCode));
-        int* mx = s_max + 8 * v;
-        if (lane == 0) {
-          mx[warp & 3] = mk;
-          mx[4 + (warp & 3)] = mv;
+        load_codes(j + 1, page, ofs1, nk, nv);
+        const int ofs2 = ofs;
+        const int page_next = load_page(j + 2);
+        // the tile's largest codes, then the factors of the warp's 32 rows, one per lane: row
+        // i * (128 / G) + (32 / G) * warp + q of the tile in lane (32 / G) * i + q
+        const uint32_t hv = __vmaxu2(cv & 0xff00ffu, (cv >> 8) & 0xff00ffu);
+        int E = max(static_cast<int>(__reduce_max_sync(0xffffffffu, max(hv & 0xffffu, hv >> 16))),
+                    kMinValueCode);
+        if (v == 0) {
+          const float Ev = static_cast<float>(E - 127);
+          const uint32_t hk = __vmaxu2(ck & 0xff00ffu, (ck >> 8) & 0xff00ffu);
+          E = __reduce_max_sync(0xffffffffu, max(hk & 0xffffu, hk >> 16));
+          if (tid == 0)
+            s_tile[tile & 7] =
+                make_float2(__uint_as_float(static_cast<uint32_t>(max(E - 7, 1)) << 23), Ev);
         }
-        if (v == 0)
-          asm volatile("bar.sync 3, 128;" ::: "memory");
-        else
-          asm volatile("bar.sync 4, 128;" ::: "memory");
-        const int Ek = max(max(mx[0], mx[1]), max(mx[2], mx[3]));
-        const int Ev = max(max(mx[4], mx[5]), max(mx[6], mx[7]));
-        s_mul[128 * v + tid] = row_scale(v == 0 ? Ek - ck : Ev - cv);
-        if (v == 0 && tid == 0)
-          s_tile[tile & 7] =
-              make_float2(__uint_as_float(static_cast<uint32_t>(max(Ek - 7, 1)) << 23),
-                          static_cast<float>(Ev - 127));
-        if (v == 0)
-          asm volatile("bar.sync 3, 128;" ::: "memory");
-        else
-          asm volatile("bar.sync 4, 128;" ::: "memory");
-        code = next;
+        uint32_t factor;
+        {
+          constexpr int Q = 32 / G;
+          const int r = (lane / Q) * (128 / G) + Q * (warp & 3) + lane % Q;
+          const uint32_t four = __shfl_sync(0xffffffffu, v == 0 ? ck : cv, r >> 2);
+          factor = row_scale(E - static_cast<int>((four >> (8 * (r & 3))) & 0xffu));
+          factor |= factor << 16;
+        }
         const uint32_t rs = f % C::NRAW, s = f % NS;
-        ok = ok && warp_wait(&raw_full[rs], (f / C::NRAW) & 1, abort_flag, p.status) &&
+        ok = warp_wait(&raw_full[rs], (f / C::NRAW) & 1, abort_flag, p.status) &&
              (f < static_cast<uint32_t>(NS) ||
               warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
-        if (!ok) continue;
+        if (!ok) break;
         const uint8_t* src = sRaw + rs * C::RAW;
         uint8_t* dst = sKV + s * C::TILE;
         const bool edge = key0 + BN > min(w.L, w.k_end);
@@ -501,11 +526,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 #pragma unroll 1
         for (int i0 = 0; i0 < G; i0 += 4) {
           uint4 x[4];
-          uint32_t m[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             x[i] = *reinterpret_cast<const uint4*>(src + 16 * ((i0 + i) * 128 + tid));
-            m[i] = s_mul[128 * v + (i0 + i) * kRowStep + r0];
           }
           if (edge) {  // rows past the end: zeros; the drafts' values: if finite
 #pragma unroll
@@ -519,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t mm = m[i] | (m[i] << 16);
+            const uint32_t mm = __shfl_sync(0xffffffffu, factor, (32 / G) * (i0 + i) + lane / G);
             const uint4 lo = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].x), mm),
                                         hmul2(e4m3x2_hi_to_f16x2(x[i].x), mm),
                                         hmul2(e4m3x2_to_f16x2(x[i].y), mm),
@@ -539,6 +562,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           mbar_arrive(&kv_full[s]);
           mbar_arrive(&raw_empty[rs]);
         }
+        ck = pack(nk);
+        cv = pack(nv);
+        page = page_next;
+        ofs1 = ofs2;
       }
     }
     }
