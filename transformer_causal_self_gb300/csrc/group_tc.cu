@@ -41,7 +41,6 @@ constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 1
 
 template <int D, bool F8>
 struct Cfg {
-  // e4m3: registers move from the other warpgroups to the softmax (2*136 + 64 + 2*72 = 5*96)
   static constexpr int kThreads = F8 ? 640 : 384;
   static constexpr int TILE = BN * D * 2;  // a Q, K or V tile of 16-bit values
   static constexpr int RAW = BN * D;       // an e4m3 tile
@@ -63,7 +62,7 @@ struct TParams {
   CacheRows rows;
   const uint8_t* k_scale;
   const uint8_t* v_scale;
-  int words;
+  int words, scale_words;  // scale_words: four rows' scale bytes can be read as a word
   int box_rows;
   float* part_o;
   float* part_ml;
@@ -88,15 +87,6 @@ struct View {
 // f16 or bf16 operands, fp32 accumulators, M = 128
 constexpr uint32_t idesc(bool f16, int N, int b_mn) {
   return idesc_bf16_f32(128, N, 0, b_mn) & (f16 ? ~((7u << 7) | (7u << 10)) : ~0u);
-}
-
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
@@ -148,6 +138,20 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])
                :
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
                : "memory");
 }
 
@@ -244,7 +248,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8 && warp < 12) {
-   if constexpr (F8) regs_dec<64>();
    if (warp == kWarpProducer) {
     // ------------------------------------------------------------ TMA producer
     // fills K_0, V_0, K_1, V_1, ...; lane i copies box i of a tile (see group_attn.cu)
@@ -428,10 +431,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   } else if (warp >= kWarpConvert) {
     // ------------------------------------------------------------ e4m3 tiles to f16
     if constexpr (F8) {
-    regs_dec<72>();
     const int v = (warp - kWarpConvert) >> 2;  // 0: keys, 1: values
     const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;
     constexpr int G = D / 16;                  // 16-channel pieces of a row
+    const uint32_t raw0 = smem_u32(sRaw), kv0 = smem_u32(sKV);
+    uint32_t to0, to1;                         // where the thread's two chunks go in a tile
+    {
+      const int r0 = tid / G, c = tid % G;
+      const uint32_t at = (c >> 2) * (BN * 128) + r0 * 128;
+      to0 = at + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
+      to1 = at + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
+    }
     const int ps = p.rows.block_table != nullptr ? p.rows.page_size : 0;
     bool ok = true;
     uint32_t f = v, tile = 0;                  // its next fill, and tile of the CTA
@@ -454,37 +464,39 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         return page;
       };
-      // four rows' bytes; 0 where there is no row
-      auto load_codes = [&](int j, int page, int at_ofs, uint32_t (&k)[4], uint32_t (&vv)[4]) {
-        const int r = row0 + j * BN;
-        bool have = j < w.n && r < w.k_end;
-        size_t at = 0;
+      // four rows' bytes of an array; 0 where there is no row
+      auto load_codes = [&](const uint8_t* scale, int j, int page, int at_ofs) -> uint32_t {
+        const int r = row0 + j * BN, left = w.k_end - r;
+        if (j >= w.n || left <= 0) return 0u;
+        size_t at;
         if (ps == 0) {
           at = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.rows.Lmax + r;
         } else {
-          have = have && page >= 0 && page < p.rows.num_pages;
+          if (page < 0 || page >= p.rows.num_pages) return 0u;
           at = (static_cast<size_t>(page) * p.Hkv + w.kvh) * ps + at_ofs;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool mine = have && r + i < w.k_end;
-          k[i] = mine && v == 0 ? p.k_scale[at + i] : 0u;
-          vv[i] = mine ? p.v_scale[at + i] : 0u;
-        }
+        if (p.scale_words) return *reinterpret_cast<const uint32_t*>(scale + at);
+        uint32_t x = 0u;
+        for (int i = 0; i < min(left, 4); ++i) x |= static_cast<uint32_t>(scale[at + i]) << (8 * i);
+        return x;
       };
-      auto pack = [](const uint32_t (&c)[4]) {
-        return c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
+      auto valid = [&](int j) -> uint32_t {  // bytes of rows there are
+        const int left = w.k_end - (row0 + j * BN);
+        return left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
       };
-      uint32_t nk[4], nv[4];
       int ofs1 = ofs;
       int page = load_page(0);
-      load_codes(0, page, ofs1, nk, nv);
+      uint32_t ck = v == 0 ? load_codes(p.k_scale, 0, page, ofs1) : 0u;
+      uint32_t cv = load_codes(p.v_scale, 0, page, ofs1);
       ofs1 = ofs;
       page = load_page(1);
-      uint32_t ck = pack(nk), cv = pack(nv);
       for (int j = 0; j < w.n; ++j, f += 2, ++tile) {
         const int key0 = w.k_begin + j * BN;
-        load_codes(j + 1, page, ofs1, nk, nv);
+        const uint32_t nk = v == 0 ? load_codes(p.k_scale, j + 1, page, ofs1) : 0u;
+        const uint32_t nv = load_codes(p.v_scale, j + 1, page, ofs1);
+        const uint32_t there = valid(j);
+        ck &= there;
+        cv &= there;
         const int ofs2 = ofs;
         const int page_next = load_page(j + 2);
         // the tile's largest codes, then the factors of the warp's 32 rows, one per lane: row
@@ -513,27 +525,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
              (f < static_cast<uint32_t>(NS) ||
               warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
         if (!ok) break;
-        const uint8_t* src = sRaw + rs * C::RAW;
-        uint8_t* dst = sKV + s * C::TILE;
         const bool edge = key0 + BN > min(w.L, w.k_end);
-        // piece i of the thread is row i * (128 / G) + tid / G, chunks 2c and 2c + 1 of it
-        // after; rows' second halves store those the other way round, so that eight lanes write
-        // eight different banks
-        const int r0 = tid / G, c = tid % G, c0 = 2 * (c & 3), flip = (c >> 2) & 1;
-        uint8_t* const at0 = dst + (c >> 2) * (BN * 128) + r0 * 128;
-        const uint32_t off0 = ((c0 + flip) ^ (r0 & 7)) << 4, off1 = ((c0 + 1 - flip) ^ (r0 & 7)) << 4;
+        // piece i of the thread is row i * (128 / G) + tid / G
         constexpr int kRowStep = 128 / G;  // (a multiple of 8: the swizzle stays)
+        const uint32_t src = raw0 + rs * C::RAW + 16 * tid;
+        const uint32_t dst0 = kv0 + s * C::TILE + to0, dst1 = kv0 + s * C::TILE + to1;
 #pragma unroll 1
         for (int i0 = 0; i0 < G; i0 += 4) {
           uint4 x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = *reinterpret_cast<const uint4*>(src + 16 * ((i0 + i) * 128 + tid));
-          }
+          for (int i = 0; i < 4; ++i) x[i] = lds128(src + (i0 + i) * 2048);
           if (edge) {  // rows past the end: zeros; the drafts' values: if finite
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = key0 + (i0 + i) * kRowStep + r0;
+              const int r = key0 + (i0 + i) * kRowStep + tid / G;
               if (r >= w.k_end) x[i] = make_uint4(0u, 0u, 0u, 0u);
               if (v == 1 && r >= w.L)
                 x[i] = make_uint4(finite_e4m3x4(x[i].x), finite_e4m3x4(x[i].y),
@@ -551,9 +556,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                                         hmul2(e4m3x2_hi_to_f16x2(x[i].z), mm),
                                         hmul2(e4m3x2_to_f16x2(x[i].w), mm),
                                         hmul2(e4m3x2_hi_to_f16x2(x[i].w), mm));
-            uint8_t* at = at0 + (i0 + i) * (kRowStep * 128);
-            *reinterpret_cast<uint4*>(at + off0) = flip ? hi : lo;
-            *reinterpret_cast<uint4*>(at + off1) = flip ? lo : hi;
+            sts128(dst0 + (i0 + i) * (kRowStep * 128), lo);
+            sts128(dst1 + (i0 + i) * (kRowStep * 128), hi);
           }
         }
         fence_proxy_async_smem();
@@ -562,8 +566,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           mbar_arrive(&kv_full[s]);
           mbar_arrive(&raw_empty[rs]);
         }
-        ck = pack(nk);
-        cv = pack(nv);
+        ck = nk;
+        cv = nv;
         page = page_next;
         ofs1 = ofs2;
       }
@@ -571,7 +575,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    if constexpr (F8) regs_inc<136>();
     const int x = warp >> 2;
     const int row = threadIdx.x & 127;  // of the query tile
     const int M = p.T * p.rep;
@@ -661,6 +664,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               for (int k = 0; k < 4; ++k)
                 mq[k] = fmax3(mq[k], __uint_as_float(r[e + k]), __uint_as_float(r[e + 4 + k]));
           };
+          if constexpr (F8) {
+            // (20 warps leave 96 registers: the loads in flight would spill)
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              tmem_ld32_issue(tS + 32u * i, ra);
+              tmem_ld32_wait(ra);
+              max32(ra);
+            }
+          } else {
           tmem_ld32_issue(tS, ra);
           tmem_ld32_wait(ra);
           tmem_ld32_issue(tS + 32u, rb);
@@ -674,13 +686,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           tmem_ld32_wait(rb);
           tmem_ld32_issue(tS, ra);
           max32(rb);
+          }
           const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
           const bool mine = top > R + kRescaleThreshold;
           if (__any_sync(0xffffffffu, mine)) {
             const float f = mine ? ex2_approx(R - top) : 1.f;
             l *= f;
             if (j >= step) {
-              tmem_ld32_wait(ra);  // (ra is read after the wait that follows, too)
+              if constexpr (!F8) tmem_ld32_wait(ra);
 #pragma unroll 1
               for (int i = 0; i < D / 32; ++i) {
                 uint32_t r[32];
@@ -713,6 +726,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             tmem_st16(at, pk);
           };
+          if constexpr (F8) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              tmem_ld32_issue(tS + 32u * i, ra);
+              tmem_ld32_wait(ra);
+              weights32(ra, tS + 16u * i);
+            }
+          } else {
           tmem_ld32_wait(ra);
           tmem_ld32_issue(tS + 32u, rb);
           weights32(ra, tS);
@@ -724,6 +745,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           weights32(ra, tS + 32u);
           tmem_ld32_wait(rb);
           weights32(rb, tS + 48u);
+          }
           const float sum = (sa0 + sa1) + (sb0 + sb1);
           l += F8 ? sum * ex2_approx(-ev - 7.f) : sum;
           tmem_st_wait();
@@ -821,6 +843,9 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.k_scale = static_cast<const uint8_t*>(a.cache.k_scale);
   p.v_scale = static_cast<const uint8_t*>(a.cache.v_scale);
   p.words = a.words;
+  p.scale_words = ((reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale)) &
+                   3u) == 0 &&
+                  (a.cache.block_table != nullptr || a.cache.Lmax % 4 == 0);
   const bool paged = a.cache.block_table != nullptr;
   const int ps = a.cache.page_size;
   p.box_rows = !paged || ps % BN == 0 ? BN : (ps < 64 ? ps : 64);
