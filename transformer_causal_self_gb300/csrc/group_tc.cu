@@ -41,6 +41,9 @@ constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 1
 
 template <int D, bool F8>
 struct Cfg {
+  // e4m3: 640 threads have 96 registers each; some of the others' go to the softmax
+  // (2*136 + 64 + 2*72 = 5*96; a tile takes 1.57 us, 1.58-1.69 with 112..144 there, 2.0 with none
+  // moved)
   static constexpr int kThreads = F8 ? 640 : 384;
   static constexpr int TILE = BN * D * 2;  // a Q, K or V tile of 16-bit values
   static constexpr int RAW = BN * D;       // an e4m3 tile
@@ -87,6 +90,23 @@ struct View {
 // f16 or bf16 operands, fp32 accumulators, M = 128
 constexpr uint32_t idesc(bool f16, int N, int b_mn) {
   return idesc_bf16_f32(128, N, 0, b_mn) & (f16 ? ~((7u << 7) | (7u << 10)) : ~0u);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
@@ -248,6 +268,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8 && warp < 12) {
+   if constexpr (F8) regs_dec<64>();
    if (warp == kWarpProducer) {
     // ------------------------------------------------------------ TMA producer
     // fills K_0, V_0, K_1, V_1, ...; lane i copies box i of a tile (see group_attn.cu)
@@ -323,76 +344,86 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
    } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t kv0 = smem_u32(sKV);
-      constexpr uint32_t kIdS = idesc(F8, BN, 0), kIdO = idesc(F8, D, 1);
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!ok) return false;
-        ok = ctl_wait(bar, parity, abort_flag, p.status, kWaitNs);
-        tc_fence_after();
-        return ok;
-      };
-      auto full = [&](uint32_t f) { return wait(&kv_full[f % NS], (f / NS) & 1); };
-      // S_x = Q K^T with the keys of fill f
-      auto qk = [&](int x, uint32_t f) {
-        const uint32_t q = smem_u32(sQ) + (pair ? x : 0) * C::TILE;
-        const uint32_t k = kv0 + (f % NS) * C::TILE;
+    // The whole warp keeps the books, so that addresses stay in uniform registers; one lane
+    // issues.  Descriptors differ in their low words alone, by constants within a product, and
+    // all waits of a step come ahead of its products: the tensor core's queue is short.
+    const bool leader = elect_one();
+    const uint64_t hi = smem_desc_sw128(0, 16, 1024), hi_v = smem_desc_sw128(0, BN * 128, 1024);
+    const uint32_t q_lo = smem_u32(sQ) >> 4, kv_lo = smem_u32(sKV) >> 4;
+    constexpr uint32_t kIdS = idesc(F8, BN, 0), kIdO = idesc(F8, D, 1);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = warp_wait(bar, parity, abort_flag, p.status);
+      return ok;
+    };
+    auto full = [&](uint32_t f) { return wait(&kv_full[f % NS], (f / NS) & 1); };
+    // S_x = Q K^T with the keys of fill f
+    auto qk = [&](int x, uint32_t f) {
+      const uint64_t q = hi + q_lo + (pair ? x : 0) * (C::TILE >> 4);
+      const uint64_t k = hi + kv_lo + (f % NS) * (C::TILE >> 4);
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = static_cast<uint32_t>((kk >> 2) * (BN * 128) + (kk & 3) * 32);
-          umma_ss(tmem + 128u * x, smem_desc_sw128(q + off, 16, 1024),
-                  smem_desc_sw128(k + off, 16, 1024), kIdS, kk > 0 ? 1u : 0u);
+          const uint32_t off = static_cast<uint32_t>((kk >> 2) * (BN * 8) + (kk & 3) * 2);
+          umma_ss(tmem + 128u * x, q + off, k + off, kIdS, kk > 0 ? 1u : 0u);
         }
         tc_commit(&s_full[x]);
-      };
-      auto pv = [&](int x, uint32_t f, bool accumulate) {
-        const uint32_t v = kv0 + (f % NS) * C::TILE;
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int x, uint32_t f, bool accumulate) {
+      const uint64_t v = hi_v + kv_lo + (f % NS) * (C::TILE >> 4);
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          umma_ts(tmem + 256u + D * x, tmem + 128u * x + 8u * kk,
-                  smem_desc_sw128(v + 2048u * kk, BN * 128, 1024), kIdO,
+          umma_ts(tmem + 256u + D * x, tmem + 128u * x + 8u * kk, v + 128u * kk, kIdO,
                   (accumulate || kk > 0) ? 1u : 0u);
-      };
-      uint32_t F = 0, np[2] = {0, 0}, used[2] = {0, 0}, piece = 0;
-      for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
-        const int n = pc.n;
-        wait(&q_ready[0], piece & 1);
-        if (pair) wait(&q_ready[1], piece & 1);
-        // first tiles of both streams
-        for (int j = 0; j < step && j < n; ++j) {
-          if (!full(F + 2 * j)) break;
-          for (int x = pair ? 0 : j; x <= (pair ? 1 : j); ++x) qk(x, F + 2 * j);
-          tc_commit(&kv_empty[(F + 2 * j) % NS]);
-        }
-        for (int j = 0; j < n && ok; ++j) {
-          const int x0 = pair ? 0 : (j & 1), x1 = pair ? 1 : x0, jn = j + step;
-          for (int x = x0; x <= x1 && ok; ++x) {
-            if (!wait(&p_full[x], np[x] & 1)) break;
-            ++np[x];
-            if (x == x0 && !full(F + 2 * j + 1)) break;
-            // the stream's first tile of a piece: its O has been read
-            if (j < step) {
-              if (used[x] > 0 && !wait(&o_empty[x], (used[x] - 1) & 1)) break;
-              ++used[x];
-            }
-            pv(x, F + 2 * j + 1, j >= step);
-            if (x == x1) tc_commit(&kv_empty[(F + 2 * j + 1) % NS]);
-            if (jn >= n) {
-              tc_commit(&o_full[x]);
-            } else {
-              if (x == x0 && !full(F + 2 * jn)) break;
-              qk(x, F + 2 * jn);
-              if (x == x1) tc_commit(&kv_empty[(F + 2 * jn) % NS]);
-            }
+      }
+      __syncwarp();
+    };
+    auto release = [&](uint64_t* bar) {  // when what has been issued is done
+      if (leader) tc_commit(bar);
+      __syncwarp();
+    };
+    uint32_t F = 0, np[2] = {0, 0}, used[2] = {0, 0}, piece = 0;
+    for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
+      const int n = pc.n;
+      wait(&q_ready[0], piece & 1);
+      if (pair) wait(&q_ready[1], piece & 1);
+      // first tiles of both streams
+      for (int j = 0; j < step && j < n; ++j) {
+        if (!full(F + 2 * j)) break;
+        tc_fence_after();
+        for (int x = pair ? 0 : j; x <= (pair ? 1 : j); ++x) qk(x, F + 2 * j);
+        release(&kv_empty[(F + 2 * j) % NS]);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int x0 = pair ? 0 : (j & 1), x1 = pair ? 1 : x0, jn = j + step;
+        if (!full(F + 2 * j + 1) || (jn < n && !full(F + 2 * jn))) break;
+        for (int x = x0; x <= x1 && ok; ++x) {
+          // the stream's first tile of a piece: its O has been read
+          if (j < step) {
+            if (used[x] > 0 && !wait(&o_empty[x], (used[x] - 1) & 1)) break;
+            ++used[x];
+          }
+          if (!wait(&p_full[x], np[x] & 1)) break;
+          ++np[x];
+          tc_fence_after();
+          pv(x, F + 2 * j + 1, j >= step);
+          if (x == x1) release(&kv_empty[(F + 2 * j + 1) % NS]);
+          if (jn >= n) {
+            release(&o_full[x]);
+          } else {
+            qk(x, F + 2 * jn);
+            if (x == x1) release(&kv_empty[(F + 2 * jn) % NS]);
           }
         }
-        F += 2 * n;
       }
-      // every MMA issued above has completed once this barrier flips
-      tc_commit(teardown);
-      mbar_wait(teardown, 0, nullptr, p.status, kDrainNs);
+      F += 2 * n;
     }
+    // every MMA issued above has completed once this barrier flips
+    release(teardown);
+    if (leader) mbar_wait(teardown, 0, nullptr, p.status, kDrainNs);
     __syncwarp();
    } else if (!F8) {
     // ------------------------------------------------------------ clean values (bf16)
@@ -431,6 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   } else if (warp >= kWarpConvert) {
     // ------------------------------------------------------------ e4m3 tiles to f16
     if constexpr (F8) {
+    regs_dec<72>();
     const int v = (warp - kWarpConvert) >> 2;  // 0: keys, 1: values
     const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;
     constexpr int G = D / 16;                  // 16-channel pieces of a row
@@ -575,6 +607,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
+    if constexpr (F8) regs_inc<136>();
     const int x = warp >> 2;
     const int row = threadIdx.x & 127;  // of the query tile
     const int M = p.T * p.rep;
