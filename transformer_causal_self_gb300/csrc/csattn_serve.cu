@@ -136,7 +136,7 @@ GroupPlan plan_for(int B, int Hkv, int rows, bool tc, bool f8, int max_seq_len, 
     // Resident CTAs (launch bounds and shared memory of the kernels), or as many as the longest
     // sequences could occupy.  The small kernel's CTAs take two tiles at least: with one, a
     // short cache ends in as many partial results as tiles (one sequence of 1000 rows, 8 KV
-    // heads: 9.8 us against 9.2).
+    // heads: 9.8 us against 8.6).
     p.least_tiles = tc ? 1 : 2;
     const long long tiles = (max_seq_len + p.unit - 1) / p.unit;
     const long long line = tiles * B * Hkv * p.rblocks;
@@ -374,7 +374,8 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: append launch");
   e = a.plan.tc ? launch_group_tc(a, st) : launch_group_attn(a, st);
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: kernel launch");
-  e = launch_group_merge(a, p.vflag, v_new, out, lse, st);
+  e = a.plan.tc ? launch_group_tc_merge(a, p.vflag, v_new, out, lse, st)
+                : launch_group_merge(a, p.vflag, v_new, out, lse, st);
   return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "attn_tree_step: merge launch");
 }
 

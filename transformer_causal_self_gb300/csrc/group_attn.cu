@@ -307,8 +307,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
       float factor = 1.f;
       if (r < C::ROWS && row < M) {
-        const int t = row / p.rep, h = kvh * p.rep + row - t * p.rep;
-        const size_t at = (static_cast<size_t>(b) * p.Hq + h) * p.T + t;
+        const size_t at = (static_cast<size_t>(b) * p.Hkv + kvh) * M + row;
         lo = *reinterpret_cast<const uint4*>(p.q + at * D + e0);
         hi = *reinterpret_cast<const uint4*>(p.q + at * D + e1);
         if (F8 && p.q_factor != nullptr) factor = p.q_factor[at];

@@ -10,9 +10,9 @@
 //              the end.
 // One CTA per SM; the CTAs take equal ranges of all the tiles (group_work.cuh), and the rings
 // and barriers run on from one piece to the next:
-//   warps 0-3, 4-7  softmax of stream 0 and 1, a query row per thread; they also write a
-//                   piece's queries to shared memory and its partial results at its end
-//   warp 8          TMA producer          warp 9   TMEM owner and MMA issuer (one thread)
+//   warps 0-3, 4-7  softmax of stream 0 and 1, a query row per thread, and the partial results
+//                   at a piece's end
+//   warp 8          TMA producer          warp 9   TMEM owner and MMA issuer
 //   warps 10-11     bf16: clean the values of tiles that not every query sees
 //   warps 12-15     e4m3: take the keys' tiles to f16;  warps 16-19  the values'
 // TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D) O_1 [256+D,256+2D); P overwrites the
@@ -58,7 +58,6 @@ struct Cfg {
 };
 
 struct TParams {
-  const uint16_t* q;
   const float* q_factor;
   const uint32_t* anc;
   GroupLine line;
@@ -206,7 +205,8 @@ __device__ __forceinline__ uint16_t row_scale(int below) {
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
-    group_tc_kernel(const __grid_constant__ TParams p, const __grid_constant__ CUtensorMap tm_k,
+    group_tc_kernel(const __grid_constant__ TParams p, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, F8>;
   extern __shared__ uint8_t smem_raw[];
@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   uint8_t* sKV = smem + (1 + pair) * C::TILE;
   uint8_t* sRaw = smem + C::TILES - C::NRAW * C::RAW;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::TILES);
-  uint64_t* q_ready = bars + 0;    // [2]
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;
   uint64_t* s_full = bars + 2;     // [2]
   uint64_t* p_full = bars + 4;     // [2]
   uint64_t* o_full = bars + 6;     // [2]
@@ -239,13 +240,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_ready[x], 4);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
       mbar_init(&o_empty[x], 4);
     }
     mbar_init(teardown, 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < 8; ++s) {
       mbar_init(&kv_full[s], F8 ? 4 : 1);
       mbar_init(&kv_empty[s], 1);
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     // ------------------------------------------------------------ TMA producer
     // fills K_0, V_0, K_1, V_1, ...; lane i copies box i of a tile (see group_attn.cu)
     if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -281,12 +284,34 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const uint32_t depth = F8 ? C::NRAW : NS;
     uint64_t* full = F8 ? raw_full : kv_full;
     uint64_t* empty = F8 ? raw_empty : kv_empty;
-    uint32_t f = 0, edges = 0;
+    uint32_t f = 0, edges = 0, piece = 0, queries = 0;
     uint64_t recent = 0;  // a byte per fill, the latest lowest: 8 + (edge % 8), or 0
     bool ok = true;
-    for (; pc.n > 0 && ok; pc.next(p.line)) {
+    // The piece's queries, once the products with the last piece's are done: behind its first
+    // tile, so that this wait does not hold that up.
+    auto load_queries = [&](const View& w) {
+      bool done = true;
+      if (lane == 0 && queries > 0)
+        done = ctl_wait(q_empty, (queries - 1) & 1, abort_flag, p.status, kWaitNs);
+      if (!__all_sync(0xffffffffu, done)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, (1 + pair) * C::TILE);
+        for (int x = 0; x <= pair; ++x)
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(sQ + x * C::TILE + kb * (BN * 128), &tm_q, q_full, kb * 64,
+                        (w.rb * (1 + pair) + x) * BN, w.b * p.Hkv + w.kvh);
+      }
+      ++queries;
+      __syncwarp();
+      return true;
+    };
+    // (the kernel before wrote queries and the drafts' rows by plain stores)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    if (pc.n > 0) load_queries(View(pc, p));
+    for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
       const View w(pc, p);
       for (int j = 0; j < w.n && ok; ++j) {
+        if (j == 1 && piece > 0 && !(ok = load_queries(w))) break;
         int plane = w.b * p.Hkv + w.kvh, prow = w.k_begin + j * BN;
         if (lane < nbox && R.block_table != nullptr) {
           const int tr = prow + r0;
@@ -333,6 +358,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           __syncwarp();
         }
       }
+      if (ok && w.n == 1 && piece > 0) ok = load_queries(w);
     }
     if (lane == 0 && *abort_flag) {
       // every copy still in flight lands before the CTA's shared memory is released
@@ -341,6 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         mbar_wait(e ? &edge_full[e & 3u] : &full[(f - i) % depth],
                   e ? (e >> 2) & 1u : ((f - i) / depth) & 1u, nullptr, p.status, kDrainNs);
       }
+      if (queries > 0) mbar_wait(q_full, (queries - 1) & 1, nullptr, p.status, kDrainNs);
     }
    } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
@@ -388,14 +415,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     uint32_t F = 0, np[2] = {0, 0}, used[2] = {0, 0}, piece = 0;
     for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
       const int n = pc.n;
-      wait(&q_ready[0], piece & 1);
-      if (pair) wait(&q_ready[1], piece & 1);
+      wait(q_full, piece & 1);
       // first tiles of both streams
       for (int j = 0; j < step && j < n; ++j) {
         if (!full(F + 2 * j)) break;
         tc_fence_after();
         for (int x = pair ? 0 : j; x <= (pair ? 1 : j); ++x) qk(x, F + 2 * j);
         release(&kv_empty[(F + 2 * j) % NS]);
+        if (j == n - 1) release(q_empty);
       }
       for (int j = 0; j < n && ok; ++j) {
         const int x0 = pair ? 0 : (j & 1), x1 = pair ? 1 : x0, jn = j + step;
@@ -415,7 +442,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             release(&o_full[x]);
           } else {
             qk(x, F + 2 * jn);
-            if (x == x1) release(&kv_empty[(F + 2 * jn) % NS]);
+            if (x == x1) {
+              release(&kv_empty[(F + 2 * jn) % NS]);
+              if (jn == n - 1) release(q_empty);
+            }
           }
         }
       }
@@ -614,47 +644,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + 128u * x;
     const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(D) * x;
-    // the thread's query row of a piece: its index in [B, Hq, T], -1 for padding
-    auto query = [&](const GroupPiece& q, int* t) -> long long {
-      const int kvh = q.head / p.rblocks, rb = q.head - kvh * p.rblocks;
-      const int r = rb * (pair ? 256 : 128) + (pair ? x * 128 : 0) + row;
-      *t = r < M ? r / p.rep : 0;
-      if (r >= M) return -1;
-      return (static_cast<long long>(q.b) * p.Hq + kvh * p.rep + r - *t * p.rep) * p.T + *t;
-    };
-    // the piece's queries, 16-byte chunks in the swizzled layout of a K-major operand; the
-    // products that read the last piece's have completed
-    auto put_queries = [&](const GroupPiece& q) {
-      if (!pair && x == 1) return;
-      int t;
-      const long long qi = query(q, &t);
-      uint8_t* dst = sQ + (pair ? x : 0) * C::TILE + row * 128;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (qi < 0 ? 0 : qi) * D);
-#pragma unroll
-      for (int c0 = 0; c0 < D / 8; c0 += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = qi >= 0 ? src[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(dst + (c0 >> 3) * (BN * 128) + ((c ^ (row & 7)) << 4)) = v[c];
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_ready[pair ? x : 0]);
-    };
-
     uint32_t ns = 0, tile0 = 0, done[2] = {0, 0};  // done: pieces in which stream 0, 1 had tiles
     bool ok = true;
-    put_queries(pc);
-    while (pc.n > 0) {  // (to the end: the warps' barriers go together)
+    for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the warps' barriers go together)
       const View w(pc, p);
-      int t;
-      const long long qi = query(pc, &t);
-      const bool live = qi >= 0;
+      const int r = (w.rb * (1 + pair) + (pair ? x : 0)) * BN + row;  // of the KV head's
+      const bool live = r < M;
       const bool warp_live = __any_sync(0xffffffffu, live);
+      const int t = live ? r / p.rep : 0;
       float row_factor = p.scale_log2;
-      if (F8 && live) row_factor *= p.q_factor[qi];
+      if (F8 && live) row_factor *= p.q_factor[(static_cast<size_t>(w.b) * p.Hkv + w.kvh) * M + r];
       const uint32_t* anc = p.anc + (static_cast<size_t>(w.b) * p.T + t) * p.words;
       const size_t slot = static_cast<size_t>(blockIdx.x) + pc.segment(p.line);
       if (threadIdx.x == 0) pc.leave_for_merge(p.line);
@@ -788,15 +787,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       tile0 += w.n;
-      // The products with this piece's queries have completed (their scores were seen); with
-      // one query tile, those of both streams.
       if (!pair) {
         if (x == 1) s_ml[row] = make_float2(R, l);
         asm volatile("bar.sync 2, 256;" ::: "memory");
       }
-      pc.next(p.line);
-      if (ok && pc.n > 0) put_queries(pc);
-      // partial result: R, l and O, relative to 2^R
+      // partial result: R, l and O, relative to 2^R; four channels of all rows together, so that
+      // a warp's lanes, which hold a row each, store 512 bytes in a row
       const bool two = !pair && w.n > 1;  // both streams had tiles of this row
       if (pair || x == 0) {
         ok = ok && warp_wait(&o_full[x], done[0] & 1, abort_flag, p.status) &&
@@ -818,7 +814,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               f1 = o_scale * e1;
             }
             const size_t at = slot * p.part_rows + (pair ? x * 128 : 0) + row;
-            float* dst = p.part_o + at * D;
+            float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * p.part_rows +
+                          (pair ? x * 128 : 0) + row;
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
               uint32_t r[32];
@@ -834,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               if (live) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<float4*>(dst + 32 * i + e) =
+                  dst[static_cast<size_t>(8 * i + e / 4) * p.part_rows] =
                       make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
               }
             }
@@ -863,11 +860,140 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   }
 }
 
+// group_merge_kernel (group_attn.cu) for this kernel's layout: eight query rows of a block per
+// CTA, 16 threads each, which take every 16th quad of channels; a load of eight rows' quads is
+// 128 bytes in a row, and four neighbouring quads of the output fill a sector.
+constexpr int kMergeRows = 8;
+constexpr int kMaxWords = 8;  // (256 drafts)
+template <int D>
+__global__ void __launch_bounds__(128) group_tc_merge_kernel(
+    const float4* __restrict__ part_o, const float* __restrict__ part_ml, const int2* seg,
+    int blocks, int part_rows, int block_rows, int rblocks, const uint32_t* __restrict__ anc,
+    const uint8_t* __restrict__ vflag, const __nv_bfloat16* __restrict__ v_new, bool f8,
+    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int Hkv, int rep, int T, int words) {
+  constexpr int V = D / 64;  // quads of a thread: q0, q0 + 16
+  constexpr int U = 8;       // partial results whose loads are in flight together
+  const int lane = threadIdx.x & 31;
+  const int at_block = static_cast<int>(blockIdx.x) / blocks;  // (sequence, KV head, row block)
+  const int in_block = (static_cast<int>(blockIdx.x) - at_block * blocks) * kMergeRows + (lane & 7);
+  const int q0 = (threadIdx.x >> 5) * 4 + (lane >> 3);
+  const int plane = at_block / rblocks, rb = at_block - plane * rblocks;
+  const int b = plane / Hkv, g = plane - b * Hkv;
+  const int r = rb * block_rows + in_block, t = r / rep;
+  const bool live = r < T * rep && in_block < block_rows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  uint32_t flags[kMaxWords];  // drafts whose values are not finite
+#pragma unroll
+  for (int w = 0; w < kMaxWords; ++w) {
+    flags[w] = 0u;
+    if (w < words) {
+      const int j = 32 * w + lane;
+      flags[w] = __ballot_sync(0xffffffffu,
+                               j < T && vflag[static_cast<size_t>(plane) * T + j] != 0);
+    }
+  }
+  if (!live) return;
+  const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
+  const int2 at_seg = seg[at_block];
+  const int ns = ((mine[t >> 5] >> (t & 31)) & 1u) ? at_seg.y : 0;  // 0: padding
+  float m = -INFINITY, l = 0.f;
+  float4 acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < ns; s0 += U) {
+    float2 ml[U];
+    float4 o[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + u >= ns) continue;
+      const size_t slot = static_cast<size_t>(at_seg.x) + s0 + u;
+      ml[u] = *reinterpret_cast<const float2*>(part_ml + 2 * (slot * part_rows + in_block));
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        o[u][v] = part_o[(slot * (D / 4) + q0 + 16 * v) * part_rows + in_block];
+    }
+    float mx = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
+    // (one that saw nothing holds zeros, or NaN)
+    const float f = m == -INFINITY ? 1.f : ex2_approx(m - mx);
+    l *= f;
+    m = mx;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      acc[v] = make_float4(acc[v].x * f, acc[v].y * f, acc[v].z * f, acc[v].w * f);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float e = ml[u].x == -INFINITY ? 1.f : ex2_approx(ml[u].x - m);
+      l += e * ml[u].y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        acc[v].x += e * o[u][v].x;
+        acc[v].y += e * o[u][v].y;
+        acc[v].z += e * o[u][v].z;
+        acc[v].w += e * o[u][v].w;
+      }
+    }
+  }
+  const bool any = !(l <= 0.f);  // NaN stays
+  const float inv = any ? 1.f / l : 0.f;
+  const size_t row = (static_cast<size_t>(plane) * rep + r - t * rep) * T + t;  // [B, Hq, T]
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = 4 * (q0 + 16 * v);
+    float x[4] = {any ? acc[v].x * inv : 0.f, any ? acc[v].y * inv : 0.f,
+                  any ? acc[v].z * inv : 0.f, any ? acc[v].w * inv : 0.f};
+    if (ns > 0) {
+#pragma unroll
+      for (int w = 0; w < kMaxWords; ++w) {
+        if (w >= words) break;
+        for (uint32_t left = flags[w] & mine[w]; left != 0u; left &= left - 1u) {
+          const __nv_bfloat16* vn =
+              v_new + (static_cast<size_t>(plane) * T + 32 * w + __ffs(left) - 1) * D + c;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = __bfloat162float(vn[e]);
+            // (an e4m3 cache holds NaN for an infinity)
+            if (!isfinite(y)) x[e] += f8 ? __int_as_float(0x7fffffff) : y;
+          }
+        }
+      }
+    }
+    *reinterpret_cast<uint2*>(out + row * D + c) =
+        make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  }
+  if (lse != nullptr && q0 == 0)
+    lse[row] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D>
+cudaError_t launch_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new, void* out,
+                         float* lse, cudaStream_t stream) {
+  const int blocks = (a.plan.part_rows + kMergeRows - 1) / kMergeRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.Hkv * a.plan.rblocks * blocks), 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(
+      &cfg, group_tc_merge_kernel<D>, reinterpret_cast<const float4*>(a.part_o),
+      static_cast<const float*>(a.part_ml), static_cast<const int2*>(a.seg), blocks,
+      a.plan.part_rows, a.plan.block_rows, a.plan.rblocks, a.anc, vflag,
+      static_cast<const __nv_bfloat16*>(v_new), a.cache.k_scale != nullptr,
+      static_cast<__nv_bfloat16*>(out), lse, a.Hkv, a.Hq / a.Hkv, a.T, a.words);
+}
+
 template <int D, bool F8>
 cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   using C = Cfg<D, F8>;
   TParams p{};
-  p.q = static_cast<const uint16_t*>(a.q);
   p.q_factor = a.q_factor;
   p.anc = a.anc;
   p.line = group_line(a);
@@ -891,17 +1017,19 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.rep = a.Hq / a.Hkv;
   p.rblocks = a.plan.rblocks;
   p.part_rows = a.plan.part_rows;
+  const int rows = a.T * p.rep;
   p.pair = a.plan.block_rows == 256 ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
 
-  alignas(64) CUtensorMap tk, tv;
+  alignas(64) CUtensorMap tq, tk, tv;
   const int trows = paged ? ps : a.cache.Lmax;
   const int planes = paged ? a.cache.num_pages * a.Hkv : a.B * a.Hkv;
   const bool made = F8 ? make_tmap_u8_3d(&tk, a.cache.k, D, trows, planes, p.box_rows, false) &&
                              make_tmap_u8_3d(&tv, a.cache.v, D, trows, planes, p.box_rows, false)
                        : make_tmap_bf16_3d(&tk, a.cache.k, D, trows, planes, p.box_rows) &&
                              make_tmap_bf16_3d(&tv, a.cache.v, D, trows, planes, p.box_rows);
-  if (!made) return cudaErrorInvalidValue;
+  // (16-bit values, whichever: f16 for an 8-bit cache)
+  if (!made || !make_tmap_bf16_3d(&tq, a.q, D, rows, a.B * a.Hkv, BN)) return cudaErrorInvalidValue;
   static SmemLimitOnce smem_limit;
   cudaError_t e = smem_limit.set(group_tc_kernel<D, F8>, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -915,7 +1043,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.after_prep ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, group_tc_kernel<D, F8>, p, tk, tv);
+  return cudaLaunchKernelEx(&cfg, group_tc_kernel<D, F8>, p, tq, tk, tv);
 }
 
 }  // namespace
@@ -924,6 +1052,12 @@ cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream) {
   const bool f8 = a.cache.k_scale != nullptr;
   if (a.d == 64) return f8 ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
   return f8 ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);
+}
+
+cudaError_t launch_group_tc_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
+                                  void* out, float* lse, cudaStream_t stream) {
+  return a.d == 64 ? launch_merge<64>(a, vflag, v_new, out, lse, stream)
+                   : launch_merge<128>(a, vflag, v_new, out, lse, stream);
 }
 
 }  // namespace csattn

@@ -217,8 +217,9 @@ struct GroupPlan {
 // query t sees those in its bit mask anc[b, t] (words of 32 bits; drafts = 0: no such rows).
 struct GroupArgs {
   KvCache cache;
-  const void* q;         // [B, Hq, T, d] bf16; with q_factor f16 (query_to_f16, fp8.cuh)
-  const float* q_factor; // null, or [B, Hq, T]: an 8-bit cache's queries as launch_tree_prep
+  const void* q;         // [B, Hkv, T * Hq/Hkv, d] bf16, row t * Hq/Hkv + head of the group (T = 1:
+                         // [B, Hq, 1, d]); with q_factor f16 (query_to_f16, fp8.cuh)
+  const float* q_factor; // null, or one per row: an 8-bit cache's queries as launch_tree_prep
                          // leaves them
   const int32_t* lens;   // device [B]
   const uint32_t* anc;   // device [B, T, words]
@@ -231,7 +232,8 @@ struct GroupArgs {
   int min_len;           // lens[b] below it or above max_seq_len - drafts is an error (decode: 1)
   GroupPlan plan;
   int2* seg;             // [B * Hkv * rblocks] scratch
-  float* part_o;         // [pieces, subs, part_rows, d], pieces = grid + segments
+  float* part_o;         // [pieces, subs, part_rows, d], pieces = grid + segments; from
+                         // launch_group_tc [pieces, d / 4, part_rows, 4]
   float* part_ml;        // [pieces, subs, part_rows, 2]
   bool after_prep;       // launched behind launch_tree_prep (programmatic dependent launch)
   uint32_t* status;
@@ -250,6 +252,9 @@ cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream);
 // zeros) and are put into the outputs of the queries that see them here.
 cudaError_t launch_group_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
                                void* out, float* lse, cudaStream_t stream);
+// the same behind launch_group_tc
+cudaError_t launch_group_tc_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
+                               void* out, float* lse, cudaStream_t stream);
 
 // The work of a tree step ahead of its attention: checks lengths and parents, appends the
 // drafts' keys and values at rows L + t (keys rotated at L + depth), rotates the queries.
@@ -263,8 +268,8 @@ struct TreePrepArgs {
   int B, Hq, Hkv, Tn, d, max_seq_len;
   int rope;
   RopeTable theta;
-  void* q_rot;      // [B, Hq, Tn, d] bf16, or f16 for an 8-bit cache, then with
-  float* q_factor;  // [B, Hq, Tn]
+  void* q_rot;      // as GroupArgs::q: bf16, or f16 for an 8-bit cache, then with
+  float* q_factor;
   uint32_t* anc;    // [B, Tn, words]
   int32_t* lens;    // [B]: cache_lens, or -1 where a check failed
   uint8_t* vflag;   // [B, Hkv, Tn]

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
   if (rope != 0 && tid < D / 2)
     rope_cos_sin<false>(pos, theta.hi[tid], theta.lo[tid], s_cos[tid], s_sin[tid]);
   __syncthreads();
-  const int items = (Hq + 2 * Hkv) * G;
+  const int rep = Hq / Hkv, items = (Hq + 2 * Hkv) * G;
   for (int i0 = 0; i0 < items; i0 += kThreads) {  // (whole warps take part in the shuffles)
     const int i = i0 + tid;
     const bool live = i < items;
@@ -123,6 +123,9 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
                       pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
     }
     if (is_q) {
+      // the rows of a KV head's queries one behind another, draft by draft
+      const int kvh = g / rep;
+      const size_t q_row = (static_cast<size_t>(b) * Hkv + kvh) * Tn * rep + t * rep + g - kvh * rep;
       if constexpr (F8) {  // (query_to_f16 with the angles at hand)
         const int E = min(max(static_cast<int>(top >> 7), 15), 254);
         const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
@@ -131,11 +134,9 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
         hi = make_uint4(pack_f16x2(y[8] * f, y[9] * f), pack_f16x2(y[10] * f, y[11] * f),
                         pack_f16x2(y[12] * f, y[13] * f), pack_f16x2(y[14] * f, y[15] * f));
         if (c == 0)
-          q_factor[(static_cast<size_t>(b) * Hq + g) * Tn + t] =
-              __uint_as_float(static_cast<uint32_t>(E - 14) << 23);
+          q_factor[q_row] = __uint_as_float(static_cast<uint32_t>(E - 14) << 23);
       }
-      __nv_bfloat16* dst =
-          q_rot + ((static_cast<size_t>(b) * Hq + g) * Tn + t) * static_cast<size_t>(D);
+      __nv_bfloat16* dst = q_rot + q_row * D;
       *reinterpret_cast<uint4*>(dst + e0) = lo;
       *reinterpret_cast<uint4*>(dst + e1) = hi;
       continue;
