@@ -860,42 +860,49 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   }
 }
 
-// group_merge_kernel (group_attn.cu) for this kernel's layout: eight query rows of a block per
-// CTA, 16 threads each, which take every 16th quad of channels; a load of eight rows' quads is
-// 128 bytes in a row, and four neighbouring quads of the output fill a sector.
-constexpr int kMergeRows = 8;
+// group_merge_kernel (group_attn.cu) for this kernel's layout: a warp takes eight query rows and
+// 4 V quads of channels, so that its loads are 128 bytes in a row each and its output fills whole
+// sectors.  For many rows the instructions per row count, so V is 4; for few the latency, so V
+// is 1 and up to eight partial results are in flight (16384 rows of two to four: 80.8 against 90.7 us for the whole step with
+// V = 4; 256 rows of eight: 14.4 against 15.0 with V = 1).
 constexpr int kMaxWords = 8;  // (256 drafts)
-template <int D>
-__global__ void __launch_bounds__(128) group_tc_merge_kernel(
+template <int D, int V>
+struct MergeShape {
+  static constexpr int WARPS = D / 16 / V;  // of the same rows
+  static constexpr int GROUPS = WARPS < 4 ? 4 / WARPS : 1;
+  static constexpr int ROWS = 8 * GROUPS, THREADS = 32 * WARPS * GROUPS;
+};
+
+template <int D, int V>
+__global__ void __launch_bounds__(MergeShape<D, V>::THREADS) group_tc_merge_kernel(
     const float4* __restrict__ part_o, const float* __restrict__ part_ml, const int2* seg,
     int blocks, int part_rows, int block_rows, int rblocks, const uint32_t* __restrict__ anc,
     const uint8_t* __restrict__ vflag, const __nv_bfloat16* __restrict__ v_new, bool f8,
     __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int Hkv, int rep, int T, int words) {
-  constexpr int V = D / 64;  // quads of a thread: q0, q0 + 16
-  constexpr int U = 8;       // partial results whose loads are in flight together
-  const int lane = threadIdx.x & 31;
+  using S = MergeShape<D, V>;
+  constexpr int U = V == 1 ? 8 : 4;  // partial results whose loads are in flight together
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int at_block = static_cast<int>(blockIdx.x) / blocks;  // (sequence, KV head, row block)
-  const int in_block = (static_cast<int>(blockIdx.x) - at_block * blocks) * kMergeRows + (lane & 7);
-  const int q0 = (threadIdx.x >> 5) * 4 + (lane >> 3);
+  const int in_block = (static_cast<int>(blockIdx.x) - at_block * blocks) * S::ROWS +
+                       8 * (warp / S::WARPS) + (lane & 7);
+  const int quad = (warp % S::WARPS) * 4 * V + (lane >> 3);  // and quad + 4, ...
   const int plane = at_block / rblocks, rb = at_block - plane * rblocks;
   const int b = plane / Hkv, g = plane - b * Hkv;
-  const int r = rb * block_rows + in_block, t = r / rep;
-  const bool live = r < T * rep && in_block < block_rows;
+  const int r = rb * block_rows + in_block;
+  const bool live = r < T * rep && in_block < part_rows;
+  const int t = live ? r / rep : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  uint32_t flags[kMaxWords];  // drafts whose values are not finite
+  const int2 at_seg = seg[at_block];
+  const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
+  const uint32_t own = mine[t >> 5];
+  // (read ahead of the partial results, used behind them)
+  uint8_t odd[kMaxWords];
 #pragma unroll
   for (int w = 0; w < kMaxWords; ++w) {
-    flags[w] = 0u;
-    if (w < words) {
-      const int j = 32 * w + lane;
-      flags[w] = __ballot_sync(0xffffffffu,
-                               j < T && vflag[static_cast<size_t>(plane) * T + j] != 0);
-    }
+    odd[w] = 0;
+    if (w < words && 32 * w + lane < T) odd[w] = vflag[static_cast<size_t>(plane) * T + 32 * w + lane];
   }
-  if (!live) return;
-  const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
-  const int2 at_seg = seg[at_block];
-  const int ns = ((mine[t >> 5] >> (t & 31)) & 1u) ? at_seg.y : 0;  // 0: padding
+  const int ns = live && ((own >> (t & 31)) & 1u) ? at_seg.y : 0;  // 0: padding
   float m = -INFINITY, l = 0.f;
   float4 acc[V];
 #pragma unroll
@@ -906,14 +913,12 @@ __global__ void __launch_bounds__(128) group_tc_merge_kernel(
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s0 + u >= ns) continue;
       const size_t slot = static_cast<size_t>(at_seg.x) + s0 + u;
       ml[u] = *reinterpret_cast<const float2*>(part_ml + 2 * (slot * part_rows + in_block));
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        o[u][v] = part_o[(slot * (D / 4) + q0 + 16 * v) * part_rows + in_block];
+        o[u][v] = part_o[(slot * (D / 4) + quad + 4 * v) * part_rows + in_block];
     }
     float mx = m;
 #pragma unroll
@@ -927,55 +932,58 @@ __global__ void __launch_bounds__(128) group_tc_merge_kernel(
       acc[v] = make_float4(acc[v].x * f, acc[v].y * f, acc[v].z * f, acc[v].w * f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (s0 + u >= ns) break;
       const float e = ml[u].x == -INFINITY ? 1.f : ex2_approx(ml[u].x - m);
       l += e * ml[u].y;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        acc[v].x += e * o[u][v].x;
-        acc[v].y += e * o[u][v].y;
-        acc[v].z += e * o[u][v].z;
-        acc[v].w += e * o[u][v].w;
-      }
+      for (int v = 0; v < V; ++v)
+        acc[v] = make_float4(acc[v].x + e * o[u][v].x, acc[v].y + e * o[u][v].y,
+                             acc[v].z + e * o[u][v].z, acc[v].w + e * o[u][v].w);
     }
   }
   const bool any = !(l <= 0.f);  // NaN stays
   const float inv = any ? 1.f / l : 0.f;
-  const size_t row = (static_cast<size_t>(plane) * rep + r - t * rep) * T + t;  // [B, Hq, T]
+  float x[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = 4 * (q0 + 16 * v);
-    float x[4] = {any ? acc[v].x * inv : 0.f, any ? acc[v].y * inv : 0.f,
-                  any ? acc[v].z * inv : 0.f, any ? acc[v].w * inv : 0.f};
-    if (ns > 0) {
+    x[v][0] = any ? acc[v].x * inv : 0.f;
+    x[v][1] = any ? acc[v].y * inv : 0.f;
+    x[v][2] = any ? acc[v].z * inv : 0.f;
+    x[v][3] = any ? acc[v].w * inv : 0.f;
+  }
 #pragma unroll
-      for (int w = 0; w < kMaxWords; ++w) {
-        if (w >= words) break;
-        for (uint32_t left = flags[w] & mine[w]; left != 0u; left &= left - 1u) {
-          const __nv_bfloat16* vn =
-              v_new + (static_cast<size_t>(plane) * T + 32 * w + __ffs(left) - 1) * D + c;
+  for (int w = 0; w < kMaxWords; ++w) {
+    const uint32_t flags = __ballot_sync(0xffffffffu, odd[w] != 0);
+    if (flags == 0u || ns == 0) continue;
+    for (uint32_t left = flags & mine[w]; left != 0u; left &= left - 1u) {
+      const __nv_bfloat16* vn =
+          v_new + (static_cast<size_t>(plane) * T + 32 * w + __ffs(left) - 1) * D + 4 * quad;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = __bfloat162float(vn[e]);
-            // (an e4m3 cache holds NaN for an infinity)
-            if (!isfinite(y)) x[e] += f8 ? __int_as_float(0x7fffffff) : y;
-          }
-        }
+      for (int e = 0; e < 4 * V; ++e) {
+        const float y = __bfloat162float(vn[16 * (e / 4) + e % 4]);
+        // (an e4m3 cache holds NaN for an infinity)
+        if (!isfinite(y)) x[e / 4][e % 4] += f8 ? __int_as_float(0x7fffffff) : y;
       }
     }
-    *reinterpret_cast<uint2*>(out + row * D + c) =
-        make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
   }
-  if (lse != nullptr && q0 == 0)
+  if (!live) return;
+  const size_t row = (static_cast<size_t>(plane) * rep + r - t * rep) * T + t;  // [B, Hq, T]
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    *reinterpret_cast<uint2*>(out + row * D + 4 * quad + 16 * v) =
+        make_uint2(pack_bf16x2(x[v][0], x[v][1]), pack_bf16x2(x[v][2], x[v][3]));
+  if (lse != nullptr && quad == 0)
     lse[row] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D>
+template <int D, int V>
 cudaError_t launch_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new, void* out,
                          float* lse, cudaStream_t stream) {
-  const int blocks = (a.plan.part_rows + kMergeRows - 1) / kMergeRows;
+  using S = MergeShape<D, V>;
+  const int blocks = (a.plan.part_rows + S::ROWS - 1) / S::ROWS;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.Hkv * a.plan.rblocks * blocks), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.blockDim = dim3(S::THREADS, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -983,7 +991,7 @@ cudaError_t launch_merge(const GroupArgs& a, const uint8_t* vflag, const void* v
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(
-      &cfg, group_tc_merge_kernel<D>, reinterpret_cast<const float4*>(a.part_o),
+      &cfg, group_tc_merge_kernel<D, V>, reinterpret_cast<const float4*>(a.part_o),
       static_cast<const float*>(a.part_ml), static_cast<const int2*>(a.seg), blocks,
       a.plan.part_rows, a.plan.block_rows, a.plan.rblocks, a.anc, vflag,
       static_cast<const __nv_bfloat16*>(v_new), a.cache.k_scale != nullptr,
@@ -1056,8 +1064,11 @@ cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_group_tc_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
                                   void* out, float* lse, cudaStream_t stream) {
-  return a.d == 64 ? launch_merge<64>(a, vflag, v_new, out, lse, stream)
-                   : launch_merge<128>(a, vflag, v_new, out, lse, stream);
+  if (a.B * a.Hq * a.T <= 4096)
+    return a.d == 64 ? launch_merge<64, 1>(a, vflag, v_new, out, lse, stream)
+                     : launch_merge<128, 1>(a, vflag, v_new, out, lse, stream);
+  return a.d == 64 ? launch_merge<64, 4>(a, vflag, v_new, out, lse, stream)
+                   : launch_merge<128, 4>(a, vflag, v_new, out, lse, stream);
 }
 
 }  // namespace csattn

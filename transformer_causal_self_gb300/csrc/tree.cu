@@ -47,8 +47,8 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int Tn, int w
   return true;
 }
 
-// One CTA per (draft, sequence): the masks are worked out by every CTA (a few rounds in
-// shared memory), then the draft's rows, 16 channels per thread: keys rotated at its
+// One CTA per (draft, sequence), or several: the masks are worked out by every CTA (a few rounds
+// in shared memory), then the draft's rows, 16 channels per thread: keys rotated at its
 // position and values to the cache (bf16 or e4m3), queries rotated into q_rot.  A few
 // hundred KB at most: bound by launch and memory latency.
 template <int D, bool F8>
@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     void* __restrict__ v_cache, uint8_t* __restrict__ k_scale, uint8_t* __restrict__ v_scale,
     const int32_t* __restrict__ cache_lens, const int32_t* __restrict__ parents, CacheRows rows,
     int Hq, int Tn, int max_seq_len, int rope, RopeTable theta, __nv_bfloat16* __restrict__ q_rot,
-    float* __restrict__ q_factor, uint32_t* __restrict__ anc, int32_t* __restrict__ lens, uint8_t* __restrict__ vflag, int words,
-    uint32_t* status) {
+    float* __restrict__ q_factor, uint32_t* __restrict__ anc, int32_t* __restrict__ lens,
+    uint8_t* __restrict__ vflag, int words, uint32_t* status) {
   constexpr int G = D / 16;
   __shared__ uint32_t s_anc[kThreads][kWords];
   __shared__ int s_up[kThreads];
@@ -67,24 +67,44 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
   const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, Hkv = rows.Hkv;
   // the attention kernel may be scheduled; it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int rep = Hq / Hkv, items = (Hq + 2 * Hkv) * G, step = gridDim.z * kThreads;
+  // 16 channels of a row, each thread's first while the masks are worked out
+  auto load = [&](int i, uint4* lo, uint4* hi) {
+    *lo = *hi = make_uint4(0u, 0u, 0u, 0u);
+    if (i >= items) return;
+    const int head = i / G, c = i % G;
+    const bool is_q = head < Hq, is_v = head >= Hq + Hkv;
+    int e0, e1;
+    rope_piece(is_v ? 0 : rope, D / 2, c, &e0, &e1);
+    const __nv_bfloat16* x =
+        (is_q ? q_new : (is_v ? v_new : k_new)) +
+        ((static_cast<size_t>(b) * (is_q ? Hq : Hkv) + (is_q ? head : head - Hq - (is_v ? Hkv : 0))) *
+             Tn + t) * static_cast<size_t>(D);
+    *lo = *reinterpret_cast<const uint4*>(x + e0);
+    *hi = *reinterpret_cast<const uint4*>(x + e1);
+  };
   const int L = cache_lens[b];
-  const bool fine = tree_masks(parents + static_cast<size_t>(b) * Tn, Tn, words, s_anc, s_up) &&
-                    L >= 0 && L <= max_seq_len - Tn;
-  if (tid == 0 && t == 0) {
+  uint4 lo, hi;
+  load(blockIdx.z * kThreads + tid, &lo, &hi);
+  const bool fits = L >= 0 && L <= max_seq_len - Tn;
+  const long long row0 = fits ? rows.at(b, 0, L + t) : -1;  // of KV head 0
+  const bool fine =
+      tree_masks(parents + static_cast<size_t>(b) * Tn, Tn, words, s_anc, s_up) && fits;
+  if (tid == 0 && t == 0 && blockIdx.z == 0) {
     lens[b] = fine ? L : -1;
     if (!fine) atomicOr(status, kStatusDeviceArg);
   }
   if (!fine) return;  // the sequence's cache is left as it was
   __syncthreads();
-  if (tid < words) anc[(static_cast<size_t>(b) * Tn + t) * words + tid] = s_anc[t][tid];
+  if (blockIdx.z == 0 && tid < words) anc[(static_cast<size_t>(b) * Tn + t) * words + tid] = s_anc[t][tid];
   int depth = -1;
   for (int w = 0; w < words; ++w) depth += __popc(s_anc[t][w]);
   const int pos = L + max(depth, 0);  // (padding is written like a first token, never seen)
   if (rope != 0 && tid < D / 2)
     rope_cos_sin<false>(pos, theta.hi[tid], theta.lo[tid], s_cos[tid], s_sin[tid]);
   __syncthreads();
-  const int rep = Hq / Hkv, items = (Hq + 2 * Hkv) * G;
-  for (int i0 = 0; i0 < items; i0 += kThreads) {  // (whole warps take part in the shuffles)
+  // (whole warps take part in the shuffles)
+  for (int i0 = blockIdx.z * kThreads; i0 < items; i0 += step) {
     const int i = i0 + tid;
     const bool live = i < items;
     const int head = live ? i / G : 0, c = i % G;
@@ -93,14 +113,7 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     const int layout = is_v ? 0 : rope;
     int e0, e1;
     rope_piece(layout, D / 2, c, &e0, &e1);
-    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-    if (live) {
-      const __nv_bfloat16* x =
-          (is_q ? q_new : (is_v ? v_new : k_new)) +
-          ((static_cast<size_t>(b) * (is_q ? Hq : Hkv) + g) * Tn + t) * static_cast<size_t>(D);
-      lo = *reinterpret_cast<const uint4*>(x + e0);
-      hi = *reinterpret_cast<const uint4*>(x + e1);
-    }
+    if (i0 >= step) load(i, &lo, &hi);
     bool bad;
     const uint32_t top = row_absmax<G>(lo, hi, &bad);
     if (!live) continue;  // (no shuffle below)
@@ -142,11 +155,12 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
       continue;
     }
     if (is_v && c == 0) vflag[(static_cast<size_t>(b) * Hkv + g) * Tn + t] = bad ? 1 : 0;
-    const long long row = rows.at(b, g, L + t);
-    if (row < 0) {
+    if (row0 < 0) {  // a page outside the pool
       if (c == 0) atomicOr(status, kStatusDeviceArg);
       continue;
     }
+    const long long row =
+        row0 + static_cast<long long>(g) * (rows.block_table != nullptr ? rows.page_size : rows.Lmax);
     if constexpr (F8) {
       uint8_t* dst = static_cast<uint8_t*>(is_v ? v_cache : k_cache) + row * D;
       *reinterpret_cast<uint2*>(dst + e0) =
@@ -263,7 +277,10 @@ cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
   const bool f8 = a.cache.k_scale != nullptr;
   auto* kernel = a.d == 128 ? (f8 ? tree_prep_kernel<128, true> : tree_prep_kernel<128, false>)
                             : (f8 ? tree_prep_kernel<64, true> : tree_prep_kernel<64, false>);
-  kernel<<<dim3(a.Tn, a.B), kThreads, 0, stream>>>(
+  // a draft's rows shared by several CTAs while these are all resident at once
+  const int parts = ((a.Hq + 2 * a.Hkv) * (a.d / 16) + kThreads - 1) / kThreads;
+  const bool few = static_cast<long long>(a.Tn) * a.B * parts <= 2 * 152 && parts <= 65535;
+  kernel<<<dim3(a.Tn, a.B, few ? parts : 1), kThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(a.q_new), static_cast<const __nv_bfloat16*>(a.k_new),
       static_cast<const __nv_bfloat16*>(a.v_new), a.cache.k, a.cache.v,
       static_cast<uint8_t*>(a.cache.k_scale), static_cast<uint8_t*>(a.cache.v_scale),
