@@ -497,9 +497,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;
     constexpr int G = D / 16;                  // 16-channel pieces of a row
     const uint32_t raw0 = smem_u32(sRaw), kv0 = smem_u32(sKV);
+    // The thread's piece: column c of row r0.  Eight lanes share a wavefront, and a row's pieces
+    // c and c + 4 go to the same banks (to the tile's two halves); so at 128 channels two rows
+    // change places in their upper four pieces, and odd rows' chunks lie between even ones'.
+    const int c = tid % G, r0 = D == 128 ? 2 * (tid >> 4) + (((tid >> 2) ^ (tid >> 3)) & 1) : tid / G;
     uint32_t to0, to1;                         // where the thread's two chunks go in a tile
     {
-      const int r0 = tid / G, c = tid % G;
       const uint32_t at = (c >> 2) * (BN * 128) + r0 * 128;
       to0 = at + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
       to1 = at + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
@@ -588,9 +591,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
         if (!ok) break;
         const bool edge = key0 + BN > min(w.L, w.k_end);
-        // piece i of the thread is row i * (128 / G) + tid / G
+        // piece i of the thread is row i * (128 / G) + r0
         constexpr int kRowStep = 128 / G;  // (a multiple of 8: the swizzle stays)
-        const uint32_t src = raw0 + rs * C::RAW + 16 * tid;
+        const uint32_t src = raw0 + rs * C::RAW + r0 * D + 16 * c;
         const uint32_t dst0 = kv0 + s * C::TILE + to0, dst1 = kv0 + s * C::TILE + to1;
 #pragma unroll 1
         for (int i0 = 0; i0 < G; i0 += 4) {
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           if (edge) {  // rows past the end: zeros; the drafts' values: if finite
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = key0 + (i0 + i) * kRowStep + tid / G;
+              const int r = key0 + (i0 + i) * kRowStep + r0;
               if (r >= w.k_end) x[i] = make_uint4(0u, 0u, 0u, 0u);
               if (v == 1 && r >= w.L)
                 x[i] = make_uint4(finite_e4m3x4(x[i].x), finite_e4m3x4(x[i].y),
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t mm = __shfl_sync(0xffffffffu, factor, (32 / G) * (i0 + i) + lane / G);
+            const uint32_t mm = __shfl_sync(0xffffffffu, factor, (32 / G) * (i0 + i) + r0 % (32 / G));
             const uint4 lo = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].x), mm),
                                         hmul2(e4m3x2_hi_to_f16x2(x[i].x), mm),
                                         hmul2(e4m3x2_to_f16x2(x[i].y), mm),
@@ -863,8 +866,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 // group_merge_kernel (group_attn.cu) for this kernel's layout: a warp takes eight query rows and
 // 4 V quads of channels, so that its loads are 128 bytes in a row each and its output fills whole
 // sectors.  For many rows the instructions per row count, so V is 4; for few the latency, so V
-// is 1 and up to eight partial results are in flight (16384 rows of two to four: 80.8 against 90.7 us for the whole step with
-// V = 4; 256 rows of eight: 14.4 against 15.0 with V = 1).
+// is 1 and up to eight partial results are in flight (the whole step with 16384 rows of two to
+// four: 80.8 us against 90.7 with V = 1; 256 rows of eight: 14.4 against 15.0 with V = 2).
 constexpr int kMaxWords = 8;  // (256 drafts)
 template <int D, int V>
 struct MergeShape {
