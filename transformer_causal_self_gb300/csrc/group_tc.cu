@@ -236,14 +236,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   float2* s_tile = s_ml + 128;  // e4m3 [8]: 2^(E_k - 7), E_v of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
-      mbar_init(&o_empty[x], 4);
+      mbar_init(&o_empty[x], pair ? 4 : 8);
     }
     mbar_init(teardown, 1);
     mbar_init(q_full, 1);
@@ -259,26 +257,25 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
     *abort_flag = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  GroupPiece pc = group_start(p.line, p.status, -1);
-  if (pc.n == 0) return;
-  const int step = pair ? 1 : 2;  // between a stream's tiles
   if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  GroupPiece pc = group_start(p.line, p.status, -1);  // (n = 0: every loop below ends at once)
+  const int step = pair ? 1 : 2;  // between a stream's tiles
 
   if (warp >= 8 && warp < 12) {
    if constexpr (F8) regs_dec<64>();
    if (warp == kWarpProducer) {
     // ------------------------------------------------------------ TMA producer
     // fills K_0, V_0, K_1, V_1, ...; lane i copies box i of a tile (see group_attn.cu)
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
     const CacheRows& R = p.rows;
     const int nbox = BN / p.box_rows, r0 = lane * p.box_rows;
     const uint32_t depth = F8 ? C::NRAW : NS;
@@ -790,68 +787,79 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       tile0 += w.n;
+      // Partial result: R, l and O, relative to 2^R; four channels of all rows together, so that
+      // a warp's lanes, which hold a row each, store 512 bytes in a row.  With one query tile
+      // stream 0 adds stream 1's sums to its own and hands back the factors of the two outputs;
+      // then each stream's warps write half of the channels.
+      const bool two = !pair && w.n > 1;  // both streams had tiles of this row
+      const float o_scale = F8 ? 1.f / 16384.f : 1.f;  // 2^-7 of w, 2^-7 of V16
+      float f0 = o_scale, f1 = 0.f;
       if (!pair) {
         if (x == 1) s_ml[row] = make_float2(R, l);
         asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (x == 0) {
+          if (two) {
+            const float2 other = s_ml[row];
+            const float m = fmaxf(R, other.x);
+            // (a stream that saw nothing holds zeros, or NaN)
+            const float e0 = R == -INFINITY ? 1.f : ex2_approx(R - m);
+            const float e1 = other.x == -INFINITY ? 1.f : ex2_approx(other.x - m);
+            l = l * e0 + other.y * e1;
+            R = m;
+            f0 = o_scale * e0;
+            f1 = o_scale * e1;
+          }
+          s_ml[row] = make_float2(f0, f1);
+        }
+        asm volatile("bar.sync 5, 256;" ::: "memory");
+        if (x == 1) {
+          const float2 f = s_ml[row];
+          f0 = f.x;
+          f1 = f.y;
+        }
       }
-      // partial result: R, l and O, relative to 2^R; four channels of all rows together, so that
-      // a warp's lanes, which hold a row each, store 512 bytes in a row
-      const bool two = !pair && w.n > 1;  // both streams had tiles of this row
-      if (pair || x == 0) {
-        ok = ok && warp_wait(&o_full[x], done[0] & 1, abort_flag, p.status) &&
-             (!two || warp_wait(&o_full[1], done[1] & 1, abort_flag, p.status));
-        if (ok) {
-          tc_fence_after();
-          if (warp_live) {
-            const float o_scale = F8 ? 1.f / 16384.f : 1.f;  // 2^-7 of w, 2^-7 of V16
-            float f0 = o_scale, f1 = 0.f;
-            if (two) {
-              const float2 other = s_ml[row];
-              const float m = fmaxf(R, other.x);
-              // (a stream that saw nothing holds zeros, or NaN)
-              const float e0 = R == -INFINITY ? 1.f : ex2_approx(R - m);
-              const float e1 = other.x == -INFINITY ? 1.f : ex2_approx(other.x - m);
-              l = l * e0 + other.y * e1;
-              R = m;
-              f0 = o_scale * e0;
-              f1 = o_scale * e1;
-            }
-            const size_t at = slot * p.part_rows + (pair ? x * 128 : 0) + row;
-            float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * p.part_rows +
-                          (pair ? x * 128 : 0) + row;
+      const int own = pair ? x : 0;  // the (first) stream whose output this is
+      ok = ok && warp_wait(&o_full[own], done[0] & 1, abort_flag, p.status) &&
+           (!two || warp_wait(&o_full[1], done[1] & 1, abort_flag, p.status));
+      if (ok) {
+        tc_fence_after();
+        if (warp_live) {
+          const size_t at = slot * p.part_rows + 128 * own + row;
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * p.part_rows +
+                        128 * own + row;
+          const uint32_t t0 = tmem + lane_off + 256u + static_cast<uint32_t>(D * own);
+          const int i1 = pair || x == 1 ? D / 32 : D / 64;
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t r[32];
-              tmem_ld32_sync(tO + 32u * i, r);
-              float o[32];
+          for (int i = pair || x == 0 ? 0 : D / 64; i < i1; ++i) {
+            uint32_t r[32];
+            tmem_ld32_sync(t0 + 32u * i, r);
+            float o[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * f0;
-              if (two) {
-                tmem_ld32_sync(tO + D + 32u * i, r);
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * f0;
+            if (two) {
+              tmem_ld32_sync(t0 + D + 32u * i, r);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), f1, o[e]);
-              }
-              if (live) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  dst[static_cast<size_t>(8 * i + e / 4) * p.part_rows] =
-                      make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-              }
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), f1, o[e]);
             }
-            if (live) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(R, l);
+            if (live) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                dst[static_cast<size_t>(8 * i + e / 4) * p.part_rows] =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&o_empty[x]);
-            if (two) mbar_arrive(&o_empty[1]);
-          }
+          if (live && (pair || x == 0))
+            *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(R, l);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&o_empty[own]);
+          if (two) mbar_arrive(&o_empty[1]);
         }
       }
       ++done[0];
       done[1] += two || pair;
-      // (stream 1's next sums go to s_ml only after stream 0 has read these)
-      if (!pair) asm volatile("bar.sync 5, 256;" ::: "memory");
     }
   }
 

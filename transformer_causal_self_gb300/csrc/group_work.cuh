@@ -65,10 +65,11 @@ __device__ __forceinline__ GroupPiece group_start(const GroupLine& g, uint32_t* 
                                                   int reported) {
   const int lane = threadIdx.x & 31;
   const bool tell = blockIdx.x == 0 && threadIdx.x < 32;
-  unsigned sum = 0;
+  unsigned sum = 0, first = 0;  // first: the tiles of sequence `lane`
   for (int b = lane; b < g.B; b += 32) {
     const int L = g.lens[b], t = g.tiles(L);
     sum += t;
+    if (b == lane) first = t;
     if (tell && t == 0) {
       if ((L < g.min_len || L > g.max_len) && L != reported) atomicOr(status, kStatusDeviceArg);
       for (int h = 0; h < g.heads; ++h) g.seg[b * g.heads + h] = make_int2(0, 0);
@@ -84,7 +85,7 @@ __device__ __forceinline__ GroupPiece group_start(const GroupLine& g, uint32_t* 
   unsigned before = 0;
   for (int b0 = 0;; b0 += 32) {
     const int b = b0 + lane;
-    const unsigned t = b < g.B ? g.tiles(g.lens[b]) : 0;
+    const unsigned t = b0 == 0 ? first : (b < g.B ? g.tiles(g.lens[b]) : 0);
     unsigned upto = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
