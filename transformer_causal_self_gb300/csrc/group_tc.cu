@@ -873,10 +873,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 
 // group_merge_kernel (group_attn.cu) for this kernel's layout: a warp takes eight query rows and
 // 4 V quads of channels, so that its loads are 128 bytes in a row each and its output fills whole
-// sectors.  For many rows the instructions per row count, so V is 4; for few the latency, so V
-// is 1 and up to eight partial results are in flight (the whole step with 16384 rows of two to
-// four: 80.8 us against 90.7 with V = 1; 256 rows of eight: 14.4 against 15.0 with V = 2).
-constexpr int kMaxWords = 8;  // (256 drafts)
+// sectors.  For many rows the instructions per row and the registers count (all CTAs resident at
+// once hide the three loads that follow one another), so V is 2 with three partial results in
+// flight; for few rows the latency, so V is 1 with eight.  The whole step with 16384 rows of two
+// to four: 74.3 us (V = 2, 3 in flight), 75-76 (2 or 4 in flight; V = 4), 91 (V = 1); with 256
+// rows of eight: 13.4 us with V = 1, 14 with V = 2.
 template <int D, int V>
 struct MergeShape {
   static constexpr int WARPS = D / 16 / V;  // of the same rows
@@ -891,7 +892,7 @@ __global__ void __launch_bounds__(MergeShape<D, V>::THREADS) group_tc_merge_kern
     const uint8_t* __restrict__ vflag, const __nv_bfloat16* __restrict__ v_new, bool f8,
     __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int Hkv, int rep, int T, int words) {
   using S = MergeShape<D, V>;
-  constexpr int U = V == 1 ? 8 : 4;  // partial results whose loads are in flight together
+  constexpr int U = V == 1 ? 8 : 3;  // partial results whose loads are in flight together
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int at_block = static_cast<int>(blockIdx.x) / blocks;  // (sequence, KV head, row block)
   const int in_block = (static_cast<int>(blockIdx.x) - at_block * blocks) * S::ROWS +
@@ -906,13 +907,8 @@ __global__ void __launch_bounds__(MergeShape<D, V>::THREADS) group_tc_merge_kern
   const int2 at_seg = seg[at_block];
   const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
   const uint32_t own = mine[t >> 5];
-  // (read ahead of the partial results, used behind them)
-  uint8_t odd[kMaxWords];
-#pragma unroll
-  for (int w = 0; w < kMaxWords; ++w) {
-    odd[w] = 0;
-    if (w < words && 32 * w + lane < T) odd[w] = vflag[static_cast<size_t>(plane) * T + 32 * w + lane];
-  }
+  bool odd = false;  // does any draft have values that are not finite?
+  for (int j = lane; j < T; j += 32) odd |= vflag[static_cast<size_t>(plane) * T + j] != 0;
   const int ns = live && ((own >> (t & 31)) & 1u) ? at_seg.y : 0;  // 0: padding
   float m = -INFINITY, l = 0.f;
   float4 acc[V];
@@ -962,18 +958,20 @@ __global__ void __launch_bounds__(MergeShape<D, V>::THREADS) group_tc_merge_kern
     x[v][2] = any ? acc[v].z * inv : 0.f;
     x[v][3] = any ? acc[v].w * inv : 0.f;
   }
+  if (__any_sync(0xffffffffu, odd)) {
+    for (int w = 0; w < words; ++w) {
+      const int j = 32 * w + lane;
+      const uint32_t flags = __ballot_sync(
+          0xffffffffu, j < T && vflag[static_cast<size_t>(plane) * T + j] != 0);
+      for (uint32_t left = ns > 0 ? flags & mine[w] : 0u; left != 0u; left &= left - 1u) {
+        const __nv_bfloat16* vn =
+            v_new + (static_cast<size_t>(plane) * T + 32 * w + __ffs(left) - 1) * D + 4 * quad;
 #pragma unroll
-  for (int w = 0; w < kMaxWords; ++w) {
-    const uint32_t flags = __ballot_sync(0xffffffffu, odd[w] != 0);
-    if (flags == 0u || ns == 0) continue;
-    for (uint32_t left = flags & mine[w]; left != 0u; left &= left - 1u) {
-      const __nv_bfloat16* vn =
-          v_new + (static_cast<size_t>(plane) * T + 32 * w + __ffs(left) - 1) * D + 4 * quad;
-#pragma unroll
-      for (int e = 0; e < 4 * V; ++e) {
-        const float y = __bfloat162float(vn[16 * (e / 4) + e % 4]);
-        // (an e4m3 cache holds NaN for an infinity)
-        if (!isfinite(y)) x[e / 4][e % 4] += f8 ? __int_as_float(0x7fffffff) : y;
+        for (int e = 0; e < 4 * V; ++e) {
+          const float y = __bfloat162float(vn[16 * (e / 4) + e % 4]);
+          // (an e4m3 cache holds NaN for an infinity)
+          if (!isfinite(y)) x[e / 4][e % 4] += f8 ? __int_as_float(0x7fffffff) : y;
+        }
       }
     }
   }
@@ -1078,8 +1076,8 @@ cudaError_t launch_group_tc_merge(const GroupArgs& a, const uint8_t* vflag, cons
   if (a.B * a.Hq * a.T <= 4096)
     return a.d == 64 ? launch_merge<64, 1>(a, vflag, v_new, out, lse, stream)
                      : launch_merge<128, 1>(a, vflag, v_new, out, lse, stream);
-  return a.d == 64 ? launch_merge<64, 4>(a, vflag, v_new, out, lse, stream)
-                   : launch_merge<128, 4>(a, vflag, v_new, out, lse, stream);
+  return a.d == 64 ? launch_merge<64, 2>(a, vflag, v_new, out, lse, stream)
+                   : launch_merge<128, 2>(a, vflag, v_new, out, lse, stream);
 }
 
 }  // namespace csattn
