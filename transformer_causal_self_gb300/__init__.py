@@ -8,6 +8,7 @@ if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -662,18 +663,27 @@ def _device_of(name: str, t: torch.Tensor, ndim: int) -> int:
     return dev
 
 
-# the current stream's handle without a Stream object around it
+# the current device and its current stream's handle, without the objects around them (a call has
+# a tensor on the device, so CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+def _used_on(t: torch.Tensor, stream) -> torch.Tensor:
     """An output or workspace of a call on `stream` (None: the current one)."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
     if stream is not None:  # not handed out again before that stream's work is done
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                        torch.cuda.ExternalStream(_stream_handle(stream), device=dev))
+                        torch.cuda.ExternalStream(_stream_handle(stream), device=t.device))
     return t
+
+
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+    return _used_on(torch.empty(shape, dtype=dtype, device=dev), stream)
+
+
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    return _used_on(torch.empty_like(t), stream)
 
 
 # Workspaces of calls that bring none are kept, one per thread and stream: calls of one thread on
@@ -688,20 +698,22 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: int, stream):
     if given is not None:
         if given.get_device() != dev or not given.is_contiguous():
             raise ValueError(f"workspace: must be contiguous on cuda:{dev}")
-    elif (stream is None and 0 < need <= _KEPT_BYTES and torch.cuda.current_device() == dev
+    elif (stream is None and 0 < need <= _KEPT_BYTES and _current_device() == dev
           and not torch.cuda.is_current_stream_capturing()):
         kept = _kept.__dict__
         key = (dev, _raw_stream(dev))
-        given = kept.get(key)
-        if given is None or given.numel() < need:
-            given = kept[key] = torch.empty((need,), dtype=torch.uint8, device=dev)
+        held = kept.get(key)
+        if held is None or held[2] < need:
+            given = torch.empty((need,), dtype=torch.uint8, device=dev)
+            held = kept[key] = given, given.data_ptr(), need
+        return held
     else:
         given = _empty((max(need, 16),), torch.uint8, dev, stream)
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 def _run(dev: int, fn, *args) -> None:
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -830,10 +842,12 @@ def cache_read_fp8_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: 
                      v_scale, block_table, seq_lens, k_out, v_out, stream)
 
 
+@functools.lru_cache(maxsize=1024)  # (a call costs as much as the checks of three tensors)
 def decode_fp8_workspace_size(B, Hq, Hkv, Lmax, d, num_splits: int = 0) -> int:
     return int(load_library().csattn_decode_fp8_workspace_size(B, Hq, Hkv, Lmax, d, num_splits))
 
 
+@functools.lru_cache(maxsize=1024)
 def tree_workspace_size(B, Hq, Hkv, Tn, Lmax, d, num_splits: int = 0) -> int:
     return int(load_library().csattn_tree_workspace_size(B, Hq, Hkv, Tn, Lmax, d, num_splits))
 
@@ -850,10 +864,10 @@ def _decode_fp8(fn, q, k, v, k_scale, v_scale, block_table, seq_lens, out, rope_
     if cshape[3] != d:
         raise ValueError("q and the cache differ in head size")
     if out is None:
-        out = _empty(shape, torch.bfloat16, dev, stream)
+        out = _like(q, stream)
     if max_seq_len is None:
         max_seq_len = rows
-    need = 0 if workspace is not None else load_library().csattn_decode_fp8_workspace_size(
+    need = 0 if workspace is not None else decode_fp8_workspace_size(
         B, Hq, Hkv, max_seq_len, d, num_splits)
     workspace, wp, wn = _workspace(workspace, need, dev, stream)
     _run(dev, fn, _ptr("q", q, shape, _BF16, dev), *cache, *table,
@@ -908,10 +922,10 @@ def _tree_step(fn, q_new, k_new, v_new, k, v, k_scale, v_scale, block_table, cac
         raise ValueError("q_new and the cache differ in head size")
     kshape = (B, Hkv, Tn, d)
     if out is None:
-        out = _empty(qshape, torch.bfloat16, dev, stream)
+        out = _like(q_new, stream)
     if max_seq_len is None:
         max_seq_len = rows
-    need = 0 if workspace is not None else load_library().csattn_tree_workspace_size(
+    need = 0 if workspace is not None else tree_workspace_size(
         B, Hq, Hkv, Tn, max_seq_len, d, num_splits)
     workspace, wp, wn = _workspace(workspace, need, dev, stream)
     _run(dev, fn, _ptr("q_new", q_new, qshape, _BF16, dev),
