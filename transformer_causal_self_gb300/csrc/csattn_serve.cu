@@ -140,8 +140,9 @@ GroupPlan plan_for(int B, int Hkv, int rows, bool tc, bool f8, int max_seq_len, 
     p.least_tiles = tc ? 1 : 2;
     const long long tiles = (max_seq_len + p.unit - 1) / p.unit;
     const long long line = tiles * B * Hkv * p.rblocks;
+    const int resident = kSms * (tc ? 1 : (f8 ? 3 : 2));
     p.most_grid = p.grid = static_cast<int>(
-        std::min<long long>(kSms * (tc ? 1 : (f8 ? 3 : 2)), (line + p.least_tiles - 1) / p.least_tiles));
+        std::min<long long>(resident, (line + p.least_tiles - 1) / p.least_tiles));
   }
   return p;
 }

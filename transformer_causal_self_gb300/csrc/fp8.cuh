@@ -205,23 +205,17 @@ __device__ __forceinline__ void rope_piece(int layout, int half, int c, int* e0,
 }
 
 // A query row for the products with an e4m3 cache: 16 channels of it (bf16) in each of G lanes
-// are rotated at `pos` (rope != 0) in fp32 and rounded once, to f16, scaled by a power of two
-// that puts the largest channel before the rotation in [2^14, 2^15).  Returns what the scores
-// are multiplied by.  All lanes of the warp call it.
+// are rotated (rope != 0) in fp32 and rounded once, to f16, scaled by a power of two that puts
+// the largest channel before the rotation in [2^14, 2^15).  Returns what the scores are
+// multiplied by.  All lanes of the warp call it.
 template <int G>
-__device__ __forceinline__ float query_to_f16(uint4& lo, uint4& hi, int rope, int pos,
-                                              const RopeTable& theta, int c) {
+__device__ __forceinline__ float query_to_f16(uint4& lo, uint4& hi, int rope,
+                                              const float (&cs)[8], const float (&sn)[8]) {
   bool bad;
   const uint32_t top = row_absmax<G>(lo, hi, &bad);
   const int E = min(max(static_cast<int>(top >> 7), 15), 254);  // (scales stay normal numbers)
   const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
-  float cs[8], sn[8], y[16];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    cs[j] = 1.f;
-    sn[j] = 0.f;
-    if (rope != 0) rope_cos_sin<false>(pos, theta.hi[8 * c + j], theta.lo[8 * c + j], cs[j], sn[j]);
-  }
+  float y[16];
   rope16(lo, hi, rope, cs, sn, y);
   lo = make_uint4(pack_f16x2(y[0] * f, y[1] * f), pack_f16x2(y[2] * f, y[3] * f),
                   pack_f16x2(y[4] * f, y[5] * f), pack_f16x2(y[6] * f, y[7] * f));

@@ -3,7 +3,8 @@
 //
 // All T * Hq/Hkv query rows of a KV head read the same cache rows, so they are one side of a
 // matrix product and every cache row is read from HBM once per 8 * NT of them.  A CTA:
-//   warp 4      TMA producer: 64-row K and V tiles into a ring
+//   warp 4      producer: 64-row K and V tiles (and their scale bytes) into a ring by TMA, and a
+//               piece's queries, rotated, ahead of its other tiles
 //   warps 0..3  16 cache rows each per tile, by mma.sync m16n8k16 with the cache rows (then the
 //               channels) on the side of 16 and the query rows on the side of 8:
 //               S^T = K Q^T, then O^T += V^T P^T; softmax statistics in fp32 between the two;
@@ -56,7 +57,10 @@ struct Cfg {
   static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? 4 : 6);
   static constexpr int RING = NS * STAGE;
   static constexpr int Q_BYTES = ROWS * QS;         // twice: the next piece's go to the other
-  static constexpr int SMEM = 1024 + RING + 2 * Q_BYTES + 128 + 2 * ROWS * 4;
+  static constexpr int BARS = 192;
+  static constexpr int CODES = F8 ? 2 * KT : 0;     // scale bytes of a tile: keys', values'
+  static constexpr int SMEM = 1024 + RING + 2 * Q_BYTES + BARS + 2 * ROWS * 4 + NS * CODES;
+  static_assert(8 * (2 * NS + 4) + 4 <= BARS, "barriers");
 };
 
 struct GParams {
@@ -69,6 +73,7 @@ struct GParams {
   const uint8_t* v_scale;
   int words, rope;
   int box_rows;
+  bool code_copies;  // scale bytes lie so that bulk copies can take them
   float* part_o;
   float* part_ml;
   uint32_t* status;
@@ -157,8 +162,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   uint8_t* s_q = smem + C::RING;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING + 2 * C::Q_BYTES);
   uint64_t* empty = full + NS;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
-  float* s_qf = reinterpret_cast<float*>(smem + C::RING + 2 * C::Q_BYTES + 128);  // [2][ROWS]
+  uint64_t* q_full = empty + NS;   // [2]: a piece's queries in buffer piece % 2
+  uint64_t* q_empty = q_full + 2;  // [2]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(q_empty + 2);
+  float* s_qf = reinterpret_cast<float*>(smem + C::RING + 2 * C::Q_BYTES + C::BARS);  // [2][ROWS]
+  uint8_t* s_codes = reinterpret_cast<uint8_t*>(s_qf + 2 * C::ROWS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // what launch_tree_prep wrote is visible from here on
@@ -167,8 +175,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], F8 && !p.code_copies ? 2 : 1);
       mbar_init(&empty[s], NW);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], NW);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -187,40 +199,156 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
+    // (the kernel before wrote the drafts' rows by plain stores)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     const CacheRows& R = p.rows;
+    const int M = p.T * p.rep;
     const int nbox = KT / p.box_rows, r0 = lane * p.box_rows;
     int issued = 0;
+    // The queries of a piece: D/16 lanes per row, 16 channels each.  Rotated here for one query
+    // per head (then all rows are at one position); a tree's come rotated.  They are read ahead
+    // of a piece's first tile and staged behind it.
+    constexpr int G = D / 16, PASSES = C::ROWS * G / 32;
+    const int qc = lane % G;
+    int e0, e1;
+    rope_piece(p.rope, D / 2, qc, &e0, &e1);
+    uint4 q_lo[PASSES], q_hi[PASSES];
+    float factor[PASSES];
+    auto load_queries = [&](const GroupPiece& pc) {
+      const int kvh = pc.head / p.rblocks;
+      const int row0 = (pc.head - kvh * p.rblocks) * C::ROWS + lane / G;
+      const size_t at = (static_cast<size_t>(pc.b) * p.Hkv + kvh) * M + row0;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        q_lo[i] = q_hi[i] = make_uint4(0u, 0u, 0u, 0u);
+        factor[i] = 1.f;
+        if (row0 + 32 / G * i < M) {
+          const __nv_bfloat16* src = p.q + (at + 32 / G * i) * D;
+          q_lo[i] = *reinterpret_cast<const uint4*>(src + e0);
+          q_hi[i] = *reinterpret_cast<const uint4*>(src + e1);
+          if (F8 && p.q_factor != nullptr) factor[i] = p.q_factor[at + 32 / G * i];
+        }
+      }
+    };
+    auto stage_queries = [&](int pos, int piece) {
+      const int buf = piece & 1;
+      bool room = true;
+      if (piece >= 2 && lane == 0)
+        room = ctl_wait(&q_empty[buf], ((piece >> 1) - 1) & 1, abort_flag, p.status, kWaitNs);
+      if (!__all_sync(0xffffffffu, room)) return false;
+      float cs[8], sn[8];
+      if constexpr (F8) {
+        // lane i has angles N (i / G).. of chunk i % G, and hands them to the lanes of the chunk
+        constexpr int N = G / 4;
+        float c1[N], s1[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int at = 8 * qc + N * (lane / G) + j;
+          c1[j] = 1.f;
+          s1[j] = 0.f;
+          if (p.rope != 0)
+            rope_cos_sin<false>(pos, p.theta.hi[at], p.theta.lo[at], c1[j], s1[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          cs[j] = __shfl_sync(0xffffffffu, c1[j % N], G * (j / N) + qc);
+          sn[j] = __shfl_sync(0xffffffffu, s1[j % N], G * (j / N) + qc);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = 32 / G * i + lane / G;
+        uint8_t* dst = s_q + buf * C::Q_BYTES + r * C::QS;
+        if constexpr (F8) {
+          if (p.q_factor == nullptr)
+            factor[i] = query_to_f16<G>(q_lo[i], q_hi[i], p.rope, cs, sn);
+          if (qc == 0) s_qf[buf * C::ROWS + r] = factor[i] * p.scale_log2;
+          // a lane's four bytes of a K row are channels 4(lane%4).. of 16, so the product's
+          // index runs over the 16 channels as 0 1, 4 5, 8 9, 12 13, then 2 3, 6 7, ...
+          const uint32_t wl[4] = {q_lo[i].x, q_lo[i].y, q_lo[i].z, q_lo[i].w};
+          const uint32_t wh[4] = {q_hi[i].x, q_hi[i].y, q_hi[i].z, q_hi[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int off = 2 * ((j >> 1) * 2 + (j & 1) * 8);  // bytes within a half chunk
+            const int b0 = (e0 & 15) ? 8 : 0, b1 = (e1 & 15) ? 8 : 0;
+            *reinterpret_cast<uint32_t*>(dst + 2 * (e0 & ~15) + off + b0) = wl[j];
+            *reinterpret_cast<uint32_t*>(dst + 2 * (e1 & ~15) + off + b1) = wh[j];
+          }
+        } else {
+          *reinterpret_cast<uint4*>(dst + 2 * e0) = q_lo[i];
+          *reinterpret_cast<uint4*>(dst + 2 * e1) = q_hi[i];
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[buf]);
+      return true;
+    };
     bool ok = true;
-    for (; pc.n > 0 && ok; pc.next(p.line)) {
+    for (int piece = 0; pc.n > 0 && ok; pc.next(p.line), ++piece) {
       const int b = pc.b, kvh = pc.head / p.rblocks, total = pc.L + p.line.drafts;
+      // the queries behind as many tiles as find room at once: the ring, or (it is full of the
+      // last piece's) one
+      const int q_at = min(pc.n, piece == 0 && (!F8 || p.code_copies) ? NS : 1) - 1;
+      load_queries(pc);
+      // without bulk copies: the bytes of two rows per lane, a tile ahead
+      auto load_codes = [&](int t, uint8_t (&byte)[4]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = (pc.t0 + t) * KT + lane + 32 * i;
+          const long long at = t < pc.n && r < total ? R.at(b, kvh, r) : -1;
+          byte[i] = at >= 0 ? p.k_scale[at] : 0;
+          byte[2 + i] = at >= 0 ? p.v_scale[at] : 0;
+        }
+      };
+      uint8_t byte[4];
+      if (F8 && !p.code_copies) load_codes(0, byte);
       for (int t = 0; t < pc.n; ++t) {
-        const int s = issued % NS, use = issued / NS;
-        int plane = b * p.Hkv + kvh, prow = (pc.t0 + t) * KT;
-        if (lane < nbox && R.block_table != nullptr) {
-          const int tr = prow + r0;
+        const int s = issued % NS, use = issued / NS, row0 = (pc.t0 + t) * KT;
+        uint8_t* codes = s_codes + s * C::CODES;
+        int plane = b * p.Hkv + kvh, prow = row0;
+        int code_rows = min(KT, R.Lmax - row0);  // scale bytes of the lane's box to copy
+        bool lost = false;                       // its page is outside the pool
+        if (R.block_table != nullptr) {
+          const int tr = row0 + r0;
           plane = R.num_pages * p.Hkv;
           prow = 0;
-          if (tr < total) {
+          code_rows = 0;
+          if (lane < nbox && tr < total) {
             const int page =
                 R.block_table[static_cast<size_t>(b) * R.max_pages + tr / R.page_size];
-            if (page >= 0 && page < R.num_pages)
+            lost = page < 0 || page >= R.num_pages;
+            if (!lost) {
               plane = page * p.Hkv + kvh;
-            else
+              code_rows = p.box_rows;
+            } else {
               atomicOr(p.status, kStatusDeviceArg);
+            }
             prow = tr % R.page_size;
           }
         }
-        int okw = 1;
-        if (lane == 0) {
-          if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
-            okw = 0;
-          else
-            mbar_arrive_expect_tx(&full[s], C::STAGE);
-        }
-        if (!__shfl_sync(0xffffffffu, okw, 0)) {
+        if (lane >= nbox) code_rows = 0;
+        bool room = true;
+        if (lane == 0 && use > 0)
+          room = ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs);
+        if (!__all_sync(0xffffffffu, room)) {
           ok = false;
           break;
         }
+        uint32_t bytes = C::STAGE;
+        if constexpr (F8) {
+          if (lost && p.code_copies) {  // the rows read as zeros: their scale has to be a number
+            for (int i = 0; i < p.box_rows; i += 16) {
+              *reinterpret_cast<uint4*>(codes + r0 + i) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(codes + KT + r0 + i) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          if (p.code_copies)
+            bytes += 2 * __reduce_add_sync(0xffffffffu, static_cast<unsigned>(code_rows));
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+        __syncwarp();
         if (lane < nbox) {
           uint8_t* kd = smem + s * C::STAGE + r0 * (F8 ? D : 128);
           uint8_t* vd = kd + C::TILE;
@@ -229,9 +357,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
             tma_load_3d(kd + kb * (KT * 128), &tm_k, &full[s], kb * 64, prow, plane);
           for (int kb = 0; kb < kBlocks; ++kb)
             tma_load_3d(vd + kb * (KT * 128), &tm_v, &full[s], kb * 64, prow, plane);
+          if (F8 && p.code_copies && code_rows > 0) {
+            const size_t at =
+                static_cast<size_t>(plane) * (R.block_table != nullptr ? R.page_size : R.Lmax) +
+                prow;
+            bulk_load(codes + r0, p.k_scale + at, code_rows, &full[s]);
+            bulk_load(codes + KT + r0, p.v_scale + at, code_rows, &full[s]);
+          }
         }
         __syncwarp();
         ++issued;
+        if (t == q_at) ok = stage_queries(pc.L - 1, piece);
+        if (F8 && !p.code_copies) {
+          uint8_t next[4];
+          load_codes(t + 1, next);
+          codes[lane] = byte[0];
+          codes[lane + 32] = byte[1];
+          codes[KT + lane] = byte[2];
+          codes[KT + lane + 32] = byte[3];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) byte[i] = next[i];
+        }
+        if (!ok) break;
       }
     }
     if (lane == 0 && *abort_flag) {
@@ -254,357 +403,282 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
   bool ok = true;
   int used = 0;  // tiles of the CTA so far
   for (int piece = 0; pc.n > 0; pc.next(p.line), ++piece) {
-  const int b = pc.b, kvh = pc.head / p.rblocks, L = pc.L, total = L + p.line.drafts;
-  const int row_base = (pc.head - kvh * p.rblocks) * C::ROWS;  // first query row
-  const int k_begin = pc.t0 * KT, ntiles = pc.n;
-  const int k_end = min(total, k_begin + ntiles * KT);
+    const int b = pc.b, kvh = pc.head / p.rblocks, L = pc.L, total = L + p.line.drafts;
+    const int row_base = (pc.head - kvh * p.rblocks) * C::ROWS;  // first query row
+    const int k_begin = pc.t0 * KT, ntiles = pc.n;
+    const int k_end = min(total, k_begin + ntiles * KT);
 
-  // scale bytes of the warp's 16 rows of a tile: lanes 0..15 the keys', 16..31 the values';
-  // rows past the sequence and pages outside the pool read 0 (their data is zero or masked).
-  // Two loads that depend on one another, so each is issued a tile or two ahead of its use.
-  // (The page's number and the row in it move on by additions: a tile is 64 rows.)
-  const bool paged = F8 && p.rows.block_table != nullptr;
-  const int code_row = k_begin + 16 * warp + (lane & 15);
-  const int ps = paged ? p.rows.page_size : 1;
-  const int32_t* const table = p.rows.block_table + static_cast<size_t>(b) * p.rows.max_pages;
-  const uint8_t* const scale_of = lane < 16 ? p.k_scale : p.v_scale;
-  int pg = code_row / ps, ofs = code_row - pg * ps;  // of the next page lookup
-  auto load_page = [&](int t) -> int2 {              // page of the row in tile t, offset in it
-    const int at = ofs;
-    int page = 0;
-    if (paged) {
-      if (t < ntiles && code_row + t * KT < total) page = table[pg];
-      ofs += KT;
-      if (ps < KT) {
-        pg += KT / ps;
-        ofs = at;
-      } else if (ofs >= ps) {
-        ++pg;
-        ofs -= ps;
-      }
-    }
-    return make_int2(page, at);
-  };
-  auto load_code = [&](int t, int2 page) -> uint32_t {
-    const int r = code_row + t * KT;
-    if (!F8 || t >= ntiles || r >= total) return 0u;
-    if (!paged) return scale_of[(static_cast<size_t>(b) * p.Hkv + kvh) * p.rows.Lmax + r];
-    if (page.x < 0 || page.x >= p.rows.num_pages) return 0u;
-    return scale_of[(static_cast<size_t>(page.x) * p.Hkv + kvh) * ps + page.y];
-  };
-  const int2 page0 = load_page(0), page1 = load_page(1);
-  int2 page2 = load_page(2);
-  uint32_t codes = load_code(0, page0), codes1 = load_code(1, page1);
-
-  // queries into shared memory: D/16 lanes per row, 16 channels each
-  {
-    constexpr int G = D / 16;
-    for (int r1 = 0; r1 < C::ROWS; r1 += 32 * NW / G) {  // (whole warps shuffle below)
-      const int r = r1 + static_cast<int>(threadIdx.x) / G;
-      const int c = threadIdx.x % G, row = row_base + r;
-      int e0, e1;
-      rope_piece(p.rope, D / 2, c, &e0, &e1);
-      uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-      float factor = 1.f;
-      if (r < C::ROWS && row < M) {
-        const size_t at = (static_cast<size_t>(b) * p.Hkv + kvh) * M + row;
-        lo = *reinterpret_cast<const uint4*>(p.q + at * D + e0);
-        hi = *reinterpret_cast<const uint4*>(p.q + at * D + e1);
-        if (F8 && p.q_factor != nullptr) factor = p.q_factor[at];
-      }
-      if (F8 && p.q_factor == nullptr)
-        factor = query_to_f16<G>(lo, hi, p.rope, L - 1, p.theta, c);
-      if (r >= C::ROWS) continue;  // (no shuffle below)
-      if (F8 && c == 0) s_qf[(piece & 1) * C::ROWS + r] = factor * p.scale_log2;
-      uint8_t* dst = s_q + (piece & 1) * C::Q_BYTES + r * C::QS;
-      if constexpr (F8) {
-        // a lane's four bytes of a K row are channels 4(lane%4).. of 16, so the product's
-        // index runs over the 16 channels as 0 1, 4 5, 8 9, 12 13, then 2 3, 6 7, ...
-        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int off = 2 * ((j >> 1) * 2 + (j & 1) * 8);  // bytes within a half chunk
-          const int b0 = (e0 & 15) ? 8 : 0, b1 = (e1 & 15) ? 8 : 0;
-          *reinterpret_cast<uint32_t*>(dst + 2 * (e0 & ~15) + off + b0) = wl[j];
-          *reinterpret_cast<uint32_t*>(dst + 2 * (e1 & ~15) + off + b1) = wh[j];
-        }
-      } else {
-        *reinterpret_cast<uint4*>(dst + 2 * e0) = lo;
-        *reinterpret_cast<uint4*>(dst + 2 * e1) = hi;
-      }
-    }
-  }
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * NW) : "memory");
-
-  const uint32_t q_addr = smem_u32(s_q + (piece & 1) * C::Q_BYTES) + (lane & 7) * C::QS + mi * 16;
-  uint32_t qb[NT][D / 16][2];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int kk = 0; kk < D / 16; kk += 2) {
-      uint32_t w[4];
-      ldsm_x4(q_addr + j * 8 * C::QS + kk * 32, w);
-      qb[j][kk][0] = w[0];
-      qb[j][kk][1] = w[1];
-      qb[j][kk + 1][0] = w[2];
-      qb[j][kk + 1][1] = w[3];
-    }
-  float qf[NT][2];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) qf[j][h] = F8 ? s_qf[(piece & 1) * C::ROWS + 8 * j + cq + h] : p.scale_log2;
-
-  float o[D / 16][NT][4];
-  float m_used[NT][2], n_used[NT][2], l_part[NT][2];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[c][j][0] = o[c][j][1] = o[c][j][2] = o[c][j][3] = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) m_used[j][h] = n_used[j][h] = -INFINITY, l_part[j][h] = 0.f;
-  }
-
-  bool unset = true;  // some query row has no maximum yet
-  for (int t = 0; t < ntiles && ok; ++t, ++used) {
-    const int s = used % NS;
-    const uint32_t codes2 = load_code(t + 2, page2);
-    page2 = load_page(t + 3);
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (used / NS) & 1, abort_flag, p.status,
-                                           kWaitNs))) {
-      ok = false;
-      break;
-    }
-    const uint32_t kbase = smem_base + s * C::STAGE;
-    const uint32_t vbase = kbase + C::TILE;
-    const int key0 = k_begin + t * KT + 16 * warp;  // first cache row of the warp
-    float sc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; kk += 2) {
-      uint32_t a[2][4];
-      if constexpr (F8) {
-        uint32_t w[4];
-        ldsm_x4(kbase + tile_off<D, F8>(kr, kk + (mi >> 1)), w);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          a[i][0] = e4m3x2_to_f16x2(w[2 * i]);
-          a[i][1] = e4m3x2_to_f16x2(w[2 * i + 1]);
-          a[i][2] = e4m3x2_hi_to_f16x2(w[2 * i]);
-          a[i][3] = e4m3x2_hi_to_f16x2(w[2 * i + 1]);
-        }
-      } else {
-        ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + (mi >> 1)), a[0]);
-        ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + 2 + (mi >> 1)), a[1]);
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma<F8>(sc[j], a[0], qb[j][kk][0], qb[j][kk][1]);
-        mma<F8>(sc[j], a[1], qb[j][kk + 1][0], qb[j][kk + 1][1]);
-      }
-    }
-    // factors of the thread's two cache rows
-    float kf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
-    if constexpr (F8) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        kf[i] = __uint_as_float(__shfl_sync(0xffffffffu, codes, r0 + 8 * i) << 23);
-        ev[i] = static_cast<float>(
-            static_cast<int>(__shfl_sync(0xffffffffu, codes, 16 + r0 + 8 * i)) - 127);
-      }
-    }
-    // cache rows that a query row does not see: their scores become -inf
-    const bool edge = key0 + 16 > min(L, k_end);
-    uint32_t hide = 0u;  // bit 4j + 2i + h
-    if (edge) {
-      const uint32_t in = key0 + 16 <= k_end ? 0xffffu
-                          : key0 >= k_end    ? 0u
-                                             : (1u << (k_end - key0)) - 1u;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int tq = min((row_base + 8 * j + cq + h) / p.rep, p.T - 1);
-          const uint32_t* anc = p.anc + (static_cast<size_t>(b) * p.T + tq) * p.words;
-          const uint32_t see =
-              in & (key0 + 16 <= L ? 0xffffu : draft_bits(anc, p.words, key0 - L));
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            hide |= (1u ^ ((see >> (r0 + 8 * i)) & 1u)) << (4 * j + 2 * i + h);
-        }
-    }
-    // x - m for every score (x rounded by itself, as in m: the largest gives 0); where one exceeds its maximum by the threshold (or there is none
-    // yet) the maxima are raised first
-    float d[NT][4];
-    bool over = false;
+    ok = __all_sync(0xffffffffu, mbar_wait(&q_full[piece & 1], (piece >> 1) & 1, abort_flag,
+                                           p.status, kWaitNs));
+    if (!ok) break;
+    const uint32_t q_addr = smem_u32(s_q + (piece & 1) * C::Q_BYTES) + (lane & 7) * C::QS + mi * 16;
+    uint32_t qb[NT][D / 16][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = e >> 1, h = e & 1;
-        d[j][e] = __fmul_rn(sc[j][e], F8 ? kf[i] * qf[j][h] : qf[j][h]) - m_used[j][h];
-        if (edge && ((hide >> (4 * j + e)) & 1u)) d[j][e] = -INFINITY;
-        over |= d[j][e] > kRescaleThreshold;
-        if constexpr (F8) over |= d[j][e] + ev[i] > n_used[j][h] + kRescaleThreshold;
+      for (int kk = 0; kk < D / 16; kk += 2) {
+        uint32_t w[4];
+        ldsm_x4(q_addr + j * 8 * C::QS + kk * 32, w);
+        qb[j][kk][0] = w[0];
+        qb[j][kk][1] = w[1];
+        qb[j][kk + 1][0] = w[2];
+        qb[j][kk + 1][1] = w[3];
       }
-    if (__any_sync(0xffffffffu, over || unset)) {
-      unset = false;
+    float qf[NT][2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x[2];
+      for (int h = 0; h < 2; ++h)
+        qf[j][h] = F8 ? s_qf[(piece & 1) * C::ROWS + 8 * j + cq + h] : p.scale_log2;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_empty[piece & 1]);
+
+    float o[D / 16][NT][4];
+    float m_used[NT][2], n_used[NT][2], l_part[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[c][j][0] = o[c][j][1] = o[c][j][2] = o[c][j][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) m_used[j][h] = n_used[j][h] = -INFINITY, l_part[j][h] = 0.f;
+    }
+
+    bool unset = true;  // some query row has no maximum yet
+    for (int t = 0; t < ntiles && ok; ++t, ++used) {
+      const int s = used % NS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (used / NS) & 1, abort_flag, p.status,
+                                             kWaitNs))) {
+        ok = false;
+        break;
+      }
+      const uint32_t kbase = smem_base + s * C::STAGE;
+      const uint32_t vbase = kbase + C::TILE;
+      const int key0 = k_begin + t * KT + 16 * warp;  // first cache row of the warp
+      float sc[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; kk += 2) {
+        uint32_t a[2][4];
+        if constexpr (F8) {
+          uint32_t w[4];
+          ldsm_x4(kbase + tile_off<D, F8>(kr, kk + (mi >> 1)), w);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            x[i] = __fmul_rn(sc[j][2 * i + h], F8 ? kf[i] * qf[j][h] : qf[j][h]);
-            if (edge && ((hide >> (4 * j + 2 * i + h)) & 1u)) x[i] = -INFINITY;
+            a[i][0] = e4m3x2_to_f16x2(w[2 * i]);
+            a[i][1] = e4m3x2_to_f16x2(w[2 * i + 1]);
+            a[i][2] = e4m3x2_hi_to_f16x2(w[2 * i]);
+            a[i][3] = e4m3x2_hi_to_f16x2(w[2 * i + 1]);
           }
-          const float mx = column_max(fmaxf(x[0], x[1]));
-          if (mx > m_used[j][h] + kRescaleThreshold) {
-            const float r = m_used[j][h] - mx;
-            l_part[j][h] *= ex2_approx(r);  // 0 when m_used was -inf
-            if constexpr (F8)
-              n_used[j][h] += r;  // the numerator's reference m + n stays where it was
-            else
-              f[h] = ex2_approx(r);
-            m_used[j][h] = mx;
-          }
-          // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
-          const float m_ref = m_used[j][h] == -INFINITY ? 0.f : m_used[j][h];
-          unset |= m_used[j][h] == -INFINITY;
+        } else {
+          ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + (mi >> 1)), a[0]);
+          ldsm_x4(kbase + tile_off<D, F8>(kr, 2 * kk + 2 + (mi >> 1)), a[1]);
+        }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) d[j][2 * i + h] = x[i] - m_ref;
-          if constexpr (F8) {
-            const float my = column_max(fmaxf(d[j][h] + ev[0], d[j][2 + h] + ev[1]));
-            if (my > n_used[j][h] + kRescaleThreshold) {
-              f[h] = ex2_approx(n_used[j][h] - my);
-              n_used[j][h] = my;
+        for (int j = 0; j < NT; ++j) {
+          mma<F8>(sc[j], a[0], qb[j][kk][0], qb[j][kk][1]);
+          mma<F8>(sc[j], a[1], qb[j][kk + 1][0], qb[j][kk + 1][1]);
+        }
+      }
+      // factors of the thread's two cache rows
+      float kf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
+      if constexpr (F8) {  // (of rows past the sequence: any value, their scores are -inf below)
+        const uint8_t* codes = s_codes + s * C::CODES + 16 * warp + r0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          kf[i] = __uint_as_float(static_cast<uint32_t>(codes[8 * i]) << 23);
+          ev[i] = static_cast<float>(static_cast<int>(codes[KT + 8 * i]) - 127);
+        }
+      }
+      // cache rows that a query row does not see: their scores become -inf
+      const bool edge = key0 + 16 > min(L, k_end);
+      uint32_t hide = 0u;  // bit 4j + 2i + h
+      if (edge) {
+        const uint32_t in = key0 + 16 <= k_end ? 0xffffu
+                            : key0 >= k_end    ? 0u
+                                               : (1u << (k_end - key0)) - 1u;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int tq = min((row_base + 8 * j + cq + h) / p.rep, p.T - 1);
+            const uint32_t* anc = p.anc + (static_cast<size_t>(b) * p.T + tq) * p.words;
+            const uint32_t see =
+                in & (key0 + 16 <= L ? 0xffffu : draft_bits(anc, p.words, key0 - L));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              hide |= (1u ^ ((see >> (r0 + 8 * i)) & 1u)) << (4 * j + 2 * i + h);
+          }
+      }
+      // x - m for every score (x rounded by itself, as in m: the largest gives 0); where one
+      // exceeds its maximum by the threshold (or there is none yet) the maxima are raised first
+      float d[NT][4];
+      bool over = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = e >> 1, h = e & 1;
+          d[j][e] = __fmul_rn(sc[j][e], F8 ? kf[i] * qf[j][h] : qf[j][h]) - m_used[j][h];
+          if (edge && ((hide >> (4 * j + e)) & 1u)) d[j][e] = -INFINITY;
+          over |= d[j][e] > kRescaleThreshold;
+          if constexpr (F8) over |= d[j][e] + ev[i] > n_used[j][h] + kRescaleThreshold;
+        }
+      if (__any_sync(0xffffffffu, over || unset)) {
+        unset = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              x[i] = __fmul_rn(sc[j][2 * i + h], F8 ? kf[i] * qf[j][h] : qf[j][h]);
+              if (edge && ((hide >> (4 * j + 2 * i + h)) & 1u)) x[i] = -INFINITY;
+            }
+            const float mx = column_max(fmaxf(x[0], x[1]));
+            if (mx > m_used[j][h] + kRescaleThreshold) {
+              const float r = m_used[j][h] - mx;
+              l_part[j][h] *= ex2_approx(r);  // 0 when m_used was -inf
+              if constexpr (F8)
+                n_used[j][h] += r;  // the numerator's reference m + n stays where it was
+              else
+                f[h] = ex2_approx(r);
+              m_used[j][h] = mx;
+            }
+            // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
+            const float m_ref = m_used[j][h] == -INFINITY ? 0.f : m_used[j][h];
+            unset |= m_used[j][h] == -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) d[j][2 * i + h] = x[i] - m_ref;
+            if constexpr (F8) {
+              const float my = column_max(fmaxf(d[j][h] + ev[0], d[j][2 + h] + ev[1]));
+              if (my > n_used[j][h] + kRescaleThreshold) {
+                f[h] = ex2_approx(n_used[j][h] - my);
+                n_used[j][h] = my;
+              }
+            }
+          }
+          if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[c][j][0] *= f[0];
+              o[c][j][1] *= f[1];
+              o[c][j][2] *= f[0];
+              o[c][j][3] *= f[1];
             }
           }
         }
-        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+        unset = __any_sync(0xffffffffu, unset);
+      }
+      // weights, turned to the layout of the second product
+      uint32_t pb[NT][2];
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            o[c][j][0] *= f[0];
-            o[c][j][1] *= f[1];
-            o[c][j][2] *= f[0];
-            o[c][j][3] *= f[1];
+      for (int j = 0; j < NT; ++j) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = ex2_approx(d[j][e]);
+          l_part[j][e & 1] += v;
+          w[e] = v;
+          if constexpr (F8) {
+            const float n_ref = n_used[j][e & 1] == -INFINITY ? 0.f : n_used[j][e & 1];
+            w[e] = ex2_approx(d[j][e] + (ev[e >> 1] + (kWeightLog2 - n_ref)));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          pb[j][i] = transpose8x8(F8 ? pack_f16x2(w[2 * i], w[2 * i + 1])
+                                     : pack_bf16x2(w[2 * i], w[2 * i + 1]));
+      }
+      // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
+      // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
+      // merge puts it where it belongs).
+      if (edge) {
+        uint8_t* vt = smem + s * C::STAGE + C::TILE;
+        for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
+          const int rr = e / (C::ROW / 16), cc = e % (C::ROW / 16);
+          uint4* at = reinterpret_cast<uint4*>(vt + tile_off<D, F8>(16 * warp + rr, cc));
+          if (key0 + rr >= k_end) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+          } else if (key0 + rr >= L) {
+            const uint4 v = *at;
+            *at = make_uint4(finite_word<F8>(v.x), finite_word<F8>(v.y), finite_word<F8>(v.z),
+                             finite_word<F8>(v.w));
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; c += 2) {
+        uint32_t a[2][4];
+        if constexpr (F8) {
+          // a transposed load hands a lane channels (2n, 2n + 1) of two cache rows: regrouped by
+          // channel they are rows n (even channels) and n + 8 (odd) of the operand
+          uint32_t r[4];
+          ldsm_x4_t(vbase + tile_off<D, F8>(vr, c + (mi >> 1)), r);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t u = __byte_perm(r[2 * i], 0u, 0x3120);
+            const uint32_t v = __byte_perm(r[2 * i + 1], 0u, 0x3120);
+            a[i][0] = e4m3x2_to_f16x2(u);
+            a[i][1] = e4m3x2_hi_to_f16x2(u);
+            a[i][2] = e4m3x2_to_f16x2(v);
+            a[i][3] = e4m3x2_hi_to_f16x2(v);
+          }
+        } else {
+          ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * c + (mi & 1)), a[0]);
+          ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * c + 2 + (mi & 1)), a[1]);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma<F8>(o[c][j], a[0], pb[j][0], pb[j][1]);
+          mma<F8>(o[c + 1][j], a[1], pb[j][0], pb[j][1]);
+        }
+      }
+      if (edge) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 4);
+        l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 8);
+        l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 16);
+      }
+    if (!ok) break;
+    if (threadIdx.x == 0) pc.leave_for_merge(p.line);
+    // the warp's partial result, relative to the maximum of x
+    const size_t slot =
+        (static_cast<size_t>(blockIdx.x) + pc.segment(p.line)) * NW + warp;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * j + cq + h;
+        if (row_base + r >= M) continue;
+        // (a row that saw nothing holds zeros, or NaN if its scores were NaN)
+        const float f =
+            F8 && n_used[j][h] != -INFINITY ? ex2_approx(n_used[j][h] - kWeightLog2) : 1.f;
+        const size_t at = slot * p.part_rows + r;
+        float* dst = p.part_o + at * D;
+        if (r0 == 0)
+          *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_used[j][h], l_part[j][h]);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          if constexpr (F8) {
+            *reinterpret_cast<float2*>(dst + 16 * c + 2 * r0) =
+                make_float2(o[c][j][h] * f, o[c][j][2 + h] * f);
+          } else {
+            dst[16 * c + r0] = o[c][j][h];
+            dst[16 * c + r0 + 8] = o[c][j][2 + h];
           }
         }
       }
-      unset = __any_sync(0xffffffffu, unset);
-    }
-    // weights, turned to the layout of the second product
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = ex2_approx(d[j][e]);
-        l_part[j][e & 1] += v;
-        w[e] = v;
-        if constexpr (F8) {
-          const float n_ref = n_used[j][e & 1] == -INFINITY ? 0.f : n_used[j][e & 1];
-          w[e] = ex2_approx(d[j][e] + (ev[e >> 1] + (kWeightLog2 - n_ref)));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        pb[j][i] = transpose8x8(F8 ? pack_f16x2(w[2 * i], w[2 * i + 1])
-                                   : pack_bf16x2(w[2 * i], w[2 * i + 1]));
-    }
-    // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
-    // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
-    // merge puts it where it belongs).
-    if (edge) {
-      uint8_t* vt = smem + s * C::STAGE + C::TILE;
-      for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
-        const int rr = e / (C::ROW / 16), cc = e % (C::ROW / 16);
-        uint4* at = reinterpret_cast<uint4*>(vt + tile_off<D, F8>(16 * warp + rr, cc));
-        if (key0 + rr >= k_end) {
-          *at = make_uint4(0u, 0u, 0u, 0u);
-        } else if (key0 + rr >= L) {
-          const uint4 v = *at;
-          *at = make_uint4(finite_word<F8>(v.x), finite_word<F8>(v.y), finite_word<F8>(v.z),
-                           finite_word<F8>(v.w));
-        }
-      }
-      __syncwarp();
-    }
-#pragma unroll
-    for (int c = 0; c < D / 16; c += 2) {
-      uint32_t a[2][4];
-      if constexpr (F8) {
-        // a transposed load hands a lane channels (2n, 2n + 1) of two cache rows: regrouped by
-        // channel they are rows n (even channels) and n + 8 (odd) of the operand
-        uint32_t r[4];
-        ldsm_x4_t(vbase + tile_off<D, F8>(vr, c + (mi >> 1)), r);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t u = __byte_perm(r[2 * i], 0u, 0x3120);
-          const uint32_t v = __byte_perm(r[2 * i + 1], 0u, 0x3120);
-          a[i][0] = e4m3x2_to_f16x2(u);
-          a[i][1] = e4m3x2_hi_to_f16x2(u);
-          a[i][2] = e4m3x2_to_f16x2(v);
-          a[i][3] = e4m3x2_hi_to_f16x2(v);
-        }
-      } else {
-        ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * c + (mi & 1)), a[0]);
-        ldsm_x4_t(vbase + tile_off<D, F8>(vr, 2 * c + 2 + (mi & 1)), a[1]);
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma<F8>(o[c][j], a[0], pb[j][0], pb[j][1]);
-        mma<F8>(o[c + 1][j], a[1], pb[j][0], pb[j][1]);
-      }
-    }
-    if (edge) fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
-    codes = codes1;
-    codes1 = codes2;
-  }
-
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 4);
-      l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 8);
-      l_part[j][h] += __shfl_xor_sync(0xffffffffu, l_part[j][h], 16);
-    }
-  if (!ok) continue;  // (to the end: the warps' barriers go together)
-  if (threadIdx.x == 0) pc.leave_for_merge(p.line);
-  // the warp's partial result, relative to the maximum of x
-  const size_t slot =
-      (static_cast<size_t>(blockIdx.x) + pc.segment(p.line)) * NW + warp;
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 8 * j + cq + h;
-      if (row_base + r >= M) continue;
-      // (a row that saw nothing holds zeros, or NaN if its scores were NaN)
-      const float f =
-          F8 && n_used[j][h] != -INFINITY ? ex2_approx(n_used[j][h] - kWeightLog2) : 1.f;
-      const size_t at = slot * p.part_rows + r;
-      float* dst = p.part_o + at * D;
-      if (r0 == 0)
-        *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_used[j][h], l_part[j][h]);
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        if constexpr (F8) {
-          *reinterpret_cast<float2*>(dst + 16 * c + 2 * r0) =
-              make_float2(o[c][j][h] * f, o[c][j][2 + h] * f);
-        } else {
-          dst[16 * c + r0] = o[c][j][h];
-          dst[16 * c + r0 + 8] = o[c][j][2 + h];
-        }
-      }
-    }
   }
 }
 
@@ -624,7 +698,7 @@ __global__ void __launch_bounds__(128) group_merge_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = static_cast<int>(blockIdx.x) * (4 / W) + warp / W;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= rows) return;  // (W > 1: the whole CTA)
+  if (row >= rows) return;
   const int rep = Hq / Hkv;
   const int t = row % T, bh = row / T, b = bh / Hq, h = bh - b * Hq, g = h / rep;
   const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
@@ -681,20 +755,20 @@ __global__ void __launch_bounds__(128) group_merge_kernel(
       s_part[warp][V * 32 + 1] = m;
     }
     __syncthreads();
-    if (warp != 0) return;
+    if (warp % W != 0) return;
     float mx = m;
 #pragma unroll
-    for (int w = 1; w < W; ++w) mx = fmaxf(mx, s_part[w][V * 32 + 1]);
+    for (int w = 1; w < W; ++w) mx = fmaxf(mx, s_part[warp + w][V * 32 + 1]);
     l = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float mw = s_part[w][V * 32 + 1];
+      const float mw = s_part[warp + w][V * 32 + 1];
       const float e = mw == -INFINITY ? 1.f : ex2_approx(mw - mx);
-      l += e * s_part[w][V * 32];
+      l += e * s_part[warp + w][V * 32];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += e * s_part[w][V * lane + i];
+      for (int i = 0; i < V; ++i) acc[i] += e * s_part[warp + w][V * lane + i];
     }
     m = mx;
   }
@@ -743,6 +817,9 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.rope = a.rope;
   const bool paged = a.cache.block_table != nullptr;
   p.box_rows = paged && a.cache.page_size < KT ? a.cache.page_size : KT;
+  const uintptr_t scales =
+      reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale);
+  p.code_copies = scales % 16 == 0 && (paged || a.cache.Lmax % 16 == 0);
   p.part_o = a.part_o;
   p.part_ml = a.part_ml;
   p.status = a.status;
@@ -815,10 +892,16 @@ cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_group_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
                                void* out, float* lse, cudaStream_t stream) {
-  // few rows: four warps each, so that the partials are read side by side
-  if (a.B * a.Hq * a.T <= 4096)
+  // Few rows have many partials: four warps each, which read them side by side.  2048 rows of
+  // eight: 111.5 us for the whole decode with two, 115.1 with four, 113.2 with one; 256 rows of
+  // 32: 99.8 with four, 101.7 with two, 103.6 with one.
+  const int rows = a.B * a.Hq * a.T;
+  if (rows <= 1024)
     return a.d == 128 ? launch_merge<128, 4>(a, vflag, v_new, out, lse, stream)
                       : launch_merge<64, 4>(a, vflag, v_new, out, lse, stream);
+  if (rows <= 4096)
+    return a.d == 128 ? launch_merge<128, 2>(a, vflag, v_new, out, lse, stream)
+                      : launch_merge<64, 2>(a, vflag, v_new, out, lse, stream);
   return a.d == 128 ? launch_merge<128, 1>(a, vflag, v_new, out, lse, stream)
                     : launch_merge<64, 1>(a, vflag, v_new, out, lse, stream);
 }

@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     // The thread's piece: column c of row r0.  Eight lanes share a wavefront, and a row's pieces
     // c and c + 4 go to the same banks (to the tile's two halves); so at 128 channels two rows
     // change places in their upper four pieces, and odd rows' chunks lie between even ones'.
-    const int c = tid % G, r0 = D == 128 ? 2 * (tid >> 4) + (((tid >> 2) ^ (tid >> 3)) & 1) : tid / G;
+    const int c = tid % G;
+    const int r0 = D == 128 ? 2 * (tid >> 4) + (((tid >> 2) ^ (tid >> 3)) & 1) : tid / G;
     uint32_t to0, to1;                         // where the thread's two chunks go in a tile
     {
       const uint32_t at = (c >> 2) * (BN * 128) + r0 * 128;
@@ -609,7 +610,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t mm = __shfl_sync(0xffffffffu, factor, (32 / G) * (i0 + i) + r0 % (32 / G));
+            const uint32_t mm =
+                __shfl_sync(0xffffffffu, factor, (32 / G) * (i0 + i) + r0 % (32 / G));
             const uint4 lo = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].x), mm),
                                         hmul2(e4m3x2_hi_to_f16x2(x[i].x), mm),
                                         hmul2(e4m3x2_to_f16x2(x[i].y), mm),
@@ -1019,9 +1021,9 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.k_scale = static_cast<const uint8_t*>(a.cache.k_scale);
   p.v_scale = static_cast<const uint8_t*>(a.cache.v_scale);
   p.words = a.words;
-  p.scale_words = ((reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale)) &
-                   3u) == 0 &&
-                  (a.cache.block_table != nullptr || a.cache.Lmax % 4 == 0);
+  const uintptr_t scales =
+      reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale);
+  p.scale_words = scales % 4 == 0 && (a.cache.block_table != nullptr || a.cache.Lmax % 4 == 0);
   const bool paged = a.cache.block_table != nullptr;
   const int ps = a.cache.page_size;
   p.box_rows = !paged || ps % BN == 0 ? BN : (ps < 64 ? ps : 64);

@@ -76,10 +76,9 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     const bool is_q = head < Hq, is_v = head >= Hq + Hkv;
     int e0, e1;
     rope_piece(is_v ? 0 : rope, D / 2, c, &e0, &e1);
-    const __nv_bfloat16* x =
-        (is_q ? q_new : (is_v ? v_new : k_new)) +
-        ((static_cast<size_t>(b) * (is_q ? Hq : Hkv) + (is_q ? head : head - Hq - (is_v ? Hkv : 0))) *
-             Tn + t) * static_cast<size_t>(D);
+    const int g = is_q ? head : head - Hq - (is_v ? Hkv : 0);
+    const __nv_bfloat16* x = (is_q ? q_new : (is_v ? v_new : k_new)) +
+                             ((static_cast<size_t>(b) * (is_q ? Hq : Hkv) + g) * Tn + t) * D;
     *lo = *reinterpret_cast<const uint4*>(x + e0);
     *hi = *reinterpret_cast<const uint4*>(x + e1);
   };
@@ -96,7 +95,8 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
   }
   if (!fine) return;  // the sequence's cache is left as it was
   __syncthreads();
-  if (blockIdx.z == 0 && tid < words) anc[(static_cast<size_t>(b) * Tn + t) * words + tid] = s_anc[t][tid];
+  if (blockIdx.z == 0 && tid < words)
+    anc[(static_cast<size_t>(b) * Tn + t) * words + tid] = s_anc[t][tid];
   int depth = -1;
   for (int w = 0; w < words; ++w) depth += __popc(s_anc[t][w]);
   const int pos = L + max(depth, 0);  // (padding is written like a first token, never seen)
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     if (is_q) {
       // the rows of a KV head's queries one behind another, draft by draft
       const int kvh = g / rep;
-      const size_t q_row = (static_cast<size_t>(b) * Hkv + kvh) * Tn * rep + t * rep + g - kvh * rep;
+      const size_t q_row =
+          (static_cast<size_t>(b) * Hkv + kvh) * Tn * rep + t * rep + g - kvh * rep;
       if constexpr (F8) {  // (query_to_f16 with the angles at hand)
         const int E = min(max(static_cast<int>(top >> 7), 15), 254);
         const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
@@ -159,8 +160,8 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
       if (c == 0) atomicOr(status, kStatusDeviceArg);
       continue;
     }
-    const long long row =
-        row0 + static_cast<long long>(g) * (rows.block_table != nullptr ? rows.page_size : rows.Lmax);
+    const int plane = rows.block_table != nullptr ? rows.page_size : rows.Lmax;  // rows of a head
+    const long long row = row0 + static_cast<long long>(g) * plane;
     if constexpr (F8) {
       uint8_t* dst = static_cast<uint8_t*>(is_v ? v_cache : k_cache) + row * D;
       *reinterpret_cast<uint2*>(dst + e0) =
