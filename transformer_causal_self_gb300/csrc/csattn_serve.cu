@@ -116,7 +116,8 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
 constexpr int kSms = 152;
 constexpr int kTcRows = 16;  // trees with more query rows than this go to launch_group_tc
 
-GroupPlan plan_for(int B, int Hkv, int rows, bool tc, bool f8, int max_seq_len, int num_splits) {
+GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, bool f8, int max_seq_len,
+                   int num_splits) {
   GroupPlan p{};
   p.tc = tc;
   p.unit = tc ? 128 : 64;
@@ -140,7 +141,7 @@ GroupPlan plan_for(int B, int Hkv, int rows, bool tc, bool f8, int max_seq_len, 
     p.least_tiles = tc ? 1 : 2;
     const long long tiles = (max_seq_len + p.unit - 1) / p.unit;
     const long long line = tiles * B * Hkv * p.rblocks;
-    const int resident = kSms * (tc ? 1 : (f8 ? 3 : 2));
+    const int resident = kSms * (tc ? 1 : group_attn_ctas(d, f8, p.block_rows));
     p.most_grid = p.grid = static_cast<int>(
         std::min<long long>(resident, (line + p.least_tiles - 1) / p.least_tiles));
   }
@@ -246,7 +247,7 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
     return rc;
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
-  a.plan = plan_for(B, Hkv, Hq / Hkv, false, true, max_seq_len, num_splits);
+  a.plan = plan_for(B, Hkv, Hq / Hkv, d, false, true, max_seq_len, num_splits);
   if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
   const size_t partials = partial_bytes(a.plan, B, Hkv, d);
   if ((rc = check_workspace(fn, workspace, workspace_bytes,
@@ -292,9 +293,10 @@ struct TreeSpace {
   }
 };
 
-GroupPlan tree_plan(int B, int Hq, int Hkv, int Tn, bool f8, int max_seq_len, int num_splits) {
+GroupPlan tree_plan(int B, int Hq, int Hkv, int Tn, int d, bool f8, int max_seq_len,
+                    int num_splits) {
   const int rows = Tn * (Hq / Hkv);
-  return plan_for(B, Hkv, rows, rows > kTcRows, f8, max_seq_len, num_splits);
+  return plan_for(B, Hkv, rows, d, rows > kTcRows, f8, max_seq_len, num_splits);
 }
 
 int tree_step(const char* fn, const void* q_new, const void* k_new, const void* v_new,
@@ -320,7 +322,7 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
     return rc;
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
   GroupArgs a{};
-  a.plan = tree_plan(B, Hq, Hkv, Tn, cache_dtype == CSATTN_E4M3, max_seq_len, num_splits);
+  a.plan = tree_plan(B, Hq, Hkv, Tn, d, cache_dtype == CSATTN_E4M3, max_seq_len, num_splits);
   if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
   const TreeSpace at(a.plan, B, Hq, Hkv, Tn, d);
   if ((rc = check_workspace(fn, workspace, workspace_bytes, at.total)) != CSATTN_OK) return rc;
@@ -488,7 +490,7 @@ int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const 
 
 size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
   if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits)) return 0;
-  const GroupPlan p = plan_for(B, Hkv, Hq / Hkv, false, true, Lmax, num_splits);
+  const GroupPlan p = plan_for(B, Hkv, Hq / Hkv, d, false, true, Lmax, num_splits);
   return align256(partial_bytes(p, B, Hkv, d)) + seg_bytes(p, B, Hkv);
 }
 
@@ -525,7 +527,7 @@ size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int 
                                   int num_splits) {
   if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits) || Tn < 1 || Tn > kMaxTree) return 0;
   // (an 8-bit cache's plan takes no less room)
-  const GroupPlan p = tree_plan(B, Hq, Hkv, Tn, true, Lmax, num_splits);
+  const GroupPlan p = tree_plan(B, Hq, Hkv, Tn, d, true, Lmax, num_splits);
   return TreeSpace(p, B, Hq, Hkv, Tn, d).total;
 }
 

@@ -52,9 +52,9 @@ struct Cfg {
   static constexpr int STAGE = 2 * TILE;
   static constexpr int ROWS = 8 * NT;               // query rows of a CTA
   static constexpr int QS = 2 * D + 16;             // bytes between query rows (no bank twice)
-  // resident CTAs and ring: about 190 KB in flight per SM
-  static constexpr int CTAS = F8 ? 3 : 2;
-  static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? 4 : 6);
+  // resident CTAs (group_attn_ctas) and ring: 160-190 KB in flight per SM
+  static constexpr int CTAS = group_attn_ctas(D, F8, ROWS);
+  static constexpr int NS = STAGE == 32768 ? 3 : (STAGE == 16384 ? (F8 && CTAS == 2 ? 5 : 4) : 6);
   static constexpr int RING = NS * STAGE;
   static constexpr int Q_BYTES = ROWS * QS;         // twice: the next piece's go to the other
   static constexpr int BARS = 192;

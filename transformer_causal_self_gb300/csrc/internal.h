@@ -242,6 +242,12 @@ inline GroupLine group_line(const GroupArgs& a) {
   return GroupLine{a.lens,     a.seg, a.B,         a.drafts, a.min_len, a.max_seq_len - a.drafts,
                    a.plan.unit, a.Hkv * a.plan.rblocks, a.plan.tiles_per_cta, a.plan.least_tiles};
 }
+// CTAs of launch_group_attn's kernel per SM.  e4m3: three, except where 16 query rows of 128
+// channels do not fit 128 registers a thread (8 sequences of 8000 rows: 45 us with two, 68 with
+// three and what they spill).
+constexpr int group_attn_ctas(int d, bool f8, int block_rows) {
+  return f8 && !(d == 128 && block_rows > 8) ? 3 : 2;
+}
 cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
 // The same on tcgen05, for many query rows; rope is 0.
 cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream);
