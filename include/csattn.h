@@ -522,8 +522,9 @@ int csattn_cache_append_paged(const void* k_new, const void* v_new, void* k_page
  * largest finite magnitude of the row; for keys that are rotated, sqrt(2) * a of the row
  * before its rotation, so that the code does not depend on the position.  Each value is
  * rounded once (to nearest even) from fp32; infinities and NaN are stored as NaN, and what
- * would round to 2^128 as 1.875 * 2^127.  The value x8 * 2^(code - 127) is a bf16 number, so reading a row back is exact.  The calls
- * below read codes in [3, 247] (another code reads as some power of two, infinity or 0).
+ * would round to 2^128 as 1.875 * 2^127.  The value x8 * 2^(code - 127) is a bf16 number, so
+ * reading a row back is exact.  The calls below read codes in [3, 247] (another code reads as
+ * some power of two, infinity or 0).
  */
 
 /*
@@ -582,7 +583,8 @@ size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d,
  *             11 bits) when rope_base > 0, used as given otherwise
  *   seq_lens  device int32 [B], 1 <= seq_lens[b] <= max_seq_len <= Lmax
  *   out       [B, Hq, 1, d] bf16
- *   num_splits  0: automatic; > 0: splits of every sequence's rows
+ *   num_splits  0: automatic; > 0: the work is cut into pieces of ceil(max_seq_len / num_splits)
+ *               rows, in whole tiles of 64
  *   workspace   >= csattn_decode_fp8_workspace_size() bytes, 16-byte aligned, in use until the
  *             work on `stream` completes (calls that may run at once need one each)
  * Requirements: dtype CSATTN_BF16 (of q and out), d in {64, 128}, any Hq / Hkv,
@@ -631,10 +633,14 @@ size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int 
  *              cache (CSATTN_BF16)
  *   cache_lens device int32 [B], 0 <= cache_lens[b] <= max_seq_len - Tn; not modified
  *   out        [B, Hq, Tn, d] bf16;  lse  NULL or fp32 [B, Hq, Tn] (natural log)
- *   rope_base, rope_layout  as csattn_attn_fwd;  scale, num_splits as csattn_attn_decode
+ *   rope_base, rope_layout  as csattn_attn_fwd;  scale as csattn_attn_decode, num_splits as
+ *              csattn_attn_decode_fp8 (tiles of 64 or 128 rows)
  *   max_seq_len  bounds cache_lens[b] + Tn (<= Lmax; <= 49152 with RoPE)
  *   workspace  >= csattn_tree_workspace_size() bytes, 16-byte aligned, in use until the work on
  *              `stream` completes (calls that may run at once need one each)
+ * Over an 8-bit cache the rotated queries are rounded to 11 bits and, with more than 16 query
+ * rows per KV head (Tn * Hq / Hkv), 128 cache rows share an exponent in the products: what is
+ * below 2^-30 of the largest key or value among them loses bits, below 2^-40 it vanishes.
  * Requirements: 1 <= Tn <= 256, d in {64, 128}, any Hq / Hkv.  Values of drafts that a query
  * does not see have no part in its output whatever they hold (NaN and infinities included).
  * Rows at or past cache_lens[b] + Tn are neither used nor written.  A length out of range or

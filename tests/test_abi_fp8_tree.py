@@ -156,6 +156,32 @@ def test_workspace_sizes_cover_every_length():
     assert csattn.tree_workspace_size(1, 8, 8, 257, 1000, 64) == 0
 
 
+@pytest.mark.parametrize("d,Hq,Tn", [(64, 8, 1), (128, 8, 2), (128, 12, 1), (128, 8, 12), (64, 32, 64)])
+def test_tree_workspace_covers_both_caches(lib, d, Hq, Tn):
+    import re
+    for splits in (0, 3):
+        for msl in (256, 3000, 30000):
+            have = lib.csattn_tree_workspace_size(4, Hq, 1, Tn, 30000, d, splits)
+            for cache, scales in ((1, None), (2, FAKE)):
+                assert call(lib, "tree", False, B=4, Hq=Hq, Hkv=1, Tn=Tn, Lmax=30000, msl=msl, d=d,
+                            cache=cache, ks=scales, vs=scales, splits=splits, wb=0) == -5
+                need = int(re.search(rb"workspace of (\d+) bytes",
+                                     lib.csattn_last_error()).group(1))
+                assert 0 < need <= have
+
+
+def test_sizes_past_the_limits(lib):
+    for kw in (dict(Hq=2 * ((1 << 20) + 2), wb=1 << 60), dict(B=65535, Hq=8192, Tn=8, wb=1 << 60)):
+        for op in (["decode", "tree"] if "B" not in kw else ["tree"]):
+            assert call(lib, op, False, **kw) == -2, op
+            assert b"too large" in lib.csattn_last_error()
+    assert lib.csattn_decode_fp8_workspace_size(1, 1 << 21, 1, 100, 64, 0) == 0
+    assert lib.csattn_decode_fp8_workspace_size(1 << 20, 8, 8, 100, 64, 0) == 0
+    assert lib.csattn_decode_fp8_workspace_size(1, 8, 8, 1 << 30, 64, 0) == 0
+    assert lib.csattn_decode_fp8_workspace_size(1, 8, 8, 100, 96, 0) == 0
+    assert lib.csattn_tree_workspace_size(65535, 8192, 8, 8, 100, 64, 0) == 0
+
+
 def test_binding_refuses_wrong_tensors():
     """CPU tensors, before anything is launched."""
     import transformer_causal_self_gb300 as csattn

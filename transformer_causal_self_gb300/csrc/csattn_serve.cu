@@ -13,6 +13,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kMaxTree = 256;  // drafts of a tree
+constexpr int kMaxHeads = 1 << 20;
 
 // The paged arguments; *lmax receives the rows a sequence has room for.
 int check_pages(const char* fn, const int32_t* block_table, int Hkv, int page_size, int num_pages,
@@ -105,8 +106,8 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
   if (num_splits < 0) return api_fail(CSATTN_ERR_INVALID_ARG, "%s: num_splits < 0", fn);
   if (!std::isfinite(scale))
     return api_fail(CSATTN_ERR_INVALID_ARG, "%s: scale not finite", fn);
-  if (static_cast<long long>(B) * Hq * T > (1LL << 31) - 1)
-    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: B * Hq * queries too large", fn);
+  if (Hq > kMaxHeads || static_cast<long long>(B) * Hq * T > (1LL << 31) - 1)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Hq=%d or B * Hq * queries too large", fn, Hq);
   return CSATTN_OK;
 }
 
@@ -114,7 +115,10 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
 // or, with an explicit number of splits, as many CTAs as parts of that many equal ones of the
 // longest sequence can fill.
 constexpr int kSms = 152;
-constexpr int kTcRows = 16;  // trees with more query rows than this go to launch_group_tc
+// Trees with more query rows per KV head than this go to launch_group_tc (128 channels, 8
+// sequences of 8000 rows; here / there: 16 rows bf16 57 / 58 us, e4m3 45 / 58; 20 rows 91 / 58
+// and 69 / 58, the cache being read once per 16 rows here).
+constexpr int kTcRows = 16;
 
 GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, bool f8, int max_seq_len,
                    int num_splits) {
@@ -169,8 +173,11 @@ int check_line(const char* fn, const GroupPlan& p, int B, int Hkv, int max_seq_l
   return CSATTN_OK;
 }
 
-bool sizes_ok(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
-  return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Lmax >= 1 && d >= 1 && num_splits >= 0;
+// (as check_cache and check_heads, for the workspace sizes)
+bool sizes_ok(int B, int Hq, int Hkv, int T, int Lmax, int d, int num_splits) {
+  return B >= 1 && B <= 65535 && Hq >= 1 && Hq <= kMaxHeads && Hkv >= 1 && Hkv <= 65535 &&
+         Hq % Hkv == 0 && static_cast<long long>(B) * Hq * T <= (1LL << 31) - 1 && Lmax >= 1 &&
+         Lmax < (1 << 30) && (d == 64 || d == 128) && num_splits >= 0;
 }
 
 int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
@@ -489,7 +496,7 @@ int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const 
 }
 
 size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
-  if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits)) return 0;
+  if (!sizes_ok(B, Hq, Hkv, 1, Lmax, d, num_splits)) return 0;
   const GroupPlan p = plan_for(B, Hkv, Hq / Hkv, d, false, true, Lmax, num_splits);
   return align256(partial_bytes(p, B, Hkv, d)) + seg_bytes(p, B, Hkv);
 }
@@ -525,7 +532,7 @@ int csattn_attn_decode_fp8_paged(const void* q, const void* k_pages, const void*
 
 size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int d,
                                   int num_splits) {
-  if (!sizes_ok(B, Hq, Hkv, Lmax, d, num_splits) || Tn < 1 || Tn > kMaxTree) return 0;
+  if (Tn < 1 || Tn > kMaxTree || !sizes_ok(B, Hq, Hkv, Tn, Lmax, d, num_splits)) return 0;
   // (an 8-bit cache's plan takes no less room)
   const GroupPlan p = tree_plan(B, Hq, Hkv, Tn, d, true, Lmax, num_splits);
   return TreeSpace(p, B, Hq, Hkv, Tn, d).total;
