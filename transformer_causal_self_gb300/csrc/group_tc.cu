@@ -272,370 +272,371 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   const int step = pair ? 1 : 2;  // between a stream's tiles
 
   if (warp >= 8 && warp < 12) {
-   if constexpr (F8) regs_dec<64>();
-   if (warp == kWarpProducer) {
-    // ------------------------------------------------------------ TMA producer
-    // fills K_0, V_0, K_1, V_1, ...; lane i copies box i of a tile (see group_attn.cu)
-    const CacheRows& R = p.rows;
-    const int nbox = BN / p.box_rows, r0 = lane * p.box_rows;
-    const uint32_t depth = F8 ? C::NRAW : NS;
-    uint64_t* full = F8 ? raw_full : kv_full;
-    uint64_t* empty = F8 ? raw_empty : kv_empty;
-    uint32_t f = 0, edges = 0, piece = 0, queries = 0;
-    uint64_t recent = 0;  // a byte per fill, the latest lowest: 8 + (edge % 8), or 0
-    bool ok = true;
-    // The piece's queries, once the products with the last piece's are done: behind its first
-    // tile, so that this wait does not hold that up.
-    auto load_queries = [&](const View& w) {
-      bool done = true;
-      if (lane == 0 && queries > 0)
-        done = ctl_wait(q_empty, (queries - 1) & 1, abort_flag, p.status, kWaitNs);
-      if (!__all_sync(0xffffffffu, done)) return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, (1 + pair) * C::TILE);
-        for (int x = 0; x <= pair; ++x)
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(sQ + x * C::TILE + kb * (BN * 128), &tm_q, q_full, kb * 64,
-                        (w.rb * (1 + pair) + x) * BN, w.b * p.Hkv + w.kvh);
-      }
-      ++queries;
-      __syncwarp();
-      return true;
-    };
-    // (the kernel before wrote queries and the drafts' rows by plain stores)
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    if (pc.n > 0) load_queries(View(pc, p));
-    for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
-      const View w(pc, p);
-      for (int j = 0; j < w.n && ok; ++j) {
-        if (j == 1 && piece > 0 && !(ok = load_queries(w))) break;
-        int plane = w.b * p.Hkv + w.kvh, prow = w.k_begin + j * BN;
-        if (lane < nbox && R.block_table != nullptr) {
-          const int tr = prow + r0;
-          plane = R.num_pages * p.Hkv;
-          prow = 0;
-          if (tr < w.total) {
-            const int page =
-                R.block_table[static_cast<size_t>(w.b) * R.max_pages + tr / R.page_size];
-            if (page >= 0 && page < R.num_pages)
-              plane = page * p.Hkv + w.kvh;
-            else
-              atomicOr(p.status, kStatusDeviceArg);
-            prow = tr % R.page_size;
-          }
+    if constexpr (F8) regs_dec<64>();
+    if (warp == kWarpProducer) {
+      // ------------------------------------------------------------ TMA producer
+      // fills K_0, V_0, K_1, V_1, ...; lane i copies box i of a tile (see group_attn.cu)
+      const CacheRows& R = p.rows;
+      const int nbox = BN / p.box_rows, r0 = lane * p.box_rows;
+      const uint32_t depth = F8 ? C::NRAW : NS;
+      uint64_t* full = F8 ? raw_full : kv_full;
+      uint64_t* empty = F8 ? raw_empty : kv_empty;
+      uint32_t f = 0, edges = 0, piece = 0, queries = 0;
+      uint64_t recent = 0;  // a byte per fill, the latest lowest: 8 + (edge % 8), or 0
+      bool ok = true;
+      // The piece's queries, once the products with the last piece's are done: behind its first
+      // tile, so that this wait does not hold that up.
+      auto load_queries = [&](const View& w) {
+        bool done = true;
+        if (lane == 0 && queries > 0)
+          done = ctl_wait(q_empty, (queries - 1) & 1, abort_flag, p.status, kWaitNs);
+        if (!__all_sync(0xffffffffu, done)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, (1 + pair) * C::TILE);
+          for (int x = 0; x <= pair; ++x)
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_load_3d(sQ + x * C::TILE + kb * (BN * 128), &tm_q, q_full, kb * 64,
+                          (w.rb * (1 + pair) + x) * BN, w.b * p.Hkv + w.kvh);
         }
-        for (int v = 0; v < 2; ++v, ++f) {
-          const uint32_t s = f % depth, use = f / depth;
-          // bf16 values of edge tiles go by way of the cleaning warps
-          const bool edge = !F8 && v == 1 && j >= w.first_edge;
-          uint64_t* landed = edge ? &edge_full[edges & 3] : &full[s];
-          int okw = 1;
-          if (lane == 0) {
-            if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
-              okw = 0;
-            else
-              mbar_arrive_expect_tx(landed, F8 ? C::RAW : C::TILE);
-          }
-          if (!__shfl_sync(0xffffffffu, okw, 0)) {
-            ok = false;
-            break;
-          }
-          const CUtensorMap* tm = v == 0 ? &tm_k : &tm_v;
-          if (lane < nbox) {
-            if constexpr (F8) {
-              tma_load_3d(sRaw + s * C::RAW + r0 * D, tm, landed, 0, prow, plane);
-            } else {
-              for (int kb = 0; kb < D / 64; ++kb)
-                tma_load_3d(sKV + s * C::TILE + kb * (BN * 128) + r0 * 128, tm, landed, kb * 64,
-                            prow, plane);
+        ++queries;
+        __syncwarp();
+        return true;
+      };
+      // (the kernel before wrote queries and the drafts' rows by plain stores)
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      if (pc.n > 0) load_queries(View(pc, p));
+      for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
+        const View w(pc, p);
+        for (int j = 0; j < w.n && ok; ++j) {
+          if (j == 1 && piece > 0 && !(ok = load_queries(w))) break;
+          int plane = w.b * p.Hkv + w.kvh, prow = w.k_begin + j * BN;
+          if (lane < nbox && R.block_table != nullptr) {
+            const int tr = prow + r0;
+            plane = R.num_pages * p.Hkv;
+            prow = 0;
+            if (tr < w.total) {
+              const int page =
+                  R.block_table[static_cast<size_t>(w.b) * R.max_pages + tr / R.page_size];
+              if (page >= 0 && page < R.num_pages)
+                plane = page * p.Hkv + w.kvh;
+              else
+                atomicOr(p.status, kStatusDeviceArg);
+              prow = tr % R.page_size;
             }
           }
-          recent = (recent << 8) | (edge ? 8u + (edges & 7u) : 0u);
-          edges += edge;
-          __syncwarp();
-        }
-      }
-      if (ok && w.n == 1 && piece > 0) ok = load_queries(w);
-    }
-    if (lane == 0 && *abort_flag) {
-      // every copy still in flight lands before the CTA's shared memory is released
-      for (uint32_t i = 1; i <= depth && i <= f; ++i, recent >>= 8) {
-        const uint32_t e = recent & 15u;
-        mbar_wait(e ? &edge_full[e & 3u] : &full[(f - i) % depth],
-                  e ? (e >> 2) & 1u : ((f - i) / depth) & 1u, nullptr, p.status, kDrainNs);
-      }
-      if (queries > 0) mbar_wait(q_full, (queries - 1) & 1, nullptr, p.status, kDrainNs);
-    }
-   } else if (warp == kWarpMma) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp keeps the books, so that addresses stay in uniform registers; one lane
-    // issues.  Descriptors differ in their low words alone, by constants within a product, and
-    // all waits of a step come ahead of its products: the tensor core's queue is short.
-    const bool leader = elect_one();
-    const uint64_t hi = smem_desc_sw128(0, 16, 1024), hi_v = smem_desc_sw128(0, BN * 128, 1024);
-    const uint32_t q_lo = smem_u32(sQ) >> 4, kv_lo = smem_u32(sKV) >> 4;
-    constexpr uint32_t kIdS = idesc(F8, BN, 0), kIdO = idesc(F8, D, 1);
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = warp_wait(bar, parity, abort_flag, p.status);
-      return ok;
-    };
-    auto full = [&](uint32_t f) { return wait(&kv_full[f % NS], (f / NS) & 1); };
-    // S_x = Q K^T with the keys of fill f
-    auto qk = [&](int x, uint32_t f) {
-      const uint64_t q = hi + q_lo + (pair ? x : 0) * (C::TILE >> 4);
-      const uint64_t k = hi + kv_lo + (f % NS) * (C::TILE >> 4);
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = static_cast<uint32_t>((kk >> 2) * (BN * 8) + (kk & 3) * 2);
-          umma_ss(tmem + 128u * x, q + off, k + off, kIdS, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(&s_full[x]);
-      }
-      __syncwarp();
-    };
-    auto pv = [&](int x, uint32_t f, bool accumulate) {
-      const uint64_t v = hi_v + kv_lo + (f % NS) * (C::TILE >> 4);
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          umma_ts(tmem + 256u + D * x, tmem + 128u * x + 8u * kk, v + 128u * kk, kIdO,
-                  (accumulate || kk > 0) ? 1u : 0u);
-      }
-      __syncwarp();
-    };
-    auto release = [&](uint64_t* bar) {  // when what has been issued is done
-      if (leader) tc_commit(bar);
-      __syncwarp();
-    };
-    uint32_t F = 0, np[2] = {0, 0}, used[2] = {0, 0}, piece = 0;
-    for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
-      const int n = pc.n;
-      wait(q_full, piece & 1);
-      // first tiles of both streams
-      for (int j = 0; j < step && j < n; ++j) {
-        if (!full(F + 2 * j)) break;
-        tc_fence_after();
-        for (int x = pair ? 0 : j; x <= (pair ? 1 : j); ++x) qk(x, F + 2 * j);
-        release(&kv_empty[(F + 2 * j) % NS]);
-        if (j == n - 1) release(q_empty);
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        const int x0 = pair ? 0 : (j & 1), x1 = pair ? 1 : x0, jn = j + step;
-        if (!full(F + 2 * j + 1) || (jn < n && !full(F + 2 * jn))) break;
-        for (int x = x0; x <= x1 && ok; ++x) {
-          // the stream's first tile of a piece: its O has been read
-          if (j < step) {
-            if (used[x] > 0 && !wait(&o_empty[x], (used[x] - 1) & 1)) break;
-            ++used[x];
+          for (int v = 0; v < 2; ++v, ++f) {
+            const uint32_t s = f % depth, use = f / depth;
+            // bf16 values of edge tiles go by way of the cleaning warps
+            const bool edge = !F8 && v == 1 && j >= w.first_edge;
+            uint64_t* landed = edge ? &edge_full[edges & 3] : &full[s];
+            int okw = 1;
+            if (lane == 0) {
+              if (use > 0 && !ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs))
+                okw = 0;
+              else
+                mbar_arrive_expect_tx(landed, F8 ? C::RAW : C::TILE);
+            }
+            if (!__shfl_sync(0xffffffffu, okw, 0)) {
+              ok = false;
+              break;
+            }
+            const CUtensorMap* tm = v == 0 ? &tm_k : &tm_v;
+            if (lane < nbox) {
+              if constexpr (F8) {
+                tma_load_3d(sRaw + s * C::RAW + r0 * D, tm, landed, 0, prow, plane);
+              } else {
+                for (int kb = 0; kb < D / 64; ++kb)
+                  tma_load_3d(sKV + s * C::TILE + kb * (BN * 128) + r0 * 128, tm, landed, kb * 64,
+                              prow, plane);
+              }
+            }
+            recent = (recent << 8) | (edge ? 8u + (edges & 7u) : 0u);
+            edges += edge;
+            __syncwarp();
           }
-          if (!wait(&p_full[x], np[x] & 1)) break;
-          ++np[x];
+        }
+        if (ok && w.n == 1 && piece > 0) ok = load_queries(w);
+      }
+      if (lane == 0 && *abort_flag) {
+        // every copy still in flight lands before the CTA's shared memory is released
+        for (uint32_t i = 1; i <= depth && i <= f; ++i, recent >>= 8) {
+          const uint32_t e = recent & 15u;
+          mbar_wait(e ? &edge_full[e & 3u] : &full[(f - i) % depth],
+                    e ? (e >> 2) & 1u : ((f - i) / depth) & 1u, nullptr, p.status, kDrainNs);
+        }
+        if (queries > 0) mbar_wait(q_full, (queries - 1) & 1, nullptr, p.status, kDrainNs);
+      }
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp keeps the books, so that addresses stay in uniform registers; one lane
+      // issues.  Descriptors differ in their low words alone, by constants within a product, and
+      // all waits of a step come ahead of its products: the tensor core's queue is short.
+      const bool leader = elect_one();
+      const uint64_t hi = smem_desc_sw128(0, 16, 1024), hi_v = smem_desc_sw128(0, BN * 128, 1024);
+      const uint32_t q_lo = smem_u32(sQ) >> 4, kv_lo = smem_u32(sKV) >> 4;
+      constexpr uint32_t kIdS = idesc(F8, BN, 0), kIdO = idesc(F8, D, 1);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = warp_wait(bar, parity, abort_flag, p.status);
+        return ok;
+      };
+      auto full = [&](uint32_t f) { return wait(&kv_full[f % NS], (f / NS) & 1); };
+      // S_x = Q K^T with the keys of fill f
+      auto qk = [&](int x, uint32_t f) {
+        const uint64_t q = hi + q_lo + (pair ? x : 0) * (C::TILE >> 4);
+        const uint64_t k = hi + kv_lo + (f % NS) * (C::TILE >> 4);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = static_cast<uint32_t>((kk >> 2) * (BN * 8) + (kk & 3) * 2);
+            umma_ss(tmem + 128u * x, q + off, k + off, kIdS, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[x]);
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int x, uint32_t f, bool accumulate) {
+        const uint64_t v = hi_v + kv_lo + (f % NS) * (C::TILE >> 4);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            umma_ts(tmem + 256u + D * x, tmem + 128u * x + 8u * kk, v + 128u * kk, kIdO,
+                    (accumulate || kk > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+      };
+      auto release = [&](uint64_t* bar) {  // when what has been issued is done
+        if (leader) tc_commit(bar);
+        __syncwarp();
+      };
+      uint32_t F = 0, np[2] = {0, 0}, used[2] = {0, 0}, piece = 0;
+      for (; pc.n > 0 && ok; pc.next(p.line), ++piece) {
+        const int n = pc.n;
+        wait(q_full, piece & 1);
+        // first tiles of both streams
+        for (int j = 0; j < step && j < n; ++j) {
+          if (!full(F + 2 * j)) break;
           tc_fence_after();
-          pv(x, F + 2 * j + 1, j >= step);
-          if (x == x1) release(&kv_empty[(F + 2 * j + 1) % NS]);
-          if (jn >= n) {
-            release(&o_full[x]);
-          } else {
-            qk(x, F + 2 * jn);
-            if (x == x1) {
-              release(&kv_empty[(F + 2 * jn) % NS]);
-              if (jn == n - 1) release(q_empty);
+          for (int x = pair ? 0 : j; x <= (pair ? 1 : j); ++x) qk(x, F + 2 * j);
+          release(&kv_empty[(F + 2 * j) % NS]);
+          if (j == n - 1) release(q_empty);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int x0 = pair ? 0 : (j & 1), x1 = pair ? 1 : x0, jn = j + step;
+          if (!full(F + 2 * j + 1) || (jn < n && !full(F + 2 * jn))) break;
+          for (int x = x0; x <= x1 && ok; ++x) {
+            // the stream's first tile of a piece: its O has been read
+            if (j < step) {
+              if (used[x] > 0 && !wait(&o_empty[x], (used[x] - 1) & 1)) break;
+              ++used[x];
+            }
+            if (!wait(&p_full[x], np[x] & 1)) break;
+            ++np[x];
+            tc_fence_after();
+            pv(x, F + 2 * j + 1, j >= step);
+            if (x == x1) release(&kv_empty[(F + 2 * j + 1) % NS]);
+            if (jn >= n) {
+              release(&o_full[x]);
+            } else {
+              qk(x, F + 2 * jn);
+              if (x == x1) {
+                release(&kv_empty[(F + 2 * jn) % NS]);
+                if (jn == n - 1) release(q_empty);
+              }
             }
           }
         }
+        F += 2 * n;
       }
-      F += 2 * n;
-    }
-    // every MMA issued above has completed once this barrier flips
-    release(teardown);
-    if (leader) mbar_wait(teardown, 0, nullptr, p.status, kDrainNs);
-    __syncwarp();
-   } else if (!F8) {
-    // ------------------------------------------------------------ clean values (bf16)
-    // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
-    // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
-    // merge puts it where it belongs).
-    bool ok = true;
-    uint32_t F = 0, edges = 0;
-    for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the two warps' barriers go together)
-      const View w(pc, p);
-      for (int j = w.first_edge; j < w.n; ++j, ++edges) {
-        const uint32_t s = (F + 2 * j + 1) % NS;
-        ok = ok && warp_wait(&edge_full[edges & 3], (edges >> 2) & 1, abort_flag, p.status);
-        const int key0 = w.k_begin + j * BN;
-        uint8_t* tile = sKV + s * C::TILE;
-        for (int e = threadIdx.x - 32 * kWarpClean; ok && e < BN * (D / 8); e += 64) {
-          // (chunks of a row in any order: all are treated alike)
-          const int kb = e / (BN * 8), r = e / 8 % BN, c = e % 8;
-          if (key0 + r < w.L) continue;
-          uint4* at = reinterpret_cast<uint4*>(tile + kb * (BN * 128) + r * 128 + c * 16);
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (key0 + r < w.k_end) {
-            v = *at;
-            v = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z),
-                           finite_bf16x2(v.w));
+      // every MMA issued above has completed once this barrier flips
+      release(teardown);
+      if (leader) mbar_wait(teardown, 0, nullptr, p.status, kDrainNs);
+      __syncwarp();
+    } else if (!F8) {
+      // ------------------------------------------------------------ clean values (bf16)
+      // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
+      // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
+      // merge puts it where it belongs).
+      bool ok = true;
+      uint32_t F = 0, edges = 0;
+      for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the two warps' barriers go together)
+        const View w(pc, p);
+        for (int j = w.first_edge; j < w.n; ++j, ++edges) {
+          const uint32_t s = (F + 2 * j + 1) % NS;
+          ok = ok && warp_wait(&edge_full[edges & 3], (edges >> 2) & 1, abort_flag, p.status);
+          const int key0 = w.k_begin + j * BN;
+          uint8_t* tile = sKV + s * C::TILE;
+          for (int e = threadIdx.x - 32 * kWarpClean; ok && e < BN * (D / 8); e += 64) {
+            // (chunks of a row in any order: all are treated alike)
+            const int kb = e / (BN * 8), r = e / 8 % BN, c = e % 8;
+            if (key0 + r < w.L) continue;
+            uint4* at = reinterpret_cast<uint4*>(tile + kb * (BN * 128) + r * 128 + c * 16);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (key0 + r < w.k_end) {
+              v = *at;
+              v = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z),
+                             finite_bf16x2(v.w));
+            }
+            *at = v;
           }
-          *at = v;
+          fence_proxy_async_smem();
+          asm volatile("bar.sync 3, 64;" ::: "memory");
+          if (ok && threadIdx.x == 32 * kWarpClean) mbar_arrive(&kv_full[s]);
         }
-        fence_proxy_async_smem();
-        asm volatile("bar.sync 3, 64;" ::: "memory");
-        if (ok && threadIdx.x == 32 * kWarpClean) mbar_arrive(&kv_full[s]);
+        F += 2 * w.n;
       }
-      F += 2 * w.n;
     }
-   }
   } else if (warp >= kWarpConvert) {
     // ------------------------------------------------------------ e4m3 tiles to f16
     if constexpr (F8) {
-    regs_dec<72>();
-    const int v = (warp - kWarpConvert) >> 2;  // 0: keys, 1: values
-    const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;
-    constexpr int G = D / 16;                  // 16-channel pieces of a row
-    const uint32_t raw0 = smem_u32(sRaw), kv0 = smem_u32(sKV);
-    // The thread's piece: column c of row r0.  Eight lanes share a wavefront, and a row's pieces
-    // c and c + 4 go to the same banks (to the tile's two halves); so at 128 channels two rows
-    // change places in their upper four pieces, and odd rows' chunks lie between even ones'.
-    const int c = tid % G;
-    const int r0 = D == 128 ? 2 * (tid >> 4) + (((tid >> 2) ^ (tid >> 3)) & 1) : tid / G;
-    uint32_t to0, to1;                         // where the thread's two chunks go in a tile
-    {
-      const uint32_t at = (c >> 2) * (BN * 128) + r0 * 128;
-      to0 = at + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
-      to1 = at + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
-    }
-    const int ps = p.rows.block_table != nullptr ? p.rows.page_size : 0;
-    bool ok = true;
-    uint32_t f = v, tile = 0;                  // its next fill, and tile of the CTA
-    for (; pc.n > 0 && ok; pc.next(p.line)) {
-      const View w(pc, p);
-      // Scale bytes: every warp has those of all 128 rows, four per lane (no page ends inside
-      // them), packed.  The page number comes first, so each of the two loads is issued a tile
-      // ahead of its use, and taken over at the tile's end (a register move waits for a load).
-      const int row0 = w.k_begin + 4 * lane;
-      int pg = ps > 0 ? row0 / ps : 0, ofs = row0 - pg * ps;  // of the next page lookup
-      const int32_t* const table =
-          p.rows.block_table + static_cast<size_t>(w.b) * p.rows.max_pages;
-      auto load_page = [&](int j) -> int {
-        const int page = ps > 0 && j < w.n && row0 + j * BN < w.k_end ? table[pg] : 0;
-        if (ps >= BN) {
-          ofs += BN;
-          if (ofs >= ps) ++pg, ofs -= ps;
-        } else if (ps > 0) {
-          pg += BN / ps;
-        }
-        return page;
-      };
-      // four rows' bytes of an array; 0 where there is no row
-      auto load_codes = [&](const uint8_t* scale, int j, int page, int at_ofs) -> uint32_t {
-        const int r = row0 + j * BN, left = w.k_end - r;
-        if (j >= w.n || left <= 0) return 0u;
-        size_t at;
-        if (ps == 0) {
-          at = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.rows.Lmax + r;
-        } else {
-          if (page < 0 || page >= p.rows.num_pages) return 0u;
-          at = (static_cast<size_t>(page) * p.Hkv + w.kvh) * ps + at_ofs;
-        }
-        if (p.scale_words) return *reinterpret_cast<const uint32_t*>(scale + at);
-        uint32_t x = 0u;
-        for (int i = 0; i < min(left, 4); ++i) x |= static_cast<uint32_t>(scale[at + i]) << (8 * i);
-        return x;
-      };
-      auto valid = [&](int j) -> uint32_t {  // bytes of rows there are
-        const int left = w.k_end - (row0 + j * BN);
-        return left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
-      };
-      int ofs1 = ofs;
-      int page = load_page(0);
-      uint32_t ck = v == 0 ? load_codes(p.k_scale, 0, page, ofs1) : 0u;
-      uint32_t cv = load_codes(p.v_scale, 0, page, ofs1);
-      ofs1 = ofs;
-      page = load_page(1);
-      for (int j = 0; j < w.n; ++j, f += 2, ++tile) {
-        const int key0 = w.k_begin + j * BN;
-        const uint32_t nk = v == 0 ? load_codes(p.k_scale, j + 1, page, ofs1) : 0u;
-        const uint32_t nv = load_codes(p.v_scale, j + 1, page, ofs1);
-        const uint32_t there = valid(j);
-        ck &= there;
-        cv &= there;
-        const int ofs2 = ofs;
-        const int page_next = load_page(j + 2);
-        // the tile's largest codes, then the factors of the warp's 32 rows, one per lane: row
-        // i * (128 / G) + (32 / G) * warp + q of the tile in lane (32 / G) * i + q
-        const uint32_t hv = __vmaxu2(cv & 0xff00ffu, (cv >> 8) & 0xff00ffu);
-        int E = max(static_cast<int>(__reduce_max_sync(0xffffffffu, max(hv & 0xffffu, hv >> 16))),
-                    kMinValueCode);
-        if (v == 0) {
-          const float Ev = static_cast<float>(E - 127);
-          const uint32_t hk = __vmaxu2(ck & 0xff00ffu, (ck >> 8) & 0xff00ffu);
-          E = __reduce_max_sync(0xffffffffu, max(hk & 0xffffu, hk >> 16));
-          if (tid == 0)
-            s_tile[tile & 7] =
-                make_float2(__uint_as_float(static_cast<uint32_t>(max(E - 7, 1)) << 23), Ev);
-        }
-        uint32_t factor;
-        {
-          constexpr int Q = 32 / G;
-          const int r = (lane / Q) * (128 / G) + Q * (warp & 3) + lane % Q;
-          const uint32_t four = __shfl_sync(0xffffffffu, v == 0 ? ck : cv, r >> 2);
-          factor = row_scale(E - static_cast<int>((four >> (8 * (r & 3))) & 0xffu));
-          factor |= factor << 16;
-        }
-        const uint32_t rs = f % C::NRAW, s = f % NS;
-        ok = warp_wait(&raw_full[rs], (f / C::NRAW) & 1, abort_flag, p.status) &&
-             (f < static_cast<uint32_t>(NS) ||
-              warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
-        if (!ok) break;
-        const bool edge = key0 + BN > min(w.L, w.k_end);
-        // piece i of the thread is row i * (128 / G) + r0
-        constexpr int kRowStep = 128 / G;  // (a multiple of 8: the swizzle stays)
-        const uint32_t src = raw0 + rs * C::RAW + r0 * D + 16 * c;
-        const uint32_t dst0 = kv0 + s * C::TILE + to0, dst1 = kv0 + s * C::TILE + to1;
+      regs_dec<72>();
+      const int v = (warp - kWarpConvert) >> 2;  // 0: keys, 1: values
+      const int tid = (threadIdx.x - 32 * kWarpConvert) & 127;
+      constexpr int G = D / 16;                  // 16-channel pieces of a row
+      const uint32_t raw0 = smem_u32(sRaw), kv0 = smem_u32(sKV);
+      // The thread's piece: column c of row r0.  Eight lanes share a wavefront, and a row's pieces
+      // c and c + 4 go to the same banks (to the tile's two halves); so at 128 channels two rows
+      // change places in their upper four pieces, and odd rows' chunks lie between even ones'.
+      const int c = tid % G;
+      const int r0 = D == 128 ? 2 * (tid >> 4) + (((tid >> 2) ^ (tid >> 3)) & 1) : tid / G;
+      uint32_t to0, to1;                         // where the thread's two chunks go in a tile
+      {
+        const uint32_t at = (c >> 2) * (BN * 128) + r0 * 128;
+        to0 = at + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
+        to1 = at + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
+      }
+      const int ps = p.rows.block_table != nullptr ? p.rows.page_size : 0;
+      bool ok = true;
+      uint32_t f = v, tile = 0;                  // its next fill, and tile of the CTA
+      for (; pc.n > 0 && ok; pc.next(p.line)) {
+        const View w(pc, p);
+        // Scale bytes: every warp has those of all 128 rows, four per lane (no page ends inside
+        // them), packed.  The page number comes first, so each of the two loads is issued a tile
+        // ahead of its use, and taken over at the tile's end (a register move waits for a load).
+        const int row0 = w.k_begin + 4 * lane;
+        int pg = ps > 0 ? row0 / ps : 0, ofs = row0 - pg * ps;  // of the next page lookup
+        const int32_t* const table =
+            p.rows.block_table + static_cast<size_t>(w.b) * p.rows.max_pages;
+        auto load_page = [&](int j) -> int {
+          const int page = ps > 0 && j < w.n && row0 + j * BN < w.k_end ? table[pg] : 0;
+          if (ps >= BN) {
+            ofs += BN;
+            if (ofs >= ps) ++pg, ofs -= ps;
+          } else if (ps > 0) {
+            pg += BN / ps;
+          }
+          return page;
+        };
+        // four rows' bytes of an array; 0 where there is no row
+        auto load_codes = [&](const uint8_t* scale, int j, int page, int at_ofs) -> uint32_t {
+          const int r = row0 + j * BN, left = w.k_end - r;
+          if (j >= w.n || left <= 0) return 0u;
+          size_t at;
+          if (ps == 0) {
+            at = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.rows.Lmax + r;
+          } else {
+            if (page < 0 || page >= p.rows.num_pages) return 0u;
+            at = (static_cast<size_t>(page) * p.Hkv + w.kvh) * ps + at_ofs;
+          }
+          if (p.scale_words) return *reinterpret_cast<const uint32_t*>(scale + at);
+          uint32_t x = 0u;
+          for (int i = 0; i < min(left, 4); ++i)
+            x |= static_cast<uint32_t>(scale[at + i]) << (8 * i);
+          return x;
+        };
+        auto valid = [&](int j) -> uint32_t {  // bytes of rows there are
+          const int left = w.k_end - (row0 + j * BN);
+          return left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
+        };
+        int ofs1 = ofs;
+        int page = load_page(0);
+        uint32_t ck = v == 0 ? load_codes(p.k_scale, 0, page, ofs1) : 0u;
+        uint32_t cv = load_codes(p.v_scale, 0, page, ofs1);
+        ofs1 = ofs;
+        page = load_page(1);
+        for (int j = 0; j < w.n; ++j, f += 2, ++tile) {
+          const int key0 = w.k_begin + j * BN;
+          const uint32_t nk = v == 0 ? load_codes(p.k_scale, j + 1, page, ofs1) : 0u;
+          const uint32_t nv = load_codes(p.v_scale, j + 1, page, ofs1);
+          const uint32_t there = valid(j);
+          ck &= there;
+          cv &= there;
+          const int ofs2 = ofs;
+          const int page_next = load_page(j + 2);
+          // the tile's largest codes, then the factors of the warp's 32 rows, one per lane: row
+          // i * (128 / G) + (32 / G) * warp + q of the tile in lane (32 / G) * i + q
+          const uint32_t hv = __vmaxu2(cv & 0xff00ffu, (cv >> 8) & 0xff00ffu);
+          int E = max(static_cast<int>(__reduce_max_sync(0xffffffffu, max(hv & 0xffffu, hv >> 16))),
+                      kMinValueCode);
+          if (v == 0) {
+            const float Ev = static_cast<float>(E - 127);
+            const uint32_t hk = __vmaxu2(ck & 0xff00ffu, (ck >> 8) & 0xff00ffu);
+            E = __reduce_max_sync(0xffffffffu, max(hk & 0xffffu, hk >> 16));
+            if (tid == 0)
+              s_tile[tile & 7] =
+                  make_float2(__uint_as_float(static_cast<uint32_t>(max(E - 7, 1)) << 23), Ev);
+          }
+          uint32_t factor;
+          {
+            constexpr int Q = 32 / G;
+            const int r = (lane / Q) * (128 / G) + Q * (warp & 3) + lane % Q;
+            const uint32_t four = __shfl_sync(0xffffffffu, v == 0 ? ck : cv, r >> 2);
+            factor = row_scale(E - static_cast<int>((four >> (8 * (r & 3))) & 0xffu));
+            factor |= factor << 16;
+          }
+          const uint32_t rs = f % C::NRAW, s = f % NS;
+          ok = warp_wait(&raw_full[rs], (f / C::NRAW) & 1, abort_flag, p.status) &&
+               (f < static_cast<uint32_t>(NS) ||
+                warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
+          if (!ok) break;
+          const bool edge = key0 + BN > min(w.L, w.k_end);
+          // piece i of the thread is row i * (128 / G) + r0
+          constexpr int kRowStep = 128 / G;  // (a multiple of 8: the swizzle stays)
+          const uint32_t src = raw0 + rs * C::RAW + r0 * D + 16 * c;
+          const uint32_t dst0 = kv0 + s * C::TILE + to0, dst1 = kv0 + s * C::TILE + to1;
 #pragma unroll 1
-        for (int i0 = 0; i0 < G; i0 += 4) {
-          uint4 x[4];
+          for (int i0 = 0; i0 < G; i0 += 4) {
+            uint4 x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = lds128(src + (i0 + i) * 2048);
-          if (edge) {  // rows past the end: zeros; the drafts' values: if finite
+            for (int i = 0; i < 4; ++i) x[i] = lds128(src + (i0 + i) * 2048);
+            if (edge) {  // rows past the end: zeros; the drafts' values: if finite
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = key0 + (i0 + i) * kRowStep + r0;
+                if (r >= w.k_end) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (v == 1 && r >= w.L)
+                  x[i] = make_uint4(finite_e4m3x4(x[i].x), finite_e4m3x4(x[i].y),
+                                    finite_e4m3x4(x[i].z), finite_e4m3x4(x[i].w));
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = key0 + (i0 + i) * kRowStep + r0;
-              if (r >= w.k_end) x[i] = make_uint4(0u, 0u, 0u, 0u);
-              if (v == 1 && r >= w.L)
-                x[i] = make_uint4(finite_e4m3x4(x[i].x), finite_e4m3x4(x[i].y),
-                                  finite_e4m3x4(x[i].z), finite_e4m3x4(x[i].w));
+              const uint32_t mm =
+                  __shfl_sync(0xffffffffu, factor, (32 / G) * (i0 + i) + r0 % (32 / G));
+              const uint4 lo = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].x), mm),
+                                          hmul2(e4m3x2_hi_to_f16x2(x[i].x), mm),
+                                          hmul2(e4m3x2_to_f16x2(x[i].y), mm),
+                                          hmul2(e4m3x2_hi_to_f16x2(x[i].y), mm));
+              const uint4 hi = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].z), mm),
+                                          hmul2(e4m3x2_hi_to_f16x2(x[i].z), mm),
+                                          hmul2(e4m3x2_to_f16x2(x[i].w), mm),
+                                          hmul2(e4m3x2_hi_to_f16x2(x[i].w), mm));
+              sts128(dst0 + (i0 + i) * (kRowStep * 128), lo);
+              sts128(dst1 + (i0 + i) * (kRowStep * 128), hi);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t mm =
-                __shfl_sync(0xffffffffu, factor, (32 / G) * (i0 + i) + r0 % (32 / G));
-            const uint4 lo = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].x), mm),
-                                        hmul2(e4m3x2_hi_to_f16x2(x[i].x), mm),
-                                        hmul2(e4m3x2_to_f16x2(x[i].y), mm),
-                                        hmul2(e4m3x2_hi_to_f16x2(x[i].y), mm));
-            const uint4 hi = make_uint4(hmul2(e4m3x2_to_f16x2(x[i].z), mm),
-                                        hmul2(e4m3x2_hi_to_f16x2(x[i].z), mm),
-                                        hmul2(e4m3x2_to_f16x2(x[i].w), mm),
-                                        hmul2(e4m3x2_hi_to_f16x2(x[i].w), mm));
-            sts128(dst0 + (i0 + i) * (kRowStep * 128), lo);
-            sts128(dst1 + (i0 + i) * (kRowStep * 128), hi);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&kv_full[s]);
+            mbar_arrive(&raw_empty[rs]);
           }
+          ck = nk;
+          cv = nv;
+          page = page_next;
+          ofs1 = ofs2;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&kv_full[s]);
-          mbar_arrive(&raw_empty[rs]);
-        }
-        ck = nk;
-        cv = nv;
-        page = page_next;
-        ofs1 = ofs2;
       }
-    }
     }
   } else {
     // ------------------------------------------------------------ softmax
