@@ -50,7 +50,8 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int Tn, int w
 // One CTA per (draft, sequence), or several: the masks are worked out by every CTA (a few rounds
 // in shared memory), then the draft's rows, 16 channels per thread: keys rotated at its
 // position and values to the cache (bf16 or e4m3), queries rotated into q_rot.  A few
-// hundred KB at most: bound by launch and memory latency.
+// hundred KB at most: bound by launch and memory latency (3.5 us for 8 drafts of one sequence,
+// 6.6 to 6.9 for 512 drafts; 128 channels, 48 heads).
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     const __nv_bfloat16* __restrict__ q_new, const __nv_bfloat16* __restrict__ k_new,
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
 // L + a_i.  A CTA moves some KV heads of one sequence, kMoveRows rows at a time: all of their
 // 16-byte pieces are read, then, behind a barrier, written.  a_i >= i, so what a group of rows
 // overwrites has been read by it or by an earlier one.  Bound by latency (a walk up the tree,
-// the block table, the rows): a few KB per sequence.
+// the block table, the rows): a few KB per sequence, 2.3 us for one, 4.4 for 256.
 constexpr int kMoveRows = 8;
 constexpr int kMoveBatch = 4;  // pieces per thread in flight
 
