@@ -655,14 +655,24 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(D) * x;
     uint32_t ns = 0, tile0 = 0, done[2] = {0, 0};  // done: pieces in which stream 0, 1 had tiles
     bool ok = true;
-    for (; pc.n > 0; pc.next(p.line)) {  // (to the end: the warps' barriers go together)
+    // the thread's query row of a piece, of the KV head's (at or past M: none), and its factor
+    auto row_of = [&](const View& w) {
+      return (w.rb * (1 + pair) + (pair ? x : 0)) * BN + row;
+    };
+    auto factor_of = [&](const GroupPiece& q) -> float {
+      if (!F8 || q.n == 0) return 1.f;
+      const View w(q, p);
+      const int r = row_of(w);
+      return r < M ? p.q_factor[(static_cast<size_t>(w.b) * p.Hkv + w.kvh) * M + r] : 1.f;
+    };
+    float factor = factor_of(pc);
+    while (pc.n > 0) {  // (to the end: the warps' barriers go together)
       const View w(pc, p);
-      const int r = (w.rb * (1 + pair) + (pair ? x : 0)) * BN + row;  // of the KV head's
+      const int r = row_of(w);
       const bool live = r < M;
       const bool warp_live = __any_sync(0xffffffffu, live);
       const int t = live ? r / p.rep : 0;
-      float row_factor = p.scale_log2;
-      if (F8 && live) row_factor *= p.q_factor[(static_cast<size_t>(w.b) * p.Hkv + w.kvh) * M + r];
+      const float row_factor = p.scale_log2 * factor;
       const uint32_t* anc = p.anc + (static_cast<size_t>(w.b) * p.T + t) * p.words;
       const size_t slot = static_cast<size_t>(blockIdx.x) + pc.segment(p.line);
       if (threadIdx.x == 0) pc.leave_for_merge(p.line);
@@ -796,6 +806,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       tile0 += w.n;
+      // (what the next piece begins with is read beside the end of this one)
+      pc.next(p.line);
+      factor = factor_of(pc);
       // Partial result: R, l and O, relative to 2^R; four channels of all rows together, so that
       // a warp's lanes, which hold a row each, store 512 bytes in a row.  With one query tile
       // stream 0 adds stream 1's sums to its own and hands back the factors of the two outputs;
