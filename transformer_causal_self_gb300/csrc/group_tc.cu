@@ -27,11 +27,11 @@
 // R is raised only by more than 2^8, as elsewhere; w is then at most 2^8 (bf16), or 2^15 with
 // the 2^7 that the e4m3 path adds for f16's range.
 //
-// A 128-row tile of 128 channels takes an SM 1.60 us with up to 128 query rows over bf16 (6.2
-// TB/s over all SMs: HBM) and 1.89 with 256 (1350 TFLOP/s: each stream's chain of product,
-// softmax and product, two of which overlap; the tensor pipe is 47 % busy); over e4m3 1.46 (half
-// the bytes: the tiles' way through shared memory, raw and as f16) and 2.07.  64 channels: 0.87,
-// 1.27, 1.11, 1.67 us.  A piece adds 4 to 6 us, the partial results and the next scores.
+// A 128-row tile of 128 channels takes an SM 1.49 us with up to 128 query rows over bf16 (6.7
+// TB/s over all SMs: HBM) and 1.81 with 256 (1410 TFLOP/s: 32 products of N = 128, of which the
+// tensor core takes one in about 110 cycles; one rounding less in the softmax changed nothing);
+// over e4m3 1.39 (half the bytes: the tiles' way through shared memory, raw and as f16) and 1.99.
+// 64 channels: 0.80, 1.23, 1.05, 1.63 us.  A piece adds 3 to 6 us: partial results, next scores.
 #include "fp8.cuh"
 #include "internal.h"
 
@@ -727,19 +727,19 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               max32(ra);
             }
           } else {
-          tmem_ld32_issue(tS, ra);
-          tmem_ld32_wait(ra);
-          tmem_ld32_issue(tS + 32u, rb);
-          max32(ra);
-          tmem_ld32_wait(rb);
-          tmem_ld32_issue(tS + 64u, ra);
-          max32(rb);
-          tmem_ld32_wait(ra);
-          tmem_ld32_issue(tS + 96u, rb);
-          max32(ra);
-          tmem_ld32_wait(rb);
-          tmem_ld32_issue(tS, ra);
-          max32(rb);
+            tmem_ld32_issue(tS, ra);
+            tmem_ld32_wait(ra);
+            tmem_ld32_issue(tS + 32u, rb);
+            max32(ra);
+            tmem_ld32_wait(rb);
+            tmem_ld32_issue(tS + 64u, ra);
+            max32(rb);
+            tmem_ld32_wait(ra);
+            tmem_ld32_issue(tS + 96u, rb);
+            max32(ra);
+            tmem_ld32_wait(rb);
+            tmem_ld32_issue(tS, ra);
+            max32(rb);
           }
           const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
           const bool mine = top > R + kRescaleThreshold;
@@ -788,17 +788,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               weights32(ra, tS + 16u * i);
             }
           } else {
-          tmem_ld32_wait(ra);
-          tmem_ld32_issue(tS + 32u, rb);
-          weights32(ra, tS);
-          tmem_ld32_wait(rb);
-          tmem_ld32_issue(tS + 64u, ra);
-          weights32(rb, tS + 16u);
-          tmem_ld32_wait(ra);
-          tmem_ld32_issue(tS + 96u, rb);
-          weights32(ra, tS + 32u);
-          tmem_ld32_wait(rb);
-          weights32(rb, tS + 48u);
+            tmem_ld32_wait(ra);
+            tmem_ld32_issue(tS + 32u, rb);
+            weights32(ra, tS);
+            tmem_ld32_wait(rb);
+            tmem_ld32_issue(tS + 64u, ra);
+            weights32(rb, tS + 16u);
+            tmem_ld32_wait(ra);
+            tmem_ld32_issue(tS + 96u, rb);
+            weights32(ra, tS + 32u);
+            tmem_ld32_wait(rb);
+            weights32(rb, tS + 48u);
           }
           const float sum = (sa0 + sa1) + (sb0 + sb1);
           l += F8 ? sum * ex2_approx(-ev - 7.f) : sum;
