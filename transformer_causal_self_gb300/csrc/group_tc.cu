@@ -28,8 +28,8 @@
 // the 2^7 that the e4m3 path adds for f16's range.
 //
 // A 128-row tile of 128 channels takes an SM 1.49 us with up to 128 query rows over bf16 (6.7
-// TB/s over all SMs: HBM) and 1.81 with 256 (1410 TFLOP/s: 32 products of N = 128, of which the
-// tensor core takes one in about 110 cycles; one rounding less in the softmax changed nothing);
+// TB/s over all SMs: HBM) and 1.81 with 256 (1410 TFLOP/s: 32 products of N = 128, which at
+// one in 118 cycles take 1.82 us; one rounding less in the softmax changed nothing);
 // over e4m3 1.39 (half the bytes: the tiles' way through shared memory, raw and as f16) and 1.99.
 // 64 channels: 0.80, 1.23, 1.05, 1.63 us.  A piece adds 3 to 6 us: partial results, next scores.
 #include "fp8.cuh"
