@@ -76,6 +76,29 @@ def test_decode_many_sequences(d, page):
     assert_bf16_close(to_np(out), ref, "decode")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,L", [(1, 4, 1, 20000), (1, 4, 2, 3000), (2, 8, 4, 1500),
+                                        (4, 8, 8, 600), (16, 16, 8, 130), (130, 64, 8, 20)])
+def test_decode_from_one_to_many_partial_results(B, Hq, Hkv, L, d):
+    """Rows with hundreds of partial results to merge (one long sequence) down to a few."""
+    g = H.gen(L + d)
+    k, v = (torch.randn(B, Hkv, L, d, generator=g, dtype=torch.float32).to(torch.bfloat16).to(dev())
+            for _ in range(2))
+    q = torch.randn(B, Hq, 1, d, generator=g).to(torch.bfloat16).to(dev())
+    c = {n: x.to(dev()) for n, x in H.empty_cache(B, Hkv, L, d, 0, True, seed=1).items()
+         if isinstance(x, torch.Tensor)}
+    csattn.cache_append_fp8(k, v, c["k"], c["v"], c["ks"], c["vs"], H.i32([0] * B))
+    lens = [max(1, L - 7 * b) for b in range(B)]
+    out = csattn.attn_decode_fp8(q, c["k"], c["v"], c["ks"], c["vs"], H.i32(lens))
+    csattn.check_status()
+    kk, vv = (c[n].double() * torch.exp2(c[n + "s"].double() - 127)[..., None] for n in ("k", "v"))
+    s = torch.einsum("bgjd,bgkd->bgjk", q.double().view(B, Hkv, Hq // Hkv, d), kk) / np.sqrt(d)
+    s.masked_fill_(torch.arange(L, device=dev()) >= torch.tensor(lens, device=dev()).view(B, 1, 1, 1),
+                   float("-inf"))
+    ref = (torch.softmax(s, -1) @ vv).view(B, Hq, 1, d)
+    assert_bf16_close(to_np(out), ref.cpu().numpy(), "decode")
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("Hq,Tn", [(2, 6), (8, 12), (8, 40)])
 def test_rows_of_zeros(Hq, Tn, e4m3):

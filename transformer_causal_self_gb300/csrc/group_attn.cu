@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
 // query row: `subs` for each piece of its segment.  W warps per row (W > 1 for few rows with
 // many partials), four (d = 128) or two channels per lane.
 template <int D, int W>
-__global__ void __launch_bounds__(128) group_merge_kernel(
+__global__ void __launch_bounds__(32 * (W > 4 ? W : 4)) group_merge_kernel(
     const float* __restrict__ part_o, const float* __restrict__ part_ml, const int2* seg, int heads,
     int subs, int part_rows, int block_rows, int rblocks, const uint32_t* __restrict__ anc,
     const uint8_t* __restrict__ vflag, const __nv_bfloat16* __restrict__ v_new, bool f8,
@@ -703,9 +703,9 @@ __global__ void __launch_bounds__(128) group_merge_kernel(
     int words) {
   constexpr int V = D / 32;
   constexpr int U = W > 1 ? 8 : 4;  // partial results whose loads are in flight together
-  __shared__ float s_part[W > 1 ? 4 : 1][V * 32 + 2];
+  __shared__ float s_part[W > 4 ? W : (W > 1 ? 4 : 1)][V * 32 + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = static_cast<int>(blockIdx.x) * (4 / W) + warp / W;
+  const int row = static_cast<int>(blockIdx.x) * (W < 4 ? 4 / W : 1) + warp / W;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
   const int rep = Hq / Hkv;
@@ -875,8 +875,9 @@ cudaError_t launch_merge(const GroupArgs& a, const uint8_t* vflag, const void* v
                          float* lse, cudaStream_t stream) {
   const int rows = a.B * a.Hq * a.T;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((static_cast<unsigned>(rows) + 4 / W - 1) / (4 / W), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  constexpr int kRowsPerCta = W < 4 ? 4 / W : 1;
+  cfg.gridDim = dim3((static_cast<unsigned>(rows) + kRowsPerCta - 1) / kRowsPerCta, 1, 1);
+  cfg.blockDim = dim3(32 * (W > 4 ? W : 4), 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -901,11 +902,20 @@ cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_group_merge(const GroupArgs& a, const uint8_t* vflag, const void* v_new,
                                void* out, float* lse, cudaStream_t stream) {
-  // Few rows have many partials: four warps each, which read them side by side.  2048 rows of
-  // eight: 111.5 us for the whole decode with two, 115.1 with four, 113.2 with one; 256 rows of
-  // 32: 99.8 with four, 101.7 with two, 103.6 with one.
-  const int rows = a.B * a.Hq * a.T;
-  if (rows <= 1024)
+  // Warps per row, by the partials that a row has on average.  The whole decode in us with 1, 2,
+  // 4, 8, 16 warps: 8192 rows of 5: 59.4, 63.0; 2048 rows of 8: 113.2, 111.5, 115.1; 1024 of 11:
+  // -, 48.3, 49.0, 51.4; 512 of 18: -, 30.2, 29.7, 30.5; 128 of 60: -, -, 47.7, 46.3, 46.5; 32 of
+  // 230: -, -, 25.9, 22.0, 20.5.
+  const int rows = a.B * a.Hq * a.T, segments = a.B * a.Hkv * a.plan.rblocks;
+  const int partials = static_cast<int>(
+      a.plan.subs * (static_cast<long long>(a.plan.grid) + segments) / segments);
+  if (partials > 120)
+    return a.d == 128 ? launch_merge<128, 16>(a, vflag, v_new, out, lse, stream)
+                      : launch_merge<64, 16>(a, vflag, v_new, out, lse, stream);
+  if (partials > 40)
+    return a.d == 128 ? launch_merge<128, 8>(a, vflag, v_new, out, lse, stream)
+                      : launch_merge<64, 8>(a, vflag, v_new, out, lse, stream);
+  if (partials > 12)
     return a.d == 128 ? launch_merge<128, 4>(a, vflag, v_new, out, lse, stream)
                       : launch_merge<64, 4>(a, vflag, v_new, out, lse, stream);
   if (rows <= 4096)
