@@ -15,12 +15,13 @@ namespace {
 
 constexpr int kThreads = 256;  // >= the largest Tn
 constexpr int kWords = kThreads / 32;
+constexpr int kStride = kWords + 1;  // of a draft's mask words (odd: neighbours' in other banks)
 
 // Ancestor masks (self included; zero for padding) of a sequence's drafts into s_anc and
 // whether every parent is valid, by pointer doubling: after round r a token's mask holds
 // its 2^r nearest, and its pointer the next one above.  All kThreads threads call it.
 __device__ __forceinline__ bool tree_masks(const int32_t* parents, int Tn, int words,
-                                           uint32_t (*s_anc)[kWords], int* s_up) {
+                                           uint32_t (*s_anc)[kStride], int* s_up) {
   const int t = static_cast<int>(threadIdx.x);
   int up = t < Tn ? parents[t] : -2;
   bool bad = t < Tn && (up < -2 || up >= t);
@@ -28,18 +29,22 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int Tn, int w
   __syncthreads();
   if (!bad && up >= 0) bad = s_up[up] == -2;  // below padding
   if (__syncthreads_or(bad)) return false;
-  for (int w = 0; w < words; ++w)
-    s_anc[t][w] = (up != -2 && (t >> 5) == w) ? 1u << (t & 31) : 0u;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w)
+    if (w < words) s_anc[t][w] = (up != -2 && (t >> 5) == w) ? 1u << (t & 31) : 0u;
   while (__syncthreads_or(up >= 0)) {
     uint32_t more[kWords];
     int next = -1;
     if (up >= 0) {
-      for (int w = 0; w < words; ++w) more[w] = s_anc[up][w];
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) more[w] = w < words ? s_anc[up][w] : 0u;
       next = s_up[up];
     }
     __syncthreads();
     if (up >= 0) {
-      for (int w = 0; w < words; ++w) s_anc[t][w] |= more[w];
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+        if (w < words) s_anc[t][w] |= more[w];
       s_up[t] = next;
       up = next;
     }
@@ -50,8 +55,8 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int Tn, int w
 // One CTA per (draft, sequence), or several: the masks are worked out by every CTA (a few rounds
 // in shared memory), then the draft's rows, 16 channels per thread: keys rotated at its
 // position and values to the cache (bf16 or e4m3), queries rotated into q_rot.  A few
-// hundred KB at most: bound by launch and memory latency (3.5 us for 8 drafts of one sequence,
-// 6.6 to 6.9 for 512 drafts; 128 channels, 48 heads).
+// hundred KB at most: bound by launch and memory latency (3.1 us for 8 drafts of one sequence,
+// about 6 for 512 drafts; 128 channels, 48 heads).
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     const __nv_bfloat16* __restrict__ q_new, const __nv_bfloat16* __restrict__ k_new,
@@ -62,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     float* __restrict__ q_factor, uint32_t* __restrict__ anc, int32_t* __restrict__ lens,
     uint8_t* __restrict__ vflag, int words, uint32_t* status) {
   constexpr int G = D / 16;
-  __shared__ uint32_t s_anc[kThreads][kWords];
+  __shared__ uint32_t s_anc[kThreads][kStride];
   __shared__ int s_up[kThreads];
   __shared__ float s_cos[64], s_sin[64];
   const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, Hkv = rows.Hkv;
