@@ -248,3 +248,60 @@ def test_stream_argument():
     s.synchronize()
     csattn.check_status()
     assert H.same_bits(a, b) and H.same_bits(a, e)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_behind_kernels_that_write_their_inputs(graph):
+    """A generation loop on one stream without a wait on the host: every call's inputs are written
+    by the kernel right before it (their blocks may be scheduled while that one still runs)."""
+    B, Hq, Hkv, d, Tn, steps, base = 2, 8, 2, 128, 12, 12, 10000.0
+    g = H.gen(11)
+    xs = [[torch.randn(B, h, n, d, generator=g).to(torch.bfloat16).to(dev())
+           for h, n in ((Hkv, 1), (Hkv, 1), (Hq, 1), (Hq, Tn), (Hkv, Tn), (Hkv, Tn))]
+          for _ in range(steps)]
+    parents = H.i32([[t // 2 - 1 for t in range(Tn)]] * B)
+
+    c0 = {n: x.to(dev()) for n, x in H.empty_cache(B, Hkv, 256, d, 0, True, seed=2).items()
+          if isinstance(x, torch.Tensor)}
+    zero, first = H.i32([0, 0]), H.i32([0, 3])
+
+    def loop(wait):
+        def do(f):
+            if wait:
+                torch.cuda.synchronize()
+            return f()
+
+        c = {n: x.clone() for n, x in c0.items()}
+        cache, scales = (c["k"], c["v"], c["ks"], c["vs"]), dict(k_scale=c["ks"], v_scale=c["vs"])
+        buf = [torch.zeros_like(x) for x in xs[0]]
+        lens, acc, outs = first.clone(), zero.clone(), []
+        prompt = torch.ones(B, Hkv, 3, d, dtype=torch.bfloat16, device=dev())
+        do(lambda: csattn.cache_append_fp8(prompt, prompt, *cache, zero))
+        for i, x in enumerate(xs):
+            for to, new in zip(buf, x):
+                do(lambda: to.copy_(new))
+            do(lambda: csattn.cache_append_fp8(buf[0], buf[1], *cache, lens, rope_base=base))
+            do(lambda: lens.add_(1))
+            outs.append(do(lambda: csattn.attn_decode_fp8(buf[2], *cache, lens, rope_base=base)))
+            outs.append(do(lambda: csattn.attn_tree_step(buf[3], buf[4], buf[5], c["k"], c["v"],
+                                                         lens, parents, rope_base=base, **scales)))
+            do(lambda: acc.fill_(i % Tn))
+            new_lens = do(lambda: csattn.tree_commit(c["k"], c["v"], lens, parents, acc, **scales))
+            do(lambda: lens.copy_(new_lens))
+        ko, vo = (torch.zeros(B, Hkv, 256, d, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+        do(lambda: csattn.cache_read_fp8(*cache, lens, ko, vo))
+        return outs + [ko, vo, lens]
+
+    want = loop(True)
+    if graph:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            got = loop(False)
+        gr.replay()
+        gr.replay()
+    else:
+        got = loop(False)
+    torch.cuda.synchronize()
+    csattn.check_status()
+    for a, b in zip(got, want):
+        assert H.same_bits(a, b)

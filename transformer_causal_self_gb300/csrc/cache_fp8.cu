@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(kThreads, 8) append_fp8_kernel(
     th_lo[tid] = theta.lo[tid];
   }
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int Hkv = rows.Hkv;
   const int groups = (Hkv + span - 1) / span;
   // (32-bit indices: the launcher checks that the items are < 2^31)
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kThreads) read_fp8_kernel(
   const bool is_k = blk < k_blocks;
   if (!is_k) blk -= k_blocks;
   const int b = bg / rows.Hkv, g = bg - b * rows.Hkv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = seq_lens[b];
   if (n < 0 || n > Lout || n > rows.Lmax) {
     if (is_k && blk == 0 && g == 0 && threadIdx.x == 0) atomicOr(status, kStatusDeviceArg);
@@ -196,12 +198,12 @@ cudaError_t launch_cache_append_fp8(const void* k_new, const void* v_new, const 
   if (items + 2 * kThreads >= 0x3fffffffLL) return cudaErrorInvalidValue;
   const int blocks = static_cast<int>((items + kThreads - 1) / kThreads);
   auto* kernel = d == 128 ? append_fp8_kernel<128> : append_fp8_kernel<64>;
-  kernel<<<2 * blocks, kThreads, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new),
-      static_cast<uint8_t*>(cache.k), static_cast<uint8_t*>(cache.v),
-      static_cast<uint8_t*>(cache.k_scale), static_cast<uint8_t*>(cache.v_scale), cache_lens,
-      rows_of(cache, Hkv), B, Tn, span, rope, theta, status, blocks);
-  return cudaGetLastError();
+  return launch_behind(kernel, dim3(2 * blocks), kThreads, stream,
+                       static_cast<const __nv_bfloat16*>(k_new),
+                       static_cast<const __nv_bfloat16*>(v_new), static_cast<uint8_t*>(cache.k),
+                       static_cast<uint8_t*>(cache.v), static_cast<uint8_t*>(cache.k_scale),
+                       static_cast<uint8_t*>(cache.v_scale), cache_lens, rows_of(cache, Hkv), B, Tn,
+                       span, rope, theta, status, blocks);
 }
 
 cudaError_t launch_cache_read_fp8(const KvCache& cache, const int32_t* seq_lens, void* k_out,
@@ -211,12 +213,12 @@ cudaError_t launch_cache_read_fp8(const KvCache& cache, const int32_t* seq_lens,
   const long long blocks = (pieces + kThreads * kRows - 1) / (kThreads * kRows);
   if (2 * blocks * B * Hkv > 0x7fffffffLL || pieces > 0x3fffffffLL) return cudaErrorInvalidValue;
   auto* kernel = d == 128 ? read_fp8_kernel<128> : read_fp8_kernel<64>;
-  kernel<<<static_cast<unsigned>(2 * blocks * B * Hkv), kThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(cache.k), static_cast<const uint8_t*>(cache.v),
-      static_cast<const uint8_t*>(cache.k_scale), static_cast<const uint8_t*>(cache.v_scale),
-      seq_lens, rows_of(cache, Hkv), static_cast<__nv_bfloat16*>(k_out),
-      static_cast<__nv_bfloat16*>(v_out), Lout, status, static_cast<int>(blocks));
-  return cudaGetLastError();
+  return launch_behind(kernel, dim3(static_cast<unsigned>(2 * blocks * B * Hkv)), kThreads, stream,
+                       static_cast<const uint8_t*>(cache.k), static_cast<const uint8_t*>(cache.v),
+                       static_cast<const uint8_t*>(cache.k_scale),
+                       static_cast<const uint8_t*>(cache.v_scale), seq_lens, rows_of(cache, Hkv),
+                       static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), Lout,
+                       status, static_cast<int>(blocks));
 }
 
 }  // namespace csattn

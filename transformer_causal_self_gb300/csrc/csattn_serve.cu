@@ -377,7 +377,6 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = a.part_o + partial_floats(a.plan, B, Hkv) * d;
   a.seg = reinterpret_cast<int2*>(ws + at.seg);
-  a.after_prep = true;
   a.status = p.status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_tree_prep(p, st);

@@ -861,7 +861,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.after_prep ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, group_attn_kernel<D, F8, NT>, p, tk, tv);
 }
 

@@ -235,13 +235,31 @@ struct GroupArgs {
   float* part_o;         // [pieces, subs, part_rows, d], pieces = grid + segments; from
                          // launch_group_tc [pieces, d / 4, part_rows, 4]
   float* part_ml;        // [pieces, subs, part_rows, 2]
-  bool after_prep;       // launched behind launch_tree_prep (programmatic dependent launch)
   uint32_t* status;
 };
 inline GroupLine group_line(const GroupArgs& a) {
   return GroupLine{a.lens,     a.seg, a.B,         a.drafts, a.min_len, a.max_seq_len - a.drafts,
                    a.plan.unit, a.Hkv * a.plan.rblocks, a.plan.tiles_per_cta, a.plan.least_tiles};
 }
+// A launch whose blocks may be scheduled while the stream's kernel before it ends (in a graph, 64
+// tokens appended: 3.0 -> 2.7 us, 256 trees committed: 4.45 -> 3.95).  Every thread of the kernel
+// passes griddepcontrol.wait, behind which that kernel has ended and its writes are visible,
+// before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
+                          A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // CTAs of launch_group_attn's kernel per SM.  e4m3: three, except where 16 query rows of 128
 // channels do not fit 128 registers a thread (8 sequences of 8000 rows: 45 us with two, 68 with
 // three and what they spill).

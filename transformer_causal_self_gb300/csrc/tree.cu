@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
   __shared__ int s_up[kThreads];
   __shared__ float s_cos[64], s_sin[64];
   const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, Hkv = rows.Hkv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // the attention kernel may be scheduled; it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rep = Hq / Hkv, items = (Hq + 2 * Hkv) * G, step = gridDim.z * kThreads;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(
   __shared__ uint8_t s_path[kThreads];                   // the path, at its end
   __shared__ long long s_from[kThreads], s_to[kThreads];  // of row i, in rows, KV head 0
   __shared__ int s_n;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g0 = blockIdx.x * heads, b = blockIdx.y, tid = threadIdx.x;
   const int nh = min(heads, rows.Hkv - g0);
   const int L = cache_lens[b], last = accepted[b];
@@ -287,13 +289,15 @@ cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
   // a draft's rows shared by several CTAs while these are all resident at once
   const int parts = ((a.Hq + 2 * a.Hkv) * (a.d / 16) + kThreads - 1) / kThreads;
   const bool few = static_cast<long long>(a.Tn) * a.B * parts <= 2 * 152 && parts <= 65535;
-  kernel<<<dim3(a.Tn, a.B, few ? parts : 1), kThreads, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(a.q_new), static_cast<const __nv_bfloat16*>(a.k_new),
-      static_cast<const __nv_bfloat16*>(a.v_new), a.cache.k, a.cache.v,
-      static_cast<uint8_t*>(a.cache.k_scale), static_cast<uint8_t*>(a.cache.v_scale),
-      a.cache_lens, a.parents, rows_of(a.cache, a.Hkv), a.Hq, a.Tn, a.max_seq_len, a.rope, a.theta,
-      static_cast<__nv_bfloat16*>(a.q_rot), a.q_factor, a.anc, a.lens, a.vflag, a.words, a.status);
-  return cudaGetLastError();
+  return launch_behind(kernel, dim3(a.Tn, a.B, few ? parts : 1), kThreads, stream,
+                       static_cast<const __nv_bfloat16*>(a.q_new),
+                       static_cast<const __nv_bfloat16*>(a.k_new),
+                       static_cast<const __nv_bfloat16*>(a.v_new), a.cache.k, a.cache.v,
+                       static_cast<uint8_t*>(a.cache.k_scale),
+                       static_cast<uint8_t*>(a.cache.v_scale), a.cache_lens, a.parents,
+                       rows_of(a.cache, a.Hkv), a.Hq, a.Tn, a.max_seq_len, a.rope, a.theta,
+                       static_cast<__nv_bfloat16*>(a.q_rot), a.q_factor, a.anc, a.lens, a.vflag,
+                       a.words, a.status);
 }
 
 cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
@@ -304,11 +308,11 @@ cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
   // heads per CTA: few while that leaves SMs idle, at most 16 (their scale bytes fill a CTA)
   const int heads = std::max(1, std::min({16, Hkv, static_cast<int>(
                                                        static_cast<long long>(Hkv) * B / 152)}));
-  tree_commit_kernel<<<dim3((Hkv + heads - 1) / heads, B), kThreads, 0, stream>>>(
-      static_cast<uint4*>(cache.k), static_cast<uint4*>(cache.v),
-      static_cast<uint8_t*>(cache.k_scale), static_cast<uint8_t*>(cache.v_scale), cache_lens,
-      parents, accepted, new_lens, rows_of(cache, Hkv), Tn, pieces, heads, status);
-  return cudaGetLastError();
+  return launch_behind(tree_commit_kernel, dim3((Hkv + heads - 1) / heads, B), kThreads, stream,
+                       static_cast<uint4*>(cache.k), static_cast<uint4*>(cache.v),
+                       static_cast<uint8_t*>(cache.k_scale), static_cast<uint8_t*>(cache.v_scale),
+                       cache_lens, parents, accepted, new_lens, rows_of(cache, Hkv), Tn, pieces,
+                       heads, status);
 }
 
 }  // namespace csattn
