@@ -3,7 +3,10 @@
 // Append: token t of sequence b goes to row r = cache_lens[b] + t, its key rotated at r
 // in fp32 and rounded once, to e4m3; the value is rounded as given.  Read: rows
 // 0..seq_lens[b]-1 back to bf16, exactly.  Both move each byte once and are bound by
-// HBM (4 bytes in, 2 + 1/64 out per channel pair; the reverse for the read).
+// HBM (4 bytes in, 2 + 1/64 out per channel pair; the reverse for the read), by latency where
+// they are short.  128 channels, 8 KV heads: the append of 4 x 4096 tokens takes 21.7 us (101 MB,
+// 4.7 TB/s: less than two waves, whose loads, angles and stores follow one another), of 64 tokens
+// 2.7 us; the read of 32768 rows 33.0 us (202 MB, 6.1 TB/s), of 8 x 17..1024 rows 4.9 us.
 #include <algorithm>
 
 #include "fp8.cuh"

@@ -33,7 +33,7 @@
 // for 575 MB of 8 sequences (6.1 TB/s; the issue slots are 41 % busy, most of it e4m3 to f16);
 // 64 sequences of 512 to 8192 rows take 93.5 us for 576 MB (their ends add pieces: a piece's
 // queries and scale bytes are taken off the compute warps, which cost 114 us), and one of 1000
-// rows 8.7 us, the latencies of two launches, the lengths, a tile and the merge.
+// rows 8.6 us, the latencies of two launches, the lengths, a tile and the merge.
 #include <climits>
 
 #include "fp8.cuh"
