@@ -55,6 +55,17 @@ def test_many_sequences(Hq, Tn, e4m3):
     _run_and_check(case, lens, 0.0)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d,Hq,Hkv,Tn,page,kind", [(64, 2, 1, 33, 16, "padded"),
+                                                   (128, 3, 3, 18, 0, "random"),
+                                                   (128, 10, 2, 11, 32, "flat")])
+def test_many_drafts(d, Hq, Hkv, Tn, page, kind, e4m3):
+    """More drafts than CTAs at once: several of them in one, the last ones of a sequence fewer."""
+    lens = [(37 * b) % 41 for b in range(80)]
+    case = T._case(80, Hq, Hkv, d, Tn, lens, 41 + Tn, page, e4m3, kind, seed=Tn)
+    _run_and_check(case, lens, 10000.0)
+
+
 @pytest.mark.parametrize("d,page", [(64, 16), (128, 0)])
 def test_decode_many_sequences(d, page):
     lens = [1 + (37 * b) % 150 for b in range(75)]

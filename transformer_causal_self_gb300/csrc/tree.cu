@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 256;  // >= the largest Tn
 constexpr int kWords = kThreads / 32;
+constexpr int kDrafts = 4;  // drafts of a CTA, where it has several
 constexpr int kStride = kWords + 1;  // of a draft's mask words (odd: neighbours' in other banks)
 
 // Ancestor masks (self included; zero for padding) of a sequence's drafts into s_anc and
@@ -52,12 +53,13 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int Tn, int w
   return true;
 }
 
-// One CTA per (draft, sequence), or several: the masks are worked out by every CTA (a few rounds
-// in shared memory), then the draft's rows, 16 channels per thread: keys rotated at its
-// position and values to the cache (bf16 or e4m3), queries rotated into q_rot.  A few
-// hundred KB at most: bound by launch and memory latency (3.1 us for 8 drafts of one sequence,
-// about 6 for 512 drafts; 128 channels, 48 heads).
-template <int D, bool F8>
+// One CTA per draft of a sequence; several where few drafts leave SMs idle, and up to N drafts per
+// CTA where there are many.  Every CTA works out the sequence's masks (a few rounds in shared
+// memory), then its drafts' rows, 16 channels per thread: keys rotated at their positions and
+// values to the cache (bf16 or e4m3), queries rotated into q_rot.  Bound by launch and memory
+// latency for a few hundred drafts (3.1 us for 8 of one sequence, about 6 for 512; 128 channels,
+// 48 heads), by the queries' bytes, in and out, for thousands.
+template <int D, bool F8, int N>
 __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     const __nv_bfloat16* __restrict__ q_new, const __nv_bfloat16* __restrict__ k_new,
     const __nv_bfloat16* __restrict__ v_new, void* __restrict__ k_cache,
@@ -65,123 +67,143 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
     const int32_t* __restrict__ cache_lens, const int32_t* __restrict__ parents, CacheRows rows,
     int Hq, int Tn, int max_seq_len, int rope, RopeTable theta, __nv_bfloat16* __restrict__ q_rot,
     float* __restrict__ q_factor, uint32_t* __restrict__ anc, int32_t* __restrict__ lens,
-    uint8_t* __restrict__ vflag, int words, uint32_t* status) {
+    uint8_t* __restrict__ vflag, int words, int drafts, uint32_t* status) {
   constexpr int G = D / 16;
   __shared__ uint32_t s_anc[kThreads][kStride];
   __shared__ int s_up[kThreads];
-  __shared__ float s_cos[64], s_sin[64];
-  const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, Hkv = rows.Hkv;
+  __shared__ float s_cos[N][64], s_sin[N][64];
+  if (N == 1) drafts = 1;
+  const int t0 = blockIdx.x * drafts, b = blockIdx.y, tid = threadIdx.x, Hkv = rows.Hkv;
+  const int rep = Hq / Hkv, items = (Hq + 2 * Hkv) * G, step = gridDim.z * kThreads;
+  const int all = min(drafts, Tn - t0) * items;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the attention kernel may be scheduled; it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int rep = Hq / Hkv, items = (Hq + 2 * Hkv) * G, step = gridDim.z * kThreads;
-  // 16 channels of a row, each thread's first while the masks are worked out
-  auto load = [&](int i, uint4* lo, uint4* hi) {
+  const int L = cache_lens[b];
+  const bool fits = L >= 0 && L <= max_seq_len - Tn;
+  // 16 channels of a row and, for a key or value, its cache row of KV head 0: each thread's first
+  // while the masks are worked out, the next ones beside the arithmetic on the last
+  auto load = [&](int i, uint4* lo, uint4* hi, long long* row0) {
     *lo = *hi = make_uint4(0u, 0u, 0u, 0u);
-    if (i >= items) return;
-    const int head = i / G, c = i % G;
+    *row0 = -1;
+    if (i >= all) return;
+    const int k = N == 1 ? 0 : i / items, t = t0 + k, j = i - k * items, head = j / G;
     const bool is_q = head < Hq, is_v = head >= Hq + Hkv;
     int e0, e1;
-    rope_piece(is_v ? 0 : rope, D / 2, c, &e0, &e1);
+    rope_piece(is_v ? 0 : rope, D / 2, j % G, &e0, &e1);
     const int g = is_q ? head : head - Hq - (is_v ? Hkv : 0);
     const __nv_bfloat16* x = (is_q ? q_new : (is_v ? v_new : k_new)) +
                              ((static_cast<size_t>(b) * (is_q ? Hq : Hkv) + g) * Tn + t) * D;
     *lo = *reinterpret_cast<const uint4*>(x + e0);
     *hi = *reinterpret_cast<const uint4*>(x + e1);
+    if (!is_q && fits) *row0 = rows.at(b, 0, L + t);
   };
-  const int L = cache_lens[b];
   uint4 lo, hi;
-  load(blockIdx.z * kThreads + tid, &lo, &hi);
-  const bool fits = L >= 0 && L <= max_seq_len - Tn;
-  const long long row0 = fits ? rows.at(b, 0, L + t) : -1;  // of KV head 0
+  long long row0;
+  load(blockIdx.z * kThreads + tid, &lo, &hi, &row0);
   const bool fine =
       tree_masks(parents + static_cast<size_t>(b) * Tn, Tn, words, s_anc, s_up) && fits;
-  if (tid == 0 && t == 0 && blockIdx.z == 0) {
+  if (tid == 0 && t0 == 0 && blockIdx.z == 0) {
     lens[b] = fine ? L : -1;
     if (!fine) atomicOr(status, kStatusDeviceArg);
   }
   if (!fine) return;  // the sequence's cache is left as it was
   __syncthreads();
-  if (blockIdx.z == 0 && tid < words)
-    anc[(static_cast<size_t>(b) * Tn + t) * words + tid] = s_anc[t][tid];
-  int depth = -1;
-  for (int w = 0; w < words; ++w) depth += __popc(s_anc[t][w]);
-  const int pos = L + max(depth, 0);  // (padding is written like a first token, never seen)
-  if (rope != 0 && tid < D / 2)
-    rope_cos_sin<false>(pos, theta.hi[tid], theta.lo[tid], s_cos[tid], s_sin[tid]);
+  if (blockIdx.z == 0 && tid < min(drafts, Tn - t0) * words)
+    anc[(static_cast<size_t>(b) * Tn + t0) * words + tid] = s_anc[t0 + tid / words][tid % words];
+  if (rope != 0) {
+    for (int i = tid; i < min(drafts, Tn - t0) * (D / 2); i += kThreads) {
+      const int k = i / (D / 2), c = i % (D / 2);
+      int depth = -1;
+      for (int w = 0; w < words; ++w) depth += __popc(s_anc[t0 + k][w]);
+      // (padding is written like a first token, never seen)
+      rope_cos_sin<false>(L + max(depth, 0), theta.hi[c], theta.lo[c], s_cos[k][c], s_sin[k][c]);
+    }
+  }
   __syncthreads();
   // (whole warps take part in the shuffles)
-  for (int i0 = blockIdx.z * kThreads; i0 < items; i0 += step) {
+  for (int i0 = blockIdx.z * kThreads; i0 < all; i0 += step) {
     const int i = i0 + tid;
-    const bool live = i < items;
-    const int head = live ? i / G : 0, c = i % G;
+    const bool live = i < all;
+    const int k = N == 1 || !live ? 0 : i / items, t = t0 + k, j = live ? i - k * items : 0;
+    const int head = j / G, c = i % G;
     const bool is_q = head < Hq, is_v = head >= Hq + Hkv;
     const int g = is_q ? head : head - Hq - (is_v ? Hkv : 0);
     const int layout = is_v ? 0 : rope;
     int e0, e1;
     rope_piece(layout, D / 2, c, &e0, &e1);
-    if (i0 >= step) load(i, &lo, &hi);
+    uint4 next_lo, next_hi;
+    long long next_row0;
+    if (N > 1) load(i + step, &next_lo, &next_hi, &next_row0);
+    if (N == 1 && i0 >= step) load(i, &lo, &hi, &row0);
     bool bad;
     const uint32_t top = row_absmax<G>(lo, hi, &bad);
-    if (!live) continue;  // (no shuffle below)
-    float cs[8], sn[8], y[16];
+    auto write = [&]() {
+      float cs[8], sn[8], y[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      cs[j] = layout != 0 ? s_cos[8 * c + j] : 1.f;
-      sn[j] = layout != 0 ? s_sin[8 * c + j] : 0.f;
-    }
-    const int code = scale_code(top, layout != 0);
-    if (F8 && !is_q) {
-      lo = scale_row(lo, code);
-      hi = scale_row(hi, code);
-    }
-    rope16(lo, hi, layout, cs, sn, y);
-    if (layout != 0) {
-      lo = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                      pack_bf16x2(y[6], y[7]));
-      hi = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]),
-                      pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
-    }
-    if (is_q) {
-      // the rows of a KV head's queries one behind another, draft by draft
-      const int kvh = g / rep;
-      const size_t q_row =
-          (static_cast<size_t>(b) * Hkv + kvh) * Tn * rep + t * rep + g - kvh * rep;
-      if constexpr (F8) {  // (query_to_f16 with the angles at hand)
-        const int E = min(max(static_cast<int>(top >> 7), 15), 254);
-        const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
-        lo = make_uint4(pack_f16x2(y[0] * f, y[1] * f), pack_f16x2(y[2] * f, y[3] * f),
-                        pack_f16x2(y[4] * f, y[5] * f), pack_f16x2(y[6] * f, y[7] * f));
-        hi = make_uint4(pack_f16x2(y[8] * f, y[9] * f), pack_f16x2(y[10] * f, y[11] * f),
-                        pack_f16x2(y[12] * f, y[13] * f), pack_f16x2(y[14] * f, y[15] * f));
-        if (c == 0)
-          q_factor[q_row] = __uint_as_float(static_cast<uint32_t>(E - 14) << 23);
+      for (int n = 0; n < 8; ++n) {
+        cs[n] = layout != 0 ? s_cos[k][8 * c + n] : 1.f;
+        sn[n] = layout != 0 ? s_sin[k][8 * c + n] : 0.f;
       }
-      __nv_bfloat16* dst = q_rot + q_row * D;
-      *reinterpret_cast<uint4*>(dst + e0) = lo;
-      *reinterpret_cast<uint4*>(dst + e1) = hi;
-      continue;
-    }
-    if (is_v && c == 0) vflag[(static_cast<size_t>(b) * Hkv + g) * Tn + t] = bad ? 1 : 0;
-    if (row0 < 0) {  // a page outside the pool
-      if (c == 0) atomicOr(status, kStatusDeviceArg);
-      continue;
-    }
-    const int plane = rows.block_table != nullptr ? rows.page_size : rows.Lmax;  // rows of a head
-    const long long row = row0 + static_cast<long long>(g) * plane;
-    if constexpr (F8) {
-      uint8_t* dst = static_cast<uint8_t*>(is_v ? v_cache : k_cache) + row * D;
-      *reinterpret_cast<uint2*>(dst + e0) =
-          make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
-                     pack_e4m3x4(y[4], y[5], y[6], y[7], code, bad));
-      *reinterpret_cast<uint2*>(dst + e1) =
-          make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11], code, bad),
-                     pack_e4m3x4(y[12], y[13], y[14], y[15], code, bad));
-      if (c == 0) (is_v ? v_scale : k_scale)[row] = static_cast<uint8_t>(code);
-    } else {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? v_cache : k_cache) + row * D;
-      *reinterpret_cast<uint4*>(dst + e0) = lo;
-      *reinterpret_cast<uint4*>(dst + e1) = hi;
+      const int code = scale_code(top, layout != 0);
+      if (F8 && !is_q) {
+        lo = scale_row(lo, code);
+        hi = scale_row(hi, code);
+      }
+      rope16(lo, hi, layout, cs, sn, y);
+      if (layout != 0) {
+        lo = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                        pack_bf16x2(y[6], y[7]));
+        hi = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]),
+                        pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
+      }
+      if (is_q) {
+        // the rows of a KV head's queries one behind another, draft by draft
+        const int kvh = g / rep;
+        const size_t q_row =
+            (static_cast<size_t>(b) * Hkv + kvh) * Tn * rep + t * rep + g - kvh * rep;
+        if constexpr (F8) {  // (query_to_f16 with the angles at hand)
+          const int E = min(max(static_cast<int>(top >> 7), 15), 254);
+          const float f = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
+          lo = make_uint4(pack_f16x2(y[0] * f, y[1] * f), pack_f16x2(y[2] * f, y[3] * f),
+                          pack_f16x2(y[4] * f, y[5] * f), pack_f16x2(y[6] * f, y[7] * f));
+          hi = make_uint4(pack_f16x2(y[8] * f, y[9] * f), pack_f16x2(y[10] * f, y[11] * f),
+                          pack_f16x2(y[12] * f, y[13] * f), pack_f16x2(y[14] * f, y[15] * f));
+          if (c == 0)
+            q_factor[q_row] = __uint_as_float(static_cast<uint32_t>(E - 14) << 23);
+        }
+        __nv_bfloat16* dst = q_rot + q_row * D;
+        *reinterpret_cast<uint4*>(dst + e0) = lo;
+        *reinterpret_cast<uint4*>(dst + e1) = hi;
+        return;
+      }
+      if (is_v && c == 0) vflag[(static_cast<size_t>(b) * Hkv + g) * Tn + t] = bad ? 1 : 0;
+      if (row0 < 0) {  // a page outside the pool
+        if (c == 0) atomicOr(status, kStatusDeviceArg);
+        return;
+      }
+      const int plane = rows.block_table != nullptr ? rows.page_size : rows.Lmax;  // rows of a head
+      const long long row = row0 + static_cast<long long>(g) * plane;
+      if constexpr (F8) {
+        uint8_t* dst = static_cast<uint8_t*>(is_v ? v_cache : k_cache) + row * D;
+        *reinterpret_cast<uint2*>(dst + e0) =
+            make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3], code, bad),
+                       pack_e4m3x4(y[4], y[5], y[6], y[7], code, bad));
+        *reinterpret_cast<uint2*>(dst + e1) =
+            make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11], code, bad),
+                       pack_e4m3x4(y[12], y[13], y[14], y[15], code, bad));
+        if (c == 0) (is_v ? v_scale : k_scale)[row] = static_cast<uint8_t>(code);
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? v_cache : k_cache) + row * D;
+        *reinterpret_cast<uint4*>(dst + e0) = lo;
+        *reinterpret_cast<uint4*>(dst + e1) = hi;
+      }
+    };
+    if (live) write();  // (no shuffle in it)
+    if (N > 1) {
+      lo = next_lo;
+      hi = next_hi;
+      row0 = next_row0;
     }
   }
 }
@@ -284,12 +306,24 @@ CacheRows rows_of(const KvCache& c, int Hkv) {
 
 cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
   const bool f8 = a.cache.k_scale != nullptr;
-  auto* kernel = a.d == 128 ? (f8 ? tree_prep_kernel<128, true> : tree_prep_kernel<128, false>)
-                            : (f8 ? tree_prep_kernel<64, true> : tree_prep_kernel<64, false>);
   // a draft's rows shared by several CTAs while these are all resident at once
   const int parts = ((a.Hq + 2 * a.Hkv) * (a.d / 16) + kThreads - 1) / kThreads;
   const bool few = static_cast<long long>(a.Tn) * a.B * parts <= 2 * 152 && parts <= 65535;
-  return launch_behind(kernel, dim3(a.Tn, a.B, few ? parts : 1), kThreads, stream,
+  // several drafts in a CTA where there are more than are resident at once: the masks are worked
+  // out once for them (64 sequences of 500 rows, 64 drafts: 127 and 138 us for the whole step over
+  // bf16 and e4m3, 135 and 151 with one draft each; 512 drafts: 2 us less with one each)
+  const int drafts = static_cast<int>(
+      std::min<long long>(kDrafts, (static_cast<long long>(a.Tn) * a.B + 607) / 608));
+  auto* kernel = a.d == 128
+                     ? (f8 ? tree_prep_kernel<128, true, 1> : tree_prep_kernel<128, false, 1>)
+                     : (f8 ? tree_prep_kernel<64, true, 1> : tree_prep_kernel<64, false, 1>);
+  if (drafts > 1)
+    kernel = a.d == 128 ? (f8 ? tree_prep_kernel<128, true, kDrafts>
+                              : tree_prep_kernel<128, false, kDrafts>)
+                        : (f8 ? tree_prep_kernel<64, true, kDrafts>
+                              : tree_prep_kernel<64, false, kDrafts>);
+  return launch_behind(kernel, dim3((a.Tn + drafts - 1) / drafts, a.B, few ? parts : 1), kThreads,
+                       stream,
                        static_cast<const __nv_bfloat16*>(a.q_new),
                        static_cast<const __nv_bfloat16*>(a.k_new),
                        static_cast<const __nv_bfloat16*>(a.v_new), a.cache.k, a.cache.v,
@@ -297,7 +331,7 @@ cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
                        static_cast<uint8_t*>(a.cache.v_scale), a.cache_lens, a.parents,
                        rows_of(a.cache, a.Hkv), a.Hq, a.Tn, a.max_seq_len, a.rope, a.theta,
                        static_cast<__nv_bfloat16*>(a.q_rot), a.q_factor, a.anc, a.lens, a.vflag,
-                       a.words, a.status);
+                       a.words, drafts, a.status);
 }
 
 cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
