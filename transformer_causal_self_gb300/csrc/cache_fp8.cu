@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 8) append_fp8_kernel(
     cs[j] = 1.f;
     sn[j] = 0.f;
     if (layout != 0)
-      rope_cos_sin<false>(L + t, th_hi[8 * c + j], th_lo[8 * c + j], cs[j], sn[j]);
+      angle_cos_sin(L + t, th_hi[8 * c + j], th_lo[8 * c + j], cs[j], sn[j]);
   }
   uint8_t* const out = is_k ? k_cache : v_cache;
   uint8_t* const scale = is_k ? k_scale : v_scale;

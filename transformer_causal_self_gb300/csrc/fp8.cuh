@@ -166,6 +166,36 @@ struct CacheRows {
   }
 };
 
+// cos and sin of pos * theta, theta = hi + lo, 0 <= pos * theta < 2^16: the product as two floats
+// (exact but for lo's), the nearest multiple of pi/2 taken off it in three parts, then the Taylor
+// sums on [-pi/4, pi/4] (truncated below 2^-27).  Off by less than 2^-23, a quarter of what
+// __sincosf is: a key is rounded to e4m3 once, and every error before decides more ties.
+__device__ __forceinline__ void angle_cos_sin(int pos, float th_hi, float th_lo, float& c,
+                                              float& s) {
+  const float p = static_cast<float>(pos);
+  const float a_hi = p * th_hi;
+  const float a_lo = fmaf(p, th_lo, fmaf(p, th_hi, -a_hi));
+  const float k = rintf(a_hi * 0.63661977f);  // 2 / pi
+  float r = fmaf(-k, 1.5703125f, a_hi);       // pi/2 = 201/128 + 2029/2^22 + 7.549789954e-8
+  r = fmaf(-k, 4.837512969970703125e-4f, r);
+  r = fmaf(-k, 7.549789954e-8f, r) + a_lo;
+  const float z = r * r;
+  float sn = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+  sn = fmaf(sn, z, 1.f / 120.f);
+  sn = fmaf(sn, z, -1.f / 6.f);
+  sn = fmaf(sn * z, r, r);
+  float cs = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+  cs = fmaf(cs, z, -1.f / 720.f);
+  cs = fmaf(cs, z, 1.f / 24.f);
+  cs = fmaf(cs, z, -0.5f);
+  cs = fmaf(cs, z, 1.f);
+  const int q = static_cast<int>(k);
+  s = (q & 1) ? cs : sn;
+  c = (q & 1) ? sn : cs;
+  if (q & 2) s = -s;
+  if ((q + 1) & 2) c = -c;
+}
+
 // RoPE of 16 channels held as two pieces of eight (see rope_piece): y[0..7] and y[8..15]
 // are the turned channels of the first and the second piece.  layout 1 (split-half): pairs
 // (u_i, w_i), angle i; layout 2 (adjacent): piece one holds pairs 0..3, piece two 4..7.

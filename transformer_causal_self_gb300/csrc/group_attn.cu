@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
           c1[j] = 1.f;
           s1[j] = 0.f;
           if (p.rope != 0)
-            rope_cos_sin<false>(pos, p.theta.hi[at], p.theta.lo[at], c1[j], s1[j]);
+            angle_cos_sin(pos, p.theta.hi[at], p.theta.lo[at], c1[j], s1[j]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -117,7 +117,12 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
       int depth = -1;
       for (int w = 0; w < words; ++w) depth += __popc(s_anc[t0 + k][w]);
       // (padding is written like a first token, never seen)
-      rope_cos_sin<false>(L + max(depth, 0), theta.hi[c], theta.lo[c], s_cos[k][c], s_sin[k][c]);
+      const int pos = L + max(depth, 0);
+      // (a bf16 cache's rows are those of the other appends to it)
+      if constexpr (F8)
+        angle_cos_sin(pos, theta.hi[c], theta.lo[c], s_cos[k][c], s_sin[k][c]);
+      else
+        rope_cos_sin<false>(pos, theta.hi[c], theta.lo[c], s_cos[k][c], s_sin[k][c]);
     }
   }
   __syncthreads();
