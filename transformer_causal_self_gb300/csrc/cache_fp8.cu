@@ -4,9 +4,9 @@
 // in fp32 and rounded once, to e4m3; the value is rounded as given.  Read: rows
 // 0..seq_lens[b]-1 back to bf16, exactly.  Both move each byte once and are bound by
 // HBM (4 bytes in, 2 + 1/64 out per channel pair; the reverse for the read), by latency where
-// they are short.  128 channels, 8 KV heads: the append of 4 x 4096 tokens takes 21.7 us (101 MB,
-// 4.7 TB/s: less than two waves, whose loads, angles and stores follow one another), of 64 tokens
-// 2.7 us; the read of 32768 rows 33.0 us (202 MB, 6.1 TB/s), of 8 x 17..1024 rows 4.9 us.
+// they are short.  128 channels, 8 KV heads: the append of 4 x 4096 tokens takes 20.9 us (101 MB,
+// 4.8 TB/s: less than two waves, whose loads, angles and stores follow one another), of 64 tokens
+// 2.8 us; the read of 32768 rows 33.0 us (202 MB, 6.1 TB/s), of 8 x 17..1024 rows 4.9 us.
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -21,8 +21,10 @@ constexpr int kHeads = 2;  // KV heads whose loads (two each) a thread has in fl
 // Thread item (b, head group, t, c): 16 channels of a token in `span` KV heads, kHeads at a time;
 // the G = d/16 threads of a row are neighbouring lanes.  The first k_blocks blocks take the
 // keys (whose angles serve all of the thread's heads), the others the values.
+// (Seven blocks per SM: eight leave 64 registers and spill, 22.3 us for the prompts above against
+// 20.9; six take 24.2.)
 template <int D>
-__global__ void __launch_bounds__(kThreads, 8) append_fp8_kernel(
+__global__ void __launch_bounds__(kThreads, 7) append_fp8_kernel(
     const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
     uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, uint8_t* __restrict__ k_scale,
     uint8_t* __restrict__ v_scale, const int32_t* __restrict__ cache_lens, CacheRows rows, int B,
