@@ -1,0 +1,140 @@
+"""Attention over an 8-bit cache at the ends of the scale codes' range and with rows of very
+different scales beside one another, against float64.
+
+Tolerance, per output element, with w_j a query's weights (of sum 1) and A = sum_j w_j |v_j|:
+  2^-8 |out|           the output's rounding to bf16 (half a step, doubled)
+  2^-11 A              weights rounded to 11 bits (half a step: 2^-12 A) and what is below f16's
+                       least (2^-31 of the largest term for each row: < 2^-20 A for 1000 rows)
+  2^-17 max|x| A       scores x as fp32 sums of d <= 128 products and one fp32 addition: off by
+                       at most 2^-18 of sum |q_i k_i| * scale * log2(e), which is taken as x here
+  2^-133               a step of bf16 below its normal numbers
+The reference reads the rows the cache holds and rounds the query as the kernels do."""
+import numpy as np
+import pytest
+import torch
+
+import transformer_causal_self_gb300 as csattn
+from oracle import attn as OA
+from tests import fp8_helpers as H
+from tests import test_gpu_tree as T
+from tests.gpu_helpers import dev, to_np
+
+pytestmark = pytest.mark.gpu
+
+
+def _reference(q, kk, vv, seen):
+    """q [Hq, T, d] rounded, kk, vv [Hkv, n, d], seen [T, n]: (out, lse, bound) in float64."""
+    Hq, n_t, d = q.shape
+    rep = Hq // kk.shape[0]
+    out, bound, lse = np.zeros(q.shape), np.zeros(q.shape), np.zeros((Hq, n_t))
+    for h in range(Hq):
+        for t in range(n_t):
+            k, v = kk[h // rep][seen[t]], vv[h // rep][seen[t]]
+            z = (k @ q[h, t]) / np.sqrt(d)
+            big = np.max(np.abs(k) @ np.abs(q[h, t])) / np.sqrt(d) * 1.4427
+            w = np.exp(z - z.max())
+            lse[h, t] = z.max() + np.log(w.sum())
+            w /= w.sum()
+            out[h, t] = w @ v
+            a = w @ np.abs(v)
+            bound[h, t] = (2.0 ** -8 * np.abs(out[h, t]) + (2.0 ** -11 + 2.0 ** -17 * big) * a +
+                           2.0 ** -133)
+    return out, lse, bound
+
+
+def _close(got, ref, bound, what):
+    assert np.all(np.isfinite(got)), what
+    off = np.abs(got - ref) / bound
+    assert off.max() <= 1.0, f"{what}: {off.max():.3g} times the bound"
+
+
+def _check_tree(q, k, v, prefix_k, prefix_v, parents, d, page=0, queries=None, **kw):
+    """A step over a prefix [Hkv, L, d] (float tensors of bf16 values); `queries`: the drafts
+    whose outputs are checked."""
+    Hkv, L, _ = prefix_k.shape
+    Hq, Tn = q.shape[1:3]
+    c = H.empty_cache(1, Hkv, L + Tn, d, page, True, seed=1)
+    if L:
+        H.set_rows(c, 0, 0, prefix_k, prefix_v)
+    cd = H.to_dev(c)
+    lse = torch.zeros(1, Hq, Tn, device=dev())
+    out = T._step(cd, q.to(dev()), k.to(dev()), v.to(dev()), H.i32([L]), H.i32([parents]),
+                  lse=lse, **kw)
+    csattn.check_status()
+    kk, vv = H.rows(H.to_cpu(cd), 0, L + Tn)
+    anc = OA.tree_ancestors(parents)
+    at = [t for t in range(Tn) if anc[t, t]] if queries is None else queries
+    seen = [np.concatenate([np.arange(L), L + np.nonzero(anc[t])[0]]).astype(int) for t in at]
+    ref, ref_lse, bound = _reference(H.round_query(q[0, :, at].double().numpy(), True), kk, vv,
+                                     seen)
+    _close(to_np(out)[0][:, at], ref, bound, "out")
+    got = lse.double().cpu().numpy()[0][:, at]
+    assert np.max(np.abs(got - ref_lse) / np.maximum(1.0, np.abs(ref_lse))) <= 1e-3
+    return out
+
+
+def _inputs(Hq, Hkv, L, Tn, d, seed):
+    g = H.gen(seed)
+    new = [torch.randn(1, h, Tn, d, generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv)]
+    old = [torch.randn(Hkv, L, d, generator=g).to(torch.bfloat16) for _ in range(2)]
+    return new + old
+
+
+def _decode(q, k, v, **kw):
+    """q [1, Hq, 1, d], k, v [Hkv, L, d]: checked decode over them."""
+    Hkv, L, d = k.shape
+    c = H.empty_cache(1, Hkv, L, d, 0, True, seed=2)
+    H.set_rows(c, 0, 0, k, v)
+    cd = H.to_dev(c)
+    out = csattn.attn_decode_fp8(q.to(dev()), cd["k"], cd["v"], cd["ks"], cd["vs"], H.i32([L]),
+                                 **kw)
+    csattn.check_status()
+    kk, vv = H.rows(c, 0, L)
+    seen = [np.arange(L)]
+    ref, _, bound = _reference(H.round_query(q[0].double().numpy(), True), kk, vv, seen)
+    _close(to_np(out)[0], ref, bound, "decode")
+
+
+# (a value of a row's largest code: 1.75 * 2^127 and more; of its least: 448 * 2^-124 and less)
+SPANS = {"top": lambda x, n: torch.where(x < 0, -1.0, 1.0) * 2.0 ** 127 * 1.8,
+         "bottom": lambda x, n: x * 2.0 ** -122,
+         "least": lambda x, n: x * 2.0 ** -128,
+         "low": lambda x, n: x * 2.0 ** -112,
+         "halves": lambda x, n: torch.where(torch.arange(n)[:, None] < n // 2, x * 2.0 ** -118,
+                                            x * 2.0 ** 100),
+         "halves, upper first": lambda x, n: torch.where(torch.arange(n)[:, None] >= n // 2,
+                                                         x * 2.0 ** -118, x * 2.0 ** 100),
+         "top and one": lambda x, n: torch.where(torch.arange(n)[:, None] % 128 == 5,
+                                                 1.9 * 2.0 ** 127, x),
+         "zeros and one large": lambda x, n: torch.where(torch.arange(n)[:, None] == 5,
+                                                         x * 2.0 ** 60, 0.0)}
+
+
+@pytest.mark.parametrize("splits", [0, 1, 7])
+@pytest.mark.parametrize("span", SPANS)
+@pytest.mark.parametrize("d,Hq", [(64, 4), (128, 4), (128, 12)])
+def test_decode_over_the_range_of_values(d, Hq, span, splits):
+    q, _, _, pk, pv = _inputs(Hq, 1, 512, 1, d, 3)
+    _decode(q, pk, SPANS[span](pv.double(), 512).to(torch.bfloat16), num_splits=splits)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("span", SPANS)
+@pytest.mark.parametrize("d,Hq,Tn", [(128, 2, 4), (64, 4, 4)])
+def test_tree_over_the_range_of_values(d, Hq, Tn, span, splits):
+    """In one tile, over the tiles of one CTA and over CTAs."""
+    q, k, v, pk, pv = _inputs(Hq, 1, 512 - Tn, Tn, d, 4)
+    both = SPANS[span](torch.cat([pv, v[0]], 1).double(), 512).to(torch.bfloat16)
+    _check_tree(q, k, both[None, :, 512 - Tn:], pk, both[:, :512 - Tn].contiguous(),
+                [t // 2 - 1 for t in range(Tn)], d, num_splits=splits)
+
+
+@pytest.mark.parametrize("shift", [-116, -100, -40, 40, 100, 116])
+@pytest.mark.parametrize("Hq,Tn", [(2, 4), (4, 4)])
+def test_keys_and_queries_over_the_range(Hq, Tn, shift):
+    """Keys and queries whose scales cancel."""
+    q, k, v, pk, pv = _inputs(Hq, 1, 300, Tn, 128, 6)
+    q = (q.double() * 2.0 ** -shift).to(torch.bfloat16)
+    k, pk = ((x.double() * 2.0 ** shift).to(torch.bfloat16) for x in (k, pk))
+    _check_tree(q, k, v, pk, pv, [-1] * Tn, 128)
+    _decode(q[:, :, :1].contiguous(), pk, pv)

@@ -661,7 +661,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       }
     if (!ok) break;
     if (threadIdx.x == 0) pc.leave_for_merge(p.line);
-    // the warp's partial result, relative to the maximum of x
+    // The warp's partial result.  bf16: relative to the maximum of x.  e4m3: to the power of two
+    // that leaves l in [0.5, 1), and its values times 2^-kPartLog2, so that they are of the
+    // output's size whatever the values' scales; the factor of o is taken in two halves, 2^n
+    // alone leaving fp32's range at the ends of the codes'.
     const size_t slot =
         (static_cast<size_t>(blockIdx.x) + pc.segment(p.line)) * NW + warp;
 #pragma unroll
@@ -671,17 +674,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
         const int r = 8 * j + cq + h;
         if (row_base + r >= M) continue;
         // (a row that saw nothing holds zeros, or NaN if its scores were NaN)
-        const float f =
-            F8 && n_used[j][h] != -INFINITY ? ex2_approx(n_used[j][h] - kWeightLog2) : 1.f;
+        float m = m_used[j][h], l = l_part[j][h], f = 1.f;
+        if (F8 && n_used[j][h] != -INFINITY) {
+          const int up = log2_above(l);
+          m += static_cast<float>(up);
+          l *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          f = ex2_approx(0.5f * (n_used[j][h] -
+                                 (kWeightLog2 + kPartLog2 + static_cast<float>(up))));
+        }
         const size_t at = slot * p.part_rows + r;
         float* dst = p.part_o + at * D;
-        if (r0 == 0)
-          *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_used[j][h], l_part[j][h]);
+        if (r0 == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m, l);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           if constexpr (F8) {
             *reinterpret_cast<float2*>(dst + 16 * c + 2 * r0) =
-                make_float2(o[c][j][h] * f, o[c][j][2 + h] * f);
+                make_float2(o[c][j][h] * f * f, o[c][j][2 + h] * f * f);
           } else {
             dst[16 * c + r0] = o[c][j][h];
             dst[16 * c + r0 + 8] = o[c][j][2 + h];
@@ -692,8 +700,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
 }
 
 // out[b, h, t, :] = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the partial results of a
-// query row: `subs` for each piece of its segment.  W warps per row (W > 1 for few rows with
-// many partials), four (d = 128) or two channels per lane.
+// query row: `subs` for each piece of its segment, times 2^kPartLog2 for an e4m3 cache.  W warps
+// per row (W > 1 for few rows with many partials), four (d = 128) or two channels per lane.
 template <int D, int W>
 __global__ void __launch_bounds__(32 * (W > 4 ? W : 4)) group_merge_kernel(
     const float* __restrict__ part_o, const float* __restrict__ part_ml, const int2* seg, int heads,
@@ -782,7 +790,7 @@ __global__ void __launch_bounds__(32 * (W > 4 ? W : 4)) group_merge_kernel(
     m = mx;
   }
   const bool any = !(l <= 0.f);  // NaN stays
-  const float inv = any ? 1.f / l : 0.f;
+  const float inv = any ? (f8 ? kPartScale : 1.f) / l : 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = any ? acc[i] * inv : 0.f;
   if (vflag != nullptr && ns > 0) {

@@ -40,6 +40,14 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
       : "memory");
 }
 
+// Partial results over an e4m3 cache hold values of the output's size times 2^-kPartLog2: 4096 of
+// them, as large as bf16 goes, add up within fp32, and bf16's least (2^-133) keeps four bits.
+constexpr float kPartLog2 = 12.f, kPartScale = 4096.f;
+// e with l in [2^(e-1), 2^e), at most 100 (also of infinities and NaN): 2^-e is a normal number
+__device__ __forceinline__ int log2_above(float l) {
+  return min(static_cast<int>((__float_as_uint(l) >> 23) & 0xffu) - 126, 100);
+}
+
 struct GroupLine {
   const int32_t* lens;
   int2* seg;            // [B * heads] of a segment: its first piece and their number
