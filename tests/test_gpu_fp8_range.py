@@ -120,7 +120,8 @@ def test_decode_over_the_range_of_values(d, Hq, span, splits):
 
 @pytest.mark.parametrize("splits", [0, 1, 4])
 @pytest.mark.parametrize("span", SPANS)
-@pytest.mark.parametrize("d,Hq,Tn", [(128, 2, 4), (64, 4, 4)])
+@pytest.mark.parametrize("d,Hq,Tn", [(128, 2, 4), (64, 4, 4), (64, 8, 12), (128, 8, 12),
+                                       (128, 8, 20)])
 def test_tree_over_the_range_of_values(d, Hq, Tn, span, splits):
     """In one tile, over the tiles of one CTA and over CTAs."""
     q, k, v, pk, pv = _inputs(Hq, 1, 512 - Tn, Tn, d, 4)

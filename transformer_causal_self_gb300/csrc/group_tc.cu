@@ -25,7 +25,9 @@
 // numbers per tile, and one exponential serves denominator and numerator:
 //   w = 2^(x + E_v - R), O += w V16, l += 2^(-E_v) * sum w, R the running maximum of x + E_v.
 // R is raised only by more than 2^8, as elsewhere; w is then at most 2^8 (bf16), or 2^15 with
-// the 2^7 that the e4m3 path adds for f16's range.
+// the 2^7 that the e4m3 path adds for f16's range.  Where x + E_v is so far below R that w would
+// leave fp32's range (small values beside large ones), a tile's weights are taken relative to its
+// own maximum: its values vanish beside the others, its share of l need not.
 //
 // A 128-row tile of 128 channels takes an SM 1.49 us with up to 128 query rows over bf16 (6.7
 // TB/s over all SMs: HBM) and 1.81 with 256 (1410 TFLOP/s: 32 products of N = 128, which at
@@ -42,6 +44,9 @@ constexpr int BN = 128;  // cache rows per tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr float kRescaleThreshold = 8.0f;
+// e4m3: below R by kLowTile (2^(7 - 96 - 30) is still a normal number) the largest weight of a tile
+// is put at 2^-kLowWeight, which is 0 in f16
+constexpr float kLowTile = 96.0f, kLowWeight = 60.0f;
 constexpr int kMinValueCode = 27;  // E_v >= -100
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 12;
 
@@ -744,8 +749,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
           const bool mine = top > R + kRescaleThreshold;
           if (__any_sync(0xffffffffu, mine)) {
-            const float f = mine ? ex2_approx(R - top) : 1.f;
+            float f = mine ? ex2_approx(F8 ? 0.5f * (R - top) : R - top) : 1.f;
             l *= f;
+            if constexpr (F8) {  // (O may vanish beside the tile to come, l need not)
+              l *= f;
+              f *= f;
+            }
             if (j >= step) {
               if constexpr (!F8) tmem_ld32_wait(ra);
 #pragma unroll 1
@@ -760,8 +769,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             if (mine) R = top;
           }
+          // what the tile's weights are relative to
+          const bool low = F8 && top < R - kLowTile && top != -INFINITY;
+          const float Rt = low ? top + (7.f + kLowWeight) : R;
           // (nothing seen yet: 2^-inf = 0, and a NaN score stays NaN)
-          const float off = (F8 ? ev + 7.f : 0.f) - (R == -INFINITY ? 0.f : R);
+          const float off = (F8 ? ev + 7.f : 0.f) - (Rt == -INFINITY ? 0.f : Rt);
           float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
           auto weights32 = [&](const uint32_t (&r)[32], uint32_t at) {
             uint32_t pk[16];
@@ -801,7 +813,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             weights32(rb, tS + 48u);
           }
           const float sum = (sa0 + sa1) + (sb0 + sb1);
-          l += F8 ? sum * ex2_approx(-ev - 7.f) : sum;
+          if constexpr (F8) {  // (a factor at a time: their product may leave fp32's range)
+            const float g = low ? ex2_approx(0.5f * (Rt - R)) : 1.f;
+            l += sum * 0.0078125f * ex2_approx(-ev) * g * g;
+          } else {
+            l += sum;
+          }
           tmem_st_wait();
         }
         tc_fence_before();
@@ -817,22 +834,35 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       // stream 0 adds stream 1's sums to its own and hands back the factors of the two outputs;
       // then each stream's warps write half of the channels.
       const bool two = !pair && w.n > 1;  // both streams had tiles of this row
-      const float o_scale = F8 ? 1.f / 16384.f : 1.f;  // 2^-7 of w, 2^-7 of V16
-      float f0 = o_scale, f1 = 0.f;
-      if (!pair) {
+      // e4m3: relative to the power of two that leaves l in [0.5, 1), R counting the values' scales;
+      // returned is what O is multiplied by (2^-7 of w, 2^-7 of V16, kPartLog2)
+      auto relative = [](float& R, float& l) -> float {
+        if constexpr (!F8) return 1.f;
+        const int up = log2_above(l);
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        R += static_cast<float>(up);
+        l *= f;
+        return f * (1.f / (16384.f * kPartScale));
+      };
+      float f0 = 1.f, f1 = 0.f;
+      if (pair) {
+        f0 = relative(R, l);
+      } else {
         if (x == 1) s_ml[row] = make_float2(R, l);
         asm volatile("bar.sync 2, 256;" ::: "memory");
         if (x == 0) {
+          f0 = relative(R, l);
           if (two) {
-            const float2 other = s_ml[row];
+            float2 other = s_ml[row];
+            f1 = relative(other.x, other.y);
             const float m = fmaxf(R, other.x);
             // (a stream that saw nothing holds zeros, or NaN)
             const float e0 = R == -INFINITY ? 1.f : ex2_approx(R - m);
             const float e1 = other.x == -INFINITY ? 1.f : ex2_approx(other.x - m);
             l = l * e0 + other.y * e1;
             R = m;
-            f0 = o_scale * e0;
-            f1 = o_scale * e1;
+            f0 *= e0;
+            f1 *= e1;
           }
           s_ml[row] = make_float2(f0, f1);
         }
@@ -974,7 +1004,7 @@ __global__ void __launch_bounds__(MergeShape<D, V>::THREADS) group_tc_merge_kern
     }
   }
   const bool any = !(l <= 0.f);  // NaN stays
-  const float inv = any ? 1.f / l : 0.f;
+  const float inv = any ? (f8 ? kPartScale : 1.f) / l : 0.f;
   float x[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
