@@ -131,7 +131,7 @@ def test_tree_over_the_range_of_values(d, Hq, Tn, span, splits):
 
 
 @pytest.mark.parametrize("shift", [-116, -100, -40, 40, 100, 116])
-@pytest.mark.parametrize("Hq,Tn", [(2, 4), (4, 4)])
+@pytest.mark.parametrize("Hq,Tn", [(2, 4), (8, 12)])
 def test_keys_and_queries_over_the_range(Hq, Tn, shift):
     """Keys and queries whose scales cancel."""
     q, k, v, pk, pv = _inputs(Hq, 1, 300, Tn, 128, 6)

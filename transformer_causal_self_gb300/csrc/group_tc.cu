@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 39);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::TILES + C::BARS);  // [128]
-  float2* s_tile = s_ml + 128;  // e4m3 [8]: 2^(E_k - 7), E_v of a tile
+  float2* s_tile = s_ml + 128;  // e4m3 [8]: 2^E_k, E_v of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             E = __reduce_max_sync(0xffffffffu, max(hk & 0xffffu, hk >> 16));
             if (tid == 0)
               s_tile[tile & 7] =
-                  make_float2(__uint_as_float(static_cast<uint32_t>(max(E - 7, 1)) << 23), Ev);
+                  make_float2(__uint_as_float(static_cast<uint32_t>(E) << 23), Ev);
           }
           uint32_t factor;
           {
@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           if constexpr (F8) {
             const float2 ts = s_tile[(tile0 + j) & 7];
             c *= ts.x;
+            c *= 0.0078125f;  // (by itself: 2^(E_k - 7) may be too small)
             ev = ts.y;
           }
           c = fmaxf(c, 1.17549435e-38f);  // (a hidden score's -inf times 0 would be NaN)
