@@ -638,9 +638,10 @@ size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int 
  *   max_seq_len  bounds cache_lens[b] + Tn (<= Lmax; <= 49152 with RoPE)
  *   workspace  >= csattn_tree_workspace_size() bytes, 16-byte aligned, in use until the work on
  *              `stream` completes (calls that may run at once need one each)
- * Over an 8-bit cache the rotated queries are rounded to 11 bits and, with more than 16 query
- * rows per KV head (Tn * Hq / Hkv), 128 cache rows share an exponent in the products: what is
- * below 2^-30 of the largest key or value among them loses bits, below 2^-40 it vanishes.
+ * Over an 8-bit cache the rotated queries and the weights are rounded to 11 bits.  With more
+ * than 16 query rows per KV head (Tn * Hq / Hkv), rows with scale code 3 (zeros, or all below
+ * 2^-115) may lose bits beside much larger rows among the same 128; and 128 rows whose scales
+ * are further apart than 2^12 (values) or 2^22 (keys) take about twice the time of others.
  * Requirements: 1 <= Tn <= 256, d in {64, 128}, any Hq / Hkv.  Values of drafts that a query
  * does not see have no part in its output whatever they hold (NaN and infinities included).
  * Rows at or past cache_lens[b] + Tn are neither used nor written.  A length out of range or

@@ -80,6 +80,48 @@ def _inputs(Hq, Hkv, L, Tn, d, seed):
     return new + old
 
 
+HUGE = [float(torch.finfo(torch.bfloat16).max), 1e30]
+
+
+@pytest.mark.parametrize("L", [0, 30, 300])
+@pytest.mark.parametrize("what", ["keys", "values", "both"])
+@pytest.mark.parametrize("Tn,Hq,d", [(6, 2, 64), (6, 2, 128), (40, 4, 64), (40, 4, 128),
+                                     (40, 8, 128)])
+def test_finite_values_of_unseen_drafts_stay_out(Tn, Hq, d, what, L):
+    """The largest finite values, and 1e30, in a branch and in padding: the drafts that see
+    neither have the outputs of a run without them, but for the weights' rounding."""
+    q, k, v, pk, pv = _inputs(Hq, 1, L, Tn, d, Tn + d + L)
+    parents = [-1, 0, -1, 2] + [-1] * (Tn - 6) + [-2, -2]
+    free = [t for t in range(Tn - 2) if t not in (2, 3)]
+    for huge in HUGE:
+        kb, vb = k.clone(), v.clone()
+        for t in (2, 3, Tn - 2, Tn - 1):
+            if what != "values":
+                kb[0, 0, t] = torch.where(k[0, 0, t] < 0, -huge, huge)
+            if what != "keys":
+                vb[0, 0, t] = torch.where(v[0, 0, t] < 0, -huge, huge)
+        _check_tree(q, kb, vb, pk, pv, parents, d, queries=free)
+
+
+@pytest.mark.parametrize("Tn,Hq", [(6, 2), (40, 4)])
+@pytest.mark.parametrize("base", [1e30, 1e10, 1e-20])
+def test_rows_of_another_scale_in_sight(Tn, Hq, base):
+    """A value row far from the others' scale, and keys far below them, in everybody's sight."""
+    d, L = 128, 200
+    q, k, v, pk, pv = _inputs(Hq, 1, L, Tn, d, 5)
+    pv[0, 7] = pv[0, 7] * base
+    pk[0, 11::16] = pk[0, 11::16] * 1e-12
+    k[0, 0, 1] = 0
+    _check_tree(q, k, v, pk, pv, [-1] * Tn, d)
+    # a small value with nearly all of the weight beside large ones with hardly any
+    q[:] = 1
+    pk[0], k[0, 0] = 0, 0
+    pk[0, 3] = 4.0                               # x = 4 * 128 / sqrt(128) = 45 nats = 65 octaves
+    pv[0, 3] = pv[0, 3] * 2.0 ** -40
+    pv[0, 4:] = pv[0, 4:] * 2.0 ** 20
+    _check_tree(q, k, v, pk, pv, [-1] * Tn, d)
+
+
 def _decode(q, k, v, **kw):
     """q [1, Hq, 1, d], k, v [Hkv, L, d]: checked decode over them."""
     Hkv, L, d = k.shape

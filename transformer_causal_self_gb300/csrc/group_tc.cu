@@ -20,14 +20,19 @@
 //
 // An e4m3 tile becomes f16 with one scale for all its rows: row j is multiplied by 2^(7 - (E -
 // e_j)), E the largest exponent of the tile (at least -100 for values).  That is exact while
-// e_j is within about 15 of E; below, a row's error is an absolute 2^-32 of the tile's largest
-// value, which fp32 sums would not resolve either.  So the scales reach the softmax as two
-// numbers per tile, and one exponential serves denominator and numerator:
+// e_j is within 22 of E.  So the scales reach the softmax as two numbers per tile, and one
+// exponential serves denominator and numerator:
 //   w = 2^(x + E_v - R), O += w V16, l += 2^(-E_v) * sum w, R the running maximum of x + E_v.
 // R is raised only by more than 2^8, as elsewhere; w is then at most 2^8 (bf16), or 2^15 with
 // the 2^7 that the e4m3 path adds for f16's range.  Where x + E_v is so far below R that w would
 // leave fp32's range (small values beside large ones), a tile's weights are taken relative to its
 // own maximum: its values vanish beside the others, its share of l need not.
+// A tile whose rows are further apart (values: by more than 2^12, where R, which counts E_v
+// whether a query sees the largest row or not, would cost the others' weights bits of f16) keeps
+// its rows as they are, times 2^7, and the softmax takes every column's exponents from the scale
+// bytes: x_j = S_j 2^(e_j - 7), w_j = 2^(x_j + ev_j - R), R over the columns that the query sees,
+// and a second exponential for l.  So a draft that a query does not see, or padding, has no part
+// in its output however large it is.  Rows with the least code (zeros) do not count as far apart.
 //
 // A 128-row tile of 128 channels takes an SM 1.49 us with up to 128 query rows over bf16 (6.7
 // TB/s over all SMs: HBM) and 1.81 with 256 (1410 TFLOP/s: 32 products of N = 128, which at
@@ -48,6 +53,8 @@ constexpr float kRescaleThreshold = 8.0f;
 // is put at 2^-kLowWeight, which is 0 in f16
 constexpr float kLowTile = 96.0f, kLowWeight = 60.0f;
 constexpr int kMinValueCode = 27;  // E_v >= -100
+constexpr int kWideKeys = 22, kWideValues = 12;  // exponents further apart: a column each;
+constexpr float kOwnScales = 152.f;               // such a tile's E_v (2^-152 is 0)
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 12;
 
 template <int D, bool F8>
@@ -208,6 +215,85 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Scale bytes of a tile, four rows in each lane of a warp (0 where there is no row): the largest
+// (at least `least`), and whether one of the lane's rows is more than `limit` below it.
+struct TileScale {
+  int E;
+  bool far;
+  __device__ __forceinline__ TileScale(uint32_t four, int least, int limit) {
+    const uint32_t a = four & 0xff00ffu, b = (four >> 8) & 0xff00ffu;
+    const uint32_t hi = __vmaxu2(a, b);
+    E = max(static_cast<int>(__reduce_max_sync(0xffffffffu, max(hi & 0xffffu, hi >> 16))), least);
+    // 4 is taken off each half, so that codes up to kScaleMin wrap round to the top (the upper
+    // half loses 5 where the lower one does not carry: one octave later is as good)
+    static_assert(kScaleMin == 3, "codes that do not count");
+    const uint32_t lo = __vminu2(a + 0xfffbfffcu, b + 0xfffbfffcu);
+    far = E - 4 - static_cast<int>(min(lo & 0xffffu, lo >> 16)) > limit;
+  }
+};
+
+__device__ __forceinline__ void tmem_ld4_sync(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// A tile whose columns keep scales of their own (see the file's head): x_j + ev_j - kOwnScales takes
+// the place of every score of the thread's row.  Returns the largest x_j + ev_j and log2 of the sum
+// of 2^x_j.  Out of line: these tiles are rare, and inline the softmax loop no longer fits the
+// instruction cache as well (16 x 32 drafts over 512..8192 rows 76.8 us, like this 73.8).
+__device__ __noinline__ float2 own_scales(const TParams& p, int b, int kvh, int row0, int k_end,
+                                          uint32_t tS, float row_factor) {
+  const int lane = threadIdx.x & 31, r = row0 + 4 * lane;
+  uint32_t own_k = 0u, own_v = 0u;  // four rows' codes (no page ends inside them)
+  const long long at = r < k_end ? p.rows.at(b, kvh, r) : -1;
+  for (int i = 0; at >= 0 && i < 4 && r + i < k_end; ++i) {
+    own_k |= static_cast<uint32_t>(p.k_scale[at + i]) << (8 * i);
+    own_v |= static_cast<uint32_t>(p.v_scale[at + i]) << (8 * i);
+  }
+  const TileScale sk(own_k, 0, kWideKeys), sv(own_v, kMinValueCode, kWideValues);
+  if (!__any_sync(0xffffffffu, sk.far)) own_k = 0x01010101u * sk.E;
+  own_v = __any_sync(0xffffffffu, sv.far) ? __vmaxu4(own_v, 0x01010101u * kMinValueCode)
+                                          : 0x01010101u * sv.E;
+  float x0 = -INFINITY, sum = 0.f, top = -INFINITY;
+  __syncwarp();
+  for (int i = 0; i < BN; i += 4) {
+    const uint32_t ek = __shfl_sync(0xffffffffu, own_k, i >> 2);
+    const uint32_t ev4 = __shfl_sync(0xffffffffu, own_v, i >> 2);
+    uint32_t s4[4];
+    float xs[4];
+    tmem_ld4_sync(tS + i, s4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float f = __uint_as_float(((ek >> (8 * e)) & 0xffu) << 23);
+      // (neither 0 nor infinity: a hidden score is -inf, another may be 0)
+      const float g = fminf(fmaxf(row_factor * f * 0.0078125f, 1.17549435e-38f), 3e38f);
+      xs[e] = __fmul_rn(__uint_as_float(s4[e]), g);
+      const float y =
+          xs[e] + (static_cast<float>((ev4 >> (8 * e)) & 0xffu) - (127.f + kOwnScales));
+      top = fmaxf(top, y);
+      s4[e] = __float_as_uint(y);
+    }
+    tmem_st4(tS + i, s4);
+    const float up = fmaxf(fmaxf(x0, fmaxf(xs[0], xs[1])), fmaxf(xs[2], xs[3]));
+    const float at0 = up == -INFINITY ? 0.f : up;
+    sum *= ex2_approx(x0 - at0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += ex2_approx(xs[e] - at0);
+    x0 = up;
+  }
+  tmem_st_wait();
+  return make_float2(top + kOwnScales, sum == 0.f ? -INFINITY : x0 + __log2f(sum));
+}
+
 // 2^(7 - below) in f16 (0 where that is less than f16's least)
 __device__ __forceinline__ uint16_t row_scale(int below) {
   return __half_as_ushort(
@@ -244,7 +330,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 39);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::TILES + C::BARS);  // [128]
-  float2* s_tile = s_ml + 128;  // e4m3 [8]: 2^E_k, E_v of a tile
+  float2* s_tile = s_ml + 128;  // e4m3 [8]: 2^E_k, E_v (or kOwnScales) of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -579,23 +665,26 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           const int page_next = load_page(j + 2);
           // the tile's largest codes, then the factors of the warp's 32 rows, one per lane: row
           // i * (128 / G) + (32 / G) * warp + q of the tile in lane (32 / G) * i + q
-          const uint32_t hv = __vmaxu2(cv & 0xff00ffu, (cv >> 8) & 0xff00ffu);
-          int E = max(static_cast<int>(__reduce_max_sync(0xffffffffu, max(hv & 0xffffu, hv >> 16))),
-                      kMinValueCode);
+          TileScale sc(cv, kMinValueCode, kWideValues);
+          bool wide = sc.far;
           if (v == 0) {
-            const float Ev = static_cast<float>(E - 127);
-            const uint32_t hk = __vmaxu2(ck & 0xff00ffu, (ck >> 8) & 0xff00ffu);
-            E = __reduce_max_sync(0xffffffffu, max(hk & 0xffffu, hk >> 16));
+            const float Ev = static_cast<float>(sc.E - 127);
+            sc = TileScale(ck, 0, kWideKeys);
+            wide = __any_sync(0xffffffffu, wide || sc.far);
             if (tid == 0)
-              s_tile[tile & 7] =
-                  make_float2(__uint_as_float(static_cast<uint32_t>(E) << 23), Ev);
+              s_tile[tile & 7] = make_float2(
+                  __uint_as_float(static_cast<uint32_t>(sc.E) << 23), wide ? kOwnScales : Ev);
+            if (wide) wide = __any_sync(0xffffffffu, sc.far);
+          } else {
+            wide = __any_sync(0xffffffffu, wide);
           }
           uint32_t factor;
           {
             constexpr int Q = 32 / G;
             const int r = (lane / Q) * (128 / G) + Q * (warp & 3) + lane % Q;
             const uint32_t four = __shfl_sync(0xffffffffu, v == 0 ? ck : cv, r >> 2);
-            factor = row_scale(E - static_cast<int>((four >> (8 * (r & 3))) & 0xffu));
+            const int code = static_cast<int>((four >> (8 * (r & 3))) & 0xffu);
+            factor = row_scale(!wide ? sc.E - code : v == 0 ? 0 : max(kMinValueCode - code, 0));
             factor |= factor << 16;
           }
           const uint32_t rs = f % C::NRAW, s = f % NS;
@@ -695,6 +784,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         tc_fence_after();
         if (warp_live) {
           float c = row_factor, ev = 0.f;
+          volatile float own_l;  // (in memory: set and read for such tiles alone)
           if constexpr (F8) {
             const float2 ts = s_tile[(tile0 + j) & 7];
             c *= ts.x;
@@ -747,7 +837,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             tmem_ld32_issue(tS, ra);
             max32(rb);
           }
-          const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
+          float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
+          // (then c = 1, and the sum of the tile's weights comes by way of own_l)
+          if (F8 && __builtin_expect(ev == kOwnScales, 0)) {
+            const float2 t = own_scales(p, w.b, w.kvh, w.k_begin + j * BN, w.k_end, tS, row_factor);
+            top = t.x;
+            own_l = t.y;
+            c = 1.f;
+          }
           const bool mine = top > R + kRescaleThreshold;
           if (__any_sync(0xffffffffu, mine)) {
             float f = mine ? ex2_approx(F8 ? 0.5f * (R - top) : R - top) : 1.f;
@@ -817,6 +914,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           if constexpr (F8) {  // (a factor at a time: their product may leave fp32's range)
             const float g = low ? ex2_approx(0.5f * (Rt - R)) : 1.f;
             l += sum * 0.0078125f * ex2_approx(-ev) * g * g;
+            if (__builtin_expect(ev == kOwnScales, 0)) {  // (2^-ev is 0)
+              const float h = ex2_approx(0.5f * (own_l - (R == -INFINITY ? 0.f : R)));
+              l += h * h;
+            }
           } else {
             l += sum;
           }
