@@ -704,6 +704,14 @@ int csattn_check_status(void* stream);
  */
 int csattn_selftest_bounded_wait(int limit_us, void* stream);
 
+/*
+ * The calling thread's next csattn_attn_decode_fp8 or csattn_attn_tree_step (or paged form) that
+ * launches runs with a barrier that waits for one arrival more than will come.  Its waits run out
+ * after 2 seconds, its kernels return normally, csattn_check_status() afterwards returns
+ * CSATTN_ERR_TIMEOUT, and its outputs are undefined.
+ */
+int csattn_selftest_lost_arrival(void);
+
 /* Message describing the last error returned on the calling thread. */
 const char* csattn_last_error(void);
 

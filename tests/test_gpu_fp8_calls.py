@@ -1,0 +1,51 @@
+"""Calls of the 8-bit cache and of token trees in their less usual circumstances: waits
+that run out."""
+import pytest
+import torch
+
+import transformer_causal_self_gb300 as csattn
+from tests import fp8_helpers as H
+from tests import test_gpu_tree as T
+from tests.gpu_helpers import dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("call", ["decode", "tree", "tree_8bit", "wide", "wide_8bit", "pair_8bit"])
+def test_a_wait_that_runs_out_is_reported(call):
+    """Many sequences, so that every CTA begins several segments; a workspace of bytes that are no
+    slots of it.  The merge finds what every segment left for it and the GPU stays usable."""
+    B, Hkv, d, L = 300, 2, 64, 100
+    Hq, Tn = {"wide": (16, 6), "wide_8bit": (16, 6), "pair_8bit": (16, 20)}.get(call, (4, 2))
+    g = H.gen(1)
+    c = H.to_dev(H.empty_cache(B, Hkv, L + Tn, d, 0, call.endswith("8bit") or call == "decode", 1))
+    for n in ("k", "v"):
+        H.raw(c[n]).zero_()
+    for n in [n for n in ("ks", "vs") if n in c]:
+        c[n].fill_(120)
+    lens = H.i32([L] * B)
+    q = torch.randn(B, Hq, Tn, d, generator=g).to(torch.bfloat16).to(dev())
+    k, v = (torch.randn(B, Hkv, Tn, d, generator=g).to(torch.bfloat16).to(dev()) for _ in range(2))
+    parents = H.i32([[-1] * Tn] * B)
+    if call == "decode":
+        need = csattn.decode_fp8_workspace_size(B, Hq, Hkv, L + Tn, d)
+    else:
+        need = csattn.tree_workspace_size(B, Hq, Hkv, Tn, L + Tn, d)
+
+    def run():
+        ws = torch.full((need,), 0x7E, dtype=torch.uint8, device=dev())
+        if call == "decode":
+            return csattn.attn_decode_fp8(q[:, :, :1].contiguous(), c["k"], c["v"], c["ks"],
+                                          c["vs"], lens, workspace=ws)
+        return T._step(c, q, k, v, lens, parents, workspace=ws)
+
+    want = run().clone()
+    csattn.check_status()
+    csattn.selftest_lost_arrival()
+    run()
+    with pytest.raises(csattn.CsattnError) as e:
+        csattn.check_status()
+    assert e.value.status == -4
+    again = run()
+    csattn.check_status()
+    assert H.same_bits(again, want)

@@ -23,7 +23,7 @@ __all__ = [
     "rope_rotate", "fwd_workspace_size", "fwd_ext_workspace_size", "fwd_host_workspace_size",
     "bwd_workspace_size", "bwd_ext_workspace_size", "decode_workspace_size",
     "decode_host_workspace_size", "decode_step_workspace_size", "check_status",
-    "selftest_bounded_wait", "EXPORTED_SYMBOLS",
+    "selftest_bounded_wait", "selftest_lost_arrival", "EXPORTED_SYMBOLS",
     "cache_append_fp8", "cache_append_fp8_paged", "cache_read_fp8", "cache_read_fp8_paged",
     "attn_decode_fp8", "attn_decode_fp8_paged", "attn_tree_step", "attn_tree_step_paged",
     "tree_commit", "tree_commit_paged", "decode_fp8_workspace_size", "tree_workspace_size",
@@ -103,6 +103,7 @@ _SIGNATURES = {
     "csattn_tree_commit_paged": (_c_int, [_vp] * 9 + [_c_int] * 8 + [_vp]),
     "csattn_check_status": (_c_int, [_vp]),
     "csattn_selftest_bounded_wait": (_c_int, [_c_int, _vp]),
+    "csattn_selftest_lost_arrival": (_c_int, []),
     "csattn_last_error": (ctypes.c_char_p, []),
     "csattn_status_str": (ctypes.c_char_p, [_c_int]),
     "csattn_version": (_c_int, []),
@@ -1026,3 +1027,9 @@ def check_status(stream=None) -> None:
 def selftest_bounded_wait(limit_us: int, stream=None) -> None:
     """Launch the kernel whose barrier wait must run out (see csattn_selftest_bounded_wait)."""
     _check(load_library().csattn_selftest_bounded_wait(int(limit_us), _stream_handle(stream)))
+
+
+def selftest_lost_arrival() -> None:
+    """The thread's next 8-bit decode or tree step runs into its wait limit (see
+    csattn_selftest_lost_arrival)."""
+    _check(load_library().csattn_selftest_lost_arrival())

@@ -180,6 +180,14 @@ bool sizes_ok(int B, int Hq, int Hkv, int T, int Lmax, int d, int num_splits) {
          Lmax < (1 << 30) && (d == 64 || d == 128) && num_splits >= 0;
 }
 
+// csattn_selftest_lost_arrival: the thread's next call
+thread_local int g_lost = 0;
+int take_lost() {
+  const int lost = g_lost;
+  g_lost = 0;
+  return lost;
+}
+
 int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
   if (workspace == nullptr || bytes < need || !aligned(workspace, 16))
     return api_fail(CSATTN_ERR_WORKSPACE,
@@ -278,6 +286,7 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
   int sms = 0;
   if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
   if ((rc = encoder_ready(fn)) != CSATTN_OK) return rc;
+  a.lost = take_lost();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_group_attn(a, st);
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_decode_fp8: kernel launch");
@@ -378,6 +387,7 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
   a.part_ml = a.part_o + partial_floats(a.plan, B, Hkv) * d;
   a.seg = reinterpret_cast<int2*>(ws + at.seg);
   a.status = p.status;
+  a.lost = take_lost();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_tree_prep(p, st);
   if (e != cudaSuccess) return api_fail_cuda(e, "attn_tree_step: append launch");
@@ -590,6 +600,11 @@ int csattn_tree_commit_paged(void* k_pages, void* v_pages, void* k_scale, void* 
                      paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
                            num_pages, max_pages),
                      cache_lens, parents, accepted, new_lens, B, Hkv, Tn, d, cache_dtype, stream);
+}
+
+int csattn_selftest_lost_arrival(void) {
+  g_lost = 1;
+  return CSATTN_OK;
 }
 
 }  // extern "C"

@@ -78,6 +78,7 @@ struct GParams {
   const uint8_t* k_scale;
   const uint8_t* v_scale;
   int words, rope;
+  int lost;          // arrivals that the queries' barrier waits for and nothing makes (selftest)
   int box_rows;
   bool code_copies;  // scale bytes lie so that bulk copies can take them
   float* part_o;
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
       mbar_init(&empty[s], NW);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
+      mbar_init(&q_full[i], 1 + p.lost);
       mbar_init(&q_empty[i], NW);
     }
     *abort_flag = 0;
@@ -697,6 +698,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
         }
       }
   }
+  // After a wait that ran out (otherwise n = 0): the merge, which follows whatever happened here,
+  // reads where a segment's results are, those of the segments that were not reached too.
+  if (threadIdx.x == 0)
+    for (; pc.n > 0; pc.next(p.line)) pc.leave_for_merge(p.line);
 }
 
 // out[b, h, t, :] = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the partial results of a
@@ -832,6 +837,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.v_scale = static_cast<const uint8_t*>(a.cache.v_scale);
   p.words = a.words;
   p.rope = a.rope;
+  p.lost = a.lost;
   const bool paged = a.cache.block_table != nullptr;
   p.box_rows = paged && a.cache.page_size < KT ? a.cache.page_size : KT;
   const uintptr_t scales =

@@ -88,6 +88,7 @@ struct TParams {
   float* part_ml;
   uint32_t* status;
   int Hq, Hkv, T, rep, rblocks, part_rows, pair;
+  int lost;  // arrivals that the queries' barrier waits for and nothing makes (selftest)
   float scale_log2;
 };
 
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       mbar_init(&o_empty[x], pair ? 4 : 8);
     }
     mbar_init(teardown, 1);
-    mbar_init(q_full, 1);
+    mbar_init(q_full, 1 + p.lost);
     mbar_init(q_empty, 1);
     for (int s = 0; s < 8; ++s) {
       mbar_init(&kv_full[s], F8 ? 4 : 1);
@@ -1193,6 +1194,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.part_rows = a.plan.part_rows;
   const int rows = a.T * p.rep;
   p.pair = a.plan.block_rows == 256 ? 1 : 0;
+  p.lost = a.lost;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
 
   alignas(64) CUtensorMap tq, tk, tv;

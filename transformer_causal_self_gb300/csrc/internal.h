@@ -236,6 +236,7 @@ struct GroupArgs {
                          // launch_group_tc [pieces, d / 4, part_rows, 4]
   float* part_ml;        // [pieces, subs, part_rows, 2]
   uint32_t* status;
+  int lost;              // 0; 1: the kernel waits for an arrival that nothing makes (selftest)
 };
 inline GroupLine group_line(const GroupArgs& a) {
   return GroupLine{a.lens,     a.seg, a.B,         a.drafts, a.min_len, a.max_seq_len - a.drafts,
