@@ -1,5 +1,5 @@
 """Calls of the 8-bit cache and of token trees in their less usual circumstances: waits
-that run out."""
+that run out, memory that another stream still uses."""
 import pytest
 import torch
 
@@ -49,3 +49,33 @@ def test_a_wait_that_runs_out_is_reported(call):
     again = run()
     csattn.check_status()
     assert H.same_bits(again, want)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("which", ["out", "workspace"])
+def test_stream_argument_beside_memory_in_use(which, raw):
+    """A block that was freed while work queued on the current stream still reads it does not
+    become the output or workspace of a call on another stream."""
+    B, Hq, d, Tn, L = 2, 64, 128, 64, 500
+    c, q, k, v, p = T._case(B, Hq, 8, d, Tn, [L] * B, 600, 64, False, "random", seed=8)
+    cd = H.to_dev(c)
+    args = (cd, q.to(dev()), k.to(dev()), v.to(dev()), H.i32([L] * B), H.i32(p))
+    want = T._step(*args, rope_base=10000.0)
+    need = csattn.tree_workspace_size(B, Hq, 8, Tn, cd["table"].shape[1] * 64, d)
+    given = (dict(workspace=torch.empty(need, dtype=torch.uint8, device=dev())) if which == "out"
+             else dict(out=torch.empty_like(want)))
+    size = want.numel() * 2 if which == "out" else need
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x = torch.full((size,), 7, dtype=torch.uint8, device=dev())
+    y = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # (about 50 ms)
+    y.copy_(x)
+    del x
+    got = T._step(*args, rope_base=10000.0, stream=s.cuda_stream if raw else s, **given)
+    torch.cuda.synchronize()
+    csattn.check_status()
+    assert H.same_bits(got, want)
+    assert bool((y == 7).all())

@@ -632,7 +632,7 @@ def cache_append_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.
 # ------------------------------------------------- 8-bit cache and token trees
 # These calls check shapes, types and devices of every tensor, run on the tensors' device
 # (whichever is current) and, when they allocate an output or a workspace for a `stream` of the
-# caller's, tie it to that stream.  (Written with few Python calls: a step over a short cache
+# caller's, take it from that stream's memory.  (Written with few Python calls: a step over a short cache
 # takes the GPU less time than this file.)
 
 _BF16, _I32, _F32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
@@ -671,20 +671,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _used_on(t: torch.Tensor, stream) -> torch.Tensor:
-    """An output or workspace of a call on `stream` (None: the current one)."""
-    if stream is not None:  # not handed out again before that stream's work is done
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                        torch.cuda.ExternalStream(_stream_handle(stream), device=t.device))
+def _empty(shape, dtype, dev: int, stream, returned: bool = True) -> torch.Tensor:
+    """An output (`returned`) or workspace of a call on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    # Memory of that stream, which nothing that is queued on the current one still uses; and an
+    # output, which the caller will use there, is not handed out again before that is done.
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=dev)
+    caller = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if returned:
+        t.record_stream(caller)
     return t
-
-
-def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
-    return _used_on(torch.empty(shape, dtype=dtype, device=dev), stream)
-
-
-def _like(t: torch.Tensor, stream) -> torch.Tensor:
-    return _used_on(torch.empty_like(t), stream)
 
 
 # Workspaces of calls that bring none are kept, one per thread and stream: calls of one thread on
@@ -709,7 +709,7 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: int, stream):
             held = kept[key] = given, given.data_ptr(), need
         return held
     else:
-        given = _empty((max(need, 16),), torch.uint8, dev, stream)
+        given = _empty((max(need, 16),), torch.uint8, dev, stream, returned=False)
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
@@ -865,7 +865,7 @@ def _decode_fp8(fn, q, k, v, k_scale, v_scale, block_table, seq_lens, out, rope_
     if cshape[3] != d:
         raise ValueError("q and the cache differ in head size")
     if out is None:
-        out = _like(q, stream)
+        out = _empty(shape, torch.bfloat16, dev, stream)
     if max_seq_len is None:
         max_seq_len = rows
     need = 0 if workspace is not None else decode_fp8_workspace_size(
@@ -923,7 +923,7 @@ def _tree_step(fn, q_new, k_new, v_new, k, v, k_scale, v_scale, block_table, cac
         raise ValueError("q_new and the cache differ in head size")
     kshape = (B, Hkv, Tn, d)
     if out is None:
-        out = _like(q_new, stream)
+        out = _empty(qshape, torch.bfloat16, dev, stream)
     if max_seq_len is None:
         max_seq_len = rows
     need = 0 if workspace is not None else tree_workspace_size(
