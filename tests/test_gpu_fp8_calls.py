@@ -1,5 +1,6 @@
 """Calls of the 8-bit cache and of token trees in their less usual circumstances: waits
-that run out, memory that another stream still uses."""
+that run out, memory that another stream still uses, pages
+out of range."""
 import pytest
 import torch
 
@@ -79,3 +80,32 @@ def test_stream_argument_beside_memory_in_use(which, raw):
     csattn.check_status()
     assert H.same_bits(got, want)
     assert bool((y == 7).all())
+
+
+def _refused():
+    with pytest.raises(csattn.CsattnError) as e:
+        csattn.check_status()
+    assert e.value.status == -6
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("Tn,Hq", [(5, 2), (20, 4)])
+def test_draft_rows_on_a_page_outside_the_pool_read_as_zeros(Tn, Hq, e4m3):
+    """Their values do not reach the outputs, infinities and NaN among them neither."""
+    L, page, d = 16, 16, 64
+    c, q, k, v, _ = T._case(1, Hq, 1, d, Tn, [L], 48, page, e4m3, "flat", seed=5)
+    k[:] = 0  # (what is read as zero as well: the outputs with and without the page compare)
+    v[0, 0, 1, 3], v[0, 0, 2, 4] = float("inf"), float("nan")
+    cd = H.to_dev(c)
+    cd["table"][0, 1] = -1
+    out = T._step(cd, q.to(dev()), k.to(dev()), v.to(dev()), H.i32([L]), H.i32([[-1] * Tn]))
+    _refused()
+    zero = H.to_dev(c)
+    v0 = v.clone()
+    v0[:, :, :16] = 0
+    if Tn > 16:
+        v0[:, :, 16:] = v[:, :, 16:]
+    want = T._step(zero, q.to(dev()), k.to(dev()), v0.to(dev()), H.i32([L]), H.i32([[-1] * Tn]))
+    csattn.check_status()
+    assert torch.isfinite(out).all()
+    assert (out.float() - want.float()).abs().max() <= 2.0 ** -6

@@ -182,8 +182,10 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
         *reinterpret_cast<uint4*>(dst + e1) = hi;
         return;
       }
-      if (is_v && c == 0) vflag[(static_cast<size_t>(b) * Hkv + g) * Tn + t] = bad ? 1 : 0;
-      if (row0 < 0) {  // a page outside the pool
+      // (a row on a page outside the pool reads as zeros)
+      if (is_v && c == 0)
+        vflag[(static_cast<size_t>(b) * Hkv + g) * Tn + t] = bad && row0 >= 0 ? 1 : 0;
+      if (row0 < 0) {
         if (c == 0) atomicOr(status, kStatusDeviceArg);
         return;
       }
