@@ -1,6 +1,6 @@
 """Calls of the 8-bit cache and of token trees in their less usual circumstances: waits
 that run out, memory that another stream still uses, pages
-out of range."""
+and lengths out of range."""
 import pytest
 import torch
 
@@ -109,3 +109,21 @@ def test_draft_rows_on_a_page_outside_the_pool_read_as_zeros(Tn, Hq, e4m3):
     csattn.check_status()
     assert torch.isfinite(out).all()
     assert (out.float() - want.float()).abs().max() <= 2.0 ** -6
+
+
+def test_every_length_out_of_range_is_reported():
+    d, B = 64, 3
+    c, q, _, _, _ = T._case(B, 2, 1, d, 1, [10] * B, 32, 0, True, T.CHAIN, seed=6)
+    cd = H.to_dev(c)
+    for bad in (0, -1, -2, 33, 2 ** 31 - 1, -2 ** 31, -2 ** 31 + 1):
+        out = csattn.attn_decode_fp8(q.to(dev()), cd["k"], cd["v"], cd["ks"], cd["vs"],
+                                     H.i32([10, bad, 10]))
+        _refused()
+        assert torch.all(out[1] == 0) and torch.isfinite(out).all() and torch.any(out[2] != 0)
+        c2, q2, k2, v2, _ = T._case(B, 2, 1, d, 3, [10] * B, 32, 0, True, T.CHAIN, seed=6)
+        if bad in (0,):
+            continue
+        out = T._step(H.to_dev(c2), q2.to(dev()), k2.to(dev()), v2.to(dev()),
+                      H.i32([10, bad, 10]), H.i32([[-1, 0, 1]] * B))
+        _refused()
+        assert torch.all(out[1] == 0)

@@ -34,8 +34,6 @@
 // 64 sequences of 512 to 8192 rows take 93.5 us for 576 MB (their ends add pieces: a piece's
 // queries and scale bytes are taken off the compute warps, which cost 114 us), and one of 1000
 // rows 8.6 us, the latencies of two launches, the lengths, a tile and the merge.
-#include <climits>
-
 #include "fp8.cuh"
 #include "group_work.cuh"
 #include "internal.h"
@@ -192,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  // (launch_tree_prep has reported what it marks with -1)
-  GroupPiece pc = group_start(p.line, p.status, p.line.drafts > 0 ? -1 : INT_MIN);
+  // (a tree's lengths have been checked by launch_tree_prep)
+  GroupPiece pc = group_start(p.line, p.status, p.line.drafts > 0);
   if (pc.n == 0) return;
   __syncthreads();
 

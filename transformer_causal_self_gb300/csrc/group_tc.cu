@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  GroupPiece pc = group_start(p.line, p.status, -1);  // (n = 0: every loop below ends at once)
+  GroupPiece pc = group_start(p.line, p.status, true);  // (n = 0: every loop below ends at once)
   const int step = pair ? 1 : 2;  // between a stream's tiles
 
   if (warp >= 8 && warp < 12) {

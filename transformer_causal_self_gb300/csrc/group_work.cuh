@@ -94,9 +94,9 @@ struct GroupPiece {
 };
 
 // The CTA's first piece (n = 0: none); every warp calls it by itself.  The first warp of the
-// first CTA raises kStatusDeviceArg for a length that is not valid, unless it is `reported`.
+// first CTA raises kStatusDeviceArg for a length that is not valid, unless that is `reported`.
 __device__ __forceinline__ GroupPiece group_start(const GroupLine& g, uint32_t* status,
-                                                  int reported) {
+                                                  bool reported) {
   const int lane = threadIdx.x & 31;
   const bool tell = blockIdx.x == 0 && threadIdx.x < 32;
   unsigned sum = 0, first = 0;  // first: the tiles of sequence `lane`
@@ -105,7 +105,7 @@ __device__ __forceinline__ GroupPiece group_start(const GroupLine& g, uint32_t* 
     sum += t;
     if (b == lane) first = t;
     if (tell && t == 0) {
-      if ((L < g.min_len || L > g.max_len) && L != reported) atomicOr(status, kStatusDeviceArg);
+      if ((L < g.min_len || L > g.max_len) && !reported) atomicOr(status, kStatusDeviceArg);
       for (int h = 0; h < g.heads; ++h) g.seg[b * g.heads + h] = make_int2(0, 0);
     }
   }
