@@ -1,6 +1,6 @@
 """Calls of the 8-bit cache and of token trees in their less usual circumstances: waits
 that run out, memory that another stream still uses, pages
-and lengths out of range."""
+and lengths out of range, streams of other libraries."""
 import pytest
 import torch
 
@@ -127,3 +127,32 @@ def test_every_length_out_of_range_is_reported():
                       H.i32([10, bad, 10]), H.i32([[-1, 0, 1]] * B))
         _refused()
         assert torch.all(out[1] == 0)
+
+
+def test_workspaces_are_kept_for_torch_streams_and_can_be_let_go():
+    c, q, _, _, _ = T._case(1, 4, 1, 64, 1, [40], 64, 0, True, T.CHAIN, seed=3)
+    cd, qd, lens = H.to_dev(c), q.to(dev()), H.i32([40])
+
+    def run():
+        return csattn.attn_decode_fp8(qd, cd["k"], cd["v"], cd["ks"], cd["vs"], lens)
+
+    csattn.release_workspaces()
+    want = run()
+    assert len(csattn._kept.__dict__) == 1
+    mine = torch.cuda.Stream()
+    with torch.cuda.stream(mine):
+        mine.wait_stream(torch.cuda.default_stream())
+        assert H.same_bits(run(), want)
+    assert len(csattn._kept.__dict__) == 2
+    # a stream that torch does not own: no workspace is kept under its handle
+    other = torch.cuda.ExternalStream(torch.cuda.Stream().cuda_stream)
+    with torch.cuda.stream(other):
+        other.wait_stream(torch.cuda.default_stream())
+        assert H.same_bits(run(), want)
+    assert len(csattn._kept.__dict__) == 2
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    csattn.release_workspaces()
+    assert not csattn._kept.__dict__ and torch.cuda.memory_allocated() < held
+    assert H.same_bits(run(), want)
+    csattn.check_status()

@@ -27,6 +27,7 @@ __all__ = [
     "cache_append_fp8", "cache_append_fp8_paged", "cache_read_fp8", "cache_read_fp8_paged",
     "attn_decode_fp8", "attn_decode_fp8_paged", "attn_tree_step", "attn_tree_step_paged",
     "tree_commit", "tree_commit_paged", "decode_fp8_workspace_size", "tree_workspace_size",
+    "release_workspaces",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -669,6 +670,8 @@ def _device_of(name: str, t: torch.Tensor, ndim: int) -> int:
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_stream_id = getattr(torch._C, "_cuda_getCurrentStream", None) or (
+    lambda dev: (torch.cuda.current_stream(dev).stream_id,))
 
 
 def _empty(shape, dtype, dev: int, stream, returned: bool = True) -> torch.Tensor:
@@ -689,7 +692,8 @@ def _empty(shape, dtype, dev: int, stream, returned: bool = True) -> torch.Tenso
 
 # Workspaces of calls that bring none are kept, one per thread and stream: calls of one thread on
 # one stream follow one another on the GPU, and two threads, two streams or two captured graphs
-# never share one.  Larger ones, and those of a capture or a `stream` argument, are allocated.
+# never share one.  Larger ones, and those of a capture, a `stream` argument or a stream that is not
+# torch's own (whose handle may become another stream's while its work is in flight), are allocated.
 _KEPT_BYTES = 64 << 20
 _kept = threading.local()
 
@@ -700,9 +704,11 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: int, stream):
         if given.get_device() != dev or not given.is_contiguous():
             raise ValueError(f"workspace: must be contiguous on cuda:{dev}")
     elif (stream is None and 0 < need <= _KEPT_BYTES and _current_device() == dev
-          and not torch.cuda.is_current_stream_capturing()):
+          and not torch.cuda.is_current_stream_capturing()
+          and ((raw := _raw_stream(dev)) == 0 or _stream_id(dev)[0] != raw)):
+        # (an external stream's id is its handle)
         kept = _kept.__dict__
-        key = (dev, _raw_stream(dev))
+        key = (dev, raw)
         held = kept.get(key)
         if held is None or held[2] < need:
             given = torch.empty((need,), dtype=torch.uint8, device=dev)
@@ -711,6 +717,12 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: int, stream):
     else:
         given = _empty((max(need, 16),), torch.uint8, dev, stream, returned=False)
     return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def release_workspaces() -> None:
+    """Lets go of the workspaces that calls of the 8-bit decode and of tree steps have kept for this
+    thread (up to 64 MB for each stream that it made such calls on; a thread's end does, too)."""
+    _kept.__dict__.clear()
 
 
 def _run(dev: int, fn, *args) -> None:
