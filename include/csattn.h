@@ -557,9 +557,10 @@ int csattn_cache_append_fp8_paged(const void* k_new, const void* v_new, void* k_
  * [B, Hkv, Lout, d], in the form csattn_attn_fwd_ext (k given rotated) and
  * csattn_attn_prefill_paged (each sequence one page) read.  Rows at or past seq_lens[b] are
  * left as they were.  Requirements: dtype CSATTN_BF16 (of the outputs), 1 <= Lout < 2^24,
- * B * Hkv * Lout < 2^33; outputs 16-byte aligned.  A seq_lens[b] outside [0, min(Lmax, Lout)]
- * leaves the sequence's outputs as they were and raises CSATTN_ERR_DEVICE_ARG in the status
- * word; a page index outside the pool raises it and its rows read as zeros.
+ * B * Hkv < 2^30, B * Hkv * Lout < 2^33; outputs 16-byte aligned.  A seq_lens[b] outside
+ * [0, min(Lmax, Lout)] leaves the sequence's outputs as they were and raises
+ * CSATTN_ERR_DEVICE_ARG in the status word; a page index outside the pool raises it and its rows
+ * read as zeros.
  */
 int csattn_cache_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
                           const void* v_scale, const int32_t* seq_lens, void* k_out, void* v_out,

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads, 7) append_fp8_kernel(
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int Hkv = rows.Hkv;
   const int groups = (Hkv + span - 1) / span;
-  // (32-bit indices: the launcher checks that the items are < 2^31)
+  // (32-bit indices: B * Hkv * Tn * d < 2^33, so there are no more than 2^29 items)
   int i = (static_cast<int>(blockIdx.x) - (is_k ? 0 : k_blocks)) * kThreads + tid;
   bool live = i < B * groups * Tn * G;
   if (!live) i = 0;
@@ -200,7 +200,6 @@ cudaError_t launch_cache_append_fp8(const void* k_new, const void* v_new, const 
   const long long tokens = static_cast<long long>(B) * Tn * (d / 16);
   const int span = 2 * tokens >= 152LL * 6 * kThreads ? Hkv : std::min(Hkv, kHeads);
   const long long items = tokens * ((Hkv + span - 1) / span);
-  if (items + 2 * kThreads >= 0x3fffffffLL) return cudaErrorInvalidValue;
   const int blocks = static_cast<int>((items + kThreads - 1) / kThreads);
   auto* kernel = d == 128 ? append_fp8_kernel<128> : append_fp8_kernel<64>;
   return launch_behind(kernel, dim3(2 * blocks), kThreads, stream,
@@ -216,7 +215,7 @@ cudaError_t launch_cache_read_fp8(const KvCache& cache, const int32_t* seq_lens,
                                   cudaStream_t stream) {
   const long long pieces = static_cast<long long>(std::min(Lout, cache.Lmax)) * (d / 16);
   const long long blocks = (pieces + kThreads * kRows - 1) / (kThreads * kRows);
-  if (2 * blocks * B * Hkv > 0x7fffffffLL || pieces > 0x3fffffffLL) return cudaErrorInvalidValue;
+  // (a grid below 2^31: B * Hkv < 2^30, and B * Hkv * Lout < 2^33 where there are more blocks)
   auto* kernel = d == 128 ? read_fp8_kernel<128> : read_fp8_kernel<64>;
   return launch_behind(kernel, dim3(static_cast<unsigned>(2 * blocks * B * Hkv)), kThreads, stream,
                        static_cast<const uint8_t*>(cache.k), static_cast<const uint8_t*>(cache.v),

@@ -239,6 +239,8 @@ int read_fp8(const char* fn, const KvCache& c, const int32_t* seq_lens, void* k_
   if (Lout < 1) return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Lout=%d must be >= 1", fn, Lout);
   if (Lout >= (1 << 24) || static_cast<long long>(B) * Hkv * Lout >= (1LL << 33))
     return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Lout=%d too large", fn, Lout);
+  if (static_cast<long long>(B) * Hkv >= (1LL << 30))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: B=%d * Hkv=%d too large", fn, B, Hkv);
   uint32_t* status = nullptr;
   int sms = 0;
   if ((rc = api_device_info(&status, &sms)) != CSATTN_OK) return rc;
