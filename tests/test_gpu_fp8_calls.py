@@ -1,13 +1,14 @@
 """Calls of the 8-bit cache and of token trees in their less usual circumstances: waits
 that run out, memory that another stream still uses, pages
-and lengths out of range, streams of other libraries."""
+and lengths out of range, streams of other libraries, odd
+numbers of rows."""
 import pytest
 import torch
 
 import transformer_causal_self_gb300 as csattn
 from tests import fp8_helpers as H
 from tests import test_gpu_tree as T
-from tests.gpu_helpers import dev
+from tests.gpu_helpers import assert_bf16_close, dev, to_np
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +157,20 @@ def test_workspaces_are_kept_for_torch_streams_and_can_be_let_go():
     assert not csattn._kept.__dict__ and torch.cuda.memory_allocated() < held
     assert H.same_bits(run(), want)
     csattn.check_status()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,heads", [(1, 1), (1, 3), (3, 5), (1, 4097)])
+def test_odd_numbers_of_rows(B, heads, d):
+    """The last block of the merge has fewer rows than it has room for (and a barrier, but for the
+    last case)."""
+    L = 20
+    c, q, _, _, _ = T._case(B, heads, heads, d, 1, [L] * B, 24, 0, True, T.CHAIN, seed=heads)
+    cd = H.to_dev(c)
+    out = csattn.attn_decode_fp8(q.to(dev()), cd["k"], cd["v"], cd["ks"], cd["vs"], H.i32([L] * B))
+    csattn.check_status()
+    kk, vv = (torch.stack([torch.from_numpy(H.rows(c, b, L)[i]) for b in range(B)])
+              for i in range(2))
+    s = torch.einsum("bhqd,bhkd->bhqk", q.double(), kk) / d ** 0.5
+    ref = torch.softmax(s, -1) @ vv
+    assert_bf16_close(to_np(out), ref.numpy(), "decode")

@@ -716,9 +716,12 @@ __global__ void __launch_bounds__(32 * (W > 4 ? W : 4)) group_merge_kernel(
   constexpr int U = W > 1 ? 8 : 4;  // partial results whose loads are in flight together
   __shared__ float s_part[W > 4 ? W : (W > 1 ? 4 : 1)][V * 32 + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = static_cast<int>(blockIdx.x) * (W < 4 ? 4 / W : 1) + warp / W;
+  const int at_row = static_cast<int>(blockIdx.x) * (W < 4 ? 4 / W : 1) + warp / W;
+  // (a warp past the last row works on that row, too, where there is a barrier to come)
+  const bool live = at_row < rows;
+  const int row = live ? at_row : rows - 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= rows) return;
+  if (W == 1 && !live) return;
   const int rep = Hq / Hkv;
   const int t = row % T, bh = row / T, b = bh / Hq, h = bh - b * Hq, g = h / rep;
   const uint32_t* mine = anc + (static_cast<size_t>(b) * T + t) * words;
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(32 * (W > 4 ? W : 4)) group_merge_kernel(
       s_part[warp][V * 32 + 1] = m;
     }
     __syncthreads();
-    if (warp % W != 0) return;
+    if (!live || warp % W != 0) return;
     float mx = m;
 #pragma unroll
     for (int w = 1; w < W; ++w) mx = fmaxf(mx, s_part[warp + w][V * 32 + 1]);
