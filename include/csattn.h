@@ -524,7 +524,8 @@ int csattn_cache_append_paged(const void* k_new, const void* v_new, void* k_page
  * rounded once (to nearest even) from fp32; infinities and NaN are stored as NaN, and what
  * would round to 2^128 as 1.875 * 2^127.  The value x8 * 2^(code - 127) is a bf16 number, so
  * reading a row back is exact.  The calls below read codes in [3, 247] (another code reads as
- * some power of two, infinity or 0).
+ * some power of two, infinity or 0).  A rope_base in (0, 1) is accepted by them as long as the
+ * largest angle, (Lmax or max_seq_len) * rope_base^(-(d-2)/d), is at most 49152.
  */
 
 /*

@@ -66,8 +66,9 @@ int check_dtype(const char* fn, int dtype) {
                   "%s: only bf16 is implemented (dtype %d)", fn, dtype);
 }
 
-// positions: how many the call may rotate at
-int check_rope(const char* fn, float rope_base, int rope_layout, int positions) {
+// positions: how many the call may rotate at.  (With a base below 1 the last frequency is the
+// largest, and the angles' reduction bounds its angle like that of theta_0 = 1.)
+int check_rope(const char* fn, float rope_base, int rope_layout, int positions, int d) {
   if (rope_layout != CSATTN_ROPE_SPLIT_HALF && rope_layout != CSATTN_ROPE_ADJACENT)
     return api_fail(CSATTN_ERR_INVALID_ARG, "%s: unknown rope_layout %d", fn, rope_layout);
   if (!std::isfinite(rope_base))
@@ -75,6 +76,10 @@ int check_rope(const char* fn, float rope_base, int rope_layout, int positions) 
   if (rope_base > 0.f && positions > kMaxRopePositions)
     return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: RoPE supports positions < %d, got %d", fn,
                     kMaxRopePositions, positions);
+  if (rope_base > 0.f && rope_base < 1.f &&
+      positions * std::pow(static_cast<double>(rope_base), -(d - 2.0) / d) > kMaxRopePositions)
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: RoPE angles past %d (rope_base=%g, %d positions)",
+                    fn, kMaxRopePositions, rope_base, positions);
   return CSATTN_OK;
 }
 
@@ -216,7 +221,7 @@ int append_fp8(const char* fn, const void* k_new, const void* v_new, const KvCac
     return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Tn=%d not in [1, cache rows %d]", fn, Tn, c.Lmax);
   if (static_cast<long long>(B) * Hkv * Tn * d >= (1LL << 33))
     return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Tn=%d too large", fn, Tn);
-  if ((rc = check_rope(fn, rope_base, rope_layout, c.Lmax)) != CSATTN_OK) return rc;
+  if ((rc = check_rope(fn, rope_base, rope_layout, c.Lmax, d)) != CSATTN_OK) return rc;
   RopeTable th{};
   const int rope = rope_of(rope_base, rope_layout, d, &th);
   uint32_t* status = nullptr;
@@ -262,7 +267,7 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
   if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
   if ((rc = check_heads(fn, B, Hq, Hkv, 1, scale, max_seq_len, c.Lmax, num_splits)) != CSATTN_OK)
     return rc;
-  if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
+  if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len, d)) != CSATTN_OK) return rc;
   GroupArgs a{};
   a.plan = plan_for(B, Hkv, Hq / Hkv, d, false, true, max_seq_len, num_splits);
   if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
@@ -338,7 +343,7 @@ int tree_step(const char* fn, const void* q_new, const void* k_new, const void* 
     return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Tn=%d exceeds %d drafts", fn, Tn, kMaxTree);
   if ((rc = check_heads(fn, B, Hq, Hkv, Tn, scale, max_seq_len, c.Lmax, num_splits)) != CSATTN_OK)
     return rc;
-  if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len)) != CSATTN_OK) return rc;
+  if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len, d)) != CSATTN_OK) return rc;
   GroupArgs a{};
   a.plan = tree_plan(B, Hq, Hkv, Tn, d, cache_dtype == CSATTN_E4M3, max_seq_len, num_splits);
   if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
