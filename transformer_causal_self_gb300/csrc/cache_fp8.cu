@@ -196,9 +196,9 @@ cudaError_t launch_cache_append_fp8(const void* k_new, const void* v_new, const 
                                     int rope, const RopeTable& theta, uint32_t* status,
                                     cudaStream_t stream) {
   // All heads of a token in one thread while that still fills the GPU (one set of angles serves
-  // them all): 152 SMs * 6 blocks; otherwise kHeads of them.
+  // them all): six blocks per SM; otherwise kHeads of them.
   const long long tokens = static_cast<long long>(B) * Tn * (d / 16);
-  const int span = 2 * tokens >= 152LL * 6 * kThreads ? Hkv : std::min(Hkv, kHeads);
+  const int span = 2 * tokens >= 6LL * kSms * kThreads ? Hkv : std::min(Hkv, kHeads);
   const long long items = tokens * ((Hkv + span - 1) / span);
   const int blocks = static_cast<int>((items + kThreads - 1) / kThreads);
   auto* kernel = d == 128 ? append_fp8_kernel<128> : append_fp8_kernel<64>;

@@ -119,7 +119,6 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
 // The kernel for `rows` query rows per KV head, and how its work is shared out: a wave of CTAs,
 // or, with an explicit number of splits, as many CTAs as parts of that many equal ones of the
 // longest sequence can fill.
-constexpr int kSms = 152;
 // Trees with more query rows per KV head than this go to launch_group_tc (128 channels, 8
 // sequences of 8000 rows; here / there: 16 rows bf16 57 / 58 us, e4m3 45 / 58; 20 rows 91 / 58
 // and 69 / 58, the cache being read once per 16 rows here).

@@ -322,6 +322,9 @@ int api_device_info(uint32_t** status, int* num_sms);
 bool api_valid_page_size(int page_size);
 void api_rope_table(RopeTable* t, int d, double base);
 constexpr int kMaxRopePositions = 49152;  // largest position whose angle reduction is exact
+// SMs of a GB300, which waves of CTAs are cut for (a constant: workspace sizes depend on it, and are
+// asked for without a device)
+constexpr int kSms = 152;
 
 // Raises a kernel's dynamic shared-memory limit once per device (the attribute
 // lasts for the process), so repeated launches skip the driver call.

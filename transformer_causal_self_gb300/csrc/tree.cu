@@ -315,12 +315,12 @@ cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
   const bool f8 = a.cache.k_scale != nullptr;
   // a draft's rows shared by several CTAs while these are all resident at once
   const int parts = ((a.Hq + 2 * a.Hkv) * (a.d / 16) + kThreads - 1) / kThreads;
-  const bool few = static_cast<long long>(a.Tn) * a.B * parts <= 2 * 152 && parts <= 65535;
+  const bool few = static_cast<long long>(a.Tn) * a.B * parts <= 2 * kSms && parts <= 65535;
   // several drafts in a CTA where there are more than are resident at once: the masks are worked
   // out once for them (64 sequences of 500 rows, 64 drafts: 127 and 138 us for the whole step over
   // bf16 and e4m3, 135 and 151 with one draft each; 512 drafts: 2 us less with one each)
   const int drafts = static_cast<int>(
-      std::min<long long>(kDrafts, (static_cast<long long>(a.Tn) * a.B + 607) / 608));
+      std::min<long long>(kDrafts, (static_cast<long long>(a.Tn) * a.B + 4 * kSms - 1) / (4 * kSms)));
   auto* kernel = a.d == 128
                      ? (f8 ? tree_prep_kernel<128, true, 1> : tree_prep_kernel<128, false, 1>)
                      : (f8 ? tree_prep_kernel<64, true, 1> : tree_prep_kernel<64, false, 1>);
@@ -348,7 +348,7 @@ cudaError_t launch_tree_commit(const KvCache& cache, const int32_t* cache_lens,
   const int pieces = d * (cache.k_scale != nullptr ? 1 : 2) / 16;
   // heads per CTA: few while that leaves SMs idle, at most 16 (their scale bytes fill a CTA)
   const int heads = std::max(1, std::min({16, Hkv, static_cast<int>(
-                                                       static_cast<long long>(Hkv) * B / 152)}));
+                                                       static_cast<long long>(Hkv) * B / kSms)}));
   return launch_behind(tree_commit_kernel, dim3((Hkv + heads - 1) / heads, B), kThreads, stream,
                        static_cast<uint4*>(cache.k), static_cast<uint4*>(cache.v),
                        static_cast<uint8_t*>(cache.k_scale), static_cast<uint8_t*>(cache.v_scale),
