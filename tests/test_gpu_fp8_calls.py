@@ -1,11 +1,12 @@
-"""Calls of the 8-bit cache and of token trees in their less usual circumstances: waits
-that run out, memory that another stream still uses, pages
-and lengths out of range, streams of other libraries, odd
-numbers of rows."""
+"""Calls of the 8-bit cache and of token trees in their less usual circumstances: waits that
+run out, memory that another stream still uses, pages and lengths out of range, streams of other
+libraries, odd numbers of rows; and the bound of the log-sum-exp over a bf16 cache."""
+import numpy as np
 import pytest
 import torch
 
 import transformer_causal_self_gb300 as csattn
+from oracle import attn as OA
 from tests import fp8_helpers as H
 from tests import test_gpu_tree as T
 from tests.gpu_helpers import assert_bf16_close, dev, to_np
@@ -174,3 +175,45 @@ def test_odd_numbers_of_rows(B, heads, d):
     s = torch.einsum("bhqd,bhkd->bhqk", q.double(), kk) / d ** 0.5
     ref = torch.softmax(s, -1) @ vv
     assert_bf16_close(to_np(out), ref.numpy(), "decode")
+
+
+def _rotation_ties(x, pos, base, layout):
+    """Rotated queries x [Hq, T, d] in float64, and for each channel the bf16 step that a
+    rotation in fp32 may fall off by: its angles' sine and cosine are good to 2^-20, so that a value
+    within 2^-19 of its pair's length of the middle of two bf16 numbers may go to either."""
+    r = OA.rope_rotate(x, pos, base, layout)
+    half = x.shape[-1] // 2
+    if layout == "split_half":
+        pair = np.tile(np.hypot(x[..., :half], x[..., half:]), 2)
+    else:
+        pair = np.repeat(np.hypot(x[..., 0::2], x[..., 1::2]), 2, axis=-1)
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(r), 2.0 ** -126))) - 7)
+    off = np.abs(np.abs(r) / step - np.floor(np.abs(r) / step) - 0.5) * step
+    return r, np.where(off <= 2.0 ** -19 * pair, step, 0.0)
+
+
+@pytest.mark.parametrize("factor", [1.0, 4.0])
+@pytest.mark.parametrize("Hq,Tn,d", [(4, 4, 128), (8, 40, 128), (4, 32, 64)])
+def test_lse_over_a_bf16_cache(Hq, Tn, d, factor):
+    """lse against float64 over many seeds: off by at most what the channels that fall on the other
+    side of a bf16 tie move a score by, and the fp32 sums (2^-17 of sum |q_i k_i| * scale, and 2^-18
+    for exponentials and logarithm)."""
+    L = 300
+    for seed in range(12):
+        c, q, k, v, p = T._case(1, Hq, 1, d, Tn, [L], L + Tn, 0, False, "random", seed=seed)
+        q = (q.float() * factor).to(torch.bfloat16)
+        cd = H.to_dev(c)
+        lse = torch.zeros(1, Hq, Tn, device=dev())
+        T._step(cd, q.to(dev()), k.to(dev()), v.to(dev()), H.i32([L]), H.i32(p), lse=lse,
+                rope_base=10000.0)
+        csattn.check_status()
+        anc = OA.tree_ancestors(p[0])
+        pos = L + np.maximum(anc.sum(1) - 1, 0)
+        kk, vv = H.rows(H.to_cpu(cd), 0, L + Tn)
+        r, tie = _rotation_ties(q[0].double().numpy(), pos, 10000.0, "split_half")
+        qr = OA.round_to_bf16(r)
+        _, ref = OA.tree_attention(qr, kk, vv, L, anc)
+        a = np.abs(kk[0]).T / np.sqrt(d)
+        bound = (tie @ a).max(-1) + 2.0 ** -17 * (np.abs(qr) @ a).max(-1) + 2.0 ** -18
+        off = np.abs(lse.double().cpu().numpy()[0] - ref) / bound
+        assert off.max() <= 1.0, (seed, off.max())

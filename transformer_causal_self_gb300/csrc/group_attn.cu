@@ -25,7 +25,8 @@
 // a large weight (a first token that takes up attention) counts in full.  n is relative to m, so
 // that no exponent is lost beside a large score.  w is rounded to f16 (11 bits) scaled by 2^7,
 // so what is below 2^-32 of the largest vanishes; the bf16 cache's P is rounded to bf16 (8
-// bits), as in the other bf16 kernels; sums are fp32 throughout.
+// bits: the values on the other side of the product are bf16, and f16 would not hold them), as in
+// the other bf16 kernels; sums are fp32 throughout.
 // A maximum is raised only when a score exceeds it by 2^8, and only then do the lanes exchange
 // theirs: the usual tile costs one vote.
 //

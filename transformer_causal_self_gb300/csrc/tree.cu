@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads) tree_prep_kernel(
         hi = scale_row(hi, code);
       }
       rope16(lo, hi, layout, cs, sn, y);
+      // (bf16: rounded to the cache's type, queries too: the products take both sides in one type)
       if (layout != 0) {
         lo = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                         pack_bf16x2(y[6], y[7]));
