@@ -177,6 +177,33 @@ def test_odd_numbers_of_rows(B, heads, d):
     assert_bf16_close(to_np(out), ref.numpy(), "decode")
 
 
+def test_stream_argument_in_a_capture():
+    """A stream that the capture has been forked to: its outputs and workspaces are the graph's."""
+    B, L = 2, 200
+    c, q, k, v, p = T._case(B, 8, 1, 64, 20, [L] * B, 300, 64, True, "random", seed=9)
+    cd, ce = H.to_dev(c), H.to_dev(c)
+    args = (q.to(dev()), k.to(dev()), v.to(dev()), H.i32([L] * B), H.i32(p))
+    want = T._step(ce, *args, rope_base=10000.0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        side.wait_stream(torch.cuda.current_stream())
+        out = T._step(cd, *args, rope_base=10000.0, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        two = T._step(cd, *args, rope_base=10000.0, stream=torch.cuda.current_stream())
+        both = out + two
+    for _ in range(3):
+        gr.replay()
+        # (calls in between, which take memory from the same streams)
+        T._step(ce, *args, rope_base=10000.0, stream=side)
+        T._step(ce, *args, rope_base=10000.0)
+    torch.cuda.synchronize()
+    csattn.check_status()
+    assert H.same_bits(out, want) and H.same_bits(two, want)
+    assert H.same_bits(both, want + want)
+
+
 def _rotation_ties(x, pos, base, layout):
     """Rotated queries x [Hq, T, d] in float64, and for each channel the bf16 step that a
     rotation in fp32 may fall off by: its angles' sine and cosine are good to 2^-20, so that a value
