@@ -122,6 +122,52 @@ def test_rows_of_another_scale_in_sight(Tn, Hq, base):
     _check_tree(q, k, v, pk, pv, [-1] * Tn, d)
 
 
+@pytest.mark.parametrize("v_shift", [0, -100, 100])
+@pytest.mark.parametrize("L", [0, 300])
+@pytest.mark.parametrize("Tn,Hq,d", [(4, 2, 64), (5, 8, 64), (40, 8, 128)])
+def test_a_key_that_decides_alone(Tn, Hq, d, L, v_shift):
+    """A draft's key of 1e30: scores of 1e30, beside which a scale's exponent is lost.  Its own
+    query takes its value, exactly, where the score is positive, and the others' where it is not;
+    without a prefix it has nothing else to see."""
+    q, k, v, pk, pv = _inputs(Hq, 1, L, Tn, d, 9)
+    v, pv = ((x.double() * 2.0 ** v_shift).to(torch.bfloat16) for x in (v, pv))
+    k[0, 0, 2] = torch.where(k[0, 0, 2] < 0, -1e30, 1e30)
+    others = [t for t in range(Tn) if t != 2]
+    out = _check_tree(q, k, v, pk, pv, [-1] * Tn, d, queries=others)
+    _, own = OA.quantise_rows(v[0, 0, 2].double().numpy(), OA.e4m3_exponents(v[0, 0, 2], False))
+    got = to_np(out)[0, :, 2]
+    score = (q[0, :, 2].double() @ k[0, 0, 2].double()).numpy()
+    for h in range(Hq):
+        if L == 0 or score[h] > 0:
+            assert np.array_equal(got[h], own), h
+        else:
+            # (as if the draft were not there)
+            kk, vv = pk[0].double().numpy(), pv[0].double().numpy()
+            z = kk @ q[0, h, 2].double().numpy() / np.sqrt(d)
+            w = np.exp(z - z.max())
+            ref = w / w.sum() @ vv
+            # (the prefix unquantised here: half a step of e4m3 in keys and values)
+            assert np.linalg.norm(got[h] - ref) <= 2.0 ** -2 * np.linalg.norm(ref), h
+
+
+@pytest.mark.parametrize("splits", [0, 1, 7])
+@pytest.mark.parametrize("Hq", [2, 12])
+def test_equal_large_scores_weigh_alike(Hq, splits):
+    """300 equal keys whose score is past 2^24: the mean of the values, in whatever pieces."""
+    d, L = 64, 300
+    _, _, _, _, pv = _inputs(1, 1, L, 1, d, 2)
+    c = H.empty_cache(1, 1, L, d, 0, True, seed=2)
+    H.set_rows(c, 0, 0, torch.full((1, L, d), 2.0 ** 40, dtype=torch.bfloat16), pv)
+    cd = H.to_dev(c)
+    q = torch.ones(1, Hq, 1, d, dtype=torch.bfloat16, device=dev())
+    out = csattn.attn_decode_fp8(q, cd["k"], cd["v"], cd["ks"], cd["vs"], H.i32([L]),
+                                 num_splits=splits)
+    csattn.check_status()
+    vv = H.rows(c, 0, L)[1][0]
+    bound = 2.0 ** -8 * np.abs(vv.mean(0)) + 2.0 ** -11 * np.abs(vv).mean(0)
+    _close(to_np(out)[0, :, 0], np.broadcast_to(vv.mean(0), (Hq, d)), bound, "mean")
+
+
 def _decode(q, k, v, **kw):
     """q [1, Hq, 1, d], k, v [Hkv, L, d]: checked decode over them."""
     Hkv, L, d = k.shape
@@ -148,6 +194,11 @@ SPANS = {"top": lambda x, n: torch.where(x < 0, -1.0, 1.0) * 2.0 ** 127 * 1.8,
                                                          x * 2.0 ** -118, x * 2.0 ** 100),
          "top and one": lambda x, n: torch.where(torch.arange(n)[:, None] % 128 == 5,
                                                  1.9 * 2.0 ** 127, x),
+         "both in every tile": lambda x, n: torch.where(torch.arange(n)[:, None] % 3 == 0,
+                                                        x * 2.0 ** -118, x * 2.0 ** -90),
+         "far apart, halves": lambda x, n: x * torch.exp2(
+             20.0 * (torch.arange(n)[:, None] % 2) + torch.where(
+                 torch.arange(n)[:, None] < n // 2, 90.0, -110.0)),
          "zeros and one large": lambda x, n: torch.where(torch.arange(n)[:, None] == 5,
                                                          x * 2.0 ** 60, 0.0)}
 

@@ -676,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F8, NT>::CTAS)
         // (a row that saw nothing holds zeros, or NaN if its scores were NaN)
         float m = m_used[j][h], l = l_part[j][h], f = 1.f;
         if (F8 && n_used[j][h] != -INFINITY) {
-          const int up = log2_above(l);
+          // (beside a maximum past 2^23 it would be lost)
+          const int up = fabsf(m) < 8388608.f ? log2_above(l) : 0;
           m += static_cast<float>(up);
           l *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
           f = ex2_approx(0.5f * (n_used[j][h] -

@@ -19,7 +19,7 @@
 // first half of its S and is read by the second product from there.
 //
 // An e4m3 tile becomes f16 with one scale for all its rows: row j is multiplied by 2^(7 - (E -
-// e_j)), E the largest exponent of the tile (at least -100 for values).  That is exact while
+// e_j)), E the largest exponent of the tile (at least -102 for values).  That is exact while
 // e_j is within 22 of E.  So the scales reach the softmax as two numbers per tile, and one
 // exponential serves denominator and numerator:
 //   w = 2^(x + E_v - R), O += w V16, l += 2^(-E_v) * sum w, R the running maximum of x + E_v.
@@ -52,7 +52,7 @@ constexpr float kRescaleThreshold = 8.0f;
 // e4m3: below R by kLowTile (2^(7 - 96 - 30) is still a normal number) the largest weight of a tile
 // is put at 2^-kLowWeight, which is 0 in f16
 constexpr float kLowTile = 96.0f, kLowWeight = 60.0f;
-constexpr int kMinValueCode = 27;  // E_v >= -100
+constexpr int kMinValueCode = 25;  // E_v >= -102 (the least code is within 22 of it)
 constexpr int kWideKeys = 22, kWideValues = 12;  // exponents further apart: a column each;
 constexpr float kOwnScales = 152.f;               // such a tile's E_v (2^-152 is 0)
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 12;
@@ -247,10 +247,11 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
                : "memory");
 }
 
-// A tile whose columns keep scales of their own (see the file's head): x_j + ev_j - kOwnScales takes
-// the place of every score of the thread's row.  Returns the largest x_j + ev_j and log2 of the sum
-// of 2^x_j.  Out of line: these tiles are rare, and inline the softmax loop no longer fits the
-// instruction cache as well (16 x 32 drafts over 512..8192 rows 76.8 us, like this 73.8).
+// A tile whose columns keep scales of their own (see the file's head): y_j = x_j + ev_j takes the
+// place of every score of the thread's row, less kOwnScales.  Returns the largest of them, and log2
+// of the sum of 2^x_j relative to it (y_j - top first: beside a large score ev_j is lost in y_j).
+// Out of line: these tiles are rare, and inline the softmax loop no longer fits the instruction
+// cache as well (16 x 32 drafts over 512..8192 rows 76.8 us, like this 73.8).
 __device__ __noinline__ float2 own_scales(const TParams& p, int b, int kvh, int row0, int k_end,
                                           uint32_t tS, float row_factor) {
   const int lane = threadIdx.x & 31, r = row0 + 4 * lane;
@@ -264,35 +265,38 @@ __device__ __noinline__ float2 own_scales(const TParams& p, int b, int kvh, int 
   if (!__any_sync(0xffffffffu, sk.far)) own_k = 0x01010101u * sk.E;
   own_v = __any_sync(0xffffffffu, sv.far) ? __vmaxu4(own_v, 0x01010101u * kMinValueCode)
                                           : 0x01010101u * sv.E;
-  float x0 = -INFINITY, sum = 0.f, top = -INFINITY;
+  float top = -INFINITY;
   __syncwarp();
   for (int i = 0; i < BN; i += 4) {
     const uint32_t ek = __shfl_sync(0xffffffffu, own_k, i >> 2);
     const uint32_t ev4 = __shfl_sync(0xffffffffu, own_v, i >> 2);
     uint32_t s4[4];
-    float xs[4];
     tmem_ld4_sync(tS + i, s4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float f = __uint_as_float(((ek >> (8 * e)) & 0xffu) << 23);
       // (neither 0 nor infinity: a hidden score is -inf, another may be 0)
       const float g = fminf(fmaxf(row_factor * f * 0.0078125f, 1.17549435e-38f), 3e38f);
-      xs[e] = __fmul_rn(__uint_as_float(s4[e]), g);
-      const float y =
-          xs[e] + (static_cast<float>((ev4 >> (8 * e)) & 0xffu) - (127.f + kOwnScales));
+      const float x = __fmul_rn(__uint_as_float(s4[e]), g);
+      const float y = x + (static_cast<float>((ev4 >> (8 * e)) & 0xffu) - (127.f + kOwnScales));
       top = fmaxf(top, y);
       s4[e] = __float_as_uint(y);
     }
     tmem_st4(tS + i, s4);
-    const float up = fmaxf(fmaxf(x0, fmaxf(xs[0], xs[1])), fmaxf(xs[2], xs[3]));
-    const float at0 = up == -INFINITY ? 0.f : up;
-    sum *= ex2_approx(x0 - at0);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum += ex2_approx(xs[e] - at0);
-    x0 = up;
   }
   tmem_st_wait();
-  return make_float2(top + kOwnScales, sum == 0.f ? -INFINITY : x0 + __log2f(sum));
+  const float at0 = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;  // times 2^18: -120 <= -ev_j <= 102
+  for (int i = 0; i < BN; i += 4) {
+    const uint32_t ev4 = __shfl_sync(0xffffffffu, own_v, i >> 2);
+    uint32_t s4[4];
+    tmem_ld4_sync(tS + i, s4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sum += ex2_approx((__uint_as_float(s4[e]) - at0) +
+                        (145.f - static_cast<float>((ev4 >> (8 * e)) & 0xffu)));
+  }
+  return make_float2(top, __log2f(sum) - 18.f);  // (0: -inf; NaN stays)
 }
 
 // 2^(7 - below) in f16 (0 where that is less than f16's least)
@@ -785,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         tc_fence_after();
         if (warp_live) {
           float c = row_factor, ev = 0.f;
-          volatile float own_l;  // (in memory: set and read for such tiles alone)
+          volatile float own_l, own_top;  // (in memory: set and read for such tiles alone)
           if constexpr (F8) {
             const float2 ts = s_tile[(tile0 + j) & 7];
             c *= ts.x;
@@ -842,7 +846,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           // (then c = 1, and the sum of the tile's weights comes by way of own_l)
           if (F8 && __builtin_expect(ev == kOwnScales, 0)) {
             const float2 t = own_scales(p, w.b, w.kvh, w.k_begin + j * BN, w.k_end, tS, row_factor);
-            top = t.x;
+            top = t.x + kOwnScales;
+            own_top = t.x;
             own_l = t.y;
             c = 1.f;
           }
@@ -916,8 +921,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const float g = low ? ex2_approx(0.5f * (Rt - R)) : 1.f;
             l += sum * 0.0078125f * ex2_approx(-ev) * g * g;
             if (__builtin_expect(ev == kOwnScales, 0)) {  // (2^-ev is 0)
-              const float h = ex2_approx(0.5f * (own_l - (R == -INFINITY ? 0.f : R)));
-              l += h * h;
+              // (by the largest weight as it was rounded, in two halves)
+              const float h =
+                  own_l == -INFINITY ? 0.f : ex2_approx(0.5f * (own_l + (own_top + off - 7.f)));
+              l += (h * g) * (h * g);
             }
           } else {
             l += sum;
