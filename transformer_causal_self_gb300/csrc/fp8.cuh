@@ -138,10 +138,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // zero the bytes of four e4m3 that are NaN
 __device__ __forceinline__ uint32_t finite_e4m3x4(uint32_t w) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (((w >> (8 * i)) & 0x7fu) == 0x7fu) w &= ~(0xffu << (8 * i));
-  return w;
+  const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // 0x7f + 1
+  return w & ~(nan | (nan - (nan >> 7)));
 }
 
 // Where the rows of a cache are: contiguous [B, Hkv, Lmax, ...] (block_table == nullptr)
