@@ -54,7 +54,7 @@ constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLowTile = 96.0f, kLowWeight = 60.0f;
 constexpr int kMinValueCode = 25;  // E_v >= -102 (the least code is within 22 of it)
 constexpr int kWideKeys = 22, kWideValues = 12;  // exponents further apart: a column each;
-constexpr float kOwnScales = 152.f;               // such a tile's E_v (2^-152 is 0)
+constexpr float kOwnScales = 1000.f;              // such a tile's E_v
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpConvert = 12;
 
 template <int D, bool F8>
@@ -241,19 +241,25 @@ __device__ __forceinline__ void tmem_ld4_sync(uint32_t taddr, uint32_t (&r)[4]) 
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, const uint32_t (&r)[2]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
 
-// A tile whose columns keep scales of their own (see the file's head): y_j = x_j + ev_j takes the
-// place of every score of the thread's row, less kOwnScales.  Returns the largest of them, and log2
-// of the sum of 2^x_j relative to it (y_j - top first: beside a large score ev_j is lost in y_j).
-// Out of line: these tiles are rare, and inline the softmax loop no longer fits the instruction
-// cache as well (16 x 32 drafts over 512..8192 rows 76.8 us, like this 73.8).
+// The softmax of a tile whose columns keep scales of their own (see the file's head), for the
+// thread's row: S in TMEM becomes the weights, R and l (and O, if there is one) are brought up to
+// date; returns R and l.  Out of line: these tiles are rare, and inline the softmax loop no longer
+// fits the instruction cache as well (16 x 32 drafts over 512..8192 rows 76.8 us, like this 73.8).
+template <int D>
 __device__ __noinline__ float2 own_scales(const TParams& p, int b, int kvh, int row0, int k_end,
-                                          uint32_t tS, float row_factor) {
+                                          uint32_t tS, uint32_t tO, bool has_o, float row_factor,
+                                          float R, float l) {
   const int lane = threadIdx.x & 31, r = row0 + 4 * lane;
   uint32_t own_k = 0u, own_v = 0u;  // four rows' codes (no page ends inside them)
   const long long at = r < k_end ? p.rows.at(b, kvh, r) : -1;
@@ -261,15 +267,16 @@ __device__ __noinline__ float2 own_scales(const TParams& p, int b, int kvh, int 
     own_k |= static_cast<uint32_t>(p.k_scale[at + i]) << (8 * i);
     own_v |= static_cast<uint32_t>(p.v_scale[at + i]) << (8 * i);
   }
+  __syncwarp();
   const TileScale sk(own_k, 0, kWideKeys), sv(own_v, kMinValueCode, kWideValues);
   if (!__any_sync(0xffffffffu, sk.far)) own_k = 0x01010101u * sk.E;
   own_v = __any_sync(0xffffffffu, sv.far) ? __vmaxu4(own_v, 0x01010101u * kMinValueCode)
                                           : 0x01010101u * sv.E;
-  float top = -INFINITY;
   __syncwarp();
-  for (int i = 0; i < BN; i += 4) {
+  float top = -INFINITY;
+  for (int i = 0; i < BN; i += 4) {  // y_j = x_j + ev_j
     const uint32_t ek = __shfl_sync(0xffffffffu, own_k, i >> 2);
-    const uint32_t ev4 = __shfl_sync(0xffffffffu, own_v, i >> 2);
+    const uint32_t ev = __shfl_sync(0xffffffffu, own_v, i >> 2);
     uint32_t s4[4];
     tmem_ld4_sync(tS + i, s4);
 #pragma unroll
@@ -277,26 +284,50 @@ __device__ __noinline__ float2 own_scales(const TParams& p, int b, int kvh, int 
       const float f = __uint_as_float(((ek >> (8 * e)) & 0xffu) << 23);
       // (neither 0 nor infinity: a hidden score is -inf, another may be 0)
       const float g = fminf(fmaxf(row_factor * f * 0.0078125f, 1.17549435e-38f), 3e38f);
-      const float x = __fmul_rn(__uint_as_float(s4[e]), g);
-      const float y = x + (static_cast<float>((ev4 >> (8 * e)) & 0xffu) - (127.f + kOwnScales));
+      const float y = __fmul_rn(__uint_as_float(s4[e]), g) +
+                      (static_cast<float>((ev >> (8 * e)) & 0xffu) - 127.f);
       top = fmaxf(top, y);
       s4[e] = __float_as_uint(y);
     }
     tmem_st4(tS + i, s4);
   }
   tmem_st_wait();
-  const float at0 = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;  // times 2^18: -120 <= -ev_j <= 102
+  const bool mine = top > R + kRescaleThreshold;
+  if (__any_sync(0xffffffffu, mine)) {
+    const float f = mine ? ex2_approx(0.5f * (R - top)) : 1.f;
+    l = l * f * f;
+    if (mine) R = top;
+    __syncwarp();
+    for (int i = 0; has_o && i < D; i += 4) {
+      uint32_t o4[4];
+      tmem_ld4_sync(tO + i, o4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o4[e] = __float_as_uint(__uint_as_float(o4[e]) * f * f);
+      tmem_st4(tO + i, o4);
+    }
+  }
+  // w_j = 2^(y_j - R), and 2^x_j by way of y_j - top, then - ev_j (-120 <= -ev_j <= 102, so times
+  // 2^18): beside a large score ev_j is lost in y_j
+  const float Rn = R == -INFINITY ? 0.f : R, at0 = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  __syncwarp();
   for (int i = 0; i < BN; i += 4) {
-    const uint32_t ev4 = __shfl_sync(0xffffffffu, own_v, i >> 2);
+    const uint32_t ev = __shfl_sync(0xffffffffu, own_v, i >> 2);
     uint32_t s4[4];
+    float w[4];
     tmem_ld4_sync(tS + i, s4);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      sum += ex2_approx((__uint_as_float(s4[e]) - at0) +
-                        (145.f - static_cast<float>((ev4 >> (8 * e)) & 0xffu)));
+    for (int e = 0; e < 4; ++e) {
+      const float y = __uint_as_float(s4[e]);
+      sum += ex2_approx((y - at0) + (145.f - static_cast<float>((ev >> (8 * e)) & 0xffu)));
+      w[e] = ex2_approx((y - Rn) + 7.f);
+    }
+    const uint32_t pk[2] = {pack_f16x2(w[0], w[1]), pack_f16x2(w[2], w[3])};
+    tmem_st2(tS + i / 2, pk);
   }
-  return make_float2(top, __log2f(sum) - 18.f);  // (0: -inf; NaN stays)
+  tmem_st_wait();
+  const float g = top == -INFINITY ? 1.f : ex2_approx(0.5f * (top - R));
+  return make_float2(R, l + sum * (1.f / 262144.f) * g * g);
 }
 
 // 2^(7 - below) in f16 (0 where that is less than f16's least)
@@ -789,7 +820,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         tc_fence_after();
         if (warp_live) {
           float c = row_factor, ev = 0.f;
-          volatile float own_l, own_top;  // (in memory: set and read for such tiles alone)
           if constexpr (F8) {
             const float2 ts = s_tile[(tile0 + j) & 7];
             c *= ts.x;
@@ -808,6 +838,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               mask_scores(tS + 32u * i, ~(in & draft_bits32(anc, p.words, k0 - w.L)));
             }
             tmem_st_wait();
+          }
+          if constexpr (F8) {
+            if (__builtin_expect(ev == kOwnScales, 0)) {
+              const float2 t = own_scales<D>(p, w.b, w.kvh, w.k_begin + j * BN, w.k_end, tS, tO,
+                                             j >= step, row_factor, R, l);
+              R = t.x;
+              l = t.y;
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[x]);
+              continue;
+            }
           }
           // (the next columns' load runs beside the arithmetic on these)
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -842,15 +884,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             tmem_ld32_issue(tS, ra);
             max32(rb);
           }
-          float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
-          // (then c = 1, and the sum of the tile's weights comes by way of own_l)
-          if (F8 && __builtin_expect(ev == kOwnScales, 0)) {
-            const float2 t = own_scales(p, w.b, w.kvh, w.k_begin + j * BN, w.k_end, tS, row_factor);
-            top = t.x + kOwnScales;
-            own_top = t.x;
-            own_l = t.y;
-            c = 1.f;
-          }
+          const float top = __fmul_rn(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), c) + ev;
           const bool mine = top > R + kRescaleThreshold;
           if (__any_sync(0xffffffffu, mine)) {
             float f = mine ? ex2_approx(F8 ? 0.5f * (R - top) : R - top) : 1.f;
@@ -916,24 +950,23 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             tmem_ld32_wait(rb);
             weights32(rb, tS + 48u);
           }
+          // (the weights are handed over ahead of the arithmetic on their sum)
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
           const float sum = (sa0 + sa1) + (sb0 + sb1);
           if constexpr (F8) {  // (a factor at a time: their product may leave fp32's range)
             const float g = low ? ex2_approx(0.5f * (Rt - R)) : 1.f;
             l += sum * 0.0078125f * ex2_approx(-ev) * g * g;
-            if (__builtin_expect(ev == kOwnScales, 0)) {  // (2^-ev is 0)
-              // (by the largest weight as it was rounded, in two halves)
-              const float h =
-                  own_l == -INFINITY ? 0.f : ex2_approx(0.5f * (own_l + (own_top + off - 7.f)));
-              l += (h * g) * (h * g);
-            }
           } else {
             l += sum;
           }
-          tmem_st_wait();
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       tile0 += w.n;
       // (what the next piece begins with is read beside the end of this one)
