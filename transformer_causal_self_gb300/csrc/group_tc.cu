@@ -14,6 +14,7 @@
 //                   at a piece's end
 //   warp 8          TMA producer          warp 9   TMEM owner and MMA issuer
 //   warps 10-11     bf16: clean the values of tiles that not every query sees
+//                   e4m3: scale bytes of every second tile
 //   warps 12-15     e4m3: take the keys' tiles to f16;  warps 16-19  the values'
 // TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D) O_1 [256+D,256+2D); P overwrites the
 // first half of its S and is read by the second product from there.
@@ -65,13 +66,15 @@ struct Cfg {
   static constexpr int kThreads = F8 ? 640 : 384;
   static constexpr int TILE = BN * D * 2;  // a Q, K or V tile of 16-bit values
   static constexpr int RAW = BN * D;       // an e4m3 tile
-  static constexpr int NRAW = F8 ? 4 : 0;
+  // raw tiles: as much as four of 128 channels (with eight of 64 the warps that read the scale
+  // bytes are far enough ahead: 8 x 32 drafts over 8000 rows, 64-row pages, 48.9 -> 45.0 us)
+  static constexpr int NRAW = F8 ? 512 / D : 0;
   // ring tiles that fit beside one or two query tiles
   static constexpr int NS1 = F8 ? 4 : (D == 128 ? 6 : 8);
   static constexpr int NS2 = F8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
   static constexpr int TILES = (NS1 + 1 > NS2 + 2 ? NS1 + 1 : NS2 + 2) * TILE + NRAW * RAW;
-  static constexpr int BARS = 336;
-  static constexpr int SMEM = 1024 + TILES + BARS + 128 * 8 + (F8 ? 8 * 8 : 0);
+  static constexpr int BARS = NRAW > 4 ? 384 : 336;
+  static constexpr int SMEM = 1024 + TILES + BARS + 128 * 8 + (F8 ? 8 * 8 + NRAW * BN : 0);
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -360,13 +363,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   uint64_t* teardown = bars + 10;
   uint64_t* kv_full = bars + 11;   // [8]
   uint64_t* kv_empty = bars + 19;  // [8]
-  uint64_t* raw_full = bars + 27;  // [4]
-  uint64_t* raw_empty = bars + 31; // [4]
-  uint64_t* edge_full = bars + 35; // [4] bf16: values to be cleaned, edge tile by edge tile
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 39);
+  constexpr int kRaw = C::NRAW > 4 ? C::NRAW : 4;
+  uint64_t* raw_full = bars + 27;            // [kRaw]
+  uint64_t* raw_empty = raw_full + kRaw;     // [kRaw]
+  uint64_t* edge_full = raw_empty + kRaw;    // [4] bf16: values to be cleaned, edge by edge tile
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(edge_full + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float2* s_ml = reinterpret_cast<float2*>(smem + C::TILES + C::BARS);  // [128]
   float2* s_tile = s_ml + 128;  // e4m3 [8]: 2^E_k, E_v (or kOwnScales) of a tile
+  uint8_t* s_below = reinterpret_cast<uint8_t*>(s_tile + 8);  // [NRAW][BN]: rows of raw tiles
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -384,9 +389,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       mbar_init(&kv_empty[s], 1);
     }
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_full[s], F8 ? 2 : 1);
       mbar_init(&raw_empty[s], 4);
       mbar_init(&edge_full[s], 1);
+    }
+    for (int s = 4; s < C::NRAW; ++s) {
+      mbar_init(&raw_full[s], 2);
+      mbar_init(&raw_empty[s], 4);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -588,7 +597,101 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       release(teardown);
       if (leader) mbar_wait(teardown, 0, nullptr, p.status, kDrainNs);
       __syncwarp();
-    } else if (!F8) {
+    } else if (F8) {
+      if constexpr (F8) {
+        // ---------------------------------------------------------- scale bytes (e4m3)
+        // Of every tile: the exponents that the softmax needs (s_tile), and how far every row is
+        // below its tile's largest (s_below: a byte per row and raw tile), with the raw tiles'
+        // barriers as the copies.  The two warps take every second tile (8 sequences of 8000 rows,
+        // 64 channels, 20 query rows: 50.1 us, 54.3 with one warp for all).
+        const int ps = p.rows.block_table != nullptr ? p.rows.page_size : 0;
+        bool ok = true;
+        uint32_t tile0 = 0;
+        for (; pc.n > 0 && ok; tile0 += pc.n, pc.next(p.line)) {
+          const View w(pc, p);
+          const int first = (warp - kWarpClean + tile0) & 1;  // of the warp's tiles
+          // Four rows per lane (no page ends inside them), packed.  The page number comes first, so
+          // each of the two loads is issued a tile ahead of its use, and taken over at the tile's
+          // end (a register move waits for a load).
+          const int row0 = w.k_begin + first * BN + 4 * lane;
+          int pg = ps > 0 ? row0 / ps : 0, ofs = row0 - pg * ps;  // of the next page lookup
+          const int32_t* const table =
+              p.rows.block_table + static_cast<size_t>(w.b) * p.rows.max_pages;
+          auto load_page = [&](int i) -> int {  // of the warp's i-th tile
+            const int page = ps > 0 && row0 + 2 * i * BN < w.k_end ? table[pg] : 0;
+            if (ps >= BN) {
+              ofs += 2 * BN;
+              while (ofs >= ps) ++pg, ofs -= ps;
+            } else if (ps > 0) {
+              pg += 2 * BN / ps;
+            }
+            return page;
+          };
+          // four rows' bytes of an array; 0 where there is no row
+          auto load_codes = [&](const uint8_t* scale, int i, int page, int at_ofs) -> uint32_t {
+            const int r = row0 + 2 * i * BN, left = w.k_end - r;
+            if (left <= 0) return 0u;
+            size_t at;
+            if (ps == 0) {
+              at = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.rows.Lmax + r;
+            } else {
+              if (page < 0 || page >= p.rows.num_pages) return 0u;
+              at = (static_cast<size_t>(page) * p.Hkv + w.kvh) * ps + at_ofs;
+            }
+            if (p.scale_words) return *reinterpret_cast<const uint32_t*>(scale + at);
+            uint32_t x = 0u;
+            for (int e = 0; e < min(left, 4); ++e)
+              x |= static_cast<uint32_t>(scale[at + e]) << (8 * e);
+            return x;
+          };
+          auto valid = [&](int i) -> uint32_t {  // bytes of rows there are
+            const int left = w.k_end - (row0 + 2 * i * BN);
+            return left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
+          };
+          int ofs1 = ofs;
+          int page = load_page(0);
+          uint32_t ck = load_codes(p.k_scale, 0, page, ofs1);
+          uint32_t cv = load_codes(p.v_scale, 0, page, ofs1);
+          ofs1 = ofs;
+          page = load_page(1);
+          for (int i = 0; first + 2 * i < w.n; ++i) {
+            const uint32_t tile = tile0 + first + 2 * i;
+            const uint32_t nk = load_codes(p.k_scale, i + 1, page, ofs1);
+            const uint32_t nv = load_codes(p.v_scale, i + 1, page, ofs1);
+            const uint32_t there = valid(i);
+            ck &= there;
+            cv &= there;
+            const int ofs2 = ofs;
+            const int page_next = load_page(i + 2);
+            const TileScale sk(ck, 0, kWideKeys), sv(cv, kMinValueCode, kWideValues);
+            const bool wide_k = __any_sync(0xffffffffu, sk.far);
+            const bool wide_v = __any_sync(0xffffffffu, sv.far);
+            // (no byte borrows: E is the largest; rows of their own scale: 2^7, or the floor's)
+            const uint32_t below[2] = {
+                wide_k ? 0u : 0x01010101u * sk.E - ck,
+                (wide_v ? __vmaxu4(cv, 0x01010101u * kMinValueCode) : 0x01010101u * sv.E) - cv};
+            for (int v = 0; v < 2; ++v) {
+              const uint32_t f = 2 * tile + v, rs = f % C::NRAW;
+              if (f >= C::NRAW)
+                ok = warp_wait(&raw_empty[rs], (f / C::NRAW - 1) & 1, abort_flag, p.status);
+              if (!ok) break;
+              reinterpret_cast<uint32_t*>(s_below)[BN / 4 * rs + lane] = below[v];
+              if (v == 0 && lane == 0)
+                s_tile[tile & 7] =
+                    make_float2(__uint_as_float(static_cast<uint32_t>(sk.E) << 23),
+                                wide_k || wide_v ? kOwnScales : static_cast<float>(sv.E - 127));
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&raw_full[rs]);
+            }
+            if (!ok) break;
+            ck = nk;
+            cv = nv;
+            page = page_next;
+            ofs1 = ofs2;
+          }
+        }
+      }
+    } else {
       // ------------------------------------------------------------ clean values (bf16)
       // Values of rows that not every query sees must not reach a product (0 * inf is NaN):
       // rows past the sequence are zeroed, and in the drafts' rows what is not finite (the
@@ -641,93 +744,26 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         to0 = at + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
         to1 = at + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
       }
-      const int ps = p.rows.block_table != nullptr ? p.rows.page_size : 0;
       bool ok = true;
-      uint32_t f = v, tile = 0;                  // its next fill, and tile of the CTA
+      uint32_t f = v;                            // its next fill
       for (; pc.n > 0 && ok; pc.next(p.line)) {
         const View w(pc, p);
-        // Scale bytes: every warp has those of all 128 rows, four per lane (no page ends inside
-        // them), packed.  The page number comes first, so each of the two loads is issued a tile
-        // ahead of its use, and taken over at the tile's end (a register move waits for a load).
-        const int row0 = w.k_begin + 4 * lane;
-        int pg = ps > 0 ? row0 / ps : 0, ofs = row0 - pg * ps;  // of the next page lookup
-        const int32_t* const table =
-            p.rows.block_table + static_cast<size_t>(w.b) * p.rows.max_pages;
-        auto load_page = [&](int j) -> int {
-          const int page = ps > 0 && j < w.n && row0 + j * BN < w.k_end ? table[pg] : 0;
-          if (ps >= BN) {
-            ofs += BN;
-            if (ofs >= ps) ++pg, ofs -= ps;
-          } else if (ps > 0) {
-            pg += BN / ps;
-          }
-          return page;
-        };
-        // four rows' bytes of an array; 0 where there is no row
-        auto load_codes = [&](const uint8_t* scale, int j, int page, int at_ofs) -> uint32_t {
-          const int r = row0 + j * BN, left = w.k_end - r;
-          if (j >= w.n || left <= 0) return 0u;
-          size_t at;
-          if (ps == 0) {
-            at = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.rows.Lmax + r;
-          } else {
-            if (page < 0 || page >= p.rows.num_pages) return 0u;
-            at = (static_cast<size_t>(page) * p.Hkv + w.kvh) * ps + at_ofs;
-          }
-          if (p.scale_words) return *reinterpret_cast<const uint32_t*>(scale + at);
-          uint32_t x = 0u;
-          for (int i = 0; i < min(left, 4); ++i)
-            x |= static_cast<uint32_t>(scale[at + i]) << (8 * i);
-          return x;
-        };
-        auto valid = [&](int j) -> uint32_t {  // bytes of rows there are
-          const int left = w.k_end - (row0 + j * BN);
-          return left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
-        };
-        int ofs1 = ofs;
-        int page = load_page(0);
-        uint32_t ck = v == 0 ? load_codes(p.k_scale, 0, page, ofs1) : 0u;
-        uint32_t cv = load_codes(p.v_scale, 0, page, ofs1);
-        ofs1 = ofs;
-        page = load_page(1);
-        for (int j = 0; j < w.n; ++j, f += 2, ++tile) {
+        for (int j = 0; j < w.n; ++j, f += 2) {
           const int key0 = w.k_begin + j * BN;
-          const uint32_t nk = v == 0 ? load_codes(p.k_scale, j + 1, page, ofs1) : 0u;
-          const uint32_t nv = load_codes(p.v_scale, j + 1, page, ofs1);
-          const uint32_t there = valid(j);
-          ck &= there;
-          cv &= there;
-          const int ofs2 = ofs;
-          const int page_next = load_page(j + 2);
-          // the tile's largest codes, then the factors of the warp's 32 rows, one per lane: row
-          // i * (128 / G) + (32 / G) * warp + q of the tile in lane (32 / G) * i + q
-          TileScale sc(cv, kMinValueCode, kWideValues);
-          bool wide = sc.far;
-          if (v == 0) {
-            const float Ev = static_cast<float>(sc.E - 127);
-            sc = TileScale(ck, 0, kWideKeys);
-            wide = __any_sync(0xffffffffu, wide || sc.far);
-            if (tid == 0)
-              s_tile[tile & 7] = make_float2(
-                  __uint_as_float(static_cast<uint32_t>(sc.E) << 23), wide ? kOwnScales : Ev);
-            if (wide) wide = __any_sync(0xffffffffu, sc.far);
-          } else {
-            wide = __any_sync(0xffffffffu, wide);
-          }
-          uint32_t factor;
-          {
-            constexpr int Q = 32 / G;
-            const int r = (lane / Q) * (128 / G) + Q * (warp & 3) + lane % Q;
-            const uint32_t four = __shfl_sync(0xffffffffu, v == 0 ? ck : cv, r >> 2);
-            const int code = static_cast<int>((four >> (8 * (r & 3))) & 0xffu);
-            factor = row_scale(!wide ? sc.E - code : v == 0 ? 0 : max(kMinValueCode - code, 0));
-            factor |= factor << 16;
-          }
           const uint32_t rs = f % C::NRAW, s = f % NS;
           ok = warp_wait(&raw_full[rs], (f / C::NRAW) & 1, abort_flag, p.status) &&
                (f < static_cast<uint32_t>(NS) ||
                 warp_wait(&kv_empty[s], (f / NS - 1) & 1, abort_flag, p.status));
           if (!ok) break;
+          // the factors of the warp's 32 rows, one per lane: row i * (128 / G) + (32 / G) * warp + q
+          // of the tile in lane (32 / G) * i + q
+          uint32_t factor;
+          {
+            constexpr int Q = 32 / G;
+            const int r = (lane / Q) * (128 / G) + Q * (warp & 3) + lane % Q;
+            factor = row_scale(s_below[BN * (f % C::NRAW) + r]);
+            factor |= factor << 16;
+          }
           const bool edge = key0 + BN > min(w.L, w.k_end);
           // piece i of the thread is row i * (128 / G) + r0
           constexpr int kRowStep = 128 / G;  // (a multiple of 8: the swizzle stays)
@@ -770,10 +806,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_arrive(&kv_full[s]);
             mbar_arrive(&raw_empty[rs]);
           }
-          ck = nk;
-          cv = nv;
-          page = page_next;
-          ofs1 = ofs2;
         }
       }
     }
