@@ -342,8 +342,7 @@ __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) {
 // RoPE angle pos * theta for theta given as an unevaluated sum hi + lo of two
 // floats, reduced into about [-pi, pi] before the sine and cosine are taken.
 // The product is split exactly with an FMA (Dekker), then 2*pi is removed in
-// three parts (Cody-Waite reduction, with eight times the parts of pi/4 in sinf of S. L. Moshier's
-// Cephes library): kTwoPiA has 8 significant bits and
+// three parts (Cody-Waite reduction): kTwoPiA has 8 significant bits and
 // kTwoPiB 11, so k*kTwoPiA and k*kTwoPiB are exact for |k| < 2^13, i.e. for
 // angles up to about 5.1e4 radians; positions are below 2^24.
 constexpr float kTwoPiA = 6.28125f;                 // 201 / 32

@@ -120,8 +120,9 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
 // or, with an explicit number of splits, as many CTAs as parts of that many equal ones of the
 // longest sequence can fill.
 // Trees with more query rows per KV head than this go to launch_group_tc (128 channels, 8
-// sequences of 8000 rows; here / there: 16 rows bf16 57 / 58 us, e4m3 45 / 58; 20 rows 91 / 58
-// and 69 / 58, the cache being read once per 16 rows here).
+// sequences of 8000 rows: 16 rows 50.4 us bf16, 41.7 e4m3 here; 20 rows 52.5 and 55.5 there; the
+// other way round, when this was chosen, 16 rows took 58 and 58, and 20 rows 91 and 69, the cache
+// being read once per 16 rows here).
 constexpr int kTcRows = 16;
 
 GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, bool f8, int max_seq_len,

@@ -166,9 +166,10 @@ struct CacheRows {
 
 // cos and sin of pos * theta, theta = hi + lo, 0 <= pos * theta < 2^16: the product as two floats
 // (exact but for lo's), the nearest multiple of pi/2 taken off it in three parts (a Cody-Waite
-// reduction; the parts are twice those of pi/4 in sinf of S. L. Moshier's Cephes library), then
-// the Taylor sums on [-pi/4, pi/4] (truncated below 2^-27).  Off by less than 2^-23, a quarter of
-// what __sincosf is: a key is rounded to e4m3 once, and every error before decides more ties.
+// reduction; the parts are twice those of pi/4 in sinf of S. L. Moshier's Cephes library, whose
+// eightfold common.cuh takes for 2 pi), then the Taylor sums on [-pi/4, pi/4] (truncated below
+// 2^-27).  Off by less than 2^-23, a quarter of what __sincosf is: a key is rounded to e4m3 once,
+// and every error before decides more ties.
 // (On the host, too, where it is tested against long doubles.)
 __host__ __device__ __forceinline__ void angle_cos_sin(int pos, float th_hi, float th_lo, float& c,
                                                        float& s) {

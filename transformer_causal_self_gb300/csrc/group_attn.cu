@@ -30,11 +30,11 @@
 // A maximum is raised only when a score exceeds it by 2^8, and only then do the lanes exchange
 // theirs: the usual tile costs one vote.
 //
-// What bounds it (128 channels, 4 query heads per KV head, e4m3): HBM for long sequences, 94.5 us
-// for 575 MB of 8 sequences (6.1 TB/s; the issue slots are 41 % busy, most of it e4m3 to f16);
-// 64 sequences of 512 to 8192 rows take 93.5 us for 576 MB (their ends add pieces: a piece's
+// What bounds it (128 channels, 4 query heads per KV head, e4m3): HBM for long sequences, 88.6 us
+// for 561 MB of 8 sequences (6.3 TB/s; the issue slots are 42 % busy, most of it e4m3 to f16);
+// 64 sequences of 512 to 8192 rows take 93.3 us for 576 MB (their ends add pieces: a piece's
 // queries and scale bytes are taken off the compute warps, which cost 114 us), and one of 1000
-// rows 8.6 us, the latencies of two launches, the lengths, a tile and the merge.
+// rows 8.7 us, the latencies of two launches, the lengths, a tile and the merge.
 #include "fp8.cuh"
 #include "group_work.cuh"
 #include "internal.h"

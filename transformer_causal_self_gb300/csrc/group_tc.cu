@@ -35,11 +35,12 @@
 // and a second exponential for l.  So a draft that a query does not see, or padding, has no part
 // in its output however large it is.  Rows with the least code (zeros) do not count as far apart.
 //
-// A 128-row tile of 128 channels takes an SM 1.49 us with up to 128 query rows over bf16 (6.7
-// TB/s over all SMs: HBM) and 1.81 with 256 (1410 TFLOP/s: 32 products of N = 128, which at
-// one in 118 cycles take 1.82 us; one rounding less in the softmax changed nothing);
-// over e4m3 1.39 (half the bytes: the tiles' way through shared memory, raw and as f16) and 1.99.
-// 64 channels: 0.80, 1.23, 1.05, 1.63 us.  A piece adds 3 to 6 us: partial results, next scores.
+// A 128-row tile of 128 channels takes an SM (slope from 8000 to 24000 rows) 1.38 us with up to 128
+// query rows over bf16 (HBM) and 1.85 with 256 (1380 TFLOP/s: 32 products of N = 128, which at one
+// in 118 cycles take 1.82 us; one rounding less in the softmax changed nothing); over e4m3 1.29
+// (half the bytes; the tiles' way through shared memory, raw and as f16, is 0.87, the rest is the
+// chain copy, conversion, S, softmax, O) and 2.00.  64 channels: 0.78, 1.22, 0.97, 1.59 us.  A
+// piece adds 3 to 6 us: partial results, next scores.
 #include "fp8.cuh"
 #include "internal.h"
 
@@ -258,7 +259,9 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
 // The softmax of a tile whose columns keep scales of their own (see the file's head), for the
 // thread's row: S in TMEM becomes the weights, R and l (and O, if there is one) are brought up to
 // date; returns R and l.  Out of line: these tiles are rare, and inline the softmax loop no longer
-// fits the instruction cache as well (16 x 32 drafts over 512..8192 rows 76.8 us, like this 73.8).
+// fits the instruction cache as well (16 x 32 drafts over 512..8192 rows: 76.8 us with it inline,
+// 73.8 like this, when this was chosen).  A row far away in every tile costs 25 % of such a step,
+// every second row far away 80 %.
 template <int D>
 __device__ __noinline__ float2 own_scales(const TParams& p, int b, int kvh, int row0, int k_end,
                                           uint32_t tS, uint32_t tO, bool has_o, float row_factor,

@@ -318,8 +318,8 @@ cudaError_t launch_tree_prep(const TreePrepArgs& a, cudaStream_t stream) {
   const int parts = ((a.Hq + 2 * a.Hkv) * (a.d / 16) + kThreads - 1) / kThreads;
   const bool few = static_cast<long long>(a.Tn) * a.B * parts <= 2 * kSms && parts <= 65535;
   // several drafts in a CTA where there are more than are resident at once: the masks are worked
-  // out once for them (64 sequences of 500 rows, 64 drafts: 127 and 138 us for the whole step over
-  // bf16 and e4m3, 135 and 151 with one draft each; 512 drafts: 2 us less with one each)
+  // out once for them (64 sequences of 500 rows, 64 drafts: 125 and 137 us for the whole step over
+  // bf16 and e4m3, 8 and 13 more with one draft each; 512 drafts: 2 us less with one each)
   const int drafts = static_cast<int>(
       std::min<long long>(kDrafts, (static_cast<long long>(a.Tn) * a.B + 4 * kSms - 1) / (4 * kSms)));
   auto* kernel = a.d == 128
