@@ -645,8 +645,8 @@ size_t csattn_tree_workspace_size(int B, int Hq, int Hkv, int Tn, int Lmax, int 
  * rounding; lse is that of the rounded queries, whose channels may fall to either side of a tie).
  * Over an 8-bit cache both are rounded to 11 bits, and what is below 2^-30 of a query's largest
  * product of weight and value vanishes.  With more than 16 query rows per KV head (Tn * Hq / Hkv),
- * rows with scale code 3 (zeros, or all below 2^-115) count as zeros beside rows more than 2^22
- * larger among the same 128; and 128 rows whose scales are further apart than 2^12 (values) or
+ * rows with scale codes 3 and 4 (zeros, or all below 2^-114) may count as zeros beside rows more
+ * than 2^22 larger among the same 128; and 128 rows whose scales are further apart than 2^12 (values) or
  * 2^22 (keys) take about twice the time of others.
  * Requirements: 1 <= Tn <= 256, d in {64, 128}, any Hq / Hkv.  Values of drafts that a query
  * does not see have no part in its output whatever they hold (NaN and infinities included).

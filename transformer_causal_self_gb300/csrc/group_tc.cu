@@ -33,7 +33,7 @@
 // its rows as they are, times 2^7, and the softmax takes every column's exponents from the scale
 // bytes: x_j = S_j 2^(e_j - 7), w_j = 2^(x_j + ev_j - R), R over the columns that the query sees,
 // and a second exponential for l.  So a draft that a query does not see, or padding, has no part
-// in its output however large it is.  Rows with the least code (zeros) do not count as far apart.
+// in its output however large it is.  Rows of the least code (zeros) do not count as far apart.
 //
 // A 128-row tile of 128 channels takes an SM (slope from 8000 to 24000 rows) 1.38 us with up to 128
 // query rows over bf16 (HBM) and 1.85 with 256 (1380 TFLOP/s: 32 products of N = 128, which at one
@@ -229,8 +229,9 @@ struct TileScale {
     const uint32_t a = four & 0xff00ffu, b = (four >> 8) & 0xff00ffu;
     const uint32_t hi = __vmaxu2(a, b);
     E = max(static_cast<int>(__reduce_max_sync(0xffffffffu, max(hi & 0xffffu, hi >> 16))), least);
-    // 4 is taken off each half, so that codes up to kScaleMin wrap round to the top (the upper
-    // half loses 5 where the lower one does not carry: one octave later is as good)
+    // 4 is taken off each half, so that codes up to kScaleMin wrap round to the top.  (The upper
+    // half loses 5 where the lower one does not carry: code 4 may go with them, and others are
+    // far one octave earlier.)
     static_assert(kScaleMin == 3, "codes that do not count");
     const uint32_t lo = __vminu2(a + 0xfffbfffcu, b + 0xfffbfffcu);
     far = E - 4 - static_cast<int>(min(lo & 0xffffu, lo >> 16)) > limit;
