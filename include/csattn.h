@@ -694,6 +694,192 @@ int csattn_tree_commit_paged(void* k_pages, void* v_pages, void* k_scale, void* 
                              int d, int cache_dtype, void* stream);
 
 /*
+ * 4-bit KV cache.  A cache row of one KV head is d e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), two channels to a byte (channel 2i in the low four bits of byte i), and one
+ * scale byte for every 16 channels: 4.5 bits a channel.  A scale byte is an f16's upper bits
+ * without its sign, 5 of exponent and 3 of mantissa: shifted left by 7 it is the f16 s, and a
+ * channel stands for x4 * s.  k_cache, v_cache are [B, Hkv, Lmax, d/2] bytes (or pages
+ * [num_pages, Hkv, page_size, d/2]), k_scale, v_scale [B, Hkv, Lmax, d/16] (or [num_pages, Hkv,
+ * page_size, d/16]), all 16-byte aligned.
+ * A write takes for a block of largest magnitude a the scale nearest to a / 6 (ties to even, at
+ * most 10240, byte 226) and the e2m1 nearest to x / s (ties to even, at most 6; the sign of x
+ * stays); both are exactly rounded.  So magnitudes past 61440 saturate there, and a block all
+ * below 6 * 2^-18 is stored as zeros.  A block with an infinity or NaN is stored as byte 255 and
+ * zeros, and reads as 16 NaN.  x4 * s is a bf16 (and an f16) number: reading is exact.  The calls
+ * below read bytes 0..226 and 255 (of another byte the scale is f16's, some number, infinity or
+ * NaN).
+ * Keys are stored, and queries used, as given: csattn_qk_norm_rope or csattn_rope_rotate rotates
+ * them first.
+ */
+
+/*
+ * Appends Tn tokens per sequence to a 4-bit cache: token t of sequence b goes to row
+ * cache_lens[b] + t.
+ *   k_new, v_new  [B, Hkv, Tn, d] bf16
+ * Requirements: dtype CSATTN_BF16 (of k_new and v_new), d in {64, 128}, 1 <= Tn <= Lmax < 2^30,
+ * B * Hkv * Tn * d < 2^33; k_new, v_new 16-byte aligned, cache_lens 4-byte.  A sequence with
+ * cache_lens[b] < 0 or cache_lens[b] + Tn > Lmax is left untouched and raises
+ * CSATTN_ERR_DEVICE_ARG in the status word.
+ */
+int csattn_cache_append_fp4(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                            void* k_scale, void* v_scale, const int32_t* cache_lens, int B,
+                            int Hkv, int Tn, int Lmax, int d, int dtype, void* stream);
+
+/* csattn_cache_append_fp4 into pages (block_table, page sizes and the handling of a page
+ * index outside the pool as csattn_cache_append_paged). */
+int csattn_cache_append_fp4_paged(const void* k_new, const void* v_new, void* k_pages,
+                                  void* v_pages, void* k_scale, void* v_scale,
+                                  const int32_t* block_table, const int32_t* cache_lens, int B,
+                                  int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                                  int d, int dtype, void* stream);
+
+/*
+ * csattn_cache_append_fp4 of a step's N tokens, of whatever sequences, to the slots that
+ * csattn_page_tables gives: token n goes to row slots[n] % page_size of page slots[n] / page_size.
+ *   k_new, v_new  bf16, token n's head g at n * stride of a token + g * stride of a head
+ *   strides  host int64 [4], in elements, multiples of 8: k_new's of a token and of a head, then
+ *            v_new's (so that both may be parts of a fused projection's rows); NULL: both are
+ *            [N, Hkv, d]
+ *   slots    device int64 [N], 8-byte aligned; a negative one: no row is written.  One at or past
+ *            num_pages * page_size raises CSATTN_ERR_DEVICE_ARG and no row is written.  No slot
+ *            may occur twice.
+ */
+int csattn_cache_append_fp4_slots(const void* k_new, const void* v_new, const int64_t* strides,
+                                  void* k_pages, void* v_pages, void* k_scale, void* v_scale,
+                                  const int64_t* slots, int N, int Hkv, int page_size,
+                                  int num_pages, int d, int dtype, void* stream);
+
+/*
+ * Reads rows 0..seq_lens[b]-1 of a 4-bit cache back to bf16 (exactly); arguments, requirements
+ * and errors as csattn_cache_read_fp8.
+ */
+int csattn_cache_read_fp4(const void* k_cache, const void* v_cache, const void* k_scale,
+                          const void* v_scale, const int32_t* seq_lens, void* k_out, void* v_out,
+                          int B, int Hkv, int Lmax, int Lout, int d, int dtype, void* stream);
+int csattn_cache_read_fp4_paged(const void* k_pages, const void* v_pages, const void* k_scale,
+                                const void* v_scale, const int32_t* block_table,
+                                const int32_t* seq_lens, void* k_out, void* v_out, int B, int Hkv,
+                                int page_size, int num_pages, int max_pages, int Lout, int d,
+                                int dtype, void* stream);
+
+/*
+ * Bytes of device workspace csattn_attn_decode_fp4 and its paged form (Lmax = max_pages *
+ * page_size) need, for any max_seq_len <= Lmax.  0 for sizes they reject.
+ */
+size_t csattn_decode_fp4_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits);
+
+/*
+ * csattn_attn_decode over a 4-bit cache: one new query per sequence, whose own key and value
+ * are in the cache already.
+ *   q         [B, Hq, 1, d] bf16, used as given
+ *   seq_lens  device int32 [B], 0 <= seq_lens[b] <= max_seq_len <= Lmax; 0 (padding of a batch):
+ *             the output is 0
+ *   out       [B, Hq, 1, d] bf16
+ *   scale, num_splits, workspace  as csattn_attn_decode_fp8
+ * The cache's values enter the products exactly, the queries rounded to 11 bits (bf16 has 8;
+ * channels below 2^-38 of a query's largest vanish), the softmax weights rounded to 11 bits
+ * (those below 2^-32 of a query's largest vanish); sums are fp32.
+ * Requirements: dtype CSATTN_BF16 (of q and out), d in {64, 128}, any Hq / Hkv.  Rows at or
+ * beyond seq_lens[b] are never used.  A seq_lens[b] outside [0, max_seq_len] raises
+ * CSATTN_ERR_DEVICE_ARG in the status word and that sequence's output is zero; a page index
+ * outside the pool raises it and its rows read as zeros.
+ */
+int csattn_attn_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
+                           const void* k_scale, const void* v_scale, const int32_t* seq_lens,
+                           void* out, int B, int Hq, int Hkv, int Lmax, int d, int dtype,
+                           float scale, int max_seq_len, int num_splits, void* workspace,
+                           size_t workspace_bytes, void* stream);
+int csattn_attn_decode_fp4_paged(const void* q, const void* k_pages, const void* v_pages,
+                                 const void* k_scale, const void* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                 int B, int Hq, int Hkv, int page_size, int num_pages,
+                                 int max_pages, int d, int dtype, float scale, int max_seq_len,
+                                 int num_splits, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Pages, slots and positions of a step's new tokens, from the sequences' lengths alone.  Sequence
+ * b holds cache_lens[b] rows in its first ceil(cache_lens[b] / page_size) pages and gets
+ * new_lens[b] more; the step's tokens are those of sequence 0, then 1, and so on.
+ *   cache_lens, new_lens  device int32 [B]
+ *   block_table  device int32 [B, max_pages]; entries of the pages that the sequences take are
+ *              written, others are left as they were
+ *   free_pages   device int32 [free_size], num_free device int32 [1]: the free pages are
+ *              free_pages[0..num_free-1], and are taken from the end on (sequence 0's first page
+ *              is free_pages[num_free - 1])
+ *   seq_lens     device int32 [B]: cache_lens + new_lens
+ *   starts       device int32 [B + 1]: the tokens ahead of each sequence's, and of all (at most N)
+ *   slots        device int64 [N]: a token's page * page_size + row in the page, as
+ *              csattn_cache_append_fp4_slots reads them; -1 where there is no token
+ *   positions    device int32 [N]: a token's row in its sequence; 0 where there is no token
+ *   free_left    device int32 [1]: the pages that are still free (free_pages stays as it was; a
+ *              page comes back when it is written to free_pages[free_left] and that is raised)
+ * A sequence fails if a length is negative or their sum is past max_pages * page_size, if its
+ * tokens do not all fit in N, or if the sequences up to and with it want more pages than there
+ * are and it wants one: it then takes no page, its tokens have slot -1 and position 0, its
+ * seq_lens[b] is cache_lens[b] (0 if that is out of range), and CSATTN_ERR_DEVICE_ARG is raised in
+ * the status word.  A page index outside [0, num_pages), in the table or the list, raises it,
+ * is not written to the table, and tokens that would be there have slot -1.  So does a num_free
+ * outside [0, free_size], which is taken as the nearer end.
+ * Requirements: 1 <= B <= 65535, 1 <= N <= 2^30, max_pages * page_size < 2^30, page sizes as
+ * csattn_cache_append_paged; pointers 4-byte aligned, slots 8-byte.  Outputs overlap neither each
+ * other nor an input.  Asynchronous on `stream`.
+ */
+int csattn_page_tables(const int32_t* cache_lens, const int32_t* new_lens, int32_t* block_table,
+                       const int32_t* free_pages, const int32_t* num_free, int32_t* seq_lens,
+                       int32_t* starts, int64_t* slots, int32_t* positions, int32_t* free_left,
+                       int B, int N, int page_size, int num_pages, int max_pages, int free_size,
+                       void* stream);
+
+/*
+ * RMS norm of every head's queries and keys, its gain, and the rotation, in one pass:
+ *   y = R_pos (x / sqrt(mean(x^2) + eps) * w) over the d channels of a head, rounded once
+ *   q [B, Hq, T, d], k [B, Hkv, T, d]  bf16 or fp32 (`dtype`); q_out, k_out the same, dense
+ *   q_weight, k_weight  [d] of the same type; NULL: gains of 1
+ *   norm       1; 0: no norm and no gains, the rotation alone
+ *   positions  device int32 [B, T], in [0, 2^24); NULL: token t is at pos0 + t
+ *   strides    host int64 [6], in elements: q's of a sequence, a head and a token, then k's, each a
+ *              multiple of 16 bytes (so that both may be parts of a fused projection's rows
+ *              [B, T, heads, d]); NULL: both dense.  The d channels of a head are contiguous.
+ *   rope_base  >= 1: pair p of channels is turned by position * rope_base^(-2p/d); <= 0: no
+ *              rotation;  rope_layout  as csattn_attn_fwd
+ * Sums and everything between load and store are fp32 (squares past fp32's range overflow: a head
+ * with magnitudes of 2^60 and above has no meaningful norm); sines and cosines are good to 2^-22
+ * at any position.  Requirements: d in {64, 128}, fp32 also {16, 32}; B * heads * T * d < 2^33,
+ * T < 2^24; pointers 16-byte aligned (positions 4-byte).  A position out of range raises
+ * CSATTN_ERR_DEVICE_ARG in the status word and that token is turned as at position 0.  The
+ * outputs may not overlap the inputs.  Asynchronous on `stream`.
+ */
+int csattn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                        const int32_t* positions, void* q_out, void* k_out, int B, int Hq, int Hkv,
+                        int T, int d, int dtype, const int64_t* strides, int pos0, int norm,
+                        float eps, float rope_base, int rope_layout, void* stream);
+
+/* Bytes of device workspace csattn_qk_norm_rope_bwd needs where gains have gradients. */
+size_t csattn_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * Backward of csattn_qk_norm_rope (same q, k, gains, positions, eps, base and layout):
+ *   g = R_pos^T dy,  n = x / sqrt(mean(x^2) + eps),
+ *   dx = (g w - n mean(g w n)) / sqrt(mean(x^2) + eps),  dw = sum over sequences, heads and
+ *   tokens of g n
+ *   dq_out, dk_out  the outputs' gradients, dense;  dq, dk  written, [B, heads, T, d]
+ *   dq_weight, dk_weight  fp32 [d], written; NULL where the gain is
+ *   strides    host int64 [12]: q's, k's, dq's, dk's (as above); NULL: all dense.  No two
+ *              elements of dq or dk may share a place.
+ *   workspace  >= csattn_qk_norm_rope_bwd_workspace_size(d) bytes, 16-byte aligned, in use until
+ *              the work on `stream` completes; may be NULL without gains
+ * The gains' gradients are added up in fp32 in an order that depends on the sizes alone: the same
+ * call gives the same bits.
+ */
+int csattn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                            const void* q_weight, const void* k_weight, const int32_t* positions,
+                            void* dq, void* dk, float* dq_weight, float* dk_weight, int B, int Hq,
+                            int Hkv, int T, int d, int dtype, const int64_t* strides, int pos0,
+                            int norm, float eps, float rope_base, int rope_layout, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
  * Synchronize `stream`, then read and clear this device's status word.
  * Returns CSATTN_OK, CSATTN_ERR_TIMEOUT (a kernel wait ran out of time),
  * CSATTN_ERR_DEVICE_ARG (a device-side argument check failed) or
@@ -711,8 +897,8 @@ int csattn_check_status(void* stream);
 int csattn_selftest_bounded_wait(int limit_us, void* stream);
 
 /*
- * The calling thread's next csattn_attn_decode_fp8 or csattn_attn_tree_step (or paged form) that
- * launches runs with a barrier that waits for one arrival more than will come.  Its waits run out
+ * The calling thread's next csattn_attn_decode_fp8, csattn_attn_decode_fp4 or
+ * csattn_attn_tree_step (or paged form) that launches runs with a barrier that waits for one arrival more than will come.  Its waits run out
  * after 2 seconds, its kernels return normally, csattn_check_status() afterwards returns
  * CSATTN_ERR_TIMEOUT, and its outputs are undefined.
  */

@@ -14,8 +14,10 @@ Modules:
     weighted sum of V; plus the decode form and the split log-sum-exp merge.
   * ``naive`` -- an independently written scalar-loop version (Python floats and
     ``math`` only), used to brute-force-check ``attn`` on tiny inputs.
+  * ``step``  -- the 4-bit cache format, block tables, and the norm of queries and keys; pinned by
+    ``tests/test_abi_fp4_step.py``.
 
 Every function here is pinned by ``tests/test_oracle_pins.py``; none is
 "parity unpinned".
 """
-from . import attn, naive  # noqa: F401
+from . import attn, naive, step  # noqa: F401

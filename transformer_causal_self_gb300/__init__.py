@@ -11,7 +11,7 @@ import ctypes
 import functools
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -28,6 +28,10 @@ __all__ = [
     "attn_decode_fp8", "attn_decode_fp8_paged", "attn_tree_step", "attn_tree_step_paged",
     "tree_commit", "tree_commit_paged", "decode_fp8_workspace_size", "tree_workspace_size",
     "release_workspaces",
+    "cache_append_fp4", "cache_append_fp4_paged", "cache_append_fp4_slots", "cache_read_fp4",
+    "cache_read_fp4_paged", "attn_decode_fp4", "attn_decode_fp4_paged",
+    "decode_fp4_workspace_size", "page_tables", "PageTables", "qk_norm_rope", "qk_norm_rope_bwd",
+    "qk_norm_rope_bwd_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -102,6 +106,23 @@ _SIGNATURES = {
                                      _vp]),
     "csattn_tree_commit": (_c_int, [_vp] * 8 + [_c_int] * 6 + [_vp]),
     "csattn_tree_commit_paged": (_c_int, [_vp] * 9 + [_c_int] * 8 + [_vp]),
+    "csattn_cache_append_fp4": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_vp]),
+    "csattn_cache_append_fp4_paged": (_c_int, [_vp] * 8 + [_c_int] * 8 + [_vp]),
+    "csattn_cache_append_fp4_slots": (_c_int, [_vp] * 8 + [_c_int] * 6 + [_vp]),
+    "csattn_cache_read_fp4": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_vp]),
+    "csattn_cache_read_fp4_paged": (_c_int, [_vp] * 8 + [_c_int] * 8 + [_vp]),
+    "csattn_decode_fp4_workspace_size": (_c_size, [_c_int] * 6),
+    "csattn_attn_decode_fp4": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_c_float, _c_int, _c_int, _vp,
+                                                                  _c_size, _vp]),
+    "csattn_attn_decode_fp4_paged": (_c_int, [_vp] * 8 + [_c_int] * 8 +
+                                     [_c_float, _c_int, _c_int, _vp, _c_size, _vp]),
+    "csattn_page_tables": (_c_int, [_vp] * 10 + [_c_int] * 6 + [_vp]),
+    "csattn_qk_norm_rope": (_c_int, [_vp] * 7 + [_c_int] * 6 + [_vp, _c_int, _c_int, _c_float,
+                                                               _c_float, _c_int, _vp]),
+    "csattn_qk_norm_rope_bwd_workspace_size": (_c_size, [_c_int]),
+    "csattn_qk_norm_rope_bwd": (_c_int, [_vp] * 11 + [_c_int] * 6 +
+                                [_vp, _c_int, _c_int, _c_float, _c_float, _c_int, _vp, _c_size,
+                                 _vp]),
     "csattn_check_status": (_c_int, [_vp]),
     "csattn_selftest_bounded_wait": (_c_int, [_c_int, _vp]),
     "csattn_selftest_lost_arrival": (_c_int, []),
@@ -720,8 +741,8 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: int, stream):
 
 
 def release_workspaces() -> None:
-    """Lets go of the workspaces that calls of the 8-bit decode and of tree steps have kept for this
-    thread (up to 64 MB for each stream that it made such calls on; a thread's end does, too)."""
+    """Lets go of the workspaces that calls of the 8-bit and 4-bit decodes, of tree steps and of
+    qk_norm_rope_bwd have kept for this thread (up to 64 MB for each stream that it made such calls on; a thread's end does, too)."""
     _kept.__dict__.clear()
 
 
@@ -1031,6 +1052,377 @@ def tree_commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table:
                         v_scale, block_table, cache_lens, parents, accepted, new_lens, stream)
 
 
+# ------------------------------------------------------------------- 4-bit cache
+_FP4 = (torch.uint8,) + tuple(getattr(torch, n) for n in ("float4_e2m1fn_x2",) if hasattr(torch, n))
+_U8, _I64 = (torch.uint8,), (torch.int64,)
+
+
+def _fp4_ptrs(k, v, k_scale, v_scale, dev: int):
+    """Pointers of a 4-bit cache, [.., Hkv, rows, d/2], and its scales, [.., Hkv, rows, d/16]; and
+    (first size, Hkv, rows, d)."""
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"caches have 4 dimensions, got {len(shape)}")
+    n, Hkv, rows, half = shape
+    scales = (n, Hkv, rows, half // 8)
+    return ((_ptr("keys' cache", k, shape, _FP4, dev), _ptr("values' cache", v, shape, _FP4, dev),
+             _ptr("k_scale", k_scale, scales, _U8, dev), _ptr("v_scale", v_scale, scales, _U8, dev)),
+            (n, Hkv, rows, 2 * half))
+
+
+def _append_fp4(fn, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                stream):
+    dev = _device_of("k_new", k_new, 4)
+    shape = k_new.shape
+    B, Hkv, Tn, d = shape
+    cache, cshape = _fp4_ptrs(k_cache, v_cache, k_scale, v_scale, dev)
+    table, size, _ = _cache_sizes(cshape, block_table, B, dev)
+    if cshape[1] != Hkv or cshape[3] != d:
+        raise ValueError("k_new and the cache differ in heads or head size")
+    _run(dev, fn, _ptr("k_new", k_new, shape, _BF16, dev), _ptr("v_new", v_new, shape, _BF16, dev),
+         *cache, *table, _ptr("cache_lens", cache_lens, (B,), _I32, dev), B, Hkv, Tn, *size, d,
+         CSATTN_BF16, _handle(dev, stream))
+
+
+def cache_append_fp4(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                     cache_lens: torch.Tensor, *, stream=None) -> None:
+    """Append Tn tokens per sequence to a 4-bit cache (C: csattn_cache_append_fp4).
+
+    k_new, v_new [B,Hkv,Tn,d] bf16, stored as given (rotate the keys first: qk_norm_rope); caches
+    [B,Hkv,Lmax,d/2] uint8 (or torch's packed e2m1 type) with scales [B,Hkv,Lmax,d/16] uint8;
+    cache_lens int32 [B] on the device, not advanced.
+    """
+    _append_fp4(load_library().csattn_cache_append_fp4, k_new, v_new, k_cache, v_cache, k_scale,
+                v_scale, None, cache_lens, stream)
+
+
+def cache_append_fp4_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                           v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           block_table: torch.Tensor, cache_lens: torch.Tensor, *,
+                           stream=None) -> None:
+    """cache_append_fp4 into pages [num_pages,Hkv,page_size,d/2], scales
+    [num_pages,Hkv,page_size,d/16] (C: csattn_cache_append_fp4_paged)."""
+    _append_fp4(load_library().csattn_cache_append_fp4_paged, k_new, v_new, k_pages, v_pages,
+                k_scale, v_scale, block_table, cache_lens, stream)
+
+
+def cache_append_fp4_slots(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                           v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           slots: torch.Tensor, *, stream=None) -> None:
+    """Append a step's N tokens to the slots of page_tables (C: csattn_cache_append_fp4_slots).
+
+    k_new, v_new [N,Hkv,d] bf16, views of a fused projection's rows among them (the channels of a
+    head contiguous, other strides multiples of 8); slots int64 [N], negative: no row.
+    """
+    dev = _device_of("k_new", k_new, 3)
+    shape = k_new.shape
+    N, Hkv, d = shape
+    cache, cshape = _fp4_ptrs(k_pages, v_pages, k_scale, v_scale, dev)
+    if cshape[1] != Hkv or cshape[3] != d:
+        raise ValueError("k_new and the cache differ in heads or head size")
+    kp, ks = _strided("k_new", k_new, shape, _BF16, dev)
+    vp, vs = _strided("v_new", v_new, shape, _BF16, dev)
+    _run(dev, load_library().csattn_cache_append_fp4_slots, kp, vp,
+         None if ks is vs is None else _strides((ks, vs), shape), *cache,
+         _ptr("slots", slots, (N,), _I64, dev), N, Hkv, cshape[2], cshape[0], d, CSATTN_BF16,
+         _handle(dev, stream))
+
+
+def _strided(name: str, t: torch.Tensor, shape, dtypes, dev: int):
+    """Address and strides (None: contiguous) of a tensor whose last dimension is contiguous."""
+    if t.is_contiguous():
+        return _ptr(name, t, shape, dtypes, dev), None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    strides = t.stride()
+    if strides[-1] != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    return t.data_ptr(), strides[:-1]
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(parts, *shapes):
+    """A host array of the strides of all dimensions but the last of several tensors, None: dense
+    (of the shape at its place, or the last one given)."""
+    flat = []
+    for i, part in enumerate(parts):
+        if part is None:
+            shape = shapes[min(i, len(shapes) - 1)]
+            step, part = shape[-1], []
+            for n in reversed(shape[:-1]):
+                part.insert(0, step)
+                step *= n
+        flat += part
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def _read_fp4(fn, k, v, k_scale, v_scale, block_table, seq_lens, k_out, v_out, stream):
+    dev = _device_of("seq_lens", seq_lens, 1)
+    B = seq_lens.shape[0]
+    cache, cshape = _fp4_ptrs(k, v, k_scale, v_scale, dev)
+    _, Hkv, _, d = cshape
+    table, size, rows = _cache_sizes(cshape, block_table, B, dev)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        k_out, v_out = (_empty((B, Hkv, rows, d), torch.bfloat16, dev, stream) for _ in range(2))
+    if k_out.dim() != 4:
+        raise ValueError("k_out: 4 dimensions expected")
+    Lout = k_out.shape[2]
+    shape = (B, Hkv, Lout, d)
+    _run(dev, fn, *cache, *table, _ptr("seq_lens", seq_lens, (B,), _I32, dev),
+         _ptr("k_out", k_out, shape, _BF16, dev), _ptr("v_out", v_out, shape, _BF16, dev), B, Hkv,
+         *size, Lout, d, CSATTN_BF16, _handle(dev, stream))
+    return k_out, v_out
+
+
+def cache_read_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                   v_scale: torch.Tensor, seq_lens: torch.Tensor,
+                   k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None, *,
+                   stream=None):
+    """Rows 0..seq_lens[b]-1 of a 4-bit cache as bf16, exactly (C: csattn_cache_read_fp4).
+
+    k_out, v_out [B,Hkv,Lout,d] (allocated with Lout = Lmax when not given; rows at or past
+    seq_lens[b] are not written).  Returns (k_out, v_out).
+    """
+    return _read_fp4(load_library().csattn_cache_read_fp4, k_cache, v_cache, k_scale, v_scale,
+                     None, seq_lens, k_out, v_out, stream)
+
+
+def cache_read_fp4_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                         k_out: Optional[torch.Tensor] = None,
+                         v_out: Optional[torch.Tensor] = None, *, stream=None):
+    """cache_read_fp4 from pages (C: csattn_cache_read_fp4_paged); the outputs are contiguous,
+    [B,Hkv,Lout,d]."""
+    return _read_fp4(load_library().csattn_cache_read_fp4_paged, k_pages, v_pages, k_scale,
+                     v_scale, block_table, seq_lens, k_out, v_out, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def decode_fp4_workspace_size(B, Hq, Hkv, Lmax, d, num_splits: int = 0) -> int:
+    return int(load_library().csattn_decode_fp4_workspace_size(B, Hq, Hkv, Lmax, d, num_splits))
+
+
+def _decode_fp4(fn, q, k, v, k_scale, v_scale, block_table, seq_lens, out, scale, max_seq_len,
+                num_splits, workspace, stream):
+    dev = _device_of("q", q, 4)
+    B, Hq, _, d = q.shape
+    shape = (B, Hq, 1, d)
+    cache, cshape = _fp4_ptrs(k, v, k_scale, v_scale, dev)
+    Hkv = cshape[1]
+    table, size, rows = _cache_sizes(cshape, block_table, B, dev)
+    if cshape[3] != d:
+        raise ValueError("q and the cache differ in head size")
+    if out is None:
+        out = _empty(shape, torch.bfloat16, dev, stream)
+    if max_seq_len is None:
+        max_seq_len = rows
+    need = 0 if workspace is not None else decode_fp4_workspace_size(
+        B, Hq, Hkv, max_seq_len, d, num_splits)
+    workspace, wp, wn = _workspace(workspace, need, dev, stream)
+    _run(dev, fn, _ptr("q", q, shape, _BF16, dev), *cache, *table,
+         _ptr("seq_lens", seq_lens, (B,), _I32, dev), _ptr("out", out, shape, _BF16, dev), B, Hq,
+         Hkv, *size, d, CSATTN_BF16, scale, max_seq_len, num_splits, wp, wn, _handle(dev, stream))
+    return out
+
+
+def attn_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scale: torch.Tensor, v_scale: torch.Tensor, seq_lens: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, *, scale: float = 0.0,
+                    max_seq_len: Optional[int] = None, num_splits: int = 0,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Decode over a 4-bit cache (C: csattn_attn_decode_fp4).
+
+    q [B,Hq,1,d] bf16, used as given (rotated: qk_norm_rope); caches [B,Hkv,Lmax,d/2] with scales
+    [B,Hkv,Lmax,d/16] as cache_append_fp4 writes them (the new token included); seq_lens int32 [B]
+    on the device, 0 for a sequence that is padding (its output is 0).  max_seq_len defaults to
+    Lmax (always a valid bound).
+    """
+    return _decode_fp4(load_library().csattn_attn_decode_fp4, q, k_cache, v_cache, k_scale,
+                       v_scale, None, seq_lens, out, scale, max_seq_len, num_splits, workspace,
+                       stream)
+
+
+def attn_decode_fp4_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                          k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                          seq_lens: torch.Tensor, out: Optional[torch.Tensor] = None, *,
+                          scale: float = 0.0, max_seq_len: Optional[int] = None,
+                          num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """attn_decode_fp4 over pages [num_pages,Hkv,page_size,d/2], scales
+    [num_pages,Hkv,page_size,d/16] (C: csattn_attn_decode_fp4_paged)."""
+    return _decode_fp4(load_library().csattn_attn_decode_fp4_paged, q, k_pages, v_pages, k_scale,
+                       v_scale, block_table, seq_lens, out, scale, max_seq_len, num_splits,
+                       workspace, stream)
+
+
+# ---------------------------------------------- block tables; norm and rotation of q and k
+class PageTables(NamedTuple):
+    """What page_tables returns (the block table is written in place)."""
+    seq_lens: torch.Tensor   # int32 [B], lengths with the new tokens
+    starts: torch.Tensor     # int32 [B + 1], where each sequence's tokens begin in the step
+    slots: torch.Tensor      # int64 [N], of each token; -1: none
+    positions: torch.Tensor  # int32 [N], of each token
+    free_left: torch.Tensor  # int32 [1], pages that are still free
+
+
+def page_tables(cache_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                free_pages: torch.Tensor, num_free: torch.Tensor, num_tokens: int, *,
+                page_size: int, num_pages: int, out: Optional[PageTables] = None,
+                stream=None) -> PageTables:
+    """Pages, slots and positions of a step's new tokens (C: csattn_page_tables).
+
+    Sequence b holds cache_lens[b] rows and gets new_lens[b] tokens (int32 [B] on the device).
+    Pages that this takes come from the end of free_pages[:num_free] (int32; num_free int32 [1] on
+    the device) and are written into block_table int32 [B,max_pages]; free_pages stays as it is,
+    and free_left is the next step's num_free.  num_tokens: the step's size, at least the sum of
+    new_lens (the tokens behind have slot -1).  Sequences for which there is no room are left as
+    they were and reported by check_status().  out: the tensors to write.
+    """
+    dev = _device_of("cache_lens", cache_lens, 1)
+    B = cache_lens.shape[0]
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table [B, max_pages] and free_pages [pages] expected")
+    per = block_table.shape[1]
+    if out is None:
+        out = PageTables(_empty((B,), torch.int32, dev, stream),
+                         _empty((B + 1,), torch.int32, dev, stream),
+                         _empty((num_tokens,), torch.int64, dev, stream),
+                         _empty((num_tokens,), torch.int32, dev, stream),
+                         _empty((1,), torch.int32, dev, stream))
+    _run(dev, load_library().csattn_page_tables, _ptr("cache_lens", cache_lens, (B,), _I32, dev),
+         _ptr("new_lens", new_lens, (B,), _I32, dev),
+         _ptr("block_table", block_table, (B, per), _I32, dev),
+         _ptr("free_pages", free_pages, free_pages.shape, _I32, dev),
+         _ptr("num_free", num_free, (1,), _I32, dev), _ptr("seq_lens", out[0], (B,), _I32, dev),
+         _ptr("starts", out[1], (B + 1,), _I32, dev),
+         _ptr("slots", out[2], (num_tokens,), _I64, dev),
+         _ptr("positions", out[3], (num_tokens,), _I32, dev),
+         _ptr("free_left", out[4], (1,), _I32, dev), B, num_tokens, page_size, num_pages, per,
+         free_pages.shape[0], _handle(dev, stream))
+    return out
+
+
+def _norm_args(q, k, q_weight, k_weight, positions, norm):
+    """(dev, types, shapes of q and k, pointers of the gains and positions)."""
+    dev = _device_of("q", q, 4)
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q: {q.dtype}, expected bf16 or fp32")
+    types = (q.dtype,)
+    qshape, kshape = q.shape, k.shape
+    B, _, T, d = qshape
+    if k.dim() != 4 or (kshape[0], kshape[2], kshape[3]) != (B, T, d):
+        raise ValueError("q [B,Hq,T,d] and k [B,Hkv,T,d] differ in B, T or d")
+    return (dev, types, qshape, kshape,
+            None if q_weight is None else _ptr("q_weight", q_weight, (d,), types, dev),
+            None if k_weight is None else _ptr("k_weight", k_weight, (d,), types, dev),
+            None if positions is None else _ptr("positions", positions, (B, T), _I32, dev))
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, *,
+                 norm: bool = True, eps: float = 1e-6, rope_base: float = 0.0,
+                 rope_layout: str = "split_half", pos0: int = 0, stream=None):
+    """RMS norm of every head's queries and keys, its gain and the rotation, in one pass
+    (C: csattn_qk_norm_rope).
+
+    q [B,Hq,T,d], k [B,Hkv,T,d] bf16 or fp32, views of a fused projection among them (the channels
+    of a head contiguous); gains [d] of the same type (None: 1); positions int32 [B,T] (None:
+    pos0 + t).  norm=False rotates alone.  A step's packed tokens are a batch of N sequences of one
+    token.  Returns (q_out, k_out), contiguous.
+    """
+    dev, types, qshape, kshape, qw, kw, pos = _norm_args(q, k, q_weight, k_weight, positions, norm)
+    B, Hq, T, d = qshape
+    if q_out is None:
+        q_out = _empty(qshape, q.dtype, dev, stream)
+    if k_out is None:
+        k_out = _empty(kshape, q.dtype, dev, stream)
+    qp, qs = _strided("q", q, qshape, types, dev)
+    kp, ks = _strided("k", k, kshape, types, dev)
+    _run(dev, load_library().csattn_qk_norm_rope, qp, kp, qw, kw, pos,
+         _ptr("q_out", q_out, qshape, types, dev), _ptr("k_out", k_out, kshape, types, dev), B, Hq,
+         kshape[1], T, d, CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
+         None if qs is ks is None else _strides((qs, ks), qshape, kshape), pos0, 1 if norm else 0,
+         eps, rope_base, _ROPE_LAYOUT[rope_layout], _handle(dev, stream))
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=16)
+def qk_norm_rope_bwd_workspace_size(d: int) -> int:
+    return int(load_library().csattn_qk_norm_rope_bwd_workspace_size(d))
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                     q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None,
+                     positions: Optional[torch.Tensor] = None, dq: Optional[torch.Tensor] = None,
+                     dk: Optional[torch.Tensor] = None, dq_weight: Optional[torch.Tensor] = None,
+                     dk_weight: Optional[torch.Tensor] = None, *, norm: bool = True,
+                     eps: float = 1e-6, rope_base: float = 0.0, rope_layout: str = "split_half",
+                     pos0: int = 0, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of qk_norm_rope (C: csattn_qk_norm_rope_bwd).
+
+    dq_out, dk_out: the gradients of its outputs, contiguous; dq, dk of q's and k's shapes, views
+    of a fused projection's gradient among them (allocated dense when not given).  Returns
+    (dq, dk, dq_weight, dk_weight), the last two fp32 [d], None where the gain is.
+    """
+    dev, types, qshape, kshape, qw, kw, pos = _norm_args(q, k, q_weight, k_weight, positions, norm)
+    B, Hq, T, d = qshape
+    if (dq_weight is not None and qw is None) or (dk_weight is not None and kw is None):
+        raise ValueError("a gradient for a gain that is not given")
+    if dq is None:
+        dq = _empty(qshape, q.dtype, dev, stream)
+    if dk is None:
+        dk = _empty(kshape, q.dtype, dev, stream)
+    if qw is not None and dq_weight is None:
+        dq_weight = _empty((d,), torch.float32, dev, stream)
+    if kw is not None and dk_weight is None:
+        dk_weight = _empty((d,), torch.float32, dev, stream)
+    need = 0
+    if workspace is None and (qw is not None or kw is not None):
+        need = qk_norm_rope_bwd_workspace_size(d)
+    qp, qs = _strided("q", q, qshape, types, dev)
+    kp, ks = _strided("k", k, kshape, types, dev)
+    dqp, dqs = _strided("dq", dq, qshape, types, dev)
+    dkp, dks = _strided("dk", dk, kshape, types, dev)
+    for name, t, strides in (("dq", dq, dqs), ("dk", dk, dks)):
+        if strides is not None and _shares_places(t.shape, strides):
+            raise ValueError(f"{name}: elements share a place")
+    wp = wn = 0
+    if workspace is not None or need:
+        workspace, wp, wn = _workspace(workspace, need, dev, stream)
+    _run(dev, load_library().csattn_qk_norm_rope_bwd,
+         _ptr("dq_out", dq_out, qshape, types, dev), _ptr("dk_out", dk_out, kshape, types, dev),
+         qp, kp, qw, kw, pos, dqp, dkp,
+         None if qw is None else _ptr("dq_weight", dq_weight, (d,), _F32, dev),
+         None if kw is None else _ptr("dk_weight", dk_weight, (d,), _F32, dev), B, Hq, kshape[1],
+         T, d, CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
+         None if qs is ks is dqs is dks is None else
+         _strides((qs, ks, dqs, dks), qshape, kshape, qshape, kshape), pos0, 1 if norm else 0, eps,
+         rope_base, _ROPE_LAYOUT[rope_layout], wp, wn, _handle(dev, stream))
+    return dq, dk, dq_weight, dk_weight
+
+
+@functools.lru_cache(maxsize=1024)
+def _shares_places(shape, strides) -> bool:
+    """Whether two elements of a strided tensor of contiguous last dimension may share a place: a
+    dimension's stride is less than what the smaller ones span."""
+    span = shape[-1]
+    for stride, n in sorted(zip(strides, shape[:-1])):
+        if n > 1:
+            if stride < span:
+                return True
+            span = stride * (n - 1) + span
+    return False
+
+
 def check_status(stream=None) -> None:
     """Synchronize the stream and raise if a kernel reported a timeout or a device-side error."""
     _check(load_library().csattn_check_status(_stream_handle(stream)))
@@ -1042,6 +1434,6 @@ def selftest_bounded_wait(limit_us: int, stream=None) -> None:
 
 
 def selftest_lost_arrival() -> None:
-    """The thread's next 8-bit decode or tree step runs into its wait limit (see
+    """The thread's next 8-bit or 4-bit decode or tree step runs into its wait limit (see
     csattn_selftest_lost_arrival)."""
     _check(load_library().csattn_selftest_lost_arrival())

@@ -1,4 +1,4 @@
-// C ABI of the 8-bit KV cache and of the token-tree calls: argument checks, split sizes,
+// C ABI of the 8-bit and 4-bit KV caches and of the token-tree calls: argument checks, split sizes,
 // workspace layout and dispatch.  See include/csattn.h for the contract of every entry point.
 #include <algorithm>
 #include <cmath>
@@ -125,7 +125,8 @@ int check_heads(const char* fn, int B, int Hq, int Hkv, int T, float scale, int 
 // being read once per 16 rows here).
 constexpr int kTcRows = 16;
 
-GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, bool f8, int max_seq_len,
+// cache: the element's bits, 16, 8 or 4 (then launch_decode_fp4).
+GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, int cache, int max_seq_len,
                    int num_splits) {
   GroupPlan p{};
   p.tc = tc;
@@ -150,7 +151,9 @@ GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, bool f8, int max_se
     p.least_tiles = tc ? 1 : 2;
     const long long tiles = (max_seq_len + p.unit - 1) / p.unit;
     const long long line = tiles * B * Hkv * p.rblocks;
-    const int resident = kSms * (tc ? 1 : group_attn_ctas(d, f8, p.block_rows));
+    const int resident = kSms * (tc           ? 1
+                                 : cache == 4 ? decode_fp4_ctas(d, p.block_rows)
+                                              : group_attn_ctas(d, cache == 8, p.block_rows));
     p.most_grid = p.grid = static_cast<int>(
         std::min<long long>(resident, (line + p.least_tiles - 1) / p.least_tiles));
   }
@@ -269,7 +272,7 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
     return rc;
   if ((rc = check_rope(fn, rope_base, rope_layout, max_seq_len, d)) != CSATTN_OK) return rc;
   GroupArgs a{};
-  a.plan = plan_for(B, Hkv, Hq / Hkv, d, false, true, max_seq_len, num_splits);
+  a.plan = plan_for(B, Hkv, Hq / Hkv, d, false, 8, max_seq_len, num_splits);
   if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
   const size_t partials = partial_bytes(a.plan, B, Hkv, d);
   if ((rc = check_workspace(fn, workspace, workspace_bytes,
@@ -301,6 +304,114 @@ int decode_fp8(const char* fn, const void* q, const KvCache& c, const int32_t* s
   return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "attn_decode_fp8: merge launch");
 }
 
+// (the rows of four or eight scale bytes are read as words)
+int check_fp4(const char* fn, const KvCache& c, const int32_t* lens, int B, int Hkv, int d) {
+  const int rc = check_cache(fn, c, true, lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (!aligned(c.k_scale, 16) || !aligned(c.v_scale, 16))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned scales", fn);
+  return CSATTN_OK;
+}
+
+int append_fp4(const char* fn, const void* k_new, const void* v_new, const KvCache& c,
+               const int32_t* cache_lens, int B, int Hkv, int Tn, int d, int dtype, void* stream) {
+  int rc = check_fp4(fn, c, cache_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (k_new == nullptr || v_new == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(k_new, 16) || !aligned(v_new, 16))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
+  if (Tn < 1 || Tn > c.Lmax)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Tn=%d not in [1, cache rows %d]", fn, Tn, c.Lmax);
+  if (static_cast<long long>(B) * Hkv * Tn * d >= (1LL << 33))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Tn=%d too large", fn, Tn);
+  Fp4AppendArgs a{};
+  a.k_new = k_new;
+  a.v_new = v_new;
+  const long long strides[3] = {d, static_cast<long long>(Tn) * d,
+                                static_cast<long long>(Hkv) * Tn * d};
+  std::copy(strides, strides + 3, a.k_strides);
+  std::copy(strides, strides + 3, a.v_strides);
+  a.cache = c;
+  a.cache_lens = cache_lens;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.Tn = Tn;
+  a.d = d;
+  int sms = 0;
+  if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
+  const cudaError_t e = launch_cache_append_fp4(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "cache_append_fp4: kernel launch");
+}
+
+int read_fp4(const char* fn, const KvCache& c, const int32_t* seq_lens, void* k_out, void* v_out,
+             int B, int Hkv, int Lout, int d, int dtype, void* stream) {
+  int rc = check_fp4(fn, c, seq_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (k_out == nullptr || v_out == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(k_out, 16) || !aligned(v_out, 16))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
+  if (Lout < 1) return api_fail(CSATTN_ERR_INVALID_ARG, "%s: Lout=%d must be >= 1", fn, Lout);
+  if (Lout >= (1 << 24) || static_cast<long long>(B) * Hkv * Lout >= (1LL << 33))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: Lout=%d too large", fn, Lout);
+  if (static_cast<long long>(B) * Hkv >= (1LL << 30))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: B=%d * Hkv=%d too large", fn, B, Hkv);
+  uint32_t* status = nullptr;
+  int sms = 0;
+  if ((rc = api_device_info(&status, &sms)) != CSATTN_OK) return rc;
+  const cudaError_t e = launch_cache_read_fp4(c, seq_lens, k_out, v_out, B, Hkv, Lout, d, status,
+                                              static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "cache_read_fp4: kernel launch");
+}
+
+int decode_fp4(const char* fn, const void* q, const KvCache& c, const int32_t* seq_lens, void* out,
+               int B, int Hq, int Hkv, int d, int dtype, float scale, int max_seq_len,
+               int num_splits, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_fp4(fn, c, seq_lens, B, Hkv, d);
+  if (rc != CSATTN_OK) return rc;
+  if (q == nullptr || out == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
+  if ((rc = check_heads(fn, B, Hq, Hkv, 1, scale, max_seq_len, c.Lmax, num_splits)) != CSATTN_OK)
+    return rc;
+  GroupArgs a{};
+  a.plan = plan_for(B, Hkv, Hq / Hkv, d, false, 4, max_seq_len, num_splits);
+  if ((rc = check_line(fn, a.plan, B, Hkv, max_seq_len)) != CSATTN_OK) return rc;
+  const size_t partials = partial_bytes(a.plan, B, Hkv, d);
+  if ((rc = check_workspace(fn, workspace, workspace_bytes,
+                            align256(partials) + seg_bytes(a.plan, B, Hkv))) != CSATTN_OK)
+    return rc;
+  a.cache = c;
+  a.q = q;
+  a.lens = seq_lens;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.T = 1;
+  a.d = d;
+  a.scale = scale > 0.f ? scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+  a.max_seq_len = max_seq_len;
+  a.min_len = 0;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + partial_floats(a.plan, B, Hkv) * d;
+  a.seg = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + align256(partials));
+  int sms = 0;
+  if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
+  if ((rc = encoder_ready(fn)) != CSATTN_OK) return rc;
+  a.lost = take_lost();
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_decode_fp4(a, st);
+  if (e != cudaSuccess) return api_fail_cuda(e, "attn_decode_fp4: kernel launch");
+  a.cache.k_scale = a.cache.v_scale = nullptr;  // (partial results as over a bf16 cache)
+  e = launch_group_merge(a, nullptr, nullptr, out, nullptr, st);
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "attn_decode_fp4: merge launch");
+}
+
 // Workspace of a tree step: partials, then rotated queries, masks, lengths and value flags.
 struct TreeSpace {
   size_t seg, q_rot, q_factor, anc, lens, vflag, total;
@@ -319,7 +430,7 @@ struct TreeSpace {
 GroupPlan tree_plan(int B, int Hq, int Hkv, int Tn, int d, bool f8, int max_seq_len,
                     int num_splits) {
   const int rows = Tn * (Hq / Hkv);
-  return plan_for(B, Hkv, rows, d, rows > kTcRows, f8, max_seq_len, num_splits);
+  return plan_for(B, Hkv, rows, d, rows > kTcRows, f8 ? 8 : 16, max_seq_len, num_splits);
 }
 
 int tree_step(const char* fn, const void* q_new, const void* k_new, const void* v_new,
@@ -513,7 +624,7 @@ int csattn_cache_read_fp8_paged(const void* k_pages, const void* v_pages, const 
 
 size_t csattn_decode_fp8_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
   if (!sizes_ok(B, Hq, Hkv, 1, Lmax, d, num_splits)) return 0;
-  const GroupPlan p = plan_for(B, Hkv, Hq / Hkv, d, false, true, Lmax, num_splits);
+  const GroupPlan p = plan_for(B, Hkv, Hq / Hkv, d, false, 8, Lmax, num_splits);
   return align256(partial_bytes(p, B, Hkv, d)) + seg_bytes(p, B, Hkv);
 }
 
@@ -607,6 +718,130 @@ int csattn_tree_commit_paged(void* k_pages, void* v_pages, void* k_scale, void* 
                      paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
                            num_pages, max_pages),
                      cache_lens, parents, accepted, new_lens, B, Hkv, Tn, d, cache_dtype, stream);
+}
+
+int csattn_cache_append_fp4(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                            void* k_scale, void* v_scale, const int32_t* cache_lens, int B,
+                            int Hkv, int Tn, int Lmax, int d, int dtype, void* stream) {
+  return append_fp4("cache_append_fp4", k_new, v_new,
+                    contiguous(k_cache, v_cache, k_scale, v_scale, Lmax), cache_lens, B, Hkv, Tn,
+                    d, dtype, stream);
+}
+
+int csattn_cache_append_fp4_paged(const void* k_new, const void* v_new, void* k_pages,
+                                  void* v_pages, void* k_scale, void* v_scale,
+                                  const int32_t* block_table, const int32_t* cache_lens, int B,
+                                  int Hkv, int Tn, int page_size, int num_pages, int max_pages,
+                                  int d, int dtype, void* stream) {
+  const char* fn = "cache_append_fp4_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return append_fp4(fn, k_new, v_new,
+                    paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                          num_pages, max_pages),
+                    cache_lens, B, Hkv, Tn, d, dtype, stream);
+}
+
+int csattn_cache_append_fp4_slots(const void* k_new, const void* v_new, const int64_t* strides,
+                                  void* k_pages, void* v_pages, void* k_scale, void* v_scale,
+                                  const int64_t* slots, int N, int Hkv, int page_size,
+                                  int num_pages, int d, int dtype, void* stream) {
+  const char* fn = "cache_append_fp4_slots";
+  int lmax = 0;
+  // (slots stand in the lengths' and the table's place in the checks that the calls share)
+  if (slots == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  const int32_t* some = reinterpret_cast<const int32_t*>(slots);
+  int rc = check_pages(fn, some, Hkv, page_size, num_pages, 1, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  Fp4AppendArgs a{};
+  a.cache = paged(k_pages, v_pages, k_scale, v_scale, nullptr, lmax, page_size, num_pages, 1);
+  if ((rc = check_fp4(fn, a.cache, some, 1, Hkv, d)) != CSATTN_OK) return rc;
+  if (k_new == nullptr || v_new == nullptr)
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8))
+    return api_fail(CSATTN_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if ((rc = check_dtype(fn, dtype)) != CSATTN_OK) return rc;
+  if (N < 1) return api_fail(CSATTN_ERR_INVALID_ARG, "%s: N=%d must be >= 1", fn, N);
+  if (static_cast<long long>(N) * Hkv * d >= (1LL << 33))
+    return api_fail(CSATTN_ERR_UNSUPPORTED, "%s: N=%d too large", fn, N);
+  a.k_new = k_new;
+  a.v_new = v_new;
+  for (int i = 0; i < 2; ++i) {
+    const long long dense = i == 0 ? static_cast<long long>(Hkv) * d : d;
+    a.k_strides[i] = strides != nullptr ? strides[i] : dense;
+    a.v_strides[i] = strides != nullptr ? strides[2 + i] : dense;
+    for (const long long x : {a.k_strides[i], a.v_strides[i]})
+      if ((i == 0 ? N : Hkv) > 1 && (x < 0 || x % 8 != 0 || x >= (1LL << 40)))
+        return api_fail(CSATTN_ERR_INVALID_ARG,
+                        "%s: a stride of %lld elements (8 of them are read at once)", fn, x);
+  }
+  a.slots = slots;
+  a.B = 1;
+  a.Hkv = Hkv;
+  a.Tn = N;
+  a.d = d;
+  int sms = 0;
+  if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
+  const cudaError_t e = launch_cache_append_fp4(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSATTN_OK : api_fail_cuda(e, "cache_append_fp4_slots: kernel launch");
+}
+
+int csattn_cache_read_fp4(const void* k_cache, const void* v_cache, const void* k_scale,
+                          const void* v_scale, const int32_t* seq_lens, void* k_out, void* v_out,
+                          int B, int Hkv, int Lmax, int Lout, int d, int dtype, void* stream) {
+  return read_fp4("cache_read_fp4", contiguous(k_cache, v_cache, k_scale, v_scale, Lmax), seq_lens,
+                  k_out, v_out, B, Hkv, Lout, d, dtype, stream);
+}
+
+int csattn_cache_read_fp4_paged(const void* k_pages, const void* v_pages, const void* k_scale,
+                                const void* v_scale, const int32_t* block_table,
+                                const int32_t* seq_lens, void* k_out, void* v_out, int B, int Hkv,
+                                int page_size, int num_pages, int max_pages, int Lout, int d,
+                                int dtype, void* stream) {
+  const char* fn = "cache_read_fp4_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return read_fp4(fn,
+                  paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                        num_pages, max_pages),
+                  seq_lens, k_out, v_out, B, Hkv, Lout, d, dtype, stream);
+}
+
+size_t csattn_decode_fp4_workspace_size(int B, int Hq, int Hkv, int Lmax, int d, int num_splits) {
+  if (!sizes_ok(B, Hq, Hkv, 1, Lmax, d, num_splits)) return 0;
+  const GroupPlan p = plan_for(B, Hkv, Hq / Hkv, d, false, 4, Lmax, num_splits);
+  return align256(partial_bytes(p, B, Hkv, d)) + seg_bytes(p, B, Hkv);
+}
+
+int csattn_attn_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
+                           const void* k_scale, const void* v_scale, const int32_t* seq_lens,
+                           void* out, int B, int Hq, int Hkv, int Lmax, int d, int dtype,
+                           float scale, int max_seq_len, int num_splits, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  return decode_fp4("attn_decode_fp4", q, contiguous(k_cache, v_cache, k_scale, v_scale, Lmax),
+                    seq_lens, out, B, Hq, Hkv, d, dtype, scale, max_seq_len, num_splits, workspace,
+                    workspace_bytes, stream);
+}
+
+int csattn_attn_decode_fp4_paged(const void* q, const void* k_pages, const void* v_pages,
+                                 const void* k_scale, const void* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                 int B, int Hq, int Hkv, int page_size, int num_pages,
+                                 int max_pages, int d, int dtype, float scale, int max_seq_len,
+                                 int num_splits, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const char* fn = "attn_decode_fp4_paged";
+  int lmax = 0;
+  const int rc = check_pages(fn, block_table, Hkv, page_size, num_pages, max_pages, &lmax);
+  if (rc != CSATTN_OK) return rc;
+  return decode_fp4(fn, q,
+                    paged(k_pages, v_pages, k_scale, v_scale, block_table, lmax, page_size,
+                          num_pages, max_pages),
+                    seq_lens, out, B, Hq, Hkv, d, dtype, scale, max_seq_len, num_splits, workspace,
+                    workspace_bytes, stream);
 }
 
 int csattn_selftest_lost_arrival(void) {

@@ -1,0 +1,629 @@
+// Decode over a 4-bit cache (fp4.cuh): one new query per sequence and head.
+//
+// out = softmax(q K^T scale) V with K and V in e2m1 times a scale per 16 channels.  All Hq / Hkv
+// query rows of a KV head read the same cache rows, so they are one side of a matrix product and
+// a row is read from HBM and taken to f16 once for 8 * NT of them.  A CTA:
+//   warp 4      producer: KT-row K and V tiles and their scale bytes into a ring by TMA, and a
+//               piece's queries, as f16, ahead of its other tiles
+//   warps 0..3  KT / 4 cache rows each per tile, by mma.sync m16n8k16 with the cache rows (then
+//               the channels) on the side of 16 and the query rows on the side of 8:
+//               S^T = K Q^T, then O^T += V^T P^T, softmax statistics in fp32 between the two;
+//               each leaves a partial result of its own per piece.
+// CTAs, a wave of them, take equal ranges of all the tiles (group_work.cuh); the partial results
+// are merged by group_merge_kernel.
+//
+// The operands: K and V enter as x4 * s, which f16 holds exactly (one conversion and one product
+// for two of them); q is taken to f16 by a power of two per row (query_to_f16: 11 bits, and
+// channels below 2^-38 of the largest vanish); the weights are 2^(x - m) with m = the running
+// maximum - 7, rounded to f16 (11 bits; what is below 2^-32 of the largest vanishes).  Sums are
+// fp32 throughout.  The maximum is raised only when a score exceeds it by 2^8, and only then do
+// the lanes exchange theirs.
+//
+// The index of a product's sum may run over the channels (the rows) in any order that both sides
+// share, and its rows may be any 16 cache rows.  So a lane takes a row's channels as whole words
+// of the cache: for S^T lane (g, j) the j-th quarter of row perm(g), for O^T the g-th eighth of
+// rows perm(2j), perm(2j + 1); there two rows' nibbles are paired in the words before they are
+// taken apart, four instructions for 16 values.  perm keeps both kinds of loads free of bank
+// conflicts: any two neighbours differ in parity, as do the lanes' rows of a load.
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "group_work.cuh"
+#include "internal.h"
+
+namespace csattn {
+namespace {
+
+constexpr int KT = 64;  // cache rows per tile
+constexpr int NW = 4;   // compute warps
+constexpr int RG = KT / (16 * NW);  // groups of 16 rows per warp and tile
+constexpr int kThreads = 32 * (NW + 1);
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 100000000ull;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kWeightLog2 = 7.0f;  // weights are at most 2^(8 + 7) < 65504
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int ROW = D / 2;
+  static constexpr int SROW = D / 16;  // scale bytes of a row
+  static constexpr int TILE = KT * ROW;
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int CODES = 2 * KT * SROW;       // keys' scales, values' scales
+  static constexpr int ROWS = 8 * NT;               // query rows of a CTA
+  static constexpr int QS = 2 * D + 16;             // bytes between query rows
+  static constexpr int CTAS = decode_fp4_ctas(D, ROWS);
+  static constexpr int NS = D == 128 ? 6 : 8;
+  static constexpr int RING = NS * STAGE;
+  static constexpr int Q_BYTES = ROWS * QS;         // twice: the next piece's go to the other
+  static constexpr int BARS = 192;
+  static constexpr int SMEM = 1024 + RING + NS * CODES + 2 * Q_BYTES + BARS + 2 * ROWS * 4;
+  static_assert(8 * (2 * NS + 4) + 4 <= BARS, "barriers");
+};
+
+struct Params {
+  const __nv_bfloat16* q;
+  GroupLine line;
+  CacheRows rows;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  int lost;          // arrivals that the queries' barrier waits for and nothing makes (selftest)
+  int box_rows;
+  bool code_copies;  // scale bytes lie so that bulk copies can take them
+  float* part_o;
+  float* part_ml;
+  uint32_t* status;
+  int rep, rblocks, part_rows;
+  float scale_log2;
+};
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// max over the eight lanes that hold one query row's column
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+// The cache row (of eight) that fragment row m stands for.  128 channels: rows of 64 bytes, whose
+// four chunks TMA's 64-byte swizzle permutes by (row / 2) % 4.  The quarters of rows perm(2p) and
+// perm(2p + 1), loaded together, cover all banks as one row is even and one odd; the eighths 0..3
+// of rows perm(0), perm(2), .. = 0 3 4 7 do, as their chunks are {0,1} ^ row / 2.
+// 64 channels: rows of 32 bytes, not swizzled; loaded together are rows that differ modulo 4.
+template <int D>
+__device__ __forceinline__ int perm(int m) {
+  if constexpr (D == 128) return m ^ ((m >> 1) & 1);
+  // 0 2 1 3 6 4 7 5
+  return (0x57463120u >> (4 * m)) & 7u;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
+    decode_fp4_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v) {
+  using C = Cfg<D, NT>;
+  constexpr int NS = C::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* s_codes = smem + C::RING;
+  uint8_t* s_q = s_codes + NS * C::CODES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_q + 2 * C::Q_BYTES);
+  uint64_t* empty = full + NS;
+  uint64_t* q_full = empty + NS;   // [2]: a piece's queries in buffer piece % 2
+  uint64_t* q_empty = q_full + 2;  // [2]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(q_empty + 2);
+  float* s_qf = reinterpret_cast<float*>(s_q + 2 * C::Q_BYTES + C::BARS);  // [2][ROWS]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // let the merge be scheduled once every CTA has started; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], p.code_copies ? 1 : 2);
+      mbar_init(&empty[s], NW);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1 + p.lost);
+      mbar_init(&q_empty[i], NW);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  GroupPiece pc = group_start(p.line, p.status, false);
+  if (pc.n == 0) return;
+  __syncthreads();
+
+  if (warp == NW) {
+    // ------------------------------------------------------------ producer
+    // lane i copies box i of a tile (paged: boxes of box_rows rows never cross a page; a
+    // box past the sequence, or a page index outside the pool, which is reported, reads
+    // zeros: its plane is past the tensor map).  Lane 0 waits and arms the stage first.
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    // (the kernel before may have written the cache's rows by plain stores)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    const uint64_t once = evict_first_policy();
+    const CacheRows& R = p.rows;
+    const int nbox = KT / p.box_rows, r0 = lane * p.box_rows;
+    int issued = 0;
+    // The queries of a piece: D/16 lanes per row, 16 channels each, read ahead of the piece's
+    // first tile and staged behind it.
+    constexpr int G = D / 16, PASSES = C::ROWS * G / 32;
+    const int qc = lane % G;
+    uint4 q_lo[PASSES], q_hi[PASSES];
+    auto load_queries = [&](const GroupPiece& pc) {
+      const int kvh = pc.head / p.rblocks;
+      const int row0 = (pc.head - kvh * p.rblocks) * C::ROWS + lane / G;
+      const size_t at = (static_cast<size_t>(pc.b) * R.Hkv + kvh) * p.rep + row0;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        q_lo[i] = q_hi[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row0 + 32 / G * i < p.rep) {
+          const uint4* src =
+              reinterpret_cast<const uint4*>(p.q + (at + 32 / G * i) * D + 16 * qc);
+          q_lo[i] = src[0];
+          q_hi[i] = src[1];
+        }
+      }
+    };
+    auto stage_queries = [&](int piece) {
+      const int buf = piece & 1;
+      bool room = true;
+      if (piece >= 2 && lane == 0)
+        room = ctl_wait(&q_empty[buf], ((piece >> 1) - 1) & 1, abort_flag, p.status, kWaitNs);
+      if (!__all_sync(0xffffffffu, room)) return false;
+      const float none[8] = {};
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = 32 / G * i + lane / G;
+        uint8_t* dst = s_q + buf * C::Q_BYTES + r * C::QS + 32 * qc;
+        const float factor = query_to_f16<G>(q_lo[i], q_hi[i], 0, none, none);
+        if (qc == 0) s_qf[buf * C::ROWS + r] = factor * p.scale_log2;
+        *reinterpret_cast<uint4*>(dst) = q_lo[i];
+        *reinterpret_cast<uint4*>(dst + 16) = q_hi[i];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[buf]);
+      return true;
+    };
+    bool ok = true;
+    for (int piece = 0; pc.n > 0 && ok; pc.next(p.line), ++piece) {
+      const int b = pc.b, kvh = pc.head / p.rblocks, total = pc.L;
+      // the queries behind as many tiles as find room at once: the ring, or (it is full of the
+      // last piece's) one
+      const int q_at = min(pc.n, piece == 0 && p.code_copies ? NS : 1) - 1;
+      load_queries(pc);
+      for (int t = 0; t < pc.n; ++t) {
+        const int s = issued % NS, use = issued / NS, row0 = (pc.t0 + t) * KT;
+        uint8_t* codes = s_codes + s * C::CODES;
+        int plane = b * R.Hkv + kvh, prow = row0;
+        int code_rows = min(KT, R.Lmax - row0);  // rows of the lane's box whose scales are copied
+        bool lost = false;                       // its page is outside the pool
+        if (R.block_table != nullptr) {
+          const int tr = row0 + r0;
+          plane = R.num_pages * R.Hkv;
+          prow = 0;
+          code_rows = 0;
+          if (lane < nbox && tr < total) {
+            const int page =
+                R.block_table[static_cast<size_t>(b) * R.max_pages + tr / R.page_size];
+            lost = page < 0 || page >= R.num_pages;
+            if (!lost) {
+              plane = page * R.Hkv + kvh;
+              code_rows = p.box_rows;
+            } else {
+              atomicOr(p.status, kStatusDeviceArg);
+            }
+            prow = tr % R.page_size;
+          }
+        }
+        if (lane >= nbox) code_rows = 0;
+        bool room = true;
+        if (lane == 0 && use > 0)
+          room = ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs);
+        if (!__all_sync(0xffffffffu, room)) {
+          ok = false;
+          break;
+        }
+        uint32_t bytes = C::STAGE;
+        if (lost && p.code_copies) {  // the rows read as zeros: their scales have to be numbers
+          for (int i = 0; i < p.box_rows * C::SROW; i += 16) {
+            *reinterpret_cast<uint4*>(codes + r0 * C::SROW + i) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(codes + (KT + r0) * C::SROW + i) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        if (p.code_copies)
+          bytes += 2 * C::SROW * __reduce_add_sync(0xffffffffu, static_cast<unsigned>(code_rows));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+        __syncwarp();
+        if (lane < nbox) {
+          uint8_t* kd = smem + s * C::STAGE + r0 * C::ROW;
+          tma_load_3d_once(kd, &tm_k, &full[s], 0, prow, plane, once);
+          tma_load_3d_once(kd + C::TILE, &tm_v, &full[s], 0, prow, plane, once);
+          if (p.code_copies && code_rows > 0) {
+            const size_t at =
+                static_cast<size_t>(plane) * (R.block_table != nullptr ? R.page_size : R.Lmax) +
+                prow;
+            bulk_load(codes + r0 * C::SROW, p.k_scale + at * C::SROW, code_rows * C::SROW,
+                      &full[s]);
+            bulk_load(codes + (KT + r0) * C::SROW, p.v_scale + at * C::SROW, code_rows * C::SROW,
+                      &full[s]);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (t == q_at) ok = stage_queries(piece);
+        if (!p.code_copies) {
+          // a row's scale bytes are a word of four or eight bytes
+          using Word = std::conditional_t<D == 128, uint2, uint32_t>;
+#pragma unroll
+          for (int i = 0; i < KT / 32; ++i) {
+            const int r = lane + 32 * i;
+            const long long at = row0 + r < total ? R.at(b, kvh, row0 + r) : -1;
+            Word kw{}, vw{};
+            if (at >= 0) {
+              kw = *reinterpret_cast<const Word*>(p.k_scale + at * C::SROW);
+              vw = *reinterpret_cast<const Word*>(p.v_scale + at * C::SROW);
+            }
+            *reinterpret_cast<Word*>(codes + r * C::SROW) = kw;
+            *reinterpret_cast<Word*>(codes + (KT + r) * C::SROW) = vw;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
+        if (!ok) break;
+      }
+    }
+    if (lane == 0 && *abort_flag) {
+      const int first = issued > NS ? issued - NS : 0;
+      for (int t = first; t < issued; ++t)
+        mbar_wait(&full[t % NS], (t / NS) & 1, nullptr, p.status, kDrainNs);
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- compute warps
+  constexpr int KW = D / 32;  // words of a row that a lane has for S^T (a quarter)
+  constexpr int VW = D / 64;  // for O^T (an eighth)
+  const int g = lane >> 2, j = lane & 3;
+  const int cq = 2 * j;  // fragment columns cq and cq + 1 (query rows)
+  const uint32_t smem_base = smem_u32(smem), codes_base = smem_u32(s_codes);
+  const int wrow = 16 * RG * warp;  // first row of the warp in a tile
+  // a lane's byte offsets within a tile, for the first 16 rows
+  const int kr = wrow + perm<D>(g);
+  const int va = wrow + perm<D>(2 * j), vb = wrow + perm<D>(2 * j + 1);
+  auto chunk = [](int row, int byte) {
+    return D == 128 ? row * 64 + (byte ^ (((row >> 1) & 3) << 4)) : row * 32 + byte;
+  };
+  const uint32_t k_off = chunk(kr, 4 * KW * j);
+  const uint32_t va_off = chunk(va, 4 * VW * g), vb_off = chunk(vb, 4 * VW * g);
+  const uint32_t ks_off = kr * C::SROW + (D / 64) * j;
+  const uint32_t vs_col = (KT * C::SROW) + (D == 128 ? g : g >> 1);
+  bool ok = true;
+  int used = 0;  // tiles of the CTA so far
+  for (int piece = 0; pc.n > 0; pc.next(p.line), ++piece) {
+    const int kvh = pc.head / p.rblocks;
+    const int row_base = (pc.head - kvh * p.rblocks) * C::ROWS;  // first query row
+    const int k_begin = pc.t0 * KT, ntiles = pc.n;
+    const int k_end = min(pc.L, k_begin + ntiles * KT);
+
+    ok = __all_sync(0xffffffffu, mbar_wait(&q_full[piece & 1], (piece >> 1) & 1, abort_flag,
+                                           p.status, kWaitNs));
+    if (!ok) break;
+    // the lane's quarter of its query row, in pairs of channels
+    uint32_t qb[NT][D / 8];
+    float qf[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t q_addr =
+          smem_u32(s_q) + (piece & 1) * C::Q_BYTES + (8 * n + g) * C::QS + (D / 2) * j;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t w[4];
+        lds<4>(q_addr + 16 * i, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qb[n][4 * i + e] = w[e];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) qf[n][h] = s_qf[(piece & 1) * C::ROWS + 8 * n + cq + h];
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_empty[piece & 1]);
+
+    float o[D / 16][NT][4];
+    float m_ref[NT][2], l_part[NT][2];  // m_ref: the maximum - kWeightLog2
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[c][n][0] = o[c][n][1] = o[c][n][2] = o[c][n][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) m_ref[n][h] = -INFINITY, l_part[n][h] = 0.f;
+    }
+
+    bool unset = true;  // some query row has no maximum yet
+    for (int t = 0; t < ntiles && ok; ++t, ++used) {
+      const int s = used % NS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (used / NS) & 1, abort_flag, p.status,
+                                             kWaitNs))) {
+        ok = false;
+        break;
+      }
+      const uint32_t kbase = smem_base + s * C::STAGE, vbase = kbase + C::TILE;
+      const uint32_t cbase = codes_base + s * C::CODES;
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg) {
+        const int key0 = k_begin + t * KT + wrow + 16 * rg;  // first cache row of the group
+        // S^T: rows perm(g) and perm(g) + 8
+        uint32_t ka[KW], kb[KW];
+        lds<KW>(kbase + k_off + (16 * rg) * C::ROW, ka);
+        lds<KW>(kbase + k_off + (16 * rg + 8) * C::ROW, kb);
+        uint32_t sa[D / 64], sb[D / 64];
+        if constexpr (D == 128) {
+          const uint32_t x = lds_u16(cbase + ks_off + (16 * rg) * C::SROW);
+          const uint32_t y = lds_u16(cbase + ks_off + (16 * rg + 8) * C::SROW);
+          sa[0] = (x & 0xffu) * 0x00800080u;
+          sa[1] = (x >> 8) * 0x00800080u;
+          sb[0] = (y & 0xffu) * 0x00800080u;
+          sb[1] = (y >> 8) * 0x00800080u;
+        } else {
+          sa[0] = lds_u8(cbase + ks_off + (16 * rg) * C::SROW) * 0x00800080u;
+          sb[0] = lds_u8(cbase + ks_off + (16 * rg + 8) * C::SROW) * 0x00800080u;
+        }
+        float sc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {  // a word: eight channels, two steps of the sum
+          const uint32_t fa = sa[w / 2], fb = sb[w / 2];
+          const uint32_t a0 = mul_f16x2(e2m1x2_to_f16x2<0>(ka[w]), fa);
+          const uint32_t a1 = mul_f16x2(e2m1x2_to_f16x2<0>(kb[w]), fb);
+          const uint32_t a2 = mul_f16x2(e2m1x2_to_f16x2<1>(ka[w]), fa);
+          const uint32_t a3 = mul_f16x2(e2m1x2_to_f16x2<1>(kb[w]), fb);
+          const uint32_t c0 = mul_f16x2(e2m1x2_to_f16x2<2>(ka[w]), fa);
+          const uint32_t c1 = mul_f16x2(e2m1x2_to_f16x2<2>(kb[w]), fb);
+          const uint32_t c2 = mul_f16x2(e2m1x2_to_f16x2<3>(ka[w]), fa);
+          const uint32_t c3 = mul_f16x2(e2m1x2_to_f16x2<3>(kb[w]), fb);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma(sc[n], a0, a1, a2, a3, qb[n][4 * w], qb[n][4 * w + 1]);
+            mma(sc[n], c0, c1, c2, c3, qb[n][4 * w + 2], qb[n][4 * w + 3]);
+          }
+        }
+        // rows past the sequence: their scores become -inf
+        const bool edge = key0 + 16 > k_end;
+        const bool out0 = key0 + perm<D>(g) >= k_end, out1 = key0 + perm<D>(g) + 8 >= k_end;
+        // x - m_ref for every score (x rounded by itself, as in the maximum); where one exceeds
+        // the maximum by the threshold (or there is none yet) the maxima are raised first
+        float d[NT][4];
+        bool over = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[n][e] = __fmul_rn(sc[n][e], qf[n][e & 1]);
+            if (edge && (e < 2 ? out0 : out1)) sc[n][e] = -INFINITY;
+            d[n][e] = sc[n][e] - m_ref[n][e & 1];
+            over |= d[n][e] > kRescaleThreshold + kWeightLog2;
+          }
+        if (__any_sync(0xffffffffu, over || unset)) {
+          unset = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float mx = column_max(fmaxf(sc[n][h], sc[n][2 + h])) - kWeightLog2;
+              if (mx > m_ref[n][h] + kRescaleThreshold) {
+                f[h] = ex2_approx(m_ref[n][h] - mx);  // 0 when m_ref was -inf
+                l_part[n][h] *= f[h];
+                m_ref[n][h] = mx;
+              }
+              // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
+              const float ref = m_ref[n][h] == -INFINITY ? 0.f : m_ref[n][h];
+              unset |= m_ref[n][h] == -INFINITY;
+              d[n][h] = sc[n][h] - ref;
+              d[n][2 + h] = sc[n][2 + h] - ref;
+            }
+            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                o[c][n][0] *= f[0];
+                o[c][n][1] *= f[1];
+                o[c][n][2] *= f[0];
+                o[c][n][3] *= f[1];
+              }
+            }
+          }
+          unset = __any_sync(0xffffffffu, unset);
+        }
+        // weights, turned to the layout of the second product
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = ex2_approx(d[n][e]);
+            l_part[n][e & 1] += w[e];
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            pb[n][i] = transpose8x8(pack_f16x2(w[2 * i], w[2 * i + 1]));
+        }
+        // O^T: rows perm(2j), perm(2j + 1) and eight further
+        uint32_t x[2][2][VW];  // [+8][row of the pair]
+        uint32_t sv[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          lds<VW>(vbase + va_off + (16 * rg + 8 * i) * C::ROW, x[i][0]);
+          lds<VW>(vbase + vb_off + (16 * rg + 8 * i) * C::ROW, x[i][1]);
+          uint32_t ua = lds_u8(cbase + vs_col + (va + 16 * rg + 8 * i) * C::SROW);
+          uint32_t ub = lds_u8(cbase + vs_col + (vb + 16 * rg + 8 * i) * C::SROW);
+          if (edge) {  // (a scale past the sequence may be a NaN)
+            if (key0 - wrow + va + 8 * i >= k_end) ua = 0u;
+            if (key0 - wrow + vb + 8 * i >= k_end) ub = 0u;
+          }
+          sv[i] = (ua | (ub << 16)) << 7;
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          // the rows' even channels, then their odd ones: byte b is channel 8w + 2b (+ 1)
+          uint32_t ev[2], od[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t u = x[i][0][w], v = x[i][1][w];
+            ev[i] = (u & 0x0f0f0f0fu) | ((v << 4) & 0xf0f0f0f0u);
+            od[i] = ((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u);
+          }
+          auto step = [&](int c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            a0 = mul_f16x2(a0, sv[0]);
+            a1 = mul_f16x2(a1, sv[0]);
+            a2 = mul_f16x2(a2, sv[1]);
+            a3 = mul_f16x2(a3, sv[1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma(o[c][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          };
+          step(4 * w, e2m1x2_to_f16x2<0>(ev[0]), e2m1x2_to_f16x2<0>(od[0]),
+               e2m1x2_to_f16x2<0>(ev[1]), e2m1x2_to_f16x2<0>(od[1]));
+          step(4 * w + 1, e2m1x2_to_f16x2<1>(ev[0]), e2m1x2_to_f16x2<1>(od[0]),
+               e2m1x2_to_f16x2<1>(ev[1]), e2m1x2_to_f16x2<1>(od[1]));
+          step(4 * w + 2, e2m1x2_to_f16x2<2>(ev[0]), e2m1x2_to_f16x2<2>(od[0]),
+               e2m1x2_to_f16x2<2>(ev[1]), e2m1x2_to_f16x2<2>(od[1]));
+          step(4 * w + 3, e2m1x2_to_f16x2<3>(ev[0]), e2m1x2_to_f16x2<3>(od[0]),
+               e2m1x2_to_f16x2<3>(ev[1]), e2m1x2_to_f16x2<3>(od[1]));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l_part[n][h] += __shfl_xor_sync(0xffffffffu, l_part[n][h], 4);
+        l_part[n][h] += __shfl_xor_sync(0xffffffffu, l_part[n][h], 8);
+        l_part[n][h] += __shfl_xor_sync(0xffffffffu, l_part[n][h], 16);
+      }
+    if (!ok) break;
+    if (threadIdx.x == 0) pc.leave_for_merge(p.line);
+    // The warp's partial result, relative to m_ref.
+    const size_t slot = (static_cast<size_t>(blockIdx.x) + pc.segment(p.line)) * NW + warp;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * n + cq + h;
+        if (row_base + r >= p.rep) continue;
+        const size_t at = slot * p.part_rows + r;
+        if (g == 0)
+          *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_ref[n][h], l_part[n][h]);
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + (D / 8) * g);
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 2)
+          dst[c / 2] = make_float4(o[c][n][h], o[c][n][2 + h], o[c + 1][n][h], o[c + 1][n][2 + h]);
+      }
+  }
+  // After a wait that ran out (otherwise n = 0): the merge, which follows whatever happened here,
+  // reads where a segment's results are, those of the segments that were not reached too.
+  if (threadIdx.x == 0)
+    for (; pc.n > 0; pc.next(p.line)) pc.leave_for_merge(p.line);
+}
+
+template <int D, int NT>
+cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, NT>;
+  Params p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.line = group_line(a);
+  p.rows = CacheRows{a.cache.block_table, a.Hkv, a.cache.Lmax, a.cache.page_size,
+                     a.cache.num_pages, a.cache.max_pages};
+  p.k_scale = static_cast<const uint8_t*>(a.cache.k_scale);
+  p.v_scale = static_cast<const uint8_t*>(a.cache.v_scale);
+  p.lost = a.lost;
+  const bool paged = a.cache.block_table != nullptr;
+  p.box_rows = KT;
+  if (paged && a.cache.page_size % KT != 0) p.box_rows = a.cache.page_size < 64 ? a.cache.page_size : 64;
+  // (the scales' base is 16-byte aligned, and so is every page's and tile's)
+  p.code_copies = paged || a.cache.Lmax * C::SROW % 16 == 0;
+  p.part_o = a.part_o;
+  p.part_ml = a.part_ml;
+  p.status = a.status;
+  p.rep = a.Hq / a.Hkv;
+  p.rblocks = a.plan.rblocks;
+  p.part_rows = a.plan.part_rows;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+
+  alignas(64) CUtensorMap tk, tv;
+  const int rows = paged ? a.cache.page_size : a.cache.Lmax;
+  const int planes = paged ? a.cache.num_pages * a.Hkv : a.B * a.Hkv;
+  if (!make_tmap_u8_3d(&tk, a.cache.k, C::ROW, rows, planes, p.box_rows, D == 128) ||
+      !make_tmap_u8_3d(&tv, a.cache.v, C::ROW, rows, planes, p.box_rows, D == 128))
+    return cudaErrorInvalidValue;
+  static SmemLimitOnce smem_limit;
+  cudaError_t e = smem_limit.set(decode_fp4_kernel<D, NT>, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.plan.grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_fp4_kernel<D, NT>, p, tk, tv);
+}
+
+template <int D>
+cudaError_t launch_rows(const GroupArgs& a, cudaStream_t stream) {
+  return a.plan.block_rows <= 8 ? launch_t<D, 1>(a, stream) : launch_t<D, 2>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp4(const GroupArgs& a, cudaStream_t stream) {
+  return a.d == 64 ? launch_rows<64>(a, stream) : launch_rows<128>(a, stream);
+}
+
+}  // namespace csattn

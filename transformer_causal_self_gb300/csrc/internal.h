@@ -197,6 +197,69 @@ cudaError_t launch_cache_read_fp8(const KvCache& cache, const int32_t* seq_lens,
                                   void* v_out, int B, int Hkv, int Lout, int d, uint32_t* status,
                                   cudaStream_t stream);
 
+// The same of a 4-bit cache (fp4.cuh; two channels per byte, a scale byte per 16 channels): keys
+// and values as given, to the rows behind cache_lens, or of pages to those that slots [Tn] name
+// (then B = 1; a negative slot: no row).  Strides of a token, a head and a sequence, in elements.
+struct Fp4AppendArgs {
+  const void* k_new;
+  const void* v_new;
+  long long k_strides[3], v_strides[3];
+  KvCache cache;
+  const int32_t* cache_lens;  // null: slots
+  const int64_t* slots;
+  int B, Hkv, Tn, d;
+  uint32_t* status;
+};
+cudaError_t launch_cache_append_fp4(const Fp4AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_read_fp4(const KvCache& cache, const int32_t* seq_lens, void* k_out,
+                                  void* v_out, int B, int Hkv, int Lout, int d, uint32_t* status,
+                                  cudaStream_t stream);
+
+// Block tables, slots and positions of a step's N new tokens (csattn_page_tables).
+struct PageTablesArgs {
+  const int32_t* held;   // [B] rows that a sequence has
+  const int32_t* fresh;  // [B] its new tokens
+  int32_t* block_table;  // [B, max_pages]
+  const int32_t* free_pages;
+  const int32_t* num_free;
+  int32_t* seq_lens;   // [B]
+  int32_t* starts;     // [B + 1]
+  int64_t* slots;      // [N]
+  int32_t* positions;  // [N]
+  int32_t* free_left;
+  int B, N, page_size, num_pages, max_pages, free_size;
+  uint32_t* status;
+};
+cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream);
+
+// RMS norm of heads and the rotation (csattn_qk_norm_rope), and its gradients.
+struct QkNormSide {  // the queries or the keys
+  const void* x;
+  long long batch, head, token;  // x's strides in elements
+  const void* w;  // gain [d], or null
+  void* y;        // [B, H, T, d]: written, or its gradient (backward)
+  void* dx;       // backward
+  long long dx_batch, dx_head, dx_token;
+  int H;
+  int span, groups;  // (set by the launchers)
+  unsigned items;
+};
+struct QkNormArgs {
+  QkNormSide q, k;
+  const int32_t* positions;  // [B, T], or null: pos0 + t
+  int B, T, d, pos0;
+  int norm;
+  float eps;
+  int rope;         // 0 none, 1 split-half, 2 adjacent
+  RopeTable turns;  // frequencies in quarter turns (rope_turns.cuh)
+  float* partial;   // [qk_norm_bwd_blocks() + 1, d] where gains have gradients, or null
+  uint32_t* status;
+  int q_blocks;     // (set by the launchers)
+};
+cudaError_t launch_qk_norm(QkNormArgs a, bool bf16, cudaStream_t stream);
+cudaError_t launch_qk_norm_bwd(QkNormArgs a, bool bf16, float* dqw, float* dkw,
+                               cudaStream_t stream);
+
 // How launch_group_attn or launch_group_tc shares out its work (group_work.cuh).
 struct GroupPlan {
   bool tc;             // launch_group_tc
@@ -268,6 +331,9 @@ constexpr int group_attn_ctas(int d, bool f8, int block_rows) {
   return f8 && !(d == 128 && block_rows > 8) ? 3 : 2;
 }
 cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
+// The same for one query per head over a 4-bit cache; drafts is 0 and q is used as given.
+constexpr int decode_fp4_ctas(int d, int block_rows) { return d == 128 && block_rows > 8 ? 2 : 3; }
+cudaError_t launch_decode_fp4(const GroupArgs& a, cudaStream_t stream);
 // The same on tcgen05, for many query rows; rope is 0.
 cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream);
 
@@ -325,6 +391,8 @@ constexpr int kMaxRopePositions = 49152;  // largest position whose angle reduct
 // SMs of a GB300, which waves of CTAs are cut for (a constant: workspace sizes depend on it, and are
 // asked for without a device)
 constexpr int kSms = 152;
+// blocks of the norm's backward pass (each leaves a sum of the gains' gradients)
+constexpr int qk_norm_bwd_blocks() { return 4 * kSms; }
 
 // Raises a kernel's dynamic shared-memory limit once per device (the attribute
 // lasts for the process), so repeated launches skip the driver call.
