@@ -34,17 +34,16 @@
 namespace csattn {
 namespace {
 
-constexpr int KT = 64;  // cache rows per tile
-constexpr int NW = 4;   // compute warps
-constexpr int RG = KT / (16 * NW);  // groups of 16 rows per warp and tile
+constexpr int NW = 4;  // compute warps, RG groups of 16 rows of a tile each
 constexpr int kThreads = 32 * (NW + 1);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kWeightLog2 = 7.0f;  // weights are at most 2^(8 + 7) < 65504
 
-template <int D, int NT>
+template <int D, int NT, int RG>
 struct Cfg {
+  static constexpr int KT = 16 * NW * RG;  // cache rows per tile
   static constexpr int ROW = D / 2;
   static constexpr int SROW = D / 16;  // scale bytes of a row
   static constexpr int TILE = KT * ROW;
@@ -53,12 +52,15 @@ struct Cfg {
   static constexpr int ROWS = 8 * NT;               // query rows of a CTA
   static constexpr int QS = 2 * D + 16;             // bytes between query rows
   static constexpr int CTAS = decode_fp4_ctas(D, ROWS);
-  static constexpr int NS = D == 128 ? 6 : 8;
-  static constexpr int RING = NS * STAGE;
   static constexpr int Q_BYTES = ROWS * QS;         // twice: the next piece's go to the other
   static constexpr int BARS = 192;
-  static constexpr int SMEM = 1024 + RING + NS * CODES + 2 * Q_BYTES + BARS + 2 * ROWS * 4;
-  static_assert(8 * (2 * NS + 4) + 4 <= BARS, "barriers");
+  static constexpr int REST = 1024 + 2 * Q_BYTES + BARS + 2 * ROWS * 4;
+  // the ring: what the resident CTAs have room for (1 KB of an SM's 228 goes with each)
+  static constexpr int ROOM = (228 * 1024 / CTAS - 1024 - REST) / (STAGE + CODES);
+  static constexpr int NS = ROOM < 6 ? ROOM : 6;
+  static constexpr int RING = NS * STAGE;
+  static constexpr int SMEM = REST + RING + NS * CODES;
+  static_assert(NS >= 2 && 8 * (2 * NS + 4) + 4 <= BARS, "barriers");
 };
 
 struct Params {
@@ -79,12 +81,12 @@ struct Params {
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -100,20 +102,25 @@ template <int N>
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 4)
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
   else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "r"(addr)
+                 : "memory");
   else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
   uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
   return r;
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   uint32_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr));
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
   return r;
 }
 
@@ -129,11 +136,13 @@ __device__ __forceinline__ int perm(int m) {
   return (0x57463120u >> (4 * m)) & 7u;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
+template <int D, int NT, int RG>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
     decode_fp4_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D, NT, RG>;
+  constexpr int KT = C::KT;
+  using Scales = std::conditional_t<D == 128, uint2, uint32_t>;  // a row's scale bytes
   constexpr int NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -181,7 +190,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
     const uint64_t once = evict_first_policy();
     const CacheRows& R = p.rows;
     const int nbox = KT / p.box_rows, r0 = lane * p.box_rows;
-    int issued = 0;
+    int issued = 0, s = 0, phase = 1;  // (a stage's first use waits for nothing: phase 1 is over)
+    // The page that the lane's box of tile t of the piece is in, and the row in it; -1: past the
+    // sequence.
+    auto page_of = [&](const GroupPiece& pc, int t, int& prow) {
+      const int row = (pc.t0 + t) * KT + r0;
+      prow = 0;
+      if (lane >= nbox || t >= pc.n || row >= pc.L) return -1;
+      const int at = row / R.page_size;
+      prow = row - at * R.page_size;
+      return R.block_table[static_cast<size_t>(pc.b) * R.max_pages + at];
+    };
     // The queries of a piece: D/16 lanes per row, 16 channels each, read ahead of the piece's
     // first tile and staged behind it.
     constexpr int G = D / 16, PASSES = C::ROWS * G / 32;
@@ -229,34 +248,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
       // last piece's) one
       const int q_at = min(pc.n, piece == 0 && p.code_copies ? NS : 1) - 1;
       load_queries(pc);
+      int next_row = 0, next_page = R.block_table != nullptr ? page_of(pc, 0, next_row) : 0;
       for (int t = 0; t < pc.n; ++t) {
-        const int s = issued % NS, use = issued / NS, row0 = (pc.t0 + t) * KT;
+        const int row0 = (pc.t0 + t) * KT;
         uint8_t* codes = s_codes + s * C::CODES;
         int plane = b * R.Hkv + kvh, prow = row0;
         int code_rows = min(KT, R.Lmax - row0);  // rows of the lane's box whose scales are copied
         bool lost = false;                       // its page is outside the pool
         if (R.block_table != nullptr) {
-          const int tr = row0 + r0;
-          plane = R.num_pages * R.Hkv;
-          prow = 0;
-          code_rows = 0;
-          if (lane < nbox && tr < total) {
-            const int page =
-                R.block_table[static_cast<size_t>(b) * R.max_pages + tr / R.page_size];
-            lost = page < 0 || page >= R.num_pages;
-            if (!lost) {
-              plane = page * R.Hkv + kvh;
-              code_rows = p.box_rows;
-            } else {
-              atomicOr(p.status, kStatusDeviceArg);
-            }
-            prow = tr % R.page_size;
-          }
+          const bool in = lane < nbox && row0 + r0 < total;
+          const int page = next_page;
+          prow = next_row;
+          next_page = page_of(pc, t + 1, next_row);  // (read while this tile's stage is waited for)
+          lost = in && (page < 0 || page >= R.num_pages);
+          plane = in && !lost ? page * R.Hkv + kvh : R.num_pages * R.Hkv;
+          code_rows = in && !lost ? p.box_rows : 0;
+          if (lost) atomicOr(p.status, kStatusDeviceArg);
         }
         if (lane >= nbox) code_rows = 0;
         bool room = true;
-        if (lane == 0 && use > 0)
-          room = ctl_wait(&empty[s], (use - 1) & 1, abort_flag, p.status, kWaitNs);
+        if (lane == 0) room = ctl_wait(&empty[s], phase, abort_flag, p.status, kWaitNs);
         if (!__all_sync(0xffffffffu, room)) {
           ok = false;
           break;
@@ -292,23 +303,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
         __syncwarp();
         ++issued;
         if (t == q_at) ok = stage_queries(piece);
+        const int at_s = s;
+        if (++s == NS) s = 0, phase ^= 1;
         if (!p.code_copies) {
-          // a row's scale bytes are a word of four or eight bytes
-          using Word = std::conditional_t<D == 128, uint2, uint32_t>;
 #pragma unroll
           for (int i = 0; i < KT / 32; ++i) {
             const int r = lane + 32 * i;
             const long long at = row0 + r < total ? R.at(b, kvh, row0 + r) : -1;
-            Word kw{}, vw{};
+            Scales kw{}, vw{};
             if (at >= 0) {
-              kw = *reinterpret_cast<const Word*>(p.k_scale + at * C::SROW);
-              vw = *reinterpret_cast<const Word*>(p.v_scale + at * C::SROW);
+              kw = *reinterpret_cast<const Scales*>(p.k_scale + at * C::SROW);
+              vw = *reinterpret_cast<const Scales*>(p.v_scale + at * C::SROW);
             }
-            *reinterpret_cast<Word*>(codes + r * C::SROW) = kw;
-            *reinterpret_cast<Word*>(codes + (KT + r) * C::SROW) = vw;
+            *reinterpret_cast<Scales*>(codes + r * C::SROW) = kw;
+            *reinterpret_cast<Scales*>(codes + (KT + r) * C::SROW) = vw;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
+          if (lane == 0) mbar_arrive(&full[at_s]);
         }
         if (!ok) break;
       }
@@ -337,17 +348,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
   const uint32_t k_off = chunk(kr, 4 * KW * j);
   const uint32_t va_off = chunk(va, 4 * VW * g), vb_off = chunk(vb, 4 * VW * g);
   const uint32_t ks_off = kr * C::SROW + (D / 64) * j;
-  const uint32_t vs_col = (KT * C::SROW) + (D == 128 ? g : g >> 1);
+  const uint32_t vs_a = (KT + va) * C::SROW + (D == 128 ? g : g >> 1);
+  const uint32_t vs_b = (KT + vb) * C::SROW + (D == 128 ? g : g >> 1);
   bool ok = true;
-  int used = 0;  // tiles of the CTA so far
+  int s = 0, phase = 0;  // the ring's next stage, and which of its uses
   for (int piece = 0; pc.n > 0; pc.next(p.line), ++piece) {
     const int kvh = pc.head / p.rblocks;
     const int row_base = (pc.head - kvh * p.rblocks) * C::ROWS;  // first query row
     const int k_begin = pc.t0 * KT, ntiles = pc.n;
     const int k_end = min(pc.L, k_begin + ntiles * KT);
 
-    ok = __all_sync(0xffffffffu, mbar_wait(&q_full[piece & 1], (piece >> 1) & 1, abort_flag,
-                                           p.status, kWaitNs));
+    ok = __all_sync(0xffffffffu, ctl_wait(&q_full[piece & 1], (piece >> 1) & 1, abort_flag,
+                                          p.status, kWaitNs));
     if (!ok) break;
     // the lane's quarter of its query row, in pairs of channels
     uint32_t qb[NT][D / 8];
@@ -364,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
         for (int e = 0; e < 4; ++e) qb[n][4 * i + e] = w[e];
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) qf[n][h] = s_qf[(piece & 1) * C::ROWS + 8 * n + cq + h];
+      for (int h = 0; h < 2; ++h)  // (not 0: a masked score times it stays -inf)
+        qf[n][h] = fmaxf(s_qf[(piece & 1) * C::ROWS + 8 * n + cq + h], 0x1p-120f);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_empty[piece & 1]);
@@ -380,19 +393,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
     }
 
     bool unset = true;  // some query row has no maximum yet
-    for (int t = 0; t < ntiles && ok; ++t, ++used) {
-      const int s = used % NS;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (used / NS) & 1, abort_flag, p.status,
-                                             kWaitNs))) {
+    for (int t = 0; t < ntiles && ok; ++t) {
+      if (!__all_sync(0xffffffffu, ctl_wait(&full[s], phase, abort_flag, p.status, kWaitNs))) {
         ok = false;
         break;
       }
       const uint32_t kbase = smem_base + s * C::STAGE, vbase = kbase + C::TILE;
       const uint32_t cbase = codes_base + s * C::CODES;
+      const int key0 = k_begin + t * KT + wrow;  // first cache row of the warp
+      // S^T: rows perm(g) and perm(g) + 8 of each group of 16
+      float sc[RG][NT][4];
 #pragma unroll
       for (int rg = 0; rg < RG; ++rg) {
-        const int key0 = k_begin + t * KT + wrow + 16 * rg;  // first cache row of the group
-        // S^T: rows perm(g) and perm(g) + 8
         uint32_t ka[KW], kb[KW];
         lds<KW>(kbase + k_off + (16 * rg) * C::ROW, ka);
         lds<KW>(kbase + k_off + (16 * rg + 8) * C::ROW, kb);
@@ -408,9 +420,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
           sa[0] = lds_u8(cbase + ks_off + (16 * rg) * C::SROW) * 0x00800080u;
           sb[0] = lds_u8(cbase + ks_off + (16 * rg + 8) * C::SROW) * 0x00800080u;
         }
-        float sc[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        for (int n = 0; n < NT; ++n)
+          sc[rg][n][0] = sc[rg][n][1] = sc[rg][n][2] = sc[rg][n][3] = 0.f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {  // a word: eight channels, two steps of the sum
           const uint32_t fa = sa[w / 2], fb = sb[w / 2];
@@ -424,85 +436,104 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
           const uint32_t c3 = mul_f16x2(e2m1x2_to_f16x2<3>(kb[w]), fb);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma(sc[n], a0, a1, a2, a3, qb[n][4 * w], qb[n][4 * w + 1]);
-            mma(sc[n], c0, c1, c2, c3, qb[n][4 * w + 2], qb[n][4 * w + 3]);
+            mma(sc[rg][n], a0, a1, a2, a3, qb[n][4 * w], qb[n][4 * w + 1]);
+            mma(sc[rg][n], c0, c1, c2, c3, qb[n][4 * w + 2], qb[n][4 * w + 3]);
           }
         }
-        // rows past the sequence: their scores become -inf
-        const bool edge = key0 + 16 > k_end;
-        const bool out0 = key0 + perm<D>(g) >= k_end, out1 = key0 + perm<D>(g) + 8 >= k_end;
-        // x - m_ref for every score (x rounded by itself, as in the maximum); where one exceeds
-        // the maximum by the threshold (or there is none yet) the maxima are raised first
-        float d[NT][4];
-        bool over = false;
+      }
+      // rows past the sequence: their scores become -inf, and their values' scales, which may be
+      // NaN, 0 (a branch that few tiles take)
+      const bool edge = key0 + 16 * RG > k_end;
+      if (edge) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sc[n][e] = __fmul_rn(sc[n][e], qf[n][e & 1]);
-            if (edge && (e < 2 ? out0 : out1)) sc[n][e] = -INFINITY;
-            d[n][e] = sc[n][e] - m_ref[n][e & 1];
-            over |= d[n][e] > kRescaleThreshold + kWeightLog2;
-          }
-        if (__any_sync(0xffffffffu, over || unset)) {
-          unset = false;
+          for (int i = 0; i < 2; ++i)
+            if (key0 + 16 * rg + 8 * i + perm<D>(g) >= k_end) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float mx = column_max(fmaxf(sc[n][h], sc[n][2 + h])) - kWeightLog2;
-              if (mx > m_ref[n][h] + kRescaleThreshold) {
-                f[h] = ex2_approx(m_ref[n][h] - mx);  // 0 when m_ref was -inf
-                l_part[n][h] *= f[h];
-                m_ref[n][h] = mx;
-              }
-              // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
-              const float ref = m_ref[n][h] == -INFINITY ? 0.f : m_ref[n][h];
-              unset |= m_ref[n][h] == -INFINITY;
-              d[n][h] = sc[n][h] - ref;
-              d[n][2 + h] = sc[n][2 + h] - ref;
+              for (int n = 0; n < NT; ++n)
+                sc[rg][n][2 * i] = sc[rg][n][2 * i + 1] = -INFINITY;
             }
-            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+        for (int r = lane; r < 16 * RG; r += 32)
+          if (key0 + r >= k_end)
+            *reinterpret_cast<Scales*>(s_codes + s * C::CODES + (KT + wrow + r) * C::SROW) =
+                Scales{};
+        __syncwarp();
+      }
+      // The largest scores; where one exceeds the maximum by the threshold (or there is none yet)
+      // the maxima are raised first.
+      float top[NT][2];
+      bool over = unset;
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                o[c][n][0] *= f[0];
-                o[c][n][1] *= f[1];
-                o[c][n][2] *= f[0];
-                o[c][n][3] *= f[1];
-              }
-            }
-          }
-          unset = __any_sync(0xffffffffu, unset);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          top[n][h] = fmaxf(sc[0][n][h], sc[0][n][2 + h]);
+#pragma unroll
+          for (int rg = 1; rg < RG; ++rg)
+            top[n][h] = fmax3(top[n][h], sc[rg][n][h], sc[rg][n][2 + h]);
+          top[n][h] *= qf[n][h];
+          over |= top[n][h] > m_ref[n][h] + (kRescaleThreshold + kWeightLog2);
         }
-        // weights, turned to the layout of the second product
-        uint32_t pb[NT][2];
+      if (__any_sync(0xffffffffu, over)) {
+        unset = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mx = column_max(top[n][h]) - kWeightLog2;
+            if (mx > m_ref[n][h] + kRescaleThreshold) {
+              f[h] = ex2_approx(m_ref[n][h] - mx);  // 0 when m_ref was -inf
+              l_part[n][h] *= f[h];
+              m_ref[n][h] = mx;
+            }
+            unset |= m_ref[n][h] == -INFINITY;
+          }
+          if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[c][n][0] *= f[0];
+              o[c][n][1] *= f[1];
+              o[c][n][2] *= f[0];
+              o[c][n][3] *= f[1];
+            }
+          }
+        }
+        unset = __any_sync(0xffffffffu, unset);
+      }
+      // weights, turned to the layout of the second product
+      uint32_t pb[RG][NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float ref[2];  // (a row that has seen nothing yet: 2^-inf = 0, and a NaN score stays NaN)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) ref[h] = m_ref[n][h] == -INFINITY ? 0.f : m_ref[n][h];
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) {
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            w[e] = ex2_approx(d[n][e]);
+            w[e] = ex2_approx(fmaf(sc[rg][n][e], qf[n][e & 1], -ref[e & 1]));
             l_part[n][e & 1] += w[e];
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            pb[n][i] = transpose8x8(pack_f16x2(w[2 * i], w[2 * i + 1]));
+            pb[rg][n][i] = transpose8x8(pack_f16x2(w[2 * i], w[2 * i + 1]));
         }
-        // O^T: rows perm(2j), perm(2j + 1) and eight further
+      }
+      // O^T: rows perm(2j), perm(2j + 1) and eight further
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg) {
         uint32_t x[2][2][VW];  // [+8][row of the pair]
         uint32_t sv[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           lds<VW>(vbase + va_off + (16 * rg + 8 * i) * C::ROW, x[i][0]);
           lds<VW>(vbase + vb_off + (16 * rg + 8 * i) * C::ROW, x[i][1]);
-          uint32_t ua = lds_u8(cbase + vs_col + (va + 16 * rg + 8 * i) * C::SROW);
-          uint32_t ub = lds_u8(cbase + vs_col + (vb + 16 * rg + 8 * i) * C::SROW);
-          if (edge) {  // (a scale past the sequence may be a NaN)
-            if (key0 - wrow + va + 8 * i >= k_end) ua = 0u;
-            if (key0 - wrow + vb + 8 * i >= k_end) ub = 0u;
-          }
-          sv[i] = (ua | (ub << 16)) << 7;
+          const uint32_t ua = lds_u8(cbase + vs_a + (16 * rg + 8 * i) * C::SROW);
+          const uint32_t ub = lds_u8(cbase + vs_b + (16 * rg + 8 * i) * C::SROW);
+          sv[i] = ua * 0x80u + ub * 0x800000u;
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
@@ -520,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
             a2 = mul_f16x2(a2, sv[1]);
             a3 = mul_f16x2(a3, sv[1]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma(o[c][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n)
+              mma(o[c][n], a0, a1, a2, a3, pb[rg][n][0], pb[rg][n][1]);
           };
           step(4 * w, e2m1x2_to_f16x2<0>(ev[0]), e2m1x2_to_f16x2<0>(od[0]),
                e2m1x2_to_f16x2<0>(ev[1]), e2m1x2_to_f16x2<0>(od[1]));
@@ -532,8 +564,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
                e2m1x2_to_f16x2<3>(ev[1]), e2m1x2_to_f16x2<3>(od[1]));
         }
       }
+      if (edge) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
+      if (++s == NS) s = 0, phase ^= 1;
     }
 
 #pragma unroll
@@ -569,9 +603,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS)
     for (; pc.n > 0; pc.next(p.line)) pc.leave_for_merge(p.line);
 }
 
-template <int D, int NT>
+template <int D, int NT, int RG>
 cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D, NT, RG>;
+  constexpr int KT = C::KT;
   Params p{};
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.line = group_line(a);
@@ -600,7 +635,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
       !make_tmap_u8_3d(&tv, a.cache.v, C::ROW, rows, planes, p.box_rows, D == 128))
     return cudaErrorInvalidValue;
   static SmemLimitOnce smem_limit;
-  cudaError_t e = smem_limit.set(decode_fp4_kernel<D, NT>, C::SMEM);
+  cudaError_t e = smem_limit.set(decode_fp4_kernel<D, NT, RG>, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.plan.grid), 1, 1);
@@ -612,12 +647,17 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp4_kernel<D, NT>, p, tk, tv);
+  return cudaLaunchKernelEx(&cfg, decode_fp4_kernel<D, NT, RG>, p, tk, tv);
 }
 
+template <int D, int NT>
+cudaError_t launch_unit(const GroupArgs& a, cudaStream_t stream) {
+  return a.plan.unit == kFp4ShortTile ? launch_t<D, NT, kFp4ShortTile / (16 * NW)>(a, stream)
+                                      : launch_t<D, NT, kFp4LongTile / (16 * NW)>(a, stream);
+}
 template <int D>
 cudaError_t launch_rows(const GroupArgs& a, cudaStream_t stream) {
-  return a.plan.block_rows <= 8 ? launch_t<D, 1>(a, stream) : launch_t<D, 2>(a, stream);
+  return a.plan.block_rows <= 8 ? launch_unit<D, 1>(a, stream) : launch_unit<D, 2>(a, stream);
 }
 
 }  // namespace

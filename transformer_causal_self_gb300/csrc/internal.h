@@ -332,7 +332,12 @@ constexpr int group_attn_ctas(int d, bool f8, int block_rows) {
 }
 cudaError_t launch_group_attn(const GroupArgs& a, cudaStream_t stream);
 // The same for one query per head over a 4-bit cache; drafts is 0 and q is used as given.
-constexpr int decode_fp4_ctas(int d, int block_rows) { return d == 128 && block_rows > 8 ? 2 : 3; }
+// CTAs of its kernel per SM: as many as the registers of 8 or 16 query rows leave room for.
+constexpr int decode_fp4_ctas(int d, int block_rows) {
+  return (d == 128 ? 3 : 4) - (block_rows > 8 ? 1 : 0);
+}
+// Cache rows of its tiles: plan_for takes the long ones where the GPU is full with the short ones.
+constexpr int kFp4ShortTile = 64, kFp4LongTile = 192;
 cudaError_t launch_decode_fp4(const GroupArgs& a, cudaStream_t stream);
 // The same on tcgen05, for many query rows; rope is 0.
 cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream);
