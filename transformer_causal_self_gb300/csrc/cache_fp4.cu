@@ -28,7 +28,6 @@ struct AppendParams {
   const int64_t* slots;
   CacheRows rows;
   int Tn;
-  unsigned items;  // B * Hkv * Tn * (D / 8) < 2^30
   uint32_t* status;
 };
 
@@ -39,55 +38,68 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* code) {
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   *code = fp4_scale_code(top);
   const float s = fp4_scale(*code);
-  // (the reciprocal of 0 would meet zeros; that of a NaN goes with zeros for the values)
-  return *code == kFp4Nan ? 0u : pack_e2m1x8(x, s > 0.f ? __frcp_rn(s) : 0.f);
+  // (a scale of 0 leaves zeros, a NaN goes with zeros)
+  return *code == kFp4Nan ? 0u : pack_e2m1x8(x, s > 0.f ? fp4_inverse(s) : 0.f);
 }
 
-// Thread item (b, g, t, c): consecutive threads write consecutive rows of a KV head.
-template <int D>
+// Thread item (b, g, t, c), U tokens a block's rows apart: consecutive threads write consecutive
+// rows of a KV head.
+template <int D, int U>
 __global__ void __launch_bounds__(kThreads) append_fp4_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int G = D / 8;
+  constexpr int G = D / 8, R = kThreads / G;  // lanes of a row, a block's rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  unsigned at = blockIdx.x * kThreads + threadIdx.x;
-  const bool live = at < p.items;
-  if (!live) at = 0;
-  const int c = static_cast<int>(at % G);
-  at /= G;
-  const int t = static_cast<int>(at % p.Tn);
-  at /= p.Tn;
+  const int c = static_cast<int>(threadIdx.x) % G;
+  const int t0 = static_cast<int>(blockIdx.x) * (R * U) + static_cast<int>(threadIdx.x) / G;
   const int Hkv = p.rows.Hkv;
-  const int g = static_cast<int>(at % Hkv), b = static_cast<int>(at / Hkv);
-  const uint4 k = *reinterpret_cast<const uint4*>(p.k_new + b * p.k_seq + g * p.k_head +
-                                                  t * p.k_token + 8 * c);
-  const uint4 v = *reinterpret_cast<const uint4*>(p.v_new + b * p.v_seq + g * p.v_head +
-                                                  t * p.v_token + 8 * c);
-  long long row = -1;
-  bool wrong = false;
-  if (p.slots != nullptr) {
-    const long long slot = p.slots[t];
-    if (slot >= 0) {  // (a negative one: no token)
-      // (a pool of 2^32 rows does not fit the card)
-      const unsigned ps = p.rows.page_size, at32 = static_cast<unsigned>(slot), page = at32 / ps;
-      wrong = (slot >> 32) != 0 || page >= static_cast<unsigned>(p.rows.num_pages);
-      if (!wrong) row = (static_cast<long long>(page) * Hkv + g) * ps + (at32 - page * ps);
-    }
-  } else {
-    const int L = p.cache_lens[b];
-    wrong = L < 0 || L > p.rows.Lmax - p.Tn;  // (no overflow: Lmax, Tn < 2^30)
-    if (!wrong) {
-      row = p.rows.at(b, g, L + t);
-      wrong = row < 0;
+  const int g = static_cast<int>(blockIdx.y), b = static_cast<int>(blockIdx.z);
+  const __nv_bfloat16* k_src = p.k_new + b * p.k_seq + g * p.k_head + 8 * c;
+  const __nv_bfloat16* v_src = p.v_new + b * p.v_seq + g * p.v_head + 8 * c;
+  uint4 k[U], v[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int t = t0 + i * R;
+    k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < p.Tn) {
+      k[i] = *reinterpret_cast<const uint4*>(k_src + t * p.k_token);
+      v[i] = *reinterpret_cast<const uint4*>(v_src + t * p.v_token);
     }
   }
-  if (live && wrong && c == 0 && g == 0) atomicOr(p.status, kStatusDeviceArg);
-  uint32_t kc, vc;
-  const uint32_t k4 = quantise8(k, &kc), v4 = quantise8(v, &vc);
-  if (!live || row < 0) return;
-  *reinterpret_cast<uint32_t*>(p.k_cache + row * (D / 2) + 4 * c) = k4;
-  *reinterpret_cast<uint32_t*>(p.v_cache + row * (D / 2) + 4 * c) = v4;
-  if ((c & 1) == 0) {
-    p.k_scale[row * (D / 16) + c / 2] = static_cast<uint8_t>(kc);
-    p.v_scale[row * (D / 16) + c / 2] = static_cast<uint8_t>(vc);
+  long long row[U];
+  bool wrong = false;
+  const int L = p.slots == nullptr ? p.cache_lens[b] : 0;
+  const bool fits = L >= 0 && L <= p.rows.Lmax - p.Tn;  // (no overflow: Lmax, Tn < 2^30)
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int t = t0 + i * R;
+    row[i] = -1;
+    if (t >= p.Tn) continue;
+    if (p.slots != nullptr) {
+      const long long slot = p.slots[t];
+      if (slot >= 0) {  // (a negative one: no token)
+        // (a pool of 2^32 rows does not fit the card)
+        const unsigned ps = p.rows.page_size, at32 = static_cast<unsigned>(slot), page = at32 / ps;
+        if ((slot >> 32) == 0 && page < static_cast<unsigned>(p.rows.num_pages))
+          row[i] = (static_cast<long long>(page) * Hkv + g) * ps + (at32 - page * ps);
+        else
+          wrong = true;
+      }
+    } else {
+      if (fits) row[i] = p.rows.at(b, g, L + t);
+      wrong |= row[i] < 0;
+    }
+  }
+  if (wrong && c == 0 && g == 0) atomicOr(p.status, kStatusDeviceArg);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    uint32_t kc, vc;
+    const uint32_t k4 = quantise8(k[i], &kc), v4 = quantise8(v[i], &vc);
+    if (row[i] < 0) continue;
+    *reinterpret_cast<uint32_t*>(p.k_cache + row[i] * (D / 2) + 4 * c) = k4;
+    *reinterpret_cast<uint32_t*>(p.v_cache + row[i] * (D / 2) + 4 * c) = v4;
+    if ((c & 1) == 0) {
+      p.k_scale[row[i] * (D / 16) + c / 2] = static_cast<uint8_t>(kc);
+      p.v_scale[row[i] * (D / 16) + c / 2] = static_cast<uint8_t>(vc);
+    }
   }
 }
 
@@ -97,40 +109,55 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint32_t h, float s) {
   return pack_bf16x2(f.x * s, f.y * s);
 }
 
-// Eight channels per thread item (b, g, r, c); kRows rows, a block's threads apart.
-constexpr int kRows = 4;
+// Eight channels of a key and of the value beside it per thread item (b, g, r, c), kRows rows a
+// block's rows apart: a row is found once for both.
+constexpr int kRows = 2;
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_fp4_kernel(
     const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
     const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
     const int32_t* __restrict__ seq_lens, CacheRows rows, __nv_bfloat16* __restrict__ k_out,
-    __nv_bfloat16* __restrict__ v_out, int Lout, uint32_t* status, int k_blocks) {
-  constexpr int G = D / 8;
-  const int bg = static_cast<int>(blockIdx.x) / (2 * k_blocks);
-  int blk = static_cast<int>(blockIdx.x) - bg * (2 * k_blocks);
-  const bool is_k = blk < k_blocks;
-  if (!is_k) blk -= k_blocks;
+    __nv_bfloat16* __restrict__ v_out, int Lout, uint32_t* status, int blocks, int shift) {
+  constexpr int G = D / 8, R = kThreads / G;
+  const int bg = static_cast<int>(blockIdx.x) / blocks;
+  const int blk = static_cast<int>(blockIdx.x) - bg * blocks;
   const int b = bg / rows.Hkv, g = bg - b * rows.Hkv;
+  const int c = static_cast<int>(threadIdx.x) % G;
+  const int r0 = blk * (R * kRows) + static_cast<int>(threadIdx.x) / G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (the table is read beside the length; its entries of no row are any)
+  int at[kRows], page[kRows];
+  if (rows.block_table != nullptr) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      // (shift: of a page size that is a power of two, or negative)
+      const int r = min(r0 + k * R, rows.Lmax - 1);
+      at[k] = shift >= 0 ? r >> shift : r / rows.page_size;
+      page[k] = rows.block_table[static_cast<size_t>(b) * rows.max_pages + at[k]];
+    }
+  }
   const int n = seq_lens[b];
   if (n < 0 || n > Lout || n > rows.Lmax) {
-    if (is_k && blk == 0 && g == 0 && threadIdx.x == 0) atomicOr(status, kStatusDeviceArg);
+    if (blk == 0 && g == 0 && threadIdx.x == 0) atomicOr(status, kStatusDeviceArg);
     return;  // the sequence is left as it was
   }
-  const uint8_t* src = is_k ? k_cache : v_cache;
-  const uint8_t* scale = is_k ? k_scale : v_scale;
-  __nv_bfloat16* dst = (is_k ? k_out : v_out) + static_cast<size_t>(bg) * Lout * D;
-  const int i0 = blk * (kThreads * kRows) + static_cast<int>(threadIdx.x);
-  uint32_t x[kRows], code[kRows];
+  uint32_t x[kRows][2], code[kRows][2];
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const int i = i0 + k * kThreads, r = i / G, c = i % G;
-    x[k] = code[k] = 0u;
+    const int r = r0 + k * R;
+    x[k][0] = x[k][1] = code[k][0] = code[k][1] = 0u;
     if (r < n) {
-      const long long row = rows.at(b, g, r);
+      long long row = (static_cast<long long>(b) * rows.Hkv + g) * rows.Lmax + r;
+      if (rows.block_table != nullptr)
+        row = page[k] < 0 || page[k] >= rows.num_pages
+                  ? -1
+                  : (static_cast<long long>(page[k]) * rows.Hkv + g) * rows.page_size + r -
+                        at[k] * rows.page_size;
       if (row >= 0) {
-        x[k] = *reinterpret_cast<const uint32_t*>(src + row * (D / 2) + 4 * c);
-        code[k] = scale[row * (D / 16) + c / 2];
+        x[k][0] = *reinterpret_cast<const uint32_t*>(k_cache + row * (D / 2) + 4 * c);
+        x[k][1] = *reinterpret_cast<const uint32_t*>(v_cache + row * (D / 2) + 4 * c);
+        code[k][0] = k_scale[row * (D / 16) + c / 2];
+        code[k][1] = v_scale[row * (D / 16) + c / 2];
       } else if (c == 0) {
         atomicOr(status, kStatusDeviceArg);  // the row reads as zeros
       }
@@ -138,12 +165,17 @@ __global__ void __launch_bounds__(kThreads) read_fp4_kernel(
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const int i = i0 + k * kThreads, r = i / G, c = i % G;
+    const int r = r0 + k * R;
     if (r >= n) break;
-    const float s = fp4_scale(code[k]);
-    *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + 8 * c) =
-        make_uint4(to_bf16x2(e2m1x2_to_f16x2<0>(x[k]), s), to_bf16x2(e2m1x2_to_f16x2<1>(x[k]), s),
-                   to_bf16x2(e2m1x2_to_f16x2<2>(x[k]), s), to_bf16x2(e2m1x2_to_f16x2<3>(x[k]), s));
+    const size_t to = (static_cast<size_t>(bg) * Lout + r) * D + 8 * c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s = fp4_scale(code[k][i]);
+      const uint32_t y = x[k][i];
+      *reinterpret_cast<uint4*>((i == 0 ? k_out : v_out) + to) =
+          make_uint4(to_bf16x2(e2m1x2_to_f16x2<0>(y), s), to_bf16x2(e2m1x2_to_f16x2<1>(y), s),
+                     to_bf16x2(e2m1x2_to_f16x2<2>(y), s), to_bf16x2(e2m1x2_to_f16x2<3>(y), s));
+    }
   }
 }
 
@@ -171,26 +203,34 @@ cudaError_t launch_cache_append_fp4(const Fp4AppendArgs& a, cudaStream_t stream)
   p.slots = a.slots;
   p.rows = rows_of(a.cache, a.Hkv);
   p.Tn = a.Tn;
-  p.items = static_cast<unsigned>(static_cast<long long>(a.B) * a.Hkv * a.Tn * (a.d / 8));
   p.status = a.status;
-  auto* kernel = a.d == 128 ? append_fp4_kernel<128> : append_fp4_kernel<64>;
-  return launch_behind(kernel, dim3(static_cast<unsigned>((p.items + kThreads - 1) / kThreads)),
-                       kThreads, stream, p);
+  // two tokens per thread where that still fills the GPU
+  const long long threads = static_cast<long long>(a.B) * a.Hkv * a.Tn * (a.d / 8);
+  const int U = threads >= 2LL * 12 * kSms * kThreads ? 2 : 1;
+  const unsigned rows = kThreads / (a.d / 8) * U;
+  auto* kernel = a.d == 128 ? (U == 2 ? append_fp4_kernel<128, 2> : append_fp4_kernel<128, 1>)
+                            : (U == 2 ? append_fp4_kernel<64, 2> : append_fp4_kernel<64, 1>);
+  const dim3 grid((static_cast<unsigned>(a.Tn) + rows - 1) / rows, static_cast<unsigned>(a.Hkv),
+                  static_cast<unsigned>(a.B));  // (Hkv, B <= 65535)
+  return launch_behind(kernel, grid, kThreads, stream, p);
 }
 
 cudaError_t launch_cache_read_fp4(const KvCache& cache, const int32_t* seq_lens, void* k_out,
                                   void* v_out, int B, int Hkv, int Lout, int d, uint32_t* status,
                                   cudaStream_t stream) {
-  const long long pieces = static_cast<long long>(std::min(Lout, cache.Lmax)) * (d / 8);
-  const long long blocks = (pieces + kThreads * kRows - 1) / (kThreads * kRows);
+  const long long per = kThreads / (d / 8) * kRows;
+  const long long blocks = (std::min(Lout, cache.Lmax) + per - 1) / per;
+  int shift = -1;
+  if (cache.page_size > 0 && (cache.page_size & (cache.page_size - 1)) == 0)
+    for (shift = 0; (1 << shift) < cache.page_size;) ++shift;
   // (a grid below 2^31: B * Hkv < 2^30, and B * Hkv * Lout < 2^33 where there are more blocks)
   auto* kernel = d == 128 ? read_fp4_kernel<128> : read_fp4_kernel<64>;
-  return launch_behind(kernel, dim3(static_cast<unsigned>(2 * blocks * B * Hkv)), kThreads, stream,
+  return launch_behind(kernel, dim3(static_cast<unsigned>(blocks * B * Hkv)), kThreads, stream,
                        static_cast<const uint8_t*>(cache.k), static_cast<const uint8_t*>(cache.v),
                        static_cast<const uint8_t*>(cache.k_scale),
                        static_cast<const uint8_t*>(cache.v_scale), seq_lens, rows_of(cache, Hkv),
                        static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), Lout,
-                       status, static_cast<int>(blocks));
+                       status, static_cast<int>(blocks), shift);
 }
 
 }  // namespace csattn

@@ -107,8 +107,6 @@ int norm_args(const char* fn, QkNormArgs* a, const void* q, const void* k, const
   a->k.x = k;
   a->q.w = q_weight;
   a->k.w = k_weight;
-  a->q.y = const_cast<void*>(q_out);
-  a->k.y = const_cast<void*>(k_out);
   a->q.H = Hq;
   a->k.H = Hkv;
   a->positions = positions;
@@ -212,6 +210,13 @@ int csattn_qk_norm_rope(const void* q, const void* k, const void* q_weight, cons
   int rc = norm_args("qk_norm_rope", &a, q, k, q_weight, k_weight, positions, q_out, k_out, B, Hq,
                      Hkv, T, d, dtype, strides, pos0, norm, eps, rope_base, rope_layout);
   if (rc != CSATTN_OK) return rc;
+  a.q.y = q_out;
+  a.k.y = k_out;
+  for (QkNormSide* s : {&a.q, &a.k}) {
+    s->y_token = d;
+    s->y_head = static_cast<long long>(T) * d;
+    s->y_batch = s->H * s->y_head;
+  }
   int sms = 0;
   if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
   const cudaError_t e =
@@ -220,7 +225,7 @@ int csattn_qk_norm_rope(const void* q, const void* k, const void* q_weight, cons
 }
 
 size_t csattn_qk_norm_rope_bwd_workspace_size(int d) {
-  return d > 0 && d <= 128 ? (qk_norm_bwd_blocks() + 1) * static_cast<size_t>(d) * 4 : 0;
+  return d > 0 && d <= 128 ? (qk_norm_bwd_blocks() + 2) * static_cast<size_t>(d) * 4 : 0;
 }
 
 int csattn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
@@ -243,13 +248,15 @@ int csattn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* 
     return api_fail(CSATTN_ERR_INVALID_ARG, "%s: a gain and its gradient go together", fn);
   const int size = dtype == CSATTN_BF16 ? 2 : 4;
   rc = set_strides(fn, strides != nullptr ? strides + 6 : nullptr, B, Hq, T, d, size,
-                   &a.q.dx_batch, &a.q.dx_head, &a.q.dx_token);
+                   &a.q.y_batch, &a.q.y_head, &a.q.y_token);
   if (rc != CSATTN_OK) return rc;
   rc = set_strides(fn, strides != nullptr ? strides + 9 : nullptr, B, Hkv, T, d, size,
-                   &a.k.dx_batch, &a.k.dx_head, &a.k.dx_token);
+                   &a.k.y_batch, &a.k.y_head, &a.k.y_token);
   if (rc != CSATTN_OK) return rc;
-  a.q.dx = dq;
-  a.k.dx = dk;
+  a.q.dy = dq_out;
+  a.k.dy = dk_out;
+  a.q.y = dq;
+  a.k.y = dk;
   if (dq_weight != nullptr || dk_weight != nullptr) {
     const size_t need = csattn_qk_norm_rope_bwd_workspace_size(d);
     if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))

@@ -31,13 +31,13 @@ constexpr uint32_t kFp4Nan = 255;
 // scale byte of a block whose largest magnitude has the bf16 bits `top` (0x7f80 and above: an
 // infinity or NaN is in it)
 __device__ __forceinline__ uint32_t fp4_scale_code(uint32_t top) {
-  if (top >= 0x7f80u) return kFp4Nan;
   const float t = fminf(__uint_as_float(top << 16) * (1.f / 6.f), 10240.f);
-  // (below 2^-14 in steps of 2^-17, by way of steps of 2^-29)
-  if (t < 6.103515625e-5f)
-    return static_cast<uint32_t>(rintf((t * 131072.f + 2048.f) - 2048.f));
+  // (below 2^-14 in steps of 2^-17, by way of steps of 2^-29; both by adding what has that step)
+  const float y = (t * 131072.f + 2048.f) - 2048.f + 12582912.f;
+  const uint32_t small = __float_as_uint(y) & 15u;
   const uint32_t h = __half_as_ushort(__float2half_rn(t));
-  return min((h + 63u + ((h >> 7) & 1u)) >> 7, kFp4Top);
+  const uint32_t code = min((h + 63u + ((h >> 7) & 1u)) >> 7, kFp4Top);
+  return top >= 0x7f80u ? kFp4Nan : (t < 6.103515625e-5f ? small : code);
 }
 
 // s of a byte
@@ -45,23 +45,26 @@ __device__ __forceinline__ float fp4_scale(uint32_t code) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(code << 7)));
 }
 
-// two f16 to e2m1 (to nearest even, at most 6 in magnitude), the low half in the low four bits
-__device__ __forceinline__ uint32_t f16x2_to_e2m1x2(uint32_t h) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f16x2 t, %1;\n\tcvt.u16.u8 %0, t;\n\t}"
-      : "=h"(r)
-      : "r"(h));
+// eight bf16 times inv to e2m1 (to nearest even, at most 6 in magnitude), by way of f16
+__device__ __forceinline__ uint32_t pack_e2m1x8(const uint4& x, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4], r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = pack_f16x2(bf16lo_to_f32(w[i]) * inv, bf16hi_to_f32(w[i]) * inv);
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e2m1x2.f16x2 b, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 c, %3;\n\tcvt.rn.satfinite.e2m1x2.f16x2 d, %4;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
   return r;
 }
 
-// eight bf16 to e2m1 of their quotients with 1 / inv
-__device__ __forceinline__ uint32_t pack_e2m1x8(const uint4& x, float inv) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r |= f16x2_to_e2m1x2(pack_f16x2(bf16lo_to_f32(w[i]) * inv, bf16hi_to_f32(w[i]) * inv))
-         << (8 * i);
+// 1 / s within 2^-23 of it, s a scale that is not 0
+__device__ __forceinline__ float fp4_inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
   return r;
 }
 

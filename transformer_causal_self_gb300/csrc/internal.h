@@ -237,9 +237,9 @@ struct QkNormSide {  // the queries or the keys
   const void* x;
   long long batch, head, token;  // x's strides in elements
   const void* w;  // gain [d], or null
-  void* y;        // [B, H, T, d]: written, or its gradient (backward)
-  void* dx;       // backward
-  long long dx_batch, dx_head, dx_token;
+  const void* dy; // backward: the output's gradient, [B, H, T, d]
+  void* y;        // written: the output, or x's gradient
+  long long y_batch, y_head, y_token;
   int H;
   int span, groups;  // (set by the launchers)
   unsigned items;
@@ -252,7 +252,7 @@ struct QkNormArgs {
   float eps;
   int rope;         // 0 none, 1 split-half, 2 adjacent
   RopeTable turns;  // frequencies in quarter turns (rope_turns.cuh)
-  float* partial;   // [qk_norm_bwd_blocks() + 1, d] where gains have gradients, or null
+  float* partial;   // [qk_norm_bwd_blocks() + 2, d] where gains have gradients, or null
   uint32_t* status;
   int q_blocks;     // (set by the launchers)
 };
@@ -310,11 +310,12 @@ inline GroupLine group_line(const GroupArgs& a) {
 // passes griddepcontrol.wait, behind which that kernel has ended and its writes are visible,
 // before it touches memory.
 template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
-                          A... args) {
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -322,6 +323,12 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStre
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
+                          A... args) {
+  return launch_behind(kernel, grid, threads, size_t{0}, stream, args...);
 }
 
 // CTAs of launch_group_attn's kernel per SM.  e4m3: three, except where 16 query rows of 128
@@ -397,7 +404,7 @@ constexpr int kMaxRopePositions = 49152;  // largest position whose angle reduct
 // asked for without a device)
 constexpr int kSms = 152;
 // blocks of the norm's backward pass (each leaves a sum of the gains' gradients)
-constexpr int qk_norm_bwd_blocks() { return 4 * kSms; }
+constexpr int qk_norm_bwd_blocks() { return 3 * kSms; }
 
 // Raises a kernel's dynamic shared-memory limit once per device (the attribute
 // lasts for the process), so repeated launches skip the driver call.
