@@ -35,6 +35,33 @@ def test_contiguous_caches_of_odd_lengths(d, Lmax):
     H.assert_close(out, H.expect(c, q, lens))
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,page", [
+    (128, 32, 8, 64), (128, 4, 1, 16), (128, 7, 1, 192), (128, 8, 8, 0), (128, 16, 1, 128),
+    (128, 40, 2, 64), (64, 8, 2, 64), (64, 12, 12, 16), (64, 16, 1, 32), (64, 24, 1, 384),
+    (64, 3, 3, 0)])
+def test_long_tiles(d, Hq, Hkv, page):
+    """Caches with room for so much that the tiles are of 192 rows: lengths around their ends, the
+    pages' and the groups' of 16 rows within them."""
+    lens = [192, 1, 193, 191, 0, 400, 48, 49, 160, 576, 577, 65, 384, 15, 240, 17]
+    room = 6144 + (0 if page else 9)  # (contiguous planes whose scales are not on 16 bytes, too)
+    c, q = H.filled(len(lens), Hq, Hkv, d, page, lens, 577 if page else 640, seed=Hq)
+    if page:  # entries of pages that no row is on
+        per = -(-room // page)
+        table = torch.full((len(lens), per), -1, dtype=torch.int32)
+        table[:, :c["table"].shape[1]] = c["table"]
+        c["table"] = table
+        out = H.decode(H.to_dev(c), q.to(dev()), H.i32(lens))
+    else:
+        big = H.empty_cache(len(lens), Hkv, room, d, 0, seed=1)
+        for n in H.NAMES:
+            big[n][:, :, :c[n].shape[2]] = c[n]
+        c = big
+        out = H.decode(H.to_dev(c), q.to(dev()), H.i32(lens))
+    csattn.check_status()
+    assert torch.all(out[4] == 0)
+    H.assert_close(out, H.expect(c, q, lens))
+
+
 @pytest.mark.parametrize("gain,scale", [(8.0, 0.0), (1e-3, 0.0), (1.0, 3.0), (1e30, 1e-30),
                                         (1e-30, 1e30), (30.0, 0.0)])
 def test_large_and_small_scores(gain, scale):

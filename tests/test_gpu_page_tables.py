@@ -57,6 +57,14 @@ def test_tables(held, new, page, more):
     assert not check(held, new, table, free, len(free), sum(new) + more or 1, page, total)
 
 
+def test_an_empty_free_list():
+    """Steps that fit into the pages at hand, and one that does not."""
+    table = torch.tensor([[3, 1], [0, 2]], dtype=torch.int32)
+    none = torch.empty(0, dtype=torch.int32)
+    assert not check([17, 5], [3, 11], table, none, 0, 14, 16, 4)
+    assert check([16, 16], [1, 0], table[:, :1].repeat(1, 3), none, 0, 4, 16, 4)
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_random_steps(seed):
     g = gen(seed)

@@ -695,10 +695,13 @@ _stream_id = getattr(torch._C, "_cuda_getCurrentStream", None) or (
     lambda dev: (torch.cuda.current_stream(dev).stream_id,))
 
 
+_DEVICES = [torch.device("cuda", i) for i in range(64)]  # (read faster than made from a number)
+
+
 def _empty(shape, dtype, dev: int, stream, returned: bool = True) -> torch.Tensor:
     """An output (`returned`) or workspace of a call on `stream` (None: the current one)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
     # Memory of that stream, which nothing that is queued on the current one still uses; and an
     # output, which the caller will use there, is not handed out again before that is done.
     if not isinstance(stream, torch.cuda.Stream):
@@ -1053,6 +1056,14 @@ def tree_commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table:
 
 
 # ------------------------------------------------------------------- 4-bit cache
+def _out(name: str, given: Optional[torch.Tensor], shape, dtypes, dev: int, stream):
+    """(tensor, address) of an output: the one given, or a new one."""
+    if given is None:
+        given = _empty(shape, dtypes[0], dev, stream)
+        return given, given.data_ptr()
+    return given, _ptr(name, given, shape, dtypes, dev)
+
+
 _FP4 = (torch.uint8,) + tuple(getattr(torch, n) for n in ("float4_e2m1fn_x2",) if hasattr(torch, n))
 _U8, _I64 = (torch.uint8,), (torch.int64,)
 
@@ -1219,16 +1230,15 @@ def _decode_fp4(fn, q, k, v, k_scale, v_scale, block_table, seq_lens, out, scale
     table, size, rows = _cache_sizes(cshape, block_table, B, dev)
     if cshape[3] != d:
         raise ValueError("q and the cache differ in head size")
-    if out is None:
-        out = _empty(shape, torch.bfloat16, dev, stream)
+    out, op = _out("out", out, shape, _BF16, dev, stream)
     if max_seq_len is None:
         max_seq_len = rows
     need = 0 if workspace is not None else decode_fp4_workspace_size(
         B, Hq, Hkv, max_seq_len, d, num_splits)
     workspace, wp, wn = _workspace(workspace, need, dev, stream)
     _run(dev, fn, _ptr("q", q, shape, _BF16, dev), *cache, *table,
-         _ptr("seq_lens", seq_lens, (B,), _I32, dev), _ptr("out", out, shape, _BF16, dev), B, Hq,
-         Hkv, *size, d, CSATTN_BF16, scale, max_seq_len, num_splits, wp, wn, _handle(dev, stream))
+         _ptr("seq_lens", seq_lens, (B,), _I32, dev), op, B, Hq, Hkv, *size, d, CSATTN_BF16, scale,
+         max_seq_len, num_splits, wp, wn, _handle(dev, stream))
     return out
 
 
@@ -1289,27 +1299,23 @@ def page_tables(cache_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     B = cache_lens.shape[0]
     if block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("block_table [B, max_pages] and free_pages [pages] expected")
-    per = block_table.shape[1]
-    if out is None:
-        out = PageTables(_empty((B,), torch.int32, dev, stream),
-                         _empty((B + 1,), torch.int32, dev, stream),
-                         _empty((num_tokens,), torch.int64, dev, stream),
-                         _empty((num_tokens,), torch.int32, dev, stream),
-                         _empty((1,), torch.int32, dev, stream))
+    per, N = block_table.shape[1], num_tokens
+    given = (None,) * 5 if out is None else out
+    lens, lp = _out("seq_lens", given[0], (B,), _I32, dev, stream)
+    starts, sp = _out("starts", given[1], (B + 1,), _I32, dev, stream)
+    slots, tp = _out("slots", given[2], (N,), _I64, dev, stream)
+    positions, pp = _out("positions", given[3], (N,), _I32, dev, stream)
+    left, fp = _out("free_left", given[4], (1,), _I32, dev, stream)
     _run(dev, load_library().csattn_page_tables, _ptr("cache_lens", cache_lens, (B,), _I32, dev),
          _ptr("new_lens", new_lens, (B,), _I32, dev),
          _ptr("block_table", block_table, (B, per), _I32, dev),
          _ptr("free_pages", free_pages, free_pages.shape, _I32, dev),
-         _ptr("num_free", num_free, (1,), _I32, dev), _ptr("seq_lens", out[0], (B,), _I32, dev),
-         _ptr("starts", out[1], (B + 1,), _I32, dev),
-         _ptr("slots", out[2], (num_tokens,), _I64, dev),
-         _ptr("positions", out[3], (num_tokens,), _I32, dev),
-         _ptr("free_left", out[4], (1,), _I32, dev), B, num_tokens, page_size, num_pages, per,
-         free_pages.shape[0], _handle(dev, stream))
-    return out
+         _ptr("num_free", num_free, (1,), _I32, dev), lp, sp, tp, pp, fp, B, N, page_size,
+         num_pages, per, free_pages.shape[0], _handle(dev, stream))
+    return PageTables(lens, starts, slots, positions, left) if out is None else out
 
 
-def _norm_args(q, k, q_weight, k_weight, positions, norm):
+def _norm_args(q, k, q_weight, k_weight, positions):
     """(dev, types, shapes of q and k, pointers of the gains and positions)."""
     dev = _device_of("q", q, 4)
     if q.dtype not in (torch.bfloat16, torch.float32):
@@ -1338,17 +1344,14 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     pos0 + t).  norm=False rotates alone.  A step's packed tokens are a batch of N sequences of one
     token.  Returns (q_out, k_out), contiguous.
     """
-    dev, types, qshape, kshape, qw, kw, pos = _norm_args(q, k, q_weight, k_weight, positions, norm)
+    dev, types, qshape, kshape, qw, kw, pos = _norm_args(q, k, q_weight, k_weight, positions)
     B, Hq, T, d = qshape
-    if q_out is None:
-        q_out = _empty(qshape, q.dtype, dev, stream)
-    if k_out is None:
-        k_out = _empty(kshape, q.dtype, dev, stream)
+    q_out, qop = _out("q_out", q_out, qshape, types, dev, stream)
+    k_out, kop = _out("k_out", k_out, kshape, types, dev, stream)
     qp, qs = _strided("q", q, qshape, types, dev)
     kp, ks = _strided("k", k, kshape, types, dev)
-    _run(dev, load_library().csattn_qk_norm_rope, qp, kp, qw, kw, pos,
-         _ptr("q_out", q_out, qshape, types, dev), _ptr("k_out", k_out, kshape, types, dev), B, Hq,
-         kshape[1], T, d, CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
+    _run(dev, load_library().csattn_qk_norm_rope, qp, kp, qw, kw, pos, qop, kop, B, Hq, kshape[1],
+         T, d, CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
          None if qs is ks is None else _strides((qs, ks), qshape, kshape), pos0, 1 if norm else 0,
          eps, rope_base, _ROPE_LAYOUT[rope_layout], _handle(dev, stream))
     return q_out, k_out
@@ -1373,7 +1376,7 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     of a fused projection's gradient among them (allocated dense when not given).  Returns
     (dq, dk, dq_weight, dk_weight), the last two fp32 [d], None where the gain is.
     """
-    dev, types, qshape, kshape, qw, kw, pos = _norm_args(q, k, q_weight, k_weight, positions, norm)
+    dev, types, qshape, kshape, qw, kw, pos = _norm_args(q, k, q_weight, k_weight, positions)
     B, Hq, T, d = qshape
     if (dq_weight is not None and qw is None) or (dk_weight is not None and kw is None):
         raise ValueError("a gradient for a gain that is not given")
@@ -1381,10 +1384,11 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
         dq = _empty(qshape, q.dtype, dev, stream)
     if dk is None:
         dk = _empty(kshape, q.dtype, dev, stream)
-    if qw is not None and dq_weight is None:
-        dq_weight = _empty((d,), torch.float32, dev, stream)
-    if kw is not None and dk_weight is None:
-        dk_weight = _empty((d,), torch.float32, dev, stream)
+    dqwp = dkwp = None
+    if qw is not None:
+        dq_weight, dqwp = _out("dq_weight", dq_weight, (d,), _F32, dev, stream)
+    if kw is not None:
+        dk_weight, dkwp = _out("dk_weight", dk_weight, (d,), _F32, dev, stream)
     need = 0
     if workspace is None and (qw is not None or kw is not None):
         need = qk_norm_rope_bwd_workspace_size(d)
@@ -1400,10 +1404,7 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
         workspace, wp, wn = _workspace(workspace, need, dev, stream)
     _run(dev, load_library().csattn_qk_norm_rope_bwd,
          _ptr("dq_out", dq_out, qshape, types, dev), _ptr("dk_out", dk_out, kshape, types, dev),
-         qp, kp, qw, kw, pos, dqp, dkp,
-         None if qw is None else _ptr("dq_weight", dq_weight, (d,), _F32, dev),
-         None if kw is None else _ptr("dk_weight", dk_weight, (d,), _F32, dev), B, Hq, kshape[1],
-         T, d, CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
+         qp, kp, qw, kw, pos, dqp, dkp, dqwp, dkwp, B, Hq, kshape[1], T, d, CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
          None if qs is ks is dqs is dks is None else
          _strides((qs, ks, dqs, dks), qshape, kshape, qshape, kshape), pos0, 1 if norm else 0, eps,
          rope_base, _ROPE_LAYOUT[rope_layout], wp, wn, _handle(dev, stream))
