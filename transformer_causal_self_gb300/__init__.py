@@ -745,7 +745,8 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: int, stream):
 
 def release_workspaces() -> None:
     """Lets go of the workspaces that calls of the 8-bit and 4-bit decodes, of tree steps and of
-    qk_norm_rope_bwd have kept for this thread (up to 64 MB for each stream that it made such calls on; a thread's end does, too)."""
+    qk_norm_rope_bwd have kept for this thread (up to 64 MB for each stream that it made such calls
+    on; a thread's end does, too)."""
     _kept.__dict__.clear()
 
 
@@ -1404,7 +1405,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
         workspace, wp, wn = _workspace(workspace, need, dev, stream)
     _run(dev, load_library().csattn_qk_norm_rope_bwd,
          _ptr("dq_out", dq_out, qshape, types, dev), _ptr("dk_out", dk_out, kshape, types, dev),
-         qp, kp, qw, kw, pos, dqp, dkp, dqwp, dkwp, B, Hq, kshape[1], T, d, CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
+         qp, kp, qw, kw, pos, dqp, dkp, dqwp, dkwp, B, Hq, kshape[1], T, d,
+         CSATTN_BF16 if types[0] is torch.bfloat16 else CSATTN_F32,
          None if qs is ks is dqs is dks is None else
          _strides((qs, ks, dqs, dks), qshape, kshape, qshape, kshape), pos0, 1 if norm else 0, eps,
          rope_base, _ROPE_LAYOUT[rope_layout], wp, wn, _handle(dev, stream))

@@ -3,10 +3,10 @@
 // out = softmax(q K^T scale) V with K and V in e2m1 times a scale per 16 channels.  All Hq / Hkv
 // query rows of a KV head read the same cache rows, so they are one side of a matrix product and
 // a row is read from HBM and taken to f16 once for 8 * NT of them.  A CTA:
-//   warp 4      producer: KT-row K and V tiles and their scale bytes into a ring by TMA, and a
-//               piece's queries, as f16, ahead of its other tiles
-//   warps 0..3  KT / 4 cache rows each per tile, by mma.sync m16n8k16 with the cache rows (then
-//               the channels) on the side of 16 and the query rows on the side of 8:
+//   warp 4      producer: tiles of 64 or 192 K and V rows and their scale bytes into a ring by
+//               TMA, and a piece's queries, as f16, ahead of its other tiles
+//   warps 0..3  RG groups of 16 cache rows each per tile, by mma.sync m16n8k16 with the cache rows
+//               (then the channels) on the side of 16 and the query rows on the side of 8:
 //               S^T = K Q^T, then O^T += V^T P^T, softmax statistics in fp32 between the two;
 //               each leaves a partial result of its own per piece.
 // CTAs, a wave of them, take equal ranges of all the tiles (group_work.cuh); the partial results
@@ -24,7 +24,18 @@
 // of the cache: for S^T lane (g, j) the j-th quarter of row perm(g), for O^T the g-th eighth of
 // rows perm(2j), perm(2j + 1); there two rows' nibbles are paired in the words before they are
 // taken apart, four instructions for 16 values.  perm keeps both kinds of loads free of bank
-// conflicts: any two neighbours differ in parity, as do the lanes' rows of a load.
+// conflicts.
+//
+// What bounds it (128 channels, 4 query heads per KV head): the instructions that take the cache to
+// f16.  A group of 16 rows of K and V is 64 conversions (two cycles of the ALU each), 64 products
+// with scales (two cycles of another pipe), 16 mma and some 80 others.  64 sequences of 512 to 8192
+// rows take 65.0 us for 322 MB (5.0 TB/s; the 8-bit cache 93 us), 4 of 30000 to 32768 33.5 us for
+// 145 MB, of which 5 us are two launches, the first tile and the merge.  With the copies alone
+// these take 57.6 and 26.6 us, with the products alone 60.6 and 31.9 (of which, in tiles of 128
+// rows, the conversions were 7 us of the latter, the scale products 5.5, the mma 1.5).  Tiles of 192
+// rows (three groups per warp in one stretch of code) against 128 and 64: 66.6, 70.9, 88.8 us; more
+// warps with fewer registers (four CTAs), two sums per score and rarer polling changed nothing.
+#include <algorithm>
 #include <type_traits>
 
 #include "fp4.cuh"
@@ -617,7 +628,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.lost = a.lost;
   const bool paged = a.cache.block_table != nullptr;
   p.box_rows = KT;
-  if (paged && a.cache.page_size % KT != 0) p.box_rows = a.cache.page_size < 64 ? a.cache.page_size : 64;
+  if (paged && a.cache.page_size % KT != 0) p.box_rows = std::min(a.cache.page_size, 64);
   // (the scales' base is 16-byte aligned, and so is every page's and tile's)
   p.code_copies = paged || a.cache.Lmax * C::SROW % 16 == 0;
   p.part_o = a.part_o;
