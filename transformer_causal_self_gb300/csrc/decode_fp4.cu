@@ -4,7 +4,7 @@
 // query rows of a KV head read the same cache rows, so they are one side of a matrix product and
 // a row is read from HBM and taken to f16 once for 8 * NT of them.  A CTA:
 //   warp 4      producer: tiles of 64 or 192 K and V rows and their scale bytes into a ring by
-//               TMA, and a piece's queries, as f16, ahead of its other tiles
+//               TMA, and a piece's queries, as f16, behind its first tile
 //   warps 0..3  RG groups of 16 cache rows each per tile, by mma.sync m16n8k16 with the cache rows
 //               (then the channels) on the side of 16 and the query rows on the side of 8:
 //               S^T = K Q^T, then O^T += V^T P^T, softmax statistics in fp32 between the two;
@@ -29,11 +29,11 @@
 // What bounds it (128 channels, 4 query heads per KV head): the instructions that take the cache to
 // f16.  A group of 16 rows of K and V is 64 conversions (two cycles of the ALU each), 64 products
 // with scales (two cycles of another pipe), 16 mma and some 80 others.  64 sequences of 512 to 8192
-// rows take 65.0 us for 322 MB (5.0 TB/s; the 8-bit cache 93 us), 4 of 30000 to 32768 33.5 us for
+// rows take 65.2 us for 322 MB (4.9 TB/s; the 8-bit cache 93 us), 4 of 30000 to 32768 33.4 us for
 // 145 MB, of which 5 us are two launches, the first tile and the merge.  With the copies alone
 // these take 57.6 and 26.6 us, with the products alone 60.6 and 31.9 (of which, in tiles of 128
-// rows, the conversions were 7 us of the latter, the scale products 5.5, the mma 1.5).  Tiles of 192
-// rows (three groups per warp in one stretch of code) against 128 and 64: 66.6, 70.9, 88.8 us; more
+// rows, the conversions were 7 us of the latter, the scale products 5.5, the mma 1.5).  Tiles of
+// 192 rows (three groups per warp in one stretch of code) against 128 and 64: 66.6, 70.9, 88.8 us; more
 // warps with fewer registers (four CTAs), two sums per score and rarer polling changed nothing.
 #include <algorithm>
 #include <type_traits>
@@ -255,9 +255,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
     bool ok = true;
     for (int piece = 0; pc.n > 0 && ok; pc.next(p.line), ++piece) {
       const int b = pc.b, kvh = pc.head / p.rblocks, total = pc.L;
-      // the queries behind as many tiles as find room at once: the ring, or (it is full of the
-      // last piece's) one
-      const int q_at = min(pc.n, piece == 0 && p.code_copies ? NS : 1) - 1;
       load_queries(pc);
       int next_row = 0, next_page = R.block_table != nullptr ? page_of(pc, 0, next_row) : 0;
       for (int t = 0; t < pc.n; ++t) {
@@ -277,13 +274,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
           if (lost) atomicOr(p.status, kStatusDeviceArg);
         }
         if (lane >= nbox) code_rows = 0;
+        uint32_t bytes = C::STAGE;
+        if (p.code_copies)
+          bytes += 2 * C::SROW * __reduce_add_sync(0xffffffffu, static_cast<unsigned>(code_rows));
         bool room = true;
         if (lane == 0) room = ctl_wait(&empty[s], phase, abort_flag, p.status, kWaitNs);
         if (!__all_sync(0xffffffffu, room)) {
           ok = false;
           break;
         }
-        uint32_t bytes = C::STAGE;
         if (lost && p.code_copies) {  // the rows read as zeros: their scales have to be numbers
           for (int i = 0; i < p.box_rows * C::SROW; i += 16) {
             *reinterpret_cast<uint4*>(codes + r0 * C::SROW + i) = make_uint4(0u, 0u, 0u, 0u);
@@ -292,8 +291,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
           }
           fence_proxy_async_smem();
         }
-        if (p.code_copies)
-          bytes += 2 * C::SROW * __reduce_add_sync(0xffffffffu, static_cast<unsigned>(code_rows));
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
         __syncwarp();
@@ -313,7 +310,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
         }
         __syncwarp();
         ++issued;
-        if (t == q_at) ok = stage_queries(piece);
+        // Behind the first tile: the queries are there by the time that it has been asked for.
+        // (Behind as many as find room they came late: 1 x 1000 rows 7.8 against 7.3 us, 1 x 16000
+        // 14.8 against 13.9, and the batches above the same.)
+        if (t == 0) ok = stage_queries(piece);
         const int at_s = s;
         if (++s == NS) s = 0, phase ^= 1;
         if (!p.code_copies) {
