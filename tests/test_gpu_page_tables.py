@@ -102,6 +102,28 @@ def test_lengths_out_of_range(b, h, n):
     assert check(held, new, table, free, len(free), 40, 16, total)
 
 
+@pytest.mark.parametrize("big", [[2 ** 31 - 1] * 2, [2 ** 31 - 1] * 2 + [2], [2 ** 31 - 1] * 3,
+                                 [2 ** 31 - 1] * 4, [2 ** 31 - 5], [2 ** 30] * 4])
+@pytest.mark.parametrize("B,N", [(257, 8), (600, 2100)])
+def test_lengths_that_add_up_past_32_bits(big, B, N):
+    """No token of the step: all slots are -1, and nothing is written around them."""
+    held, new = [3] * B, big + [0] * (256 - len(big)) + [1] * (B - 256)
+    table, free, total = pools(held, [0] * B, 16, 5)
+    slots = torch.full((N + 512,), 77, dtype=torch.int64, device=dev())
+    positions = torch.full((N + 512,), 77, dtype=torch.int32, device=dev())
+    z = torch.zeros(B + 1, dtype=torch.int32, device=dev())
+    out = csattn.PageTables(z[:B].clone(), z, slots[256:256 + N], positions[256:256 + N],
+                            z[:1].clone())
+    csattn.page_tables(i32(held), i32(new), table.to(dev()), free.to(dev()), i32([len(free)]), N,
+                       page_size=16, num_pages=total, out=out)
+    refused()
+    for x, inside in ((slots, -1), (positions, 0)):
+        assert (x[256:256 + N] == inside).all()
+        assert (x[:256] == 77).all() and (x[256 + N:] == 77).all()
+    assert out.seq_lens.tolist() == held and out.free_left.item() == len(free)
+    assert out.starts.tolist() == [0] + [N] * B
+
+
 def test_pages_out_of_range():
     held, new = [5, 17, 0, 30], [3, 1, 40, 4]
     for where in range(4):

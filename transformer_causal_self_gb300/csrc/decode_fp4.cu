@@ -630,7 +630,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   p.box_rows = KT;
   if (paged && a.cache.page_size % KT != 0) p.box_rows = std::min(a.cache.page_size, 64);
   // (the scales' base is 16-byte aligned, and so is every page's and tile's)
-  p.code_copies = paged || a.cache.Lmax * C::SROW % 16 == 0;
+  p.code_copies = paged || a.cache.Lmax % (16 / C::SROW) == 0;
   p.part_o = a.part_o;
   p.part_ml = a.part_ml;
   p.status = a.status;

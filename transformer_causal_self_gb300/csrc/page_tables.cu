@@ -96,7 +96,9 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
     // the CTA's tokens among these requests'
-    const int lo = static_cast<int>(max(static_cast<long long>(t0), tok_base));
+    // (tok_base may be past 32 bits)
+    const int lo = static_cast<int>(
+        min(max(static_cast<long long>(t0), tok_base), static_cast<long long>(t1)));
     const int hi = static_cast<int>(min(static_cast<long long>(t1), tok_base + tok_sum));
     for (int t = lo + tid; t < hi; t += kThreads) {
       int r = 0;  // the first request that ends behind t
