@@ -848,7 +848,7 @@ int csattn_page_tables(const int32_t* cache_lens, const int32_t* new_lens, int32
  * at any position.  Requirements: d in {64, 128}, fp32 also {16, 32}; B * heads * T * d < 2^33,
  * T < 2^24; pointers 16-byte aligned (positions 4-byte).  A position out of range raises
  * CSATTN_ERR_DEVICE_ARG in the status word and that token is turned as at position 0.  The
- * outputs may not overlap the inputs.  Asynchronous on `stream`.
+ * outputs overlap neither each other nor an input.  Asynchronous on `stream`.
  */
 int csattn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
                         const int32_t* positions, void* q_out, void* k_out, int B, int Hq, int Hkv,
@@ -870,7 +870,7 @@ size_t csattn_qk_norm_rope_bwd_workspace_size(int d);
  *   workspace  >= csattn_qk_norm_rope_bwd_workspace_size(d) bytes, 16-byte aligned, in use until
  *              the work on `stream` completes; may be NULL without gains
  * The gains' gradients are added up in fp32 in an order that depends on the sizes alone: the same
- * call gives the same bits.
+ * call gives the same bits.  What is written overlaps nothing else of the call's.
  */
 int csattn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
                             const void* q_weight, const void* k_weight, const int32_t* positions,
