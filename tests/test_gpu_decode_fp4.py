@@ -176,6 +176,58 @@ def test_many_sequences_and_one_long_one():
     H.assert_close(out, H.expect(c, q, lens))
 
 
+@pytest.mark.parametrize("d,rep,splits", [(128, 4, 0), (128, 1, 1), (128, 9, 0), (64, 4, 0),
+                                          (64, 5, 1), (64, 16, 0), (64, 1, 0)])
+def test_many_tiles_per_cta_from_any_pages(d, rep, splits):
+    """Ranges of more tiles than a warp's lanes read pages for at once: the same bits from pages of
+    every size, from a contiguous cache and from one whose planes start anywhere; right for some
+    sequences; and rows on pages outside the pool read as zeros whichever way they are copied."""
+    B, Hkv, room = (24, 8, 6144) if splits == 0 else (2, 2, 6144)
+    g = H.gen(rep)
+    lens = [room - 131 * b for b in range(B)]
+    lens[1] = 777
+    c = {"table": None, "page": 0}
+    for n in ("k", "v"):
+        c[n] = torch.randint(0, 256, (B, Hkv, room, d // 2), generator=g, dtype=torch.uint8)
+        c[n + "s"] = torch.randint(90, 130, (B, Hkv, room, d // 16), generator=g, dtype=torch.uint8)
+    q = torch.randn(B, Hkv * rep, 1, d, generator=g).to(torch.bfloat16)
+    qd, ld = q.to(dev()), H.i32(lens)
+    want = H.decode(H.to_dev(c), qd, ld, num_splits=splits)
+    csattn.check_status()
+    for b in (1, B - 1):
+        only = [n if i == b else 0 for i, n in enumerate(lens)]
+        H.assert_close(want[b:b + 1], tuple(x[b:b + 1] for x in H.expect(c, q, only)))
+    shifted = dict(c)
+    for n in H.NAMES:
+        shifted[n] = torch.cat([c[n], torch.full_like(c[n][:, :, :1], 255)], 2).contiguous()
+    out = H.decode(H.to_dev(shifted), qd, ld, num_splits=splits, max_seq_len=room)
+    csattn.check_status()
+    assert H.same(out, want)
+    for page in (16, 32, 64, 128, 192, 384, 1024):
+        per = room // page
+        order = torch.randperm(B * per, generator=g)
+        paged = {"page": page, "table": torch.empty(B * per, dtype=torch.int32)}
+        paged["table"][:] = order.argsort().to(torch.int32)
+        paged["table"] = paged["table"].view(B, per)
+        for n in H.NAMES:  # page p of the pool is piece order[p] of the sequences
+            x = c[n].view(B, Hkv, per, page, -1).transpose(1, 2).reshape(B * per, Hkv, page, -1)
+            paged[n] = x[order].contiguous()
+        pd = H.to_dev(paged)
+        out = H.decode(pd, qd, ld, num_splits=splits)
+        csattn.check_status()
+        assert H.same(out, want), page
+        at = 5000 // page if page < 1024 else 1
+        pd["table"][0, at] = B * per
+        out = H.decode(pd, qd, ld, num_splits=splits)
+        H.refused()
+        zero = dict(c)
+        for n in H.NAMES:
+            zero[n] = c[n].clone()
+            zero[n][0, :, at * page:(at + 1) * page] = 0
+        other = H.decode(H.to_dev(zero), qd, ld, num_splits=splits)
+        assert H.same(out, other) and not H.same(out, want), page
+
+
 @pytest.mark.parametrize("B,heads", [(1, 1), (1, 3), (3, 5), (1, 4097)])
 def test_odd_numbers_of_rows(B, heads):
     lens = [20] * B

@@ -156,12 +156,14 @@ GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, int cache, int max_
                                               : group_attn_ctas(d, cache == 8, p.block_rows));
     p.most_grid = p.grid = static_cast<int>(
         std::min<long long>(resident, (line + p.least_tiles - 1) / p.least_tiles));
-    // 4-bit caches: tiles of 192 rows keep more independent work in a warp and cost fewer waits (64
-    // sequences of 512 to 8192 rows: 66.6 us, with 64 rows 88.8, with 128 70.9), but they take
-    // longer to arrive and to end (one sequence of 1000 rows: 8.6 us, 7.9 and 8.2): the short ones
-    // where they do not give every resident CTA one.
+    // 4-bit caches: longer tiles keep more independent work in a warp and cost fewer waits, but
+    // they take longer to arrive and to end: 64-row tiles where those do not give every resident
+    // CTA one.  128 channels, tiles of 64, 128 and 192 rows: 64 sequences of 512 to 8192 rows 88.8,
+    // 64.8 and 64.3 us, 4 of 30000 to 32768 44.3, 32.3 and 33.1, one of 4000 8.8 and 10.2 with the
+    // longer ones, one of 1000 7.9, 8.2 and 8.6: 128.  64 channels, 32 sequences of 4000 to 8000
+    // rows 32.6 us with 128 and 30.6 with 192.
     if (cache == 4 && line > resident) {
-      p.unit = kFp4LongTile;
+      p.unit = fp4_long_tile(d);
       const long long longer = (max_seq_len + p.unit - 1) / p.unit;
       p.grid = static_cast<int>(
           std::min<long long>(resident, (longer * B * Hkv * p.rblocks + 1) / p.least_tiles));

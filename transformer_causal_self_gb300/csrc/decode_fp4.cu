@@ -3,7 +3,7 @@
 // out = softmax(q K^T scale) V with K and V in e2m1 times a scale per 16 channels.  All Hq / Hkv
 // query rows of a KV head read the same cache rows, so they are one side of a matrix product and
 // a row is read from HBM and taken to f16 once for 8 * NT of them.  A CTA:
-//   warp 4      producer: tiles of 64 or 192 K and V rows and their scale bytes into a ring by
+//   warp 4      producer: tiles of 64, 128 or 192 K and V rows and their scale bytes into a ring by
 //               TMA, and a piece's queries, as f16, behind its first tile
 //   warps 0..3  RG groups of 16 cache rows each per tile, by mma.sync m16n8k16 with the cache rows
 //               (then the channels) on the side of 16 and the query rows on the side of 8:
@@ -29,12 +29,13 @@
 // What bounds it (128 channels, 4 query heads per KV head): the instructions that take the cache to
 // f16.  A group of 16 rows of K and V is 64 conversions (two cycles of the ALU each), 64 products
 // with scales (two cycles of another pipe), 16 mma and some 80 others.  64 sequences of 512 to 8192
-// rows take 65.2 us for 322 MB (4.9 TB/s; the 8-bit cache 93 us), 4 of 30000 to 32768 33.4 us for
+// rows take 64.5 us for 322 MB (5.0 TB/s; the 8-bit cache 93 us), 4 of 30000 to 32768 32.3 us for
 // 145 MB, of which 5 us are two launches, the first tile and the merge.  With the copies alone
-// these take 57.6 and 26.6 us, with the products alone 60.6 and 31.9 (of which, in tiles of 128
-// rows, the conversions were 7 us of the latter, the scale products 5.5, the mma 1.5).  Tiles of
-// 192 rows (three groups per warp in one stretch of code) against 128 and 64: 66.6, 70.9, 88.8 us; more
-// warps with fewer registers (four CTAs), two sums per score and rarer polling changed nothing.
+// these take 57.1 and 27.0 us, with the products alone 60.6 and 31.9 (of which the conversions were
+// 7 us of the latter, the scale products 5.5, the mma 1.5).  16-row pages take longer, 16
+// sequences of 4000 to 8000 rows 33.0 us (64-row pages 27.4, contiguous 25.7): their copies alone
+// do (25.6 against 21.4).  More warps with fewer registers (four CTAs), two sums per score, K and V
+// in stages of their own, tile rows of 128 bytes and rarer polling changed nothing.
 #include <algorithm>
 #include <type_traits>
 
@@ -82,6 +83,8 @@ struct Params {
   const uint8_t* v_scale;
   int lost;          // arrivals that the queries' barrier waits for and nothing makes (selftest)
   int box_rows;
+  int nbox, batch;   // boxes of a tile; tiles whose boxes' pages a warp's lanes read at once
+  int lanes_tile;    // lane * lanes_tile >> 16 is lane / nbox
   int box_shift;     // box_rows in the copies by lanes is 2^box_shift (or one box: all its bits)
   bool code_copies;  // scale bytes come by bulk copies, a box's at a time; else by the lanes'
   float* part_o;
@@ -209,14 +212,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
     asm volatile("fence.proxy.async.global;" ::: "memory");
     const uint64_t once = evict_first_policy();
     const CacheRows& R = p.rows;
-    const int nbox = KT / p.box_rows, r0 = lane * p.box_rows;
+    const int nbox = p.nbox, r0 = lane * p.box_rows;
     int issued = 0, s = 0, phase = 1;  // (a stage's first use waits for nothing: phase 1 is over)
-    // The page that the lane's box of tile t of the piece is in, and the row in it; -1: past the
-    // sequence.
-    auto page_of = [&](const GroupPiece& pc, int t, int& prow) {
-      const int row = (pc.t0 + t) * KT + r0;
+    // The pages of `batch` tiles' boxes from tile t on, one per lane (-1: past the sequence), and
+    // the rows in them: a batch of the piece is read while the one before it is used.  (Each tile's
+    // one tile ahead: 64 sequences of 512 to 8192 rows 66.5 against 63.8 us.)
+    const int lane_tile = lane * p.lanes_tile >> 16;
+    auto pages_of = [&](const GroupPiece& pc, int t, int& prow) {
+      const int row = (pc.t0 + t) * KT + lane_tile * KT + (lane - lane_tile * nbox) * p.box_rows;
       prow = 0;
-      if (lane >= nbox || t >= pc.n || row >= pc.L) return -1;
+      if (lane_tile >= min(p.batch, pc.n - t) || row >= pc.L) return -1;
       const int at = row / R.page_size;
       prow = row - at * R.page_size;
       return R.block_table[static_cast<size_t>(pc.b) * R.max_pages + at];
@@ -265,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
     for (int piece = 0; pc.n > 0 && ok; pc.next(p.line), ++piece) {
       const int b = pc.b, kvh = pc.head / p.rblocks, total = pc.L;
       load_queries(pc);
-      int next_row = 0, next_page = R.block_table != nullptr ? page_of(pc, 0, next_row) : 0;
+      int rows_now = 0, rows_next = 0, pages_next = -1, batch0 = 0;
+      int pages_now = R.block_table != nullptr ? pages_of(pc, 0, rows_now) : -1;
       for (int t = 0; t < pc.n; ++t) {
         const int row0 = (pc.t0 + t) * KT;
         uint8_t* codes = s_codes + s * C::CODES;
@@ -274,9 +280,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
         bool lost = false;                       // its page is outside the pool
         if (R.block_table != nullptr) {
           const bool in = lane < nbox && row0 + r0 < total;
-          const int page = next_page;
-          prow = next_row;
-          next_page = page_of(pc, t + 1, next_row);  // (read while this tile's stage is waited for)
+          if (t - batch0 == p.batch) {
+            batch0 = t;
+            pages_now = pages_next;
+            rows_now = rows_next;
+          }
+          const int from = (t - batch0) * nbox + lane;
+          const int page = __shfl_sync(0xffffffffu, pages_now, from);
+          prow = __shfl_sync(0xffffffffu, rows_now, from);
           lost = in && (page < 0 || page >= R.num_pages);
           plane = in && !lost ? page * R.Hkv + kvh : R.num_pages * R.Hkv;
           code_rows = in && !lost ? p.box_rows : 0;
@@ -349,6 +360,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
         // (Behind as many as find room they came late: 1 x 1000 rows 7.8 against 7.3 us, 1 x 16000
         // 14.8 against 13.9, and the batches above the same.)
         if (t == 0) ok = stage_queries(piece);
+        if (t == batch0 && R.block_table != nullptr)
+          pages_next = pages_of(pc, t + p.batch, rows_next);
         if (++s == NS) s = 0, phase ^= 1;
         if (!ok) break;
       }
@@ -653,6 +666,9 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   const bool paged = a.cache.block_table != nullptr;
   p.box_rows = KT;
   if (paged && a.cache.page_size % KT != 0) p.box_rows = std::min(a.cache.page_size, 64);
+  p.nbox = KT / p.box_rows;
+  p.batch = 32 / p.nbox;
+  p.lanes_tile = 65536 / p.nbox + 1;
   // (the scales' base is 16-byte aligned, and so is every page's and tile's.  By lanes where a box
   // is small: 16 sequences of 4000 to 8000 rows in 16-row pages 33.7 against 36.9 us, with 64
   // channels 32.4 against 36.9, in 32-row pages the same and 27.8 against 29.3; in 64-row pages, 64
@@ -692,13 +708,13 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
 template <int D, int NT, int H>
 cudaError_t launch_unit(const GroupArgs& a, cudaStream_t stream) {
   return a.plan.unit == kFp4ShortTile ? launch_t<D, NT, kFp4ShortTile / (16 * NW), H>(a, stream)
-                                      : launch_t<D, NT, kFp4LongTile / (16 * NW), H>(a, stream);
+                                      : launch_t<D, NT, fp4_long_tile(D) / (16 * NW), H>(a, stream);
 }
 template <int D>
 cudaError_t launch_rows(const GroupArgs& a, cudaStream_t stream) {
   // Up to four query rows take every other column of a product, so that a lane has weights of one
-  // column to work out and not of two (64 sequences of 512 to 8192 rows: 64.0 against 65.1 us; 32 of
-  // 4000 to 8000 with 64 channels 32.0 against 32.9).
+  // column to work out and not of two (64 sequences of 512 to 8192 rows: 64.0 against 65.1 us; 32
+  // of 4000 to 8000 with 64 channels 32.0 against 32.9).
   if (a.Hq / a.Hkv <= 4) return launch_unit<D, 1, 1>(a, stream);
   return a.plan.block_rows <= 8 ? launch_unit<D, 1, 2>(a, stream) : launch_unit<D, 2, 2>(a, stream);
 }

@@ -344,7 +344,8 @@ constexpr int decode_fp4_ctas(int d, int block_rows) {
   return (d == 128 ? 3 : 4) - (block_rows > 8 ? 1 : 0);
 }
 // Cache rows of its tiles: plan_for takes the long ones where the GPU is full with the short ones.
-constexpr int kFp4ShortTile = 64, kFp4LongTile = 192;
+constexpr int kFp4ShortTile = 64;
+constexpr int fp4_long_tile(int d) { return d == 128 ? 128 : 192; }
 cudaError_t launch_decode_fp4(const GroupArgs& a, cudaStream_t stream);
 // The same on tcgen05, for many query rows; rope is 0.
 cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t stream);
