@@ -676,7 +676,7 @@ cudaError_t launch_t(const GroupArgs& a, cudaStream_t stream) {
   // channels 32.4 against 36.9, in 32-row pages the same and 27.8 against 29.3; in 64-row pages, 64
   // sequences of 512 to 8192 rows, 71.0 against 66.5.)
   p.code_copies = paged ? p.box_rows >= 64 : a.cache.Lmax % (16 / C::SROW) == 0;
-  p.box_shift = !paged ? 31 : (p.box_rows == 16 ? 4 : (p.box_rows == 32 ? 5 : 6));
+  p.box_shift = !paged ? 31 : (p.box_rows == 16 ? 4 : 5);
   p.part_o = a.part_o;
   p.part_ml = a.part_ml;
   p.status = a.status;
