@@ -5,8 +5,8 @@
 // has eight channels of a key and of the value beside it: 16 bytes of bf16 and four of e2m1, so
 // that a warp's loads and stores are contiguous on both sides and a row is found once; two lanes
 // share a block of 16 and its scale byte.  Both move each byte once.  128 channels, 8 KV heads: the
-// append of 4 x 4096 tokens takes 16.7 us (86 MB, 5.2 TB/s; three quarters of the issue slots are
-// busy, most of them rounding), of 64 tokens 1.7; the read of 32768 rows in 128-row pages 28.3 us
+// append of 4 x 4096 tokens takes 15.5 us (86 MB, 5.5 TB/s; three quarters of the issue slots are
+// busy, most of them rounding; 16.7 with each scale worked out by both lanes), of 64 tokens 1.7; the read of 32768 rows in 128-row pages 28.3 us
 // (172 MB, 6.1 TB/s), of 64 x 64..256 rows 11.9, whose blocks have little to do between the length,
 // the table and the row.
 // (16 channels per thread, which leaves half sectors to each store: 36.9 us for the 32768 rows;
@@ -34,18 +34,23 @@ struct AppendParams {
   const int64_t* slots;
   CacheRows rows;
   int Tn;
+  unsigned per_head;  // 0: blockIdx.y is the head; else it is blockIdx.x modulo Hkv
   uint32_t* status;
 };
 
-// the byte and the e2m1 of a lane's eight channels; the lane beside it has the block's others
-__device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* code) {
+// the largest magnitude's bits in a lane's eight channels
+__device__ __forceinline__ uint32_t top8(const uint4& x) {
   const uint32_t m = absmax_bf16x2(absmax_bf16x2(x.x, x.y), absmax_bf16x2(x.z, x.w)) & 0x7fff7fffu;
-  uint32_t top = max(m & 0xffffu, m >> 16);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  *code = fp4_scale_code(top);
-  const float s = fp4_scale(*code);
-  // (a scale of 0 leaves zeros, a NaN goes with zeros)
-  return *code == kFp4Nan ? 0u : pack_e2m1x8(x, s > 0.f ? fp4_inverse(s) : 0.f);
+  return max(m & 0xffffu, m >> 16);
+}
+// 1 / s of a scale byte; 0 of a scale of 0, which leaves zeros, and negative of a NaN, which goes
+// with them
+__device__ __forceinline__ float inverse_of(uint32_t code) {
+  const float s = fp4_scale(code);
+  return code == kFp4Nan ? -1.f : (s > 0.f ? fp4_inverse(s) : 0.f);
+}
+__device__ __forceinline__ uint32_t quantise8(const uint4& x, float inv) {
+  return inv < 0.f ? 0u : pack_e2m1x8(x, inv);
 }
 
 // Thread item (b, g, t, c), U tokens a block's rows apart: consecutive threads write consecutive
@@ -56,9 +61,14 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int G = D / 8, R = kThreads / G;  // lanes of a row, a block's rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = static_cast<int>(threadIdx.x) % G;
-  const int t0 = static_cast<int>(blockIdx.x) * (R * U) + static_cast<int>(threadIdx.x) / G;
   const int Hkv = p.rows.Hkv;
-  const int g = static_cast<int>(blockIdx.y), b = static_cast<int>(blockIdx.z);
+  int blk = static_cast<int>(blockIdx.x), g = static_cast<int>(blockIdx.y);
+  if (p.per_head != 0) {
+    blk = static_cast<int>(__umulhi(blockIdx.x, p.per_head));
+    g = static_cast<int>(blockIdx.x) - blk * Hkv;
+  }
+  const int t0 = blk * (R * U) + static_cast<int>(threadIdx.x) / G;
+  const int b = static_cast<int>(blockIdx.z);
   const __nv_bfloat16* k_src = p.k_new + b * p.k_seq + g * p.k_head + 8 * c;
   const __nv_bfloat16* v_src = p.v_new + b * p.v_seq + g * p.v_head + 8 * c;
   uint4 k[U], v[U];
@@ -98,15 +108,19 @@ __global__ void __launch_bounds__(kThreads)
   if (wrong && c == 0 && g == 0) atomicOr(p.status, kStatusDeviceArg);
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    uint32_t kc, vc;
-    const uint32_t k4 = quantise8(k[i], &kc), v4 = quantise8(v[i], &vc);
+    // Two lanes share a block of the key and one of the value: the even one finds the key's scale,
+    // the odd one the value's.
+    const bool odd = (c & 1) != 0;
+    const uint32_t kt = top8(k[i]), vt = top8(v[i]);
+    const uint32_t code = fp4_scale_code(
+        max(odd ? vt : kt, __shfl_xor_sync(0xffffffffu, odd ? kt : vt, 1)));
+    const float mine = inverse_of(code), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const uint32_t k4 = quantise8(k[i], odd ? other : mine);
+    const uint32_t v4 = quantise8(v[i], odd ? mine : other);
     if (row[i] < 0) continue;
     *reinterpret_cast<uint32_t*>(p.k_cache + row[i] * (D / 2) + 4 * c) = k4;
     *reinterpret_cast<uint32_t*>(p.v_cache + row[i] * (D / 2) + 4 * c) = v4;
-    if ((c & 1) == 0) {
-      p.k_scale[row[i] * (D / 16) + c / 2] = static_cast<uint8_t>(kc);
-      p.v_scale[row[i] * (D / 16) + c / 2] = static_cast<uint8_t>(vc);
-    }
+    (odd ? p.v_scale : p.k_scale)[row[i] * (D / 16) + c / 2] = static_cast<uint8_t>(code);
   }
 }
 
@@ -217,8 +231,17 @@ cudaError_t launch_cache_append_fp4(const Fp4AppendArgs& a, cudaStream_t stream)
   const unsigned rows = kThreads / (a.d / 8) * U;
   auto* kernel = a.d == 128 ? (U == 2 ? append_fp4_kernel<128, 2> : append_fp4_kernel<128, 1>)
                             : (U == 2 ? append_fp4_kernel<64, 2> : append_fp4_kernel<64, 1>);
-  const dim3 grid((static_cast<unsigned>(a.Tn) + rows - 1) / rows, static_cast<unsigned>(a.Hkv),
-                  static_cast<unsigned>(a.B));  // (Hkv, B <= 65535)
+  const unsigned blocks = (static_cast<unsigned>(a.Tn) + rows - 1) / rows;
+  // Blocks that run together read what lies together: the heads of a token first where they are
+  // beside one another (16384 tokens by slots: 17.9 us, tokens first 19.7).  x / Hkv is then the
+  // upper half of x * ceil(2^32 / Hkv), exact while x * Hkv < 2^32.
+  const unsigned heads = static_cast<unsigned>(a.Hkv);  // (Hkv, B <= 65535)
+  const bool heads_first = heads > 1 && a.k_strides[1] < a.k_strides[0] &&
+                           1ull * blocks * heads < (1u << 31) &&
+                           1ull * blocks * heads * heads < (1ull << 32);
+  if (heads_first) p.per_head = static_cast<unsigned>(((1ull << 32) + heads - 1) / heads);
+  const dim3 grid(heads_first ? blocks * heads : blocks, heads_first ? 1u : heads,
+                  static_cast<unsigned>(a.B));
   return launch_behind(kernel, grid, kThreads, stream, p);
 }
 

@@ -28,10 +28,10 @@
 //
 // What bounds it (128 channels, 4 query heads per KV head): the instructions that take the cache
 // to f16 and multiply it.  A group of 16 rows of K and V is 64 conversions, 64 products with
-// scales, 16 mma and some 80 others; in a loop of their own the conversions take 200 cycles of a
-// scheduler, the mma 187, and the three kinds together 260; with all else a group takes 450.  64
-// sequences of 512 to 8192 rows take 64.5 us for 322 MB (5.0 TB/s; the 8-bit cache 93 us), 4 of
-// 30000 to 32768 32.0 us for 145 MB, of which 5 us are two launches, the first tile and the
+// scales, 16 mma and some 120 others; in a loop of their own the conversions take 200 cycles of
+// a scheduler, the mma 187, and the three kinds together 260; with all else a group takes 450.
+// 64 sequences of 512 to 8192 rows take 64.5 us for 322 MB (5.0 TB/s; the 8-bit cache 93 us), 4
+// of 30000 to 32768 32.0 us for 145 MB, of which 5 us are two launches, the first tile and the
 // merge.  With the copies alone these take 57.1 and 27.0 us, with the products alone 60.6 and
 // 31.9.  16-row pages take longer, 16 sequences of 4000 to 8000 rows 33.0 us (64-row pages 27.4,
 // contiguous 25.7): their copies alone do (25.6 against 21.4).  Without gain: more warps with
