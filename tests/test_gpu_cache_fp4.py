@@ -63,6 +63,31 @@ def test_append_to_slots(d, Hkv, N, page, fused):
     assert same_cache(H.to_cpu(cd), c)
 
 
+@pytest.mark.parametrize("d,Hkv,N,page", [(128, 5, 9001, 64), (64, 12, 5003, 16), (64, 7, 100, 32),
+                                          (128, 1, 4097, 128), (64, 131, 700, 64)])
+@pytest.mark.parametrize("fused", [False, True])
+def test_append_to_many_slots(d, Hkv, N, page, fused):
+    """The same rows as the append of one sequence to pages of that order."""
+    g = H.gen(N)
+    per = -(-N // page)
+    table = torch.randperm(per + 3, generator=g)[:per].to(torch.int32).to(dev())
+    at = torch.arange(N, device=dev())
+    slots = table.long()[at // page] * page + at % page
+    x = torch.randn(N, 3 * Hkv, d, generator=g).to(torch.bfloat16).to(dev())
+    k, v = x[:, Hkv:2 * Hkv], x[:, 2 * Hkv:]
+    if not fused:
+        k, v = k.contiguous(), v.contiguous()
+    new = [torch.full((per + 3, Hkv, page, n), 9, dtype=torch.uint8, device=dev())
+           for n in (d // 2, d // 2, d // 16, d // 16)]
+    want = [t.clone() for t in new]
+    csattn.cache_append_fp4_slots(k, v, *new, slots)
+    csattn.cache_append_fp4_paged(*(t.transpose(0, 1)[None].contiguous() for t in (k, v)), *want,
+                                  table[None], H.i32([0]))
+    csattn.check_status()
+    for a, b in zip(new, want):
+        assert torch.equal(a, b)
+
+
 def test_append_every_magnitude():
     """Blocks that begin with every finite bf16 magnitude, beside fractions of it on and next to
     the borders between codes; infinities and NaN."""

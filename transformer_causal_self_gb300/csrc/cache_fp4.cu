@@ -6,9 +6,9 @@
 // that a warp's loads and stores are contiguous on both sides and a row is found once; two lanes
 // share a block of 16 and its scale byte.  Both move each byte once.  128 channels, 8 KV heads: the
 // append of 4 x 4096 tokens takes 15.5 us (86 MB, 5.5 TB/s; three quarters of the issue slots are
-// busy, most of them rounding; 16.7 with each scale worked out by both lanes), of 64 tokens 1.7; the read of 32768 rows in 128-row pages 28.3 us
-// (172 MB, 6.1 TB/s), of 64 x 64..256 rows 11.9, whose blocks have little to do between the length,
-// the table and the row.
+// busy, most of them rounding; 16.7 with each scale worked out by both lanes), of 64 tokens 1.7;
+// the read of 32768 rows in 128-row pages 28.3 us (172 MB, 6.1 TB/s), of 64 x 64..256 rows 11.9,
+// whose blocks have little to do between the length, the table and the row.
 // (16 channels per thread, which leaves half sectors to each store: 36.9 us for the 32768 rows;
 // keys and values in threads of their own: 40.5.)
 #include <algorithm>
