@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const float* __restric
 unsigned blocks_of(const QkNormSide& s) { return (s.items + kThreads - 1) / kThreads; }
 
 // Heads per item and blocks of the two sides; returns the grid.  `all`: blocks that fill the GPU.
-// Items are of as many heads (which share their angles) as still give each block ZR of them,
-// because blocks' shares differ by one.
+// Items are of as many heads (which share their angles) as still give each of `all` blocks two of
+// them, or four in the backward pass (`once` false), whose blocks' shares differ by one.
 int share(QkNormArgs& a, bool bf16, long long all, bool once) {
   const long long threads = static_cast<long long>(a.B) * a.T * (a.d / (bf16 ? 16 : 8));
   int span = std::max(a.q.H, a.k.H);
