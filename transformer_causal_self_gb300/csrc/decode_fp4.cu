@@ -518,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
 #pragma unroll
           for (int rg = 1; rg < RG; ++rg)
             top[n][h] = fmax3(top[n][h], sc[rg][n][h], sc[rg][n][2 + h]);
-          top[n][h] *= qf[n][h];
-          over |= top[n][h] > m_ref[n][h] + (kRescaleThreshold + kWeightLog2);
+          top[n][h] = __fmul_rn(top[n][h], qf[n][h]);
+          over |= top[n][h] - m_ref[n][h] > kRescaleThreshold + kWeightLog2;
         }
       if (__any_sync(0xffffffffu, over)) {
         unset = false;
@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
           float f[2] = {1.f, 1.f};  // what the sums so far are scaled by
 #pragma unroll
           for (int h = 0; h < H; ++h) {
-            const float mx = column_max(top[n][h]) - kWeightLog2;
-            if (mx > m_ref[n][h] + kRescaleThreshold) {
+            const float most = column_max(top[n][h]), mx = most - kWeightLog2;
+            if (most - m_ref[n][h] > kRescaleThreshold + kWeightLog2) {
               f[h] = ex2_approx(m_ref[n][h] - mx);  // 0 when m_ref was -inf
               l_part[n][h] *= f[h];
               m_ref[n][h] = mx;
@@ -550,7 +550,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
         }
         unset = __any_sync(0xffffffffu, unset);
       }
-      // weights, turned to the layout of the second product
+      // Weights, turned to the layout of the second product.  A score is rounded by itself, as in the
+      // maximum, and the difference is exact where it counts: scores past 2^24, between which
+      // fp32 has no numbers, then have weights of at most 2^15 all the same (with an FMA, whose
+      // product is not rounded, they are off by a score's last bit: infinities, or no weight at all).
       uint32_t pb[RG][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, RG>::CTAS)
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-              w[2 * i + h] = ex2_approx(fmaf(sc[rg][n][2 * i + h], qf[n][h], -ref[h]));
+              w[2 * i + h] = ex2_approx(__fmul_rn(sc[rg][n][2 * i + h], qf[n][h]) - ref[h]);
               l_part[n][h] += w[2 * i + h];
             }
 #pragma unroll
