@@ -843,12 +843,14 @@ int csattn_page_tables(const int32_t* cache_lens, const int32_t* new_lens, int32
  *              [B, T, heads, d]); NULL: both dense.  The d channels of a head are contiguous.
  *   rope_base  >= 1: pair p of channels is turned by position * rope_base^(-2p/d); <= 0: no
  *              rotation;  rope_layout  as csattn_attn_fwd
- * Sums and everything between load and store are fp32 (squares past fp32's range overflow: a head
- * with magnitudes of 2^60 and above has no meaningful norm); sines and cosines are good to 2^-22
- * at any position.  Requirements: d in {64, 128}, fp32 also {16, 32}; B * heads * T * d < 2^33,
- * T < 2^24; pointers 16-byte aligned (positions 4-byte).  A position out of range raises
- * CSATTN_ERR_DEVICE_ARG in the status word and that token is turned as at position 0.  The
- * outputs overlap neither each other nor an input.  Asynchronous on `stream`.
+ * Sums and everything between load and store are fp32; heads whose squares leave its range are
+ * scaled by a power of two first, so that the norm holds at any magnitude.  With eps = 0 a head of
+ * zeros is 0 / 0: its outputs and gradients are NaN, and so are the gains' gradients that it
+ * enters.  Sines and cosines are good to 2^-22 at any position.  Requirements: d in {64, 128}, fp32
+ * also {16, 32}; B * heads * T * d < 2^33, T < 2^24; pointers 16-byte aligned (positions 4-byte).
+ * A position out of range raises CSATTN_ERR_DEVICE_ARG in the status word and that token is turned
+ * as at position 0.  The outputs overlap neither each other nor an input.  Asynchronous on
+ * `stream`.
  */
 int csattn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
                         const int32_t* positions, void* q_out, void* k_out, int B, int Hq, int Hkv,

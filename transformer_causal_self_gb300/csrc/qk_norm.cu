@@ -17,6 +17,7 @@
 // memory 63.7 us, with runs half as long and more warps 67).  fp32, 8 x 1024 tokens of 24 heads of
 // 64: 17.0 and 27.6 us for 101 and 151 MB.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8.cuh"
 #include "internal.h"
@@ -87,6 +88,38 @@ __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Whether a mean square (with eps; not negative) is outside [2^-80, 2^120), where squares may have been
+// lost to either end of fp32's range, or is NaN: one comparison of its bits.
+__device__ __forceinline__ bool out_of_range(float ms) {
+  return __float_as_uint(ms) - (47u << 23) >= 200u << 23;
+}
+
+// mean(x^2) + eps of a row out of that range, from its channels y times a power of two f, which is
+// returned (1 for the warp's other rows): of 1 / top, top the larger of the largest |y| and
+// sqrt(eps), as far as f is a normal number.  ms becomes f^2 times the mean square with eps, so that
+// y rsqrt(ms) is what it was, and 1 / sqrt(mean(x^2) + eps) is f rsqrt(ms).  A row with an
+// infinity or NaN is left as it was.  All lanes of the warp call it.
+template <int D, int N, int G>
+__device__ __forceinline__ float rescale(float (&y)[2 * N], float eps, float& ms) {
+  float top = sqrtf(eps);
+#pragma unroll
+  for (int j = 0; j < 2 * N; ++j) top = fmaxf(top, fabsf(y[j]));
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int e = static_cast<int>(__float_as_uint(top) >> 23);
+  const float f = out_of_range(ms) && e < 255
+                      ? __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 27), 253)) << 23)
+                      : 1.f;
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2 * N; ++j) {
+    y[j] *= f;
+    sum = fmaf(y[j], y[j], sum);
+  }
+  ms = fmaf(row_sum<G>(sum), 1.f / D, eps * f * f);
+  return f;
 }
 
 // What one thread does: 2 N channels of a token in `span` heads from g0.
@@ -183,126 +216,155 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 6)
   const uint32_t mine_at = smem_u32(s_stage) + tid * 16;
   const int total =
       first < s.items ? static_cast<int>((s.items - first + step - 1) / step) * s.span : 0;
-  // the step that is loaded next
-  unsigned li = first;
-  int lr = 0, lh = 0, lbuf = 0;
-  const T* lx = nullptr;
-  const T* ly = nullptr;
-  bool llive = false;
-  auto load = [&](bool any) {
-    if (any) {
-      if (lr == 0) {
-        llive = li + tid < s.items;
-        const Item it = item_of<G>(llive ? li + tid : c, a.T, s.groups, s.span);
-        lx = static_cast<const T*>(s.x) + it.b * s.batch + it.g0 * s.head + it.t * s.token;
-        if (BWD)
-          ly = static_cast<const T*>(s.dy) +
-               ((static_cast<size_t>(it.b) * s.H + it.g0) * a.T + it.t) * D;
-        lh = it.g0;
-      }
-      const bool there = llive && lh < s.H;
-      const uint32_t dst = mine_at + lbuf * kStage<BWD>;
-      copy16(dst, lx + e0, there);
-      copy16(dst + kThreads * 16, lx + e1, there);
-      if (BWD) {
-        copy16(dst + 2 * kThreads * 16, ly + e0, there);
-        copy16(dst + 3 * kThreads * 16, ly + e1, there);
-      }
-      // (the pointers of a head that is not there are not followed: its 0 bytes are read)
-      if (++lr == s.span) {
-        lr = 0;
-        li += step;
-      } else {
-        ++lh;
-        lx += there ? s.head : 0;
-        if (BWD) ly += there ? static_cast<size_t>(a.T) * D : 0;
-      }
-      if (++lbuf == kAhead + 1) lbuf = 0;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int n = 0; n < kAhead; ++n) load(n < total);
   float w[2 * N], dw[2 * N];
   gains<T, N>(s.w, e0, e1, w);
 #pragma unroll
   for (int j = 0; j < 2 * N; ++j) dw[j] = 0.f;
-  unsigned i = first;
-  int r = 0, h = 0, buf = 0;
-  T* out = nullptr;
-  bool live = false;
-  float cs[N], sn[N];
-  for (int n = 0; n < total; ++n) {
-    load(n + kAhead < total);
-    if (r == 0) {
-      live = i + tid < s.items;
-      const Item it = item_of<G>(live ? i + tid : c, a.T, s.groups, s.span);
-      out = static_cast<T*>(s.y) + it.b * s.y_batch + it.g0 * s.y_head + it.t * s.y_token;
-      h = it.g0;
-      angles<D, N>(a, it, live && is_q && it.g0 == 0 && it.c == 0, th_hi, th_lo, cs, sn);
-    }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-    const bool mine = live && h < s.H;
-    auto fetch = [&](int piece, float* to) {
-      Piece<T, N> p;
-      *reinterpret_cast<uint4*>(p.w) = *reinterpret_cast<const uint4*>(
-          s_stage + buf * kStage<BWD> + (piece * kThreads + tid) * 16);
-      p.get(to);
+  // The backward pass goes over its rows a second time where squares of one left fp32's range, for
+  // those alone: with a branch in the first sweep all the others take 46 to 48 us instead of 45
+  // (2 x 4096 tokens; 44 without either).
+  bool again = false;
+  auto sweep = [&](auto second) {
+    constexpr bool kAgain = decltype(second)::value;
+    // the step that is loaded next
+    unsigned li = first;
+    int lr = 0, lh = 0, lbuf = 0;
+    const T* lx = nullptr;
+    const T* ly = nullptr;
+    bool llive = false;
+    auto load = [&](bool any) {
+      if (any) {
+        if (lr == 0) {
+          llive = li + tid < s.items;
+          const Item it = item_of<G>(llive ? li + tid : c, a.T, s.groups, s.span);
+          lx = static_cast<const T*>(s.x) + it.b * s.batch + it.g0 * s.head + it.t * s.token;
+          if (BWD)
+            ly = static_cast<const T*>(s.dy) +
+                 ((static_cast<size_t>(it.b) * s.H + it.g0) * a.T + it.t) * D;
+          lh = it.g0;
+        }
+        const bool there = llive && lh < s.H;
+        const uint32_t dst = mine_at + lbuf * kStage<BWD>;
+        copy16(dst, lx + e0, there);
+        copy16(dst + kThreads * 16, lx + e1, there);
+        if (BWD) {
+          copy16(dst + 2 * kThreads * 16, ly + e0, there);
+          copy16(dst + 3 * kThreads * 16, ly + e1, there);
+        }
+        // (the pointers of a head that is not there are not followed: its 0 bytes are read)
+        if (++lr == s.span) {
+          lr = 0;
+          li += step;
+        } else {
+          ++lh;
+          lx += there ? s.head : 0;
+          if (BWD) ly += there ? static_cast<size_t>(a.T) * D : 0;
+        }
+        if (++lbuf == kAhead + 1) lbuf = 0;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float y[2 * N];
-    fetch(0, y);
-    fetch(1, y + N);
-    if constexpr (!BWD) {
-      if (a.norm) {
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 2 * N; ++j) sum = fmaf(y[j], y[j], sum);
-        const float rs = rsqrtf(fmaf(row_sum<G>(sum), 1.f / D, a.eps));
-#pragma unroll
-        for (int j = 0; j < 2 * N; ++j) y[j] *= rs * w[j];
+    for (int n = 0; n < kAhead; ++n) load(n < total);
+    unsigned i = first;
+    int r = 0, h = 0, buf = 0;
+    T* out = nullptr;
+    bool live = false;
+    float cs[N], sn[N];
+    for (int n = 0; n < total; ++n) {
+      load(n + kAhead < total);
+      if (r == 0) {
+        live = i + tid < s.items;
+        const Item it = item_of<G>(live ? i + tid : c, a.T, s.groups, s.span);
+        out = static_cast<T*>(s.y) + it.b * s.y_batch + it.g0 * s.y_head + it.t * s.y_token;
+        h = it.g0;
+        angles<D, N>(a, it, live && is_q && it.g0 == 0 && it.c == 0, th_hi, th_lo, cs, sn);
       }
-      turn<N>(y, a.rope, cs, sn, 1.f);
-    } else {
-      float g[2 * N];
-      fetch(2, g);
-      fetch(3, g + N);
-      turn<N>(g, a.rope, cs, sn, -1.f);
-      if (a.norm) {
-        float sq = 0.f, dot = 0.f;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+      const bool mine = live && h < s.H;
+      auto fetch = [&](int piece, float* to) {
+        Piece<T, N> p;
+        *reinterpret_cast<uint4*>(p.w) = *reinterpret_cast<const uint4*>(
+            s_stage + buf * kStage<BWD> + (piece * kThreads + tid) * 16);
+        p.get(to);
+      };
+      bool keep = true;
+      float y[2 * N];
+      fetch(0, y);
+      fetch(1, y + N);
+      if constexpr (!BWD) {
+        if (a.norm) {
+          float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2 * N; ++j) {
-          sq = fmaf(y[j], y[j], sq);
-          dot = fmaf(g[j] * w[j], y[j], dot);
-        }
-        sq = row_sum<G>(sq);
-        dot = row_sum<G>(dot);
-        // (a lane without a row adds nothing: its gradient is 0, and eps > 0 or not, 0 * r must be)
-        const float rs = mine ? rsqrtf(fmaf(sq, 1.f / D, a.eps)) : 0.f;
-        const float m = dot * rs * (1.f / D);
+          for (int j = 0; j < 2 * N; ++j) sum = fmaf(y[j], y[j], sum);
+          float ms = fmaf(row_sum<G>(sum), 1.f / D, a.eps);
+          if (__any_sync(0xffffffffu, out_of_range(ms))) rescale<D, N, G>(y, a.eps, ms);
+          const float rs = rsqrtf(ms);
 #pragma unroll
-        for (int j = 0; j < 2 * N; ++j) {
-          const float v = y[j] * rs;
-          dw[j] = fmaf(g[j], v, dw[j]);
-          y[j] = rs * fmaf(-v, m, g[j] * w[j]);
+          for (int j = 0; j < 2 * N; ++j) y[j] *= rs * w[j];
         }
+        turn<N>(y, a.rope, cs, sn, 1.f);
       } else {
+        float g[2 * N];
+        fetch(2, g);
+        fetch(3, g + N);
+        turn<N>(g, a.rope, cs, sn, -1.f);
+        if (a.norm) {
+          float sq = 0.f, dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2 * N; ++j) y[j] = g[j];
+          for (int j = 0; j < 2 * N; ++j) {
+            sq = fmaf(y[j], y[j], sq);
+            dot = fmaf(g[j] * w[j], y[j], dot);
+          }
+          sq = row_sum<G>(sq);
+          dot = row_sum<G>(dot);
+          float ms = fmaf(sq, 1.f / D, a.eps), f = 1.f;
+          const bool odd = mine && out_of_range(ms);
+          if constexpr (kAgain) {
+            f = rescale<D, N, G>(y, a.eps, ms);
+            dot = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * N; ++j) dot = fmaf(g[j] * w[j], y[j], dot);
+            dot = row_sum<G>(dot);
+          }
+          const bool now = mine && odd == kAgain;
+          again |= odd;
+          // (a lane without a row, or with one of the other sweep's, adds nothing: 0 * r must be 0)
+          const float rs = now ? rsqrtf(ms) : 0.f;
+          const float m = dot * rs * (1.f / D);
+#pragma unroll
+          for (int j = 0; j < 2 * N; ++j) {
+            const float v = y[j] * rs;
+            dw[j] = fmaf(g[j], v, dw[j]);
+            y[j] = rs * fmaf(-v, m, g[j] * w[j]);
+            if (kAgain) y[j] *= f;
+          }
+          keep = !kAgain || odd;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2 * N; ++j) y[j] = g[j];
+        }
       }
+      if (mine) {
+        if (keep) {
+          Piece<T, N> p;
+          p.put(y);
+          p.store(out + e0);
+          p.put(y + N);
+          p.store(out + e1);
+        }
+        out += s.y_head;
+      }
+      ++h;
+      if (++r == s.span) {
+        r = 0;
+        i += step;
+      }
+      if (++buf == kAhead + 1) buf = 0;
     }
-    if (mine) {
-      Piece<T, N> p;
-      p.put(y);
-      p.store(out + e0);
-      p.put(y + N);
-      p.store(out + e1);
-      out += s.y_head;
-    }
-    ++h;
-    if (++r == s.span) {
-      r = 0;
-      i += step;
-    }
-    if (++buf == kAhead + 1) buf = 0;
+  };
+  sweep(std::false_type{});
+  if constexpr (BWD) {
+    if (__syncthreads_or(again)) sweep(std::true_type{});
   }
   if constexpr (BWD) {
     if (a.partial == nullptr) return;
