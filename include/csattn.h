@@ -871,8 +871,10 @@ size_t csattn_qk_norm_rope_bwd_workspace_size(int d);
  *              elements of dq or dk may share a place.
  *   workspace  >= csattn_qk_norm_rope_bwd_workspace_size(d) bytes, 16-byte aligned, in use until
  *              the work on `stream` completes; may be NULL without gains
- * The gains' gradients are added up in fp32 in an order that depends on the sizes alone: the same
- * call gives the same bits.  What is written overlaps nothing else of the call's.
+ * The gains' gradients are added up in an order that depends on the sizes alone (the same call
+ * gives the same bits), in fp32 up to 1024 terms and in 64 bits beyond: each is off by at most
+ * 2^-13 of the sum of its |g n|, of however many rows.  What is written overlaps nothing else of
+ * the call's.
  */
 int csattn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
                             const void* q_weight, const void* k_weight, const int32_t* positions,

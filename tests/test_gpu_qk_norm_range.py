@@ -8,6 +8,7 @@ import torch
 
 import transformer_causal_self_gb300 as csattn
 from oracle import step as OS
+from tests.fp8_helpers import gen
 from tests.gpu_helpers import dev
 from tests.test_gpu_qk_norm import case, np64, pair_lengths, within
 
@@ -67,3 +68,46 @@ def test_a_head_of_zeros_without_eps():
     assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
     assert torch.equal(back[0], grads[0]) and torch.equal(back[1], grads[1])
     assert torch.equal(back[3], grads[3])
+
+
+def test_gains_gradients_over_many_rows_per_thread():
+    """Equal terms, whose roundings into one fp32 sum all go the same way (over 2300 rows in a
+    thread: 2^-15 of the sum and more).  Here a thread adds at most 127 of them in fp32, then 4 steps
+    of lanes' and 4 warps' sums are added, and 15 and 32 of the blocks': 2^-24 of the sum each,
+    2^-16.5 in all, and the terms' 2^-18."""
+    T, H, d = 1 << 20, 64, 16
+    c = 1 + 2.0 ** -14 - 2.0 ** -20
+    x = torch.ones(d, device=dev())
+    q, k = x.expand(1, H, T, d), x.expand(1, 1, T, d)
+    dy = [torch.full((1, h, T, d), c, device=dev()) for h in (H, 1)]
+    grads = csattn.qk_norm_rope_bwd(*dy, q, k, x, x, eps=0.0)
+    csattn.check_status()
+    for h, dw in zip((H, 1), grads[2:]):
+        want = float(np.float32(c)) * h * T
+        assert np.abs(np64(dw) / want - 1).max() <= 2.0 ** -16
+
+
+def test_many_rows_per_thread_parity():
+    """Gradients of random rows where threads have over 1100 each, the last ones fewer."""
+    T, H, d = (1 << 19) + 13, 63, 16
+    x, xk = (torch.randn(T, d, generator=gen(s)).to(dev()) for s in (1, 2))
+    w = [(1 + 0.3 * torch.randn(d, generator=gen(3))).to(dev()) for _ in range(2)]
+    dy = [torch.randn(1, h, T, d, device=dev(), generator=torch.Generator(dev()).manual_seed(h))
+          for h in (H, 1)]
+    got = csattn.qk_norm_rope_bwd(*dy, x.expand(1, H, T, d), xk.expand(1, 1, T, d), *w, eps=1e-6)
+    csattn.check_status()
+    for i, (a, g) in enumerate(zip((x, xk), dy)):
+        n = a.double() / (a.double().square().mean(-1, keepdim=True) + 1e-6).sqrt()
+        want, size = torch.zeros(d, dtype=torch.float64, device=dev()), 0.0
+        for h in range(g.shape[1]):
+            gn = g[0, h].double() * n
+            want += gn.sum(0)
+            size = size + gn.abs().sum(0)
+        assert ((got[2 + i].double() - want).abs() <= 2.0 ** -16 * size).all()
+        for h in {0, g.shape[1] // 2, g.shape[1] - 1}:
+            rx, _ = OS.qk_norm_rope_bwd(np64(g[:, h:h + 1]), np64(a)[None, None], np64(w[i]),
+                                        np.zeros((1, T)), 1e-6, 0.0, "split_half")
+            r = 1 / np.sqrt((np64(a) ** 2).mean(-1, keepdims=True) + 1e-6)
+            gw = np.abs(np64(g[0, h]) * np64(w[i]))
+            tol = 2.0 ** -18 * r * (gw + np64(n.abs()) * (gw * np64(n.abs())).mean(-1, keepdims=True))
+            within(got[i][:, h:h + 1], rx, tol[None, None], "qk"[i])

@@ -190,7 +190,14 @@ template <bool BWD>
 constexpr int kStage = (BWD ? 4 : 2) * kThreads * 16;  // of a step: two pieces of x (and of dy)
 template <bool BWD>
 constexpr int kRing = (kAhead + 1) * kStage<BWD>;
-template <typename T, int D, bool BWD>
+// A thread adds its rows' terms of dw in fp32.  Past kMany of them (2^-14 of the sum, if all their
+// roundings went one way) another kernel does it, LONG, which moves what it has to a sum of 64 bits
+// behind the ring when an item begins and kFold rows or more were added: 8 x 8192 tokens of 32 + 8
+// heads of 128, 576 rows a thread, 387 us with it and 366 without, 2 x 4096 tokens 47.6 and 45.0.
+constexpr int kMany = 1024, kFold = 64;
+template <typename T, bool BWD, bool LONG>
+constexpr int kShared = kRing<BWD> + (LONG ? 2 * kPiece<T> * kThreads * 8 : 0);
+template <typename T, int D, bool BWD, bool LONG>
 __global__ void __launch_bounds__(kThreads, BWD ? 3 : 6)
     qk_norm_kernel(const __grid_constant__ QkNormArgs a) {
   constexpr int N = kPiece<T>, G = D / (2 * N);
@@ -224,6 +231,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 6)
   // those alone: with a branch in the first sweep all the others take 46 to 48 us instead of 45
   // (2 x 4096 tokens; 44 without either).
   bool again = false;
+  double* far = reinterpret_cast<double*>(s_stage + kRing<BWD>) + tid;  // [2 N], kThreads apart
+  bool folded = false;
   auto sweep = [&](auto second) {
     constexpr bool kAgain = decltype(second)::value;
     // the step that is loaded next
@@ -270,9 +279,19 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 6)
     T* out = nullptr;
     bool live = false;
     float cs[N], sn[N];
+    int next_fold = kFold;
     for (int n = 0; n < total; ++n) {
       load(n + kAhead < total);
       if (r == 0) {
+        if (LONG && n >= next_fold) {
+#pragma unroll
+          for (int j = 0; j < 2 * N; ++j) {
+            far[j * kThreads] = (folded ? far[j * kThreads] : 0.0) + static_cast<double>(dw[j]);
+            dw[j] = 0.f;
+          }
+          folded = true;
+          next_fold = n + kFold;
+        }
         live = i + tid < s.items;
         const Item it = item_of<G>(live ? i + tid : c, a.T, s.groups, s.span);
         out = static_cast<T*>(s.y) + it.b * s.y_batch + it.g0 * s.y_head + it.t * s.y_token;
@@ -370,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 6)
     if (a.partial == nullptr) return;
 #pragma unroll
     for (int j = 0; j < 2 * N; ++j) {
+      if (LONG && folded) dw[j] = static_cast<float>(far[j * kThreads] + static_cast<double>(dw[j]));
 #pragma unroll
       for (int o = G; o < 32; o <<= 1) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], o);
       if (lane < G) s_dw[warp][j < N ? e0 + j : e1 + j - N] = dw[j];
@@ -416,10 +436,11 @@ unsigned blocks_of(const QkNormSide& s) { return (s.items + kThreads - 1) / kThr
 
 // Heads per item and blocks of the two sides; returns the grid.  `all`: blocks that fill the GPU.
 // Items are of as many heads (which share their angles) as still give each of `all` blocks two of
-// them, or four in the backward pass (`once` false), whose blocks' shares differ by one.
+// them, or four in the backward pass (`once` false), whose blocks' shares differ by one, and no more
+// than kFold there.
 int share(QkNormArgs& a, bool bf16, long long all, bool once) {
   const long long threads = static_cast<long long>(a.B) * a.T * (a.d / (bf16 ? 16 : 8));
-  int span = std::max(a.q.H, a.k.H);
+  int span = std::min(std::max(a.q.H, a.k.H), once ? 1 << 20 : kFold);
   while (span > 1 && threads * ((a.q.H + span - 1) / span + (a.k.H + span - 1) / span) <
                          (once ? 2 : 4) * all * kThreads)
     span = (span + 1) / 2;
@@ -434,13 +455,14 @@ int share(QkNormArgs& a, bool bf16, long long all, bool once) {
   return a.q_blocks + static_cast<int>((bk + rounds - 1) / rounds);
 }
 
-template <typename T, int D, bool BWD>
+template <typename T, int D, bool BWD, bool LONG>
 cudaError_t launch_t(const QkNormArgs& a, int grid, float* dqw, float* dkw, cudaStream_t stream) {
   static SmemLimitOnce smem_limit;
-  cudaError_t e = smem_limit.set(qk_norm_kernel<T, D, BWD>, kRing<BWD>);
+  constexpr int kBytes = kShared<T, BWD, LONG>;
+  cudaError_t e = smem_limit.set(qk_norm_kernel<T, D, BWD, LONG>, kBytes);
   if (e != cudaSuccess) return e;
-  e = launch_behind(qk_norm_kernel<T, D, BWD>, dim3(static_cast<unsigned>(grid)), kThreads,
-                    size_t{kRing<BWD>}, stream, a);
+  e = launch_behind(qk_norm_kernel<T, D, BWD, LONG>, dim3(static_cast<unsigned>(grid)), kThreads,
+                    size_t{kBytes}, stream, a);
   if constexpr (BWD) {
     if (e == cudaSuccess && a.partial != nullptr)
       e = launch_behind(sum_kernel<D>, dim3(D / kSumChannels, 2), kSumThreads, stream,
@@ -448,30 +470,42 @@ cudaError_t launch_t(const QkNormArgs& a, int grid, float* dqw, float* dkw, cuda
   }
   return e;
 }
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool LONG>
 cudaError_t launch_d(const QkNormArgs& a, int grid, float* dqw, float* dkw, cudaStream_t stream) {
-  if (a.d == 128) return launch_t<T, 128, BWD>(a, grid, dqw, dkw, stream);
-  if (a.d == 64) return launch_t<T, 64, BWD>(a, grid, dqw, dkw, stream);
+  if (a.d == 128) return launch_t<T, 128, BWD, LONG>(a, grid, dqw, dkw, stream);
+  if (a.d == 64) return launch_t<T, 64, BWD, LONG>(a, grid, dqw, dkw, stream);
   if constexpr (sizeof(T) == 4) {
-    if (a.d == 32) return launch_t<T, 32, BWD>(a, grid, dqw, dkw, stream);
-    return launch_t<T, 16, BWD>(a, grid, dqw, dkw, stream);
+    if (a.d == 32) return launch_t<T, 32, BWD, LONG>(a, grid, dqw, dkw, stream);
+    return launch_t<T, 16, BWD, LONG>(a, grid, dqw, dkw, stream);
   }
   return cudaErrorInvalidValue;
+}
+template <bool BWD, bool LONG>
+cudaError_t launch_type(const QkNormArgs& a, bool bf16, int grid, float* dqw, float* dkw,
+                        cudaStream_t stream) {
+  return bf16 ? launch_d<__nv_bfloat16, BWD, LONG>(a, grid, dqw, dkw, stream)
+              : launch_d<float, BWD, LONG>(a, grid, dqw, dkw, stream);
+}
+
+// rows of a side's threads, at most
+long long most_rows(const QkNormSide& s, int blocks) {
+  return (blocks_of(s) + blocks - 1LL) / blocks * s.span;
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm(QkNormArgs a, bool bf16, cudaStream_t stream) {
   const int grid = share(a, bf16, 6 * kSms, true);
-  return bf16 ? launch_d<__nv_bfloat16, false>(a, grid, nullptr, nullptr, stream)
-              : launch_d<float, false>(a, grid, nullptr, nullptr, stream);
+  return launch_type<false, false>(a, bf16, grid, nullptr, nullptr, stream);
 }
 
 cudaError_t launch_qk_norm_bwd(QkNormArgs a, bool bf16, float* dqw, float* dkw,
                                cudaStream_t stream) {
   const int grid = share(a, bf16, qk_norm_bwd_blocks(), false);
-  return bf16 ? launch_d<__nv_bfloat16, true>(a, grid, dqw, dkw, stream)
-              : launch_d<float, true>(a, grid, dqw, dkw, stream);
+  const bool many = a.partial != nullptr && std::max(most_rows(a.q, a.q_blocks),
+                                                     most_rows(a.k, grid - a.q_blocks)) > kMany;
+  return many ? launch_type<true, true>(a, bf16, grid, dqw, dkw, stream)
+              : launch_type<true, false>(a, bf16, grid, dqw, dkw, stream);
 }
 
 }  // namespace csattn
