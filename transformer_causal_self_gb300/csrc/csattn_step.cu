@@ -6,6 +6,7 @@
 
 #include "csattn.h"
 #include "internal.h"
+#include "places.h"
 
 namespace csattn {
 namespace {
@@ -56,6 +57,19 @@ int set_strides(const char* fn, const int64_t* strides, int B, int H, int T, int
   if (rc == CSATTN_OK) rc = check_stride(fn, *head, H, size);
   if (rc == CSATTN_OK) rc = check_stride(fn, *token, T, size);
   return rc;
+}
+
+// Nothing that a call writes may lie on what it reads or writes besides.
+int check_apart(const char* fn, const Places* written, int nw, const Places* read, int nr) {
+  for (int i = 0; i < nw; ++i) {
+    for (int j = 0; j < nr; ++j)
+      if (share_a_place(written[i], read[j]))
+        return api_fail(CSATTN_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+    for (int j = 0; j < i; ++j)
+      if (share_a_place(written[i], written[j]))
+        return api_fail(CSATTN_ERR_INVALID_ARG, "%s: two outputs overlap", fn);
+  }
+  return CSATTN_OK;
 }
 
 // What both directions of the norm are given; *a receives it.
@@ -217,6 +231,14 @@ int csattn_qk_norm_rope(const void* q, const void* k, const void* q_weight, cons
     s->y_head = static_cast<long long>(T) * d;
     s->y_batch = s->H * s->y_head;
   }
+  const int size = dtype == CSATTN_BF16 ? 2 : 4;
+  const long long each = 1LL * T * d * size * B;
+  const Places written[] = {{q_out, each * Hq}, {k_out, each * Hkv}};
+  const Places read[] = {{q, B, Hq, T, d, size, a.q.batch, a.q.head, a.q.token},
+                         {k, B, Hkv, T, d, size, a.k.batch, a.k.head, a.k.token},
+                         {q_weight, 1LL * d * size}, {k_weight, 1LL * d * size},
+                         {positions, 4LL * B * T}};
+  if ((rc = check_apart("qk_norm_rope", written, 2, read, 5)) != CSATTN_OK) return rc;
   int sms = 0;
   if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
   const cudaError_t e =
@@ -265,6 +287,18 @@ int csattn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* 
                       workspace_bytes);
     a.partial = static_cast<float*>(workspace);
   }
+  const long long each = 1LL * T * d * size * B;
+  const Places written[] = {
+      {dq, B, Hq, T, d, size, a.q.y_batch, a.q.y_head, a.q.y_token},
+      {dk, B, Hkv, T, d, size, a.k.y_batch, a.k.y_head, a.k.y_token},
+      {dq_weight, 4LL * d}, {dk_weight, 4LL * d},
+      {a.partial, static_cast<long long>(csattn_qk_norm_rope_bwd_workspace_size(d))}};
+  const Places read[] = {{q, B, Hq, T, d, size, a.q.batch, a.q.head, a.q.token},
+                         {k, B, Hkv, T, d, size, a.k.batch, a.k.head, a.k.token},
+                         {dq_out, each * Hq}, {dk_out, each * Hkv},
+                         {q_weight, 1LL * d * size}, {k_weight, 1LL * d * size},
+                         {positions, 4LL * B * T}};
+  if ((rc = check_apart(fn, written, 5, read, 7)) != CSATTN_OK) return rc;
   int sms = 0;
   if ((rc = api_device_info(&a.status, &sms)) != CSATTN_OK) return rc;
   const cudaError_t e = launch_qk_norm_bwd(a, dtype == CSATTN_BF16, dq_weight, dk_weight,
