@@ -776,9 +776,11 @@ size_t csattn_decode_fp4_workspace_size(int B, int Hq, int Hkv, int Lmax, int d,
  *             the output is 0
  *   out       [B, Hq, 1, d] bf16
  *   scale, num_splits, workspace  as csattn_attn_decode_fp8
- * The cache's values enter the products exactly, the queries rounded to 11 bits (bf16 has 8;
- * channels below 2^-38 of a query's largest vanish), the softmax weights rounded to 11 bits
- * (those below 2^-32 of a query's largest vanish); sums are fp32.
+ * The cache's values enter the products exactly, and so do the queries (channels below 2^-31 of a
+ * query's largest, if that is 2^-112 or more, are off by at most 2^-39 of it).  The softmax weights
+ * enter as f16, of which their query's largest is 2^7 or more: each is off by at most 2^-11 of
+ * itself, or 2^-32 of the largest where that is more (below 2^-21 of it).  Sums, the weights'
+ * before that rounding among them, are fp32, and so are scores: of any size below 2^126.
  * Requirements: dtype CSATTN_BF16 (of q and out), d in {64, 128}, any Hq / Hkv.  Rows at or
  * beyond seq_lens[b] are never used.  A seq_lens[b] outside [0, max_seq_len] raises
  * CSATTN_ERR_DEVICE_ARG in the status word and that sequence's output is zero; a page index

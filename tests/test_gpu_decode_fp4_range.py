@@ -68,3 +68,28 @@ def test_a_maximum_that_lags_behind_large_scores(d):
     lo, hi = torch.minimum(held[0], held[256]), torch.maximum(held[0], held[256])
     tol = (held[0].abs() + held[256].abs()) * 2.0 ** -7
     assert torch.all(out[:, :, 0] >= lo - tol) and torch.all(out[:, :, 0] <= hi + tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_small_weights_behind_a_dominant_one(d):
+    """Weights of 2^-19 to 2^-34 of the first row's, whose value is 0: what is left of each is within
+    2^-11 of it and 2^-32 of the largest; the other terms as in fp4_helpers.expect."""
+    L, rep = 3000, 16
+    c = H.empty_cache(1, 1, L, d, 0, seed=d)
+    k, v = torch.zeros(1, L, d), torch.full((1, L, d), 24576.0)
+    k[:, 0], v[:, 0] = 1.0, 0.0
+    H.set_rows(c, 0, 0, k.to(torch.bfloat16), v.to(torch.bfloat16))
+    ahead = torch.arange(19.0, 19.0 + rep) + 0.4  # (powers of two)
+    q = (ahead / (d ** 0.5 * 1.442695)).view(1, rep, 1, 1).expand(1, rep, 1, d)
+    q = q.to(torch.bfloat16).contiguous()
+    for splits in (0, 1, 7):
+        out = H.decode(H.to_dev(c), q.to(dev()), H.i32([L]), num_splits=splits)
+        csattn.check_status()
+        s = q[0, :, 0].double() @ torch.from_numpy(H.rows(c, 0, 1)[0][0, 0]) * d ** -0.5
+        w = torch.exp(-s) * (L - 1)
+        want = 24576.0 * w / (1 + w)
+        off = 2.0 ** -17 * s
+        tol = (want * (2.0 ** -11 + 2 * off + 2.0 ** -18 + 2.0 ** -8)
+               + 24576.0 * (L - 1) * 2.0 ** -32) * (1 + 2.0 ** -7)
+        got = out[0, :, 0].double().cpu()
+        assert torch.all((got - want[:, None]).abs() <= tol[:, None]), (got[:, 0], want, tol)

@@ -13,10 +13,12 @@
 // are merged by group_merge_kernel.
 //
 // The operands: K and V enter as x4 * s, which f16 holds exactly (one conversion and one product
-// for two of them); q is taken to f16 by a power of two per row (query_to_f16: 11 bits, and
-// channels below 2^-38 of the largest vanish); the weights are 2^(x - m) with m = the running
-// maximum - 7, rounded to f16 (11 bits; what is below 2^-32 of the largest vanishes).  Sums are
-// fp32 throughout.  The maximum is raised only when a score exceeds it by 2^8, and only then do
+// for two of them); q is taken to f16 by a power of two per row (query_to_f16: exact but for
+// channels below 2^-31 of the largest, which are off by 2^-39 of it); the weights are 2^(x - m)
+// with m = the running maximum - 7, rounded to f16: to 11 bits, and below 2^-21 of the largest,
+// where f16's subnormals begin, to steps of 2^-31 of it, because bf16's 8 bits would cost every
+// output 2^-9, and a second product for the rest of a weight a sixth of the instructions.  Their
+// sum is taken before that rounding, so that it costs nothing.  Sums are fp32.  The maximum is raised only when a score exceeds it by 2^8, and only then do
 // the lanes exchange theirs.
 //
 // The index of a product's sum may run over the channels (the rows) in any order that both sides
