@@ -93,3 +93,51 @@ def test_many_small_weights_behind_a_dominant_one(d):
                + 24576.0 * (L - 1) * 2.0 ** -32) * (1 + 2.0 ** -7)
         got = out[0, :, 0].double().cpu()
         assert torch.all((got - want[:, None]).abs() <= tol[:, None]), (got[:, 0], want, tol)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,page", [
+    (128, 32, 8, 64), (128, 16, 1, 128), (128, 7, 1, 16), (128, 8, 8, 0), (64, 8, 2, 64),
+    (64, 24, 1, 384), (64, 12, 12, 16), (64, 3, 3, 0)])
+def test_lengths_at_the_long_tiles_ends(d, Hq, Hkv, page):
+    """Caches with room for so much that the tiles are the long ones, of 128 rows (128 channels) or
+    192 (64): lengths at the ends of one, two and three of them, and a row to either side."""
+    lens = [127, 128, 129, 255, 256, 257, 383, 384, 385, 191, 192, 193, 575, 576, 577, 0, 1]
+    room = 6144 + (0 if page else 9)
+    c, q = H.filled(len(lens), Hq, Hkv, d, page, lens, 577 if page else room, seed=page + d)
+    if page:
+        table = torch.full((len(lens), room // page), -1, dtype=torch.int32)
+        table[:, :c["table"].shape[1]] = c["table"]
+        c["table"] = table
+    out = H.decode(H.to_dev(c), q.to(dev()), H.i32(lens))
+    csattn.check_status()
+    assert torch.all(out[15] == 0)
+    H.assert_close(out, H.expect(c, q, lens))
+
+
+@pytest.mark.skipif(not hasattr(torch, "float4_e2m1fn_x2"), reason="no packed e2m1 type")
+@pytest.mark.parametrize("page", [0, 64])
+def test_caches_of_torchs_packed_type(page):
+    """Appended to, read and decoded as torch.float4_e2m1fn_x2: the same bytes as of uint8."""
+    lens = [70, 3]
+    c, q = H.filled(2, 8, 2, 64, page, lens, 128, seed=3)
+    kn, vn = (H.tokens(c, 2 * 9, 2, 64, s).view(2, 9, 2, 64).transpose(1, 2).contiguous().to(dev())
+              for s in (1, 2))
+    plain, packed = H.to_dev(c), H.to_dev(c)
+    for n in ("k", "v"):
+        packed[n] = packed[n].view(torch.float4_e2m1fn_x2)
+    for x in (plain, packed):
+        H.append(x, kn, vn, H.i32(lens))
+    ends = H.i32([n + 9 for n in lens])
+    for n in ("k", "v"):
+        assert torch.equal(packed[n].view(torch.uint8), plain[n])
+    for a, b in zip(H.read(plain, ends), H.read(packed, ends)):
+        assert H.same(a[0, :, :79], b[0, :, :79]) and H.same(a[1, :, :12], b[1, :, :12])
+    assert H.same(H.decode(plain, q.to(dev()), ends), H.decode(packed, q.to(dev()), ends))
+    if page:
+        slots = torch.tensor([5, -1, 64], device=dev())
+        for x in (plain, packed):
+            csattn.cache_append_fp4_slots(kn[0, :, :3].transpose(0, 1).contiguous(),
+                                          vn[0, :, :3].transpose(0, 1).contiguous(), *H.cache(x),
+                                          slots)
+        assert torch.equal(packed["k"].view(torch.uint8), plain["k"])
+    csattn.check_status()
