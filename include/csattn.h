@@ -703,8 +703,8 @@ int csattn_tree_commit_paged(void* k_pages, void* v_pages, void* k_scale, void* 
  * page_size, d/16]), all 16-byte aligned.
  * A write takes for a block of largest magnitude a the scale nearest to a / 6 (ties to even, at
  * most 10240, byte 226) and the e2m1 nearest to x / s (ties to even, at most 6; the sign of x
- * stays); both are exactly rounded.  So magnitudes past 61440 saturate there, and a block all
- * below 6 * 2^-18 is stored as zeros.  A block with an infinity or NaN is stored as byte 255 and
+ * stays); both are exactly rounded.  So magnitudes past 61440 saturate there, and a block of
+ * at most 6 * 2^-18 is stored as zeros.  A block with an infinity or NaN is stored as byte 255 and
  * zeros, and reads as 16 NaN.  x4 * s is a bf16 (and an f16) number: reading is exact.  The calls
  * below read bytes 0..226 and 255 (of another byte the scale is f16's, some number, infinity or
  * NaN).

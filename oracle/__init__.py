@@ -17,7 +17,7 @@ Modules:
   * ``step``  -- the 4-bit cache format, block tables, and the norm of queries and keys; pinned by
     ``tests/test_abi_fp4_step.py``.
 
-Every function here is pinned by ``tests/test_oracle_pins.py``; none is
-"parity unpinned".
+Every function of ``attn`` and ``naive`` is pinned by ``tests/test_oracle_pins.py``, every one of
+``step`` by ``tests/test_abi_fp4_step.py``; none is "parity unpinned".
 """
 from . import attn, naive, step  # noqa: F401

@@ -157,11 +157,19 @@ GroupPlan plan_for(int B, int Hkv, int rows, int d, bool tc, int cache, int max_
     p.most_grid = p.grid = static_cast<int>(
         std::min<long long>(resident, (line + p.least_tiles - 1) / p.least_tiles));
     // 4-bit caches: longer tiles keep more independent work in a warp and cost fewer waits, but
-    // they take longer to arrive and to end: 64-row tiles where those do not give every resident
-    // CTA one.  128 channels, tiles of 64, 128 and 192 rows: 64 sequences of 512 to 8192 rows 88.8,
-    // 64.8 and 64.3 us, 4 of 30000 to 32768 44.3, 32.3 and 33.1, one of 4000 8.8 and 10.2 with the
-    // longer ones, one of 1000 7.9, 8.2 and 8.6: 128.  64 channels, 32 sequences of 4000 to 8000
-    // rows 32.6 us with 128 and 30.6 with 192.
+    // they take longer to arrive and to end: they are taken where 64-row tiles would give more than
+    // one to every resident CTA, although they then leave CTAs out until there are four (six) times
+    // as many, since a CTA with one long tile is done before one with two short ones.  8 KV heads,
+    // with 64-row tiles and with the long ones, in us:
+    //   128 channels, 128 rows: below the rule 4 sequences of 800 rows 8.7, 9.0 (but 1 x 3600 10.1,
+    //     9.2); past it 1 x 3700 9.6, 9.2; 1 x 4000 10.2, 8.6; 4 x 1000 8.6, 8.3; 1 x 8000 12.5, 10.9;
+    //     16 x 500 11.8, 9.0; 64 x 100 12.8, 11.8; 4 x 8000 16.6, 15.3; 64 x 1000 25.1, 21.5
+    //   64 channels, 192 rows: below it 4 x 1000 7.0, 7.2 (but 1 x 4000 8.2, 7.7); past it 1 x 5000
+    //     8.9, 7.8; 16 x 300 8.5, 7.5; 4 x 2000 8.0, 8.1; 64 x 100 9.3, 10.4; 1 x 16000 10.9, 9.6; 64 x
+    //     1000 20.2, 16.7
+    // 128 or 192 rows: 128 channels, 4 sequences of 30000 to 32768 32.3 and 33.1, one of 4000 8.8 and
+    // 10.2; 64 channels, 32 of 4000 to 8000 (8 KV heads) 32.6 and 30.6.  With an explicit number of
+    // splits the tiles are the short ones, so that a part can be as small as 64 rows.
     if (cache == 4 && line > resident) {
       p.unit = fp4_long_tile(d);
       const long long longer = (max_seq_len + p.unit - 1) / p.unit;

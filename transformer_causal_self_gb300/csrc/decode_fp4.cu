@@ -17,9 +17,9 @@
 // channels below 2^-31 of the largest, which are off by 2^-39 of it); the weights are 2^(x - m)
 // with m = the running maximum - 7, rounded to f16: to 11 bits, and below 2^-21 of the largest,
 // where f16's subnormals begin, to steps of 2^-31 of it, because bf16's 8 bits would cost every
-// output 2^-9, and a second product for the rest of a weight a sixth of the instructions.  Their
-// sum is taken before that rounding, so that it costs nothing.  Sums are fp32.  The maximum is raised only when a score exceeds it by 2^8, and only then do
-// the lanes exchange theirs.
+// output 2^-9, and the rest of a weight in a second product half as many mma again.  Their sum is
+// taken ahead of that rounding.  Sums are fp32.  The maximum is raised only when a score exceeds it
+// by 2^8, and only then do the lanes exchange theirs.
 //
 // The index of a product's sum may run over the channels (the rows) in any order that both sides
 // share, and its rows may be any 16 cache rows.  So a lane takes a row's channels as whole words
@@ -28,15 +28,19 @@
 // taken apart, four instructions for 16 values.  perm keeps both kinds of loads free of bank
 // conflicts.
 //
-// What bounds it (128 channels, 4 query heads per KV head): the instructions that take the cache
-// to f16 and multiply it.  A group of 16 rows of K and V is 64 conversions, 64 products with
-// scales, 16 mma and some 120 others; in a loop of their own the conversions take 200 cycles of
-// a scheduler, the mma 187, and the three kinds together 260; with all else a group takes 450.
-// 64 sequences of 512 to 8192 rows take 64.5 us for 322 MB (5.0 TB/s; the 8-bit cache 93 us), 4
-// of 30000 to 32768 32.0 us for 145 MB, of which 5 us are two launches, the first tile and the
+// What bounds it (128 channels, 4 query heads per KV head): latency.  A group of 16 rows of K and V
+// is 284 instructions, 64 of them conversions, 64 products with scales and 16 mma; in a loop of
+// their own these three kinds take 260 cycles of a scheduler (the conversions alone 200, the mma
+// 187), and with all else a group takes 450.  No unit is near its rate (issue slots 54 %, ALU
+// 46 %, tensor pipe 25 %, HBM 58 %): what is left is the chain copy, conversion, scale, mma,
+// maximum, exponentials, turn, conversion, scale, mma, of which three warps per scheduler do not
+// cover all.
+// 64 sequences of 512 to 8192 rows take 64.8 us for 322 MB (5.0 TB/s; the 8-bit cache 93 us), 4
+// of 30000 to 32768 32.1 us for 145 MB, of which 5 us are two launches, the first tile and the
 // merge.  With the copies alone these take 57.1 and 27.0 us, with the products alone 60.6 and
 // 31.9.  16-row pages take longer, 16 sequences of 4000 to 8000 rows 33.0 us (64-row pages 27.4,
-// contiguous 25.7): their copies alone do (25.6 against 21.4).  Without gain: more warps with
+// contiguous 25.7); their copies alone take 25.6 against 21.4, which is 4.2 of those 7.3 us, and
+// where the rest goes was not found.  Without gain: more warps with
 // fewer registers (four CTAs), two sums per score, the next tile's scores before this one's
 // values, K and V in stages of their own, tile rows of 128 bytes, all copies by the lanes (the
 // 16-row pages 37.4 us), rarer polling.

@@ -11,9 +11,9 @@
 // the store is fp32, and each value is rounded once.
 //
 // Both directions move each value once.  Forward, 4 x 4096 tokens of 32 + 8 heads of 128 (bf16, out
-// of a fused projection): 52.8 us for 336 MB, 6.4 TB/s, 94 % of a plain copy, with 77 % of the
-// issue slots busy; 64 tokens 2.7 us.  Backward, 2 x 4096 tokens: 44.8 us for 252 MB, 5.6 TB/s, bound by
-// the latency that 12 warps of 140 registers cover (with the rows in registers instead of shared
+// of a fused projection): 53.0 us for 336 MB, 6.3 TB/s, 94 % of a plain copy, with 76 % of the
+// issue slots busy; 64 tokens 2.8 us.  Backward, 2 x 4096 tokens: 45.0 us for 252 MB, 5.6 TB/s, bound
+// by the latency that 12 warps of 143 registers cover (with the rows in registers instead of shared
 // memory 63.7 us, with runs half as long and more warps 67).  fp32, 8 x 1024 tokens of 24 heads of
 // 64: 17.0 and 27.6 us for 101 and 151 MB.
 #include <algorithm>
